@@ -314,6 +314,128 @@ PKV_EXPORT pkv_status paged_attention_multi_token(void *out, const void *q, cons
                                                   size_t workspace_bytes, void *stream);
 
 /*
+ * Row-scaled FP8 (E4M3) KV cache -- kv_cache_write_fp8_rows and
+ * kv_cache_read_fp8_rows.
+ *
+ * Source: the same paragraph of the aiwiki.vn page as the per-tensor FP8 cache
+ * above (a lower-precision representation of keys and values, at a conversion
+ * cost and a risk of numerical error).  Here the scale is chosen as a row is
+ * written, one for each row x (one token's K or V of one KV head), so nothing
+ * has to be calibrated and a row of any size keeps E4M3's precision:
+ *     e        = the smallest integer with max |x_i| <= 448 * 2^e over the
+ *                finite x_i, held in [-100, 120] (-100 if there is none but 0)
+ *     code_i   = the E4M3 value nearest to x_i * 2^-e (ties to the even code;
+ *                infinities saturate to +-448; NaN gives a NaN code)
+ *     value_i  = e4m3(code_i) * 2^e
+ * Layout: K and V codes [num_blocks][num_kv_heads][block_size][head_dim] (one
+ * byte per element, both as the plain cache), scales uint8
+ * [num_blocks][num_kv_heads][block_size] holding e + 127.  Base addresses
+ * 16-byte aligned.  block_copy copies both (block_bytes Hkv * B * D for the
+ * codes, Hkv * B for the scales).  Codes and scales are exact functions of the
+ * inputs, and a value is a bf16 number.
+ * Supported: head_dim 64 or 128, block_size 16 or 32.
+ *
+ * kv_cache_write_fp8_rows -- quantise and store the K/V of new tokens.
+ *   k_new, v_new   device [num_tokens][num_kv_heads][head_dim], dtype (F32 or BF16)
+ *   k_cache, v_cache, k_scales, v_scales  device, written in place
+ *   slot_mapping   device int64 [num_tokens], as for kv_cache_write
+ *
+ * kv_cache_read_fp8_rows -- the values of stored tokens, by slot (a prefix to
+ * be attended by other kernels, stored elsewhere or compared).
+ *   k_out, v_out   device [num_tokens][num_kv_heads][head_dim], dtype
+ *   slot_mapping   device int64 [num_tokens].  slot < 0: the output row is left
+ *                  as it was.  slot >= num_blocks * block_size: likewise, and
+ *                  PKV_DEVERR_SLOT is set.  A slot may come more than once.
+ */
+PKV_EXPORT pkv_status kv_cache_write_fp8_rows(const void *k_new, const void *v_new, void *k_cache, void *v_cache,
+                                              void *k_scales, void *v_scales, const int64_t *slot_mapping,
+                                              int num_tokens, int num_kv_heads, int head_dim, int block_size,
+                                              int num_blocks, int dtype, void *stream);
+PKV_EXPORT pkv_status kv_cache_read_fp8_rows(void *k_out, void *v_out, const void *k_cache, const void *v_cache,
+                                             const void *k_scales, const void *v_scales, const int64_t *slot_mapping,
+                                             int num_tokens, int num_kv_heads, int head_dim, int block_size,
+                                             int num_blocks, int dtype, void *stream);
+
+/*
+ * Scored attention -- paged_attention_decode_scored,
+ * paged_attention_decode_scored_fp8_rows and paged_attention_multi_token_scored:
+ * attention whose scores are capped or biased and whose keys are masked beyond
+ * the context's end.  The pages have no counterpart: models whose attention is
+ * not plain need it, in every place where the plain calls stand.
+ *
+ * For the query at position p of a context of L tokens, query head h and the
+ * key at position t < L:
+ *     x = scale * q . K[t]
+ *     x = softcap * tanh(x / softcap)        if softcap > 0
+ *     x = x - alibi_slopes[h] * |p - t|      if alibi_slopes is given
+ * and the key is seen if
+ *     t >= key_start  and  (t < prefix_len  or  (t <= p and (window == 0 or p - t < window))).
+ * The output is the softmax of x over the seen keys applied to their V rows,
+ * zeros if the query sees none.
+ *   softcap        finite, >= 0; 0 = no cap
+ *   alibi_slopes   device float32 [num_heads] or NULL: the distance bias
+ *   window         >= 0; 0 = no window
+ *   prefix_lens    device int32 [num_seqs] or NULL (0): keys that every query
+ *                  of the sequence sees, whatever its position and window (a
+ *                  bidirectional prefix of a prompt; the first tokens kept
+ *                  visible beside a window).  Clamped to [0, L].
+ *   key_starts     device int32, one per query ([num_seqs] for decode,
+ *                  [num_q_tokens] for multi-token) or NULL (0): the first key
+ *                  of the query's document.  Negative values count as 0.
+ * Keys that no query of a call sees are not read (whole tiles of them).
+ * scale may be any finite number.  workspace, error bits, zero rows, supported
+ * shapes and placement invariance are those of the plain calls; the workspace
+ * holds at least ..._scored_workspace_size() bytes, 256-byte aligned (NULL
+ * where that is 0), needs no initialisation, and calls that share one must be
+ * ordered on the device.
+ *
+ * paged_attention_decode_scored -- one query per sequence, p = seq_lens[s] - 1;
+ * dtype F32 (float32 arithmetic throughout) or BF16 (float32 accumulation, the
+ * softmax weights rounded to bf16).  k_new / v_new (both or neither): the new
+ * tokens are stored first, as in paged_attention_decode_append.
+ */
+PKV_EXPORT size_t paged_attention_decode_scored_workspace_size(int num_seqs, int num_heads, int head_dim,
+                                                               int max_seq_len);
+PKV_EXPORT pkv_status paged_attention_decode_scored(void *out, const void *q, const void *k_new, const void *v_new,
+                                                    void *k_cache, void *v_cache, const int32_t *block_tables,
+                                                    const int32_t *seq_lens, int num_seqs, int num_heads,
+                                                    int num_kv_heads, int head_dim, int block_size,
+                                                    int max_blocks_per_seq, int num_blocks, int max_seq_len,
+                                                    float scale, float softcap, const float *alibi_slopes,
+                                                    int window, const int32_t *prefix_lens,
+                                                    const int32_t *key_starts, void *workspace,
+                                                    size_t workspace_bytes, int dtype, void *stream);
+
+/*
+ * paged_attention_decode_scored_fp8_rows -- the same over a row-scaled FP8
+ * cache: ordinary attention over its values.  q and out are bf16; head_dim 64
+ * or 128, block_size 16 or 32.
+ */
+PKV_EXPORT pkv_status paged_attention_decode_scored_fp8_rows(
+    void *out, const void *q, const void *k_cache, const void *v_cache, const void *k_scales, const void *v_scales,
+    const int32_t *block_tables, const int32_t *seq_lens, int num_seqs, int num_heads, int num_kv_heads,
+    int head_dim, int block_size, int max_blocks_per_seq, int num_blocks, int max_seq_len, float scale,
+    float softcap, const float *alibi_slopes, int window, const int32_t *prefix_lens, const int32_t *key_starts,
+    void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * paged_attention_multi_token_scored -- the same for the last Q_s positions of
+ * every sequence (prefill, chunks of one, verification of drafted tokens);
+ * queries, q_starts and max_q_len as for paged_attention_multi_token (bf16).
+ * key_starts must not decrease over a sequence's queries (documents stand in
+ * order): a query whose entry is below an earlier one's may miss keys between
+ * the two.
+ */
+PKV_EXPORT size_t paged_attention_multi_token_scored_workspace_size(int num_q_tokens, int num_heads, int head_dim,
+                                                                    int max_seq_len);
+PKV_EXPORT pkv_status paged_attention_multi_token_scored(
+    void *out, const void *q, const void *k_cache, const void *v_cache, const int32_t *block_tables,
+    const int32_t *seq_lens, const int32_t *q_starts, int num_seqs, int num_q_tokens, int num_heads,
+    int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq, int num_blocks, int max_q_len,
+    int max_seq_len, float scale, float softcap, const float *alibi_slopes, int window,
+    const int32_t *prefix_lens, const int32_t *key_starts, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * block_copy -- copy whole physical blocks, in every layer, for K and V.
  *
  * Source: troisinh page, section "Copy-on-Write cho Beam Search": sequences

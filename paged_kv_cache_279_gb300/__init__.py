@@ -13,6 +13,9 @@ is no CPU or PyTorch fallback.
     paged_attention_multi_token(...)      # several causal query tokens per sequence
     kv_cache_write_fp8(...), paged_attention_decode_fp8(...),
     paged_attention_decode_append_fp8(...)  # E4M3 cache, per-tensor scales
+    kv_cache_write_fp8_rows(...), kv_cache_read_fp8_rows(...)  # E4M3 cache, a scale per row
+    paged_attention_decode_scored(...), paged_attention_decode_scored_fp8_rows(...),
+    paged_attention_multi_token_scored(...)  # capped or biased scores, windows, documents, prefixes
     block_copy(k_caches, v_caches, block_pairs)
     BlockAllocator(num_blocks, block_size)   # host allocator: CoW, prefix cache, truncation
 """
@@ -38,6 +41,9 @@ __all__ = [
     "paged_attention_decode_fp8", "paged_attention_decode_append_fp8", "paged_attention_workspace_size",
     "paged_attention_multi_token", "paged_attention_multi_token_workspace_size",
     "paged_attention_decode_append", "paged_attention_decode_grouped",
+    "kv_cache_write_fp8_rows", "kv_cache_read_fp8_rows", "paged_attention_decode_scored",
+    "paged_attention_decode_scored_fp8_rows", "paged_attention_decode_scored_workspace_size",
+    "paged_attention_multi_token_scored", "paged_attention_multi_token_scored_workspace_size",
     "paged_attention_grouped_workspace_size", "block_copy", "read_device_errors", "BlockAllocator",
     "library_path",
 ]
@@ -334,6 +340,205 @@ def paged_attention_decode_grouped(out, q, k_cache, v_cache, block_tables, seq_l
         G, S, Hq, Hkv, D, B, block_tables.shape[1], NB, int(max_seq_len), float(scale), ws_ptr, ws_bytes,
         _dtype_code(q), _stream(stream))
     _check(st, "paged_attention_decode_grouped")
+    return out
+
+
+class _On:
+    """The device of the call's tensors (all on one, else ValueError), made
+    current while the library is called, and the stream the call runs on (the
+    device's current stream when none is given)."""
+
+    def __init__(self, stream, **tensors):
+        given = {n: t for n, t in tensors.items() if t is not None}
+        devs = {t.device for t in given.values() if isinstance(t, torch.Tensor) and t.is_cuda}
+        if len(devs) > 1:
+            raise ValueError("tensors on several devices: " + ", ".join(f"{n} on {t.device}" for n, t in given.items()))
+        self.device = next(iter(devs), None)
+        self._stream = stream
+        self._guard = None
+
+    def __enter__(self):
+        if self.device is not None and self.device.index != torch.cuda.current_device():
+            self._guard = torch.cuda.device(self.device)
+            self._guard.__enter__()
+        self.stream = _stream(self._stream)
+        return self
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+        return False
+
+    def scratch(self, workspace, need: int):
+        """(address, bytes) of the caller's workspace, or of one taken here."""
+        if workspace is None:
+            if need == 0:
+                return None, 0
+            workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+            if self._stream is not None:  # its memory must outlive the work on that stream, not on the current one
+                s = self._stream if hasattr(self._stream, "cuda_stream") else torch.cuda.ExternalStream(int(self._stream))
+                workspace.record_stream(s)
+        return _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
+
+
+def _fp8_rows_args(lib_call: str, k, v, k_cache, v_cache, k_scales, v_scales, slot_mapping, stream) -> None:
+    NB, Hkv, B, D = k_cache.shape
+    T = k.shape[0]
+    if tuple(k.shape) != (T, Hkv, D) or k.shape != v.shape or v_cache.shape != k_cache.shape:
+        raise ValueError("shape mismatch between token rows and FP8 caches")
+    if tuple(k_scales.shape) != (NB, Hkv, B) or tuple(v_scales.shape) != (NB, Hkv, B):
+        raise ValueError("scales must be [NB, Hkv, B]")
+    if slot_mapping.shape[0] != T:
+        raise ValueError("slot_mapping needs one entry per token")
+    if v.dtype != k.dtype:
+        raise TypeError("K and V rows differ in dtype")
+    lib = _lib.load()
+    with _On(stream, k=k, v=v, k_cache=k_cache, v_cache=v_cache, k_scales=k_scales, v_scales=v_scales,
+             slot_mapping=slot_mapping) as on:
+        st = getattr(lib, lib_call)(
+            _dev(k, "K rows"), _dev(v, "V rows"), _dev(k_cache, "k_cache", torch.uint8),
+            _dev(v_cache, "v_cache", torch.uint8), _dev(k_scales, "k_scales", torch.uint8),
+            _dev(v_scales, "v_scales", torch.uint8), _dev(slot_mapping, "slot_mapping", torch.int64, 1), T, Hkv, D, B, NB,
+            _dtype_code(k), on.stream)
+    _check(st, lib_call)
+
+
+def kv_cache_write_fp8_rows(k_new, v_new, k_cache, v_cache, k_scales, v_scales, slot_mapping, stream=None) -> None:
+    """Quantise K/V rows [T, Hkv, D] (bf16 or float32) to E4M3 codes with one
+    power-of-two scale per row, chosen here, and store both: codes in k_cache /
+    v_cache uint8 [NB, Hkv, B, D], scales in k_scales / v_scales uint8
+    [NB, Hkv, B] (exponent + 127), at slot_mapping[t] (int64; negative = skip)."""
+    _fp8_rows_args("kv_cache_write_fp8_rows", k_new, v_new, k_cache, v_cache, k_scales, v_scales, slot_mapping, stream)
+
+
+def kv_cache_read_fp8_rows(k_out, v_out, k_cache, v_cache, k_scales, v_scales, slot_mapping, stream=None):
+    """The values of the cache rows at slot_mapping[t], into k_out / v_out
+    [T, Hkv, D] (bf16, exact, or float32).  Rows of negative slots are left as
+    they were.  Returns (k_out, v_out)."""
+    _fp8_rows_args("kv_cache_read_fp8_rows", k_out, v_out, k_cache, v_cache, k_scales, v_scales, slot_mapping, stream)
+    return k_out, v_out
+
+
+def paged_attention_decode_scored_workspace_size(num_seqs: int, num_heads: int, head_dim: int, max_seq_len: int) -> int:
+    return int(_lib.load().paged_attention_decode_scored_workspace_size(num_seqs, num_heads, head_dim, max_seq_len))
+
+
+def paged_attention_multi_token_scored_workspace_size(num_q_tokens: int, num_heads: int, head_dim: int,
+                                                      max_seq_len: int) -> int:
+    return int(_lib.load().paged_attention_multi_token_scored_workspace_size(num_q_tokens, num_heads, head_dim,
+                                                                             max_seq_len))
+
+
+def _scored_shapes(out, q, k_cache, v_cache, block_tables, seq_lens, num_queries, softcap, alibi_slopes, window,
+                   prefix_lens, key_starts):
+    T, Hq, D = q.shape
+    NB, Hkv, B, Dk = k_cache.shape
+    S = seq_lens.shape[0]
+    if Dk != D or tuple(out.shape) != (T, Hq, D) or v_cache.shape != k_cache.shape or T != num_queries:
+        raise ValueError("shape mismatch")
+    if block_tables.dim() != 2 or block_tables.shape[0] != S:
+        raise ValueError("block_tables must be [S, maxB] and seq_lens [S]")
+    if alibi_slopes is not None and tuple(alibi_slopes.shape) != (Hq,):
+        raise ValueError("alibi_slopes must be [Hq]")
+    if prefix_lens is not None and tuple(prefix_lens.shape) != (S,):
+        raise ValueError("prefix_lens must be [S]")
+    if key_starts is not None and tuple(key_starts.shape) != (T,):
+        raise ValueError("key_starts needs one entry per query")
+    return T, Hq, D, NB, Hkv, B, S
+
+
+def _score_ptrs(scale, softcap, alibi_slopes, window, prefix_lens, key_starts):
+    return (float(scale), float(softcap),
+            _dev(alibi_slopes, "alibi_slopes", torch.float32, 1) if alibi_slopes is not None else None, int(window),
+            _dev(prefix_lens, "prefix_lens", torch.int32, 1) if prefix_lens is not None else None,
+            _dev(key_starts, "key_starts", torch.int32, 1) if key_starts is not None else None)
+
+
+def paged_attention_decode_scored(out, q, k_cache, v_cache, block_tables, seq_lens, scale: float, max_seq_len: int,
+                                  softcap: float = 0.0, alibi_slopes=None, window: int = 0, prefix_lens=None,
+                                  key_starts=None, k_new=None, v_new=None, workspace: Optional[torch.Tensor] = None,
+                                  stream=None) -> torch.Tensor:
+    """paged_attention_decode with capped or biased scores and masked keys: with
+    p = seq_lens[s] - 1, x = scale * q.k, then softcap * tanh(x / softcap) if
+    softcap > 0, then - alibi_slopes[h] * (p - t) (float32 [Hq]); key t is seen
+    if t >= key_starts[s] and (t < prefix_lens[s] or window == 0 or
+    p - t < window) (int32 [S] each).  With k_new / v_new [S, Hkv, D] the new
+    tokens are stored first.  A query that sees nothing gets zeros."""
+    lib = _lib.load()
+    S, Hq, D, NB, Hkv, B, _ = _scored_shapes(out, q, k_cache, v_cache, block_tables, seq_lens, seq_lens.shape[0], softcap,
+                                             alibi_slopes, window, prefix_lens, key_starts)
+    if (k_new is None) != (v_new is None):
+        raise ValueError("give both k_new and v_new, or neither")
+    if k_new is not None and (tuple(k_new.shape) != (S, Hkv, D) or v_new.shape != k_new.shape):
+        raise ValueError("k_new/v_new must be [S, Hkv, D]")
+    dt = _dtype_code(q)
+    for t, n in ((out, "out"), (k_cache, "k_cache"), (v_cache, "v_cache"), (k_new, "k_new"), (v_new, "v_new")):
+        if t is not None and t.dtype != q.dtype:
+            raise TypeError(f"{n} dtype differs from q")
+    with _On(stream, out=out, q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, seq_lens=seq_lens,
+             alibi_slopes=alibi_slopes, prefix_lens=prefix_lens, key_starts=key_starts, k_new=k_new, v_new=v_new,
+             workspace=workspace) as on:
+        ws, ws_bytes = on.scratch(workspace, paged_attention_decode_scored_workspace_size(S, Hq, D, max_seq_len))
+        st = lib.paged_attention_decode_scored(
+            _dev(out, "out"), _dev(q, "q"), _dev(k_new, "k_new") if k_new is not None else None,
+            _dev(v_new, "v_new") if v_new is not None else None, _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
+            _dev(block_tables, "block_tables", torch.int32, 2), _dev(seq_lens, "seq_lens", torch.int32, 1), S, Hq, Hkv, D,
+            B, block_tables.shape[1], NB, int(max_seq_len),
+            *_score_ptrs(scale, softcap, alibi_slopes, window, prefix_lens, key_starts), ws, ws_bytes, dt, on.stream)
+    _check(st, "paged_attention_decode_scored")
+    return out
+
+
+def paged_attention_decode_scored_fp8_rows(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens,
+                                           scale: float, max_seq_len: int, softcap: float = 0.0, alibi_slopes=None,
+                                           window: int = 0, prefix_lens=None, key_starts=None,
+                                           workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """paged_attention_decode_scored over a row-scaled FP8 cache (codes uint8
+    [NB, Hkv, B, D], scales uint8 [NB, Hkv, B]); q / out bf16 [S, Hq, D]."""
+    lib = _lib.load()
+    S, Hq, D, NB, Hkv, B, _ = _scored_shapes(out, q, k_cache, v_cache, block_tables, seq_lens, seq_lens.shape[0], softcap,
+                                             alibi_slopes, window, prefix_lens, key_starts)
+    if tuple(k_scales.shape) != (NB, Hkv, B) or tuple(v_scales.shape) != (NB, Hkv, B):
+        raise ValueError("scales must be [NB, Hkv, B]")
+    with _On(stream, out=out, q=q, k_cache=k_cache, v_cache=v_cache, k_scales=k_scales, v_scales=v_scales,
+             block_tables=block_tables, seq_lens=seq_lens, alibi_slopes=alibi_slopes, prefix_lens=prefix_lens,
+             key_starts=key_starts, workspace=workspace) as on:
+        ws, ws_bytes = on.scratch(workspace, paged_attention_decode_scored_workspace_size(S, Hq, D, max_seq_len))
+        st = lib.paged_attention_decode_scored_fp8_rows(
+            _dev(out, "out", torch.bfloat16), _dev(q, "q", torch.bfloat16), _dev(k_cache, "k_cache", torch.uint8),
+            _dev(v_cache, "v_cache", torch.uint8), _dev(k_scales, "k_scales", torch.uint8),
+            _dev(v_scales, "v_scales", torch.uint8), _dev(block_tables, "block_tables", torch.int32, 2),
+            _dev(seq_lens, "seq_lens", torch.int32, 1), S, Hq, Hkv, D, B, block_tables.shape[1], NB, int(max_seq_len),
+            *_score_ptrs(scale, softcap, alibi_slopes, window, prefix_lens, key_starts), ws, ws_bytes, on.stream)
+    _check(st, "paged_attention_decode_scored_fp8_rows")
+    return out
+
+
+def paged_attention_multi_token_scored(out, q, k_cache, v_cache, block_tables, seq_lens, q_starts, scale: float,
+                                       max_q_len: int, max_seq_len: int, softcap: float = 0.0, alibi_slopes=None,
+                                       window: int = 0, prefix_lens=None, key_starts=None,
+                                       workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """paged_attention_multi_token with capped or biased scores and masked keys
+    (see paged_attention_decode_scored): a query at position p sees key t if
+    t >= key_starts[row] (int32 [T], not decreasing over a sequence's queries)
+    and (t < prefix_lens[s], or t <= p and (window == 0 or p - t < window)); the
+    bias is - alibi_slopes[h] * |p - t|."""
+    lib = _lib.load()
+    T, Hq, D, NB, Hkv, B, S = _scored_shapes(out, q, k_cache, v_cache, block_tables, seq_lens, q.shape[0], softcap,
+                                             alibi_slopes, window, prefix_lens, key_starts)
+    if tuple(q_starts.shape) != (S + 1,):
+        raise ValueError("q_starts must be [S + 1]")
+    with _On(stream, out=out, q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, seq_lens=seq_lens,
+             q_starts=q_starts, alibi_slopes=alibi_slopes, prefix_lens=prefix_lens, key_starts=key_starts,
+             workspace=workspace) as on:
+        ws, ws_bytes = on.scratch(workspace, paged_attention_multi_token_scored_workspace_size(T, Hq, D, max_seq_len))
+        st = lib.paged_attention_multi_token_scored(
+            _dev(out, "out", torch.bfloat16), _dev(q, "q", torch.bfloat16), _dev(k_cache, "k_cache", torch.bfloat16),
+            _dev(v_cache, "v_cache", torch.bfloat16), _dev(block_tables, "block_tables", torch.int32, 2),
+            _dev(seq_lens, "seq_lens", torch.int32, 1), _dev(q_starts, "q_starts", torch.int32, 1), S, T, Hq, Hkv, D, B,
+            block_tables.shape[1], NB, int(max_q_len), int(max_seq_len),
+            *_score_ptrs(scale, softcap, alibi_slopes, window, prefix_lens, key_starts), ws, ws_bytes, on.stream)
+    _check(st, "paged_attention_multi_token_scored")
     return out
 
 

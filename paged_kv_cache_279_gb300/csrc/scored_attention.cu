@@ -1,0 +1,384 @@
+// Scored attention over the paged cache: attention whose scores are capped by
+// a tanh or biased by distance and whose keys are limited by a window, a
+// document's start and an always visible prefix (scored.cuh has the rules).
+//   * scored_simt_kernel -- one CTA per (query, kv head, 512-token partition)
+//     on CUDA cores, float32 arithmetic with expf and tanhf whatever the
+//     storage; scored_reduce_kernel merges the partitions.
+//
+// With x_t the score of a seen key in base 2 and f_t its V row's scale (1 for
+// plain caches), the running state of a row is (M, l, o) with M = max_t x_t,
+// l = sum 2^(x_t - M), o = sum 2^(x_t - M) f_t v_t; states merge by rescaling
+// to the larger M, and the result is o / l (zeros when nothing is seen).
+#include <algorithm>
+#include <climits>
+#include <cmath>
+
+#include "pkv_internal.cuh"
+#include "scored.cuh"
+
+namespace pkv {
+namespace scored {
+
+constexpr int kGMax = 8;         // query heads per KV head
+constexpr int kPartition = 512;  // tokens per CTA of the CUDA-core kernel
+
+enum Storage { kF32 = 0, kBf16 = 1, kFp8Rows = 2 };
+
+struct Args {
+    void *out;
+    const void *q;
+    const void *k_cache, *v_cache;
+    const unsigned char *k_scales, *v_scales;  // row-scaled FP8 cache
+    const int32_t *block_tables, *seq_lens;
+    const int32_t *q_starts;  // nullptr: one query per sequence
+    float *part_o;            // [queries][Hq][parts][D]
+    float *part_ml;           // [queries][Hq][parts][2]
+    int num_seqs, num_q, max_q_len, num_heads, num_kv_heads, group, block_size, max_blocks, num_blocks, max_seq_len, parts;
+    ScoreArgs s;
+    unsigned int *err;
+};
+
+// The query of a CTA: sequence, row of q and out, position, context length.
+struct Query {
+    int seq, row, pos, len;
+};
+
+// False: nothing to do (past the sequence's queries, or a bad description).
+__device__ __forceinline__ bool find_query(const Args &a, int x, Query &w, bool report) {
+    const int cap = min(a.max_seq_len, a.max_blocks * a.block_size);
+    int q0 = x, nq = 1, i = 0;
+    w.seq = x;
+    if (a.q_starts) {
+        w.seq = x / a.max_q_len;
+        i = x - w.seq * a.max_q_len;
+        q0 = a.q_starts[w.seq];
+        const int q1 = a.q_starts[w.seq + 1];
+        if (q0 < 0 || q1 < q0 || q1 > a.num_q) {
+            if (report && i == 0) flag_error(a.err, PKV_DEVERR_SEQ_LEN);
+            return false;
+        }
+        nq = q1 - q0;
+    }
+    const int raw = a.seq_lens[w.seq];
+    w.len = raw < 0 ? 0 : min(raw, cap);
+    if (report && i == 0 && (raw != w.len || (a.q_starts && (nq > a.max_q_len || nq > w.len))))
+        flag_error(a.err, PKV_DEVERR_SEQ_LEN);
+    if (i >= nq) return false;
+    w.row = q0 + i;
+    w.pos = w.len - nq + i;
+    return true;
+}
+
+template <typename T>
+__device__ __forceinline__ void put(T *p, float x);
+template <>
+__device__ __forceinline__ void put<float>(float *p, float x) { *p = x; }
+template <>
+__device__ __forceinline__ void put<__nv_bfloat16>(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
+__device__ __forceinline__ float get(float x) { return x; }
+__device__ __forceinline__ float get(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// Element d of a cache row.
+template <int ST>
+__device__ __forceinline__ float cached(const void *c, int64_t i) {
+    if constexpr (ST == kF32) return static_cast<const float *>(c)[i];
+    else if constexpr (ST == kBf16) return __bfloat162float(static_cast<const __nv_bfloat16 *>(c)[i]);
+    else {
+        float x[4];
+        e4m3x4_to_float(static_cast<const unsigned char *>(c)[i], x);
+        return x[0];
+    }
+}
+
+template <int ST, int D>
+__global__ void __launch_bounds__(128) scored_simt_kernel(const Args a) {
+    using T = typename std::conditional<ST == kF32, float, __nv_bfloat16>::type;
+    constexpr int NW = 4, E = D / 32;
+    __shared__ float so[NW][kGMax * D], sm[NW][kGMax], sl[NW][kGMax];
+    grid_dependency_wait();
+    grid_launch_dependents();
+    Query w;
+    const int kvh = blockIdx.y, part = blockIdx.z, G = a.group, B = a.block_size;
+    if (!find_query(a, blockIdx.x, w, kvh == 0 && part == 0 && threadIdx.x == 0)) return;
+    const int t0 = part * kPartition, t1 = min(w.len, t0 + kPartition);
+    if (part > 0 && t0 >= w.len) return;
+    const KeyRange kr = key_range(a.s, w.seq, w.row, w.pos, w.len);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    float qf[kGMax][E], o[kGMax][E], m[kGMax], l[kGMax], slope[kGMax];
+    const T *qb = static_cast<const T *>(a.q) + ((int64_t)w.row * a.num_heads + kvh * G) * D;
+#pragma unroll
+    for (int g = 0; g < kGMax; ++g) {
+        m[g] = -INFINITY;
+        l[g] = 0.f;
+        slope[g] = a.s.slopes && g < G ? a.s.slopes[kvh * G + g] : 0.f;
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            qf[g][j] = g < G ? get(qb[g * D + lane + 32 * j]) : 0.f;
+            o[g][j] = 0.f;
+        }
+    }
+    const int32_t *bt = a.block_tables + (int64_t)w.seq * a.max_blocks;
+    if (kr.meets(t0, t1)) {
+        for (int t = t0 + warp; t < t1; t += NW) {
+            if (!kr.sees(t)) continue;
+            const int lb = t / B, blk = bt[lb];
+            if (blk < 0 || blk >= a.num_blocks) {
+                if (lane == 0) flag_error(a.err, PKV_DEVERR_BLOCK_ID);
+                continue;
+            }
+            const int64_t row = ((int64_t)blk * a.num_kv_heads + kvh) * B + (t - lb * B);
+            float kf[E], vf[E], kscale = 1.f, vscale = 1.f;
+            if constexpr (ST == kFp8Rows) {
+                kscale = row_scale(a.k_scales[row]);
+                vscale = row_scale(a.v_scales[row]);
+            }
+#pragma unroll
+            for (int j = 0; j < E; ++j) {
+                kf[j] = cached<ST>(a.k_cache, row * D + lane + 32 * j) * kscale;
+                vf[j] = cached<ST>(a.v_cache, row * D + lane + 32 * j) * vscale;
+            }
+            const float away = (float)abs(w.pos - t);
+#pragma unroll
+            for (int g = 0; g < kGMax; ++g) {
+                if (g >= G) break;
+                float x = 0.f;
+#pragma unroll
+                for (int j = 0; j < E; ++j) x = fmaf(qf[g][j], kf[j], x);
+#pragma unroll
+                for (int sh = 16; sh > 0; sh >>= 1) x += __shfl_xor_sync(0xffffffffu, x, sh);
+                x *= a.s.scale;
+                if (a.s.softcap > 0.f) x = a.s.softcap * tanhf(x / a.s.softcap);
+                x -= slope[g] * away;
+                const float mn = fmaxf(m[g], x);
+                const float al = m[g] == mn ? 1.f : expf(m[g] - mn), p = expf(x - mn);
+                l[g] = l[g] * al + p;
+#pragma unroll
+                for (int j = 0; j < E; ++j) o[g][j] = fmaf(p, vf[j], o[g][j] * al);
+                m[g] = mn;
+            }
+        }
+    }
+#pragma unroll
+    for (int g = 0; g < kGMax; ++g) {
+#pragma unroll
+        for (int j = 0; j < E; ++j) so[warp][g * D + lane + 32 * j] = o[g][j];
+        if (lane == 0) {
+            sm[warp][g] = m[g];
+            sl[warp][g] = l[g];
+        }
+    }
+    __syncthreads();
+    const bool whole = w.len <= kPartition;
+    for (int i = threadIdx.x; i < G * D; i += 128) {
+        const int g = i / D, d = i % D;
+        float M = -INFINITY, L = 0.f, O = 0.f;
+#pragma unroll
+        for (int k = 0; k < NW; ++k) M = fmaxf(M, sm[k][g]);
+#pragma unroll
+        for (int k = 0; k < NW; ++k) {
+            if (sl[k][g] == 0.f) continue;  // a warp that saw nothing
+            const float c = sm[k][g] == M ? 1.f : expf(sm[k][g] - M);
+            O = fmaf(c, so[k][g * D + d], O);
+            L = fmaf(c, sl[k][g], L);
+        }
+        const int64_t row = (int64_t)w.row * a.num_heads + kvh * G + g;
+        if (whole) {
+            put(static_cast<T *>(a.out) + row * D + d, L != 0.f ? O / L : 0.f);
+        } else {
+            const int64_t p = row * a.parts + part;
+            a.part_o[p * D + d] = O;
+            if (d == 0) {
+                a.part_ml[2 * p] = M;
+                a.part_ml[2 * p + 1] = L;
+            }
+        }
+    }
+}
+
+// One warp per (query, head): the partitions' states, merged in order.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) scored_reduce_kernel(const Args a) {
+    constexpr int E = D / 32;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    const int64_t total = (int64_t)(a.q_starts ? (int64_t)a.num_seqs * a.max_q_len : a.num_seqs) * a.num_heads;
+    if (r >= total) return;
+    Query w;
+    if (!find_query(a, (int)(r / a.num_heads), w, false) || w.len <= kPartition) return;
+    const int64_t row = (int64_t)w.row * a.num_heads + r % a.num_heads;
+    const int n = (w.len + kPartition - 1) / kPartition;
+    const float *ml = a.part_ml + row * a.parts * 2, *po = a.part_o + row * a.parts * D + lane;
+    float M = -INFINITY, L = 0.f, o[E];
+    for (int j = 0; j < n; ++j) M = fmaxf(M, ml[2 * j]);
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+    for (int j = 0; j < n; ++j) {
+        if (ml[2 * j + 1] == 0.f) continue;
+        const float c = ml[2 * j] == M ? 1.f : expf(ml[2 * j] - M);
+        L = fmaf(c, ml[2 * j + 1], L);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(c, po[(int64_t)j * D + 32 * e], o[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) put(static_cast<T *>(a.out) + row * D + lane + 32 * e, L != 0.f ? o[e] / L : 0.f);
+}
+
+static size_t simt_workspace(int64_t queries, int64_t heads, int64_t D, int64_t max_seq_len) {
+    const int64_t parts = (max_seq_len + kPartition - 1) / kPartition;
+    return parts <= 1 ? 0 : round256((size_t)(queries * heads * parts * D * 4)) + round256((size_t)(queries * heads * parts * 8));
+}
+
+template <int ST, int D>
+static pkv_status run_simt(Args a, void *workspace, size_t bytes, cudaStream_t st) {
+    using T = typename std::conditional<ST == kF32, float, __nv_bfloat16>::type;
+    const int64_t x = a.q_starts ? (int64_t)a.num_seqs * a.max_q_len : a.num_seqs;
+    a.parts = std::max(1, (a.max_seq_len + kPartition - 1) / kPartition);
+    if (x > INT32_MAX || a.num_kv_heads > 65535 || a.parts > 65535) return PKV_ERR_UNSUPPORTED;
+    if (a.parts > 1) {
+        if (!workspace || bytes < simt_workspace(a.num_q, a.num_heads, D, a.max_seq_len) ||
+            (reinterpret_cast<uintptr_t>(workspace) & 255u))
+            return PKV_ERR_INVALID;
+        a.part_o = static_cast<float *>(workspace);
+        a.part_ml = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) +
+                                              round256((size_t)a.num_q * a.num_heads * a.parts * D * 4));
+    }
+    const dim3 grid((unsigned)x, (unsigned)a.num_kv_heads, (unsigned)a.parts);
+    pkv_status rc = launch_pdl(scored_simt_kernel<ST, D>, grid, dim3(128), 0, st, a);
+    if (rc == PKV_OK && a.parts > 1)
+        rc = launch_pdl(scored_reduce_kernel<T, D>, dim3((unsigned)((x * a.num_heads + 3) / 4)), dim3(128), 0, st, a);
+    return rc;
+}
+
+// Checks that the three calls share; *empty: valid, and nothing to do.
+static pkv_status check(const Args &a, int head_dim, int dtype, bool fp8, bool *empty) {
+    *empty = false;
+    if (a.num_seqs < 0 || a.num_q < 0 || a.num_heads < 1 || a.num_kv_heads < 1 || a.max_blocks < 1 || a.num_blocks < 1 ||
+        a.max_seq_len < 0 || a.max_q_len < 0 || !std::isfinite(a.s.scale) || !std::isfinite(a.s.softcap) ||
+        a.s.softcap < 0.f || a.s.window < 0)
+        return PKV_ERR_INVALID;
+    if (a.num_heads % a.num_kv_heads != 0) return PKV_ERR_INVALID;
+    if (dtype != PKV_F32 && dtype != PKV_BF16) return PKV_ERR_UNSUPPORTED;
+    if (head_dim != 64 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
+    if (a.block_size != 16 && a.block_size != 32 && (fp8 || a.block_size != 8)) return PKV_ERR_UNSUPPORTED;
+    if (a.num_heads / a.num_kv_heads > kGMax) return PKV_ERR_UNSUPPORTED;
+    if (a.num_seqs == 0 || a.num_q == 0) {
+        *empty = true;
+        return PKV_OK;
+    }
+    if (!a.out || !a.q || !a.k_cache || !a.v_cache || !a.block_tables || !a.seq_lens) return PKV_ERR_INVALID;
+    if (!aligned16(a.out) || !aligned16(a.q) || !aligned16(a.k_cache) || !aligned16(a.v_cache)) return PKV_ERR_INVALID;
+    if (fp8 && (!a.k_scales || !a.v_scales || !aligned16(a.k_scales) || !aligned16(a.v_scales))) return PKV_ERR_INVALID;
+    // TMA row coordinates are 32-bit, positions too
+    if (((int64_t)a.num_blocks + 1) * a.num_kv_heads * a.block_size > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+    if ((int64_t)a.max_blocks * a.block_size > INT32_MAX) return PKV_ERR_INVALID;
+    return PKV_OK;
+}
+
+}  // namespace scored
+
+pkv_status append_new_tokens(const void *k_new, const void *v_new, void *k_cache, void *v_cache,
+                             const int32_t *block_tables, const int32_t *seq_lens, int num_seqs, int num_kv_heads,
+                             int head_dim, int block_size, int max_blocks_per_seq, int num_blocks, int max_seq_len,
+                             int dtype, cudaStream_t st);
+
+}  // namespace pkv
+
+using namespace pkv;
+
+PKV_API size_t paged_attention_decode_scored_workspace_size(int num_seqs, int num_heads, int head_dim, int max_seq_len) {
+    if (num_seqs <= 0 || num_heads <= 0 || head_dim <= 0 || max_seq_len <= 0) return 0;
+    return scored::simt_workspace(num_seqs, num_heads, head_dim, max_seq_len);
+}
+
+PKV_API size_t paged_attention_multi_token_scored_workspace_size(int num_q_tokens, int num_heads, int head_dim,
+                                                                 int max_seq_len) {
+    if (num_q_tokens <= 0 || num_heads <= 0 || head_dim <= 0 || max_seq_len <= 0) return 0;
+    return scored::simt_workspace(num_q_tokens, num_heads, head_dim, max_seq_len);
+}
+
+PKV_API pkv_status paged_attention_decode_scored(void *out, const void *q, const void *k_new, const void *v_new,
+                                                 void *k_cache, void *v_cache, const int32_t *block_tables,
+                                                 const int32_t *seq_lens, int num_seqs, int num_heads, int num_kv_heads,
+                                                 int head_dim, int block_size, int max_blocks_per_seq, int num_blocks,
+                                                 int max_seq_len, float scale, float softcap, const float *alibi_slopes,
+                                                 int window, const int32_t *prefix_lens, const int32_t *key_starts,
+                                                 void *workspace, size_t workspace_bytes, int dtype, void *stream) {
+    scored::Args a{};
+    a.out = out, a.q = q, a.k_cache = k_cache, a.v_cache = v_cache;
+    a.block_tables = block_tables, a.seq_lens = seq_lens;
+    a.num_seqs = a.num_q = num_seqs, a.num_heads = num_heads, a.num_kv_heads = num_kv_heads;
+    a.group = num_kv_heads > 0 ? num_heads / num_kv_heads : 0;
+    a.block_size = block_size, a.max_blocks = max_blocks_per_seq, a.num_blocks = num_blocks, a.max_seq_len = max_seq_len;
+    a.max_q_len = 1;
+    a.s = ScoreArgs{scale, softcap, alibi_slopes, window, prefix_lens, key_starts};
+    bool empty;
+    pkv_status rc = scored::check(a, head_dim, dtype, false, &empty);
+    if (rc != PKV_OK || empty) return rc;
+    if ((k_new == nullptr) != (v_new == nullptr) || !aligned16(k_new) || !aligned16(v_new)) return PKV_ERR_INVALID;
+    if (k_new && max_seq_len < 1) return PKV_ERR_INVALID;  // every context holds at least its new token
+    a.err = device_error_word();
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (!workspace && paged_attention_decode_scored_workspace_size(num_seqs, num_heads, head_dim, max_seq_len) > 0)
+        return PKV_ERR_INVALID;
+    if (k_new) {
+        rc = append_new_tokens(k_new, v_new, k_cache, v_cache, block_tables, seq_lens, num_seqs, num_kv_heads, head_dim,
+                               block_size, max_blocks_per_seq, num_blocks, max_seq_len, dtype, st);
+        if (rc != PKV_OK) return rc;
+    }
+    if (dtype == PKV_F32)
+        return head_dim == 128 ? scored::run_simt<scored::kF32, 128>(a, workspace, workspace_bytes, st)
+                               : scored::run_simt<scored::kF32, 64>(a, workspace, workspace_bytes, st);
+    return head_dim == 128 ? scored::run_simt<scored::kBf16, 128>(a, workspace, workspace_bytes, st)
+                           : scored::run_simt<scored::kBf16, 64>(a, workspace, workspace_bytes, st);
+}
+
+PKV_API pkv_status paged_attention_decode_scored_fp8_rows(
+    void *out, const void *q, const void *k_cache, const void *v_cache, const void *k_scales, const void *v_scales,
+    const int32_t *block_tables, const int32_t *seq_lens, int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+    int block_size, int max_blocks_per_seq, int num_blocks, int max_seq_len, float scale, float softcap,
+    const float *alibi_slopes, int window, const int32_t *prefix_lens, const int32_t *key_starts, void *workspace,
+    size_t workspace_bytes, void *stream) {
+    scored::Args a{};
+    a.out = out, a.q = q, a.k_cache = k_cache, a.v_cache = v_cache;
+    a.k_scales = static_cast<const unsigned char *>(k_scales), a.v_scales = static_cast<const unsigned char *>(v_scales);
+    a.block_tables = block_tables, a.seq_lens = seq_lens;
+    a.num_seqs = a.num_q = num_seqs, a.num_heads = num_heads, a.num_kv_heads = num_kv_heads;
+    a.group = num_kv_heads > 0 ? num_heads / num_kv_heads : 0;
+    a.block_size = block_size, a.max_blocks = max_blocks_per_seq, a.num_blocks = num_blocks, a.max_seq_len = max_seq_len;
+    a.max_q_len = 1;
+    a.s = ScoreArgs{scale, softcap, alibi_slopes, window, prefix_lens, key_starts};
+    bool empty;
+    const pkv_status rc = scored::check(a, head_dim, PKV_BF16, true, &empty);
+    if (rc != PKV_OK || empty) return rc;
+    a.err = device_error_word();
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return head_dim == 128 ? scored::run_simt<scored::kFp8Rows, 128>(a, workspace, workspace_bytes, st)
+                           : scored::run_simt<scored::kFp8Rows, 64>(a, workspace, workspace_bytes, st);
+}
+
+PKV_API pkv_status paged_attention_multi_token_scored(
+    void *out, const void *q, const void *k_cache, const void *v_cache, const int32_t *block_tables,
+    const int32_t *seq_lens, const int32_t *q_starts, int num_seqs, int num_q_tokens, int num_heads, int num_kv_heads,
+    int head_dim, int block_size, int max_blocks_per_seq, int num_blocks, int max_q_len, int max_seq_len, float scale,
+    float softcap, const float *alibi_slopes, int window, const int32_t *prefix_lens, const int32_t *key_starts,
+    void *workspace, size_t workspace_bytes, void *stream) {
+    scored::Args a{};
+    a.out = out, a.q = q, a.k_cache = k_cache, a.v_cache = v_cache;
+    a.block_tables = block_tables, a.seq_lens = seq_lens, a.q_starts = q_starts;
+    a.num_seqs = num_seqs, a.num_q = num_q_tokens, a.num_heads = num_heads, a.num_kv_heads = num_kv_heads;
+    a.group = num_kv_heads > 0 ? num_heads / num_kv_heads : 0;
+    a.block_size = block_size, a.max_blocks = max_blocks_per_seq, a.num_blocks = num_blocks, a.max_seq_len = max_seq_len;
+    a.max_q_len = max_q_len;
+    a.s = ScoreArgs{scale, softcap, alibi_slopes, window, prefix_lens, key_starts};
+    bool empty;
+    const pkv_status rc = scored::check(a, head_dim, PKV_BF16, false, &empty);
+    if (rc != PKV_OK || empty) return rc;
+    if (!q_starts || max_q_len < 1) return PKV_ERR_INVALID;
+    a.err = device_error_word();
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return head_dim == 128 ? scored::run_simt<scored::kBf16, 128>(a, workspace, workspace_bytes, st)
+                           : scored::run_simt<scored::kBf16, 64>(a, workspace, workspace_bytes, st);
+}
