@@ -45,9 +45,8 @@ struct ScoreArgs {
     const int32_t *key_starts;    // [queries] or nullptr: keys t < key_start are not seen
 };
 
-// The keys that the query at position p of a context of len tokens sees:
-// [first, pre) and [lo, hi), the first empty where the two would meet or
-// overlap (then it is part of the second).
+// The keys that a query sees: [first, pre) and [lo, hi), the first empty where
+// the two would meet or overlap (then it is part of the second).
 struct KeyRange {
     int first, pre, lo, hi;
     __device__ __forceinline__ bool sees(int t) const { return (t >= lo && t < hi) || (t >= first && t < pre); }
@@ -56,24 +55,57 @@ struct KeyRange {
     }
 };
 
-__device__ __forceinline__ KeyRange key_range(const ScoreArgs &s, int seq, int64_t query, int p, int len) {
+// ks: the query's first key, pre: the sequence's prefix, both clamped; p0 .. p1:
+// the position (a query) or positions (a block of queries, the union of their
+// keys), p1 < len.
+__device__ __forceinline__ KeyRange key_range(int ks, int pre, int window, int p0, int p1) {
     KeyRange r;
-    const int ks = s.key_starts ? max(0, s.key_starts[query]) : 0;
-    const int pre = s.prefix_lens ? min(max(0, s.prefix_lens[seq]), len) : 0;
-    r.lo = max(ks, s.window > 0 ? p - s.window + 1 : 0);
-    r.hi = p + 1;  // p < len
     r.first = ks;
     r.pre = pre;
-    if (r.lo >= r.hi) {  // no key at or before p
-        r.lo = r.first;
-        r.hi = max(r.first, pre);
-        r.pre = r.first;
+    r.lo = max(ks, window > 0 ? p0 - window + 1 : 0);
+    r.hi = p1 + 1;
+    if (r.lo >= r.hi) {  // no key at or before p1
+        r.lo = ks;
+        r.hi = max(ks, pre);
+        r.pre = ks;
     } else if (pre >= r.lo) {
-        r.lo = min(r.lo, r.first);
+        r.lo = ks;
         r.hi = max(r.hi, pre);
-        r.pre = r.first;
+        r.pre = ks;
     }
     return r;
 }
 
+__device__ __forceinline__ int key_start_of(const ScoreArgs &s, int64_t query) {
+    return s.key_starts ? max(0, s.key_starts[query]) : 0;
+}
+__device__ __forceinline__ int prefix_of(const ScoreArgs &s, int seq, int len) {
+    return s.prefix_lens ? min(max(0, s.prefix_lens[seq]), len) : 0;
+}
+
+namespace scored {
+
+constexpr int kGMax = 8;  // query heads per KV head
+
+// A call's arguments, shared by every kernel of it.
+struct Args {
+    void *out;
+    const void *q;
+    const void *k_cache, *v_cache;
+    const unsigned char *k_scales, *v_scales;  // row-scaled FP8 cache
+    const int32_t *block_tables, *seq_lens;
+    const int32_t *q_starts;  // nullptr: one query per sequence
+    int num_seqs, num_q, max_q_len, num_heads, num_kv_heads, group, block_size, max_blocks, num_blocks, max_seq_len;
+    ScoreArgs s;
+    unsigned int *err;
+};
+
+// Checks that the calls share; *empty: valid, and nothing to do.
+pkv_status check(const Args &a, int head_dim, int dtype, bool fp8, bool *empty);
+
+// Several queries per sequence on the tensor cores (scored_rows.cu).
+size_t rows_workspace(int head_dim);
+pkv_status run_rows(const Args &a, int head_dim, void *workspace, size_t workspace_bytes, cudaStream_t st);
+
+}  // namespace scored
 }  // namespace pkv

@@ -19,23 +19,14 @@
 namespace pkv {
 namespace scored {
 
-constexpr int kGMax = 8;         // query heads per KV head
 constexpr int kPartition = 512;  // tokens per CTA of the CUDA-core kernel
 
 enum Storage { kF32 = 0, kBf16 = 1, kFp8Rows = 2 };
 
-struct Args {
-    void *out;
-    const void *q;
-    const void *k_cache, *v_cache;
-    const unsigned char *k_scales, *v_scales;  // row-scaled FP8 cache
-    const int32_t *block_tables, *seq_lens;
-    const int32_t *q_starts;  // nullptr: one query per sequence
-    float *part_o;            // [queries][Hq][parts][D]
-    float *part_ml;           // [queries][Hq][parts][2]
-    int num_seqs, num_q, max_q_len, num_heads, num_kv_heads, group, block_size, max_blocks, num_blocks, max_seq_len, parts;
-    ScoreArgs s;
-    unsigned int *err;
+struct SimtArgs : Args {
+    float *part_o;   // [queries][Hq][parts][D]
+    float *part_ml;  // [queries][Hq][parts][2]
+    int parts;
 };
 
 // The query of a CTA: sequence, row of q and out, position, context length.
@@ -91,7 +82,7 @@ __device__ __forceinline__ float cached(const void *c, int64_t i) {
 }
 
 template <int ST, int D>
-__global__ void __launch_bounds__(128) scored_simt_kernel(const Args a) {
+__global__ void __launch_bounds__(128) scored_simt_kernel(const SimtArgs a) {
     using T = typename std::conditional<ST == kF32, float, __nv_bfloat16>::type;
     constexpr int NW = 4, E = D / 32;
     __shared__ float so[NW][kGMax * D], sm[NW][kGMax], sl[NW][kGMax];
@@ -102,7 +93,7 @@ __global__ void __launch_bounds__(128) scored_simt_kernel(const Args a) {
     if (!find_query(a, blockIdx.x, w, kvh == 0 && part == 0 && threadIdx.x == 0)) return;
     const int t0 = part * kPartition, t1 = min(w.len, t0 + kPartition);
     if (part > 0 && t0 >= w.len) return;
-    const KeyRange kr = key_range(a.s, w.seq, w.row, w.pos, w.len);
+    const KeyRange kr = key_range(key_start_of(a.s, w.row), prefix_of(a.s, w.seq, w.len), a.s.window, w.pos, w.pos);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     float qf[kGMax][E], o[kGMax][E], m[kGMax], l[kGMax], slope[kGMax];
@@ -198,7 +189,7 @@ __global__ void __launch_bounds__(128) scored_simt_kernel(const Args a) {
 
 // One warp per (query, head): the partitions' states, merged in order.
 template <typename T, int D>
-__global__ void __launch_bounds__(128) scored_reduce_kernel(const Args a) {
+__global__ void __launch_bounds__(128) scored_reduce_kernel(const SimtArgs a) {
     constexpr int E = D / 32;
     grid_dependency_wait();
     grid_launch_dependents();
@@ -232,8 +223,10 @@ static size_t simt_workspace(int64_t queries, int64_t heads, int64_t D, int64_t 
 }
 
 template <int ST, int D>
-static pkv_status run_simt(Args a, void *workspace, size_t bytes, cudaStream_t st) {
+static pkv_status run_simt(const Args &args, void *workspace, size_t bytes, cudaStream_t st) {
     using T = typename std::conditional<ST == kF32, float, __nv_bfloat16>::type;
+    SimtArgs a{};
+    static_cast<Args &>(a) = args;
     const int64_t x = a.q_starts ? (int64_t)a.num_seqs * a.max_q_len : a.num_seqs;
     a.parts = std::max(1, (a.max_seq_len + kPartition - 1) / kPartition);
     if (x > INT32_MAX || a.num_kv_heads > 65535 || a.parts > 65535) return PKV_ERR_UNSUPPORTED;
@@ -252,8 +245,7 @@ static pkv_status run_simt(Args a, void *workspace, size_t bytes, cudaStream_t s
     return rc;
 }
 
-// Checks that the three calls share; *empty: valid, and nothing to do.
-static pkv_status check(const Args &a, int head_dim, int dtype, bool fp8, bool *empty) {
+pkv_status check(const Args &a, int head_dim, int dtype, bool fp8, bool *empty) {
     *empty = false;
     if (a.num_seqs < 0 || a.num_q < 0 || a.num_heads < 1 || a.num_kv_heads < 1 || a.max_blocks < 1 || a.num_blocks < 1 ||
         a.max_seq_len < 0 || a.max_q_len < 0 || !std::isfinite(a.s.scale) || !std::isfinite(a.s.softcap) ||
@@ -296,7 +288,8 @@ PKV_API size_t paged_attention_decode_scored_workspace_size(int num_seqs, int nu
 PKV_API size_t paged_attention_multi_token_scored_workspace_size(int num_q_tokens, int num_heads, int head_dim,
                                                                  int max_seq_len) {
     if (num_q_tokens <= 0 || num_heads <= 0 || head_dim <= 0 || max_seq_len <= 0) return 0;
-    return scored::simt_workspace(num_q_tokens, num_heads, head_dim, max_seq_len);
+    if (head_dim != 64 && head_dim != 128) return 0;
+    return scored::rows_workspace(head_dim);
 }
 
 PKV_API pkv_status paged_attention_decode_scored(void *out, const void *q, const void *k_new, const void *v_new,
@@ -376,9 +369,8 @@ PKV_API pkv_status paged_attention_multi_token_scored(
     bool empty;
     const pkv_status rc = scored::check(a, head_dim, PKV_BF16, false, &empty);
     if (rc != PKV_OK || empty) return rc;
-    if (!q_starts || max_q_len < 1) return PKV_ERR_INVALID;
+    if (!q_starts || max_q_len < 1 || max_seq_len < 1) return PKV_ERR_INVALID;
     a.err = device_error_word();
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return head_dim == 128 ? scored::run_simt<scored::kBf16, 128>(a, workspace, workspace_bytes, st)
-                           : scored::run_simt<scored::kBf16, 64>(a, workspace, workspace_bytes, st);
+    return scored::run_rows(a, head_dim, workspace, workspace_bytes, st);
 }
