@@ -45,7 +45,7 @@ constexpr int kTok = 128;   // keys per tile
 constexpr int kRows = 128;  // rows of a softmax group
 constexpr int kThreads = 384;
 constexpr int kMmaWarp = 8, kKWarp = 9, kVWarp = 10, kSchedWarp = 11;
-constexpr int kDescs = 4;  // piece descriptors in flight
+constexpr int kDescs = 6;  // piece descriptors in flight
 constexpr int kBadRing = 8;  // tiles whose invalid blocks are on record (more than the producers can be ahead)
 constexpr int kCharge = 2;   // virtual tiles of a context
 constexpr int kMinShare = kCharge + 1;
@@ -53,14 +53,12 @@ constexpr float kRescale = 8.f;
 constexpr uint32_t kTmemCols = 512, kOBase = 256;
 constexpr int kMaxCtas = 160;   // partial slots in the workspace: two per CTA
 constexpr int kMergeRows = 32;  // rows per CTA of the merge kernel
-// registers per thread of the softmax warps and of the others; (2 * 200 + 104) * 128 = the launch's 384 * 168
-constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
-
 enum Kind { kPlain = 0, kCap = 1, kBias = 2, kCapBias = 3 };
 
 struct RowsArgs : Args {
     float k1;       // plain, biased: scale * log2 e; capped: scale / softcap
     float c2;       // capped: softcap * log2 e
+    float poly[6];  // capped: c2 tanh(k1 s) = s * sum poly[i] s^2i for |k1 s| <= 1
     float *part_o;  // [2 kMaxCtas][D][256]: columns of 256 rows
     float *part_ml; // [2 kMaxCtas][256][2]
     int4 *merges;   // [kMaxCtas]: (parts, first query row, rows, kv head) of the context begun and cut in that share
@@ -71,8 +69,8 @@ struct Piece {
     int ntiles;  // 0: no more
     int i0;      // first tile within the context
     int np, pt0, mt0;   // context tile i is key tile pt0 + i (i < np) or mt0 + i - np
-    int seq, kvh, row0, nrows, pos0, len, ks0, pre;
-    int first, cpre, lo, hi;  // the context's keys (KeyRange)
+    int seq, kvh, row0, nrows, pos0, pre;
+    int ks0, cpre, lo, hi;  // the context's keys: [ks0, cpre) and [lo, hi) (KeyRange)
     int slot;                 // partial slot, -1: the whole context
     int glo[2], ghi[2];       // group g's main keys lie in [glo, ghi)
     int jlast[2];             // group g's last tile within the piece, -1: none
@@ -192,6 +190,16 @@ __device__ __forceinline__ void st16u(uint32_t taddr, const uint32_t (&v)[16]) {
                  : "memory");
 }
 
+// tanh z / z as a polynomial in z^2 over |z| <= 1: least squares of the error of tanh, reweighted towards its largest
+// (Lawson's method), in 64 bits; off by at most 2.4e-7 < 2^-21.
+constexpr double kTanh[6] = {0.9999968539, -0.3332400381, 0.1325352534, -0.05097286511, 0.01611418269, -0.002839466141};
+
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 __device__ __forceinline__ float rcp_approx(float x) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -207,102 +215,182 @@ __device__ __forceinline__ uint32_t bit_range(int a, int b) {
 }
 
 struct RowState {
-    float m, l;
-    int p;  // position
+    float m, l;    // reference and sum
+    float next;    // capped: the reference the next tile should move to (-inf: none)
+    int p;         // position
     KeyRange r;
     float slope2;  // slope * log2 e
 };
 
-// One tile of one row.  S (raw products) at sp, P (bf16 pairs) back over it.
+// Maximum over 32 values, four chains of three-input maxima; ABS: of their magnitudes.
+template <bool ABS>
+__device__ __forceinline__ float max32(const float (&s)[32]) {
+    float m[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        m[i] = ABS ? fabsf(s[i]) : s[i];
+#pragma unroll
+        for (int k = i + 4; k + 4 < 32; k += 8)
+            m[i] = ABS ? fmax3(m[i], fabsf(s[k]), fabsf(s[k + 4])) : fmax3(m[i], s[k], s[k + 4]);
+        m[i] = fmaxf(m[i], ABS ? fabsf(s[28 + i]) : s[28 + i]);
+    }
+    return fmaxf(fmax3(m[0], m[1], m[2]), m[3]);
+}
+
+// The 32 keys from t on that the row sees, as bits.
+__device__ __forceinline__ uint32_t seen32(const KeyRange &r, int t, uint32_t bad, int bshift, int word) {
+    uint32_t m = bit_range(r.lo - t, r.hi - t) | bit_range(r.first - t, r.pre - t);
+    if (bad) {
+        const int per = 32 >> bshift;  // blocks of the word
+        for (int b = 0; b < per; ++b)
+            if ((bad >> (word * per + b)) & 1u) m &= ~bit_range(b << bshift, (b + 1) << bshift);
+    }
+    return m;
+}
+
+// Raw products -> scores in base 2: c tanh(z), z = k1 s.
+__device__ __forceinline__ void cap32(float (&s)[32], const RowsArgs &a) {
+    if (!__any_sync(0xffffffffu, max32<true>(s) * fabsf(a.k1) > 1.f)) {
+        // |z| <= 1 in the whole warp: an odd polynomial (kTanh, its factors folded in on the host) on the FMA pipe, two keys
+        // an instruction; the exponential is then the only special function of a score
+        const uint64_t q0 = f32x2(a.poly[0], a.poly[0]), q1 = f32x2(a.poly[1], a.poly[1]), q2 = f32x2(a.poly[2], a.poly[2]);
+        const uint64_t q3 = f32x2(a.poly[3], a.poly[3]), q4 = f32x2(a.poly[4], a.poly[4]), q5 = f32x2(a.poly[5], a.poly[5]);
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+            const uint64_t x = f32x2(s[k], s[k + 1]), u = mul_f32x2(x, x);
+            uint64_t y = fma_f32x2(q5, u, q4);
+            y = fma_f32x2(y, u, q3);
+            y = fma_f32x2(y, u, q2);
+            y = fma_f32x2(y, u, q1);
+            y = fma_f32x2(y, u, q0);
+            f32x2_split(mul_f32x2(x, y), s[k], s[k + 1]);
+        }
+    } else {
+        // tanh z = 1 - 2 / (1 + e^2z), good to 2^-21
+        const float z2 = 2.f * 1.44269504f * a.k1;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) s[k] = a.c2 - (2.f * a.c2) * rcp_approx(1.f + ex2_approx(s[k] * z2));
+    }
+}
+
+// Weights 2^(f s + nm) of 32 keys to P (bf16 pairs) at `to`, their sum to ls.
+__device__ __forceinline__ void weights32(const float (&s)[32], float f, float nm, uint32_t to, uint64_t (&ls)[2]) {
+    const uint64_t f2 = f32x2(f, f), nm2 = f32x2(nm, nm);
+    uint32_t pk[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        float a0, a1;
+        f32x2_split(fma_f32x2(f32x2(s[2 * k], s[2 * k + 1]), f2, nm2), a0, a1);
+        const float e0 = ex2_approx(a0), e1 = ex2_approx(a1);
+        pk[k] = pack_bf16x2(e0, e1);
+        ls[k & 1] = add_f32x2(ls[k & 1], f32x2(e0, e1));
+    }
+    st16u(to, pk);
+}
+
+// One tile of one row, 32 keys at a time in loops that are not unrolled: a warp
+// has the tensor cores' 1024 cycles a tile, and unrolled code of 128 keys ran
+// at the pace of its instruction fetches (6 to 10 cycles an instruction).  S
+// (raw products) at sp, P (bf16 pairs) back over it, always behind the reads.
 // t0: the tile's first key; bad: bits of blocks with an invalid id; beyond:
-// some row of the warp may see keys past its position (a prefix).
+// some row may see keys past its position (a prefix).  Returns with `move` set
+// when O has to be scaled by `alpha` before the tile's product.
+//
+// A first pass finds the row's maximum; scores that are biased or masked are
+// written back over S by it, in base 2 (plain ones stay raw: the exponential's
+// FMA scales them).  Capped scores without a bias lie within +-c2, so that the
+// reference can be that of an earlier tile: from a row's second tile on there
+// is one pass, and a reference that proves low moves a tile later.
 template <int KIND>
-__device__ __forceinline__ void softmax_tile(uint32_t sp, int t0, uint32_t bad, int bshift, bool beyond, float k1, float c2,
-                                             RowState &st, bool &move, float &alpha) {
-    float s[kTok];
-#pragma unroll
-    for (int c = 0; c < kTok / 32; ++c) tc::ld32(sp + 32 * c, s + 32 * c);
-    tc::wait_ld();
-    // scores in base 2 (plain: left unscaled, the exponential's FMA scales them)
-    if constexpr (KIND == kCap || KIND == kCapBias) {
-        // c tanh(z) log2 e with tanh z = 1 - 2 / (1 + e^2z): good to 2^-21 of c
-        const float z2 = 2.f * 1.44269504f * k1;
-#pragma unroll
-        for (int k = 0; k < kTok; ++k) s[k] = c2 - (2.f * c2) * rcp_approx(1.f + ex2_approx(s[k] * z2));
-    } else if constexpr (KIND == kBias) {
-#pragma unroll
-        for (int k = 0; k < kTok; ++k) s[k] *= k1;
-    }
-    if constexpr (KIND == kBias || KIND == kCapBias) {
-        const float d0 = (float)(st.p - t0);
-        if (beyond) {
-#pragma unroll
-            for (int k = 0; k < kTok; ++k) s[k] = fmaf(-st.slope2, fabsf(d0 - (float)k), s[k]);
-        } else {
-            const float b0 = -st.slope2 * d0;
-#pragma unroll
-            for (int k = 0; k < kTok; ++k) s[k] += fmaf(st.slope2, (float)k, b0);
-        }
-    }
-    const bool full = ((t0 >= st.r.lo && t0 + kTok <= st.r.hi) || (t0 >= st.r.first && t0 + kTok <= st.r.pre)) && bad == 0u;
-    if (!__all_sync(0xffffffffu, full)) {
-#pragma unroll
-        for (int w = 0; w < kTok / 32; ++w) {
-            uint32_t m = bit_range(st.r.lo - t0 - 32 * w, st.r.hi - t0 - 32 * w) |
-                         bit_range(st.r.first - t0 - 32 * w, st.r.pre - t0 - 32 * w);
-            if (bad) {
-                const int per = 32 >> bshift;  // blocks of the word
-                for (int b = 0; b < per; ++b)
-                    if ((bad >> (w * per + b)) & 1u) m &= ~bit_range(b << bshift, (b + 1) << bshift);
-            }
-#pragma unroll
-            for (int k = 0; k < 32; ++k) s[32 * w + k] = (m >> k) & 1u ? s[32 * w + k] : -INFINITY;
-        }
-    }
-    float mx[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        mx[i] = s[i];
-#pragma unroll
-        for (int k = i + 8; k + 8 < kTok; k += 16) mx[i] = fmax3(mx[i], s[k], s[k + 8]);
-        mx[i] = fmaxf(mx[i], s[kTok - 8 + i]);
-    }
-    float mt = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
-    if (KIND == kPlain) mt *= k1;
-    float m_new = st.m;
+__device__ __forceinline__ void softmax_tile(uint32_t sp, int t0, uint32_t bad, const RowsArgs &a, bool beyond, RowState &st,
+                                             bool &move, float &alpha) {
+    const bool mine = ((t0 >= st.r.lo && t0 + kTok <= st.r.hi) || (t0 >= st.r.first && t0 + kTok <= st.r.pre)) && bad == 0u;
+    const bool full = __all_sync(0xffffffffu, mine);
     move = false;
-    if (mt != -INFINITY) {
-        if (st.m == -INFINITY) {
-            m_new = mt;  // nothing summed yet
-        } else if (mt > st.m + kRescale) {
-            m_new = mt;
+    alpha = 1.f;
+    uint64_t ls[2] = {0ull, 0ull};
+    // P may grow to 2^(2 c2): kept below 2^100 by taking the one-pass form for c2 <= 50 only
+    const bool once = KIND == kCap && a.c2 <= 50.f && !__any_sync(0xffffffffu, st.m == -INFINITY);
+    if (once) {
+        if (st.next > st.m + kRescale) {
+            alpha = ex2_approx(st.m - st.next);
+            st.m = st.next;
+            st.l *= alpha;
             move = true;
         }
-    }
-    alpha = move ? ex2_approx(st.m - m_new) : 1.f;
-    st.m = m_new;
-    const float nm = st.m == -INFINITY ? 0.f : -st.m;
-    const float f = KIND == kPlain ? k1 : 1.f;
-    const uint64_t f2 = f32x2(f, f), nm2 = f32x2(nm, nm);
-    uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < kTok / 32; ++c) {
+            float s[32];
+            tc::ld32(sp + 32 * c, s);
+            tc::wait_ld();
+            cap32(s, a);
+            if (!full) {
+                const uint32_t w = seen32(st.r, t0 + 32 * c, bad, a.bshift, c);
 #pragma unroll
-    for (int c = 0; c < kTok / 32; ++c) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            const int i = 32 * c + 2 * k;
-            float a0, a1;
-            if (KIND == kPlain) f32x2_split(fma_f32x2(f32x2(s[i], s[i + 1]), f2, nm2), a0, a1);
-            else f32x2_split(add_f32x2(f32x2(s[i], s[i + 1]), nm2), a0, a1);
-            const float e0 = ex2_approx(a0), e1 = ex2_approx(a1);
-            pk[k] = pack_bf16x2(e0, e1);
-            ls[k & 3] = add_f32x2(ls[k & 3], f32x2(e0, e1));
+                for (int k = 0; k < 32; ++k) s[k] = (w >> k) & 1u ? s[k] : -INFINITY;
+            }
+            mx = fmaxf(mx, max32<false>(s));
+            weights32(s, 1.f, -st.m, sp + 16 * c, ls);
         }
-        st16u(sp + 16 * c, pk);
+        st.next = mx;
+    } else {
+        const bool stored = KIND != kPlain || !full;  // the first pass writes its scores back
+        float mt = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < kTok / 32; ++c) {
+            float s[32];
+            tc::ld32(sp + 32 * c, s);
+            tc::wait_ld();
+            const int t = t0 + 32 * c;
+            if constexpr (KIND == kCap || KIND == kCapBias) cap32(s, a);
+            if constexpr (KIND == kBias || KIND == kCapBias) {
+                const float f = KIND == kBias ? a.k1 : 1.f, d0 = (float)(st.p - t);
+                if (beyond) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) s[k] = fmaf(-st.slope2, fabsf(d0 - (float)k), s[k] * f);
+                } else {
+                    // -slope (p - t - k): one FMA for the pair's bias, one for the score
+                    const uint64_t f2 = f32x2(f, f), b0 = f32x2(-st.slope2 * d0, -st.slope2 * d0), sl = f32x2(st.slope2, st.slope2);
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2)
+                        f32x2_split(fma_f32x2(f32x2(s[k], s[k + 1]), f2, fma_f32x2(sl, f32x2((float)k, (float)(k + 1)), b0)), s[k],
+                                    s[k + 1]);
+                }
+            }
+            if (!full) {
+                const uint32_t w = seen32(st.r, t, bad, a.bshift, c);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) s[k] = (w >> k) & 1u ? s[k] : -INFINITY;
+            }
+            mt = fmaxf(mt, max32<false>(s));
+            if (stored) tc::st32(sp + 32 * c, s);
+        }
+        if (stored) tc::wait_st();
+        if (KIND == kPlain) mt *= a.k1;
+        if (mt != -INFINITY) {
+            if (st.m == -INFINITY) {
+                st.m = mt;  // nothing summed yet
+            } else if (mt > st.m + kRescale) {
+                alpha = ex2_approx(st.m - mt);
+                st.m = mt;
+                st.l *= alpha;
+                move = true;
+            }
+        }
+        const float nm = st.m == -INFINITY ? 0.f : -st.m, f = KIND == kPlain ? a.k1 : 1.f;
+#pragma unroll 1
+        for (int c = 0; c < kTok / 32; ++c) {
+            float s[32];
+            tc::ld32(sp + 32 * c, s);
+            tc::wait_ld();
+            weights32(s, f, nm, sp + 16 * c, ls);
+        }
+        st.next = -INFINITY;
     }
     float x, y;
-    f32x2_split(add_f32x2(add_f32x2(ls[0], ls[1]), add_f32x2(ls[2], ls[3])), x, y);
-    st.l = st.l * alpha + (x + y);
+    f32x2_split(add_f32x2(ls[0], ls[1]), x, y);
+    st.l += x + y;
     tc::wait_st();
 }
 
@@ -341,6 +429,10 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int Hkv = a.num_kv_heads, G = a.group, B = a.block_size;
 
+    if (threadIdx.x == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
+    }
     grid_dependency_wait();
     grid_launch_dependents();
     if ((smem_u32(smem) & 1023u) != 0u) {  // swizzled tiles need it; never expected
@@ -362,13 +454,15 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     };
     int T = 0, my_s0 = 0, my_s1 = 0;
     int64_t parts = 1;
-    for (int round = 0; round < 2; ++round) {  // the total, then the sequence that holds this share's start
+    int start = 0, v = 0;  // this thread's sequence of the last pass: its laid-out start and tiles
+    // the total, then the sequence that holds this share's start (from registers when one pass covers every sequence)
+    for (int round = 0; round < (a.num_seqs > per_pass ? 2 : 1); ++round) {
         if (threadIdx.x == 0) scratch[12] = 0;
         __syncthreads();
         for (int base = 0; base < a.num_seqs; base += per_pass) {
             const int s = base + threadIdx.x / W;
             const int total = seq_total(s, round == 0 && blockIdx.x == 0);
-            const int v = sub == 0 ? total : 0;
+            v = sub == 0 ? total : 0;
             int x = v;
 #pragma unroll
             for (int sh = 1; sh < 32; sh <<= 1) {
@@ -379,7 +473,8 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             __syncthreads();
             int before = scratch[12];
             for (int w = 0; w < warp; ++w) before += scratch[w];
-            const int end = before + x, start = end - v;
+            const int end = before + x;
+            start = end - v;
             if (round == 1 && v > 0 && my_s0 >= start && my_s0 < end) {
                 scratch[13] = s;
                 scratch[14] = start;
@@ -399,6 +494,10 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         }
     }
     const int s0 = my_s0, s1 = my_s1;
+    if (a.num_seqs <= per_pass && v > 0 && s0 >= start && s0 < start + v) {
+        scratch[13] = threadIdx.x / W;
+        scratch[14] = start;
+    }
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NK; ++i) {
@@ -437,7 +536,6 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     const uint32_t q_s = smem_u32(smem + L::q), k_s = smem_u32(smem + L::kring), v_s = smem_u32(smem + L::vring);
 
     if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         bool dead = false;
         if (warp == kSchedWarp) {
             // ======================= scheduler =======================
@@ -487,10 +585,8 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                                 const int nq = min(x.Q - q0, a.per_ctx);
                                 pc.nrows = nq * G;
                                 pc.pos0 = fp + q0;
-                                pc.len = x.L;
                                 pc.ks0 = c.ks0;
                                 pc.pre = x.pre;
-                                pc.first = c.r.first;
                                 pc.cpre = c.r.pre;
                                 pc.lo = c.r.lo;
                                 pc.hi = c.r.hi;
@@ -547,7 +643,7 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 const int n = pc.ntiles;
                 if (n == 0) break;
                 const int32_t *bt = a.block_tables + (int64_t)pc.seq * a.max_blocks;
-                const KeyRange r{pc.first, pc.cpre, pc.lo, pc.hi};
+                const KeyRange r{pc.ks0, pc.cpre, pc.lo, pc.hi};
                 const int kvh = pc.kvh;
                 // this lane's block of a tile: its id, INT_MIN where no row sees a key of it
                 auto block_id = [&](int j) {
@@ -599,6 +695,7 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
 #pragma unroll
             for (int k = 0; k < kTok / 16; ++k) pv_off[k] = ((uint32_t)((16 * k / B) * (H * B * 128) + (16 * k % B) * 128)) >> 4;
             int tau = 0;
+            uint32_t idle = 0;
             int pend[2] = {-1, -1};             // tile whose P V the group still owes
             bool fresh[2] = {false, false};     // ... and it starts the piece's O
             bool owe_free[2] = {false, false};  // the previous piece's O may still be being read
@@ -645,13 +742,30 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 bool started[2] = {false, false};
                 for (int j = 0; j < n && !dead; ++j, ++tau) {
                     const int st = tau % NK;
+                    bool open[2] = {j == 0 && p > 0, j == 0 && p > 0};  // the previous piece is still to be closed
+                    if (j == 0 && p > 0) {
+                        // finish the previous piece where that need not wait, as long as this one's keys are not there
+                        while (!mbar_test_wait(&k_full[st], (uint32_t)((tau / NK) & 1)) && (open[0] || open[1]) && !dead) {
+#pragma unroll
+                            for (int g = 0; g < 2; ++g)
+                                if (open[g] && (pend[g] < 0 || mbar_test_wait(&p_full[g], (uint32_t)(npv[g] & 1)))) {
+                                    close(g);
+                                    open[g] = false;
+                                }
+                            if (++idle > kWaitLimit) {
+                                flag_error(a.err, PKV_DEVERR_TIMEOUT);
+                                dead = true;
+                            }
+                        }
+                        idle = 0;
+                    }
                     wait_or_flag(&k_full[st], (uint32_t)((tau / NK) & 1), dead, a.err);
                     const uint64_t kd = tc::smem_desc(k_s + (uint32_t)st * L::kTile, 16, 1024);
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
                         const bool act = active<ALT>(pc, g, j);
                         if (j == 0) {
-                            if (p > 0) close(g);
+                            if (open[g]) close(g);
                             had[g] = has_rows<ALT>(pc, g);
                             if (had[g] && (!ALT || g == 0)) wait_or_flag(&q_ready[g], (uint32_t)(nqr[g]++ & 1), dead, a.err);
                         } else if (!ALT || act) {
@@ -689,7 +803,6 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         }
     } else {
         // ======================= softmax =======================
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         const int g = warp >> 2, wq = warp & 3;
         const int rr = wq * 32 + lane;                // TMEM lane
         const int cr = ALT ? rr : g * kRows + rr;     // row of the context
@@ -729,13 +842,16 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 q_done();
             }
             const bool live = cr < pc.nrows;
-            const int64_t qrow = pc.row0 + (live ? cr / G : 0);
+            // warps without rows only pass the barriers; the other rows of a warp with some go by the last query's keys,
+            // so that they keep no tile from the path without masks
+            const bool live_warp = (ALT ? 0 : g * kRows) + wq * 32 < pc.nrows;
+            const int64_t qrow = pc.row0 + min(cr, pc.nrows - 1) / G;
             RowState st;
             st.m = -INFINITY;
             st.l = 0.f;
-            st.p = pc.pos0 + (live ? cr / G : 0);
+            st.next = -INFINITY;
+            st.p = pc.pos0 + min(cr, pc.nrows - 1) / G;
             st.r = key_range(max(pc.ks0, key_start_of(a.s, qrow)), pc.pre, a.s.window, st.p, st.p);
-            if (!live) st.r = KeyRange{0, 0, 0, 0};
             st.slope2 = 0.f;
             if constexpr (KIND == kBias || KIND == kCapBias)
                 st.slope2 = a.s.slopes ? a.s.slopes[pc.kvh * G + cr % G] * 1.44269504f : 0.f;
@@ -764,10 +880,10 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 if (mine && j == jl) next_q();  // every Q K^T on this Q has completed
                 const uint32_t bad = bad_ring[tau % kBadRing];
                 // V rows of keys that no row sees hold stale values, or none were loaded: zero weights must meet zeros
-                const bool whole = ((t0 >= pc.lo && t0 + kTok <= pc.hi) || (t0 >= pc.first && t0 + kTok <= pc.cpre)) && bad == 0u;
+                const bool whole = ((t0 >= pc.lo && t0 + kTok <= pc.hi) || (t0 >= pc.ks0 && t0 + kTok <= pc.cpre)) && bad == 0u;
                 if (!whole) {
                     wait_or_flag(&v_full[tau % NV], (uint32_t)((tau / NV) & 1), dead, a.err);
-                    const KeyRange r{pc.first, pc.cpre, pc.lo, pc.hi};
+                    const KeyRange r{pc.ks0, pc.cpre, pc.lo, pc.hi};
                     const uint32_t vb = v_s + (uint32_t)(tau % NV) * L::kTile;
                     for (int e = rr; e < kTok * H * 8; e += kRows) {
                         const int key = (e >> 3) % kTok, h = e / (kTok * 8), chk = e & 7;
@@ -780,7 +896,7 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 }
                 bool move = false;
                 float alpha = 1.f;
-                softmax_tile<KIND>(sp, t0, bad, a.bshift, pc.pre > 0 && t0 < pc.pre, a.k1, a.c2, st, move, alpha);
+                if (live_warp) softmax_tile<KIND>(sp, t0, bad, a, pc.pre > 0 && t0 < pc.pre, st, move, alpha);
                 if (__any_sync(0xffffffffu, move)) {
                     const uint32_t ob = trow + kOBase + (uint32_t)g * D;
 #pragma unroll 1
@@ -823,7 +939,7 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 const float Ls = st.l * wm + other.y * wo;
                 const bool odd = n > 1;  // group 1 had tiles
                 const float inv = Ls != 0.f ? 1.f / Ls : 0.f;
-                if (wq * 32 < pc.nrows) {
+                if (live_warp) {
 #pragma unroll 1
                     for (int c = g * (D / 32); c < (g + 1) * (D / 32); ++c) {  // this group's half of the columns
                         float o[16], x[16];
@@ -866,7 +982,7 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 if (dead) break;
                 tc::fence_after();
                 const float inv = st.l != 0.f ? 1.f / st.l : 0.f;
-                if (g * kRows + wq * 32 < pc.nrows) {
+                if (live_warp) {
 #pragma unroll 1
                     for (int c = 0; c < D / 16; ++c) {
                         float o[16];
@@ -997,15 +1113,6 @@ pkv_status launch(const RowsArgs &a, cudaStream_t st) {
     constexpr int smem = Layout<D, ALT>::total;
     static bool done[128] = {};
     auto kern = scored_rows_kernel<D, KIND, ALT>;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return PKV_ERR_CUDA;
-    if (!done[dev]) {
-        // the register split draws on what the block is launched with: refuse a build that has less
-        cudaFuncAttributes at;
-        if (cudaFuncGetAttributes(&at, kern) != cudaSuccess ||
-            at.numRegs * kThreads < 2 * kRows * kSoftmaxRegs + (kThreads - 2 * kRows) * kOtherRegs)
-            return PKV_ERR_CUDA;
-    }
     if (!ensure_smem(kern, smem, done)) return PKV_ERR_CUDA;
     CUtensorMap mk, mv;
     const int64_t rows = (int64_t)a.num_blocks * a.num_kv_heads * a.block_size;
@@ -1050,6 +1157,8 @@ pkv_status run_rows(const Args &args, int head_dim, void *workspace, size_t work
     const double log2e = 1.4426950408889634;
     a.k1 = a.s.softcap > 0.f ? (float)((double)a.s.scale / a.s.softcap) : (float)(a.s.scale * log2e);
     a.c2 = (float)(a.s.softcap * log2e);
+    double f = a.s.softcap * log2e * a.k1;
+    for (int i = 0; i < 6; ++i, f *= (double)a.k1 * a.k1) a.poly[i] = (float)(kTanh[i] * f);
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     a.part_o = reinterpret_cast<float *>(ws + lay.o);
     a.part_ml = reinterpret_cast<float *>(ws + lay.ml);
