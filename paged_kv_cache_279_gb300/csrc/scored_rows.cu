@@ -19,10 +19,11 @@
 // equal share.  A context cut by a share's border leaves partial states (o, m,
 // l) in the workspace, which a second kernel merges; no CTA waits for another.
 //
-// Warps: 0-3 and 4-7 two softmax groups (a thread per row = TMEM lane), 8 the
-// MMA issuer, 9 / 10 the producers of K / V tiles (one TMA box per block and
-// column half, or per block), 11 the scheduler, which walks the share and
-// publishes one descriptor per piece of a context.  While one group works on
+// Warps: 0-7 and 8-15 two softmax groups (two threads per row = TMEM lane, one
+// for each half of a tile's keys), 16 the MMA issuer, 17 / 18 the producers of
+// K / V tiles (one TMA box per block and column half, or per block), 19 the
+// scheduler, which walks the share and publishes one descriptor per piece of a
+// context.  While one group works on
 // its scores the tensor cores run the other's products: the issue order is
 // P V (group 0), Q K^T (0, next tile), P V (1), Q K^T (1, next tile).
 // Tensor memory: S of group g at columns 128 g (P overwrites its first half as
@@ -43,13 +44,16 @@ namespace {
 
 constexpr int kTok = 128;   // keys per tile
 constexpr int kRows = 128;  // rows of a softmax group
-constexpr int kThreads = 384;
-constexpr int kMmaWarp = 8, kKWarp = 9, kVWarp = 10, kSchedWarp = 11;
+constexpr int kHalf = kTok / 2;      // a softmax thread's keys of a tile
+constexpr int kGroupWarps = 8;       // two halves of four warps
+constexpr int kThreads = 640;
+constexpr int kMmaWarp = 16, kKWarp = 17, kVWarp = 18, kSchedWarp = 19;
 constexpr int kDescs = 6;  // piece descriptors in flight
-constexpr int kBadRing = 8;  // tiles whose invalid blocks are on record (more than the producers can be ahead)
+constexpr int kRecs = 8;  // tile records (more than the K producer can be ahead of the softmax)
 constexpr int kCharge = 2;   // virtual tiles of a context
 constexpr int kMinShare = kCharge + 1;
 constexpr float kRescale = 8.f;
+constexpr float kMaxC2 = 73.f;  // softcap * log2 e up to which capped scores take a fixed reference (cap 50)
 constexpr uint32_t kTmemCols = 512, kOBase = 256;
 constexpr int kMaxCtas = 160;   // partial slots in the workspace: two per CTA
 constexpr int kMergeRows = 32;  // rows per CTA of the merge kernel
@@ -58,6 +62,7 @@ enum Kind { kPlain = 0, kCap = 1, kBias = 2, kCapBias = 3 };
 struct RowsArgs : Args {
     float k1;       // plain, biased: scale * log2 e; capped: scale / softcap
     float c2;       // capped: softcap * log2 e
+    float m0;       // capped: the reference
     float poly[6];  // capped: c2 tanh(k1 s) = s * sum poly[i] s^2i for |k1 s| <= 1
     float *part_o;  // [2 kMaxCtas][D][256]: columns of 256 rows
     float *part_ml; // [2 kMaxCtas][256][2]
@@ -72,8 +77,15 @@ struct Piece {
     int seq, kvh, row0, nrows, pos0, pre;
     int ks0, cpre, lo, hi;  // the context's keys: [ks0, cpre) and [lo, hi) (KeyRange)
     int slot;                 // partial slot, -1: the whole context
-    int glo[2], ghi[2];       // group g's main keys lie in [glo, ghi)
-    int jlast[2];             // group g's last tile within the piece, -1: none
+    int jf[2], jl[2];         // group g takes the tiles jf .. jl (none: jl < jf); alternating: those of its parity
+};
+
+// A tile's record, written by the K producer.
+struct TileRec {
+    int t0;        // first key
+    uint32_t bad;  // bits of blocks with an invalid id (their keys are masked)
+    int whole;     // every key is seen by some row: no V row has to be zeroed
+    int pad;
 };
 
 __device__ __forceinline__ int key_tile(const Piece &p, int j) {
@@ -82,34 +94,33 @@ __device__ __forceinline__ int key_tile(const Piece &p, int j) {
 }
 template <bool ALT>
 __device__ __forceinline__ bool has_rows(const Piece &p, int g) { return ALT || p.nrows > g * kRows; }
-// Whether group g takes tile j of the piece (ALT: in turn; else unless none of its rows can see a key of it).
-template <bool ALT>
-__device__ __forceinline__ bool active(const Piece &p, int g, int j) {
-    if (ALT) return (j & 1) == g;
-    const int t0 = key_tile(p, j) * kTok;
-    return p.nrows > g * kRows && ((t0 < p.ghi[g] && t0 + kTok > p.glo[g]) || t0 < p.pre);
-}
-
 template <int D, bool ALT>
 struct Layout {
     static constexpr int H = D / 64;
     static constexpr int kQTile = H * kRows * 128;
     static constexpr int kQBytes = (ALT ? 1 : 2) * kQTile;
     static constexpr int kTile = H * kTok * 128;  // K or V of one tile
-    static constexpr int NK = D == 128 ? (ALT ? 3 : 2) : 4;
-    static constexpr int NV = D == 128 ? 3 : 4;
+    static constexpr int NK = D == 128 ? 2 : 4;
+    static constexpr int NV = D == 128 ? (ALT ? 3 : 2) : 4;
     static constexpr int q = 0;
     static constexpr int kring = q + kQBytes;
     static constexpr int vring = kring + NK * kTile;
-    static constexpr int xch = vring + NV * kTile;       // float2 [2][kRows]
-    static constexpr int desc = xch + (ALT ? 2 * kRows * 8 : 0);
-    static constexpr int bad = desc + kDescs * (int)sizeof(Piece);
-    static constexpr int bars = (bad + kBadRing * 4 + 7) & ~7;
-    static constexpr int kBars = 2 * NK + 2 * NV + 6 * 2 + 2 * kDescs + 1;
+    static constexpr int xch = vring + NV * kTile;        // float [2][2 groups][2 halves][kRows]: maxima of even / odd tiles
+    static constexpr int fin_ml = xch + 8 * kRows * 4;    // float2 [2 groups][2 halves][kRows]: (m, l) at a piece's end
+    static constexpr int desc = fin_ml + 4 * kRows * 8;
+    static constexpr int recs = (desc + kDescs * (int)sizeof(Piece) + 15) & ~15;
+    static constexpr int bars = recs + kRecs * (int)sizeof(TileRec);
+    static constexpr int kBars = 2 * NK + 2 * NV + 6 * 2 + 2 * kDescs + 1 + 8;
     static constexpr int misc = bars + kBars * 8;  // TMEM address, scan scratch
-    static constexpr int total = misc + 96;
+    static constexpr int total = misc + 128;
     static_assert(total <= 227 * 1024, "shared memory per CTA");
 };
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0u;
+}
 
 __device__ __forceinline__ bool wait_or_flag(uint64_t *bar, uint32_t parity, bool &dead, unsigned int *err) {
     if (dead) return false;
@@ -216,7 +227,6 @@ __device__ __forceinline__ uint32_t bit_range(int a, int b) {
 
 struct RowState {
     float m, l;    // reference and sum
-    float next;    // capped: the reference the next tile should move to (-inf: none)
     int p;         // position
     KeyRange r;
     float slope2;  // slope * log2 e
@@ -248,11 +258,12 @@ __device__ __forceinline__ uint32_t seen32(const KeyRange &r, int t, uint32_t ba
     return m;
 }
 
-// Raw products -> scores in base 2: c tanh(z), z = k1 s.
-__device__ __forceinline__ void cap32(float (&s)[32], const RowsArgs &a) {
+// Raw products -> scores in base 2 plus nm: c tanh(z) + nm, z = k1 s.
+__device__ __forceinline__ void cap32(float (&s)[32], const RowsArgs &a, float nm) {
     if (!__any_sync(0xffffffffu, max32<true>(s) * fabsf(a.k1) > 1.f)) {
         // |z| <= 1 in the whole warp: an odd polynomial (kTanh, its factors folded in on the host) on the FMA pipe, two keys
         // an instruction; the exponential is then the only special function of a score
+        const uint64_t nm2 = f32x2(nm, nm);
         const uint64_t q0 = f32x2(a.poly[0], a.poly[0]), q1 = f32x2(a.poly[1], a.poly[1]), q2 = f32x2(a.poly[2], a.poly[2]);
         const uint64_t q3 = f32x2(a.poly[3], a.poly[3]), q4 = f32x2(a.poly[4], a.poly[4]), q5 = f32x2(a.poly[5], a.poly[5]);
 #pragma unroll
@@ -263,24 +274,25 @@ __device__ __forceinline__ void cap32(float (&s)[32], const RowsArgs &a) {
             y = fma_f32x2(y, u, q2);
             y = fma_f32x2(y, u, q1);
             y = fma_f32x2(y, u, q0);
-            f32x2_split(mul_f32x2(x, y), s[k], s[k + 1]);
+            f32x2_split(fma_f32x2(x, y, nm2), s[k], s[k + 1]);
         }
     } else {
         // tanh z = 1 - 2 / (1 + e^2z), good to 2^-21
         const float z2 = 2.f * 1.44269504f * a.k1;
 #pragma unroll
-        for (int k = 0; k < 32; ++k) s[k] = a.c2 - (2.f * a.c2) * rcp_approx(1.f + ex2_approx(s[k] * z2));
+        for (int k = 0; k < 32; ++k) s[k] = (a.c2 + nm) - (2.f * a.c2) * rcp_approx(1.f + ex2_approx(s[k] * z2));
     }
 }
 
-// Weights 2^(f s + nm) of 32 keys to P (bf16 pairs) at `to`, their sum to ls.
+// Weights 2^(f s + nm) (AFFINE; else 2^s) of 32 keys to P (bf16 pairs) at `to`, their sum to ls.
+template <bool AFFINE>
 __device__ __forceinline__ void weights32(const float (&s)[32], float f, float nm, uint32_t to, uint64_t (&ls)[2]) {
     const uint64_t f2 = f32x2(f, f), nm2 = f32x2(nm, nm);
     uint32_t pk[16];
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
-        float a0, a1;
-        f32x2_split(fma_f32x2(f32x2(s[2 * k], s[2 * k + 1]), f2, nm2), a0, a1);
+        float a0 = s[2 * k], a1 = s[2 * k + 1];
+        if (AFFINE) f32x2_split(fma_f32x2(f32x2(a0, a1), f2, nm2), a0, a1);
         const float e0 = ex2_approx(a0), e1 = ex2_approx(a1);
         pk[k] = pack_bf16x2(e0, e1);
         ls[k & 1] = add_f32x2(ls[k & 1], f32x2(e0, e1));
@@ -288,105 +300,102 @@ __device__ __forceinline__ void weights32(const float (&s)[32], float f, float n
     st16u(to, pk);
 }
 
-// One tile of one row, 32 keys at a time in loops that are not unrolled: a warp
-// has the tensor cores' 1024 cycles a tile, and unrolled code of 128 keys ran
-// at the pace of its instruction fetches (6 to 10 cycles an instruction).  S
-// (raw products) at sp, P (bf16 pairs) back over it, always behind the reads.
-// t0: the tile's first key; bad: bits of blocks with an invalid id; beyond:
-// some row may see keys past its position (a prefix).  Returns with `move` set
-// when O has to be scaled by `alpha` before the tile's product.
+// One tile of one row's half (64 keys): 32 keys at a time in loops that are not
+// unrolled -- unrolled code of 128 keys ran at the pace of its instruction
+// fetches (6 to 10 cycles an instruction).  S (raw products) at sp, P (bf16
+// pairs) back over the half's first 32 columns, always behind the reads.  t0:
+// the half's first key; bad: bits of its blocks with an invalid id; beyond: some
+// row may see keys past its position (a prefix).  Returns with `move` set when O
+// has to be scaled by `alpha` before the tile's product.
 //
-// A first pass finds the row's maximum; scores that are biased or masked are
-// written back over S by it, in base 2 (plain ones stay raw: the exponential's
-// FMA scales them).  Capped scores without a bias lie within +-c2, so that the
-// reference can be that of an earlier tile: from a row's second tile on there
-// is one pass, and a reference that proves low moves a tile later.
-template <int KIND>
-__device__ __forceinline__ void softmax_tile(uint32_t sp, int t0, uint32_t bad, const RowsArgs &a, bool beyond, RowState &st,
-                                             bool &move, float &alpha) {
-    const bool mine = ((t0 >= st.r.lo && t0 + kTok <= st.r.hi) || (t0 >= st.r.first && t0 + kTok <= st.r.pre)) && bad == 0u;
+// A first pass finds the maximum, meet() gives the row's (both halves weigh by
+// the same reference); scores that are biased or masked are written back over S
+// by it, in base 2 (plain ones stay raw: the exponential's FMA scales them).
+// Capped scores without a bias need neither: they lie within +-c2, and up to
+// kMaxC2 a fixed reference c2 / 4 keeps weights within 2^-(5/4 c2) .. 2^(3/4 c2)
+// (cap 50: 2^-90 .. 2^54), far from the ends of float32's and bf16's range for
+// sums over 2^20 keys of V entries between 2^-36 and 2^53.
+template <int KIND, typename Meet>
+__device__ __forceinline__ void softmax_half(uint32_t sp, int t0, uint32_t bad, const RowsArgs &a, bool beyond,
+                                             RowState &st, bool &move, float &alpha, Meet meet) {
+    const bool mine = ((t0 >= st.r.lo && t0 + kHalf <= st.r.hi) || (t0 >= st.r.first && t0 + kHalf <= st.r.pre)) && bad == 0u;
     const bool full = __all_sync(0xffffffffu, mine);
     move = false;
     alpha = 1.f;
     uint64_t ls[2] = {0ull, 0ull};
-    // P may grow to 2^(2 c2): kept below 2^100 by taking the one-pass form for c2 <= 50 only
-    const bool once = KIND == kCap && a.c2 <= 50.f && !__any_sync(0xffffffffu, st.m == -INFINITY);
-    if (once) {
-        if (st.next > st.m + kRescale) {
-            alpha = ex2_approx(st.m - st.next);
-            st.m = st.next;
-            st.l *= alpha;
-            move = true;
-        }
-        float mx = -INFINITY;
+    if constexpr (KIND == kCap) {
+        // every score lies within +-c2: one reference does for all tiles (and every part of a context)
+        const float nm = -st.m;
 #pragma unroll 1
-        for (int c = 0; c < kTok / 32; ++c) {
+        for (int c = 0; c < kHalf / 32; ++c) {
             float s[32];
             tc::ld32(sp + 32 * c, s);
             tc::wait_ld();
-            cap32(s, a);
+            cap32(s, a, nm);
             if (!full) {
                 const uint32_t w = seen32(st.r, t0 + 32 * c, bad, a.bshift, c);
 #pragma unroll
                 for (int k = 0; k < 32; ++k) s[k] = (w >> k) & 1u ? s[k] : -INFINITY;
             }
-            mx = fmaxf(mx, max32<false>(s));
-            weights32(s, 1.f, -st.m, sp + 16 * c, ls);
+            weights32<false>(s, 1.f, 0.f, sp + 16 * c, ls);
         }
-        st.next = mx;
-    } else {
-        const bool stored = KIND != kPlain || !full;  // the first pass writes its scores back
-        float mt = -INFINITY;
+        float x, y;
+        f32x2_split(add_f32x2(ls[0], ls[1]), x, y);
+        st.l += x + y;
+        tc::wait_st();
+        return;
+    }
+    const bool stored = KIND != kPlain || !full;
+    float mt = -INFINITY;
 #pragma unroll 1
-        for (int c = 0; c < kTok / 32; ++c) {
-            float s[32];
-            tc::ld32(sp + 32 * c, s);
-            tc::wait_ld();
-            const int t = t0 + 32 * c;
-            if constexpr (KIND == kCap || KIND == kCapBias) cap32(s, a);
-            if constexpr (KIND == kBias || KIND == kCapBias) {
-                const float f = KIND == kBias ? a.k1 : 1.f, d0 = (float)(st.p - t);
-                if (beyond) {
+    for (int c = 0; c < kHalf / 32; ++c) {
+        float s[32];
+        tc::ld32(sp + 32 * c, s);
+        tc::wait_ld();
+        const int t = t0 + 32 * c;
+        if constexpr (KIND == kCapBias) cap32(s, a, 0.f);
+        if constexpr (KIND == kBias || KIND == kCapBias) {
+            const float f = KIND == kBias ? a.k1 : 1.f, d0 = (float)(st.p - t);
+            if (beyond) {
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) s[k] = fmaf(-st.slope2, fabsf(d0 - (float)k), s[k] * f);
-                } else {
-                    // -slope (p - t - k): one FMA for the pair's bias, one for the score
-                    const uint64_t f2 = f32x2(f, f), b0 = f32x2(-st.slope2 * d0, -st.slope2 * d0), sl = f32x2(st.slope2, st.slope2);
+                for (int k = 0; k < 32; ++k) s[k] = fmaf(-st.slope2, fabsf(d0 - (float)k), s[k] * f);
+            } else {
+                // -slope (p - t - k): one FMA for the pair's bias, one for the score
+                const uint64_t f2 = f32x2(f, f), b0 = f32x2(-st.slope2 * d0, -st.slope2 * d0), sl = f32x2(st.slope2, st.slope2);
 #pragma unroll
-                    for (int k = 0; k < 32; k += 2)
-                        f32x2_split(fma_f32x2(f32x2(s[k], s[k + 1]), f2, fma_f32x2(sl, f32x2((float)k, (float)(k + 1)), b0)), s[k],
-                                    s[k + 1]);
-                }
-            }
-            if (!full) {
-                const uint32_t w = seen32(st.r, t, bad, a.bshift, c);
-#pragma unroll
-                for (int k = 0; k < 32; ++k) s[k] = (w >> k) & 1u ? s[k] : -INFINITY;
-            }
-            mt = fmaxf(mt, max32<false>(s));
-            if (stored) tc::st32(sp + 32 * c, s);
-        }
-        if (stored) tc::wait_st();
-        if (KIND == kPlain) mt *= a.k1;
-        if (mt != -INFINITY) {
-            if (st.m == -INFINITY) {
-                st.m = mt;  // nothing summed yet
-            } else if (mt > st.m + kRescale) {
-                alpha = ex2_approx(st.m - mt);
-                st.m = mt;
-                st.l *= alpha;
-                move = true;
+                for (int k = 0; k < 32; k += 2)
+                    f32x2_split(fma_f32x2(f32x2(s[k], s[k + 1]), f2, fma_f32x2(sl, f32x2((float)k, (float)(k + 1)), b0)), s[k],
+                                s[k + 1]);
             }
         }
-        const float nm = st.m == -INFINITY ? 0.f : -st.m, f = KIND == kPlain ? a.k1 : 1.f;
+        if (!full) {
+            const uint32_t w = seen32(st.r, t, bad, a.bshift, c);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) s[k] = (w >> k) & 1u ? s[k] : -INFINITY;
+        }
+        mt = fmaxf(mt, max32<false>(s));
+        if (stored) tc::st32(sp + 32 * c, s);
+    }
+    if (stored) tc::wait_st();
+    if (KIND == kPlain) mt *= a.k1;
+    mt = meet(mt);
+    if (mt != -INFINITY) {
+        if (st.m == -INFINITY) {
+            st.m = mt;  // nothing summed yet
+        } else if (mt > st.m + kRescale) {
+            alpha = ex2_approx(st.m - mt);
+            st.m = mt;
+            st.l *= alpha;
+            move = true;
+        }
+    }
+    const float nm = st.m == -INFINITY ? 0.f : -st.m, f = KIND == kPlain ? a.k1 : 1.f;
 #pragma unroll 1
-        for (int c = 0; c < kTok / 32; ++c) {
-            float s[32];
-            tc::ld32(sp + 32 * c, s);
-            tc::wait_ld();
-            weights32(s, f, nm, sp + 16 * c, ls);
-        }
-        st.next = -INFINITY;
+    for (int c = 0; c < kHalf / 32; ++c) {
+        float s[32];
+        tc::ld32(sp + 32 * c, s);
+        tc::wait_ld();
+        weights32<true>(s, f, nm, sp + 16 * c, ls);
     }
     float x, y;
     f32x2_split(add_f32x2(ls[0], ls[1]), x, y);
@@ -416,16 +425,18 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     constexpr int H = L::H, NK = L::NK, NV = L::NV;
     extern __shared__ __align__(1024) unsigned char smem[];
     Piece *descs = reinterpret_cast<Piece *>(smem + L::desc);
-    uint32_t *bad_ring = reinterpret_cast<uint32_t *>(smem + L::bad);
-    float2 *xch = reinterpret_cast<float2 *>(smem + L::xch);
+    TileRec *recs = reinterpret_cast<TileRec *>(smem + L::recs);
+    float *xch = reinterpret_cast<float *>(smem + L::xch);
+    float2 *fin_ml = reinterpret_cast<float2 *>(smem + L::fin_ml);
     uint64_t *k_full = reinterpret_cast<uint64_t *>(smem + L::bars), *k_empty = k_full + NK;
     uint64_t *v_full = k_empty + NK, *v_empty = v_full + NV;
     uint64_t *s_full = v_empty + NV, *p_full = s_full + 2;      // per group
     uint64_t *q_ready = p_full + 2, *o_last = q_ready + 2, *o_free = o_last + 2;
     uint64_t *desc_full = o_free + 2, *desc_empty = desc_full + kDescs, *fin = desc_empty + kDescs;
-    uint64_t *xch_full = fin + 1;  // per group: its rows' (m, l) of a piece are in xch
+    uint64_t *xch_full = fin + 1;   // per group: its rows' m and l of a piece are in xch
+    uint64_t *pair = xch_full + 2;  // [2][4]: both halves of 32 rows have posted
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::misc);
-    int *scratch = reinterpret_cast<int *>(smem + L::misc + 16);  // [12] warp sums, carry, found sequence, its start
+    int *scratch = reinterpret_cast<int *>(smem + L::misc + 16);  // [20] warp sums, carry, found sequence, its start
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int Hkv = a.num_kv_heads, G = a.group, B = a.block_size;
 
@@ -457,7 +468,7 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     int start = 0, v = 0;  // this thread's sequence of the last pass: its laid-out start and tiles
     // the total, then the sequence that holds this share's start (from registers when one pass covers every sequence)
     for (int round = 0; round < (a.num_seqs > per_pass ? 2 : 1); ++round) {
-        if (threadIdx.x == 0) scratch[12] = 0;
+        if (threadIdx.x == 0) scratch[20] = 0;
         __syncthreads();
         for (int base = 0; base < a.num_seqs; base += per_pass) {
             const int s = base + threadIdx.x / W;
@@ -471,20 +482,20 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             }
             if (lane == 31) scratch[warp] = x;
             __syncthreads();
-            int before = scratch[12];
+            int before = scratch[20];
             for (int w = 0; w < warp; ++w) before += scratch[w];
             const int end = before + x;
             start = end - v;
             if (round == 1 && v > 0 && my_s0 >= start && my_s0 < end) {
-                scratch[13] = s;
-                scratch[14] = start;
+                scratch[21] = s;
+                scratch[22] = start;
             }
             __syncthreads();
-            if (threadIdx.x == kThreads - 1) scratch[12] = end;
+            if (threadIdx.x == kThreads - 1) scratch[20] = end;
             __syncthreads();
         }
         if (round == 0) {
-            T = scratch[12];
+            T = scratch[20];
             parts = split_parts(T, gridDim.x);
             __syncthreads();  // every thread has the total before the next round clears it
             if (threadIdx.x == 0) a.merges[blockIdx.x] = make_int4(0, 0, 0, 0);
@@ -495,8 +506,8 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     }
     const int s0 = my_s0, s1 = my_s1;
     if (a.num_seqs <= per_pass && v > 0 && s0 >= start && s0 < start + v) {
-        scratch[13] = threadIdx.x / W;
-        scratch[14] = start;
+        scratch[21] = threadIdx.x / W;
+        scratch[22] = start;
     }
 
     if (threadIdx.x == 0) {
@@ -510,16 +521,17 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 4);
-            mbar_init(&q_ready[i], 4);
+            mbar_init(&p_full[i], kGroupWarps);
+            mbar_init(&q_ready[i], kGroupWarps);
             mbar_init(&o_last[i], 1);
-            mbar_init(&o_free[i], ALT ? 8 : 4);
-            mbar_init(&xch_full[i], 4);
+            mbar_init(&o_free[i], ALT ? 2 * kGroupWarps : kGroupWarps);
+            mbar_init(&xch_full[i], kGroupWarps);
         }
         for (int i = 0; i < kDescs; ++i) {
             mbar_init(&desc_full[i], 1);
-            mbar_init(&desc_empty[i], 8 + 3);  // softmax warps, producers, MMA
+            mbar_init(&desc_empty[i], 2 * kGroupWarps + 3);  // softmax warps, producers, MMA
         }
+        for (int i = 0; i < 8; ++i) mbar_init(&pair[i], 2);
         mbar_init(fin, 1);
         fence_barrier_init();
     }
@@ -535,13 +547,13 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     const uint32_t tmem = *tmem_slot;
     const uint32_t q_s = smem_u32(smem + L::q), k_s = smem_u32(smem + L::kring), v_s = smem_u32(smem + L::vring);
 
-    if (warp >= 8) {
+    if (warp >= 2 * kGroupWarps) {
         bool dead = false;
         if (warp == kSchedWarp) {
             // ======================= scheduler =======================
-            int s = scratch[13];
+            int s = scratch[21];
             int t = s0;                 // next laid-out tile of the share
-            int seq_start = scratch[14];  // laid-out start of sequence s
+            int seq_start = scratch[22];  // laid-out start of sequence s
             int p = 0;
             while (t < s1 && !dead) {
                 const Seq x = load_seq(a, s, false);
@@ -597,14 +609,19 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                                     a.merges[blockIdx.x] = make_int4(
                                         (int)share_owner(end - 1, T, parts) - (int)blockIdx.x + 1, pc.row0, pc.nrows, kvh);
                                 for (int g = 0; g < 2; ++g) {
+                                    pc.jf[g] = ALT ? g : 0;
+                                    pc.jl[g] = pc.ntiles - 1;
+                                    if (ALT) continue;
+                                    // tiles at either end that none of the group's rows can see a key of
                                     const int qa = min(nq - 1, g * kRows / G), qb = min(nq - 1, (g * kRows + kRows - 1) / G);
-                                    pc.glo[g] = a.s.window > 0 ? max(c.r.lo, pc.pos0 + qa - a.s.window + 1) : c.r.lo;
-                                    pc.ghi[g] = pc.pos0 + qb + 1;
-                                }
-                                for (int g = 0; g < 2; ++g) {
-                                    int j = pc.ntiles - 1;
-                                    while (j >= 0 && !active<ALT>(pc, g, j)) --j;
-                                    pc.jlast[g] = j;
+                                    const int glo = a.s.window > 0 ? pc.pos0 + qa - a.s.window + 1 : 0, ghi = pc.pos0 + qb + 1;
+                                    auto idle = [&](int j) {
+                                        const int t0 = key_tile(pc, j) * kTok;
+                                        return t0 >= pc.pre && (t0 >= ghi || t0 + kTok <= glo);
+                                    };
+                                    if (pc.nrows <= g * kRows) pc.jl[g] = -1;
+                                    while (pc.jl[g] >= 0 && idle(pc.jl[g])) --pc.jl[g];
+                                    while (pc.jf[g] <= pc.jl[g] && idle(pc.jf[g])) ++pc.jf[g];
                                 }
                                 descs[d] = pc;
                                 mbar_arrive(&desc_full[d]);
@@ -663,7 +680,13 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                     const uint32_t nlive = (uint32_t)__popc(__ballot_sync(0xffffffffu, live)), badm = __ballot_sync(0xffffffffu, bad);
                     if (lane == 0) {
                         if (isk) {
-                            bad_ring[tau % kBadRing] = badm;
+                            const int t0 = key_tile(pc, j) * kTok;
+                            TileRec rec;
+                            rec.t0 = t0;
+                            rec.bad = badm;
+                            rec.whole = badm == 0u && ((t0 >= r.lo && t0 + kTok <= r.hi) || (t0 >= r.first && t0 + kTok <= r.pre));
+                            rec.pad = 0;
+                            recs[tau % kRecs] = rec;
                             if (badm) flag_error(a.err, PKV_DEVERR_BLOCK_ID);
                         }
                         mbar_arrive_expect_tx(&full[st], nlive * (uint32_t)(H * 128) << a.bshift);
@@ -687,138 +710,147 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             // copies in flight (only after a timeout) land before the CTA exits
             if (lane == 0 && dead)
                 for (int k = max(0, tau - N); k < tau; ++k) mbar_wait_bounded(&full[k % N], (uint32_t)((k / N) & 1));
-        } else if (lane == 0) {
+        } else {
             // ======================= MMA issuer =======================
+            // The whole warp walks (uniform registers), one elected lane issues.
             constexpr uint32_t idesc_qk = tc::instr_desc(kTok, false), idesc_pv = tc::instr_desc(D, true);
             const uint32_t pv_lbo = (uint32_t)(B * 128), pv_sbo = B >= 16 ? 1024u : (uint32_t)(H * B * 128);
-            uint32_t pv_off[kTok / 16];
-#pragma unroll
-            for (int k = 0; k < kTok / 16; ++k) pv_off[k] = ((uint32_t)((16 * k / B) * (H * B * 128) + (16 * k % B) * 128)) >> 4;
+            const bool leader = elect_one();
+            const uint64_t qd0 = tc::smem_desc(q_s, 16, 1024), kd0 = tc::smem_desc(k_s, 16, 1024);
+            const uint64_t vd0 = tc::smem_desc(v_s, pv_lbo, pv_sbo);
+            // 16 keys of V further: inside a block of 32 every second step, else a block (B = 8: two)
+            const uint32_t odd = B == 32 ? 16 * 128 >> 4 : (uint32_t)(H * 16 * 128) >> 4, two = (uint32_t)(2 * H * 16 * 128) >> 4;
             int tau = 0;
-            uint32_t idle = 0;
             int pend[2] = {-1, -1};             // tile whose P V the group still owes
             bool fresh[2] = {false, false};     // ... and it starts the piece's O
             bool owe_free[2] = {false, false};  // the previous piece's O may still be being read
             bool had[2] = {false, false};       // the previous piece had rows of the group
             int npv[2] = {0, 0}, nof[2] = {0, 0}, nqr[2] = {0, 0};  // phases passed: p_full, o_free, q_ready
-            auto flush = [&](int g) {
+            // the owed product; `closing`: and the end of the piece, everything issued: its softmax may read O
+            auto finish = [&](int g, bool closing) {
                 const int v = pend[g];
-                if (v < 0 || dead) return;
-                wait_or_flag(&p_full[g], (uint32_t)(npv[g] & 1), dead, a.err);
-                wait_or_flag(&v_full[v % NV], (uint32_t)((v / NV) & 1), dead, a.err);
-                if (fresh[g] && owe_free[g]) {
-                    wait_or_flag(&o_free[g], (uint32_t)(nof[g] & 1), dead, a.err);
-                    ++nof[g];
-                    owe_free[g] = false;
-                }
-                if (dead) return;
-                tc::fence_after();
-                const uint64_t vd = tc::smem_desc(v_s + (uint32_t)(v % NV) * L::kTile, pv_lbo, pv_sbo);
+                if (v >= 0 && !dead) {
+                    wait_or_flag(&p_full[g], (uint32_t)(npv[g] & 1), dead, a.err);
+                    wait_or_flag(&v_full[v % NV], (uint32_t)((v / NV) & 1), dead, a.err);
+                    if (fresh[g] && owe_free[g]) {
+                        wait_or_flag(&o_free[g], (uint32_t)(nof[g] & 1), dead, a.err);
+                        ++nof[g];
+                        owe_free[g] = false;
+                    }
+                    if (dead) return;
+                    tc::fence_after();
+                    const uint64_t vd = vd0 + (uint64_t)((uint32_t)(v % NV) * (uint32_t)(L::kTile >> 4));
+                    const uint32_t acc = fresh[g] ? 0u : 1u;
+                    if (leader) {
 #pragma unroll
-                for (int k = 0; k < kTok / 16; ++k)
-                    tc::mma_ts(tmem + kOBase + (uint32_t)g * D, tmem + (uint32_t)g * kTok + 8 * k, vd + (uint64_t)pv_off[k],
-                               idesc_pv, (fresh[g] && k == 0) ? 0u : 1u);
-                ++npv[g];
-                pend[g] = -1;
-                if (ALT) tc::commit(&v_empty[v % NV]);
-            };
-            // end of a piece for group g: everything issued; its softmax may read O
-            auto close = [&](int g) {
-                flush(g);
-                if (!had[g]) return;
-                if (owe_free[g] && !dead) {  // no product of the piece waited for it
+                        for (int k = 0; k < kTok / 16; ++k)
+                            tc::mma_ts(tmem + kOBase + (uint32_t)g * D,
+                                       tmem + (uint32_t)(g * kTok + (k < kHalf / 16 ? 8 * k : kHalf + 8 * k - kHalf / 2)),
+                                       vd + (uint64_t)((uint32_t)(k >> 1) * two + (uint32_t)(k & 1) * odd), idesc_pv,
+                                       k == 0 ? acc : 1u);
+                        if (ALT) tc::commit(&v_empty[v % NV]);
+                    }
+                    __syncwarp();
+                    ++npv[g];
+                    pend[g] = -1;
+                }
+                if (!closing || !had[g]) return;
+                if (owe_free[g]) {  // no product of the piece waited for it
                     wait_or_flag(&o_free[g], (uint32_t)(nof[g] & 1), dead, a.err);
                     ++nof[g];
                 }
                 owe_free[g] = true;
-                tc::commit(&o_last[g]);
+                if (leader) tc::commit(&o_last[g]);
+                __syncwarp();
             };
             for (int p = 0; !dead; ++p) {
                 const int d = p % kDescs;
                 if (!wait_or_flag(&desc_full[d], (uint32_t)((p / kDescs) & 1), dead, a.err)) break;
-                const Piece &pc = descs[d];
-                const int n = pc.ntiles;
+                const int n = descs[d].ntiles, nrows = descs[d].nrows;
                 if (n == 0) break;
+                const int jf[2] = {descs[d].jf[0], descs[d].jf[1]}, jl[2] = {descs[d].jl[0], descs[d].jl[1]};
                 bool started[2] = {false, false};
                 for (int j = 0; j < n && !dead; ++j, ++tau) {
                     const int st = tau % NK;
-                    bool open[2] = {j == 0 && p > 0, j == 0 && p > 0};  // the previous piece is still to be closed
-                    if (j == 0 && p > 0) {
-                        // finish the previous piece where that need not wait, as long as this one's keys are not there
-                        while (!mbar_test_wait(&k_full[st], (uint32_t)((tau / NK) & 1)) && (open[0] || open[1]) && !dead) {
-#pragma unroll
-                            for (int g = 0; g < 2; ++g)
-                                if (open[g] && (pend[g] < 0 || mbar_test_wait(&p_full[g], (uint32_t)(npv[g] & 1)))) {
-                                    close(g);
-                                    open[g] = false;
-                                }
-                            if (++idle > kWaitLimit) {
-                                flag_error(a.err, PKV_DEVERR_TIMEOUT);
-                                dead = true;
-                            }
-                        }
-                        idle = 0;
+                    bool open = j == 0 && p > 0;  // the previous piece is still to be closed
+                    if (open && !mbar_test_wait(&k_full[st], (uint32_t)((tau / NK) & 1))) {
+                        finish(0, true);  // rather than wait for this piece's keys first
+                        finish(1, true);
+                        open = false;
                     }
                     wait_or_flag(&k_full[st], (uint32_t)((tau / NK) & 1), dead, a.err);
-                    const uint64_t kd = tc::smem_desc(k_s + (uint32_t)st * L::kTile, 16, 1024);
+                    const uint64_t kd = kd0 + (uint64_t)((uint32_t)st * (uint32_t)(L::kTile >> 4));
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
-                        const bool act = active<ALT>(pc, g, j);
+                        const bool act = ALT ? (j & 1) == g : (j >= jf[g] && j <= jl[g]);
+                        if (open || (j > 0 && (!ALT || act))) finish(g, open);
                         if (j == 0) {
-                            if (open[g]) close(g);
-                            had[g] = has_rows<ALT>(pc, g);
+                            had[g] = ALT || nrows > g * kRows;
                             if (had[g] && (!ALT || g == 0)) wait_or_flag(&q_ready[g], (uint32_t)(nqr[g]++ & 1), dead, a.err);
-                        } else if (!ALT || act) {
-                            flush(g);
                         }
                         if (!act || dead) continue;
                         tc::fence_after();
-                        const uint64_t qd = tc::smem_desc(q_s + (ALT ? 0u : (uint32_t)g * L::kQTile), 16, 1024);
+                        const uint64_t qd = qd0 + (uint64_t)(ALT ? 0 : g * (L::kQTile >> 4));
+                        if (leader) {
 #pragma unroll
-                        for (int k = 0; k < D / 16; ++k) {
-                            const uint64_t off = (uint64_t)(((k >> 2) * (kTok * 128) + (k & 3) * 32) >> 4);
-                            tc::mma(tmem + (uint32_t)g * kTok, qd + off, kd + off, idesc_qk, k > 0 ? 1u : 0u);
+                            for (int k = 0; k < D / 16; ++k) {
+                                const uint64_t off = (uint64_t)(((k >> 2) * (kTok * 128) + (k & 3) * 32) >> 4);
+                                tc::mma(tmem + (uint32_t)g * kTok, qd + off, kd + off, idesc_qk, k > 0 ? 1u : 0u);
+                            }
+                            tc::commit(&s_full[g]);
                         }
-                        tc::commit(&s_full[g]);
+                        __syncwarp();
                         pend[g] = tau;
                         fresh[g] = !started[g];
                         started[g] = true;
                     }
                     if (dead) break;
-                    tc::commit(&k_empty[st]);
+                    if (leader) tc::commit(&k_empty[st]);
                     if (!ALT && tau > 0) {  // both groups' products with the previous tile's V are issued
                         wait_or_flag(&v_full[(tau - 1) % NV], (uint32_t)(((tau - 1) / NV) & 1), dead, a.err);
-                        tc::commit(&v_empty[(tau - 1) % NV]);
+                        if (leader) tc::commit(&v_empty[(tau - 1) % NV]);
                     }
+                    __syncwarp();
                 }
-                mbar_arrive(&desc_empty[d]);
+                if (lane == 0) mbar_arrive(&desc_empty[d]);
             }
             if (!dead) {
-                close(0);
-                close(1);
+                finish(0, true);
+                finish(1, true);
             }
             // every product has completed before the tensor memory is freed
-            tc::commit(fin);
+            if (leader) tc::commit(fin);
+            __syncwarp();
             mbar_wait_bounded(fin, 0u);
         }
     } else {
         // ======================= softmax =======================
-        const int g = warp >> 2, wq = warp & 3;
+        const int g = warp >> 3, hf = (warp >> 2) & 1, wq = warp & 3;
         const int rr = wq * 32 + lane;                // TMEM lane
         const int cr = ALT ? rr : g * kRows + rr;     // row of the context
         const uint32_t trow = tmem + ((uint32_t)(wq * 32) << 16);
-        const uint32_t sp = trow + (uint32_t)g * kTok;
+        const uint32_t sp = trow + (uint32_t)(g * kTok + hf * kHalf);
         bool dead = false;
-        int ns = 0;   // tiles of this group so far
-        int npl = 0;  // pieces with rows of this group so far
+        int ns = 0;     // tiles of this group so far
+        int npl = 0;    // pieces with rows of this group so far
+        int nmeet = 0;  // meetings of the halves so far
         int tau0 = 0;
-        auto copy_q = [&](const Piece &pc) {
+        // both halves of the warp's rows have come here
+        auto meet_barrier = [&]() {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&pair[g * 4 + wq]);
+            wait_or_flag(&pair[g * 4 + wq], (uint32_t)(nmeet & 1), dead, a.err);
+            ++nmeet;
+        };
+        auto slot = [&](int n, int h) -> float & { return xch[((n & 1) * 4 + g * 2 + h) * kRows + rr]; };
+        auto copy_q = [&](const Piece &pc) {  // this thread's half of its row
             const bool live = cr < pc.nrows;
             const int row = pc.row0 + (live ? cr / G : 0), head = pc.kvh * G + cr % G;
             const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.q) + ((int64_t)row * a.num_heads + head) * D;
             const uint32_t base = q_s + (ALT ? 0u : (uint32_t)g * L::kQTile) + rr * 128;
 #pragma unroll
-            for (int k = 0; k < D / 8; ++k) {
+            for (int i = 0; i < D / 16; ++i) {
+                const int k = hf * (D / 16) + i;
                 const uint32_t dst = base + (k >> 3) * (kRows * 128) + (((k & 7) ^ (rr & 7)) << 4);
                 if (live) cp_async16(dst, src + k * 8);
                 else asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(dst), "r"(0u) : "memory");
@@ -845,12 +877,12 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             // warps without rows only pass the barriers; the other rows of a warp with some go by the last query's keys,
             // so that they keep no tile from the path without masks
             const bool live_warp = (ALT ? 0 : g * kRows) + wq * 32 < pc.nrows;
-            const int64_t qrow = pc.row0 + min(cr, pc.nrows - 1) / G;
+            const int qi = min(cr, pc.nrows - 1) / G;
+            const int64_t qrow = pc.row0 + qi;
             RowState st;
-            st.m = -INFINITY;
+            st.m = KIND == kCap ? a.m0 : -INFINITY;
             st.l = 0.f;
-            st.next = -INFINITY;
-            st.p = pc.pos0 + min(cr, pc.nrows - 1) / G;
+            st.p = pc.pos0 + qi;
             st.r = key_range(max(pc.ks0, key_start_of(a.s, qrow)), pc.pre, a.s.window, st.p, st.p);
             st.slope2 = 0.f;
             if constexpr (KIND == kBias || KIND == kCapBias)
@@ -866,26 +898,23 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                     copied = true;
                 }
             };
-            const bool mine = ALT ? ((n - 1) & 1) == g : true;  // this group copies
-            const int jl = ALT ? n - 1 : pc.jlast[g];
+            const int jf = pc.jf[g], jl = pc.jl[g], pre = pc.pre;
             bool any = false;
-            for (int j = 0; j < n && !dead; ++j) {
-                if (!active<ALT>(pc, g, j)) continue;
-                const int tau = tau0 + j, t0 = key_tile(pc, j) * kTok;
+            for (int j = jf; j <= jl; j += ALT ? 2 : 1) {
+                const int tau = tau0 + j;
                 wait_or_flag(&s_full[g], (uint32_t)(ns & 1), dead, a.err);
-                ++ns;
                 if (dead) break;
                 tc::fence_after();
-                any = true;
-                if (mine && j == jl) next_q();  // every Q K^T on this Q has completed
-                const uint32_t bad = bad_ring[tau % kBadRing];
+                const TileRec rec = recs[tau % kRecs];
+                const int t0 = rec.t0;
+                const uint32_t bad = rec.bad;
+                if (j == jl) next_q();  // every Q K^T on this Q has completed (ALT: the group of the piece's last tile copies)
                 // V rows of keys that no row sees hold stale values, or none were loaded: zero weights must meet zeros
-                const bool whole = ((t0 >= pc.lo && t0 + kTok <= pc.hi) || (t0 >= pc.ks0 && t0 + kTok <= pc.cpre)) && bad == 0u;
-                if (!whole) {
+                if (!rec.whole) {
                     wait_or_flag(&v_full[tau % NV], (uint32_t)((tau / NV) & 1), dead, a.err);
                     const KeyRange r{pc.ks0, pc.cpre, pc.lo, pc.hi};
                     const uint32_t vb = v_s + (uint32_t)(tau % NV) * L::kTile;
-                    for (int e = rr; e < kTok * H * 8; e += kRows) {
+                    for (int e = hf * kRows + rr; e < kTok * H * 8; e += 2 * kRows) {
                         const int key = (e >> 3) % kTok, h = e / (kTok * 8), chk = e & 7;
                         if (r.sees(t0 + key) && !((bad >> (key >> a.bshift)) & 1u)) continue;
                         const uint32_t row = vb + (key >> a.bshift) * (H * 128 << a.bshift) + h * (128 << a.bshift) +
@@ -896,11 +925,17 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 }
                 bool move = false;
                 float alpha = 1.f;
-                if (live_warp) softmax_tile<KIND>(sp, t0, bad, a, pc.pre > 0 && t0 < pc.pre, st, move, alpha);
-                if (__any_sync(0xffffffffu, move)) {
-                    const uint32_t ob = trow + kOBase + (uint32_t)g * D;
+                if (live_warp) {
+                    softmax_half<KIND>(sp, t0 + hf * kHalf, bad >> (hf * (kHalf >> a.bshift)), a, t0 < pre, st, move, alpha, [&](float mt) {
+                                           slot(ns, hf) = mt;
+                                           meet_barrier();
+                                           return fmaxf(mt, slot(ns, hf ^ 1));
+                                       });
+                }
+                if (__any_sync(0xffffffffu, move)) {  // in both halves' warps alike: each takes half of the columns
+                    const uint32_t ob = trow + kOBase + (uint32_t)(g * D + hf * (D / 2));
 #pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
+                    for (int c = 0; c < D / 64; ++c) {
                         float o[32];
                         tc::ld32(ob + c * 32, o);
                         tc::wait_ld();
@@ -910,6 +945,8 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                     }
                     tc::wait_st();
                 }
+                any = true;
+                ++ns;
                 tc::fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[g]);
@@ -920,41 +957,54 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             }
             if (dead) break;
             tau0 += n;
-            // ---- the piece's result ----
+            // ---- the piece's result: the sums of a row's halves (ALT: and groups) meet, each thread writes its columns ----
             const int64_t orow = (qrow * a.num_heads + pc.kvh * G + cr % G) * D;
-            if constexpr (ALT) {
-                wait_or_flag(&o_last[0], (uint32_t)(npl & 1), dead, a.err);
-                wait_or_flag(&o_last[1], (uint32_t)(npl & 1), dead, a.err);
+            if (ALT || has_rows<ALT>(pc, g)) {
+                wait_or_flag(&o_last[g], (uint32_t)(npl & 1), dead, a.err);
+                if (ALT) wait_or_flag(&o_last[g ^ 1], (uint32_t)(npl & 1), dead, a.err);
                 tc::fence_after();
-                // overwritten only after the next piece's products, which wait for both groups' reads (o_free)
-                xch[g * kRows + rr] = make_float2(st.m, st.l);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&xch_full[g]);
-                wait_or_flag(&xch_full[g ^ 1], (uint32_t)(npl & 1), dead, a.err);
+                // overwritten only after the next piece's products, which wait for all these reads (o_free)
+                if (!any) st.m = -INFINITY;  // O holds nothing
+                fin_ml[(g * 2 + hf) * kRows + rr] = make_float2(st.m, st.l);
+                if constexpr (ALT) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&xch_full[g]);
+                    wait_or_flag(&xch_full[0], (uint32_t)(npl & 1), dead, a.err);
+                    wait_or_flag(&xch_full[1], (uint32_t)(npl & 1), dead, a.err);
+                } else {
+                    meet_barrier();
+                }
                 ++npl;
                 if (dead) break;
-                const float2 other = xch[(g ^ 1) * kRows + rr];
-                const float M = fmaxf(st.m, other.x);
-                const float wm = st.m == -INFINITY ? 0.f : ex2_approx(st.m - M), wo = other.x == -INFINITY ? 0.f : ex2_approx(other.x - M);
-                const float Ls = st.l * wm + other.y * wo;
-                const bool odd = n > 1;  // group 1 had tiles
+                const float l_own = st.l + fin_ml[(g * 2 + (hf ^ 1)) * kRows + rr].y;
+                float M = st.m, Ls = l_own, wm = 1.f, wo = 0.f;
+                if constexpr (ALT) {
+                    const float2 x0 = fin_ml[((g ^ 1) * 2) * kRows + rr], x1 = fin_ml[((g ^ 1) * 2 + 1) * kRows + rr];
+                    M = fmaxf(st.m, x0.x);
+                    wm = st.m == -INFINITY ? 0.f : ex2_approx(st.m - M);
+                    wo = x0.x == -INFINITY ? 0.f : ex2_approx(x0.x - M);
+                    Ls = l_own * wm + (x0.y + x1.y) * wo;
+                } else if (st.m == -INFINITY) {
+                    wm = 0.f;
+                }
                 const float inv = Ls != 0.f ? 1.f / Ls : 0.f;
                 if (live_warp) {
+                    constexpr int kCols = ALT ? D / 4 : D / 2;
+                    const int col0 = (ALT ? g * 2 + hf : hf) * kCols;
 #pragma unroll 1
-                    for (int c = g * (D / 32); c < (g + 1) * (D / 32); ++c) {  // this group's half of the columns
+                    for (int c = col0; c < col0 + kCols; c += 16) {
                         float o[16], x[16];
-                        ld16(trow + kOBase + (uint32_t)g * D + 16 * c, o);
-                        ld16(trow + kOBase + (uint32_t)(g ^ 1) * D + 16 * c, x);
+                        ld16(trow + kOBase + (uint32_t)(g * D + c), o);
+                        if (ALT) ld16(trow + kOBase + (uint32_t)((g ^ 1) * D + c), x);
                         tc::wait_ld();
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const float u = (g == 0 || odd) && wm != 0.f ? o[k] * wm : 0.f;
-                            const float v = (g == 1 || odd) && wo != 0.f ? x[k] * wo : 0.f;
-                            o[k] = u + v;
+                        for (int k = 0; k < 16; ++k) {  // a state without keys may hold anything
+                            o[k] = wm != 0.f ? o[k] * wm : 0.f;
+                            if (ALT && wo != 0.f) o[k] = fmaf(x[k], wo, o[k]);
                         }
                         if (!live) continue;
                         if (pc.slot < 0) {
-                            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow + 16 * c);
+                            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow + c);
 #pragma unroll
                             for (int k = 0; k < 2; ++k)
                                 dst[k] = make_uint4(pack_bf16x2(o[8 * k] * inv, o[8 * k + 1] * inv),
@@ -962,61 +1012,24 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                                                     pack_bf16x2(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
                                                     pack_bf16x2(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
                         } else {
-                            float *dst = a.part_o + ((int64_t)pc.slot * D + 16 * c) * (2 * kRows) + cr;
+                            float *dst = a.part_o + ((int64_t)pc.slot * D + c) * (2 * kRows) + cr;
 #pragma unroll
                             for (int k = 0; k < 16; ++k) dst[k * (2 * kRows)] = o[k];
                         }
                     }
-                    if (live && pc.slot >= 0 && g == 0)
+                    if (live && pc.slot >= 0 && hf == 0 && (!ALT || g == 0))
                         reinterpret_cast<float2 *>(a.part_ml)[(int64_t)pc.slot * (2 * kRows) + cr] = make_float2(M, Ls);
                 }
                 tc::fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(&o_free[0]);
-                    mbar_arrive(&o_free[1]);
+                    mbar_arrive(&o_free[g]);
+                    if (ALT) mbar_arrive(&o_free[g ^ 1]);
                 }
-            } else if (has_rows<ALT>(pc, g)) {
-                wait_or_flag(&o_last[g], (uint32_t)(npl & 1), dead, a.err);
-                ++npl;
-                if (dead) break;
-                tc::fence_after();
-                const float inv = st.l != 0.f ? 1.f / st.l : 0.f;
-                if (live_warp) {
-#pragma unroll 1
-                    for (int c = 0; c < D / 16; ++c) {
-                        float o[16];
-                        ld16(trow + kOBase + (uint32_t)g * D + 16 * c, o);
-                        tc::wait_ld();
-                        if (!any || st.m == -INFINITY) {
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) o[k] = 0.f;
-                        }
-                        if (!live) continue;
-                        if (pc.slot < 0) {
-                            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow + 16 * c);
-#pragma unroll
-                            for (int k = 0; k < 2; ++k)
-                                dst[k] = make_uint4(pack_bf16x2(o[8 * k] * inv, o[8 * k + 1] * inv),
-                                                    pack_bf16x2(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
-                                                    pack_bf16x2(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
-                                                    pack_bf16x2(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
-                        } else {
-                            float *dst = a.part_o + ((int64_t)pc.slot * D + 16 * c) * (2 * kRows) + cr;
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) dst[k * (2 * kRows)] = o[k];
-                        }
-                    }
-                    if (live && pc.slot >= 0)
-                        reinterpret_cast<float2 *>(a.part_ml)[(int64_t)pc.slot * (2 * kRows) + cr] = make_float2(st.m, st.l);
-                }
-                tc::fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&o_free[g]);
             }
             // No tile of this group in the piece: its Q was never read.  The next one is announced only now, after the MMA
             // thread has passed this piece's announcement (o_last), or there was none.
-            if (!ALT && jl < 0) {
+            if (!ALT && jl < jf) {
                 next_q();
                 if (copied) q_done();
             }
@@ -1131,7 +1144,7 @@ template <int D, bool ALT>
 pkv_status launch_kind(const RowsArgs &a, cudaStream_t st) {
     // a plain score's maximum is found before the scaling, which needs a positive scale
     const bool bias = a.s.slopes != nullptr;
-    if (a.s.softcap > 0.f) return bias ? launch<D, kCapBias, ALT>(a, st) : launch<D, kCap, ALT>(a, st);
+    if (a.s.softcap > 0.f) return bias || a.c2 > kMaxC2 ? launch<D, kCapBias, ALT>(a, st) : launch<D, kCap, ALT>(a, st);
     return bias || !(a.s.scale > 0.f) ? launch<D, kBias, ALT>(a, st) : launch<D, kPlain, ALT>(a, st);
 }
 
@@ -1157,6 +1170,7 @@ pkv_status run_rows(const Args &args, int head_dim, void *workspace, size_t work
     const double log2e = 1.4426950408889634;
     a.k1 = a.s.softcap > 0.f ? (float)((double)a.s.scale / a.s.softcap) : (float)(a.s.scale * log2e);
     a.c2 = (float)(a.s.softcap * log2e);
+    a.m0 = 0.25f * a.c2;
     double f = a.s.softcap * log2e * a.k1;
     for (int i = 0; i < 6; ++i, f *= (double)a.k1 * a.k1) a.poly[i] = (float)(kTanh[i] * f);
     unsigned char *ws = static_cast<unsigned char *>(workspace);
