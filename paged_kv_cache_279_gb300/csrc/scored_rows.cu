@@ -63,7 +63,7 @@ struct RowsArgs : Args {
     float k1;       // plain, biased: scale * log2 e; capped: scale / softcap
     float c2;       // capped: softcap * log2 e
     float m0;       // capped: the reference
-    float poly[6];  // capped: c2 tanh(k1 s) = s * sum poly[i] s^2i for |k1 s| <= 1
+    float near[4], far[6];  // capped: c2 tanh(k1 s) = s * sum near[i] s^2i for |k1 s| <= kTanhNear (far: kTanhFar)
     float *part_o;  // [2 kMaxCtas][D][256]: columns of 256 rows
     float *part_ml; // [2 kMaxCtas][256][2]
     int4 *merges;   // [kMaxCtas]: (parts, first query row, rows, kv head) of the context begun and cut in that share
@@ -201,9 +201,29 @@ __device__ __forceinline__ void st16u(uint32_t taddr, const uint32_t (&v)[16]) {
                  : "memory");
 }
 
-// tanh z / z as a polynomial in z^2 over |z| <= 1: least squares of the error of tanh, reweighted towards its largest
-// (Lawson's method), in 64 bits; off by at most 2.4e-7 < 2^-21.
-constexpr double kTanh[6] = {0.9999968539, -0.3332400381, 0.1325352534, -0.05097286511, 0.01611418269, -0.002839466141};
+__device__ __forceinline__ void ld16(uint32_t taddr, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void st8u(uint32_t taddr, const uint32_t (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+// tanh z / z as polynomials in z^2: least squares of the error of tanh, reweighted towards its largest (Lawson's method),
+// in 64 bits.  |z| <= 0.75: off by at most 3.7e-6; |z| <= 1.25: 2.4e-6 -- of the cap, so 2e-4 of a score at a cap of 50,
+// where the weight's rounding to bf16 is worth 2e-3 to 4e-3.
+constexpr float kTanhNear = 0.75f, kTanhFar = 1.25f;
+constexpr double kTanh3[4] = {0.9999556008, -0.3322276376, 0.1257709249, -0.03377828486};
+constexpr double kTanh5[6] = {0.9999746925, -0.3328393216, 0.1305362538, -0.04692675917, 0.01253202075, -0.001682072195};
 
 __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
     uint64_t d;
@@ -232,17 +252,17 @@ struct RowState {
     float slope2;  // slope * log2 e
 };
 
-// Maximum over 32 values, four chains of three-input maxima; ABS: of their magnitudes.
-template <bool ABS>
-__device__ __forceinline__ float max32(const float (&s)[32]) {
+// Maximum over N values, four chains of three-input maxima; ABS: of their magnitudes.
+template <bool ABS, int N>
+__device__ __forceinline__ float max_of(const float (&s)[N]) {
     float m[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         m[i] = ABS ? fabsf(s[i]) : s[i];
 #pragma unroll
-        for (int k = i + 4; k + 4 < 32; k += 8)
+        for (int k = i + 4; k + 4 < N; k += 8)
             m[i] = ABS ? fmax3(m[i], fabsf(s[k]), fabsf(s[k + 4])) : fmax3(m[i], s[k], s[k + 4]);
-        m[i] = fmaxf(m[i], ABS ? fabsf(s[28 + i]) : s[28 + i]);
+        if (N % 8 == 0) m[i] = fmaxf(m[i], ABS ? fabsf(s[N - 4 + i]) : s[N - 4 + i]);
     }
     return fmaxf(fmax3(m[0], m[1], m[2]), m[3]);
 }
@@ -258,41 +278,80 @@ __device__ __forceinline__ uint32_t seen32(const KeyRange &r, int t, uint32_t ba
     return m;
 }
 
-// Raw products -> scores in base 2 plus nm: c tanh(z) + nm, z = k1 s.
-__device__ __forceinline__ void cap32(float (&s)[32], const RowsArgs &a, float nm) {
-    if (!__any_sync(0xffffffffu, max32<true>(s) * fabsf(a.k1) > 1.f)) {
-        // |z| <= 1 in the whole warp: an odd polynomial (kTanh, its factors folded in on the host) on the FMA pipe, two keys
-        // an instruction; the exponential is then the only special function of a score
-        const uint64_t nm2 = f32x2(nm, nm);
-        const uint64_t q0 = f32x2(a.poly[0], a.poly[0]), q1 = f32x2(a.poly[1], a.poly[1]), q2 = f32x2(a.poly[2], a.poly[2]);
-        const uint64_t q3 = f32x2(a.poly[3], a.poly[3]), q4 = f32x2(a.poly[4], a.poly[4]), q5 = f32x2(a.poly[5], a.poly[5]);
+// Raw products -> scores in base 2 plus nm: c tanh(z) + nm, z = k1 s.  For |z| small in the whole warp an odd polynomial
+// (the cap's factors folded in on the host) on the FMA pipe, two keys an instruction: the exponential is then the only
+// special function of a score.  The FMA pipe is what bounds capped scores, hence the shortest polynomial for the usual
+// sizes.  cap_near computes that one whatever the sizes and cap_far does the rest again where cap_near does not hold.
+template <int N>
+__device__ __forceinline__ void cap_near(float (&s)[N], const RowsArgs &a, uint64_t nm2) {
+    const uint64_t q0 = f32x2(a.near[0], a.near[0]), q1 = f32x2(a.near[1], a.near[1]);
+    const uint64_t q2 = f32x2(a.near[2], a.near[2]), q3 = f32x2(a.near[3], a.near[3]);
 #pragma unroll
-        for (int k = 0; k < 32; k += 2) {
+    for (int k = 0; k < N; k += 2) {
+        const uint64_t x = f32x2(s[k], s[k + 1]), u = mul_f32x2(x, x);
+        const uint64_t y = fma_f32x2(fma_f32x2(fma_f32x2(q3, u, q2), u, q1), u, q0);
+        f32x2_split(fma_f32x2(x, y, nm2), s[k], s[k + 1]);
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void cap_far(float (&s)[N], const RowsArgs &a, float nm, float top) {
+    if (!__any_sync(0xffffffffu, top > kTanhFar)) {
+        const uint64_t nm2 = f32x2(nm, nm);
+#pragma unroll
+        for (int k = 0; k < N; k += 2) {
             const uint64_t x = f32x2(s[k], s[k + 1]), u = mul_f32x2(x, x);
-            uint64_t y = fma_f32x2(q5, u, q4);
-            y = fma_f32x2(y, u, q3);
-            y = fma_f32x2(y, u, q2);
-            y = fma_f32x2(y, u, q1);
-            y = fma_f32x2(y, u, q0);
+            uint64_t y = f32x2(a.far[5], a.far[5]);
+#pragma unroll
+            for (int i = 4; i >= 0; --i) y = fma_f32x2(y, u, f32x2(a.far[i], a.far[i]));
             f32x2_split(fma_f32x2(x, y, nm2), s[k], s[k + 1]);
         }
     } else {
         // tanh z = 1 - 2 / (1 + e^2z), good to 2^-21
         const float z2 = 2.f * 1.44269504f * a.k1;
 #pragma unroll
-        for (int k = 0; k < 32; ++k) s[k] = (a.c2 + nm) - (2.f * a.c2) * rcp_approx(1.f + ex2_approx(s[k] * z2));
+        for (int k = 0; k < N; ++k) s[k] = (a.c2 + nm) - (2.f * a.c2) * rcp_approx(1.f + ex2_approx(s[k] * z2));
     }
 }
 
-// Weights 2^(f s + nm) (AFFINE; else 2^s) of 32 keys to P (bf16 pairs) at `to`, their sum to ls.
-template <bool AFFINE>
+__device__ __forceinline__ void cap32(float (&s)[32], const RowsArgs &a) {
+    const float top = max_of<true>(s) * fabsf(a.k1);
+    if (!__any_sync(0xffffffffu, top > kTanhNear)) cap_near(s, a, 0ull);
+    else cap_far(s, a, 0.f, top);
+}
+
+// Capped: the weights of 16 keys of S at sp (loaded in s) to P at `to`, their sum to ls; w: the keys that are seen.
+__device__ __forceinline__ void cap_weights16(float (&s)[16], uint32_t sp, uint32_t to, const RowsArgs &a, float nm, uint64_t nm2,
+                                              bool full, uint32_t w, uint64_t (&ls)[2]) {
+    const float top = max_of<true>(s) * fabsf(a.k1);
+    cap_near(s, a, nm2);
+    if (__any_sync(0xffffffffu, top > kTanhNear)) {
+        ld16(sp, s);
+        tc::wait_ld();
+        cap_far(s, a, nm, top);
+    }
+    if (!full) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) s[k] = (w >> k) & 1u ? s[k] : -INFINITY;
+    }
+    uint32_t pk[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float e0 = ex2_approx(s[2 * k]), e1 = ex2_approx(s[2 * k + 1]);
+        pk[k] = pack_bf16x2(e0, e1);
+        ls[k & 1] = add_f32x2(ls[k & 1], f32x2(e0, e1));
+    }
+    st8u(to, pk);
+}
+
+// Weights 2^(f s + nm) of 32 keys to P (bf16 pairs) at `to`, their sum to ls.
 __device__ __forceinline__ void weights32(const float (&s)[32], float f, float nm, uint32_t to, uint64_t (&ls)[2]) {
     const uint64_t f2 = f32x2(f, f), nm2 = f32x2(nm, nm);
     uint32_t pk[16];
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
-        float a0 = s[2 * k], a1 = s[2 * k + 1];
-        if (AFFINE) f32x2_split(fma_f32x2(f32x2(a0, a1), f2, nm2), a0, a1);
+        float a0, a1;
+        f32x2_split(fma_f32x2(f32x2(s[2 * k], s[2 * k + 1]), f2, nm2), a0, a1);
         const float e0 = ex2_approx(a0), e1 = ex2_approx(a1);
         pk[k] = pack_bf16x2(e0, e1);
         ls[k & 1] = add_f32x2(ls[k & 1], f32x2(e0, e1));
@@ -324,20 +383,21 @@ __device__ __forceinline__ void softmax_half(uint32_t sp, int t0, uint32_t bad, 
     alpha = 1.f;
     uint64_t ls[2] = {0ull, 0ull};
     if constexpr (KIND == kCap) {
-        // every score lies within +-c2: one reference does for all tiles (and every part of a context)
+        // every score lies within +-c2: one reference does for all tiles (and every part of a context); 16 keys are loaded
+        // while 16 are worked on
         const float nm = -st.m;
+        const uint64_t nm2 = f32x2(nm, nm);
+        float x0[16], x1[16];
+        ld16(sp, x0);
 #pragma unroll 1
-        for (int c = 0; c < kHalf / 32; ++c) {
-            float s[32];
-            tc::ld32(sp + 32 * c, s);
+        for (int c = 0; c < kHalf; c += 32) {
+            const uint32_t w = full ? 0u : seen32(st.r, t0 + c, bad, a.bshift, c / 32);
             tc::wait_ld();
-            cap32(s, a, nm);
-            if (!full) {
-                const uint32_t w = seen32(st.r, t0 + 32 * c, bad, a.bshift, c);
-#pragma unroll
-                for (int k = 0; k < 32; ++k) s[k] = (w >> k) & 1u ? s[k] : -INFINITY;
-            }
-            weights32<false>(s, 1.f, 0.f, sp + 16 * c, ls);
+            ld16(sp + c + 16, x1);
+            cap_weights16(x0, sp + c, sp + c / 2, a, nm, nm2, full, w, ls);
+            tc::wait_ld();
+            if (c + 32 < kHalf) ld16(sp + c + 32, x0);
+            cap_weights16(x1, sp + c + 16, sp + c / 2 + 8, a, nm, nm2, full, w >> 16, ls);
         }
         float x, y;
         f32x2_split(add_f32x2(ls[0], ls[1]), x, y);
@@ -353,7 +413,7 @@ __device__ __forceinline__ void softmax_half(uint32_t sp, int t0, uint32_t bad, 
         tc::ld32(sp + 32 * c, s);
         tc::wait_ld();
         const int t = t0 + 32 * c;
-        if constexpr (KIND == kCapBias) cap32(s, a, 0.f);
+        if constexpr (KIND == kCapBias) cap32(s, a);
         if constexpr (KIND == kBias || KIND == kCapBias) {
             const float f = KIND == kBias ? a.k1 : 1.f, d0 = (float)(st.p - t);
             if (beyond) {
@@ -373,7 +433,7 @@ __device__ __forceinline__ void softmax_half(uint32_t sp, int t0, uint32_t bad, 
 #pragma unroll
             for (int k = 0; k < 32; ++k) s[k] = (w >> k) & 1u ? s[k] : -INFINITY;
         }
-        mt = fmaxf(mt, max32<false>(s));
+        mt = fmaxf(mt, max_of<false>(s));
         if (stored) tc::st32(sp + 32 * c, s);
     }
     if (stored) tc::wait_st();
@@ -395,23 +455,12 @@ __device__ __forceinline__ void softmax_half(uint32_t sp, int t0, uint32_t bad, 
         float s[32];
         tc::ld32(sp + 32 * c, s);
         tc::wait_ld();
-        weights32<true>(s, f, nm, sp + 16 * c, ls);
+        weights32(s, f, nm, sp + 16 * c, ls);
     }
     float x, y;
     f32x2_split(add_f32x2(ls[0], ls[1]), x, y);
     st.l += x + y;
     tc::wait_st();
-}
-
-__device__ __forceinline__ void ld16(uint32_t taddr, float (&v)[16]) {
-    uint32_t r[16];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 // ---------------------------------------------------------------------------
@@ -1172,7 +1221,10 @@ pkv_status run_rows(const Args &args, int head_dim, void *workspace, size_t work
     a.c2 = (float)(a.s.softcap * log2e);
     a.m0 = 0.25f * a.c2;
     double f = a.s.softcap * log2e * a.k1;
-    for (int i = 0; i < 6; ++i, f *= (double)a.k1 * a.k1) a.poly[i] = (float)(kTanh[i] * f);
+    for (int i = 0; i < 6; ++i, f *= (double)a.k1 * a.k1) {
+        a.far[i] = (float)(kTanh5[i] * f);
+        if (i < 4) a.near[i] = (float)(kTanh3[i] * f);
+    }
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     a.part_o = reinterpret_cast<float *>(ws + lay.o);
     a.part_ml = reinterpret_cast<float *>(ws + lay.ml);

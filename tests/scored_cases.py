@@ -110,7 +110,7 @@ class Case:
             rep = self.Hq // self.Hkv
             a = abs(self.scale) * max(float((np.abs(q[:, h]) @ np.abs(k[:, h // rep]).T).max()) for h in range(self.Hq))
             bias = float(self.slopes.max()) * L if self.slopes is not None else 0.0
-            x = (self.D + 16) * 2.0 ** -24 * a + 2.0 ** -20 * (1 + self.softcap) + 2.0 ** -22 * (bias + a)
+            x = (self.D + 16) * 2.0 ** -24 * a + 2.0 ** -20 + 2.0 ** (-20 if self.qlens is None else -18) * self.softcap + 2.0 ** -22 * (bias + a)
             outs.append(o)
             tols.append(2 * (2 * x + weight + L * 2.0 ** -24) * size + half * np.abs(o) * (1 + 2.0 ** -6) + 1e-30)
         return np.concatenate(outs), np.concatenate(tols)
