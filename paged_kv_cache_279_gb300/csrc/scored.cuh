@@ -83,6 +83,12 @@ __device__ __forceinline__ int prefix_of(const ScoreArgs &s, int seq, int len) {
     return s.prefix_lens ? min(max(0, s.prefix_lens[seq]), len) : 0;
 }
 
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 namespace scored {
 
 constexpr int kGMax = 8;  // query heads per KV head
@@ -102,6 +108,11 @@ struct Args {
 
 // Checks that the calls share; *empty: valid, and nothing to do.
 pkv_status check(const Args &a, int head_dim, int dtype, bool fp8, bool *empty);
+
+// One query per sequence over bf16 or row-scaled FP8 caches (scored_decode.cu).
+constexpr int kMaxDecodeSeqs = 8192;  // more go to the CUDA-core kernel
+size_t decode_workspace(int64_t num_seqs, int num_heads, int head_dim);
+pkv_status run_decode(const Args &a, int head_dim, void *workspace, size_t workspace_bytes, cudaStream_t st);
 
 // Several queries per sequence on the tensor cores (scored_rows.cu).
 size_t rows_workspace(int head_dim);

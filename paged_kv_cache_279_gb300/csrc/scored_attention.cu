@@ -282,7 +282,9 @@ using namespace pkv;
 
 PKV_API size_t paged_attention_decode_scored_workspace_size(int num_seqs, int num_heads, int head_dim, int max_seq_len) {
     if (num_seqs <= 0 || num_heads <= 0 || head_dim <= 0 || max_seq_len <= 0) return 0;
-    return scored::simt_workspace(num_seqs, num_heads, head_dim, max_seq_len);
+    // whatever the type: the tensor-core kernel's and the CUDA-core kernel's (float32, very many sequences)
+    return std::max(scored::simt_workspace(num_seqs, num_heads, head_dim, max_seq_len),
+                    num_seqs <= scored::kMaxDecodeSeqs ? scored::decode_workspace(num_seqs, num_heads, head_dim) : 0);
 }
 
 PKV_API size_t paged_attention_multi_token_scored_workspace_size(int num_q_tokens, int num_heads, int head_dim,
@@ -324,6 +326,7 @@ PKV_API pkv_status paged_attention_decode_scored(void *out, const void *q, const
     if (dtype == PKV_F32)
         return head_dim == 128 ? scored::run_simt<scored::kF32, 128>(a, workspace, workspace_bytes, st)
                                : scored::run_simt<scored::kF32, 64>(a, workspace, workspace_bytes, st);
+    if (num_seqs <= scored::kMaxDecodeSeqs && max_seq_len > 0) return scored::run_decode(a, head_dim, workspace, workspace_bytes, st);
     return head_dim == 128 ? scored::run_simt<scored::kBf16, 128>(a, workspace, workspace_bytes, st)
                            : scored::run_simt<scored::kBf16, 64>(a, workspace, workspace_bytes, st);
 }
@@ -348,6 +351,7 @@ PKV_API pkv_status paged_attention_decode_scored_fp8_rows(
     if (rc != PKV_OK || empty) return rc;
     a.err = device_error_word();
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (num_seqs <= scored::kMaxDecodeSeqs && max_seq_len > 0) return scored::run_decode(a, head_dim, workspace, workspace_bytes, st);
     return head_dim == 128 ? scored::run_simt<scored::kFp8Rows, 128>(a, workspace, workspace_bytes, st)
                            : scored::run_simt<scored::kFp8Rows, 64>(a, workspace, workspace_bytes, st);
 }

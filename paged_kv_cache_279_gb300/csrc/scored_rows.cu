@@ -231,12 +231,6 @@ __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
     return d;
 }
 
-__device__ __forceinline__ float rcp_approx(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // bits [a, b) of a 32-bit word, a and b taken from any integers
 __device__ __forceinline__ uint32_t bit_range(int a, int b) {
     a = max(a, 0);
