@@ -343,64 +343,81 @@ def paged_attention_decode_grouped(out, q, k_cache, v_cache, block_tables, seq_l
     return out
 
 
-class _On:
-    """The device of the call's tensors (all on one, else ValueError), made
-    current while the library is called, and the stream the call runs on (the
-    device's current stream when none is given)."""
-
-    def __init__(self, stream, **tensors):
-        given = {n: t for n, t in tensors.items() if t is not None}
-        devs = {t.device for t in given.values() if isinstance(t, torch.Tensor) and t.is_cuda}
-        if len(devs) > 1:
-            raise ValueError("tensors on several devices: " + ", ".join(f"{n} on {t.device}" for n, t in given.items()))
-        self.device = next(iter(devs), None)
-        self._stream = stream
-        self._guard = None
-
-    def __enter__(self):
-        if self.device is not None and self.device.index != torch.cuda.current_device():
-            self._guard = torch.cuda.device(self.device)
-            self._guard.__enter__()
-        self.stream = _stream(self._stream)
-        return self
-
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
-        return False
-
-    def scratch(self, workspace, need: int):
-        """(address, bytes) of the caller's workspace, or of one taken here."""
-        if workspace is None:
-            if need == 0:
-                return None, 0
-            workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
-            if self._stream is not None:  # its memory must outlive the work on that stream, not on the current one
-                s = self._stream if hasattr(self._stream, "cuda_stream") else torch.cuda.ExternalStream(int(self._stream))
-                workspace.record_stream(s)
-        return _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _fp8_rows_args(lib_call: str, k, v, k_cache, v_cache, k_scales, v_scales, slot_mapping, stream) -> None:
+def _device_of(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return t.get_device()
+
+
+def _ptr(t, name: str, dtype, dev: int) -> int:
+    """Address of a contiguous tensor of that type on device `dev`."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        if not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        raise ValueError(f"{name} is on {t.device}, other tensors of the call on cuda:{dev}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _opt_ptr(t, name: str, dtype, dev: int):
+    return None if t is None else _ptr(t, name, dtype, dev)
+
+
+def _stream_on(stream, dev: int) -> int:
+    """The stream a call runs on: the given one, else the current stream of its tensors' device."""
+    if stream is None:
+        return _current_raw_stream(dev) if _current_raw_stream else int(torch.cuda.current_stream(dev).cuda_stream)
+    return _stream(stream)
+
+
+def _scratch(workspace, need: int, stream, dev: int):
+    """(address, bytes) of the caller's workspace, or of one taken here."""
+    if workspace is None:
+        if need == 0:
+            return None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", dev))
+        if stream is not None:  # its memory must outlive the work on that stream, not on the current one
+            workspace.record_stream(stream if hasattr(stream, "cuda_stream") else
+                                    torch.cuda.ExternalStream(int(stream), device=dev))
+        return workspace.data_ptr(), need
+    if workspace.get_device() != dev:
+        raise ValueError("workspace must be a tensor on the device of the call's tensors")
+    return _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
+
+
+def _run_on(dev: int, what: str, fn, args) -> None:
+    """Call the library with the tensors' device current."""
+    if dev == torch.cuda.current_device():
+        st = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args)
+    if st != PKV_OK:
+        raise PkvError(st, what)
+
+
+def _fp8_rows_call(what: str, k, v, k_cache, v_cache, k_scales, v_scales, slot_mapping, stream) -> None:
     NB, Hkv, B, D = k_cache.shape
     T = k.shape[0]
-    if tuple(k.shape) != (T, Hkv, D) or k.shape != v.shape or v_cache.shape != k_cache.shape:
+    if k.shape != (T, Hkv, D) or v.shape != k.shape or v_cache.shape != k_cache.shape:
         raise ValueError("shape mismatch between token rows and FP8 caches")
-    if tuple(k_scales.shape) != (NB, Hkv, B) or tuple(v_scales.shape) != (NB, Hkv, B):
+    if k_scales.shape != (NB, Hkv, B) or v_scales.shape != (NB, Hkv, B):
         raise ValueError("scales must be [NB, Hkv, B]")
-    if slot_mapping.shape[0] != T:
+    if slot_mapping.shape != (T,):
         raise ValueError("slot_mapping needs one entry per token")
-    if v.dtype != k.dtype:
-        raise TypeError("K and V rows differ in dtype")
-    lib = _lib.load()
-    with _On(stream, k=k, v=v, k_cache=k_cache, v_cache=v_cache, k_scales=k_scales, v_scales=v_scales,
-             slot_mapping=slot_mapping) as on:
-        st = getattr(lib, lib_call)(
-            _dev(k, "K rows"), _dev(v, "V rows"), _dev(k_cache, "k_cache", torch.uint8),
-            _dev(v_cache, "v_cache", torch.uint8), _dev(k_scales, "k_scales", torch.uint8),
-            _dev(v_scales, "v_scales", torch.uint8), _dev(slot_mapping, "slot_mapping", torch.int64, 1), T, Hkv, D, B, NB,
-            _dtype_code(k), on.stream)
-    _check(st, lib_call)
+    dev, dt, u8 = _device_of(k, "K rows"), k.dtype, torch.uint8
+    _run_on(dev, what, getattr(_lib.load(), what), (
+        _ptr(k, "K rows", dt, dev), _ptr(v, "V rows", dt, dev), _ptr(k_cache, "k_cache", u8, dev),
+        _ptr(v_cache, "v_cache", u8, dev), _ptr(k_scales, "k_scales", u8, dev), _ptr(v_scales, "v_scales", u8, dev),
+        _ptr(slot_mapping, "slot_mapping", torch.int64, dev), T, Hkv, D, B, NB, _dtype_code(k), _stream_on(stream, dev)))
 
 
 def kv_cache_write_fp8_rows(k_new, v_new, k_cache, v_cache, k_scales, v_scales, slot_mapping, stream=None) -> None:
@@ -408,14 +425,14 @@ def kv_cache_write_fp8_rows(k_new, v_new, k_cache, v_cache, k_scales, v_scales, 
     power-of-two scale per row, chosen here, and store both: codes in k_cache /
     v_cache uint8 [NB, Hkv, B, D], scales in k_scales / v_scales uint8
     [NB, Hkv, B] (exponent + 127), at slot_mapping[t] (int64; negative = skip)."""
-    _fp8_rows_args("kv_cache_write_fp8_rows", k_new, v_new, k_cache, v_cache, k_scales, v_scales, slot_mapping, stream)
+    _fp8_rows_call("kv_cache_write_fp8_rows", k_new, v_new, k_cache, v_cache, k_scales, v_scales, slot_mapping, stream)
 
 
 def kv_cache_read_fp8_rows(k_out, v_out, k_cache, v_cache, k_scales, v_scales, slot_mapping, stream=None):
     """The values of the cache rows at slot_mapping[t], into k_out / v_out
     [T, Hkv, D] (bf16, exact, or float32).  Rows of negative slots are left as
     they were.  Returns (k_out, v_out)."""
-    _fp8_rows_args("kv_cache_read_fp8_rows", k_out, v_out, k_cache, v_cache, k_scales, v_scales, slot_mapping, stream)
+    _fp8_rows_call("kv_cache_read_fp8_rows", k_out, v_out, k_cache, v_cache, k_scales, v_scales, slot_mapping, stream)
     return k_out, v_out
 
 
@@ -429,29 +446,22 @@ def paged_attention_multi_token_scored_workspace_size(num_q_tokens: int, num_hea
                                                                              max_seq_len))
 
 
-def _scored_shapes(out, q, k_cache, v_cache, block_tables, seq_lens, num_queries, softcap, alibi_slopes, window,
-                   prefix_lens, key_starts):
+def _scored_shapes(out, q, k_cache, v_cache, block_tables, seq_lens, alibi_slopes, prefix_lens, key_starts):
+    """(T, Hq, D, NB, Hkv, B, S, maxB) of a scored attention call."""
     T, Hq, D = q.shape
     NB, Hkv, B, Dk = k_cache.shape
     S = seq_lens.shape[0]
-    if Dk != D or tuple(out.shape) != (T, Hq, D) or v_cache.shape != k_cache.shape or T != num_queries:
+    if Dk != D or out.shape != q.shape or v_cache.shape != k_cache.shape:
         raise ValueError("shape mismatch")
-    if block_tables.dim() != 2 or block_tables.shape[0] != S:
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or seq_lens.dim() != 1:
         raise ValueError("block_tables must be [S, maxB] and seq_lens [S]")
-    if alibi_slopes is not None and tuple(alibi_slopes.shape) != (Hq,):
+    if alibi_slopes is not None and alibi_slopes.shape != (Hq,):
         raise ValueError("alibi_slopes must be [Hq]")
-    if prefix_lens is not None and tuple(prefix_lens.shape) != (S,):
+    if prefix_lens is not None and prefix_lens.shape != (S,):
         raise ValueError("prefix_lens must be [S]")
-    if key_starts is not None and tuple(key_starts.shape) != (T,):
+    if key_starts is not None and key_starts.shape != (T,):
         raise ValueError("key_starts needs one entry per query")
-    return T, Hq, D, NB, Hkv, B, S
-
-
-def _score_ptrs(scale, softcap, alibi_slopes, window, prefix_lens, key_starts):
-    return (float(scale), float(softcap),
-            _dev(alibi_slopes, "alibi_slopes", torch.float32, 1) if alibi_slopes is not None else None, int(window),
-            _dev(prefix_lens, "prefix_lens", torch.int32, 1) if prefix_lens is not None else None,
-            _dev(key_starts, "key_starts", torch.int32, 1) if key_starts is not None else None)
+    return T, Hq, D, NB, Hkv, B, S, block_tables.shape[1]
 
 
 def paged_attention_decode_scored(out, q, k_cache, v_cache, block_tables, seq_lens, scale: float, max_seq_len: int,
@@ -464,28 +474,26 @@ def paged_attention_decode_scored(out, q, k_cache, v_cache, block_tables, seq_le
     if t >= key_starts[s] and (t < prefix_lens[s] or window == 0 or
     p - t < window) (int32 [S] each).  With k_new / v_new [S, Hkv, D] the new
     tokens are stored first.  A query that sees nothing gets zeros."""
-    lib = _lib.load()
-    S, Hq, D, NB, Hkv, B, _ = _scored_shapes(out, q, k_cache, v_cache, block_tables, seq_lens, seq_lens.shape[0], softcap,
-                                             alibi_slopes, window, prefix_lens, key_starts)
+    S, Hq, D, NB, Hkv, B, n, maxb = _scored_shapes(out, q, k_cache, v_cache, block_tables, seq_lens, alibi_slopes,
+                                                   prefix_lens, key_starts)
+    if n != S:
+        raise ValueError("one query per sequence")
     if (k_new is None) != (v_new is None):
         raise ValueError("give both k_new and v_new, or neither")
-    if k_new is not None and (tuple(k_new.shape) != (S, Hkv, D) or v_new.shape != k_new.shape):
+    if k_new is not None and (k_new.shape != (S, Hkv, D) or v_new.shape != k_new.shape):
         raise ValueError("k_new/v_new must be [S, Hkv, D]")
-    dt = _dtype_code(q)
-    for t, n in ((out, "out"), (k_cache, "k_cache"), (v_cache, "v_cache"), (k_new, "k_new"), (v_new, "v_new")):
-        if t is not None and t.dtype != q.dtype:
-            raise TypeError(f"{n} dtype differs from q")
-    with _On(stream, out=out, q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, seq_lens=seq_lens,
-             alibi_slopes=alibi_slopes, prefix_lens=prefix_lens, key_starts=key_starts, k_new=k_new, v_new=v_new,
-             workspace=workspace) as on:
-        ws, ws_bytes = on.scratch(workspace, paged_attention_decode_scored_workspace_size(S, Hq, D, max_seq_len))
-        st = lib.paged_attention_decode_scored(
-            _dev(out, "out"), _dev(q, "q"), _dev(k_new, "k_new") if k_new is not None else None,
-            _dev(v_new, "v_new") if v_new is not None else None, _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
-            _dev(block_tables, "block_tables", torch.int32, 2), _dev(seq_lens, "seq_lens", torch.int32, 1), S, Hq, Hkv, D,
-            B, block_tables.shape[1], NB, int(max_seq_len),
-            *_score_ptrs(scale, softcap, alibi_slopes, window, prefix_lens, key_starts), ws, ws_bytes, dt, on.stream)
-    _check(st, "paged_attention_decode_scored")
+    lib, code, dt, i32 = _lib.load(), _dtype_code(q), q.dtype, torch.int32
+    dev = _device_of(q, "q")
+    ws, ws_bytes = _scratch(workspace, 0 if workspace is not None else
+                            lib.paged_attention_decode_scored_workspace_size(S, Hq, D, int(max_seq_len)), stream, dev)
+    _run_on(dev, "paged_attention_decode_scored", lib.paged_attention_decode_scored, (
+        _ptr(out, "out", dt, dev), _ptr(q, "q", dt, dev), _opt_ptr(k_new, "k_new", dt, dev),
+        _opt_ptr(v_new, "v_new", dt, dev), _ptr(k_cache, "k_cache", dt, dev), _ptr(v_cache, "v_cache", dt, dev),
+        _ptr(block_tables, "block_tables", i32, dev), _ptr(seq_lens, "seq_lens", i32, dev), S, Hq, Hkv, D, B, maxb, NB,
+        int(max_seq_len), float(scale), float(softcap), _opt_ptr(alibi_slopes, "alibi_slopes", torch.float32, dev),
+        min(int(window), 2 ** 31 - 1),
+        _opt_ptr(prefix_lens, "prefix_lens", i32, dev), _opt_ptr(key_starts, "key_starts", i32, dev), ws, ws_bytes, code,
+        _stream_on(stream, dev)))
     return out
 
 
@@ -495,22 +503,24 @@ def paged_attention_decode_scored_fp8_rows(out, q, k_cache, v_cache, k_scales, v
                                            workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """paged_attention_decode_scored over a row-scaled FP8 cache (codes uint8
     [NB, Hkv, B, D], scales uint8 [NB, Hkv, B]); q / out bf16 [S, Hq, D]."""
-    lib = _lib.load()
-    S, Hq, D, NB, Hkv, B, _ = _scored_shapes(out, q, k_cache, v_cache, block_tables, seq_lens, seq_lens.shape[0], softcap,
-                                             alibi_slopes, window, prefix_lens, key_starts)
-    if tuple(k_scales.shape) != (NB, Hkv, B) or tuple(v_scales.shape) != (NB, Hkv, B):
+    S, Hq, D, NB, Hkv, B, n, maxb = _scored_shapes(out, q, k_cache, v_cache, block_tables, seq_lens, alibi_slopes,
+                                                   prefix_lens, key_starts)
+    if n != S:
+        raise ValueError("one query per sequence")
+    if k_scales.shape != (NB, Hkv, B) or v_scales.shape != (NB, Hkv, B):
         raise ValueError("scales must be [NB, Hkv, B]")
-    with _On(stream, out=out, q=q, k_cache=k_cache, v_cache=v_cache, k_scales=k_scales, v_scales=v_scales,
-             block_tables=block_tables, seq_lens=seq_lens, alibi_slopes=alibi_slopes, prefix_lens=prefix_lens,
-             key_starts=key_starts, workspace=workspace) as on:
-        ws, ws_bytes = on.scratch(workspace, paged_attention_decode_scored_workspace_size(S, Hq, D, max_seq_len))
-        st = lib.paged_attention_decode_scored_fp8_rows(
-            _dev(out, "out", torch.bfloat16), _dev(q, "q", torch.bfloat16), _dev(k_cache, "k_cache", torch.uint8),
-            _dev(v_cache, "v_cache", torch.uint8), _dev(k_scales, "k_scales", torch.uint8),
-            _dev(v_scales, "v_scales", torch.uint8), _dev(block_tables, "block_tables", torch.int32, 2),
-            _dev(seq_lens, "seq_lens", torch.int32, 1), S, Hq, Hkv, D, B, block_tables.shape[1], NB, int(max_seq_len),
-            *_score_ptrs(scale, softcap, alibi_slopes, window, prefix_lens, key_starts), ws, ws_bytes, on.stream)
-    _check(st, "paged_attention_decode_scored_fp8_rows")
+    lib, bf, u8, i32 = _lib.load(), torch.bfloat16, torch.uint8, torch.int32
+    dev = _device_of(q, "q")
+    ws, ws_bytes = _scratch(workspace, 0 if workspace is not None else
+                            lib.paged_attention_decode_scored_workspace_size(S, Hq, D, int(max_seq_len)), stream, dev)
+    _run_on(dev, "paged_attention_decode_scored_fp8_rows", lib.paged_attention_decode_scored_fp8_rows, (
+        _ptr(out, "out", bf, dev), _ptr(q, "q", bf, dev), _ptr(k_cache, "k_cache", u8, dev),
+        _ptr(v_cache, "v_cache", u8, dev), _ptr(k_scales, "k_scales", u8, dev), _ptr(v_scales, "v_scales", u8, dev),
+        _ptr(block_tables, "block_tables", i32, dev), _ptr(seq_lens, "seq_lens", i32, dev), S, Hq, Hkv, D, B, maxb, NB,
+        int(max_seq_len), float(scale), float(softcap), _opt_ptr(alibi_slopes, "alibi_slopes", torch.float32, dev),
+        min(int(window), 2 ** 31 - 1),
+        _opt_ptr(prefix_lens, "prefix_lens", i32, dev), _opt_ptr(key_starts, "key_starts", i32, dev), ws, ws_bytes,
+        _stream_on(stream, dev)))
     return out
 
 
@@ -523,22 +533,22 @@ def paged_attention_multi_token_scored(out, q, k_cache, v_cache, block_tables, s
     t >= key_starts[row] (int32 [T], not decreasing over a sequence's queries)
     and (t < prefix_lens[s], or t <= p and (window == 0 or p - t < window)); the
     bias is - alibi_slopes[h] * |p - t|."""
-    lib = _lib.load()
-    T, Hq, D, NB, Hkv, B, S = _scored_shapes(out, q, k_cache, v_cache, block_tables, seq_lens, q.shape[0], softcap,
-                                             alibi_slopes, window, prefix_lens, key_starts)
-    if tuple(q_starts.shape) != (S + 1,):
+    T, Hq, D, NB, Hkv, B, S, maxb = _scored_shapes(out, q, k_cache, v_cache, block_tables, seq_lens, alibi_slopes,
+                                                   prefix_lens, key_starts)
+    if q_starts.shape != (S + 1,):
         raise ValueError("q_starts must be [S + 1]")
-    with _On(stream, out=out, q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, seq_lens=seq_lens,
-             q_starts=q_starts, alibi_slopes=alibi_slopes, prefix_lens=prefix_lens, key_starts=key_starts,
-             workspace=workspace) as on:
-        ws, ws_bytes = on.scratch(workspace, paged_attention_multi_token_scored_workspace_size(T, Hq, D, max_seq_len))
-        st = lib.paged_attention_multi_token_scored(
-            _dev(out, "out", torch.bfloat16), _dev(q, "q", torch.bfloat16), _dev(k_cache, "k_cache", torch.bfloat16),
-            _dev(v_cache, "v_cache", torch.bfloat16), _dev(block_tables, "block_tables", torch.int32, 2),
-            _dev(seq_lens, "seq_lens", torch.int32, 1), _dev(q_starts, "q_starts", torch.int32, 1), S, T, Hq, Hkv, D, B,
-            block_tables.shape[1], NB, int(max_q_len), int(max_seq_len),
-            *_score_ptrs(scale, softcap, alibi_slopes, window, prefix_lens, key_starts), ws, ws_bytes, on.stream)
-    _check(st, "paged_attention_multi_token_scored")
+    lib, bf, i32 = _lib.load(), torch.bfloat16, torch.int32
+    dev = _device_of(q, "q")
+    ws, ws_bytes = _scratch(workspace, 0 if workspace is not None else
+                            lib.paged_attention_multi_token_scored_workspace_size(T, Hq, D, int(max_seq_len)), stream, dev)
+    _run_on(dev, "paged_attention_multi_token_scored", lib.paged_attention_multi_token_scored, (
+        _ptr(out, "out", bf, dev), _ptr(q, "q", bf, dev), _ptr(k_cache, "k_cache", bf, dev),
+        _ptr(v_cache, "v_cache", bf, dev), _ptr(block_tables, "block_tables", i32, dev),
+        _ptr(seq_lens, "seq_lens", i32, dev), _ptr(q_starts, "q_starts", i32, dev), S, T, Hq, Hkv, D, B, maxb, NB,
+        int(max_q_len), int(max_seq_len), float(scale), float(softcap),
+        _opt_ptr(alibi_slopes, "alibi_slopes", torch.float32, dev), min(int(window), 2 ** 31 - 1),
+        _opt_ptr(prefix_lens, "prefix_lens", i32, dev), _opt_ptr(key_starts, "key_starts", i32, dev), ws, ws_bytes,
+        _stream_on(stream, dev)))
     return out
 
 

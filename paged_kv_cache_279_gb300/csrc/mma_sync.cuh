@@ -71,4 +71,9 @@ __device__ __forceinline__ float f16x2_hi(uint32_t v) {
     return __half2float(__ushort_as_half((unsigned short)(v >> 16)));
 }
 
+// The same with rows 8 - 15 of A zero.
+__device__ __forceinline__ void mma_f16_8816(float (&d)[4], uint32_t a0, uint32_t a2, uint32_t b0, uint32_t b1) {
+    mma_f16_16816(d, a0, 0u, a2, 0u, b0, b1);
+}
+
 }  // namespace pkv

@@ -15,11 +15,15 @@
 //
 //     S^T = K Q^T  (tokens x heads, m16n8k16)      x = cap and bias of S, base 2
 //     O^T += V^T P^T, P = 2^(x - m)                running m, l per head
-// Row-scaled FP8: codes widen to f16 (exact).  A key's scale 2^ke multiplies its
-// scores.  A value's scale 2^ve goes into the weight, w = 2^(x + ve - m) with m
-// the maximum of x + ve, so that w <= 1 uses f16's range whatever the scales;
-// l sums w 2^-ve, and out = o / l as before.
+// Row-scaled FP8: codes widen to f16 (exact); the first product is taken heads x
+// tokens, so that the weights come out in the layout the second one takes and a
+// lane deals with one head.  (E4M3 operands of mma.sync, the query as a sum of
+// two, were no faster: 920 instructions a tile against 720.)  A key's scale 2^ke
+// multiplies its scores.  A value's scale 2^ve goes into the weight, w = 2^(x +
+// ve - m + 14) with m the maximum of x + ve, so that w <= 2^14 uses f16's range
+// whatever the scales are; l sums w 2^-ve, and out = o / l as before.
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cmath>
 
@@ -27,6 +31,12 @@
 #include "pkv_internal.cuh"
 #include "scored.cuh"
 
+#ifndef LEAD8
+#define LEAD8 2
+#define LEAD16 3
+#define MS8 8
+#define MS16 16
+#endif
 namespace pkv {
 namespace scored {
 namespace {
@@ -37,8 +47,8 @@ constexpr int kMaxWarps = 2048;   // partial slots in the workspace: two per war
 template <int D, bool F8>
 struct Tile {
     static constexpr int kTok = F8 ? 32 : 16;
-    static constexpr int kLead = F8 ? 2 : 3;      // empty tiles in front of a segment
-    static constexpr int kMinShare = F8 ? 8 : 16; // tiles (256 tokens), less where every segment is shorter
+    static constexpr int kLead = F8 ? LEAD8 : LEAD16;      // empty tiles in front of a segment
+    static constexpr int kMinShare = F8 ? MS8 : MS16; // tiles (256 tokens), less where every segment is shorter
     static constexpr int kKV = kTok * D * (F8 ? 1 : 2);
     static constexpr int kStage = 2 * kKV;
     static constexpr int kScales = F8 ? 2 * kTok : 0;  // per stage: K scales, V scales
@@ -106,8 +116,9 @@ struct Slot {
     int t0;         // first token
 };
 
-// Running state of a warp: heads 2tq and 2tq + 1, sixteen head_dim rows per
-// fragment (which ones: see attend).
+// Running state of a warp: O of heads 2tq and 2tq + 1, sixteen head_dim rows per
+// fragment (which ones: see entry()); m and l of the same heads (bf16) or of head
+// g (FP8, in [0]).
 template <int D>
 struct Acc {
     float m[2], l[2];
@@ -119,8 +130,6 @@ struct Acc {
         for (int i = 0; i < D / 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     }
     __device__ __forceinline__ void scale(float a0, float a1) {
-        l[0] *= a0;
-        l[1] *= a1;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
             o[i][0] *= a0;
@@ -131,12 +140,13 @@ struct Acc {
     }
 };
 
-// A head's query as MMA operand, and what its scores need.
+// The queries as MMA operand, and what their scores need: of heads 2tq, 2tq + 1
+// (bf16) or of head g (FP8, in [0]).
 template <int D>
 struct Query {
     uint32_t b[D / 16][2];
-    float f[2];      // factor of the raw products of heads 2tq, 2tq + 1
-    float slope[2];  // slope * log2 e
+    float f[2];             // factor of the raw products
+    float slope[2];         // slope * log2 e
 };
 
 template <int D, bool F8>
@@ -151,8 +161,8 @@ __device__ __forceinline__ void load_query(const DecodeArgs &a, int seq, int kvh
             q.b[k][1] = g < a.group ? *reinterpret_cast<const uint32_t *>(row + 16 * k + 8 + 2 * t) : 0u;
         }
     } else {
-        // entries 16c + 4t .. + 3, the order in which the K fragments receive the codes; times a power of two that takes
-        // the head's largest |q| into [2^14, 2^15) (exact: 8 significant bits)
+        // entries 16c + 4t .. + 3, the order in which the keys' codes come; times a power of two that takes the head's largest
+        // |q| into [2^14, 2^15) (exact: 8 significant bits)
         uint2 w[D / 16];
         float amax = 0.f;
 #pragma unroll
@@ -164,21 +174,22 @@ __device__ __forceinline__ void load_query(const DecodeArgs &a, int seq, int kvh
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
         const int fe = min(253, max(1, 268 - (int)((__float_as_uint(amax) >> 23) & 0xffu)));
-        const float f = __uint_as_float((uint32_t)fe << 23), back = __uint_as_float((uint32_t)(254 - fe) << 23);
+        const float f = __uint_as_float((uint32_t)fe << 23);
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) {
             q.b[c][0] = pack_f16x2(bf16x2_lo(w[c].x) * f, bf16x2_hi(w[c].x) * f);
             q.b[c][1] = pack_f16x2(bf16x2_lo(w[c].y) * f, bf16x2_hi(w[c].y) * f);
         }
-        q.f[0] *= __shfl_sync(0xffffffffu, back, 8 * t);
-        q.f[1] *= __shfl_sync(0xffffffffu, back, 8 * t + 4);
+        q.f[0] *= __uint_as_float((uint32_t)(254 - fe) << 23);
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-        q.slope[j] = a.s.slopes && 2 * t + j < a.group ? a.s.slopes[h0 + 2 * t + j] * 1.44269504f : 0.f;
+    for (int j = 0; j < 2; ++j) {
+        const int h = F8 ? g : 2 * t + j;
+        q.slope[j] = a.s.slopes && h < a.group && (!F8 || j == 0) ? a.s.slopes[h0 + h] * 1.44269504f : 0.f;
+    }
 }
 
-// Raw product -> score in base 2: `f` the head's (and key's) factor, away = |p - t|.
+// Raw product -> score in base 2: `f` the head's factor, away = p - t.
 __device__ __forceinline__ float score(float s, float f, float c2, float slope, float away) {
     float x = s * f;
     // c tanh z = c - 2 c / (1 + e^2z), good to 2^-21 of c
@@ -205,8 +216,12 @@ __device__ __forceinline__ void move_to(Acc<D> &acc, const float (&x)[N][2], flo
     ref[0] = n0 == -INFINITY ? 0.f : n0;
     ref[1] = n1 == -INFINITY ? 0.f : n1;
     // the maxima rarely move once a few tiles are in
-    if (__any_sync(0xffffffffu, n0 != acc.m[0] || n1 != acc.m[1]))
-        acc.scale(ex2_approx(acc.m[0] - ref[0]), ex2_approx(acc.m[1] - ref[1]));
+    if (__any_sync(0xffffffffu, n0 != acc.m[0] || n1 != acc.m[1])) {
+        const float a0 = ex2_approx(acc.m[0] - ref[0]), a1 = ex2_approx(acc.m[1] - ref[1]);
+        acc.l[0] *= a0;
+        acc.l[1] *= a1;
+        acc.scale(a0, a1);
+    }
     acc.m[0] = n0;
     acc.m[1] = n1;
 }
@@ -239,7 +254,7 @@ __device__ __forceinline__ void attend_bf16(const DecodeArgs &a, unsigned char *
     for (int i = 0; i < 2; ++i) {
         const int tok = r0 + 8 * i;
         const bool seen = (ok >> tok) & 1u;
-        const float away = (float)abs(pos - t.t0 - tok);
+        const float away = (float)(pos - t.t0 - tok);  // p >= t: no key past the query's position
 #pragma unroll
         for (int j = 0; j < 2; ++j) x[i][j] = seen ? score(sc[2 * i + j], q.f[j], a.c2, q.slope[j], away) : -INFINITY;
     }
@@ -276,47 +291,62 @@ __device__ __forceinline__ void attend_fp8(const DecodeArgs &a, unsigned char *s
         }
         __syncwarp();
     }
-    const int g = lane >> 2, tq = lane & 3, lj = lane >> 3, lr = lane & 7;
+    const int g = lane >> 2, tq = lane & 3, lr = lane & 7;
     const uint32_t ska = smem_u32(sk), sva = smem_u32(sv);
-    float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-    // a lane's four codes of a 16-byte chunk are entries 4t .. 4t + 3, split as the fragment's k pairs like the queries
+    // S (heads x tokens): row g head g, columns 2tq, 2tq + 1 of eight tokens each
+    float sc[4][4];
 #pragma unroll
-    for (int k = 0; k < D / 32; ++k) {
-        uint32_t x[2][4];
+    for (int n = 0; n < 4; ++n) {
+        sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            ldmatrix_x4(ska + code_chunk<D>(16 * h + lr + 8 * (lj & 1), 2 * k + (lj >> 1)), x[h][0], x[h][1], x[h][2], x[h][3]);
+        for (int k = 0; k < D / 16; k += 4) {  // four 16-byte chunks of eight token rows at once
+            uint32_t x[4];
+            ldmatrix_x4(ska + code_chunk<D>(8 * n + lr, k + (lane >> 3)), x[0], x[1], x[2], x[3]);
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t a0, a1, a2, a3;
-                e4m3x4_to_f16(x[h][2 * c], a0, a2);
-                e4m3x4_to_f16(x[h][2 * c + 1], a1, a3);
-                mma_f16_16816(sc[h], a0, a1, a2, a3, q.b[2 * k + c][0], q.b[2 * k + c][1]);
+            for (int c = 0; c < 4; ++c) {
+                uint32_t b0, b1;
+                e4m3x4_to_f16(x[c], b0, b1);
+                mma_f16_8816(sc[n], q.b[k + c][0], q.b[k + c][1], b0, b1);
             }
+        }
     }
-    float x[4][2], back[4], ref[2];  // scores plus the value's exponent; 2^-ve
+    // head g, tokens 8n + 2tq + i: scores xs, and x with the value's exponent
+    const bool full = ok == 0xffffffffu;
+    const float b0 = -q.slope[0] * (float)(pos - t.t0 - 2 * tq);  // p >= t: no key past the query's position
+    float x[4][2], xs[4][2], mx = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int tok = g + 8 * i;
-        const bool seen = (ok >> tok) & 1u;
-        const float kf = row_scale(ss[tok]);
-        const int vb = ss[32 + tok];
-        back[i] = seen ? __uint_as_float((uint32_t)(254 - vb) << 23) : 0.f;
-        const float away = (float)abs(pos - t.t0 - tok), ve = (float)(vb - 127);
+    for (int n = 0; n < 4; ++n) {
+        const uint32_t kb = *reinterpret_cast<const uint16_t *>(ss + 8 * n + 2 * tq);
+        const uint32_t vb = *reinterpret_cast<const uint16_t *>(ss + 32 + 8 * n + 2 * tq);
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-            x[i][j] = seen ? score(sc[i >> 1][2 * (i & 1) + j], q.f[j] * kf, a.c2, q.slope[j], away) + ve : -INFINITY;
+        for (int i = 0; i < 2; ++i) {
+            const float kf = __uint_as_float(i ? (kb & 0xff00u) << 15 : (kb & 0xffu) << 23);
+            const float ve = __uint_as_float(0x4b000000u | (i ? vb >> 8 : vb & 0xffu)) - 8388735.f;  // 2^23 + byte, less 2^23 + 127
+            float s = sc[n][i] * (q.f[0] * kf);
+            if (a.c2 > 0.f) s = a.c2 - 2.f * a.c2 * rcp_approx(1.f + ex2_approx(s));
+            if (a.s.slopes) s += fmaf(q.slope[0], (float)(8 * n + i), b0);
+            if (!full && !((ok >> (8 * n + 2 * tq + i)) & 1u)) s = -INFINITY;
+            xs[n][i] = s;
+            x[n][i] = s + ve;
+            if (!full && s == -INFINITY) x[n][i] = -INFINITY;  // the scale of a token that is not seen may be anything
+            mx = fmaxf(mx, x[n][i]);
+        }
     }
-    move_to<D>(acc, x, ref);
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    const float top = fmaxf(acc.m[0], mx), ref = top == -INFINITY ? 0.f : top;
+    if (__any_sync(0xffffffffu, top != acc.m[0])) {
+        const float f = ex2_approx(acc.m[0] - ref);
+        acc.l[0] *= f;
+        acc.scale(__shfl_sync(0xffffffffu, f, 8 * tq), __shfl_sync(0xffffffffu, f, 8 * tq + 4));
+    }
+    acc.m[0] = top;
+    const float up = 14.f - ref;  // weights up to 2^14
     uint32_t p[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        p[i] = pack_f16x2(ex2_approx(x[i][0] - ref[0]), ex2_approx(x[i][1] - ref[1]));
-        acc.l[0] = fmaf(f16x2_lo(p[i]), back[i], acc.l[0]);
-        acc.l[1] = fmaf(f16x2_hi(p[i]), back[i], acc.l[1]);
-        p[i] = movmatrix_trans(p[i]);
+    for (int n = 0; n < 4; ++n) {
+        p[n] = pack_f16x2(ex2_approx(x[n][0] + up), ex2_approx(x[n][1] + up));
+        acc.l[0] += ex2_approx(xs[n][0] + up) + ex2_approx(xs[n][1] + up);  // w 2^-ve
     }
     // V^T fragments from token rows: lane (g, tq) reads D / 8 consecutive entries of tokens 2tq, 2tq + 1, 2tq + 8, 2tq + 9
     // and pairs two tokens' bytes; fragment i holds entries D/8 g + 2i (rows g) and + 1 (rows g + 8)
@@ -413,7 +443,7 @@ scored_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L.bars) + warp * kNS;
     if (lane == 0) {
 #pragma unroll
-        for (int i = 0; i < kNS; ++i) mbar_init(&bars[i], 1);
+        for (int i = 0; i < kNS; ++i) mbar_init(&bars[i], F8 ? 5 : 1);  // the expected bytes, four lanes' scale bytes
         fence_barrier_init();
     }
     __syncthreads();
@@ -478,27 +508,31 @@ scored_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
 
     const int boxh = min(B, TT);
     // Issue tile k of the share (held by lane k % 32 of `from`) into its stage.
-    auto issue = [&](const Slot &from, int k) {
+    auto issue = [&](const Slot &from, int k, bool wrote) {
         const int buf = k % kNS;
         const int y0 = __shfl_sync(0xffffffffu, from.y0, k & 31), y1 = __shfl_sync(0xffffffffu, from.y1, k & 31);
         const uint32_t dk = smem_u32(ring + buf * T_::kStage), dv = dk + T_::kKV, b = smem_u32(&bars[buf]);
         const int n = (y0 >= 0) + (y1 >= 0);
         if (lane == 0) {
-            fence_proxy_async();  // the stage's generic accesses come before the copies
-            mbar_arrive_expect_tx(&bars[buf], (uint32_t)(n * boxh) * (F8 ? 2u * D + 2u : 4u * D));
+            if (wrote) fence_proxy_async();  // rows of the stage zeroed by plain stores: the copies come after them
+            mbar_arrive_expect_tx(&bars[buf], (uint32_t)(n * boxh) * (F8 ? 2u * D : 4u * D));
         }
         __syncwarp();
+        // As few copies as the scattered blocks allow: an SM starts one TMA copy in some 50 cycles, whatever its size (with
+        // the scale bytes as bulk copies of their own, eight copies a tile, 8 x 16000 FP8 tokens took 58 us).
         if constexpr (F8) {
-            // lanes: (box, K codes / V codes / K scales / V scales)
-            const int sb = lane >> 2, what = lane & 3, y = sb ? y1 : y0;
-            if (lane < 8 && y >= 0) {
-                const uint32_t off = (uint32_t)(sb * boxh);
-                if (what < 2)
-                    tma_load_2d((what ? dv : dk) + off * D, what ? &tm_v : &tm_k, b, 0, y);
-                else
-                    bulk_load(smem_u32(scales + buf * T_::kScales) + (what - 2) * TT + off, (what == 2 ? a.k_scales : a.v_scales) + y,
-                              (uint32_t)boxh, b);
+            // lanes 0 - 3: (box, codes of K / V) by TMA; 4 - 7: their scale bytes by cp.async, which arrive on the barrier too
+            const int sb = (lane >> 1) & 1, isv = lane & 1, y = sb ? y1 : y0;
+            if (lane < 4) {
+                if (y >= 0) tma_load_2d((isv ? dv : dk) + (uint32_t)(sb * boxh) * D, isv ? &tm_v : &tm_k, b, 0, y);
+            } else if (lane < 8) {
+                if (y >= 0)
+                    for (int c = 0; c < boxh; c += 16)
+                        cp_async16(smem_u32(scales + buf * T_::kScales) + isv * TT + sb * boxh + c, (isv ? a.v_scales : a.k_scales) + y + c);
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(b) : "memory");
             }
+        } else if (D == 128 && boxh == 16) {
+            if (lane < 2 && y0 >= 0) tma_load_3d(lane ? dv : dk, lane ? &tm_v : &tm_k, b, 0, y0, 0);  // both halves in one box
         } else {
             // lanes: (box, half, K / V)
             constexpr int H = D / 64;
@@ -510,7 +544,7 @@ scored_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     const int ntiles = hi - lo;
 #pragma unroll
     for (int k = 0; k < kNS; ++k)
-        if (k < ntiles) issue(cur, k);
+        if (k < ntiles) issue(cur, k, false);
 
     int seq = seq_of(lo), kvh, seg0, segn;  // the segment being attended, its laid-out start and tiles
     auto locate = [&](int t) {
@@ -553,7 +587,7 @@ scored_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 else attend_bf16<D>(a, sk, sk + T_::kKV, t, pos, q, acc, lane);
             }
             __syncwarp();
-            if (k + kNS < ntiles && !dead) issue(((k + kNS) & 31) < kNS ? nxt : cur, k + kNS);
+            if (k + kNS < ntiles && !dead) issue(((k + kNS) & 31) < kNS ? nxt : cur, k + kNS, t.mask != (TT == 32 ? 0xffffffffu : 0xffffu));
             if ((k & 31) == 31) {
                 cur = nxt;
                 nxt = resolve(lo + k + 33);
@@ -561,10 +595,21 @@ scored_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         }
         // ---- the piece's result ----
         const int g = lane >> 2, tq = lane & 3, G = a.group;
+        if constexpr (F8) {  // head g's, over its four lanes; then to the lanes of its column
+            acc.l[0] += __shfl_xor_sync(0xffffffffu, acc.l[0], 1);
+            acc.l[0] += __shfl_xor_sync(0xffffffffu, acc.l[0], 2);
+            const float l = acc.l[0], m = acc.m[0];
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < 2; ++j) {
+                acc.l[j] = __shfl_sync(0xffffffffu, l, 8 * tq + 4 * j);
+                acc.m[j] = __shfl_sync(0xffffffffu, m, 8 * tq + 4 * j);
+            }
+        } else {
 #pragma unroll
-            for (int sh = 4; sh < 32; sh <<= 1) acc.l[j] += __shfl_xor_sync(0xffffffffu, acc.l[j], sh);
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int sh = 4; sh < 32; sh <<= 1) acc.l[j] += __shfl_xor_sync(0xffffffffu, acc.l[j], sh);
+        }
         const bool whole = pa <= s0 + T_::kLead && pb == s1;  // every real tile
         const int64_t w0 = share_owner(s0 + T_::kLead, T, parts);  // the warp with the segment's first real tile
         if (gw == w0 && lane == 0)
@@ -600,6 +645,8 @@ scored_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
 // piece of warp w0 + j); zero rows where no key is seen.
 template <int D>
 __global__ void __launch_bounds__(128) scored_decode_merge_kernel(const __grid_constant__ DecodeArgs a) {
+    // Not earlier: the next call's CTAs would take their places while this kernel's wait beside the attention kernel's last
+    // ones, and end up two on some SMs (8 x 16000 tokens FP8: 58 -> 71 us).
     grid_dependency_wait();
     grid_launch_dependents();
     const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
@@ -680,16 +727,25 @@ pkv_status launch(const DecodeArgs &a, cudaStream_t st) {
     auto kern = scored_decode_kernel<D, F8>;
     if (!ensure_smem(kern, Smem<D, F8>(kMaxDecodeSeqs).total, done)) return PKV_ERR_CUDA;
     const int smem = Smem<D, F8>(a.num_seqs).total;
-    int per_sm = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kNW * 32, smem) != cudaSuccess || per_sm < 1)
-        return PKV_ERR_CUDA;
+    // CTAs per SM, asked once per shared-memory size in a row (the devices of a process are alike): (size << 8) | CTAs
+    static std::atomic<int64_t> known{0};
+    int64_t k = known.load(std::memory_order_relaxed);
+    if ((k >> 8) != smem) {
+        int per = 0;
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, kNW * 32, smem) != cudaSuccess || per < 1)
+            return PKV_ERR_CUDA;
+        known.store(k = ((int64_t)smem << 8) | per, std::memory_order_relaxed);
+    }
+    const int per_sm = (int)(k & 255);
     const int grid = std::min(sm_count() * per_sm, kMaxWarps / kNW);
     if (grid < 1) return PKV_ERR_CUDA;
     CUtensorMap mk, mv;
     const int64_t rows = (int64_t)a.num_blocks * a.num_kv_heads * a.block_size;
     const int boxh = std::min(a.block_size, Tile<D, F8>::kTok);
     if (F8 ? !make_code_map(&mk, a.k_cache, rows, D, boxh) || !make_code_map(&mv, a.v_cache, rows, D, boxh)
-           : !make_cache_map(&mk, a.k_cache, rows, D, boxh) || !make_cache_map(&mv, a.v_cache, rows, D, boxh))
+        : D == 128 && boxh == 16
+            ? !make_slab_map(&mk, a.k_cache, rows, D, boxh) || !make_slab_map(&mv, a.v_cache, rows, D, boxh)
+            : !make_cache_map(&mk, a.k_cache, rows, D, boxh) || !make_cache_map(&mv, a.v_cache, rows, D, boxh))
         return PKV_ERR_CUDA;
     pkv_status rc = launch_pdl(kern, dim3((unsigned)grid), dim3(kNW * 32), smem, st, mk, mv, a);
     if (rc == PKV_OK)

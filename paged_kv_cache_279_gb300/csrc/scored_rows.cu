@@ -1141,19 +1141,6 @@ __global__ void __launch_bounds__(128) scored_rows_merge_kernel(const __grid_con
                             pack_bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
 }
 
-// 3-D view of a bf16 cache, one box per (block, kv head) slab: [half][block row][128 B].
-bool make_slab_map(CUtensorMap *map, const void *base, int64_t rows, int D, int B) {
-    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
-    if (!enc) return false;
-    cuuint64_t dims[3] = {64u, (cuuint64_t)rows, (cuuint64_t)(D / 64)};
-    cuuint64_t strides[2] = {(cuuint64_t)D * 2, 128u};
-    cuuint32_t box[3] = {64u, (cuuint32_t)B, (cuuint32_t)(D / 64)};
-    cuuint32_t estr[3] = {1u, 1u, 1u};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 struct WsLayout {
     size_t o, ml, merges, total;
     explicit WsLayout(int D) {
