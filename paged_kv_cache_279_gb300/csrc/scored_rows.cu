@@ -1,35 +1,35 @@
 // Scored attention of several queries per sequence (prefill, chunks of one,
 // verification of drafted tokens) on the 5th-generation tensor cores.
 //
-// Per KV head, the query heads of consecutive queries form rows that meet the
-// same 128-key tiles of the paged cache:
+// Per KV head, the query heads of consecutive queries form up to 128 rows that
+// meet the same 128-key tiles of the paged cache:
 //     S = Q K^T (M 128 rows, N 128 keys, K head_dim)      scores, in tensor memory
 //     P = 2^(y(S) - m)                                     y: the score in base 2, capped and biased
 //     O += P V  (M 128, N head_dim, K 128 keys)
 // with a running reference m and sum l per row; m moves (and O is rescaled)
 // only when a tile's maximum passes it by more than 2^8.
 //
-// A context is a set of at most 256 rows (two groups of 128: paired) or, where
-// no sequence has more than 128, of at most 128 rows whose tiles the two groups
-// take in turn (alternating; their states are merged at the context's end).
-// Its tiles are those that some row sees: the tiles of the always visible
-// prefix, then those from the first row's window or document to the last row's
-// position.  All contexts are laid end to end, each behind kCharge virtual
-// tiles that stand for its fixed costs, and every CTA (one per SM) takes an
-// equal share.  A context cut by a share's border leaves partial states (o, m,
-// l) in the workspace, which a second kernel merges; no CTA waits for another.
+// A context is one such set of rows and the tiles that some row sees: those of
+// the always visible prefix, then those from the first row's window or document
+// to the last row's position.  All contexts are laid end to end, each behind
+// kCharge virtual tiles that stand for its fixed costs, and every CTA (one per
+// SM) takes an equal share.  A context cut by a share's border leaves partial
+// states (o, m, l) in the workspace, which a second kernel merges; no CTA waits
+// for another.
 //
-// Warps: 0-7 and 8-15 two softmax groups (two threads per row = TMEM lane, one
-// for each half of a tile's keys), 16 the MMA issuer, 17 / 18 the producers of
-// K / V tiles (one TMA box per block and column half, or per block), 19 the
-// scheduler, which walks the share and publishes one descriptor per piece of a
-// context.  While one group works on
-// its scores the tensor cores run the other's products: the issue order is
-// P V (group 0), Q K^T (0, next tile), P V (1), Q K^T (1, next tile).
-// Tensor memory: S of group g at columns 128 g (P overwrites its first half as
-// bf16 pairs), O at 256 + g * head_dim.  A row's S being complete implies that
-// every earlier product of the issuing thread is, P V of its group included, so
-// a rescale of O needs no wait of its own.
+// What bounds it is the softmax step between the two products (special-function,
+// FMA and issue slots, and its latency), so three tiles are in flight per SM:
+// three S buffers, three sets of four warps (a thread per row = TMEM lane), tile
+// t with set t % 3, one O.  Two chains of 128 x 128 tiles with an O each left the
+// tensor cores idle between them (8 x 512 queries of 4096: 311 us).
+//
+// Warps: 0-11 the softmax sets, 12-15 the epilogue (reads O at a context's end
+// while the sets go on), 16 the MMA issuer, 17 / 18 the producers of K (a column
+// half each) and 19 of V (one TMA box per block: one warp starts a box in some 60
+// cycles), 20 the scheduler, which walks the share, publishes one descriptor per
+// piece of a context and loads its queries (one box per column half).
+// Tensor memory: S at columns 128 (t % 3) (P overwrites its first half as bf16
+// pairs), O at 384.
 // Every wait is bounded; one that gives up flags PKV_DEVERR_TIMEOUT.
 #include <algorithm>
 #include <climits>
@@ -43,20 +43,23 @@ namespace scored {
 namespace {
 
 constexpr int kTok = 128;   // keys per tile
-constexpr int kRows = 128;  // rows of a softmax group
-constexpr int kHalf = kTok / 2;      // a softmax thread's keys of a tile
-constexpr int kGroupWarps = 8;       // two halves of four warps
-constexpr int kThreads = 640;
-constexpr int kMmaWarp = 16, kKWarp = 17, kVWarp = 18, kSchedWarp = 19;
-constexpr int kDescs = 6;  // piece descriptors in flight
-constexpr int kRecs = 8;  // tile records (more than the K producer can be ahead of the softmax)
-constexpr int kCharge = 2;   // virtual tiles of a context
+constexpr int kRows = 128;  // rows of a context
+constexpr int kSets = 3;    // softmax sets and S buffers
+constexpr int kEpiWarp = 4 * kSets, kMmaWarp = 16, kKWarp = 17, kVWarp = 19, kSchedWarp = 20, kPvWarp = 21;
+constexpr int kThreads = 22 * 32;
+constexpr int kDescs = 6;   // piece descriptors in flight
+constexpr int kRecs = 8;    // tile records (more than the K producers can be ahead of the softmax)
+#ifndef CHARGE
+#define CHARGE 2
+#endif
+constexpr int kCharge = CHARGE;  // virtual tiles of a context
 constexpr int kMinShare = kCharge + 1;
 constexpr float kRescale = 8.f;
 constexpr float kMaxC2 = 73.f;  // softcap * log2 e up to which capped scores take a fixed reference (cap 50)
-constexpr uint32_t kTmemCols = 512, kOBase = 256;
+constexpr uint32_t kTmemCols = 512, kOBase = kSets * kTok;
 constexpr int kMaxCtas = 160;   // partial slots in the workspace: two per CTA
 constexpr int kMergeRows = 32;  // rows per CTA of the merge kernel
+
 enum Kind { kPlain = 0, kCap = 1, kBias = 2, kCapBias = 3 };
 
 struct RowsArgs : Args {
@@ -64,8 +67,8 @@ struct RowsArgs : Args {
     float c2;       // capped: softcap * log2 e
     float m0;       // capped: the reference
     float near[4], far[6];  // capped: c2 tanh(k1 s) = s * sum near[i] s^2i for |k1 s| <= kTanhNear (far: kTanhFar)
-    float *part_o;  // [2 kMaxCtas][D][256]: columns of 256 rows
-    float *part_ml; // [2 kMaxCtas][256][2]
+    float *part_o;  // [2 kMaxCtas][D][kRows]: columns of rows
+    float *part_ml; // [2 kMaxCtas][kRows][2]
     int4 *merges;   // [kMaxCtas]: (parts, first query row, rows, kv head) of the context begun and cut in that share
     int bshift, per_ctx, scan_w;  // log2 block size, queries per context, lanes per sequence in the scan
 };
@@ -76,42 +79,35 @@ struct Piece {
     int np, pt0, mt0;   // context tile i is key tile pt0 + i (i < np) or mt0 + i - np
     int seq, kvh, row0, nrows, pos0, pre;
     int ks0, cpre, lo, hi;  // the context's keys: [ks0, cpre) and [lo, hi) (KeyRange)
-    int slot;                 // partial slot, -1: the whole context
-    int jf[2], jl[2];         // group g takes the tiles jf .. jl (none: jl < jf); alternating: those of its parity
+    int fks, flo, fhi;      // keys that every row sees: [flo, fhi) and [fks, pre)
+    int slot;               // partial slot, -1: the whole context
 };
 
-// A tile's record, written by the K producer.
+// A tile's record, written by the first K producer.
 struct TileRec {
     int t0;        // first key
     uint32_t bad;  // bits of blocks with an invalid id (their keys are masked)
     int whole;     // every key is seen by some row: no V row has to be zeroed
-    int pad;
+    int full;      // every key is seen by every row
 };
 
-__device__ __forceinline__ int key_tile(const Piece &p, int j) {
-    const int i = p.i0 + j;
-    return i < p.np ? p.pt0 + i : p.mt0 + i - p.np;
-}
-template <bool ALT>
-__device__ __forceinline__ bool has_rows(const Piece &p, int g) { return ALT || p.nrows > g * kRows; }
-template <int D, bool ALT>
+template <int D>
 struct Layout {
     static constexpr int H = D / 64;
     static constexpr int kQTile = H * kRows * 128;
-    static constexpr int kQBytes = (ALT ? 1 : 2) * kQTile;
     static constexpr int kTile = H * kTok * 128;  // K or V of one tile
     static constexpr int NK = D == 128 ? 2 : 4;
-    static constexpr int NV = D == 128 ? (ALT ? 3 : 2) : 4;
-    static constexpr int q = 0;
-    static constexpr int kring = q + kQBytes;
+    static constexpr int NV = D == 128 ? 2 : 4;
+    static constexpr int q = 0;                         // two tiles of queries
+    static constexpr int kring = q + 2 * kQTile;
     static constexpr int vring = kring + NK * kTile;
-    static constexpr int xch = vring + NV * kTile;        // float [2][2 groups][2 halves][kRows]: maxima of even / odd tiles
-    static constexpr int fin_ml = xch + 8 * kRows * 4;    // float2 [2 groups][2 halves][kRows]: (m, l) at a piece's end
-    static constexpr int desc = fin_ml + 4 * kRows * 8;
+    static constexpr int fin_ml = vring + NV * kTile;   // float2 [2][kSets][kRows]: (m, l) of a piece's rows, pieces in turn
+    static constexpr int mref = fin_ml + 2 * kSets * kRows * 8;  // float [kRows]: the rows' reference after the latest tile
+    static constexpr int desc = mref + kRows * 4;
     static constexpr int recs = (desc + kDescs * (int)sizeof(Piece) + 15) & ~15;
     static constexpr int bars = recs + kRecs * (int)sizeof(TileRec);
-    static constexpr int kBars = 2 * NK + 2 * NV + 6 * 2 + 2 * kDescs + 1 + 8;
-    static constexpr int misc = bars + kBars * 8;  // TMEM address, scan scratch
+    static constexpr int kBars = 2 * NK + 2 * NV + 3 * kSets + 4 * kSets + 4 + 2 + 4 + 2 * kDescs + 2;
+    static constexpr int misc = bars + kBars * 8;       // TMEM address, scan scratch
     static constexpr int total = misc + 128;
     static_assert(total <= 227 * 1024, "shared memory per CTA");
 };
@@ -353,103 +349,121 @@ __device__ __forceinline__ void weights32(const float (&s)[32], float f, float n
     st16u(to, pk);
 }
 
-// One tile of one row's half (64 keys): 32 keys at a time in loops that are not
-// unrolled -- unrolled code of 128 keys ran at the pace of its instruction
-// fetches (6 to 10 cycles an instruction).  S (raw products) at sp, P (bf16
-// pairs) back over the half's first 32 columns, always behind the reads.  t0:
-// the half's first key; bad: bits of its blocks with an invalid id; beyond: some
-// row may see keys past its position (a prefix).  Returns with `move` set when O
-// has to be scaled by `alpha` before the tile's product.
+// The rows' running reference over the tiles of a piece, handed from tile to tile.
+struct Chain {
+    float *mref;        // this row's
+    uint64_t *before;   // the tile before has left its reference (nullptr: the CTA's first tile)
+    uint64_t *mine;     // this tile has
+    uint64_t *done;     // the tile before's product is complete
+    uint32_t parity;    // of both
+    bool first;         // the piece's first tile
+};
+
+// One tile of one row, 32 keys at a time in loops that are not unrolled --
+// unrolled code of 128 keys ran at the pace of its instruction fetches (6 to 10
+// cycles an instruction).  S (raw products) at sp, P (bf16 pairs) back over its
+// first 64 columns, always behind the reads.  beyond: some row may see keys past
+// its position (a prefix).
 //
-// A first pass finds the maximum, meet() gives the row's (both halves weigh by
-// the same reference); scores that are biased or masked are written back over S
-// by it, in base 2 (plain ones stay raw: the exponential's FMA scales them).
+// A first pass finds the maximum; scores that are biased or masked are written
+// back over S by it, in base 2 (plain ones stay raw: the exponential's FMA scales
+// them).  The reference then follows from the tile before's, and where it moves,
+// O (complete up to that tile) is rescaled before this tile's weights go out.
 // Capped scores without a bias need neither: they lie within +-c2, and up to
 // kMaxC2 a fixed reference c2 / 4 keeps weights within 2^-(5/4 c2) .. 2^(3/4 c2)
 // (cap 50: 2^-90 .. 2^54), far from the ends of float32's and bf16's range for
 // sums over 2^20 keys of V entries between 2^-36 and 2^53.
-template <int KIND, typename Meet>
-__device__ __forceinline__ void softmax_half(uint32_t sp, int t0, uint32_t bad, const RowsArgs &a, bool beyond,
-                                             RowState &st, bool &move, float &alpha, Meet meet) {
-    const bool mine = ((t0 >= st.r.lo && t0 + kHalf <= st.r.hi) || (t0 >= st.r.first && t0 + kHalf <= st.r.pre)) && bad == 0u;
-    const bool full = __all_sync(0xffffffffu, mine);
-    move = false;
-    alpha = 1.f;
+template <int D, int KIND>
+__device__ __forceinline__ void softmax_tile(uint32_t sp, uint32_t op, const TileRec &rec, const RowsArgs &a, bool beyond,
+                                             RowState &st, const Chain &ch, int lane, bool &dead) {
+    const int t0 = rec.t0;
+    const bool full = rec.full != 0;
     uint64_t ls[2] = {0ull, 0ull};
     if constexpr (KIND == kCap) {
-        // every score lies within +-c2: one reference does for all tiles (and every part of a context); 16 keys are loaded
-        // while 16 are worked on
+        // 16 keys are loaded while 16 are worked on
         const float nm = -st.m;
         const uint64_t nm2 = f32x2(nm, nm);
         float x0[16], x1[16];
         ld16(sp, x0);
 #pragma unroll 1
-        for (int c = 0; c < kHalf; c += 32) {
-            const uint32_t w = full ? 0u : seen32(st.r, t0 + c, bad, a.bshift, c / 32);
+        for (int c = 0; c < kTok; c += 32) {
+            const uint32_t w = full ? 0u : seen32(st.r, t0 + c, rec.bad, a.bshift, c / 32);
             tc::wait_ld();
             ld16(sp + c + 16, x1);
             cap_weights16(x0, sp + c, sp + c / 2, a, nm, nm2, full, w, ls);
             tc::wait_ld();
-            if (c + 32 < kHalf) ld16(sp + c + 32, x0);
+            if (c + 32 < kTok) ld16(sp + c + 32, x0);
             cap_weights16(x1, sp + c + 16, sp + c / 2 + 8, a, nm, nm2, full, w >> 16, ls);
         }
-        float x, y;
-        f32x2_split(add_f32x2(ls[0], ls[1]), x, y);
-        st.l += x + y;
-        tc::wait_st();
-        return;
-    }
-    const bool stored = KIND != kPlain || !full;
-    float mt = -INFINITY;
+    } else {
+        const bool stored = KIND != kPlain || !full;
+        float mt = -INFINITY;
 #pragma unroll 1
-    for (int c = 0; c < kHalf / 32; ++c) {
-        float s[32];
-        tc::ld32(sp + 32 * c, s);
-        tc::wait_ld();
-        const int t = t0 + 32 * c;
-        if constexpr (KIND == kCapBias) cap32(s, a);
-        if constexpr (KIND == kBias || KIND == kCapBias) {
-            const float f = KIND == kBias ? a.k1 : 1.f, d0 = (float)(st.p - t);
-            if (beyond) {
+        for (int c = 0; c < kTok / 32; ++c) {
+            float s[32];
+            tc::ld32(sp + 32 * c, s);
+            tc::wait_ld();
+            const int t = t0 + 32 * c;
+            if constexpr (KIND == kCapBias) cap32(s, a);
+            if constexpr (KIND == kBias || KIND == kCapBias) {
+                const float f = KIND == kBias ? a.k1 : 1.f, d0 = (float)(st.p - t);
+                if (beyond) {
 #pragma unroll
-                for (int k = 0; k < 32; ++k) s[k] = fmaf(-st.slope2, fabsf(d0 - (float)k), s[k] * f);
-            } else {
-                // -slope (p - t - k): one FMA for the pair's bias, one for the score
-                const uint64_t f2 = f32x2(f, f), b0 = f32x2(-st.slope2 * d0, -st.slope2 * d0), sl = f32x2(st.slope2, st.slope2);
+                    for (int k = 0; k < 32; ++k) s[k] = fmaf(-st.slope2, fabsf(d0 - (float)k), s[k] * f);
+                } else {
+                    // -slope (p - t - k): one FMA for the pair's bias, one for the score
+                    const uint64_t f2 = f32x2(f, f), b0 = f32x2(-st.slope2 * d0, -st.slope2 * d0), sl = f32x2(st.slope2, st.slope2);
 #pragma unroll
-                for (int k = 0; k < 32; k += 2)
-                    f32x2_split(fma_f32x2(f32x2(s[k], s[k + 1]), f2, fma_f32x2(sl, f32x2((float)k, (float)(k + 1)), b0)), s[k],
-                                s[k + 1]);
+                    for (int k = 0; k < 32; k += 2)
+                        f32x2_split(fma_f32x2(f32x2(s[k], s[k + 1]), f2, fma_f32x2(sl, f32x2((float)k, (float)(k + 1)), b0)), s[k],
+                                    s[k + 1]);
+                }
+            }
+            if (!full) {
+                const uint32_t w = seen32(st.r, t, rec.bad, a.bshift, c);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) s[k] = (w >> k) & 1u ? s[k] : -INFINITY;
+            }
+            mt = fmaxf(mt, max_of<false>(s));
+            if (stored) tc::st32(sp + 32 * c, s);
+        }
+        if (stored) tc::wait_st();
+        if (KIND == kPlain) mt *= a.k1;
+        // the reference
+        if (ch.before) wait_or_flag(ch.before, ch.parity, dead, a.err);
+        const float old = ch.first ? -INFINITY : *ch.mref;
+        float m = old;
+        if (mt != -INFINITY && !(mt <= old + kRescale)) m = mt;  // also where nothing was seen before
+        *ch.mref = m;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ch.mine);
+        if (st.m != m) {
+            st.l = st.m == -INFINITY ? st.l : st.l * ex2_approx(st.m - m);
+            st.m = m;
+        }
+        const bool move = old != -INFINITY && m != old;
+        if (__any_sync(0xffffffffu, move)) {
+            wait_or_flag(ch.done, ch.parity, dead, a.err);
+            tc::fence_after();
+            const float alpha = move ? ex2_approx(old - m) : 1.f;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                float o[32];
+                tc::ld32(op + c * 32, o);
+                tc::wait_ld();
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] *= alpha;
+                tc::st32(op + c * 32, o);
             }
         }
-        if (!full) {
-            const uint32_t w = seen32(st.r, t, bad, a.bshift, c);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) s[k] = (w >> k) & 1u ? s[k] : -INFINITY;
-        }
-        mt = fmaxf(mt, max_of<false>(s));
-        if (stored) tc::st32(sp + 32 * c, s);
-    }
-    if (stored) tc::wait_st();
-    if (KIND == kPlain) mt *= a.k1;
-    mt = meet(mt);
-    if (mt != -INFINITY) {
-        if (st.m == -INFINITY) {
-            st.m = mt;  // nothing summed yet
-        } else if (mt > st.m + kRescale) {
-            alpha = ex2_approx(st.m - mt);
-            st.m = mt;
-            st.l *= alpha;
-            move = true;
-        }
-    }
-    const float nm = st.m == -INFINITY ? 0.f : -st.m, f = KIND == kPlain ? a.k1 : 1.f;
+        const float nm = m == -INFINITY ? 0.f : -m, f = KIND == kPlain ? a.k1 : 1.f;
 #pragma unroll 1
-    for (int c = 0; c < kHalf / 32; ++c) {
-        float s[32];
-        tc::ld32(sp + 32 * c, s);
-        tc::wait_ld();
-        weights32(s, f, nm, sp + 16 * c, ls);
+        for (int c = 0; c < kTok / 32; ++c) {
+            float s[32];
+            tc::ld32(sp + 32 * c, s);
+            tc::wait_ld();
+            weights32(s, f, nm, sp + 16 * c, ls);
+        }
     }
     float x, y;
     f32x2_split(add_f32x2(ls[0], ls[1]), x, y);
@@ -460,30 +474,33 @@ __device__ __forceinline__ void softmax_half(uint32_t sp, int t0, uint32_t bad, 
 // ---------------------------------------------------------------------------
 // The kernel
 // ---------------------------------------------------------------------------
-template <int D, int KIND, bool ALT>
+template <int D, int KIND>
 __global__ void __launch_bounds__(kThreads, 1)
-scored_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                   const __grid_constant__ RowsArgs a) {
-    using L = Layout<D, ALT>;
+scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ RowsArgs a) {
+    using L = Layout<D>;
     constexpr int H = L::H, NK = L::NK, NV = L::NV;
     extern __shared__ __align__(1024) unsigned char smem[];
     Piece *descs = reinterpret_cast<Piece *>(smem + L::desc);
     TileRec *recs = reinterpret_cast<TileRec *>(smem + L::recs);
-    float *xch = reinterpret_cast<float *>(smem + L::xch);
     float2 *fin_ml = reinterpret_cast<float2 *>(smem + L::fin_ml);
+    float *mref = reinterpret_cast<float *>(smem + L::mref);
     uint64_t *k_full = reinterpret_cast<uint64_t *>(smem + L::bars), *k_empty = k_full + NK;
     uint64_t *v_full = k_empty + NK, *v_empty = v_full + NV;
-    uint64_t *s_full = v_empty + NV, *p_full = s_full + 2;      // per group
-    uint64_t *q_ready = p_full + 2, *o_last = q_ready + 2, *o_free = o_last + 2;
-    uint64_t *desc_full = o_free + 2, *desc_empty = desc_full + kDescs, *fin = desc_empty + kDescs;
-    uint64_t *xch_full = fin + 1;   // per group: its rows' m and l of a piece are in xch
-    uint64_t *pair = xch_full + 2;  // [2][4]: both halves of 32 rows have posted
+    uint64_t *s_full = v_empty + NV, *p_full = s_full + kSets, *o_done = p_full + kSets;  // per set
+    uint64_t *m_full = o_done + kSets;                                                   // [set][4]: per warp
+    uint64_t *q_full = m_full + 4 * kSets, *q_empty = q_full + 2;                        // per query tile
+    uint64_t *o_last = q_empty + 2, *o_free = o_last + 1;
+    uint64_t *fin_full = o_free + 1, *fin_empty = fin_full + 2;                          // pieces in turn
+    uint64_t *desc_full = fin_empty + 2, *desc_empty = desc_full + kDescs, *all_done = desc_empty + kDescs;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::misc);
-    int *scratch = reinterpret_cast<int *>(smem + L::misc + 16);  // [20] warp sums, carry, found sequence, its start
+    int *scratch = reinterpret_cast<int *>(smem + L::misc + 16);  // [22] warp sums, carry, found sequence, its start
+    constexpr int kCarry = kThreads / 32, kFound = kCarry + 1, kStart = kCarry + 2;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int Hkv = a.num_kv_heads, G = a.group, B = a.block_size;
 
     if (threadIdx.x == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_q)) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
     }
@@ -494,8 +511,8 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         return;
     }
 
-    // ---- scan: laid-out tiles of every sequence; scan_w lanes share one ----
-    const int W = a.scan_w, per_pass = kThreads / W, sub = threadIdx.x % W;
+    // ---- scan: laid-out tiles of every sequence; scan_w lanes share one (of 640 threads: whole groups of lanes) ----
+    const int W = a.scan_w, per_pass = 640 / W, sub = threadIdx.x % W;
     auto seq_total = [&](int s, bool report) {
         int t = 0;
         if (s < a.num_seqs) {
@@ -511,10 +528,10 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     int start = 0, v = 0;  // this thread's sequence of the last pass: its laid-out start and tiles
     // the total, then the sequence that holds this share's start (from registers when one pass covers every sequence)
     for (int round = 0; round < (a.num_seqs > per_pass ? 2 : 1); ++round) {
-        if (threadIdx.x == 0) scratch[20] = 0;
+        if (threadIdx.x == 0) scratch[kCarry] = 0;
         __syncthreads();
         for (int base = 0; base < a.num_seqs; base += per_pass) {
-            const int s = base + threadIdx.x / W;
+            const int s = threadIdx.x < 640 ? base + threadIdx.x / W : a.num_seqs;
             const int total = seq_total(s, round == 0 && blockIdx.x == 0);
             v = sub == 0 ? total : 0;
             int x = v;
@@ -525,20 +542,20 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             }
             if (lane == 31) scratch[warp] = x;
             __syncthreads();
-            int before = scratch[20];
+            int before = scratch[kCarry];
             for (int w = 0; w < warp; ++w) before += scratch[w];
             const int end = before + x;
             start = end - v;
             if (round == 1 && v > 0 && my_s0 >= start && my_s0 < end) {
-                scratch[21] = s;
-                scratch[22] = start;
+                scratch[kFound] = s;
+                scratch[kStart] = start;
             }
             __syncthreads();
-            if (threadIdx.x == kThreads - 1) scratch[20] = end;
+            if (threadIdx.x == kThreads - 1) scratch[kCarry] = end;
             __syncthreads();
         }
         if (round == 0) {
-            T = scratch[20];
+            T = scratch[kCarry];
             parts = split_parts(T, gridDim.x);
             __syncthreads();  // every thread has the total before the next round clears it
             if (threadIdx.x == 0) a.merges[blockIdx.x] = make_int4(0, 0, 0, 0);
@@ -549,33 +566,39 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     }
     const int s0 = my_s0, s1 = my_s1;
     if (a.num_seqs <= per_pass && v > 0 && s0 >= start && s0 < start + v) {
-        scratch[21] = threadIdx.x / W;
-        scratch[22] = start;
+        scratch[kFound] = threadIdx.x / W;
+        scratch[kStart] = start;
     }
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NK; ++i) {
-            mbar_init(&k_full[i], 1);
+            mbar_init(&k_full[i], H);
             mbar_init(&k_empty[i], 1);
         }
         for (int i = 0; i < NV; ++i) {
             mbar_init(&v_full[i], 1);
             mbar_init(&v_empty[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kSets; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], kGroupWarps);
-            mbar_init(&q_ready[i], kGroupWarps);
-            mbar_init(&o_last[i], 1);
-            mbar_init(&o_free[i], ALT ? 2 * kGroupWarps : kGroupWarps);
-            mbar_init(&xch_full[i], kGroupWarps);
+            mbar_init(&p_full[i], 4);
+            mbar_init(&o_done[i], 1);
         }
+        for (int i = 0; i < 4 * kSets; ++i) mbar_init(&m_full[i], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&q_full[i], 1);
+            mbar_init(&q_empty[i], 1);
+            mbar_init(&fin_full[i], 4 * kSets);
+            mbar_init(&fin_empty[i], 4);
+        }
+        mbar_init(o_last, 1);
+        mbar_init(o_free, 4);
         for (int i = 0; i < kDescs; ++i) {
             mbar_init(&desc_full[i], 1);
-            mbar_init(&desc_empty[i], 2 * kGroupWarps + 3);  // softmax warps, producers, MMA
+            mbar_init(&desc_empty[i], 4 * kSets + 4 + 2 + H + 1);  // softmax, epilogue, MMA, producers
         }
-        for (int i = 0; i < 8; ++i) mbar_init(&pair[i], 2);
-        mbar_init(fin, 1);
+        mbar_init(&all_done[0], 1);
+        mbar_init(&all_done[1], 1);
         fence_barrier_init();
     }
     if (warp == kMmaWarp) {
@@ -589,495 +612,403 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     tc::fence_after();
     const uint32_t tmem = *tmem_slot;
     const uint32_t q_s = smem_u32(smem + L::q), k_s = smem_u32(smem + L::kring), v_s = smem_u32(smem + L::vring);
+    bool dead = false;
 
-    if (warp >= 2 * kGroupWarps) {
-        bool dead = false;
-        if (warp == kSchedWarp) {
-            // ======================= scheduler =======================
-            int s = scratch[21];
-            int t = s0;                 // next laid-out tile of the share
-            int seq_start = scratch[22];  // laid-out start of sequence s
-            int p = 0;
-            while (t < s1 && !dead) {
-                const Seq x = load_seq(a, s, false);
-                const int fp = first_pos(a, x, s), nb = (x.Q + a.per_ctx - 1) / a.per_ctx;
-                int per_kvh = 0;
-                for (int b = lane; b < nb; b += 32) per_kvh += laid_out(ctx_tiles(a, x, fp, b).n);
+    if (warp == kSchedWarp) {
+        // ======================= scheduler =======================
+        int s = scratch[kFound];
+        int t = s0;                     // next laid-out tile of the share
+        int seq_start = scratch[kStart];  // laid-out start of sequence s
+        int p = 0;
+        while (t < s1 && !dead) {
+            const Seq x = load_seq(a, s, false);
+            const int fp = first_pos(a, x, s), nb = (x.Q + a.per_ctx - 1) / a.per_ctx;
+            int per_kvh = 0;
+            for (int b = lane; b < nb; b += 32) per_kvh += laid_out(ctx_tiles(a, x, fp, b).n);
 #pragma unroll
-                for (int sh = 16; sh > 0; sh >>= 1) per_kvh += __shfl_xor_sync(0xffffffffu, per_kvh, sh);
-                for (int kvh = per_kvh > 0 ? (t - seq_start) / per_kvh : Hkv; kvh < Hkv && t < s1 && !dead; ++kvh) {
-                    int pos = seq_start + kvh * per_kvh;  // laid-out start of block b0
-                    for (int b0 = 0; b0 < nb && t < s1 && !dead; b0 += 32) {
-                        CtxTiles c{};
-                        if (b0 + lane < nb) c = ctx_tiles(a, x, fp, b0 + lane);
-                        int end = laid_out(c.n);
+            for (int sh = 16; sh > 0; sh >>= 1) per_kvh += __shfl_xor_sync(0xffffffffu, per_kvh, sh);
+            for (int kvh = per_kvh > 0 ? (t - seq_start) / per_kvh : Hkv; kvh < Hkv && t < s1 && !dead; ++kvh) {
+                int pos = seq_start + kvh * per_kvh;  // laid-out start of block b0
+                for (int b0 = 0; b0 < nb && t < s1 && !dead; b0 += 32) {
+                    CtxTiles c{};
+                    if (b0 + lane < nb) c = ctx_tiles(a, x, fp, b0 + lane);
+                    int end = laid_out(c.n);
 #pragma unroll
-                        for (int sh = 1; sh < 32; sh <<= 1) {
-                            const int y = __shfl_up_sync(0xffffffffu, end, sh);
-                            if (lane >= sh) end += y;
-                        }
-                        end += pos;
-                        const int begin = end - laid_out(c.n);
-                        // this lane's context: its real tiles [i0, i1) in the share
-                        const int i0 = max(0, max(s0, begin) - begin - kCharge), i1 = min(s1, end) - begin - kCharge;
-                        const bool mine = c.n > 0 && begin < s1 && end > s0 && i1 > i0;
-                        for (uint32_t todo = __ballot_sync(0xffffffffu, mine); todo && !dead; todo &= todo - 1) {
-                            const int d = p % kDescs;
-                            if (lane == 0 && p >= kDescs)
-                                wait_or_flag(&desc_empty[d], (uint32_t)((p / kDescs - 1) & 1), dead, a.err);
-                            dead = __shfl_sync(0xffffffffu, dead, 0);
-                            if (lane == __ffs(todo) - 1 && !dead) {
-                                Piece pc;
-                                pc.ntiles = i1 - i0;
-                                pc.i0 = i0;
-                                pc.np = c.np;
-                                pc.pt0 = c.pt0;
-                                pc.mt0 = c.mt0;
-                                pc.seq = s;
-                                pc.kvh = kvh;
-                                const int q0 = (b0 + lane) * a.per_ctx;
-                                pc.row0 = x.q0 + q0;
-                                const int nq = min(x.Q - q0, a.per_ctx);
-                                pc.nrows = nq * G;
-                                pc.pos0 = fp + q0;
-                                pc.ks0 = c.ks0;
-                                pc.pre = x.pre;
-                                pc.cpre = c.r.pre;
-                                pc.lo = c.r.lo;
-                                pc.hi = c.r.hi;
-                                const bool begins = begin + kCharge >= s0, ends = end <= s1;
-                                pc.slot = begins && ends ? -1 : 2 * (int)blockIdx.x + (begins ? 1 : 0);
-                                if (begins && !ends)
-                                    // the shares that hold the rest
-                                    a.merges[blockIdx.x] = make_int4(
-                                        (int)share_owner(end - 1, T, parts) - (int)blockIdx.x + 1, pc.row0, pc.nrows, kvh);
-                                for (int g = 0; g < 2; ++g) {
-                                    pc.jf[g] = ALT ? g : 0;
-                                    pc.jl[g] = pc.ntiles - 1;
-                                    if (ALT) continue;
-                                    // tiles at either end that none of the group's rows can see a key of
-                                    const int qa = min(nq - 1, g * kRows / G), qb = min(nq - 1, (g * kRows + kRows - 1) / G);
-                                    const int glo = a.s.window > 0 ? pc.pos0 + qa - a.s.window + 1 : 0, ghi = pc.pos0 + qb + 1;
-                                    auto idle = [&](int j) {
-                                        const int t0 = key_tile(pc, j) * kTok;
-                                        return t0 >= pc.pre && (t0 >= ghi || t0 + kTok <= glo);
-                                    };
-                                    if (pc.nrows <= g * kRows) pc.jl[g] = -1;
-                                    while (pc.jl[g] >= 0 && idle(pc.jl[g])) --pc.jl[g];
-                                    while (pc.jf[g] <= pc.jl[g] && idle(pc.jf[g])) ++pc.jf[g];
-                                }
-                                descs[d] = pc;
-                                mbar_arrive(&desc_full[d]);
+                    for (int sh = 1; sh < 32; sh <<= 1) {
+                        const int y = __shfl_up_sync(0xffffffffu, end, sh);
+                        if (lane >= sh) end += y;
+                    }
+                    end += pos;
+                    const int begin = end - laid_out(c.n);
+                    // this lane's context: its real tiles [i0, i1) in the share
+                    const int i0 = max(0, max(s0, begin) - begin - kCharge), i1 = min(s1, end) - begin - kCharge;
+                    const bool mine = c.n > 0 && begin < s1 && end > s0 && i1 > i0;
+                    for (uint32_t todo = __ballot_sync(0xffffffffu, mine); todo && !dead; todo &= todo - 1) {
+                        const int d = p % kDescs;
+                        if (lane == 0 && p >= kDescs)
+                            wait_or_flag(&desc_empty[d], (uint32_t)((p / kDescs - 1) & 1), dead, a.err);
+                        dead = __shfl_sync(0xffffffffu, dead, 0);
+                        if (lane == __ffs(todo) - 1 && !dead) {
+                            Piece pc;
+                            pc.ntiles = i1 - i0;
+                            pc.i0 = i0;
+                            pc.np = c.np;
+                            pc.pt0 = c.pt0;
+                            pc.mt0 = c.mt0;
+                            pc.seq = s;
+                            pc.kvh = kvh;
+                            const int q0 = (b0 + lane) * a.per_ctx;
+                            pc.row0 = x.q0 + q0;
+                            const int nq = min(x.Q - q0, a.per_ctx);
+                            pc.nrows = nq * G;
+                            pc.pos0 = fp + q0;
+                            pc.pre = x.pre;
+                            pc.ks0 = c.ks0;
+                            pc.cpre = c.r.pre;
+                            pc.lo = c.r.lo;
+                            pc.hi = c.r.hi;
+                            // what the last row's document or window leaves, up to the first row's position
+                            pc.fks = max(c.ks0, key_start_of(a.s, pc.row0 + nq - 1));
+                            pc.flo = max(pc.fks, a.s.window > 0 ? pc.pos0 + nq - a.s.window : 0);
+                            pc.fhi = pc.pos0 + 1;
+                            const bool begins = begin + kCharge >= s0, ends = end <= s1;
+                            pc.slot = begins && ends ? -1 : 2 * (int)blockIdx.x + (begins ? 1 : 0);
+                            if (begins && !ends)  // the shares that hold the rest
+                                a.merges[blockIdx.x] = make_int4((int)share_owner(end - 1, T, parts) - (int)blockIdx.x + 1, pc.row0,
+                                                                 pc.nrows, kvh);
+                            descs[d] = pc;
+                            mbar_arrive(&desc_full[d]);
+                            // its queries: per_ctx queries of the KV head's G heads, one box per column half
+                            const int qb = p & 1;
+                            if (p >= 2) wait_or_flag(&q_empty[qb], (uint32_t)((p / 2 - 1) & 1), dead, a.err);
+                            if (!dead) {
+                                mbar_arrive_expect_tx(&q_full[qb], (uint32_t)(H * a.per_ctx * G * 128));
+                                for (int h = 0; h < H; ++h)
+                                    tma_load_3d(q_s + (uint32_t)(qb * L::kQTile + h * (kRows * 128)), &tm_q, smem_u32(&q_full[qb]),
+                                                h * 64, kvh * G, pc.row0);
                             }
-                            __syncwarp();
-                            ++p;
                         }
-                        pos = __shfl_sync(0xffffffffu, end, 31);
-                        t = max(t, min(s1, pos));
+                        dead = __any_sync(0xffffffffu, dead);
+                        ++p;
                     }
-                }
-                seq_start += per_kvh * Hkv;
-                t = max(t, min(s1, seq_start));
-                ++s;
-                if (s >= a.num_seqs) break;
-            }
-            if (lane == 0 && !dead) {
-                const int d = p % kDescs;
-                if (p >= kDescs) wait_or_flag(&desc_empty[d], (uint32_t)((p / kDescs - 1) & 1), dead, a.err);
-                if (!dead) {
-                    descs[d].ntiles = 0;
-                    mbar_arrive(&desc_full[d]);
+                    pos = __shfl_sync(0xffffffffu, end, 31);
+                    t = max(t, min(s1, pos));
                 }
             }
-        } else if (warp == kKWarp || warp == kVWarp) {
-            // ======================= producers =======================
-            const bool isk = warp == kKWarp;
-            const int N = isk ? NK : NV;
-            uint64_t *full = isk ? k_full : v_full, *empty = isk ? k_empty : v_empty;
-            const int bpt = kTok >> a.bshift;  // blocks per tile, at most 16
-            int tau = 0;
-            for (int p = 0; !dead; ++p) {
-                const int d = p % kDescs;
-                if (!wait_or_flag(&desc_full[d], (uint32_t)((p / kDescs) & 1), dead, a.err)) break;
-                const Piece &pc = descs[d];
-                const int n = pc.ntiles;
-                if (n == 0) break;
-                const int32_t *bt = a.block_tables + (int64_t)pc.seq * a.max_blocks;
-                const KeyRange r{pc.ks0, pc.cpre, pc.lo, pc.hi};
-                const int kvh = pc.kvh;
-                // this lane's block of a tile: its id, INT_MIN where no row sees a key of it
-                auto block_id = [&](int j) {
-                    if (j >= n || lane >= bpt) return (int)INT_MIN;
-                    const int t = key_tile(pc, j) * kTok + (lane << a.bshift);
-                    return r.meets(t, t + B) ? (int)bt[t >> a.bshift] | (bt[t >> a.bshift] == INT_MIN ? 1 : 0) : INT_MIN;
-                };
-                int next = block_id(0);
-                for (int j = 0; j < n; ++j, ++tau) {
-                    const int st = tau % N;
-                    const int id = next;
-                    next = block_id(j + 1);
-                    if (tau >= N && lane == 0) wait_or_flag(&empty[st], (uint32_t)((tau / N - 1) & 1), dead, a.err);
-                    dead = __shfl_sync(0xffffffffu, dead, 0);
-                    if (dead) break;
-                    const bool live = id != INT_MIN, bad = live && (id < 0 || id >= a.num_blocks);
-                    const uint32_t nlive = (uint32_t)__popc(__ballot_sync(0xffffffffu, live)), badm = __ballot_sync(0xffffffffu, bad);
-                    if (lane == 0) {
-                        if (isk) {
-                            const int t0 = key_tile(pc, j) * kTok;
-                            TileRec rec;
-                            rec.t0 = t0;
-                            rec.bad = badm;
-                            rec.whole = badm == 0u && ((t0 >= r.lo && t0 + kTok <= r.hi) || (t0 >= r.first && t0 + kTok <= r.pre));
-                            rec.pad = 0;
-                            recs[tau % kRecs] = rec;
-                            if (badm) flag_error(a.err, PKV_DEVERR_BLOCK_ID);
-                        }
-                        mbar_arrive_expect_tx(&full[st], nlive * (uint32_t)(H * 128) << a.bshift);
-                    }
-                    __syncwarp();
-                    // an invalid id is read as block 0, its keys masked
-                    const int y = live ? (int)(((int64_t)(bad ? 0 : id) * Hkv + kvh) * B) : -1;
-                    if (isk) {
-                        const uint32_t dst = k_s + st * L::kTile;
-                        const int jb = lane / H, h = lane % H;
-                        const int yb = __shfl_sync(0xffffffffu, y, jb);
-                        if (jb < bpt && yb >= 0)
-                            tma_load_2d(dst + h * (kTok * 128) + ((jb << a.bshift) * 128), &tm_k, smem_u32(&full[st]), h * 64, yb);
-                    } else if (live) {
-                        tma_load_3d(v_s + st * L::kTile + ((lane << a.bshift) * (H * 128)), &tm_v, smem_u32(&full[st]), 0, y, 0);
-                    }
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&desc_empty[d]);
-            }
-            // copies in flight (only after a timeout) land before the CTA exits
-            if (lane == 0 && dead)
-                for (int k = max(0, tau - N); k < tau; ++k) mbar_wait_bounded(&full[k % N], (uint32_t)((k / N) & 1));
-        } else {
-            // ======================= MMA issuer =======================
-            // The whole warp walks (uniform registers), one elected lane issues.
-            constexpr uint32_t idesc_qk = tc::instr_desc(kTok, false), idesc_pv = tc::instr_desc(D, true);
-            const uint32_t pv_lbo = (uint32_t)(B * 128), pv_sbo = B >= 16 ? 1024u : (uint32_t)(H * B * 128);
-            const bool leader = elect_one();
-            const uint64_t qd0 = tc::smem_desc(q_s, 16, 1024), kd0 = tc::smem_desc(k_s, 16, 1024);
-            const uint64_t vd0 = tc::smem_desc(v_s, pv_lbo, pv_sbo);
-            // 16 keys of V further: inside a block of 32 every second step, else a block (B = 8: two)
-            const uint32_t odd = B == 32 ? 16 * 128 >> 4 : (uint32_t)(H * 16 * 128) >> 4, two = (uint32_t)(2 * H * 16 * 128) >> 4;
-            int tau = 0;
-            int pend[2] = {-1, -1};             // tile whose P V the group still owes
-            bool fresh[2] = {false, false};     // ... and it starts the piece's O
-            bool owe_free[2] = {false, false};  // the previous piece's O may still be being read
-            bool had[2] = {false, false};       // the previous piece had rows of the group
-            int npv[2] = {0, 0}, nof[2] = {0, 0}, nqr[2] = {0, 0};  // phases passed: p_full, o_free, q_ready
-            // the owed product; `closing`: and the end of the piece, everything issued: its softmax may read O
-            auto finish = [&](int g, bool closing) {
-                const int v = pend[g];
-                if (v >= 0 && !dead) {
-                    wait_or_flag(&p_full[g], (uint32_t)(npv[g] & 1), dead, a.err);
-                    wait_or_flag(&v_full[v % NV], (uint32_t)((v / NV) & 1), dead, a.err);
-                    if (fresh[g] && owe_free[g]) {
-                        wait_or_flag(&o_free[g], (uint32_t)(nof[g] & 1), dead, a.err);
-                        ++nof[g];
-                        owe_free[g] = false;
-                    }
-                    if (dead) return;
-                    tc::fence_after();
-                    const uint64_t vd = vd0 + (uint64_t)((uint32_t)(v % NV) * (uint32_t)(L::kTile >> 4));
-                    const uint32_t acc = fresh[g] ? 0u : 1u;
-                    if (leader) {
-#pragma unroll
-                        for (int k = 0; k < kTok / 16; ++k)
-                            tc::mma_ts(tmem + kOBase + (uint32_t)g * D,
-                                       tmem + (uint32_t)(g * kTok + (k < kHalf / 16 ? 8 * k : kHalf + 8 * k - kHalf / 2)),
-                                       vd + (uint64_t)((uint32_t)(k >> 1) * two + (uint32_t)(k & 1) * odd), idesc_pv,
-                                       k == 0 ? acc : 1u);
-                        if (ALT) tc::commit(&v_empty[v % NV]);
-                    }
-                    __syncwarp();
-                    ++npv[g];
-                    pend[g] = -1;
-                }
-                if (!closing || !had[g]) return;
-                if (owe_free[g]) {  // no product of the piece waited for it
-                    wait_or_flag(&o_free[g], (uint32_t)(nof[g] & 1), dead, a.err);
-                    ++nof[g];
-                }
-                owe_free[g] = true;
-                if (leader) tc::commit(&o_last[g]);
-                __syncwarp();
-            };
-            for (int p = 0; !dead; ++p) {
-                const int d = p % kDescs;
-                if (!wait_or_flag(&desc_full[d], (uint32_t)((p / kDescs) & 1), dead, a.err)) break;
-                const int n = descs[d].ntiles, nrows = descs[d].nrows;
-                if (n == 0) break;
-                const int jf[2] = {descs[d].jf[0], descs[d].jf[1]}, jl[2] = {descs[d].jl[0], descs[d].jl[1]};
-                bool started[2] = {false, false};
-                for (int j = 0; j < n && !dead; ++j, ++tau) {
-                    const int st = tau % NK;
-                    bool open = j == 0 && p > 0;  // the previous piece is still to be closed
-                    if (open && !mbar_test_wait(&k_full[st], (uint32_t)((tau / NK) & 1))) {
-                        finish(0, true);  // rather than wait for this piece's keys first
-                        finish(1, true);
-                        open = false;
-                    }
-                    wait_or_flag(&k_full[st], (uint32_t)((tau / NK) & 1), dead, a.err);
-                    const uint64_t kd = kd0 + (uint64_t)((uint32_t)st * (uint32_t)(L::kTile >> 4));
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        const bool act = ALT ? (j & 1) == g : (j >= jf[g] && j <= jl[g]);
-                        if (open || (j > 0 && (!ALT || act))) finish(g, open);
-                        if (j == 0) {
-                            had[g] = ALT || nrows > g * kRows;
-                            if (had[g] && (!ALT || g == 0)) wait_or_flag(&q_ready[g], (uint32_t)(nqr[g]++ & 1), dead, a.err);
-                        }
-                        if (!act || dead) continue;
-                        tc::fence_after();
-                        const uint64_t qd = qd0 + (uint64_t)(ALT ? 0 : g * (L::kQTile >> 4));
-                        if (leader) {
-#pragma unroll
-                            for (int k = 0; k < D / 16; ++k) {
-                                const uint64_t off = (uint64_t)(((k >> 2) * (kTok * 128) + (k & 3) * 32) >> 4);
-                                tc::mma(tmem + (uint32_t)g * kTok, qd + off, kd + off, idesc_qk, k > 0 ? 1u : 0u);
-                            }
-                            tc::commit(&s_full[g]);
-                        }
-                        __syncwarp();
-                        pend[g] = tau;
-                        fresh[g] = !started[g];
-                        started[g] = true;
-                    }
-                    if (dead) break;
-                    if (leader) tc::commit(&k_empty[st]);
-                    if (!ALT && tau > 0) {  // both groups' products with the previous tile's V are issued
-                        wait_or_flag(&v_full[(tau - 1) % NV], (uint32_t)(((tau - 1) / NV) & 1), dead, a.err);
-                        if (leader) tc::commit(&v_empty[(tau - 1) % NV]);
-                    }
-                    __syncwarp();
-                }
-                if (lane == 0) mbar_arrive(&desc_empty[d]);
-            }
-            if (!dead) {
-                finish(0, true);
-                finish(1, true);
-            }
-            // every product has completed before the tensor memory is freed
-            if (leader) tc::commit(fin);
-            __syncwarp();
-            mbar_wait_bounded(fin, 0u);
+            seq_start += per_kvh * Hkv;
+            t = max(t, min(s1, seq_start));
+            ++s;
+            if (s >= a.num_seqs) break;
         }
-    } else {
-        // ======================= softmax =======================
-        const int g = warp >> 3, hf = (warp >> 2) & 1, wq = warp & 3;
-        const int rr = wq * 32 + lane;                // TMEM lane
-        const int cr = ALT ? rr : g * kRows + rr;     // row of the context
-        const uint32_t trow = tmem + ((uint32_t)(wq * 32) << 16);
-        const uint32_t sp = trow + (uint32_t)(g * kTok + hf * kHalf);
-        bool dead = false;
-        int ns = 0;     // tiles of this group so far
-        int npl = 0;    // pieces with rows of this group so far
-        int nmeet = 0;  // meetings of the halves so far
-        int tau0 = 0;
-        // both halves of the warp's rows have come here
-        auto meet_barrier = [&]() {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&pair[g * 4 + wq]);
-            wait_or_flag(&pair[g * 4 + wq], (uint32_t)(nmeet & 1), dead, a.err);
-            ++nmeet;
-        };
-        auto slot = [&](int n, int h) -> float & { return xch[((n & 1) * 4 + g * 2 + h) * kRows + rr]; };
-        auto copy_q = [&](const Piece &pc) {  // this thread's half of its row
-            const bool live = cr < pc.nrows;
-            const int row = pc.row0 + (live ? cr / G : 0), head = pc.kvh * G + cr % G;
-            const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.q) + ((int64_t)row * a.num_heads + head) * D;
-            const uint32_t base = q_s + (ALT ? 0u : (uint32_t)g * L::kQTile) + rr * 128;
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                const int k = hf * (D / 16) + i;
-                const uint32_t dst = base + (k >> 3) * (kRows * 128) + (((k & 7) ^ (rr & 7)) << 4);
-                if (live) cp_async16(dst, src + k * 8);
-                else asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(dst), "r"(0u) : "memory");
+        if (lane == 0 && !dead) {
+            const int d = p % kDescs;
+            if (p >= kDescs) wait_or_flag(&desc_empty[d], (uint32_t)((p / kDescs - 1) & 1), dead, a.err);
+            if (!dead) {
+                descs[d].ntiles = 0;
+                mbar_arrive(&desc_full[d]);
             }
-        };
-        auto q_done = [&]() {
-            cp_async_wait_all();
-            fence_proxy_async();
-            tc::fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&q_ready[ALT ? 0 : g]);
-        };
+        }
+        // queries in flight (only after a timeout) land before the CTA exits
+        if (dead && lane == 0)
+            for (int k = max(0, p - 2); k < p; ++k) mbar_wait_bounded(&q_full[k & 1], (uint32_t)((k >> 1) & 1));
+    } else if (warp == kVWarp || (warp >= kKWarp && warp < kKWarp + H)) {
+        // ======================= producers =======================
+        const bool isk = warp != kVWarp;
+        const int half = warp - kKWarp;  // K: column half
+        const int N = isk ? NK : NV;
+        uint64_t *full = isk ? k_full : v_full, *empty = isk ? k_empty : v_empty;
+        const int bpt = kTok >> a.bshift;  // blocks per tile, at most 16
+        int tau = 0;
         for (int p = 0; !dead; ++p) {
             const int d = p % kDescs;
             if (!wait_or_flag(&desc_full[d], (uint32_t)((p / kDescs) & 1), dead, a.err)) break;
             const Piece &pc = descs[d];
             const int n = pc.ntiles;
             if (n == 0) break;
-            if (p == 0 && (ALT ? g == 0 : has_rows<ALT>(pc, g))) {
-                copy_q(pc);
-                q_done();
+            const int32_t *bt = a.block_tables + (int64_t)pc.seq * a.max_blocks;
+            const KeyRange r{pc.ks0, pc.cpre, pc.lo, pc.hi};
+            const int kvh = pc.kvh, flo = pc.flo, fhi = pc.fhi, fks = pc.fks, pre = pc.pre;
+            const int i1 = pc.i0 + n, np = pc.np, pt0 = pc.pt0, mt0 = pc.mt0;
+            // the latest keys first: with a bias by distance the largest scores come first, and the rows' reference seldom moves
+            auto first_key = [&](int j) {
+                const int i = i1 - 1 - j;
+                return (i < np ? pt0 + i : mt0 + i - np) * kTok;
+            };
+            // this lane's block of a tile: its id, INT_MIN where no row sees a key of it
+            auto block_id = [&](int j) {
+                if (j >= n || lane >= bpt) return (int)INT_MIN;
+                const int t = first_key(j) + (lane << a.bshift);
+                if (!r.meets(t, t + B)) return (int)INT_MIN;
+                return max((int)bt[t >> a.bshift], INT_MIN + 1);
+            };
+            int next = block_id(0);
+            for (int j = 0; j < n; ++j, ++tau) {
+                const int st = tau % N;
+                const int id = next;
+                next = block_id(j + 1);
+                if (tau >= N) wait_or_flag(&empty[st], (uint32_t)((tau / N - 1) & 1), dead, a.err);
+                if (__any_sync(0xffffffffu, dead)) {
+                    dead = true;
+                    break;
+                }
+                const bool live = id != INT_MIN, bad = live && (id < 0 || id >= a.num_blocks);
+                const uint32_t nlive = (uint32_t)__popc(__ballot_sync(0xffffffffu, live)), badm = __ballot_sync(0xffffffffu, bad);
+                if (lane == 0) {
+                    if (isk && half == 0) {
+                        const int t0 = first_key(j);
+                        TileRec rec;
+                        rec.t0 = t0;
+                        rec.bad = badm;
+                        rec.whole = badm == 0u && ((t0 >= r.lo && t0 + kTok <= r.hi) || (t0 >= r.first && t0 + kTok <= r.pre));
+                        rec.full = badm == 0u && ((t0 >= flo && t0 + kTok <= fhi) || (t0 >= fks && t0 + kTok <= pre));
+                        recs[tau % kRecs] = rec;
+                        if (badm) flag_error(a.err, PKV_DEVERR_BLOCK_ID);
+                    }
+                    mbar_arrive_expect_tx(&full[st], nlive * (uint32_t)((isk ? 1 : H) * 128) << a.bshift);
+                }
+                __syncwarp();
+                // an invalid id is read as block 0, its keys masked
+                if (live) {
+                    const int y = (int)(((int64_t)(bad ? 0 : id) * Hkv + kvh) * B);
+                    if (isk)
+                        tma_load_2d(k_s + st * L::kTile + half * (kTok * 128) + ((lane << a.bshift) * 128), &tm_k, smem_u32(&full[st]),
+                                    half * 64, y);
+                    else
+                        tma_load_3d(v_s + st * L::kTile + ((lane << a.bshift) * (H * 128)), &tm_v, smem_u32(&full[st]), 0, y, 0);
+                }
             }
-            const bool live = cr < pc.nrows;
-            // warps without rows only pass the barriers; the other rows of a warp with some go by the last query's keys,
-            // so that they keep no tile from the path without masks
-            const bool live_warp = (ALT ? 0 : g * kRows) + wq * 32 < pc.nrows;
-            const int qi = min(cr, pc.nrows - 1) / G;
-            const int64_t qrow = pc.row0 + qi;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&desc_empty[d]);
+        }
+        // copies in flight (only after a timeout) land before the CTA exits
+        if (lane == 0 && dead)
+            for (int k = max(0, tau - N); k < tau; ++k) mbar_wait_bounded(&full[k % N], (uint32_t)((k / N) & 1));
+    } else if (warp == kMmaWarp) {
+        // ======================= Q K^T issuer =======================
+        // Both issuers walk as whole warps (uniform registers) and one elected lane issues.
+        constexpr uint32_t idesc = tc::instr_desc(kTok, false);
+        const bool leader = elect_one();
+        const uint64_t qd0 = tc::smem_desc(q_s, 16, 1024), kd0 = tc::smem_desc(k_s, 16, 1024);
+        int st = 0, sb = 0;            // K stage, S buffer
+        uint32_t kph = 0, sph = 1;     // their phases (a buffer's first use waits for nothing)
+        int d = 0;
+        uint32_t dph = 0;
+        for (int p = 0;; ++p) {
+            wait_or_flag(&desc_full[d], dph, dead, a.err);
+            const int n = dead ? 0 : descs[d].ntiles;
+            if (n == 0) break;
+            wait_or_flag(&q_full[p & 1], (uint32_t)((p >> 1) & 1), dead, a.err);
+            const uint64_t qd = qd0 + (uint64_t)((uint32_t)(p & 1) * (uint32_t)(L::kQTile >> 4));
+            for (int j = 0; j < n; ++j) {
+                wait_or_flag(&k_full[st], kph, dead, a.err);
+                wait_or_flag(&o_done[sb], sph, dead, a.err);  // the P V that read the buffer before
+                if (dead) break;
+                tc::fence_after();
+                const uint64_t kd = kd0 + (uint64_t)((uint32_t)st * (uint32_t)(L::kTile >> 4));
+                if (leader) {
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint64_t off = (uint64_t)(((k >> 2) * (kTok * 128) + (k & 3) * 32) >> 4);
+                        tc::mma(tmem + (uint32_t)sb * kTok, qd + off, kd + off, idesc, k > 0 ? 1u : 0u);
+                    }
+                    tc::commit(&s_full[sb]);
+                    tc::commit(&k_empty[st]);
+                    if (j + 1 == n) tc::commit(&q_empty[p & 1]);
+                }
+                __syncwarp();
+                if (++st == NK) st = 0, kph ^= 1u;
+                if (++sb == kSets) sb = 0, sph ^= 1u;
+            }
+            if (lane == 0) mbar_arrive(&desc_empty[d]);
+            if (++d == kDescs) d = 0, dph ^= 1u;
+        }
+        if (leader) tc::commit(&all_done[0]);
+        __syncwarp();
+        mbar_wait_bounded(&all_done[0], 0u);
+    } else if (warp == kPvWarp) {
+        // ======================= P V issuer =======================
+        constexpr uint32_t idesc = tc::instr_desc(D, true);
+        const uint32_t pv_lbo = (uint32_t)(B * 128), pv_sbo = B >= 16 ? 1024u : (uint32_t)(H * B * 128);
+        const bool leader = elect_one();
+        const uint64_t vd0 = tc::smem_desc(v_s, pv_lbo, pv_sbo);
+        // 16 keys of V further: inside a block of 32 every second step, else a block (B = 8: two)
+        const uint32_t odd = B == 32 ? 16 * 128 >> 4 : (uint32_t)(H * 16 * 128) >> 4, two = (uint32_t)(2 * H * 16 * 128) >> 4;
+        int st = 0, sb = 0;
+        uint32_t vph = 0, sph = 0;
+        int d = 0;
+        uint32_t dph = 0;
+        for (int p = 0;; ++p) {
+            wait_or_flag(&desc_full[d], dph, dead, a.err);
+            const int n = dead ? 0 : descs[d].ntiles;
+            if (n == 0) break;
+            if (p > 0) wait_or_flag(o_free, (uint32_t)((p - 1) & 1), dead, a.err);  // the piece before's O has been read
+            for (int j = 0; j < n; ++j) {
+                wait_or_flag(&v_full[st], vph, dead, a.err);
+                wait_or_flag(&p_full[sb], sph, dead, a.err);
+                if (dead) break;
+                tc::fence_after();
+                const uint64_t vd = vd0 + (uint64_t)((uint32_t)st * (uint32_t)(L::kTile >> 4));
+                if (leader) {
+#pragma unroll
+                    for (int k = 0; k < kTok / 16; ++k)
+                        tc::mma_ts(tmem + kOBase, tmem + (uint32_t)(sb * kTok + 8 * k),
+                                   vd + (uint64_t)((uint32_t)(k >> 1) * two + (uint32_t)(k & 1) * odd), idesc, j > 0 || k > 0 ? 1u : 0u);
+                    tc::commit(&o_done[sb]);
+                    tc::commit(&v_empty[st]);
+                    if (j + 1 == n) tc::commit(o_last);
+                }
+                __syncwarp();
+                if (++st == NV) st = 0, vph ^= 1u;
+                if (++sb == kSets) sb = 0, sph ^= 1u;
+            }
+            if (lane == 0) mbar_arrive(&desc_empty[d]);
+            if (++d == kDescs) d = 0, dph ^= 1u;
+        }
+        // every product has completed before the tensor memory is freed
+        if (leader) tc::commit(&all_done[1]);
+        __syncwarp();
+        mbar_wait_bounded(&all_done[1], 0u);
+    } else if (warp < kEpiWarp) {
+        // ======================= softmax =======================
+        const int set = warp >> 2, wq = warp & 3;
+        const int rr = wq * 32 + lane;  // TMEM lane and row of the context
+        const uint32_t trow = tmem + ((uint32_t)(wq * 32) << 16);
+        const uint32_t sp = trow + (uint32_t)(set * kTok), op = trow + kOBase;
+        const int prev = set == 0 ? kSets - 1 : set - 1;  // the set of the tile before
+        int tau0 = 0;
+        for (int p = 0; !dead; ++p) {
+            const int d = p % kDescs;
+            if (!wait_or_flag(&desc_full[d], (uint32_t)((p / kDescs) & 1), dead, a.err)) break;
+            const Piece &pc = descs[d];
+            const int n = pc.ntiles, nrows = pc.nrows, pre = pc.pre;
+            if (n == 0) break;
+            // warps without rows only pass the barriers; the other rows of a warp with some go by the last query's keys
+            const bool live_warp = wq * 32 < nrows;
+            const int qi = min(rr, nrows - 1) / G;
             RowState st;
             st.m = KIND == kCap ? a.m0 : -INFINITY;
             st.l = 0.f;
             st.p = pc.pos0 + qi;
-            st.r = key_range(max(pc.ks0, key_start_of(a.s, qrow)), pc.pre, a.s.window, st.p, st.p);
+            st.r = key_range(max(pc.ks0, key_start_of(a.s, (int64_t)pc.row0 + qi)), pre, a.s.window, st.p, st.p);
             st.slope2 = 0.f;
             if constexpr (KIND == kBias || KIND == kCapBias)
-                st.slope2 = a.s.slopes ? a.s.slopes[pc.kvh * G + cr % G] * 1.44269504f : 0.f;
-            // the next piece's queries, once this group's Q is free
-            bool copied = false;
-            auto next_q = [&]() {
-                const int dn = (p + 1) % kDescs;
-                if (!wait_or_flag(&desc_full[dn], (uint32_t)(((p + 1) / kDescs) & 1), dead, a.err)) return;
-                const Piece &nx = descs[dn];
-                if (nx.ntiles > 0 && has_rows<ALT>(nx, g)) {
-                    copy_q(nx);
-                    copied = true;
-                }
-            };
-            const int jf = pc.jf[g], jl = pc.jl[g], pre = pc.pre;
+                st.slope2 = a.s.slopes ? a.s.slopes[pc.kvh * G + rr % G] * 1.44269504f : 0.f;
+            const KeyRange cr{pc.ks0, pc.cpre, pc.lo, pc.hi};
             bool any = false;
-            for (int j = jf; j <= jl; j += ALT ? 2 : 1) {
-                const int tau = tau0 + j;
-                wait_or_flag(&s_full[g], (uint32_t)(ns & 1), dead, a.err);
+            int j = set - tau0 % kSets;
+            if (j < 0) j += kSets;
+            for (; j < n; j += kSets) {
+                const int tau = tau0 + j, turn = tau / kSets;
+                wait_or_flag(&s_full[set], (uint32_t)(turn & 1), dead, a.err);
                 if (dead) break;
                 tc::fence_after();
                 const TileRec rec = recs[tau % kRecs];
-                const int t0 = rec.t0;
-                const uint32_t bad = rec.bad;
-                if (j == jl) next_q();  // every Q K^T on this Q has completed (ALT: the group of the piece's last tile copies)
+                // the tile before's barriers have come round as often as this one's, one time less for the first set
+                const int bturn = set == 0 ? turn - 1 : turn;
+                Chain ch;
+                ch.mref = mref + rr;
+                ch.before = tau > 0 ? &m_full[prev * 4 + wq] : nullptr;
+                ch.mine = &m_full[set * 4 + wq];
+                ch.done = &o_done[prev];
+                ch.parity = (uint32_t)(bturn & 1);
+                ch.first = j == 0;
+                if (live_warp) {
+                    softmax_tile<D, KIND>(sp, op, rec, a, rec.t0 < pre, st, ch, lane, dead);
+                } else if (KIND != kCap) {
+                    if (ch.before) wait_or_flag(ch.before, ch.parity, dead, a.err);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(ch.mine);
+                }
                 // V rows of keys that no row sees hold stale values, or none were loaded: zero weights must meet zeros
                 if (!rec.whole) {
-                    wait_or_flag(&v_full[tau % NV], (uint32_t)((tau / NV) & 1), dead, a.err);
-                    const KeyRange r{pc.ks0, pc.cpre, pc.lo, pc.hi};
-                    const uint32_t vb = v_s + (uint32_t)(tau % NV) * L::kTile;
-                    for (int e = hf * kRows + rr; e < kTok * H * 8; e += 2 * kRows) {
-                        const int key = (e >> 3) % kTok, h = e / (kTok * 8), chk = e & 7;
-                        if (r.sees(t0 + key) && !((bad >> (key >> a.bshift)) & 1u)) continue;
-                        const uint32_t row = vb + (key >> a.bshift) * (H * 128 << a.bshift) + h * (128 << a.bshift) +
-                                             (key & (B - 1)) * 128;
-                        asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(row + chk * 16), "r"(0u) : "memory");
+                    const int st_v = tau % NV;
+                    wait_or_flag(&v_full[st_v], (uint32_t)((tau / NV) & 1), dead, a.err);
+                    if (!cr.sees(rec.t0 + rr) || ((rec.bad >> (rr >> a.bshift)) & 1u)) {  // a thread per key
+                        const uint32_t row = v_s + (uint32_t)st_v * L::kTile + (rr >> a.bshift) * (H * 128 << a.bshift) +
+                                             (rr & (B - 1)) * 128;
+                        for (int i = 0; i < 8 * H; ++i)
+                            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(row + (i >> 3) * (128 << a.bshift) +
+                                                                                       ((i + lane) & 7) * 16),
+                                         "r"(0u)
+                                         : "memory");
                     }
                     fence_proxy_async();
                 }
-                bool move = false;
-                float alpha = 1.f;
-                if (live_warp) {
-                    softmax_half<KIND>(sp, t0 + hf * kHalf, bad >> (hf * (kHalf >> a.bshift)), a, t0 < pre, st, move, alpha, [&](float mt) {
-                                           slot(ns, hf) = mt;
-                                           meet_barrier();
-                                           return fmaxf(mt, slot(ns, hf ^ 1));
-                                       });
-                }
-                if (__any_sync(0xffffffffu, move)) {  // in both halves' warps alike: each takes half of the columns
-                    const uint32_t ob = trow + kOBase + (uint32_t)(g * D + hf * (D / 2));
-#pragma unroll 1
-                    for (int c = 0; c < D / 64; ++c) {
-                        float o[32];
-                        tc::ld32(ob + c * 32, o);
-                        tc::wait_ld();
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] *= alpha;
-                        tc::st32(ob + c * 32, o);
-                    }
-                    tc::wait_st();
-                }
                 any = true;
-                ++ns;
                 tc::fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[g]);
-                if (copied) {  // after this tile's weights: Q for the next piece
-                    q_done();
-                    copied = false;
-                }
+                if (lane == 0) mbar_arrive(&p_full[set]);
             }
             if (dead) break;
             tau0 += n;
-            // ---- the piece's result: the sums of a row's halves (ALT: and groups) meet, each thread writes its columns ----
-            const int64_t orow = (qrow * a.num_heads + pc.kvh * G + cr % G) * D;
-            if (ALT || has_rows<ALT>(pc, g)) {
-                wait_or_flag(&o_last[g], (uint32_t)(npl & 1), dead, a.err);
-                if (ALT) wait_or_flag(&o_last[g ^ 1], (uint32_t)(npl & 1), dead, a.err);
-                tc::fence_after();
-                // overwritten only after the next piece's products, which wait for all these reads (o_free)
-                if (!any) st.m = -INFINITY;  // O holds nothing
-                fin_ml[(g * 2 + hf) * kRows + rr] = make_float2(st.m, st.l);
-                if constexpr (ALT) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&xch_full[g]);
-                    wait_or_flag(&xch_full[0], (uint32_t)(npl & 1), dead, a.err);
-                    wait_or_flag(&xch_full[1], (uint32_t)(npl & 1), dead, a.err);
-                } else {
-                    meet_barrier();
-                }
-                ++npl;
-                if (dead) break;
-                const float l_own = st.l + fin_ml[(g * 2 + (hf ^ 1)) * kRows + rr].y;
-                float M = st.m, Ls = l_own, wm = 1.f, wo = 0.f;
-                if constexpr (ALT) {
-                    const float2 x0 = fin_ml[((g ^ 1) * 2) * kRows + rr], x1 = fin_ml[((g ^ 1) * 2 + 1) * kRows + rr];
-                    M = fmaxf(st.m, x0.x);
-                    wm = st.m == -INFINITY ? 0.f : ex2_approx(st.m - M);
-                    wo = x0.x == -INFINITY ? 0.f : ex2_approx(x0.x - M);
-                    Ls = l_own * wm + (x0.y + x1.y) * wo;
-                } else if (st.m == -INFINITY) {
-                    wm = 0.f;
-                }
-                const float inv = Ls != 0.f ? 1.f / Ls : 0.f;
-                if (live_warp) {
-                    constexpr int kCols = ALT ? D / 4 : D / 2;
-                    const int col0 = (ALT ? g * 2 + hf : hf) * kCols;
-#pragma unroll 1
-                    for (int c = col0; c < col0 + kCols; c += 16) {
-                        float o[16], x[16];
-                        ld16(trow + kOBase + (uint32_t)(g * D + c), o);
-                        if (ALT) ld16(trow + kOBase + (uint32_t)((g ^ 1) * D + c), x);
-                        tc::wait_ld();
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {  // a state without keys may hold anything
-                            o[k] = wm != 0.f ? o[k] * wm : 0.f;
-                            if (ALT && wo != 0.f) o[k] = fmaf(x[k], wo, o[k]);
-                        }
-                        if (!live) continue;
-                        if (pc.slot < 0) {
-                            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow + c);
-#pragma unroll
-                            for (int k = 0; k < 2; ++k)
-                                dst[k] = make_uint4(pack_bf16x2(o[8 * k] * inv, o[8 * k + 1] * inv),
-                                                    pack_bf16x2(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
-                                                    pack_bf16x2(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
-                                                    pack_bf16x2(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
-                        } else {
-                            float *dst = a.part_o + ((int64_t)pc.slot * D + c) * (2 * kRows) + cr;
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) dst[k * (2 * kRows)] = o[k];
-                        }
-                    }
-                    if (live && pc.slot >= 0 && hf == 0 && (!ALT || g == 0))
-                        reinterpret_cast<float2 *>(a.part_ml)[(int64_t)pc.slot * (2 * kRows) + cr] = make_float2(M, Ls);
-                }
-                tc::fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&o_free[g]);
-                    if (ALT) mbar_arrive(&o_free[g ^ 1]);
-                }
-            }
-            // No tile of this group in the piece: its Q was never read.  The next one is announced only now, after the MMA
-            // thread has passed this piece's announcement (o_last), or there was none.
-            if (!ALT && jl < jf) {
-                next_q();
-                if (copied) q_done();
-            }
+            // the piece's reference and sum of this set's tiles, for the epilogue
+            const int f = p & 1;
+            if (p >= 2) wait_or_flag(&fin_empty[f], (uint32_t)((p / 2 - 1) & 1), dead, a.err);
+            fin_ml[(f * kSets + set) * kRows + rr] = make_float2(any ? st.m : -INFINITY, st.l);
             __syncwarp();
-            if (lane == 0) mbar_arrive(&desc_empty[d]);
+            if (lane == 0) {
+                mbar_arrive(&fin_full[f]);
+                mbar_arrive(&desc_empty[d]);
+            }
+        }
+    } else if (warp < kEpiWarp + 4) {
+        // ======================= epilogue =======================
+        const int wq = warp & 3, rr = wq * 32 + lane;
+        const uint32_t op = tmem + ((uint32_t)(wq * 32) << 16) + kOBase;
+        for (int p = 0; !dead; ++p) {
+            const int d = p % kDescs, f = p & 1;
+            if (!wait_or_flag(&desc_full[d], (uint32_t)((p / kDescs) & 1), dead, a.err)) break;
+            const Piece &pc = descs[d];
+            if (pc.ntiles == 0) break;
+            const int nrows = pc.nrows, slot = pc.slot;
+            const int64_t orow = (((int64_t)pc.row0 + rr / G) * a.num_heads + pc.kvh * G + rr % G) * D;
+            wait_or_flag(&fin_full[f], (uint32_t)((p >> 1) & 1), dead, a.err);
+            float2 x[kSets];
+#pragma unroll
+            for (int i = 0; i < kSets; ++i) x[i] = fin_ml[(f * kSets + i) * kRows + rr];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&fin_empty[f]);
+            float M = x[0].x, l = 0.f;
+#pragma unroll
+            for (int i = 1; i < kSets; ++i) M = fmaxf(M, x[i].x);
+#pragma unroll
+            for (int i = 0; i < kSets; ++i)  // (a set without a tile: l = 0)
+                l += x[i].x == -INFINITY || x[i].x == M ? x[i].y : x[i].y * ex2_approx(x[i].x - M);
+            const float inv = l != 0.f ? 1.f / l : 0.f;
+            wait_or_flag(o_last, (uint32_t)(p & 1), dead, a.err);
+            if (dead) break;
+            tc::fence_after();
+            const bool live = rr < nrows;
+            if (wq * 32 < nrows) {
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16) {
+                    float o[16];
+                    ld16(op + (uint32_t)c, o);
+                    tc::wait_ld();
+                    if (!live) continue;
+                    if (slot < 0) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow + c);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            dst[k] = make_uint4(pack_bf16x2(o[8 * k] * inv, o[8 * k + 1] * inv),
+                                                pack_bf16x2(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
+                                                pack_bf16x2(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
+                                                pack_bf16x2(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+                    } else {
+                        float *dst = a.part_o + ((int64_t)slot * D + c) * kRows + rr;
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) dst[k * kRows] = o[k];
+                    }
+                }
+                if (live && slot >= 0)
+                    reinterpret_cast<float2 *>(a.part_ml)[(int64_t)slot * kRows + rr] = make_float2(M, l);
+            }
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(o_free);
+                mbar_arrive(&desc_empty[d]);
+            }
         }
     }
     tc::fence_before();
@@ -1097,7 +1028,7 @@ template <int D>
 __global__ void __launch_bounds__(128) scored_rows_merge_kernel(const __grid_constant__ RowsArgs a, int ctas) {
     grid_dependency_wait();
     grid_launch_dependents();
-    constexpr int kPer = 2 * kRows / kMergeRows;
+    constexpr int kPer = kRows / kMergeRows;
     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out);
     if ((int)blockIdx.x >= ctas * kPer) {
         const int s = blockIdx.x - ctas * kPer;
@@ -1120,17 +1051,17 @@ __global__ void __launch_bounds__(128) scored_rows_merge_kernel(const __grid_con
     auto slot = [&](int j) { return (int64_t)(j == 0 ? 2 * c + 1 : 2 * (c + j)); };
     const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml);
     float M = -INFINITY;
-    for (int j = 0; j < m.x; ++j) M = fmaxf(M, ml[slot(j) * (2 * kRows) + cr].x);
+    for (int j = 0; j < m.x; ++j) M = fmaxf(M, ml[slot(j) * kRows + cr].x);
     float L = 0.f, o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.f;
     for (int j = 0; j < m.x; ++j) {
-        const float2 x = ml[slot(j) * (2 * kRows) + cr];
+        const float2 x = ml[slot(j) * kRows + cr];
         const float w = x.x == -INFINITY ? 0.f : ex2_approx(x.x - M);
         L += x.y * w;
-        const float *src = a.part_o + (slot(j) * D + col) * (2 * kRows) + cr;
+        const float *src = a.part_o + (slot(j) * D + col) * kRows + cr;
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] += w * src[(int64_t)e * (2 * kRows)];
+        for (int e = 0; e < E; ++e) o[e] += w * src[e * kRows];
     }
     const float inv = L != 0.f ? 1.f / L : 0.f;
     uint4 *dst = reinterpret_cast<uint4 *>(out + ((int64_t)(m.y + cr / a.group) * a.num_heads + m.w * a.group + cr % a.group) * D + col);
@@ -1145,37 +1076,51 @@ struct WsLayout {
     size_t o, ml, merges, total;
     explicit WsLayout(int D) {
         o = 0;
-        ml = round256((size_t)2 * kMaxCtas * D * 2 * kRows * 4);
-        merges = ml + round256((size_t)2 * kMaxCtas * 2 * kRows * 8);
+        ml = round256((size_t)2 * kMaxCtas * D * kRows * 4);
+        merges = ml + round256((size_t)2 * kMaxCtas * kRows * 8);
         total = merges + round256((size_t)kMaxCtas * 16);
     }
 };
 
-template <int D, int KIND, bool ALT>
+// The queries of G heads of per_ctx tokens as one box per column half: dims (head_dim, heads, tokens), a row per (token, head).
+bool make_query_map(CUtensorMap *map, const RowsArgs &a, int D) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.num_heads, (cuuint64_t)a.num_q};
+    cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)a.num_heads * D * 2};
+    cuuint32_t box[3] = {64u, (cuuint32_t)a.group, (cuuint32_t)a.per_ctx};
+    cuuint32_t estr[3] = {1u, 1u, 1u};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(a.q), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int KIND>
 pkv_status launch(const RowsArgs &a, cudaStream_t st) {
-    constexpr int smem = Layout<D, ALT>::total;
+    constexpr int smem = Layout<D>::total;
     static bool done[128] = {};
-    auto kern = scored_rows_kernel<D, KIND, ALT>;
+    auto kern = scored_rows_kernel<D, KIND>;
     if (!ensure_smem(kern, smem, done)) return PKV_ERR_CUDA;
-    CUtensorMap mk, mv;
+    CUtensorMap mq, mk, mv;
     const int64_t rows = (int64_t)a.num_blocks * a.num_kv_heads * a.block_size;
-    if (!make_cache_map(&mk, a.k_cache, rows, D, a.block_size) || !make_slab_map(&mv, a.v_cache, rows, D, a.block_size))
+    if (!make_query_map(&mq, a, D) || !make_cache_map(&mk, a.k_cache, rows, D, a.block_size) ||
+        !make_slab_map(&mv, a.v_cache, rows, D, a.block_size))
         return PKV_ERR_CUDA;
     const int ctas = std::min(sm_count(), kMaxCtas);
     if (ctas < 1) return PKV_ERR_CUDA;
-    pkv_status rc = launch_pdl(kern, dim3((unsigned)ctas), dim3(kThreads), smem, st, mk, mv, a);
+    pkv_status rc = launch_pdl(kern, dim3((unsigned)ctas), dim3(kThreads), smem, st, mq, mk, mv, a);
     if (rc == PKV_OK)
-        rc = launch_pdl(scored_rows_merge_kernel<D>, dim3((unsigned)(ctas * (2 * kRows / kMergeRows) + a.num_seqs)), dim3(128),
-                        0, st, a, ctas);
+        rc = launch_pdl(scored_rows_merge_kernel<D>, dim3((unsigned)(ctas * (kRows / kMergeRows) + a.num_seqs)), dim3(128), 0, st,
+                        a, ctas);
     return rc;
 }
 
-template <int D, bool ALT>
+template <int D>
 pkv_status launch_kind(const RowsArgs &a, cudaStream_t st) {
     // a plain score's maximum is found before the scaling, which needs a positive scale
     const bool bias = a.s.slopes != nullptr;
-    if (a.s.softcap > 0.f) return bias || a.c2 > kMaxC2 ? launch<D, kCapBias, ALT>(a, st) : launch<D, kCap, ALT>(a, st);
-    return bias || !(a.s.scale > 0.f) ? launch<D, kBias, ALT>(a, st) : launch<D, kPlain, ALT>(a, st);
+    if (a.s.softcap > 0.f) return bias || a.c2 > kMaxC2 ? launch<D, kCapBias>(a, st) : launch<D, kCap>(a, st);
+    return bias || !(a.s.scale > 0.f) ? launch<D, kBias>(a, st) : launch<D, kPlain>(a, st);
 }
 
 }  // namespace
@@ -1187,9 +1132,7 @@ pkv_status run_rows(const Args &args, int head_dim, void *workspace, size_t work
     if (!workspace || workspace_bytes < lay.total || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return PKV_ERR_INVALID;
     RowsArgs a{};
     static_cast<Args &>(a) = args;
-    // the alternating form where no sequence has more rows than one group
-    const bool alt = (int64_t)a.max_q_len * a.group <= kRows;
-    a.per_ctx = (alt ? kRows : 2 * kRows) / a.group;
+    a.per_ctx = kRows / a.group;
     a.bshift = a.block_size == 8 ? 3 : a.block_size == 16 ? 4 : 5;
     const int64_t blocks = ((int64_t)a.max_q_len + a.per_ctx - 1) / a.per_ctx;
     a.scan_w = 1;
@@ -1210,8 +1153,7 @@ pkv_status run_rows(const Args &args, int head_dim, void *workspace, size_t work
     a.part_o = reinterpret_cast<float *>(ws + lay.o);
     a.part_ml = reinterpret_cast<float *>(ws + lay.ml);
     a.merges = reinterpret_cast<int4 *>(ws + lay.merges);
-    if (head_dim == 128) return alt ? launch_kind<128, true>(a, st) : launch_kind<128, false>(a, st);
-    return alt ? launch_kind<64, true>(a, st) : launch_kind<64, false>(a, st);
+    return head_dim == 128 ? launch_kind<128>(a, st) : launch_kind<64>(a, st);
 }
 
 }  // namespace scored
