@@ -6,8 +6,9 @@
 //     S = Q K^T (M 128 rows, N 128 keys, K head_dim)      scores, in tensor memory
 //     P = 2^(y(S) - m)                                     y: the score in base 2, capped and biased
 //     O += P V  (M 128, N head_dim, K 128 keys)
-// with a running reference m and sum l per row; m moves (and O is rescaled)
-// only when a tile's maximum passes it by more than 2^8.
+// with a reference m and a sum l per row.  m is the first 16 keys' maximum, rounded
+// up to an integer, and moves only where a score passes it by more than kJump: what
+// was summed is then scaled by a power of two, which rounds nothing.
 //
 // A context is one such set of rows and the tiles that some row sees: those of
 // the always visible prefix, then those from the first row's window or document
@@ -17,17 +18,22 @@
 // states (o, m, l) in the workspace, which a second kernel merges; no CTA waits
 // for another.
 //
-// What bounds it is the softmax step between the two products (special-function,
-// FMA and issue slots, and its latency), so three tiles are in flight per SM:
-// three S buffers, three sets of four warps (a thread per row = TMEM lane), tile
-// t with set t % 3, one O.  Two chains of 128 x 128 tiles with an O each left the
-// tensor cores idle between them (8 x 512 queries of 4096: 311 us).
+// What bounds it is the softmax step between the two products (issue slots, the FMA
+// pipe, instruction fetches and latency), so three tiles are in flight per SM: three
+// S buffers, three sets of four warps (a thread per row = TMEM lane), tile t with set
+// t % 3, one O.  Two chains of 128 x 128 tiles with an O each left the tensor cores
+// idle between them (8 x 512 queries of 4096: 311 us; this form 255 to 270 us, with
+// the tensor pipe 49 % and the issue slots 54 % busy, at the board's power limit in a
+// long run).  What costs most is code size: the loops of a tile's 16-key blocks are
+// rolled and their rare parts loops of their own; unrolled by two they took 6 to 13 %
+// longer.
 //
 // Warps: 0-11 the softmax sets, 12-15 the epilogue (reads O at a context's end
-// while the sets go on), 16 the MMA issuer, 17 / 18 the producers of K (a column
-// half each) and 19 of V (one TMA box per block: one warp starts a box in some 60
-// cycles), 20 the scheduler, which walks the share, publishes one descriptor per
-// piece of a context and loads its queries (one box per column half).
+// while the sets go on), 16 the issuer of Q K^T and 21 that of P V (one warp for
+// both products was the bottleneck: 317 us, with two 283), 17 / 18 the producers of
+// K (a column half each) and 19 of V (one TMA box per block), 20 the scheduler,
+// which walks the share, publishes one descriptor per piece of a context and loads
+// its queries (one box per column half).
 // Tensor memory: S at columns 128 (t % 3) (P overwrites its first half as bf16
 // pairs), O at 384.
 // Every wait is bounded; one that gives up flags PKV_DEVERR_TIMEOUT.
@@ -49,12 +55,9 @@ constexpr int kEpiWarp = 4 * kSets, kMmaWarp = 16, kKWarp = 17, kVWarp = 19, kSc
 constexpr int kThreads = 22 * 32;
 constexpr int kDescs = 6;   // piece descriptors in flight
 constexpr int kRecs = 8;    // tile records (more than the K producers can be ahead of the softmax)
-#ifndef CHARGE
-#define CHARGE 2
-#endif
-constexpr int kCharge = CHARGE;  // virtual tiles of a context
+constexpr int kCharge = 2;  // virtual tiles of a context
 constexpr int kMinShare = kCharge + 1;
-constexpr float kRescale = 8.f;
+constexpr float kJump = 32.f;  // a row's reference moves where a score passes it by more (weights stay below 2^kJump)
 constexpr float kMaxC2 = 73.f;  // softcap * log2 e up to which capped scores take a fixed reference (cap 50)
 constexpr uint32_t kTmemCols = 512, kOBase = kSets * kTok;
 constexpr int kMaxCtas = 160;   // partial slots in the workspace: two per CTA
@@ -66,7 +69,7 @@ struct RowsArgs : Args {
     float k1;       // plain, biased: scale * log2 e; capped: scale / softcap
     float c2;       // capped: softcap * log2 e
     float m0;       // capped: the reference
-    float near[4], far[6];  // capped: c2 tanh(k1 s) = s * sum near[i] s^2i for |k1 s| <= kTanhNear (far: kTanhFar)
+    float near[4];  // capped: c2 tanh(k1 s) = s * sum near[i] s^2i for |k1 s| <= kTanhNear
     float *part_o;  // [2 kMaxCtas][D][kRows]: columns of rows
     float *part_ml; // [2 kMaxCtas][kRows][2]
     int4 *merges;   // [kMaxCtas]: (parts, first query row, rows, kv head) of the context begun and cut in that share
@@ -77,7 +80,7 @@ struct Piece {
     int ntiles;  // 0: no more
     int i0;      // first tile within the context
     int np, pt0, mt0;   // context tile i is key tile pt0 + i (i < np) or mt0 + i - np
-    int seq, kvh, row0, nrows, pos0, pre;
+    int seq, kvh, row0, nq, nrows, pos0, pre;
     int ks0, cpre, lo, hi;  // the context's keys: [ks0, cpre) and [lo, hi) (KeyRange)
     int fks, flo, fhi;      // keys that every row sees: [flo, fhi) and [fks, pre)
     int slot;               // partial slot, -1: the whole context
@@ -103,7 +106,8 @@ struct Layout {
     static constexpr int vring = kring + NK * kTile;
     static constexpr int fin_ml = vring + NV * kTile;   // float2 [2][kSets][kRows]: (m, l) of a piece's rows, pieces in turn
     static constexpr int mref = fin_ml + 2 * kSets * kRows * 8;  // float [kRows]: the rows' reference after the latest tile
-    static constexpr int desc = mref + kRows * 4;
+    static constexpr int hint = mref + kRows * 4;  // uint64_t [kRows]
+    static constexpr int desc = hint + kRows * 8;
     static constexpr int recs = (desc + kDescs * (int)sizeof(Piece) + 15) & ~15;
     static constexpr int bars = recs + kRecs * (int)sizeof(TileRec);
     static constexpr int kBars = 2 * NK + 2 * NV + 3 * kSets + 4 * kSets + 4 + 2 + 4 + 2 * kDescs + 2;
@@ -117,6 +121,8 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
     return p != 0u;
 }
+
+__device__ __forceinline__ void prefetch_l1(const void *p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
 
 __device__ __forceinline__ bool wait_or_flag(uint64_t *bar, uint32_t parity, bool &dead, unsigned int *err) {
     if (dead) return false;
@@ -214,12 +220,26 @@ __device__ __forceinline__ void st8u(uint32_t taddr, const uint32_t (&v)[8]) {
                  : "memory");
 }
 
-// tanh z / z as polynomials in z^2: least squares of the error of tanh, reweighted towards its largest (Lawson's method),
-// in 64 bits.  |z| <= 0.75: off by at most 3.7e-6; |z| <= 1.25: 2.4e-6 -- of the cap, so 2e-4 of a score at a cap of 50,
-// where the weight's rounding to bf16 is worth 2e-3 to 4e-3.
-constexpr float kTanhNear = 0.75f, kTanhFar = 1.25f;
+__device__ __forceinline__ void ld4(uint32_t taddr, float (&v)[4]) {
+    uint32_t r[4];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void st4(uint32_t taddr, const float (&v)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(__float_as_uint(v[0])),
+                 "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3]))
+                 : "memory");
+}
+
+// tanh z / z as a polynomial in z^2: least squares of the error of tanh, reweighted towards its largest (Lawson's method),
+// in 64 bits.  |z| <= 0.75: off by at most 3.7e-6 of the cap, so 2e-4 of a score at a cap of 50, where the weight's
+// rounding to bf16 is worth 2e-3 to 4e-3.
+constexpr float kTanhNear = 0.75f;
 constexpr double kTanh3[4] = {0.9999556008, -0.3322276376, 0.1257709249, -0.03377828486};
-constexpr double kTanh5[6] = {0.9999746925, -0.3328393216, 0.1305362538, -0.04692675917, 0.01253202075, -0.001682072195};
 
 __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
     uint64_t d;
@@ -227,13 +247,13 @@ __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
     return d;
 }
 
-// bits [a, b) of a 32-bit word, a and b taken from any integers
-__device__ __forceinline__ uint32_t bit_range(int a, int b) {
-    a = max(a, 0);
-    b = min(b, 32);
-    if (a >= b) return 0u;
-    return (b == 32 ? 0xffffffffu : (1u << b) - 1u) & ~((1u << a) - 1u);
+// bits [a, b) of a 32-bit word, a and b taken from any integers (shl gives 0 from 32 on)
+__device__ __forceinline__ uint32_t bits_from(int a) {
+    uint32_t m;
+    asm("shl.b32 %0, %1, %2;" : "=r"(m) : "r"(0xffffffffu), "r"(max(a, 0)));
+    return m;
 }
+__device__ __forceinline__ uint32_t bit_range(int a, int b) { return bits_from(a) & ~bits_from(b); }
 
 struct RowState {
     float m, l;    // reference and sum
@@ -257,73 +277,108 @@ __device__ __forceinline__ float max_of(const float (&s)[N]) {
     return fmaxf(fmax3(m[0], m[1], m[2]), m[3]);
 }
 
-// The 32 keys from t on that the row sees, as bits.
-__device__ __forceinline__ uint32_t seen32(const KeyRange &r, int t, uint32_t bad, int bshift, int word) {
-    uint32_t m = bit_range(r.lo - t, r.hi - t) | bit_range(r.first - t, r.pre - t);
+// The keys of block c (16 keys) of the tile at t0 that the row sees, as bits.
+__device__ __forceinline__ uint32_t seen16(const KeyRange &r, int t0, uint32_t bad, int bshift, int c) {
+    const int t = t0 + 16 * c;
+    uint32_t w = bit_range(r.lo - t, r.hi - t);
+    if (r.pre > t) w |= bit_range(r.first - t, r.pre - t);
     if (bad) {
-        const int per = 32 >> bshift;  // blocks of the word
-        for (int b = 0; b < per; ++b)
-            if ((bad >> (word * per + b)) & 1u) m &= ~bit_range(b << bshift, (b + 1) << bshift);
+        if ((bad >> (16 * c >> bshift)) & 1u) w &= ~0xffu;
+        if ((bad >> ((16 * c + 8) >> bshift)) & 1u) w &= ~0xff00u;
     }
-    return m;
+    return w & 0xffffu;
 }
 
-// Raw products -> scores in base 2 plus nm: c tanh(z) + nm, z = k1 s.  For |z| small in the whole warp an odd polynomial
-// (the cap's factors folded in on the host) on the FMA pipe, two keys an instruction: the exponential is then the only
-// special function of a score.  The FMA pipe is what bounds capped scores, hence the shortest polynomial for the usual
-// sizes.  cap_near computes that one whatever the sizes and cap_far does the rest again where cap_near does not hold.
-template <int N>
-__device__ __forceinline__ void cap_near(float (&s)[N], const RowsArgs &a, uint64_t nm2) {
+__device__ __forceinline__ void mask16(float (&s)[16], uint32_t w) {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) s[k] = (w >> k) & 1u ? s[k] : -INFINITY;
+}
+
+__device__ __forceinline__ void no_weights16(uint32_t to) {
+    const uint32_t z[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+    st8u(to, z);
+}
+
+// Raw products of 16 keys (at sp) -> scores in base 2 plus nm: c tanh(z) + nm, z = k1 s.  For |z| small in the whole warp
+// an odd polynomial (the cap's factors folded in on the host) on the FMA pipe, two keys an instruction: the exponential is
+// then the only special function of a score.  Else, in a loop to keep the code short,
+// tanh z = 1 - 2 / (1 + e^2z), good to 2^-21; the scores go back over S.
+__device__ __forceinline__ void cap_near(float (&s)[16], const RowsArgs &a, uint64_t nm2) {
     const uint64_t q0 = f32x2(a.near[0], a.near[0]), q1 = f32x2(a.near[1], a.near[1]);
     const uint64_t q2 = f32x2(a.near[2], a.near[2]), q3 = f32x2(a.near[3], a.near[3]);
 #pragma unroll
-    for (int k = 0; k < N; k += 2) {
+    for (int k = 0; k < 16; k += 2) {
         const uint64_t x = f32x2(s[k], s[k + 1]), u = mul_f32x2(x, x);
         const uint64_t y = fma_f32x2(fma_f32x2(fma_f32x2(q3, u, q2), u, q1), u, q0);
         f32x2_split(fma_f32x2(x, y, nm2), s[k], s[k + 1]);
     }
 }
 
-template <int N>
-__device__ __forceinline__ void cap_far(float (&s)[N], const RowsArgs &a, float nm, float top) {
-    if (!__any_sync(0xffffffffu, top > kTanhFar)) {
-        const uint64_t nm2 = f32x2(nm, nm);
+__device__ __forceinline__ void cap_far(float (&s)[16], uint32_t sp, const RowsArgs &a, float nm) {
+    const float z2 = 2.f * 1.44269504f * a.k1;
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+        float x[4];
+        ld4(sp + 4 * i, x);
+        tc::wait_ld();
 #pragma unroll
-        for (int k = 0; k < N; k += 2) {
-            const uint64_t x = f32x2(s[k], s[k + 1]), u = mul_f32x2(x, x);
-            uint64_t y = f32x2(a.far[5], a.far[5]);
-#pragma unroll
-            for (int i = 4; i >= 0; --i) y = fma_f32x2(y, u, f32x2(a.far[i], a.far[i]));
-            f32x2_split(fma_f32x2(x, y, nm2), s[k], s[k + 1]);
-        }
-    } else {
-        // tanh z = 1 - 2 / (1 + e^2z), good to 2^-21
-        const float z2 = 2.f * 1.44269504f * a.k1;
-#pragma unroll
-        for (int k = 0; k < N; ++k) s[k] = (a.c2 + nm) - (2.f * a.c2) * rcp_approx(1.f + ex2_approx(s[k] * z2));
+        for (int k = 0; k < 4; ++k) x[k] = (a.c2 + nm) - (2.f * a.c2) * rcp_approx(1.f + ex2_approx(x[k] * z2));
+        st4(sp + 4 * i, x);
     }
+    tc::wait_st();
+    ld16(sp, s);
+    tc::wait_ld();
 }
 
-__device__ __forceinline__ void cap32(float (&s)[32], const RowsArgs &a) {
-    const float top = max_of<true>(s) * fabsf(a.k1);
-    if (!__any_sync(0xffffffffu, top > kTanhNear)) cap_near(s, a, 0ull);
-    else cap_far(s, a, 0.f, top);
-}
-
-// Capped: the weights of 16 keys of S at sp (loaded in s) to P at `to`, their sum to ls; w: the keys that are seen.
-__device__ __forceinline__ void cap_weights16(float (&s)[16], uint32_t sp, uint32_t to, const RowsArgs &a, float nm, uint64_t nm2,
-                                              bool full, uint32_t w, uint64_t (&ls)[2]) {
+__device__ __forceinline__ void cap16(float (&s)[16], uint32_t sp, const RowsArgs &a, float nm, uint64_t nm2) {
     const float top = max_of<true>(s) * fabsf(a.k1);
     cap_near(s, a, nm2);
-    if (__any_sync(0xffffffffu, top > kTanhNear)) {
-        ld16(sp, s);
-        tc::wait_ld();
-        cap_far(s, a, nm, top);
-    }
-    if (!full) {
+    if (__builtin_expect(__any_sync(0xffffffffu, top > kTanhNear), 0)) cap_far(s, sp, a, nm);
+}
+
+// Raw products of 16 keys at sp, the first `ahead` keys before the row's position -> scores in base 2 plus nm.  beyond: keys
+// past the position may be seen.
+template <int KIND>
+__device__ __forceinline__ void scores16(float (&s)[16], uint32_t sp, int ahead, float slope2, bool beyond, const RowsArgs &a, float nm) {
+    ld16(sp, s);
+    tc::wait_ld();
+    if constexpr (KIND == kCapBias) cap16(s, sp, a, 0.f, 0ull);
+    const float f = KIND == kCapBias ? 1.f : a.k1;
+    const uint64_t f2 = f32x2(f, f), nm2 = f32x2(nm, nm);
+    if constexpr (KIND == kPlain) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) s[k] = (w >> k) & 1u ? s[k] : -INFINITY;
+        for (int k = 0; k < 16; k += 2) f32x2_split(fma_f32x2(f32x2(s[k], s[k + 1]), f2, nm2), s[k], s[k + 1]);
+    } else {
+        // -slope |ahead - k|, linear unless the position is inside: one FMA for the pair's bias, one for the score
+        const float sl = beyond && ahead < 0 ? -slope2 : slope2, b = fmaf(-sl, (float)ahead, nm);
+        if (__builtin_expect(beyond && __any_sync(0xffffffffu, ahead > 0 && ahead < 15), 0)) {
+            if (KIND == kCapBias) {  // capped scores over S
+                st16u(sp, reinterpret_cast<const uint32_t(&)[16]>(s));
+                tc::wait_st();
+            }
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+                float x[4];
+                ld4(sp + 4 * i, x);
+                tc::wait_ld();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) x[k] = fmaf(-slope2, fabsf((float)(ahead - 4 * i - k)), fmaf(x[k], f, nm));
+                st4(sp + 4 * i, x);
+            }
+            tc::wait_st();
+            ld16(sp, s);
+            tc::wait_ld();
+            return;
+        }
+        const uint64_t b2 = f32x2(b, b), sl2 = f32x2(sl, sl);
+#pragma unroll
+        for (int k = 0; k < 16; k += 2)
+            f32x2_split(fma_f32x2(f32x2(s[k], s[k + 1]), f2, fma_f32x2(sl2, f32x2((float)k, (float)(k + 1)), b2)), s[k], s[k + 1]);
     }
+}
+
+// Weights 2^s of 16 keys to P (bf16 pairs) at `to`, their sum to ls.
+__device__ __forceinline__ void weights16(const float (&s)[16], uint32_t to, uint64_t (&ls)[2]) {
     uint32_t pk[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -334,42 +389,57 @@ __device__ __forceinline__ void cap_weights16(float (&s)[16], uint32_t sp, uint3
     st8u(to, pk);
 }
 
-// Weights 2^(f s + nm) of 32 keys to P (bf16 pairs) at `to`, their sum to ls.
-__device__ __forceinline__ void weights32(const float (&s)[32], float f, float nm, uint32_t to, uint64_t (&ls)[2]) {
-    const uint64_t f2 = f32x2(f, f), nm2 = f32x2(nm, nm);
-    uint32_t pk[16];
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-        float a0, a1;
-        f32x2_split(fma_f32x2(f32x2(s[2 * k], s[2 * k + 1]), f2, nm2), a0, a1);
-        const float e0 = ex2_approx(a0), e1 = ex2_approx(a1);
-        pk[k] = pack_bf16x2(e0, e1);
-        ls[k & 1] = add_f32x2(ls[k & 1], f32x2(e0, e1));
-    }
-    st16u(to, pk);
-}
-
-// The rows' running reference over the tiles of a piece, handed from tile to tile.
+// The rows' reference over the tiles of a piece, handed from tile to tile.
 struct Chain {
-    float *mref;        // this row's
+    float *mref;        // this row's after the tile before
+    uint64_t *hint;     // (a reference of this row, the piece it belongs to): may be read while it is written
     uint64_t *before;   // the tile before has left its reference (nullptr: the CTA's first tile)
     uint64_t *mine;     // this tile has
     uint64_t *done;     // the tile before's product is complete
     uint32_t parity;    // of both
+    int piece;
     bool first;         // the piece's first tile
 };
 
-// One tile of one row, 32 keys at a time in loops that are not unrolled --
-// unrolled code of 128 keys ran at the pace of its instruction fetches (6 to 10
-// cycles an instruction).  S (raw products) at sp, P (bf16 pairs) back over its
-// first 64 columns, always behind the reads.  beyond: some row may see keys past
-// its position (a prefix).
+__device__ __forceinline__ void set_hint(const Chain &ch, float m) {
+    const uint64_t v = (uint64_t)(uint32_t)ch.piece << 32 | __float_as_uint(m);
+    asm volatile("st.relaxed.cta.shared.b64 [%0], %1;" ::"r"(smem_u32(ch.hint)), "l"(v) : "memory");
+}
+
+// The first 16 n weights at `to` times f, a power of two.
+__device__ __forceinline__ void rescale_weights(uint32_t to, int n, float f) {
+    tc::wait_st();
+#pragma unroll 1
+    for (int c = 0; c < 2 * n; ++c) {
+        float w[4];
+        ld4(to + 4 * c, w);
+        tc::wait_ld();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t u = __float_as_uint(w[k]);
+            w[k] = __uint_as_float(pack_bf16x2(__uint_as_float(u << 16) * f, __uint_as_float(u & 0xffff0000u) * f));
+        }
+        st4(to + 4 * c, w);
+    }
+}
+
+// One tile of one row, 16 keys at a time in loops that are not unrolled: the
+// warps of an SM sub-partition work at different places, and code of more than
+// some 2 KB a tile ran at the pace of its instruction fetches (6 to 10 cycles an
+// instruction).  S (raw products) at sp, P (bf16 pairs) back over its first 64
+// columns, always behind the reads.  beyond: some row may see keys past its
+// position (a prefix).  Blocks of 16 keys that no row of the warp sees are skipped.
 //
-// A first pass finds the maximum; scores that are biased or masked are written
-// back over S by it, in base 2 (plain ones stay raw: the exponential's FMA scales
-// them).  The reference then follows from the tile before's, and where it moves,
-// O (complete up to that tile) is rescaled before this tile's weights go out.
-// Capped scores without a bias need neither: they lie within +-c2, and up to
+// One pass: a score goes straight to its weight 2^(y - m), for the reference m that
+// the tiles before have left (or will, as far as is known when this one begins; the
+// piece's first tile takes the maximum of its first 16 seen keys).  Where a score
+// passes m by more than kJump, m moves to it, and the tile's earlier weights are
+// scaled.  At the end the tile before's final reference is awaited and the larger
+// of the two taken: this tile's weights or O (complete up to the tile before) are
+// rescaled where theirs was another.  Rounded up to integers, references seldom
+// differ, and scaling is exact.
+//
+// Capped scores without a bias need none of this: they lie within +-c2, and up to
 // kMaxC2 a fixed reference c2 / 4 keeps weights within 2^-(5/4 c2) .. 2^(3/4 c2)
 // (cap 50: 2^-90 .. 2^54), far from the ends of float32's and bf16's range for
 // sums over 2^20 keys of V entries between 2^-36 and 2^53.
@@ -379,95 +449,108 @@ __device__ __forceinline__ void softmax_tile(uint32_t sp, uint32_t op, const Til
     const int t0 = rec.t0;
     const bool full = rec.full != 0;
     uint64_t ls[2] = {0ull, 0ull};
+    float x[16];
     if constexpr (KIND == kCap) {
-        // 16 keys are loaded while 16 are worked on
         const float nm = -st.m;
         const uint64_t nm2 = f32x2(nm, nm);
-        float x0[16], x1[16];
-        ld16(sp, x0);
+        // (a loop for tiles that every row sees whole: the shorter, the faster)
+        if (full) {
 #pragma unroll 1
-        for (int c = 0; c < kTok; c += 32) {
-            const uint32_t w = full ? 0u : seen32(st.r, t0 + c, rec.bad, a.bshift, c / 32);
-            tc::wait_ld();
-            ld16(sp + c + 16, x1);
-            cap_weights16(x0, sp + c, sp + c / 2, a, nm, nm2, full, w, ls);
-            tc::wait_ld();
-            if (c + 32 < kTok) ld16(sp + c + 32, x0);
-            cap_weights16(x1, sp + c + 16, sp + c / 2 + 8, a, nm, nm2, full, w >> 16, ls);
+            for (int c = 0; c < kTok / 16; ++c) {
+                ld16(sp + 16 * c, x);
+                tc::wait_ld();
+                cap16(x, sp + 16 * c, a, nm, nm2);
+                weights16(x, sp + 8 * c, ls);
+            }
+        } else {
+#pragma unroll 1
+            for (int c = 0; c < kTok / 16; ++c) {
+                const uint32_t w = seen16(st.r, t0, rec.bad, a.bshift, c);
+                if (!__any_sync(0xffffffffu, w != 0u)) {
+                    no_weights16(sp + 8 * c);
+                    continue;
+                }
+                ld16(sp + 16 * c, x);
+                tc::wait_ld();
+                cap16(x, sp + 16 * c, a, nm, nm2);
+                if (__any_sync(0xffffffffu, w != 0xffffu)) mask16(x, w);
+                weights16(x, sp + 8 * c, ls);
+            }
         }
     } else {
-        const bool stored = KIND != kPlain || !full;
-        float mt = -INFINITY;
+        float m;
+        {
+            uint64_t h;
+            asm volatile("ld.relaxed.cta.shared.b64 %0, [%1];" : "=l"(h) : "r"(smem_u32(ch.hint)) : "memory");
+            m = (int)(h >> 32) == ch.piece ? __uint_as_float((uint32_t)h) : -INFINITY;
+        }
+        float nm = m == -INFINITY ? 0.f : -m, top = m == -INFINITY ? -INFINITY : kJump;
 #pragma unroll 1
-        for (int c = 0; c < kTok / 32; ++c) {
-            float s[32];
-            tc::ld32(sp + 32 * c, s);
-            tc::wait_ld();
-            const int t = t0 + 32 * c;
-            if constexpr (KIND == kCapBias) cap32(s, a);
-            if constexpr (KIND == kBias || KIND == kCapBias) {
-                const float f = KIND == kBias ? a.k1 : 1.f, d0 = (float)(st.p - t);
-                if (beyond) {
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) s[k] = fmaf(-st.slope2, fabsf(d0 - (float)k), s[k] * f);
-                } else {
-                    // -slope (p - t - k): one FMA for the pair's bias, one for the score
-                    const uint64_t f2 = f32x2(f, f), b0 = f32x2(-st.slope2 * d0, -st.slope2 * d0), sl = f32x2(st.slope2, st.slope2);
-#pragma unroll
-                    for (int k = 0; k < 32; k += 2)
-                        f32x2_split(fma_f32x2(f32x2(s[k], s[k + 1]), f2, fma_f32x2(sl, f32x2((float)k, (float)(k + 1)), b0)), s[k],
-                                    s[k + 1]);
+        for (int c = 0; c < kTok / 16; ++c) {
+            uint32_t w = 0xffffu;
+            if (!full) {
+                w = seen16(st.r, t0, rec.bad, a.bshift, c);
+                if (!__any_sync(0xffffffffu, w != 0u)) {
+                    no_weights16(sp + 8 * c);
+                    continue;
                 }
             }
-            if (!full) {
-                const uint32_t w = seen32(st.r, t, rec.bad, a.bshift, c);
+            scores16<KIND>(x, sp + 16 * c, st.p - t0 - 16 * c, st.slope2, beyond, a, nm);
+            if (!full) mask16(x, w);
+            const float mc = max_of<false>(x);
+            if (__builtin_expect(__any_sync(0xffffffffu, mc > top), 0)) {
+                const float up = mc > top ? ceilf(mc) : 0.f;  // relative to the reference so far
+                const float f = m == -INFINITY ? 1.f : ex2_approx(-up);  // (no weight so far but 0)
+                if (__any_sync(0xffffffffu, f != 1.f)) rescale_weights(sp, c, f);
+                ls[0] = mul_f32x2(ls[0], f32x2(f, f));
+                ls[1] = mul_f32x2(ls[1], f32x2(f, f));
 #pragma unroll
-                for (int k = 0; k < 32; ++k) s[k] = (w >> k) & 1u ? s[k] : -INFINITY;
+                for (int k = 0; k < 16; ++k) x[k] -= up;
+                if (mc > top) {
+                    m = up - nm;
+                    nm = -m;
+                    top = kJump;
+                    set_hint(ch, m);
+                }
             }
-            mt = fmaxf(mt, max_of<false>(s));
-            if (stored) tc::st32(sp + 32 * c, s);
+            weights16(x, sp + 8 * c, ls);
         }
-        if (stored) tc::wait_st();
-        if (KIND == kPlain) mt *= a.k1;
-        // the reference
+        // the tile before's reference
         if (ch.before) wait_or_flag(ch.before, ch.parity, dead, a.err);
-        const float old = ch.first ? -INFINITY : *ch.mref;
-        float m = old;
-        if (mt != -INFINITY && !(mt <= old + kRescale)) m = mt;  // also where nothing was seen before
-        *ch.mref = m;
+        const float old = ch.first ? -INFINITY : *ch.mref, mf = fmaxf(old, m);
+        *ch.mref = mf;
         __syncwarp();
         if (lane == 0) mbar_arrive(ch.mine);
-        if (st.m != m) {
-            st.l = st.m == -INFINITY ? st.l : st.l * ex2_approx(st.m - m);
-            st.m = m;
+        const float f = m == -INFINITY || m == mf ? 1.f : ex2_approx(m - mf);
+        if (__any_sync(0xffffffffu, f != 1.f)) {
+            set_hint(ch, mf);
+            rescale_weights(sp, kTok / 16, f);
+            ls[0] = mul_f32x2(ls[0], f32x2(f, f));
+            ls[1] = mul_f32x2(ls[1], f32x2(f, f));
         }
-        const bool move = old != -INFINITY && m != old;
+        if (st.m != mf) {
+            st.l = st.m == -INFINITY ? st.l : st.l * ex2_approx(st.m - mf);
+            st.m = mf;
+        }
+        const bool move = old != -INFINITY && mf != old;
         if (__any_sync(0xffffffffu, move)) {
             wait_or_flag(ch.done, ch.parity, dead, a.err);
             tc::fence_after();
-            const float alpha = move ? ex2_approx(old - m) : 1.f;
+            const float alpha = move ? ex2_approx(old - mf) : 1.f;
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-                float o[32];
-                tc::ld32(op + c * 32, o);
+            for (int c = 0; c < D / 16; ++c) {
+                float o[16];
+                ld16(op + c * 16, o);
                 tc::wait_ld();
 #pragma unroll
-                for (int k = 0; k < 32; ++k) o[k] *= alpha;
-                tc::st32(op + c * 32, o);
+                for (int k = 0; k < 16; ++k) o[k] *= alpha;
+                st16u(op + c * 16, reinterpret_cast<const uint32_t(&)[16]>(o));
             }
         }
-        const float nm = m == -INFINITY ? 0.f : -m, f = KIND == kPlain ? a.k1 : 1.f;
-#pragma unroll 1
-        for (int c = 0; c < kTok / 32; ++c) {
-            float s[32];
-            tc::ld32(sp + 32 * c, s);
-            tc::wait_ld();
-            weights32(s, f, nm, sp + 16 * c, ls);
-        }
     }
-    float x, y;
-    f32x2_split(add_f32x2(ls[0], ls[1]), x, y);
-    st.l += x + y;
+    float l0, l1;
+    f32x2_split(add_f32x2(ls[0], ls[1]), l0, l1);
+    st.l += l0 + l1;
     tc::wait_st();
 }
 
@@ -485,6 +568,7 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     TileRec *recs = reinterpret_cast<TileRec *>(smem + L::recs);
     float2 *fin_ml = reinterpret_cast<float2 *>(smem + L::fin_ml);
     float *mref = reinterpret_cast<float *>(smem + L::mref);
+    uint64_t *hint = reinterpret_cast<uint64_t *>(smem + L::hint);
     uint64_t *k_full = reinterpret_cast<uint64_t *>(smem + L::bars), *k_empty = k_full + NK;
     uint64_t *v_full = k_empty + NK, *v_empty = v_full + NV;
     uint64_t *s_full = v_empty + NV, *p_full = s_full + kSets, *o_done = p_full + kSets;  // per set
@@ -570,6 +654,7 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         scratch[kStart] = start;
     }
 
+    if (threadIdx.x < kRows) hint[threadIdx.x] = ~0ull;  // no piece's
     if (threadIdx.x == 0) {
         for (int i = 0; i < NK; ++i) {
             mbar_init(&k_full[i], H);
@@ -660,6 +745,7 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             const int q0 = (b0 + lane) * a.per_ctx;
                             pc.row0 = x.q0 + q0;
                             const int nq = min(x.Q - q0, a.per_ctx);
+                            pc.nq = nq;
                             pc.nrows = nq * G;
                             pc.pos0 = fp + q0;
                             pc.pre = x.pre;
@@ -678,6 +764,9 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                                                                  pc.nrows, kvh);
                             descs[d] = pc;
                             mbar_arrive(&desc_full[d]);
+                            // the rows' loads at the piece's start
+                            if (a.s.key_starts)
+                                for (int i = 0; i < nq; i += 32) prefetch_l1(a.s.key_starts + pc.row0 + i);
                             // its queries: per_ctx queries of the KV head's G heads, one box per column half
                             const int qb = p & 1;
                             if (p >= 2) wait_or_flag(&q_empty[qb], (uint32_t)((p / 2 - 1) & 1), dead, a.err);
@@ -806,7 +895,7 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 tc::fence_after();
                 const uint64_t kd = kd0 + (uint64_t)((uint32_t)st * (uint32_t)(L::kTile >> 4));
                 if (leader) {
-#pragma unroll
+#pragma unroll 1  // (the shorter code leaves more of the instruction cache to the softmax)
                     for (int k = 0; k < D / 16; ++k) {
                         const uint64_t off = (uint64_t)(((k >> 2) * (kTok * 128) + (k & 3) * 32) >> 4);
                         tc::mma(tmem + (uint32_t)sb * kTok, qd + off, kd + off, idesc, k > 0 ? 1u : 0u);
@@ -849,7 +938,7 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 tc::fence_after();
                 const uint64_t vd = vd0 + (uint64_t)((uint32_t)st * (uint32_t)(L::kTile >> 4));
                 if (leader) {
-#pragma unroll
+#pragma unroll 1  // (the shorter code leaves more of the instruction cache to the softmax)
                     for (int k = 0; k < kTok / 16; ++k)
                         tc::mma_ts(tmem + kOBase, tmem + (uint32_t)(sb * kTok + 8 * k),
                                    vd + (uint64_t)((uint32_t)(k >> 1) * two + (uint32_t)(k & 1) * odd), idesc, j > 0 || k > 0 ? 1u : 0u);
@@ -872,6 +961,7 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         // ======================= softmax =======================
         const int set = warp >> 2, wq = warp & 3;
         const int rr = wq * 32 + lane;  // TMEM lane and row of the context
+        const int rq = rr / G, rh = rr - rq * G;  // its query and head
         const uint32_t trow = tmem + ((uint32_t)(wq * 32) << 16);
         const uint32_t sp = trow + (uint32_t)(set * kTok), op = trow + kOBase;
         const int prev = set == 0 ? kSets - 1 : set - 1;  // the set of the tile before
@@ -880,11 +970,11 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const int d = p % kDescs;
             if (!wait_or_flag(&desc_full[d], (uint32_t)((p / kDescs) & 1), dead, a.err)) break;
             const Piece &pc = descs[d];
-            const int n = pc.ntiles, nrows = pc.nrows, pre = pc.pre;
+            const int n = pc.ntiles, pre = pc.pre;
             if (n == 0) break;
             // warps without rows only pass the barriers; the other rows of a warp with some go by the last query's keys
-            const bool live_warp = wq * 32 < nrows;
-            const int qi = min(rr, nrows - 1) / G;
+            const bool live_warp = wq * 32 < pc.nrows;
+            const int qi = min(rq, pc.nq - 1);
             RowState st;
             st.m = KIND == kCap ? a.m0 : -INFINITY;
             st.l = 0.f;
@@ -892,7 +982,7 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             st.r = key_range(max(pc.ks0, key_start_of(a.s, (int64_t)pc.row0 + qi)), pre, a.s.window, st.p, st.p);
             st.slope2 = 0.f;
             if constexpr (KIND == kBias || KIND == kCapBias)
-                st.slope2 = a.s.slopes ? a.s.slopes[pc.kvh * G + rr % G] * 1.44269504f : 0.f;
+                st.slope2 = a.s.slopes ? a.s.slopes[pc.kvh * G + rh] * 1.44269504f : 0.f;
             const KeyRange cr{pc.ks0, pc.cpre, pc.lo, pc.hi};
             bool any = false;
             int j = set - tau0 % kSets;
@@ -907,6 +997,8 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 const int bturn = set == 0 ? turn - 1 : turn;
                 Chain ch;
                 ch.mref = mref + rr;
+                ch.hint = hint + rr;
+                ch.piece = p;
                 ch.before = tau > 0 ? &m_full[prev * 4 + wq] : nullptr;
                 ch.mine = &m_full[set * 4 + wq];
                 ch.done = &o_done[prev];
@@ -954,6 +1046,7 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     } else if (warp < kEpiWarp + 4) {
         // ======================= epilogue =======================
         const int wq = warp & 3, rr = wq * 32 + lane;
+        const int64_t rel = ((int64_t)(rr / G) * a.num_heads + rr % G) * D;
         const uint32_t op = tmem + ((uint32_t)(wq * 32) << 16) + kOBase;
         for (int p = 0; !dead; ++p) {
             const int d = p % kDescs, f = p & 1;
@@ -961,7 +1054,7 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const Piece &pc = descs[d];
             if (pc.ntiles == 0) break;
             const int nrows = pc.nrows, slot = pc.slot;
-            const int64_t orow = (((int64_t)pc.row0 + rr / G) * a.num_heads + pc.kvh * G + rr % G) * D;
+            const int64_t orow = ((int64_t)pc.row0 * a.num_heads + pc.kvh * G) * D + rel;
             wait_or_flag(&fin_full[f], (uint32_t)((p >> 1) & 1), dead, a.err);
             float2 x[kSets];
 #pragma unroll
@@ -1145,10 +1238,7 @@ pkv_status run_rows(const Args &args, int head_dim, void *workspace, size_t work
     a.c2 = (float)(a.s.softcap * log2e);
     a.m0 = 0.25f * a.c2;
     double f = a.s.softcap * log2e * a.k1;
-    for (int i = 0; i < 6; ++i, f *= (double)a.k1 * a.k1) {
-        a.far[i] = (float)(kTanh5[i] * f);
-        if (i < 4) a.near[i] = (float)(kTanh3[i] * f);
-    }
+    for (int i = 0; i < 4; ++i, f *= (double)a.k1 * a.k1) a.near[i] = (float)(kTanh3[i] * f);
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     a.part_o = reinterpret_cast<float *>(ws + lay.o);
     a.part_ml = reinterpret_cast<float *>(ws + lay.ml);
