@@ -350,7 +350,7 @@ __device__ __forceinline__ void scores16(float (&s)[16], uint32_t sp, int ahead,
         for (int k = 0; k < 16; k += 2) f32x2_split(fma_f32x2(f32x2(s[k], s[k + 1]), f2, nm2), s[k], s[k + 1]);
     } else {
         // -slope |ahead - k|, linear unless the position is inside: one FMA for the pair's bias, one for the score
-        const float sl = beyond && ahead < 0 ? -slope2 : slope2, b = fmaf(-sl, (float)ahead, nm);
+        const float sl = beyond && ahead <= 0 ? -slope2 : slope2, b = fmaf(-sl, (float)ahead, nm);
         if (__builtin_expect(beyond && __any_sync(0xffffffffu, ahead > 0 && ahead < 15), 0)) {
             if (KIND == kCapBias) {  // capped scores over S
                 st16u(sp, reinterpret_cast<const uint32_t(&)[16]>(s));

@@ -85,6 +85,21 @@ def test_decode_many_sequences():
         c.check(run(c, max_seq_len=256))
 
 
+@pytest.mark.parametrize("kind", ["bf16", "rows"])
+def test_decode_thousands_of_sequences(kind):
+    """More sequences than the tensor-core kernel's table holds."""
+    c = Case([(7 * i) % 23 for i in range(8200)], 2, 1, 64, 16, softcap=10.0, alibi=True, window=11, rows=kind == "rows")
+    c.check(run(c))
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,B", [(1, 1, 64, 16), (8, 1, 128, 32), (6, 2, 64, 8), (7, 7, 128, 16)])
+def test_decode_float32_partitions(Hq, Hkv, D, B):
+    """Float32 contexts around the sizes at which its kernel splits them, some of whose parts see nothing."""
+    c = Case([511, 512, 513, 1024, 1025, 2000], Hq, Hkv, D, B, dtype=torch.float32, softcap=12.0, alibi=True, window=300,
+             prefix=[0, 1, 513, 0, 600, 2])
+    c.check(run(c))
+
+
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
 def test_decode_append_stores_the_token(kind):
     dt = torch.float32 if kind == "f32" else torch.bfloat16
@@ -147,6 +162,28 @@ def test_multi_options(shape, opt):
 def test_multi_heads_and_blocks(Hq, Hkv, D, B, qlens):
     c = Case([470, 90, 600], Hq, Hkv, D, B, qlens=qlens, softcap=15.0, alibi=True, window=250, prefix=[0, 40, 20], seed=5)
     c.check(run(c))
+
+
+@pytest.mark.parametrize("opt", [{}, dict(alibi=True), dict(alibi=True, softcap=300.0), dict(softcap=400.0),
+                                 dict(alibi=True, prefix=[650, 200, 0, 1500], window=100)],
+                         ids=["plain", "alibi", "cap_alibi", "wide_cap", "prefix_alibi"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_multi_scores_far_apart(opt, D):
+    """Scores that differ by hundreds of powers of two, so that the rows' references move within tiles and between them."""
+    c = Case([700, 260, 131, 1700], 8, 2, D, 16, qlens=[200, 131, 5, 300], qmul=60.0, **opt)
+    assert c.D == D
+    c.check(run(c))
+
+
+def test_multi_scores_that_grow_and_shrink():
+    """Keys whose scores rise, or fall, steadily along the context: every tile has a larger maximum than the one before it."""
+    for sign in (1.0, -1.0):
+        c = Case([1500, 900], 4, 1, 128, 16, qlens=[140, 33])
+        for s, L in enumerate(c.lens):
+            ramp = torch.linspace(0.0, 2.0 * sign, L)[:, None, None]
+            c.ks[s] = (ramp + 0.01 * c.ks[s].float()).to(torch.bfloat16)
+        c.q = (c.q.float().abs() + 1.0).to(torch.bfloat16)
+        c.check(run(c), f"sign {sign}")
 
 
 def test_one_query_per_sequence_is_the_decode():
