@@ -1,9 +1,10 @@
 // Scored attention over the paged cache: attention whose scores are capped by
 // a tanh or biased by distance and whose keys are limited by a window, a
 // document's start and an always visible prefix (scored.cuh has the rules).
-//   * scored_simt_kernel -- one CTA per (query, kv head, 512-token partition)
-//     on CUDA cores, float32 arithmetic with expf and tanhf whatever the
-//     storage; scored_reduce_kernel merges the partitions.
+//   * scored_simt_kernel -- decode, one CTA per (sequence, kv head, 512-token
+//     partition) on CUDA cores, float32 arithmetic with expf and tanhf whatever
+//     the storage; scored_reduce_kernel merges the partitions.  It serves
+//     float32 caches, and batches of more than kMaxDecodeSeqs sequences.
 //
 // With x_t the score of a seen key in base 2 and f_t its V row's scale (1 for
 // plain caches), the running state of a row is (M, l, o) with M = max_t x_t,
@@ -24,40 +25,16 @@ constexpr int kPartition = 512;  // tokens per CTA of the CUDA-core kernel
 enum Storage { kF32 = 0, kBf16 = 1, kFp8Rows = 2 };
 
 struct SimtArgs : Args {
-    float *part_o;   // [queries][Hq][parts][D]
-    float *part_ml;  // [queries][Hq][parts][2]
+    float *part_o;   // [seqs][Hq][parts][D]
+    float *part_ml;  // [seqs][Hq][parts][2]
     int parts;
 };
 
-// The query of a CTA: sequence, row of q and out, position, context length.
-struct Query {
-    int seq, row, pos, len;
-};
-
-// False: nothing to do (past the sequence's queries, or a bad description).
-__device__ __forceinline__ bool find_query(const Args &a, int x, Query &w, bool report) {
-    const int cap = min(a.max_seq_len, a.max_blocks * a.block_size);
-    int q0 = x, nq = 1, i = 0;
-    w.seq = x;
-    if (a.q_starts) {
-        w.seq = x / a.max_q_len;
-        i = x - w.seq * a.max_q_len;
-        q0 = a.q_starts[w.seq];
-        const int q1 = a.q_starts[w.seq + 1];
-        if (q0 < 0 || q1 < q0 || q1 > a.num_q) {
-            if (report && i == 0) flag_error(a.err, PKV_DEVERR_SEQ_LEN);
-            return false;
-        }
-        nq = q1 - q0;
-    }
-    const int raw = a.seq_lens[w.seq];
-    w.len = raw < 0 ? 0 : min(raw, cap);
-    if (report && i == 0 && (raw != w.len || (a.q_starts && (nq > a.max_q_len || nq > w.len))))
-        flag_error(a.err, PKV_DEVERR_SEQ_LEN);
-    if (i >= nq) return false;
-    w.row = q0 + i;
-    w.pos = w.len - nq + i;
-    return true;
+// The context length of a sequence: what is addressable of it.
+__device__ __forceinline__ int context_len(const Args &a, int seq, bool report) {
+    const int raw = a.seq_lens[seq], len = raw < 0 ? 0 : min(raw, min(a.max_seq_len, a.max_blocks * a.block_size));
+    if (report && raw != len) flag_error(a.err, PKV_DEVERR_SEQ_LEN);
+    return len;
 }
 
 template <typename T>
@@ -69,98 +46,151 @@ __device__ __forceinline__ void put<__nv_bfloat16>(__nv_bfloat16 *p, float x) { 
 __device__ __forceinline__ float get(float x) { return x; }
 __device__ __forceinline__ float get(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-// Element d of a cache row.
-template <int ST>
-__device__ __forceinline__ float cached(const void *c, int64_t i) {
-    if constexpr (ST == kF32) return static_cast<const float *>(c)[i];
-    else if constexpr (ST == kBf16) return __bfloat162float(static_cast<const __nv_bfloat16 *>(c)[i]);
-    else {
-        float x[4];
-        e4m3x4_to_float(static_cast<const unsigned char *>(c)[i], x);
-        return x[0];
+// N (2 or 4) consecutive elements of a cache row from element i on, N | i.
+template <int ST, int N>
+__device__ __forceinline__ void load_cached(const void *c, int64_t i, float (&x)[N]) {
+    if constexpr (ST == kF32) {
+        if constexpr (N == 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(static_cast<const float *>(c) + i);
+            x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+        } else {
+            const float2 v = *reinterpret_cast<const float2 *>(static_cast<const float *>(c) + i);
+            x[0] = v.x, x[1] = v.y;
+        }
+    } else if constexpr (ST == kBf16) {
+        const uint32_t *p = reinterpret_cast<const uint32_t *>(static_cast<const __nv_bfloat16 *>(c) + i);
+        uint32_t v[N / 2];
+        if constexpr (N == 4) {
+            const uint2 w = *reinterpret_cast<const uint2 *>(p);
+            v[0] = w.x, v[1] = w.y;
+        } else {
+            v[0] = *p;
+        }
+#pragma unroll
+        for (int k = 0; k < N / 2; ++k) x[2 * k] = bf16x2_lo(v[k]), x[2 * k + 1] = bf16x2_hi(v[k]);
+    } else {
+        const unsigned char *p = static_cast<const unsigned char *>(c) + i;
+        float y[4];
+        e4m3x4_to_float(N == 4 ? *reinterpret_cast<const uint32_t *>(p) : *reinterpret_cast<const uint16_t *>(p), y);
+#pragma unroll
+        for (int k = 0; k < N; ++k) x[k] = y[k];
     }
 }
 
+// A warp takes eight tokens at once: four lanes share a token's K row (16-byte pieces in turn) for the scores of all heads,
+// and every lane owns D / 32 consecutive entries of the output.  Loads of sixteen rows are in flight; with a token at a
+// time, four float32 sequences of up to 100 tokens took 15 us instead of 9.
 template <int ST, int D>
 __global__ void __launch_bounds__(128) scored_simt_kernel(const SimtArgs a) {
     using T = typename std::conditional<ST == kF32, float, __nv_bfloat16>::type;
-    constexpr int NW = 4, E = D / 32;
+    constexpr int NW = 4, E = D / 32, C = D / 16;  // C: 4-element pieces of a K row per lane
     __shared__ float so[NW][kGMax * D], sm[NW][kGMax], sl[NW][kGMax];
+    __shared__ float4 sq[kGMax * D / 4];
     grid_dependency_wait();
     grid_launch_dependents();
-    Query w;
-    const int kvh = blockIdx.y, part = blockIdx.z, G = a.group, B = a.block_size;
-    if (!find_query(a, blockIdx.x, w, kvh == 0 && part == 0 && threadIdx.x == 0)) return;
-    const int t0 = part * kPartition, t1 = min(w.len, t0 + kPartition);
-    if (part > 0 && t0 >= w.len) return;
-    const KeyRange kr = key_range(key_start_of(a.s, w.row), prefix_of(a.s, w.seq, w.len), a.s.window, w.pos, w.pos);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int seq = blockIdx.x, kvh = blockIdx.y, part = blockIdx.z, G = a.group, B = a.block_size;
+    const int len = context_len(a, seq, kvh == 0 && part == 0 && threadIdx.x == 0), pos = len - 1;
+    const int t0 = part * kPartition, t1 = min(len, t0 + kPartition);
+    if (part > 0 && t0 >= len) return;
+    const KeyRange kr = key_range(key_start_of(a.s, seq), prefix_of(a.s, seq, len), a.s.window, pos, pos);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, piece = lane & 3;
 
-    float qf[kGMax][E], o[kGMax][E], m[kGMax], l[kGMax], slope[kGMax];
-    const T *qb = static_cast<const T *>(a.q) + ((int64_t)w.row * a.num_heads + kvh * G) * D;
+    const T *qb = static_cast<const T *>(a.q) + ((int64_t)seq * a.num_heads + kvh * G) * D;
+    for (int i = threadIdx.x; i < G * D; i += 128) reinterpret_cast<float *>(sq)[i] = get(qb[i]);
+    float o[kGMax][E], m[kGMax], l[kGMax], slope[kGMax];
 #pragma unroll
     for (int g = 0; g < kGMax; ++g) {
         m[g] = -INFINITY;
         l[g] = 0.f;
         slope[g] = a.s.slopes && g < G ? a.s.slopes[kvh * G + g] : 0.f;
 #pragma unroll
-        for (int j = 0; j < E; ++j) {
-            qf[g][j] = g < G ? get(qb[g * D + lane + 32 * j]) : 0.f;
-            o[g][j] = 0.f;
-        }
+        for (int j = 0; j < E; ++j) o[g][j] = 0.f;
     }
-    const int32_t *bt = a.block_tables + (int64_t)w.seq * a.max_blocks;
-    if (kr.meets(t0, t1)) {
-        for (int t = t0 + warp; t < t1; t += NW) {
-            if (!kr.sees(t)) continue;
+    __syncthreads();
+    const int32_t *bt = a.block_tables + (int64_t)seq * a.max_blocks;
+    for (int base = t0 + 8 * warp; base < t1; base += 8 * NW) {
+        if (!kr.meets(base, min(base + 8, t1))) continue;
+        const int t = base + (lane >> 2);
+        int64_t row = -1;  // of this lane's token
+        if (t < t1 && kr.sees(t)) {
             const int lb = t / B, blk = bt[lb];
-            if (blk < 0 || blk >= a.num_blocks) {
-                if (lane == 0) flag_error(a.err, PKV_DEVERR_BLOCK_ID);
-                continue;
-            }
-            const int64_t row = ((int64_t)blk * a.num_kv_heads + kvh) * B + (t - lb * B);
-            float kf[E], vf[E], kscale = 1.f, vscale = 1.f;
+            if (blk >= 0 && blk < a.num_blocks) row = ((int64_t)blk * a.num_kv_heads + kvh) * B + (t - lb * B);
+            else if (piece == 0) flag_error(a.err, PKV_DEVERR_BLOCK_ID);
+        }
+        float kf[C][4], vf[8][E], kscale = 1.f, vscale = 1.f;
+        if (row >= 0) {
             if constexpr (ST == kFp8Rows) {
                 kscale = row_scale(a.k_scales[row]);
                 vscale = row_scale(a.v_scales[row]);
             }
 #pragma unroll
-            for (int j = 0; j < E; ++j) {
-                kf[j] = cached<ST>(a.k_cache, row * D + lane + 32 * j) * kscale;
-                vf[j] = cached<ST>(a.v_cache, row * D + lane + 32 * j) * vscale;
+            for (int c = 0; c < C; ++c) load_cached<ST, 4>(a.k_cache, row * D + 16 * c + 4 * piece, kf[c]);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int64_t r = __shfl_sync(0xffffffffu, row, 4 * i);
+            if (r >= 0) {
+                load_cached<ST, E>(a.v_cache, r * D + E * lane, vf[i]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < E; ++j) vf[i][j] = 0.f;
             }
-            const float away = (float)abs(w.pos - t);
+        }
+        const float away = (float)abs(pos - t);
 #pragma unroll
-            for (int g = 0; g < kGMax; ++g) {
-                if (g >= G) break;
-                float x = 0.f;
+        for (int g = 0; g < kGMax; ++g) {
+            if (g >= G) break;
+            float x = 0.f;
+            if (row >= 0) {
 #pragma unroll
-                for (int j = 0; j < E; ++j) x = fmaf(qf[g][j], kf[j], x);
+                for (int c = 0; c < C; ++c) {
+                    const float4 qv = sq[(g * D + 16 * c) / 4 + piece];
+                    x = fmaf(qv.x, kf[c][0], fmaf(qv.y, kf[c][1], fmaf(qv.z, kf[c][2], fmaf(qv.w, kf[c][3], x))));
+                }
+            }
+            x += __shfl_xor_sync(0xffffffffu, x, 1);
+            x += __shfl_xor_sync(0xffffffffu, x, 2);
+            x *= kscale * a.s.scale;
+            if (a.s.softcap > 0.f) x = a.s.softcap * tanhf(x / a.s.softcap);
+            x -= slope[g] * away;
+            if (row < 0) x = -INFINITY;
+            float mx = x;
 #pragma unroll
-                for (int sh = 16; sh > 0; sh >>= 1) x += __shfl_xor_sync(0xffffffffu, x, sh);
-                x *= a.s.scale;
-                if (a.s.softcap > 0.f) x = a.s.softcap * tanhf(x / a.s.softcap);
-                x -= slope[g] * away;
-                const float mn = fmaxf(m[g], x);
-                const float al = m[g] == mn ? 1.f : expf(m[g] - mn), p = expf(x - mn);
-                l[g] = l[g] * al + p;
+            for (int sh = 4; sh < 32; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
+            const float mn = fmaxf(m[g], mx);
+            if (mn != m[g]) {
+                const float al = expf(m[g] - mn);
+                l[g] *= al;
 #pragma unroll
-                for (int j = 0; j < E; ++j) o[g][j] = fmaf(p, vf[j], o[g][j] * al);
+                for (int j = 0; j < E; ++j) o[g][j] *= al;
                 m[g] = mn;
+            }
+            const float p = row >= 0 ? expf(x - mn) : 0.f, pv = p * vscale;
+            l[g] += p;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float w = __shfl_sync(0xffffffffu, pv, 4 * i);
+#pragma unroll
+                for (int j = 0; j < E; ++j) o[g][j] = fmaf(w, vf[i][j], o[g][j]);
             }
         }
     }
 #pragma unroll
     for (int g = 0; g < kGMax; ++g) {
 #pragma unroll
-        for (int j = 0; j < E; ++j) so[warp][g * D + lane + 32 * j] = o[g][j];
+        for (int sh = 4; sh < 32; sh <<= 1) l[g] += __shfl_xor_sync(0xffffffffu, l[g], sh);
+    }
+#pragma unroll
+    for (int g = 0; g < kGMax; ++g) {
+#pragma unroll
+        for (int j = 0; j < E; ++j) so[warp][g * D + E * lane + j] = o[g][j];
         if (lane == 0) {
             sm[warp][g] = m[g];
             sl[warp][g] = l[g];
         }
     }
     __syncthreads();
-    const bool whole = w.len <= kPartition;
+    const bool whole = len <= kPartition;
     for (int i = threadIdx.x; i < G * D; i += 128) {
         const int g = i / D, d = i % D;
         float M = -INFINITY, L = 0.f, O = 0.f;
@@ -173,7 +203,7 @@ __global__ void __launch_bounds__(128) scored_simt_kernel(const SimtArgs a) {
             O = fmaf(c, so[k][g * D + d], O);
             L = fmaf(c, sl[k][g], L);
         }
-        const int64_t row = (int64_t)w.row * a.num_heads + kvh * G + g;
+        const int64_t row = (int64_t)seq * a.num_heads + kvh * G + g;
         if (whole) {
             put(static_cast<T *>(a.out) + row * D + d, L != 0.f ? O / L : 0.f);
         } else {
@@ -187,20 +217,18 @@ __global__ void __launch_bounds__(128) scored_simt_kernel(const SimtArgs a) {
     }
 }
 
-// One warp per (query, head): the partitions' states, merged in order.
+// One warp per (sequence, head): the partitions' states, merged in order.
 template <typename T, int D>
 __global__ void __launch_bounds__(128) scored_reduce_kernel(const SimtArgs a) {
     constexpr int E = D / 32;
     grid_dependency_wait();
     grid_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int64_t total = (int64_t)(a.q_starts ? (int64_t)a.num_seqs * a.max_q_len : a.num_seqs) * a.num_heads;
-    if (r >= total) return;
-    Query w;
-    if (!find_query(a, (int)(r / a.num_heads), w, false) || w.len <= kPartition) return;
-    const int64_t row = (int64_t)w.row * a.num_heads + r % a.num_heads;
-    const int n = (w.len + kPartition - 1) / kPartition;
+    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (row >= (int64_t)a.num_seqs * a.num_heads) return;
+    const int len = context_len(a, (int)(row / a.num_heads), false);
+    if (len <= kPartition) return;
+    const int n = (len + kPartition - 1) / kPartition;
     const float *ml = a.part_ml + row * a.parts * 2, *po = a.part_o + row * a.parts * D + lane;
     float M = -INFINITY, L = 0.f, o[E];
     for (int j = 0; j < n; ++j) M = fmaxf(M, ml[2 * j]);
@@ -217,9 +245,9 @@ __global__ void __launch_bounds__(128) scored_reduce_kernel(const SimtArgs a) {
     for (int e = 0; e < E; ++e) put(static_cast<T *>(a.out) + row * D + lane + 32 * e, L != 0.f ? o[e] / L : 0.f);
 }
 
-static size_t simt_workspace(int64_t queries, int64_t heads, int64_t D, int64_t max_seq_len) {
+static size_t simt_workspace(int64_t seqs, int64_t heads, int64_t D, int64_t max_seq_len) {
     const int64_t parts = (max_seq_len + kPartition - 1) / kPartition;
-    return parts <= 1 ? 0 : round256((size_t)(queries * heads * parts * D * 4)) + round256((size_t)(queries * heads * parts * 8));
+    return parts <= 1 ? 0 : round256((size_t)(seqs * heads * parts * D * 4)) + round256((size_t)(seqs * heads * parts * 8));
 }
 
 template <int ST, int D>
@@ -227,21 +255,20 @@ static pkv_status run_simt(const Args &args, void *workspace, size_t bytes, cuda
     using T = typename std::conditional<ST == kF32, float, __nv_bfloat16>::type;
     SimtArgs a{};
     static_cast<Args &>(a) = args;
-    const int64_t x = a.q_starts ? (int64_t)a.num_seqs * a.max_q_len : a.num_seqs;
     a.parts = std::max(1, (a.max_seq_len + kPartition - 1) / kPartition);
-    if (x > INT32_MAX || a.num_kv_heads > 65535 || a.parts > 65535) return PKV_ERR_UNSUPPORTED;
+    if (a.num_kv_heads > 65535 || a.parts > 65535) return PKV_ERR_UNSUPPORTED;
     if (a.parts > 1) {
-        if (!workspace || bytes < simt_workspace(a.num_q, a.num_heads, D, a.max_seq_len) ||
+        if (!workspace || bytes < simt_workspace(a.num_seqs, a.num_heads, D, a.max_seq_len) ||
             (reinterpret_cast<uintptr_t>(workspace) & 255u))
             return PKV_ERR_INVALID;
         a.part_o = static_cast<float *>(workspace);
         a.part_ml = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) +
-                                              round256((size_t)a.num_q * a.num_heads * a.parts * D * 4));
+                                              round256((size_t)a.num_seqs * a.num_heads * a.parts * D * 4));
     }
-    const dim3 grid((unsigned)x, (unsigned)a.num_kv_heads, (unsigned)a.parts);
+    const dim3 grid((unsigned)a.num_seqs, (unsigned)a.num_kv_heads, (unsigned)a.parts);
     pkv_status rc = launch_pdl(scored_simt_kernel<ST, D>, grid, dim3(128), 0, st, a);
     if (rc == PKV_OK && a.parts > 1)
-        rc = launch_pdl(scored_reduce_kernel<T, D>, dim3((unsigned)((x * a.num_heads + 3) / 4)), dim3(128), 0, st, a);
+        rc = launch_pdl(scored_reduce_kernel<T, D>, dim3((unsigned)(((int64_t)a.num_seqs * a.num_heads + 3) / 4)), dim3(128), 0, st, a);
     return rc;
 }
 

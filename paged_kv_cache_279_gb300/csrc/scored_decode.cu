@@ -31,12 +31,6 @@
 #include "pkv_internal.cuh"
 #include "scored.cuh"
 
-#ifndef LEAD8
-#define LEAD8 2
-#define LEAD16 3
-#define MS8 8
-#define MS16 16
-#endif
 namespace pkv {
 namespace scored {
 namespace {
@@ -47,8 +41,8 @@ constexpr int kMaxWarps = 2048;   // partial slots in the workspace: two per war
 template <int D, bool F8>
 struct Tile {
     static constexpr int kTok = F8 ? 32 : 16;
-    static constexpr int kLead = F8 ? LEAD8 : LEAD16;      // empty tiles in front of a segment
-    static constexpr int kMinShare = F8 ? MS8 : MS16; // tiles (256 tokens), less where every segment is shorter
+    static constexpr int kLead = F8 ? 2 : 3;  // empty tiles in front of a segment
+    static constexpr int kMinShare = F8 ? 8 : 16;  // tiles (256 tokens), less where every segment is shorter
     static constexpr int kKV = kTok * D * (F8 ? 1 : 2);
     static constexpr int kStage = 2 * kKV;
     static constexpr int kScales = F8 ? 2 * kTok : 0;  // per stage: K scales, V scales
