@@ -338,7 +338,9 @@ PKV_EXPORT pkv_status paged_attention_multi_token(void *out, const void *q, cons
  * kv_cache_write_fp8_rows -- quantise and store the K/V of new tokens.
  *   k_new, v_new   device [num_tokens][num_kv_heads][head_dim], dtype (F32 or BF16)
  *   k_cache, v_cache, k_scales, v_scales  device, written in place
- *   slot_mapping   device int64 [num_tokens], as for kv_cache_write
+ *   slot_mapping   device int64 [num_tokens], as for kv_cache_write, but each
+ *                  slot at most once in a call: of two tokens on one slot the
+ *                  codes of either may end up beside the scale of the other
  *
  * kv_cache_read_fp8_rows -- the values of stored tokens, by slot (a prefix to
  * be attended by other kernels, stored elsewhere or compared).

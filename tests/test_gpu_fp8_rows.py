@@ -50,6 +50,37 @@ def test_write_is_exact_and_touches_only_its_slots(dtype, T, Hkv, D, B):
         assert np.array_equal(c.cpu().numpy(), wc)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("k_off,v_off", [(8, 8), (0, 8), (8, 0), (16, 16)])
+def test_rows_on_any_16_byte_boundary(dtype, D, k_off, v_off):
+    """Rows that begin 16 bytes (bf16) behind a 32-byte boundary give the same bytes, and are read back to such places."""
+    T, Hkv, B = 37, 3, 16
+    k, v = _rows(T, Hkv, D, dtype, 5).cuda(), _rows(T, Hkv, D, dtype, 6).cuda()
+
+    def shifted(x, off):
+        off = off if dtype == torch.bfloat16 else off // 2
+        flat = torch.full((x.numel() + 32,), 7.0, dtype=dtype, device="cuda")
+        y = flat[off:off + x.numel()].view(x.shape)
+        y.copy_(x)
+        return flat, y
+
+    slots = torch.from_numpy(np.random.default_rng(3).permutation(5 * B)[:T].astype(np.int64)).cuda()
+    want, got = _pools(5, Hkv, B, D), _pools(5, Hkv, B, D)
+    pkv.kv_cache_write_fp8_rows(k, v, *want, slots)
+    (_, ks), (_, vs) = shifted(k, k_off), shifted(v, v_off)
+    pkv.kv_cache_write_fp8_rows(ks, vs, *got, slots)
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+    k2, v2 = torch.empty_like(k), torch.empty_like(v)
+    pkv.kv_cache_read_fp8_rows(k2, v2, *want, slots)
+    (kf, ks), (vf, vs) = shifted(torch.zeros_like(k), k_off), shifted(torch.zeros_like(v), v_off)
+    pkv.kv_cache_read_fp8_rows(ks, vs, *want, slots)
+    for plain, at, flat in ((k2, ks, kf), (v2, vs, vf)):
+        assert torch.equal(plain, at)
+        assert int((flat == 7.0).sum()) >= 32  # what lies around the rows is left
+
+
 def test_write_of_special_rows():
     D, B = 64, 16
     x = torch.zeros(12, 1, D)
