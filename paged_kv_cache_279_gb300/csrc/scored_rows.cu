@@ -124,12 +124,18 @@ __device__ __forceinline__ bool elect_one() {
 
 __device__ __forceinline__ void prefetch_l1(const void *p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
 
-__device__ __forceinline__ bool wait_or_flag(uint64_t *bar, uint32_t parity, bool &dead, unsigned int *err) {
-    if (dead) return false;
-    if (mbar_wait_bounded(bar, parity)) return true;
-    flag_error(err, PKV_DEVERR_TIMEOUT);
-    dead = true;
-    return false;
+// Waits are many and rarely long: kept to a few instructions, and one that gives up sets `dead` (then no other waits), which
+// the kernel's end reports.
+__device__ __forceinline__ bool drain(uint64_t *bar, uint32_t parity) {
+    uint32_t i = 0;
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity))
+        if (++i == kWaitLimit) return false;
+    return true;
+}
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, bool &dead) {
+    if (!dead) dead = !drain(bar, parity);
+    return !dead;
 }
 
 // ---------------------------------------------------------------------------
@@ -188,10 +194,23 @@ __device__ __forceinline__ int first_pos(const RowsArgs &a, const Seq &x, int s)
 
 __device__ __forceinline__ int laid_out(int n) { return n > 0 ? n + kCharge : 0; }
 
-__host__ __device__ __forceinline__ int64_t split_parts(int64_t T, int64_t ctas) {
-    const int64_t by_size = T / kMinShare > 1 ? T / kMinShare : 1;
-    return ctas < by_size ? ctas : by_size;
-}
+// The T laid-out tiles cut into equal shares, share c = [floor(c T / n), floor((c + 1) T / n)), in 32-bit steps
+// (T = each * n + rest).
+struct Shares {
+    int n, each, rest;
+    __device__ __forceinline__ Shares(int T, int ctas) {
+        n = min(ctas, max(T / kMinShare, 1));
+        each = T / n;
+        rest = T - each * n;
+    }
+    __device__ __forceinline__ int begin(int c) const { return c * each + (int)((uint32_t)(c * rest) / (uint32_t)n); }
+    __device__ __forceinline__ int owner(int t) const {  // the share that holds tile t
+        int c = min(n - 1, t / each);
+#pragma unroll 1
+        while (begin(c) > t) --c;
+        return c;
+    }
+};
 
 // ---------------------------------------------------------------------------
 // Softmax step
@@ -516,7 +535,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t sp, uint32_t op, const Til
             weights16(x, sp + 8 * c, ls);
         }
         // the tile before's reference
-        if (ch.before) wait_or_flag(ch.before, ch.parity, dead, a.err);
+        if (ch.before) wait_for(ch.before, ch.parity, dead);
         const float old = ch.first ? -INFINITY : *ch.mref, mf = fmaxf(old, m);
         *ch.mref = mf;
         __syncwarp();
@@ -534,7 +553,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t sp, uint32_t op, const Til
         }
         const bool move = old != -INFINITY && mf != old;
         if (__any_sync(0xffffffffu, move)) {
-            wait_or_flag(ch.done, ch.parity, dead, a.err);
+            wait_for(ch.done, ch.parity, dead);
             tc::fence_after();
             const float alpha = move ? ex2_approx(old - mf) : 1.f;
 #pragma unroll 1
@@ -602,18 +621,22 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         if (s < a.num_seqs) {
             const Seq x = load_seq(a, s, report && sub == 0);
             const int fp = first_pos(a, x, s), nb = (x.Q + a.per_ctx - 1) / a.per_ctx;
+#pragma unroll 1
             for (int b = sub; b < nb; b += W) t += laid_out(ctx_tiles(a, x, fp, b).n);
         }
+#pragma unroll 1
         for (int sh = 1; sh < W; sh <<= 1) t += __shfl_xor_sync(0xffffffffu, t, sh);
         return t * Hkv;
     };
     int T = 0, my_s0 = 0, my_s1 = 0;
-    int64_t parts = 1;
+    Shares shares(0, 1);
     int start = 0, v = 0;  // this thread's sequence of the last pass: its laid-out start and tiles
     // the total, then the sequence that holds this share's start (from registers when one pass covers every sequence)
+#pragma unroll 1
     for (int round = 0; round < (a.num_seqs > per_pass ? 2 : 1); ++round) {
         if (threadIdx.x == 0) scratch[kCarry] = 0;
         __syncthreads();
+#pragma unroll 1
         for (int base = 0; base < a.num_seqs; base += per_pass) {
             const int s = threadIdx.x < 640 ? base + threadIdx.x / W : a.num_seqs;
             const int total = seq_total(s, round == 0 && blockIdx.x == 0);
@@ -627,6 +650,7 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (lane == 31) scratch[warp] = x;
             __syncthreads();
             int before = scratch[kCarry];
+#pragma unroll 1
             for (int w = 0; w < warp; ++w) before += scratch[w];
             const int end = before + x;
             start = end - v;
@@ -640,12 +664,12 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
         if (round == 0) {
             T = scratch[kCarry];
-            parts = split_parts(T, gridDim.x);
+            shares = Shares(T, gridDim.x);
             __syncthreads();  // every thread has the total before the next round clears it
             if (threadIdx.x == 0) a.merges[blockIdx.x] = make_int4(0, 0, 0, 0);
-            if (T == 0 || blockIdx.x >= parts) return;
-            my_s0 = (int)((int64_t)blockIdx.x * T / parts);
-            my_s1 = (int)(((int64_t)blockIdx.x + 1) * T / parts);
+            if (T == 0 || (int)blockIdx.x >= shares.n) return;
+            my_s0 = shares.begin(blockIdx.x);
+            my_s1 = shares.begin(blockIdx.x + 1);
         }
     }
     const int s0 = my_s0, s1 = my_s1;
@@ -656,20 +680,25 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 
     if (threadIdx.x < kRows) hint[threadIdx.x] = ~0ull;  // no piece's
     if (threadIdx.x == 0) {
+#pragma unroll 1
         for (int i = 0; i < NK; ++i) {
             mbar_init(&k_full[i], H);
             mbar_init(&k_empty[i], 1);
         }
+#pragma unroll 1
         for (int i = 0; i < NV; ++i) {
             mbar_init(&v_full[i], 1);
             mbar_init(&v_empty[i], 1);
         }
+#pragma unroll 1
         for (int i = 0; i < kSets; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
             mbar_init(&o_done[i], 1);
         }
+#pragma unroll 1
         for (int i = 0; i < 4 * kSets; ++i) mbar_init(&m_full[i], 1);
+#pragma unroll 1
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 1);
             mbar_init(&q_empty[i], 1);
@@ -678,6 +707,7 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
         mbar_init(o_last, 1);
         mbar_init(o_free, 4);
+#pragma unroll 1
         for (int i = 0; i < kDescs; ++i) {
             mbar_init(&desc_full[i], 1);
             mbar_init(&desc_empty[i], 4 * kSets + 4 + 2 + H + 1);  // softmax, epilogue, MMA, producers
@@ -709,11 +739,14 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const Seq x = load_seq(a, s, false);
             const int fp = first_pos(a, x, s), nb = (x.Q + a.per_ctx - 1) / a.per_ctx;
             int per_kvh = 0;
+#pragma unroll 1
             for (int b = lane; b < nb; b += 32) per_kvh += laid_out(ctx_tiles(a, x, fp, b).n);
 #pragma unroll
             for (int sh = 16; sh > 0; sh >>= 1) per_kvh += __shfl_xor_sync(0xffffffffu, per_kvh, sh);
+#pragma unroll
             for (int kvh = per_kvh > 0 ? (t - seq_start) / per_kvh : Hkv; kvh < Hkv && t < s1 && !dead; ++kvh) {
                 int pos = seq_start + kvh * per_kvh;  // laid-out start of block b0
+#pragma unroll 1
                 for (int b0 = 0; b0 < nb && t < s1 && !dead; b0 += 32) {
                     CtxTiles c{};
                     if (b0 + lane < nb) c = ctx_tiles(a, x, fp, b0 + lane);
@@ -728,10 +761,11 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     // this lane's context: its real tiles [i0, i1) in the share
                     const int i0 = max(0, max(s0, begin) - begin - kCharge), i1 = min(s1, end) - begin - kCharge;
                     const bool mine = c.n > 0 && begin < s1 && end > s0 && i1 > i0;
+#pragma unroll 1
                     for (uint32_t todo = __ballot_sync(0xffffffffu, mine); todo && !dead; todo &= todo - 1) {
                         const int d = p % kDescs;
                         if (lane == 0 && p >= kDescs)
-                            wait_or_flag(&desc_empty[d], (uint32_t)((p / kDescs - 1) & 1), dead, a.err);
+                            wait_for(&desc_empty[d], (uint32_t)((p / kDescs - 1) & 1), dead);
                         dead = __shfl_sync(0xffffffffu, dead, 0);
                         if (lane == __ffs(todo) - 1 && !dead) {
                             Piece pc;
@@ -760,18 +794,20 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             const bool begins = begin + kCharge >= s0, ends = end <= s1;
                             pc.slot = begins && ends ? -1 : 2 * (int)blockIdx.x + (begins ? 1 : 0);
                             if (begins && !ends)  // the shares that hold the rest
-                                a.merges[blockIdx.x] = make_int4((int)share_owner(end - 1, T, parts) - (int)blockIdx.x + 1, pc.row0,
+                                a.merges[blockIdx.x] = make_int4(shares.owner(end - 1) - (int)blockIdx.x + 1, pc.row0,
                                                                  pc.nrows, kvh);
                             descs[d] = pc;
                             mbar_arrive(&desc_full[d]);
                             // the rows' loads at the piece's start
                             if (a.s.key_starts)
+#pragma unroll 1
                                 for (int i = 0; i < nq; i += 32) prefetch_l1(a.s.key_starts + pc.row0 + i);
                             // its queries: per_ctx queries of the KV head's G heads, one box per column half
                             const int qb = p & 1;
-                            if (p >= 2) wait_or_flag(&q_empty[qb], (uint32_t)((p / 2 - 1) & 1), dead, a.err);
+                            if (p >= 2) wait_for(&q_empty[qb], (uint32_t)((p / 2 - 1) & 1), dead);
                             if (!dead) {
                                 mbar_arrive_expect_tx(&q_full[qb], (uint32_t)(H * a.per_ctx * G * 128));
+#pragma unroll
                                 for (int h = 0; h < H; ++h)
                                     tma_load_3d(q_s + (uint32_t)(qb * L::kQTile + h * (kRows * 128)), &tm_q, smem_u32(&q_full[qb]),
                                                 h * 64, kvh * G, pc.row0);
@@ -791,7 +827,7 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
         if (lane == 0 && !dead) {
             const int d = p % kDescs;
-            if (p >= kDescs) wait_or_flag(&desc_empty[d], (uint32_t)((p / kDescs - 1) & 1), dead, a.err);
+            if (p >= kDescs) wait_for(&desc_empty[d], (uint32_t)((p / kDescs - 1) & 1), dead);
             if (!dead) {
                 descs[d].ntiles = 0;
                 mbar_arrive(&desc_full[d]);
@@ -799,7 +835,8 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
         // queries in flight (only after a timeout) land before the CTA exits
         if (dead && lane == 0)
-            for (int k = max(0, p - 2); k < p; ++k) mbar_wait_bounded(&q_full[k & 1], (uint32_t)((k >> 1) & 1));
+#pragma unroll 1
+            for (int k = max(0, p - 2); k < p; ++k) drain(&q_full[k & 1], (uint32_t)((k >> 1) & 1));
     } else if (warp == kVWarp || (warp >= kKWarp && warp < kKWarp + H)) {
         // ======================= producers =======================
         const bool isk = warp != kVWarp;
@@ -808,9 +845,10 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         uint64_t *full = isk ? k_full : v_full, *empty = isk ? k_empty : v_empty;
         const int bpt = kTok >> a.bshift;  // blocks per tile, at most 16
         int tau = 0;
+#pragma unroll 1
         for (int p = 0; !dead; ++p) {
             const int d = p % kDescs;
-            if (!wait_or_flag(&desc_full[d], (uint32_t)((p / kDescs) & 1), dead, a.err)) break;
+            if (!wait_for(&desc_full[d], (uint32_t)((p / kDescs) & 1), dead)) break;
             const Piece &pc = descs[d];
             const int n = pc.ntiles;
             if (n == 0) break;
@@ -831,11 +869,12 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 return max((int)bt[t >> a.bshift], INT_MIN + 1);
             };
             int next = block_id(0);
+#pragma unroll 1
             for (int j = 0; j < n; ++j, ++tau) {
                 const int st = tau % N;
                 const int id = next;
                 next = block_id(j + 1);
-                if (tau >= N) wait_or_flag(&empty[st], (uint32_t)((tau / N - 1) & 1), dead, a.err);
+                if (tau >= N) wait_for(&empty[st], (uint32_t)((tau / N - 1) & 1), dead);
                 if (__any_sync(0xffffffffu, dead)) {
                     dead = true;
                     break;
@@ -871,7 +910,8 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
         // copies in flight (only after a timeout) land before the CTA exits
         if (lane == 0 && dead)
-            for (int k = max(0, tau - N); k < tau; ++k) mbar_wait_bounded(&full[k % N], (uint32_t)((k / N) & 1));
+#pragma unroll 1
+            for (int k = max(0, tau - N); k < tau; ++k) drain(&full[k % N], (uint32_t)((k / N) & 1));
     } else if (warp == kMmaWarp) {
         // ======================= Q K^T issuer =======================
         // Both issuers walk as whole warps (uniform registers) and one elected lane issues.
@@ -882,15 +922,17 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         uint32_t kph = 0, sph = 1;     // their phases (a buffer's first use waits for nothing)
         int d = 0;
         uint32_t dph = 0;
+#pragma unroll 1
         for (int p = 0;; ++p) {
-            wait_or_flag(&desc_full[d], dph, dead, a.err);
+            wait_for(&desc_full[d], dph, dead);
             const int n = dead ? 0 : descs[d].ntiles;
             if (n == 0) break;
-            wait_or_flag(&q_full[p & 1], (uint32_t)((p >> 1) & 1), dead, a.err);
+            wait_for(&q_full[p & 1], (uint32_t)((p >> 1) & 1), dead);
             const uint64_t qd = qd0 + (uint64_t)((uint32_t)(p & 1) * (uint32_t)(L::kQTile >> 4));
+#pragma unroll 1
             for (int j = 0; j < n; ++j) {
-                wait_or_flag(&k_full[st], kph, dead, a.err);
-                wait_or_flag(&o_done[sb], sph, dead, a.err);  // the P V that read the buffer before
+                wait_for(&k_full[st], kph, dead);
+                wait_for(&o_done[sb], sph, dead);  // the P V that read the buffer before
                 if (dead) break;
                 tc::fence_after();
                 const uint64_t kd = kd0 + (uint64_t)((uint32_t)st * (uint32_t)(L::kTile >> 4));
@@ -913,7 +955,7 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
         if (leader) tc::commit(&all_done[0]);
         __syncwarp();
-        mbar_wait_bounded(&all_done[0], 0u);
+        drain(&all_done[0], 0u);
     } else if (warp == kPvWarp) {
         // ======================= P V issuer =======================
         constexpr uint32_t idesc = tc::instr_desc(D, true);
@@ -926,14 +968,16 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         uint32_t vph = 0, sph = 0;
         int d = 0;
         uint32_t dph = 0;
+#pragma unroll 1
         for (int p = 0;; ++p) {
-            wait_or_flag(&desc_full[d], dph, dead, a.err);
+            wait_for(&desc_full[d], dph, dead);
             const int n = dead ? 0 : descs[d].ntiles;
             if (n == 0) break;
-            if (p > 0) wait_or_flag(o_free, (uint32_t)((p - 1) & 1), dead, a.err);  // the piece before's O has been read
+            if (p > 0) wait_for(o_free, (uint32_t)((p - 1) & 1), dead);  // the piece before's O has been read
+#pragma unroll 1
             for (int j = 0; j < n; ++j) {
-                wait_or_flag(&v_full[st], vph, dead, a.err);
-                wait_or_flag(&p_full[sb], sph, dead, a.err);
+                wait_for(&v_full[st], vph, dead);
+                wait_for(&p_full[sb], sph, dead);
                 if (dead) break;
                 tc::fence_after();
                 const uint64_t vd = vd0 + (uint64_t)((uint32_t)st * (uint32_t)(L::kTile >> 4));
@@ -956,7 +1000,7 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         // every product has completed before the tensor memory is freed
         if (leader) tc::commit(&all_done[1]);
         __syncwarp();
-        mbar_wait_bounded(&all_done[1], 0u);
+        drain(&all_done[1], 0u);
     } else if (warp < kEpiWarp) {
         // ======================= softmax =======================
         const int set = warp >> 2, wq = warp & 3;
@@ -966,9 +1010,10 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const uint32_t sp = trow + (uint32_t)(set * kTok), op = trow + kOBase;
         const int prev = set == 0 ? kSets - 1 : set - 1;  // the set of the tile before
         int tau0 = 0;
+#pragma unroll 1
         for (int p = 0; !dead; ++p) {
             const int d = p % kDescs;
-            if (!wait_or_flag(&desc_full[d], (uint32_t)((p / kDescs) & 1), dead, a.err)) break;
+            if (!wait_for(&desc_full[d], (uint32_t)((p / kDescs) & 1), dead)) break;
             const Piece &pc = descs[d];
             const int n = pc.ntiles, pre = pc.pre;
             if (n == 0) break;
@@ -987,9 +1032,10 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             bool any = false;
             int j = set - tau0 % kSets;
             if (j < 0) j += kSets;
+#pragma unroll 1
             for (; j < n; j += kSets) {
                 const int tau = tau0 + j, turn = tau / kSets;
-                wait_or_flag(&s_full[set], (uint32_t)(turn & 1), dead, a.err);
+                wait_for(&s_full[set], (uint32_t)(turn & 1), dead);
                 if (dead) break;
                 tc::fence_after();
                 const TileRec rec = recs[tau % kRecs];
@@ -1007,17 +1053,18 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (live_warp) {
                     softmax_tile<D, KIND>(sp, op, rec, a, rec.t0 < pre, st, ch, lane, dead);
                 } else if (KIND != kCap) {
-                    if (ch.before) wait_or_flag(ch.before, ch.parity, dead, a.err);
+                    if (ch.before) wait_for(ch.before, ch.parity, dead);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(ch.mine);
                 }
                 // V rows of keys that no row sees hold stale values, or none were loaded: zero weights must meet zeros
                 if (!rec.whole) {
                     const int st_v = tau % NV;
-                    wait_or_flag(&v_full[st_v], (uint32_t)((tau / NV) & 1), dead, a.err);
+                    wait_for(&v_full[st_v], (uint32_t)((tau / NV) & 1), dead);
                     if (!cr.sees(rec.t0 + rr) || ((rec.bad >> (rr >> a.bshift)) & 1u)) {  // a thread per key
                         const uint32_t row = v_s + (uint32_t)st_v * L::kTile + (rr >> a.bshift) * (H * 128 << a.bshift) +
                                              (rr & (B - 1)) * 128;
+#pragma unroll 4
                         for (int i = 0; i < 8 * H; ++i)
                             asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(row + (i >> 3) * (128 << a.bshift) +
                                                                                        ((i + lane) & 7) * 16),
@@ -1035,7 +1082,7 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             tau0 += n;
             // the piece's reference and sum of this set's tiles, for the epilogue
             const int f = p & 1;
-            if (p >= 2) wait_or_flag(&fin_empty[f], (uint32_t)((p / 2 - 1) & 1), dead, a.err);
+            if (p >= 2) wait_for(&fin_empty[f], (uint32_t)((p / 2 - 1) & 1), dead);
             fin_ml[(f * kSets + set) * kRows + rr] = make_float2(any ? st.m : -INFINITY, st.l);
             __syncwarp();
             if (lane == 0) {
@@ -1048,14 +1095,15 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const int wq = warp & 3, rr = wq * 32 + lane;
         const int64_t rel = ((int64_t)(rr / G) * a.num_heads + rr % G) * D;
         const uint32_t op = tmem + ((uint32_t)(wq * 32) << 16) + kOBase;
+#pragma unroll 1
         for (int p = 0; !dead; ++p) {
             const int d = p % kDescs, f = p & 1;
-            if (!wait_or_flag(&desc_full[d], (uint32_t)((p / kDescs) & 1), dead, a.err)) break;
+            if (!wait_for(&desc_full[d], (uint32_t)((p / kDescs) & 1), dead)) break;
             const Piece &pc = descs[d];
             if (pc.ntiles == 0) break;
             const int nrows = pc.nrows, slot = pc.slot;
             const int64_t orow = ((int64_t)pc.row0 * a.num_heads + pc.kvh * G) * D + rel;
-            wait_or_flag(&fin_full[f], (uint32_t)((p >> 1) & 1), dead, a.err);
+            wait_for(&fin_full[f], (uint32_t)((p >> 1) & 1), dead);
             float2 x[kSets];
 #pragma unroll
             for (int i = 0; i < kSets; ++i) x[i] = fin_ml[(f * kSets + i) * kRows + rr];
@@ -1068,7 +1116,7 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             for (int i = 0; i < kSets; ++i)  // (a set without a tile: l = 0)
                 l += x[i].x == -INFINITY || x[i].x == M ? x[i].y : x[i].y * ex2_approx(x[i].x - M);
             const float inv = l != 0.f ? 1.f / l : 0.f;
-            wait_or_flag(o_last, (uint32_t)(p & 1), dead, a.err);
+            wait_for(o_last, (uint32_t)(p & 1), dead);
             if (dead) break;
             tc::fence_after();
             const bool live = rr < nrows;
@@ -1078,32 +1126,32 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     float o[16];
                     ld16(op + (uint32_t)c, o);
                     tc::wait_ld();
-                    if (!live) continue;
                     if (slot < 0) {
                         uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow + c);
 #pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            dst[k] = make_uint4(pack_bf16x2(o[8 * k] * inv, o[8 * k + 1] * inv),
-                                                pack_bf16x2(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
-                                                pack_bf16x2(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
-                                                pack_bf16x2(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+                        for (int k = 0; k < 2; ++k) {
+                            const uint4 v = make_uint4(pack_bf16x2(o[8 * k] * inv, o[8 * k + 1] * inv),
+                                                       pack_bf16x2(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
+                                                       pack_bf16x2(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
+                                                       pack_bf16x2(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+                            if (live) dst[k] = v;
+                        }
                     } else {
                         float *dst = a.part_o + ((int64_t)slot * D + c) * kRows + rr;
 #pragma unroll
                         for (int k = 0; k < 16; ++k) dst[k * kRows] = o[k];
                     }
                 }
-                if (live && slot >= 0)
-                    reinterpret_cast<float2 *>(a.part_ml)[(int64_t)slot * kRows + rr] = make_float2(M, l);
+                if (slot >= 0) reinterpret_cast<float2 *>(a.part_ml)[(int64_t)slot * kRows + rr] = make_float2(M, l);
             }
             tc::fence_before();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(o_free);
-                mbar_arrive(&desc_empty[d]);
-            }
+            if (lane == 0) mbar_arrive(o_free);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&desc_empty[d]);
         }
     }
+    if (dead) flag_error(a.err, PKV_DEVERR_TIMEOUT);
     tc::fence_before();
     __syncthreads();
     if (warp == kMmaWarp) {
