@@ -6,7 +6,7 @@
 //     S = Q K^T (M 128 rows, N 128 keys, K head_dim)      scores, in tensor memory
 //     P = 2^(y(S) - m)                                     y: the score in base 2, capped and biased
 //     O += P V  (M 128, N head_dim, K 128 keys)
-// with a reference m and a sum l per row.  m is the first 16 keys' maximum, rounded
+// with a reference m and a sum l per row.  m is the first 32 keys' maximum, rounded
 // up to an integer, and moves only where a score passes it by more than kJump: what
 // was summed is then scaled by a power of two, which rounds nothing.
 //
@@ -24,7 +24,7 @@
 // t % 3, one O.  Two chains of 128 x 128 tiles with an O each left the tensor cores
 // idle between them (8 x 512 queries of 4096: 311 us; this form 255 to 270 us, with
 // the tensor pipe 49 % and the issue slots 54 % busy, at the board's power limit in a
-// long run).  What costs most is code size: the loops of a tile's 16-key blocks are
+// long run).  What costs most is code size: the loops over a tile are
 // rolled and their rare parts loops of their own; unrolled by two they took 6 to 13 %
 // longer.
 //
@@ -296,47 +296,63 @@ __device__ __forceinline__ float max_of(const float (&s)[N]) {
     return fmaxf(fmax3(m[0], m[1], m[2]), m[3]);
 }
 
-// The keys of block c (16 keys) of the tile at t0 that the row sees, as bits.
-__device__ __forceinline__ uint32_t seen16(const KeyRange &r, int t0, uint32_t bad, int bshift, int c) {
-    const int t = t0 + 16 * c;
+template <int N>
+__device__ __forceinline__ void ld_s(uint32_t taddr, float (&v)[N]) {
+    if constexpr (N == 32) tc::ld32(taddr, v);
+    else ld16(taddr, v);
+    tc::wait_ld();
+}
+
+// The keys of step c (N keys) of the tile at t0 that the row sees, as bits.
+template <int N>
+__device__ __forceinline__ uint32_t seen_bits(const KeyRange &r, int t0, uint32_t bad, int bshift, int c) {
+    const int t = t0 + N * c;
     uint32_t w = bit_range(r.lo - t, r.hi - t);
     if (r.pre > t) w |= bit_range(r.first - t, r.pre - t);
     if (bad) {
-        if ((bad >> (16 * c >> bshift)) & 1u) w &= ~0xffu;
-        if ((bad >> ((16 * c + 8) >> bshift)) & 1u) w &= ~0xff00u;
-    }
-    return w & 0xffffu;
-}
-
-__device__ __forceinline__ void mask16(float (&s)[16], uint32_t w) {
 #pragma unroll
-    for (int k = 0; k < 16; ++k) s[k] = (w >> k) & 1u ? s[k] : -INFINITY;
+        for (int i = 0; i < N; i += 8)
+            if ((bad >> ((N * c + i) >> bshift)) & 1u) w &= ~(0xffu << i);
+    }
+    return N == 32 ? w : w & 0xffffu;
+}
+template <int N>
+constexpr uint32_t kAllSeen = N == 32 ? 0xffffffffu : (1u << (N & 31)) - 1u;
+
+template <int N>
+__device__ __forceinline__ void mask_s(float (&s)[N], uint32_t w) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) s[k] = (w >> k) & 1u ? s[k] : -INFINITY;
 }
 
-__device__ __forceinline__ void no_weights16(uint32_t to) {
+template <int N>
+__device__ __forceinline__ void no_weights(uint32_t to) {
     const uint32_t z[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-    st8u(to, z);
+#pragma unroll
+    for (int i = 0; i < N / 2; i += 8) st8u(to + i, z);
 }
 
-// Raw products of 16 keys (at sp) -> scores in base 2 plus nm: c tanh(z) + nm, z = k1 s.  For |z| small in the whole warp
+// Raw products of N keys (at sp) -> scores in base 2 plus nm: c tanh(z) + nm, z = k1 s.  For |z| small in the whole warp
 // an odd polynomial (the cap's factors folded in on the host) on the FMA pipe, two keys an instruction: the exponential is
 // then the only special function of a score.  Else, in a loop to keep the code short,
 // tanh z = 1 - 2 / (1 + e^2z), good to 2^-21; the scores go back over S.
-__device__ __forceinline__ void cap_near(float (&s)[16], const RowsArgs &a, uint64_t nm2) {
+template <int N>
+__device__ __forceinline__ void cap_near(float (&s)[N], const RowsArgs &a, uint64_t nm2) {
     const uint64_t q0 = f32x2(a.near[0], a.near[0]), q1 = f32x2(a.near[1], a.near[1]);
     const uint64_t q2 = f32x2(a.near[2], a.near[2]), q3 = f32x2(a.near[3], a.near[3]);
 #pragma unroll
-    for (int k = 0; k < 16; k += 2) {
+    for (int k = 0; k < N; k += 2) {
         const uint64_t x = f32x2(s[k], s[k + 1]), u = mul_f32x2(x, x);
         const uint64_t y = fma_f32x2(fma_f32x2(fma_f32x2(q3, u, q2), u, q1), u, q0);
         f32x2_split(fma_f32x2(x, y, nm2), s[k], s[k + 1]);
     }
 }
 
-__device__ __forceinline__ void cap_far(float (&s)[16], uint32_t sp, const RowsArgs &a, float nm) {
+template <int N>
+__device__ __forceinline__ void cap_far(float (&s)[N], uint32_t sp, const RowsArgs &a, float nm) {
     const float z2 = 2.f * 1.44269504f * a.k1;
 #pragma unroll 1
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < N / 4; ++i) {
         float x[4];
         ld4(sp + 4 * i, x);
         tc::wait_ld();
@@ -345,38 +361,38 @@ __device__ __forceinline__ void cap_far(float (&s)[16], uint32_t sp, const RowsA
         st4(sp + 4 * i, x);
     }
     tc::wait_st();
-    ld16(sp, s);
-    tc::wait_ld();
+    ld_s(sp, s);
 }
 
-__device__ __forceinline__ void cap16(float (&s)[16], uint32_t sp, const RowsArgs &a, float nm, uint64_t nm2) {
+template <int N>
+__device__ __forceinline__ void cap_s(float (&s)[N], uint32_t sp, const RowsArgs &a, float nm, uint64_t nm2) {
     const float top = max_of<true>(s) * fabsf(a.k1);
     cap_near(s, a, nm2);
     if (__builtin_expect(__any_sync(0xffffffffu, top > kTanhNear), 0)) cap_far(s, sp, a, nm);
 }
 
-// Raw products of 16 keys at sp, the first `ahead` keys before the row's position -> scores in base 2 plus nm.  beyond: keys
+// Raw products of N keys at sp, the first `ahead` keys before the row's position -> scores in base 2 plus nm.  beyond: keys
 // past the position may be seen.
-template <int KIND>
-__device__ __forceinline__ void scores16(float (&s)[16], uint32_t sp, int ahead, float slope2, bool beyond, const RowsArgs &a, float nm) {
-    ld16(sp, s);
-    tc::wait_ld();
-    if constexpr (KIND == kCapBias) cap16(s, sp, a, 0.f, 0ull);
+template <int KIND, int N>
+__device__ __forceinline__ void scores(float (&s)[N], uint32_t sp, int ahead, float slope2, bool beyond, const RowsArgs &a, float nm) {
+    ld_s(sp, s);
+    if constexpr (KIND == kCapBias) cap_s(s, sp, a, 0.f, 0ull);
     const float f = KIND == kCapBias ? 1.f : a.k1;
     const uint64_t f2 = f32x2(f, f), nm2 = f32x2(nm, nm);
     if constexpr (KIND == kPlain) {
 #pragma unroll
-        for (int k = 0; k < 16; k += 2) f32x2_split(fma_f32x2(f32x2(s[k], s[k + 1]), f2, nm2), s[k], s[k + 1]);
+        for (int k = 0; k < N; k += 2) f32x2_split(fma_f32x2(f32x2(s[k], s[k + 1]), f2, nm2), s[k], s[k + 1]);
     } else {
         // -slope |ahead - k|, linear unless the position is inside: one FMA for the pair's bias, one for the score
         const float sl = beyond && ahead <= 0 ? -slope2 : slope2, b = fmaf(-sl, (float)ahead, nm);
-        if (__builtin_expect(beyond && __any_sync(0xffffffffu, ahead > 0 && ahead < 15), 0)) {
+        if (__builtin_expect(beyond && __any_sync(0xffffffffu, ahead > 0 && ahead < N - 1), 0)) {
             if (KIND == kCapBias) {  // capped scores over S
-                st16u(sp, reinterpret_cast<const uint32_t(&)[16]>(s));
+#pragma unroll
+                for (int i = 0; i < N; i += 4) st4(sp + i, reinterpret_cast<const float(&)[4]>(s[i]));
                 tc::wait_st();
             }
 #pragma unroll 1
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < N / 4; ++i) {
                 float x[4];
                 ld4(sp + 4 * i, x);
                 tc::wait_ld();
@@ -385,27 +401,30 @@ __device__ __forceinline__ void scores16(float (&s)[16], uint32_t sp, int ahead,
                 st4(sp + 4 * i, x);
             }
             tc::wait_st();
-            ld16(sp, s);
-            tc::wait_ld();
+            ld_s(sp, s);
             return;
         }
         const uint64_t b2 = f32x2(b, b), sl2 = f32x2(sl, sl);
 #pragma unroll
-        for (int k = 0; k < 16; k += 2)
+        for (int k = 0; k < N; k += 2)
             f32x2_split(fma_f32x2(f32x2(s[k], s[k + 1]), f2, fma_f32x2(sl2, f32x2((float)k, (float)(k + 1)), b2)), s[k], s[k + 1]);
     }
 }
 
-// Weights 2^s of 16 keys to P (bf16 pairs) at `to`, their sum to ls.
-__device__ __forceinline__ void weights16(const float (&s)[16], uint32_t to, uint64_t (&ls)[2]) {
-    uint32_t pk[8];
+// Weights 2^s of N keys to P (bf16 pairs) at `to`, their sum to ls.
+template <int N>
+__device__ __forceinline__ void weights(const float (&s)[N], uint32_t to, uint64_t (&ls)[2]) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const float e0 = ex2_approx(s[2 * k]), e1 = ex2_approx(s[2 * k + 1]);
-        pk[k] = pack_bf16x2(e0, e1);
-        ls[k & 1] = add_f32x2(ls[k & 1], f32x2(e0, e1));
+    for (int i = 0; i < N; i += 16) {
+        uint32_t pk[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float e0 = ex2_approx(s[i + 2 * k]), e1 = ex2_approx(s[i + 2 * k + 1]);
+            pk[k] = pack_bf16x2(e0, e1);
+            ls[k & 1] = add_f32x2(ls[k & 1], f32x2(e0, e1));
+        }
+        st8u(to + i / 2, pk);
     }
-    st8u(to, pk);
 }
 
 // The rows' reference over the tiles of a piece, handed from tile to tile.
@@ -442,12 +461,13 @@ __device__ __forceinline__ void rescale_weights(uint32_t to, int n, float f) {
     }
 }
 
-// One tile of one row, 16 keys at a time in loops that are not unrolled: the
-// warps of an SM sub-partition work at different places, and code of more than
-// some 2 KB a tile ran at the pace of its instruction fetches (6 to 10 cycles an
-// instruction).  S (raw products) at sp, P (bf16 pairs) back over its first 64
-// columns, always behind the reads.  beyond: some row may see keys past its
-// position (a prefix).  Blocks of 16 keys that no row of the warp sees are skipped.
+// One tile of one row, 32 keys at a time in loops that are not unrolled: more code
+// than that ran at the pace of its instruction fetches (all 128 keys unrolled: 6 to 10
+// cycles an instruction), and 16 keys at a time wait longer for their own results
+// (prompts of documents: 203 us, with 32 176 us).  S (raw products) at sp, P (bf16
+// pairs) back over its first 64 columns, always behind the reads.  beyond: some row
+// may see keys past its position (a prefix).  Steps that no row of the warp sees are
+// skipped.
 //
 // One pass: a score goes straight to its weight 2^(y - m), for the reference m that
 // the tiles before have left (or will, as far as is known when this one begins; the
@@ -468,32 +488,31 @@ __device__ __forceinline__ void softmax_tile(uint32_t sp, uint32_t op, const Til
     const int t0 = rec.t0;
     const bool full = rec.full != 0;
     uint64_t ls[2] = {0ull, 0ull};
-    float x[16];
+    constexpr int N = 32;  // keys a step
+    float x[N];
     if constexpr (KIND == kCap) {
         const float nm = -st.m;
         const uint64_t nm2 = f32x2(nm, nm);
         // (a loop for tiles that every row sees whole: the shorter, the faster)
         if (full) {
 #pragma unroll 1
-            for (int c = 0; c < kTok / 16; ++c) {
-                ld16(sp + 16 * c, x);
-                tc::wait_ld();
-                cap16(x, sp + 16 * c, a, nm, nm2);
-                weights16(x, sp + 8 * c, ls);
+            for (int c = 0; c < kTok / N; ++c) {
+                ld_s(sp + N * c, x);
+                cap_s(x, sp + N * c, a, nm, nm2);
+                weights(x, sp + N / 2 * c, ls);
             }
         } else {
 #pragma unroll 1
-            for (int c = 0; c < kTok / 16; ++c) {
-                const uint32_t w = seen16(st.r, t0, rec.bad, a.bshift, c);
+            for (int c = 0; c < kTok / N; ++c) {
+                const uint32_t w = seen_bits<N>(st.r, t0, rec.bad, a.bshift, c);
                 if (!__any_sync(0xffffffffu, w != 0u)) {
-                    no_weights16(sp + 8 * c);
+                    no_weights<N>(sp + N / 2 * c);
                     continue;
                 }
-                ld16(sp + 16 * c, x);
-                tc::wait_ld();
-                cap16(x, sp + 16 * c, a, nm, nm2);
-                if (__any_sync(0xffffffffu, w != 0xffffu)) mask16(x, w);
-                weights16(x, sp + 8 * c, ls);
+                ld_s(sp + N * c, x);
+                cap_s(x, sp + N * c, a, nm, nm2);
+                if (__any_sync(0xffffffffu, w != kAllSeen<N>)) mask_s(x, w);
+                weights(x, sp + N / 2 * c, ls);
             }
         }
     } else {
@@ -505,26 +524,26 @@ __device__ __forceinline__ void softmax_tile(uint32_t sp, uint32_t op, const Til
         }
         float nm = m == -INFINITY ? 0.f : -m, top = m == -INFINITY ? -INFINITY : kJump;
 #pragma unroll 1
-        for (int c = 0; c < kTok / 16; ++c) {
-            uint32_t w = 0xffffu;
+        for (int c = 0; c < kTok / N; ++c) {
+            uint32_t w = kAllSeen<N>;
             if (!full) {
-                w = seen16(st.r, t0, rec.bad, a.bshift, c);
+                w = seen_bits<N>(st.r, t0, rec.bad, a.bshift, c);
                 if (!__any_sync(0xffffffffu, w != 0u)) {
-                    no_weights16(sp + 8 * c);
+                    no_weights<N>(sp + N / 2 * c);
                     continue;
                 }
             }
-            scores16<KIND>(x, sp + 16 * c, st.p - t0 - 16 * c, st.slope2, beyond, a, nm);
-            if (!full) mask16(x, w);
+            scores<KIND>(x, sp + N * c, st.p - t0 - N * c, st.slope2, beyond, a, nm);
+            if (!full) mask_s(x, w);
             const float mc = max_of<false>(x);
             if (__builtin_expect(__any_sync(0xffffffffu, mc > top), 0)) {
                 const float up = mc > top ? ceilf(mc) : 0.f;  // relative to the reference so far
                 const float f = m == -INFINITY ? 1.f : ex2_approx(-up);  // (no weight so far but 0)
-                if (__any_sync(0xffffffffu, f != 1.f)) rescale_weights(sp, c, f);
+                if (__any_sync(0xffffffffu, f != 1.f)) rescale_weights(sp, N / 16 * c, f);
                 ls[0] = mul_f32x2(ls[0], f32x2(f, f));
                 ls[1] = mul_f32x2(ls[1], f32x2(f, f));
 #pragma unroll
-                for (int k = 0; k < 16; ++k) x[k] -= up;
+                for (int k = 0; k < N; ++k) x[k] -= up;
                 if (mc > top) {
                     m = up - nm;
                     nm = -m;
@@ -532,7 +551,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t sp, uint32_t op, const Til
                     set_hint(ch, m);
                 }
             }
-            weights16(x, sp + 8 * c, ls);
+            weights(x, sp + N / 2 * c, ls);
         }
         // the tile before's reference
         if (ch.before) wait_for(ch.before, ch.parity, dead);
