@@ -227,6 +227,7 @@ __device__ __forceinline__ void attend_bf16(const DecodeArgs &a, unsigned char *
     constexpr int kHalf = 16 * 128;
     const uint32_t ok = t.mask;
     if (ok != 0xffffu) {  // tokens that are not seen may hold anything: a zero weight must meet a zero
+#pragma unroll 1
         for (int e = lane; e < D / 64 * 16 * 8; e += 32) {
             const int r = (e >> 3) & 15;
             if (!((ok >> r) & 1u)) *reinterpret_cast<uint4 *>(sv + (e >> 7) * kHalf + r * 128 + (e & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
@@ -279,6 +280,7 @@ __device__ __forceinline__ void attend_fp8(const DecodeArgs &a, unsigned char *s
                                            const Slot &t, int pos, const Query<D> &q, Acc<D> &acc, int lane) {
     const uint32_t ok = t.mask;
     if (ok != 0xffffffffu) {
+#pragma unroll 1
         for (int e = lane; e < 32 * D / 16; e += 32) {
             const int r = e / (D / 16);
             if (!((ok >> r) & 1u)) *reinterpret_cast<uint4 *>(sv + r * D + (e % (D / 16)) * 16) = make_uint4(0u, 0u, 0u, 0u);
@@ -287,66 +289,68 @@ __device__ __forceinline__ void attend_fp8(const DecodeArgs &a, unsigned char *s
     }
     const int g = lane >> 2, tq = lane & 3, lr = lane & 7;
     const uint32_t ska = smem_u32(sk), sva = smem_u32(sv);
-    // S (heads x tokens): row g head g, columns 2tq, 2tq + 1 of eight tokens each
-    float sc[4][4];
+    const bool full = ok == 0xffffffffu;
+    // 16 tokens at a time: all 32 at once (720 instructions) were slower where pieces are short (64 sequences: 36 us, so 35)
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+        // S (heads x tokens): row g head g, columns 2tq, 2tq + 1 of eight tokens each
+        float sc[2][4];
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
-        sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
+        for (int n = 0; n < 2; ++n) {
+            sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
 #pragma unroll
-        for (int k = 0; k < D / 16; k += 4) {  // four 16-byte chunks of eight token rows at once
-            uint32_t x[4];
-            ldmatrix_x4(ska + code_chunk<D>(8 * n + lr, k + (lane >> 3)), x[0], x[1], x[2], x[3]);
+            for (int k = 0; k < D / 16; k += 4) {  // four 16-byte chunks of eight token rows at once
+                uint32_t x[4];
+                ldmatrix_x4(ska + code_chunk<D>(16 * h + 8 * n + lr, k + (lane >> 3)), x[0], x[1], x[2], x[3]);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t b0, b1;
-                e4m3x4_to_f16(x[c], b0, b1);
-                mma_f16_8816(sc[n], q.b[k + c][0], q.b[k + c][1], b0, b1);
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t b0, b1;
+                    e4m3x4_to_f16(x[c], b0, b1);
+                    mma_f16_8816(sc[n], q.b[k + c][0], q.b[k + c][1], b0, b1);
+                }
             }
         }
-    }
-    // head g, tokens 8n + 2tq + i: scores xs, and x with the value's exponent
-    const bool full = ok == 0xffffffffu;
-    const float b0 = -q.slope[0] * (float)(pos - t.t0 - 2 * tq);  // p >= t: no key past the query's position
-    float x[4][2], xs[4][2], mx = -INFINITY;
+        // head g, tokens 8n + 2tq + i: scores xs, and x with the value's exponent
+        const float b0 = -q.slope[0] * (float)(pos - t.t0 - 16 * h - 2 * tq);  // p >= t: no key past the query's position
+        const uint32_t okh = ok >> (16 * h);
+        float x[2][2], xs[2][2], mx = -INFINITY;
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
-        const uint32_t kb = *reinterpret_cast<const uint16_t *>(ss + 8 * n + 2 * tq);
-        const uint32_t vb = *reinterpret_cast<const uint16_t *>(ss + 32 + 8 * n + 2 * tq);
+        for (int n = 0; n < 2; ++n) {
+            const uint32_t kb = *reinterpret_cast<const uint16_t *>(ss + 16 * h + 8 * n + 2 * tq);
+            const uint32_t vb = *reinterpret_cast<const uint16_t *>(ss + 32 + 16 * h + 8 * n + 2 * tq);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float kf = __uint_as_float(i ? (kb & 0xff00u) << 15 : (kb & 0xffu) << 23);
-            const float ve = __uint_as_float(0x4b000000u | (i ? vb >> 8 : vb & 0xffu)) - 8388735.f;  // 2^23 + byte, less 2^23 + 127
-            float s = sc[n][i] * (q.f[0] * kf);
-            if (a.c2 > 0.f) s = a.c2 - 2.f * a.c2 * rcp_approx(1.f + ex2_approx(s));
-            if (a.s.slopes) s += fmaf(q.slope[0], (float)(8 * n + i), b0);
-            if (!full && !((ok >> (8 * n + 2 * tq + i)) & 1u)) s = -INFINITY;
-            xs[n][i] = s;
-            x[n][i] = s + ve;
-            if (!full && s == -INFINITY) x[n][i] = -INFINITY;  // the scale of a token that is not seen may be anything
-            mx = fmaxf(mx, x[n][i]);
+            for (int i = 0; i < 2; ++i) {
+                const float kf = __uint_as_float(i ? (kb & 0xff00u) << 15 : (kb & 0xffu) << 23);
+                const float ve = __uint_as_float(0x4b000000u | (i ? vb >> 8 : vb & 0xffu)) - 8388735.f;  // 2^23 + byte, less 2^23 + 127
+                float s = sc[n][i] * (q.f[0] * kf);
+                if (a.c2 > 0.f) s = a.c2 - 2.f * a.c2 * rcp_approx(1.f + ex2_approx(s));
+                if (a.s.slopes) s += fmaf(q.slope[0], (float)(8 * n + i), b0);
+                if (!full && !((okh >> (8 * n + 2 * tq + i)) & 1u)) s = -INFINITY;
+                xs[n][i] = s;
+                x[n][i] = s + ve;
+                if (!full && s == -INFINITY) x[n][i] = -INFINITY;  // the scale of a token that is not seen may be anything
+                mx = fmaxf(mx, x[n][i]);
+            }
         }
-    }
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    const float top = fmaxf(acc.m[0], mx), ref = top == -INFINITY ? 0.f : top;
-    if (__any_sync(0xffffffffu, top != acc.m[0])) {
-        const float f = ex2_approx(acc.m[0] - ref);
-        acc.l[0] *= f;
-        acc.scale(__shfl_sync(0xffffffffu, f, 8 * tq), __shfl_sync(0xffffffffu, f, 8 * tq + 4));
-    }
-    acc.m[0] = top;
-    const float up = 14.f - ref;  // weights up to 2^14
-    uint32_t p[4];
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float top = fmaxf(acc.m[0], mx), ref = top == -INFINITY ? 0.f : top;
+        if (__any_sync(0xffffffffu, top != acc.m[0])) {
+            const float f = ex2_approx(acc.m[0] - ref);
+            acc.l[0] *= f;
+            acc.scale(__shfl_sync(0xffffffffu, f, 8 * tq), __shfl_sync(0xffffffffu, f, 8 * tq + 4));
+        }
+        acc.m[0] = top;
+        const float up = 14.f - ref;  // weights up to 2^14
+        uint32_t p[2];
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
-        p[n] = pack_f16x2(ex2_approx(x[n][0] + up), ex2_approx(x[n][1] + up));
-        acc.l[0] += ex2_approx(xs[n][0] + up) + ex2_approx(xs[n][1] + up);  // w 2^-ve
-    }
-    // V^T fragments from token rows: lane (g, tq) reads D / 8 consecutive entries of tokens 2tq, 2tq + 1, 2tq + 8, 2tq + 9
-    // and pairs two tokens' bytes; fragment i holds entries D/8 g + 2i (rows g) and + 1 (rows g + 8)
-    constexpr int W = D / 32;  // 32-bit words of a lane's entries
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
+        for (int n = 0; n < 2; ++n) {
+            p[n] = pack_f16x2(ex2_approx(x[n][0] + up), ex2_approx(x[n][1] + up));
+            acc.l[0] += ex2_approx(xs[n][0] + up) + ex2_approx(xs[n][1] + up);  // w 2^-ve
+        }
+        // V^T fragments from token rows: lane (g, tq) reads D / 8 consecutive entries of tokens 2tq, 2tq + 1, 2tq + 8, 2tq + 9
+        // and pairs two tokens' bytes; fragment i holds entries D/8 g + 2i (rows g) and + 1 (rows g + 8)
+        constexpr int W = D / 32;  // 32-bit words of a lane's entries
         uint32_t v[4][W];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -367,9 +371,17 @@ __device__ __forceinline__ void attend_fp8(const DecodeArgs &a, unsigned char *s
                 uint32_t a0, a1, a2, a3;
                 e4m3x4_to_f16(__byte_perm(v[0][w], v[1][w], u ? 0x7362 : 0x5140), a0, a1);
                 e4m3x4_to_f16(__byte_perm(v[2][w], v[3][w], u ? 0x7362 : 0x5140), a2, a3);
-                mma_f16_16816(acc.o[2 * w + u], a0, a1, a2, a3, p[2 * h], p[2 * h + 1]);
+                mma_f16_16816(acc.o[2 * w + u], a0, a1, a2, a3, p[0], p[1]);
             }
     }
+}
+
+__device__ __forceinline__ bool wait_tile(uint64_t *bar, uint32_t parity) {
+    uint32_t i = 0;
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity))
+        if (++i == kWaitLimit) return false;
+    return true;
 }
 
 // head_dim entry of acc.o[i][j] (rows g for j < 2, g + 8 above)
@@ -402,6 +414,7 @@ scored_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     }
     __syncthreads();
     int my_max = 0;
+#pragma unroll 1
     for (int base = 0; base < S; base += kNW * 32) {
         const int s = base + threadIdx.x;
         int v = 0;
@@ -451,6 +464,7 @@ scored_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
 
     auto seq_of = [&](int t) {  // the sequence that holds laid-out tile t: largest with prefix[seq] <= t
         int x = 0, y = S;
+#pragma unroll 1
         while (y - x > 1) {
             const int mid = (x + y) >> 1;
             if (prefix[mid] <= t) x = mid; else y = mid;
@@ -495,8 +509,10 @@ scored_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     }
     grid_dependency_wait();
     // sequences that see nothing have no tile: their rows are zeroed by the merge
+#pragma unroll 1
     for (int s = blockIdx.x; s < S; s += gridDim.x)
         if (prefix[s + 1] == prefix[s])
+#pragma unroll 1
             for (int h = threadIdx.x; h < Hkv; h += kNW * 32) a.segs[(int64_t)s * Hkv + h] = make_int2(0, -1);
     if (lo >= hi) return;
 
@@ -521,6 +537,7 @@ scored_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 if (y >= 0) tma_load_2d((isv ? dv : dk) + (uint32_t)(sb * boxh) * D, isv ? &tm_v : &tm_k, b, 0, y);
             } else if (lane < 8) {
                 if (y >= 0)
+#pragma unroll 1
                     for (int c = 0; c < boxh; c += 16)
                         cp_async16(smem_u32(scales + buf * T_::kScales) + isv * TT + sb * boxh + c, (isv ? a.v_scales : a.k_scales) + y + c);
                 asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(b) : "memory");
@@ -551,6 +568,7 @@ scored_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     load_query<D, F8>(a, seq, kvh, lane, q);
     bool dead = false;
     Acc<D> acc;
+#pragma unroll 1
     for (int k = 0; k < ntiles;) {
         // one piece: the segment's tiles in this share
         const int pa = lo + k, pb = min(hi, seg0 + segn), kend = pb - lo;
@@ -566,9 +584,10 @@ scored_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             load_query<D, F8>(a, seq, kvh, lane, qn);
         }
         acc.reset();
+#pragma unroll 1
         for (; k < kend; ++k) {
             const int buf = k % kNS;
-            if (!dead && !mbar_wait_bounded(&bars[buf], (uint32_t)((k / kNS) & 1))) {
+            if (!dead && !wait_tile(&bars[buf], (uint32_t)((k / kNS) & 1))) {
                 if (lane == 0) flag_error(a.err, PKV_DEVERR_TIMEOUT);
                 dead = true;
             }
