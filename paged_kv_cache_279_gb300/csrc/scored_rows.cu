@@ -106,11 +106,13 @@ struct Layout {
     static constexpr int vring = kring + NK * kTile;
     static constexpr int fin_ml = vring + NV * kTile;   // float2 [2][kSets][kRows]: (m, l) of a piece's rows, pieces in turn
     static constexpr int mref = fin_ml + 2 * kSets * kRows * 8;  // float [kRows]: the rows' reference after the latest tile
-    static constexpr int hint = mref + kRows * 4;  // uint64_t [kRows]
-    static constexpr int desc = hint + kRows * 8;
+    // float [4][kRows]: the first tile's, pieces in turn (three would do: the tile that last reads piece p - 3's is the third
+    // before piece p's first at the latest, and done when that one begins)
+    static constexpr int start = mref + kRows * 4;
+    static constexpr int desc = start + 4 * kRows * 4;
     static constexpr int recs = (desc + kDescs * (int)sizeof(Piece) + 15) & ~15;
     static constexpr int bars = recs + kRecs * (int)sizeof(TileRec);
-    static constexpr int kBars = 2 * NK + 2 * NV + 3 * kSets + 4 * kSets + 4 + 2 + 4 + 2 * kDescs + 2;
+    static constexpr int kBars = 2 * NK + 2 * NV + 3 * kSets + 4 * kSets + 4 + 2 + 4 + 16 + 2 * kDescs + 2;
     static constexpr int misc = bars + kBars * 8;       // TMEM address, scan scratch
     static constexpr int total = misc + 128;
     static_assert(total <= 227 * 1024, "shared memory per CTA");
@@ -320,9 +322,9 @@ template <int N>
 constexpr uint32_t kAllSeen = N == 32 ? 0xffffffffu : (1u << (N & 31)) - 1u;
 
 template <int N>
-__device__ __forceinline__ void mask_s(float (&s)[N], uint32_t w) {
+__device__ __forceinline__ void mask_s(float (&s)[N], uint32_t w, float hidden = -INFINITY) {
 #pragma unroll
-    for (int k = 0; k < N; ++k) s[k] = (w >> k) & 1u ? s[k] : -INFINITY;
+    for (int k = 0; k < N; ++k) s[k] = (w >> k) & 1u ? s[k] : hidden;
 }
 
 template <int N>
@@ -374,9 +376,13 @@ __device__ __forceinline__ void cap_s(float (&s)[N], uint32_t sp, const RowsArgs
 // Raw products of N keys at sp, the first `ahead` keys before the row's position -> scores in base 2 plus nm.  beyond: keys
 // past the position may be seen.
 template <int KIND, int N>
-__device__ __forceinline__ void scores(float (&s)[N], uint32_t sp, int ahead, float slope2, bool beyond, const RowsArgs &a, float nm) {
+__device__ __forceinline__ void scores(float (&s)[N], uint32_t sp, int ahead, float slope2, bool beyond, const RowsArgs &a, float nm,
+                                       bool full, uint32_t w) {
     ld_s(sp, s);
-    if constexpr (KIND == kCapBias) cap_s(s, sp, a, 0.f, 0ull);
+    if constexpr (KIND == kCapBias) {
+        if (!full) mask_s(s, w, 0.f);  // what is hidden has no say in how the others are capped
+        cap_s(s, sp, a, 0.f, 0ull);
+    }
     const float f = KIND == kCapBias ? 1.f : a.k1;
     const uint64_t f2 = f32x2(f, f), nm2 = f32x2(nm, nm);
     if constexpr (KIND == kPlain) {
@@ -411,7 +417,8 @@ __device__ __forceinline__ void scores(float (&s)[N], uint32_t sp, int ahead, fl
     }
 }
 
-// Weights 2^s of N keys to P (bf16 pairs) at `to`, their sum to ls.
+// Weights 2^s of N keys to P (bf16 pairs) at `to`, the sum of the rounded ones to ls: a row that one key dominates gets its
+// value exactly.
 template <int N>
 __device__ __forceinline__ void weights(const float (&s)[N], uint32_t to, uint64_t (&ls)[2]) {
 #pragma unroll
@@ -419,9 +426,8 @@ __device__ __forceinline__ void weights(const float (&s)[N], uint32_t to, uint64
         uint32_t pk[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const float e0 = ex2_approx(s[i + 2 * k]), e1 = ex2_approx(s[i + 2 * k + 1]);
-            pk[k] = pack_bf16x2(e0, e1);
-            ls[k & 1] = add_f32x2(ls[k & 1], f32x2(e0, e1));
+            pk[k] = pack_bf16x2(ex2_approx(s[i + 2 * k]), ex2_approx(s[i + 2 * k + 1]));
+            ls[k & 1] = add_f32x2(ls[k & 1], f32x2(bf16x2_lo(pk[k]), bf16x2_hi(pk[k])));
         }
         st8u(to + i / 2, pk);
     }
@@ -430,19 +436,16 @@ __device__ __forceinline__ void weights(const float (&s)[N], uint32_t to, uint64
 // The rows' reference over the tiles of a piece, handed from tile to tile.
 struct Chain {
     float *mref;        // this row's after the tile before
-    uint64_t *hint;     // (a reference of this row, the piece it belongs to): may be read while it is written
+    float *start;       // this row's reference as the piece's first tile began
+    uint64_t *started;  // that is known
+    uint32_t start_parity;
     uint64_t *before;   // the tile before has left its reference (nullptr: the CTA's first tile)
     uint64_t *mine;     // this tile has
     uint64_t *done;     // the tile before's product is complete
     uint32_t parity;    // of both
-    int piece;
     bool first;         // the piece's first tile
+    bool begun;         // this set has had a tile of the piece: its state has a reference
 };
-
-__device__ __forceinline__ void set_hint(const Chain &ch, float m) {
-    const uint64_t v = (uint64_t)(uint32_t)ch.piece << 32 | __float_as_uint(m);
-    asm volatile("st.relaxed.cta.shared.b64 [%0], %1;" ::"r"(smem_u32(ch.hint)), "l"(v) : "memory");
-}
 
 // The first 16 n weights at `to` times f, a power of two.
 __device__ __forceinline__ void rescale_weights(uint32_t to, int n, float f) {
@@ -469,9 +472,9 @@ __device__ __forceinline__ void rescale_weights(uint32_t to, int n, float f) {
 // may see keys past its position (a prefix).  Steps that no row of the warp sees are
 // skipped.
 //
-// One pass: a score goes straight to its weight 2^(y - m), for the reference m that
-// the tiles before have left (or will, as far as is known when this one begins; the
-// piece's first tile takes the maximum of its first 16 seen keys).  Where a score
+// One pass: a score goes straight to its weight 2^(y - m).  m is the reference that
+// this set's tile before left, for its first tile of a piece the one that the piece's
+// first tile found in its first step, the maximum of the keys seen there.  Where a score
 // passes m by more than kJump, m moves to it, and the tile's earlier weights are
 // scaled.  At the end the tile before's final reference is awaited and the larger
 // of the two taken: this tile's weights or O (complete up to the tile before) are
@@ -510,18 +513,28 @@ __device__ __forceinline__ void softmax_tile(uint32_t sp, uint32_t op, const Til
                     continue;
                 }
                 ld_s(sp + N * c, x);
+                mask_s(x, w, 0.f);  // what is hidden has no say in how the others are capped
                 cap_s(x, sp + N * c, a, nm, nm2);
-                if (__any_sync(0xffffffffu, w != kAllSeen<N>)) mask_s(x, w);
+                mask_s(x, w);
                 weights(x, sp + N / 2 * c, ls);
             }
         }
     } else {
-        float m;
-        {
-            uint64_t h;
-            asm volatile("ld.relaxed.cta.shared.b64 %0, [%1];" : "=l"(h) : "r"(smem_u32(ch.hint)) : "memory");
-            m = (int)(h >> 32) == ch.piece ? __uint_as_float((uint32_t)h) : -INFINITY;
+        // what a tile begins with depends on no other's pace, so results do not either
+        float m = -INFINITY;
+        bool unknown = ch.first;
+        if (ch.begun) {
+            m = st.m;
+        } else if (!ch.first) {
+            wait_for(ch.started, ch.start_parity, dead);
+            m = *ch.start;
         }
+        auto publish = [&] {
+            *ch.start = m;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(ch.started);
+            unknown = false;
+        };
         float nm = m == -INFINITY ? 0.f : -m, top = m == -INFINITY ? -INFINITY : kJump;
 #pragma unroll 1
         for (int c = 0; c < kTok / N; ++c) {
@@ -533,7 +546,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t sp, uint32_t op, const Til
                     continue;
                 }
             }
-            scores<KIND>(x, sp + N * c, st.p - t0 - N * c, st.slope2, beyond, a, nm);
+            scores<KIND>(x, sp + N * c, st.p - t0 - N * c, st.slope2, beyond, a, nm, full, w);
             if (!full) mask_s(x, w);
             const float mc = max_of<false>(x);
             if (__builtin_expect(__any_sync(0xffffffffu, mc > top), 0)) {
@@ -548,11 +561,12 @@ __device__ __forceinline__ void softmax_tile(uint32_t sp, uint32_t op, const Til
                     m = up - nm;
                     nm = -m;
                     top = kJump;
-                    set_hint(ch, m);
                 }
+                if (unknown) publish();
             }
             weights(x, sp + N / 2 * c, ls);
         }
+        if (unknown) publish();
         // the tile before's reference
         if (ch.before) wait_for(ch.before, ch.parity, dead);
         const float old = ch.first ? -INFINITY : *ch.mref, mf = fmaxf(old, m);
@@ -561,7 +575,6 @@ __device__ __forceinline__ void softmax_tile(uint32_t sp, uint32_t op, const Til
         if (lane == 0) mbar_arrive(ch.mine);
         const float f = m == -INFINITY || m == mf ? 1.f : ex2_approx(m - mf);
         if (__any_sync(0xffffffffu, f != 1.f)) {
-            set_hint(ch, mf);
             rescale_weights(sp, kTok / 16, f);
             ls[0] = mul_f32x2(ls[0], f32x2(f, f));
             ls[1] = mul_f32x2(ls[1], f32x2(f, f));
@@ -606,7 +619,7 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     TileRec *recs = reinterpret_cast<TileRec *>(smem + L::recs);
     float2 *fin_ml = reinterpret_cast<float2 *>(smem + L::fin_ml);
     float *mref = reinterpret_cast<float *>(smem + L::mref);
-    uint64_t *hint = reinterpret_cast<uint64_t *>(smem + L::hint);
+    float *start_ref = reinterpret_cast<float *>(smem + L::start);
     uint64_t *k_full = reinterpret_cast<uint64_t *>(smem + L::bars), *k_empty = k_full + NK;
     uint64_t *v_full = k_empty + NK, *v_empty = v_full + NV;
     uint64_t *s_full = v_empty + NV, *p_full = s_full + kSets, *o_done = p_full + kSets;  // per set
@@ -614,7 +627,8 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     uint64_t *q_full = m_full + 4 * kSets, *q_empty = q_full + 2;                        // per query tile
     uint64_t *o_last = q_empty + 2, *o_free = o_last + 1;
     uint64_t *fin_full = o_free + 1, *fin_empty = fin_full + 2;                          // pieces in turn
-    uint64_t *desc_full = fin_empty + 2, *desc_empty = desc_full + kDescs, *all_done = desc_empty + kDescs;
+    uint64_t *started = fin_empty + 2;                                                   // [piece % 4][4]: per warp
+    uint64_t *desc_full = started + 16, *desc_empty = desc_full + kDescs, *all_done = desc_empty + kDescs;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::misc);
     int *scratch = reinterpret_cast<int *>(smem + L::misc + 16);  // [22] warp sums, carry, found sequence, its start
     constexpr int kCarry = kThreads / 32, kFound = kCarry + 1, kStart = kCarry + 2;
@@ -697,7 +711,10 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         scratch[kStart] = start;
     }
 
-    if (threadIdx.x < kRows) hint[threadIdx.x] = ~0ull;  // no piece's
+    // rows of the query tiles that no box fills: what they hold must not differ from run to run
+    for (int i = a.per_ctx * G * 8 + threadIdx.x; i < kRows * 8; i += kThreads)
+        for (int t = 0; t < 2 * H; ++t) *reinterpret_cast<uint4 *>(smem + L::q + t * (kRows * 128) + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async();
     if (threadIdx.x == 0) {
 #pragma unroll 1
         for (int i = 0; i < NK; ++i) {
@@ -717,6 +734,8 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
 #pragma unroll 1
         for (int i = 0; i < 4 * kSets; ++i) mbar_init(&m_full[i], 1);
+#pragma unroll 1
+        for (int i = 0; i < 16; ++i) mbar_init(&started[i], 1);
 #pragma unroll 1
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 1);
@@ -1062,8 +1081,10 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 const int bturn = set == 0 ? turn - 1 : turn;
                 Chain ch;
                 ch.mref = mref + rr;
-                ch.hint = hint + rr;
-                ch.piece = p;
+                ch.start = start_ref + (p & 3) * kRows + rr;
+                ch.started = &started[(p & 3) * 4 + wq];
+                ch.start_parity = (uint32_t)((p >> 2) & 1);
+                ch.begun = any;
                 ch.before = tau > 0 ? &m_full[prev * 4 + wq] : nullptr;
                 ch.mine = &m_full[set * 4 + wq];
                 ch.done = &o_done[prev];
@@ -1074,11 +1095,17 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 } else if (KIND != kCap) {
                     if (ch.before) wait_for(ch.before, ch.parity, dead);
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(ch.mine);
+                    if (lane == 0) {
+                        if (ch.first) mbar_arrive(ch.started);
+                        mbar_arrive(ch.mine);
+                    }
                 }
                 // V rows of keys that no row sees hold stale values, or none were loaded: zero weights must meet zeros
                 if (!rec.whole) {
-                    const int st_v = tau % NV;
+                    // A parity tells a stage's use from the one before it only, and P V is known to be complete up to tile
+                    // tau - kSets: the stage's use before has to be over first (it does not wait for this tile).
+                    const int st_v = tau % NV, used = tau - NV;
+                    if (NV < kSets && used >= 0) wait_for(&o_done[used % kSets], (uint32_t)((used / kSets) & 1), dead);
                     wait_for(&v_full[st_v], (uint32_t)((tau / NV) & 1), dead);
                     if (!cr.sees(rec.t0 + rr) || ((rec.bad >> (rr >> a.bshift)) & 1u)) {  // a thread per key
                         const uint32_t row = v_s + (uint32_t)st_v * L::kTile + (rr >> a.bshift) * (H * 128 << a.bshift) +

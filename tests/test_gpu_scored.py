@@ -175,6 +175,33 @@ def test_multi_scores_far_apart(opt, D):
     c.check(run(c))
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("opt", [dict(softcap=30.0), dict(alibi=True), {}], ids=["cap", "alibi", "plain"])
+def test_multi_few_queries_of_many_sequences(opt, D):
+    """Every SM streams whole contexts of few rows, V behind K: right, and the same bits in every run."""
+    r = np.random.default_rng(5)
+    c = Case([int(x) for x in np.exp(r.uniform(np.log(64), np.log(2048), 64))], 32, 8, D, 16, qlens=[5] * 64, qmul=1.0, **opt)
+    pools = c.pools()
+    first = run(c, pools)
+    c.check(first)
+    for _ in range(5):
+        assert torch.equal(bits(run(c, pools)), bits(first))
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "rows", "multi"])
+def test_a_single_key_gives_its_value(kind):
+    """A row that sees one key gets that key's value, rounded to the output's type and no more."""
+    c = Case([300, 77, 1], 8, 2, qlens=[40, 77, 1] if kind == "multi" else None, window=1, softcap=20.0, rows=kind == "rows",
+             dtype=torch.float32 if kind == "f32" else torch.bfloat16)
+    got = run(c).float().cpu()
+    for s, L in enumerate(c.lens):
+        for i in range(int(c.q_starts[s]), int(c.q_starts[s + 1])):
+            p = L - int(c.q_starts[s + 1]) + i
+            want = c.vs[s][p].repeat_interleave(c.Hq // c.Hkv, 0).to(c.dtype).float()
+            tol = 2.0 ** -22 * want.abs() if kind == "f32" else 0.0 * want
+            assert bool(((got[i] - want).abs() <= tol).all()), (s, p)
+
+
 def test_multi_scores_that_grow_and_shrink():
     """Keys whose scores rise, or fall, steadily along the context: every tile has a larger maximum than the one before it."""
     for sign in (1.0, -1.0):
