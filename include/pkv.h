@@ -425,8 +425,8 @@ PKV_EXPORT pkv_status paged_attention_decode_scored_fp8_rows(
  * every sequence (prefill, chunks of one, verification of drafted tokens);
  * queries, q_starts and max_q_len as for paged_attention_multi_token (bf16).
  * key_starts must not decrease over a sequence's queries (documents stand in
- * order): a query whose entry is below an earlier one's may miss keys between
- * the two.
+ * order): where a query's entry is below an earlier one's, it is unspecified
+ * which of the keys between the two the sequence's queries see.
  */
 PKV_EXPORT size_t paged_attention_multi_token_scored_workspace_size(int num_q_tokens, int num_heads, int head_dim,
                                                                     int max_seq_len);
