@@ -83,6 +83,18 @@ __device__ __forceinline__ int prefix_of(const ScoreArgs &s, int seq, int len) {
     return s.prefix_lens ? min(max(0, s.prefix_lens[seq]), len) : 0;
 }
 
+// Caps above kWideCap (in base 2; 50 in base e) take tanh of small z by its series, so that a wide cap costs the scores that
+// are far below it no accuracy: tanh z = z (1 - z^2/3 + 2 z^4/15 - 17 z^6/315), off by 3.3e-7 of it at kTanhSmall.
+constexpr float kWideCap = 73.f, kTanhSmall = 0.25f;
+constexpr double kTanhSeries[4] = {1.0, -1.0 / 3.0, 2.0 / 15.0, -17.0 / 315.0};
+
+// Beyond this a cap changes no score below 1e12 by 1e-4, and larger ones are further apart than that: none is applied, which
+// keeps the factors made of it within float32's range.
+constexpr float kNoCap = 1e20f;
+
+// A host-side constant as float, kept finite (0 times it stays 0).
+inline float finite_float(double x) { return (float)(x > 3e38 ? 3e38 : x < -3e38 ? -3e38 : x); }
+
 __device__ __forceinline__ float rcp_approx(float x) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

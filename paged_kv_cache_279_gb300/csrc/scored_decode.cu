@@ -183,11 +183,21 @@ __device__ __forceinline__ void load_query(const DecodeArgs &a, int seq, int kvh
     }
 }
 
+// c tanh z, y = 2 z log2 e: c - 2 c / (1 + e^2z), good to 2^-21 of c.
+__device__ __forceinline__ float cap_score(float y, float c2) {
+    float x = c2 - 2.f * c2 * rcp_approx(1.f + ex2_approx(y));
+    if (c2 > kWideCap) {
+        const float z = y * 0.34657359f, u = z * z;
+        constexpr float s1 = (float)kTanhSeries[1], s2 = (float)kTanhSeries[2], s3 = (float)kTanhSeries[3];
+        if (fabsf(z) < kTanhSmall) x = c2 * (z * fmaf(fmaf(fmaf(s3, u, s2), u, s1), u, 1.f));
+    }
+    return x;
+}
+
 // Raw product -> score in base 2: `f` the head's factor, away = p - t.
 __device__ __forceinline__ float score(float s, float f, float c2, float slope, float away) {
     float x = s * f;
-    // c tanh z = c - 2 c / (1 + e^2z), good to 2^-21 of c
-    if (c2 > 0.f) x = c2 - 2.f * c2 * rcp_approx(1.f + ex2_approx(x));
+    if (c2 > 0.f) x = cap_score(x, c2);
     return fmaf(-slope, away, x);
 }
 
@@ -323,7 +333,7 @@ __device__ __forceinline__ void attend_fp8(const DecodeArgs &a, unsigned char *s
                 const float kf = __uint_as_float(i ? (kb & 0xff00u) << 15 : (kb & 0xffu) << 23);
                 const float ve = __uint_as_float(0x4b000000u | (i ? vb >> 8 : vb & 0xffu)) - 8388735.f;  // 2^23 + byte, less 2^23 + 127
                 float s = sc[n][i] * (q.f[0] * kf);
-                if (a.c2 > 0.f) s = a.c2 - 2.f * a.c2 * rcp_approx(1.f + ex2_approx(s));
+                if (a.c2 > 0.f) s = cap_score(s, a.c2);
                 if (a.s.slopes) s += fmaf(q.slope[0], (float)(8 * n + i), b0);
                 if (!full && !((okh >> (8 * n + 2 * tq + i)) & 1u)) s = -INFINITY;
                 xs[n][i] = s;
@@ -780,12 +790,13 @@ pkv_status run_decode(const Args &args, int head_dim, void *workspace, size_t wo
         return PKV_ERR_INVALID;
     DecodeArgs a{};
     static_cast<Args &>(a) = args;
+    if (a.s.softcap > kNoCap) a.s.softcap = 0.f;
     const bool fp8 = a.k_scales != nullptr;
     // laid-out tiles are counted in 32-bit integers
     if ((int64_t)a.num_seqs * a.num_kv_heads * ((a.max_seq_len + 15) / 16 + 4) > INT32_MAX / 2) return PKV_ERR_UNSUPPORTED;
     const double log2e = 1.4426950408889634;
-    a.c2 = (float)(a.s.softcap * log2e);
-    a.k1 = (float)(a.s.softcap > 0.f ? 2.0 * a.s.scale / a.s.softcap * log2e : a.s.scale * log2e);
+    a.c2 = finite_float(a.s.softcap * log2e);
+    a.k1 = finite_float(a.s.softcap > 0.f ? 2.0 * a.s.scale / a.s.softcap * log2e : a.s.scale * log2e);
     a.bshift = a.block_size == 8 ? 3 : a.block_size == 16 ? 4 : 5;
     const WsLayout lay((int64_t)a.num_seqs * a.num_kv_heads, a.group, head_dim);
     unsigned char *ws = static_cast<unsigned char *>(workspace);

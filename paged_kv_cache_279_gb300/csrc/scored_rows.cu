@@ -58,7 +58,7 @@ constexpr int kRecs = 8;    // tile records (more than the K producers can be ah
 constexpr int kCharge = 2;  // virtual tiles of a context
 constexpr int kMinShare = kCharge + 1;
 constexpr float kJump = 32.f;  // a row's reference moves where a score passes it by more (weights stay below 2^kJump)
-constexpr float kMaxC2 = 73.f;  // softcap * log2 e up to which capped scores take a fixed reference (cap 50)
+constexpr float kMaxC2 = kWideCap;  // softcap * log2 e up to which capped scores take a fixed reference (cap 50)
 constexpr uint32_t kTmemCols = 512, kOBase = kSets * kTok;
 constexpr int kMaxCtas = 160;   // partial slots in the workspace: two per CTA
 constexpr int kMergeRows = 32;  // rows per CTA of the merge kernel
@@ -69,7 +69,8 @@ struct RowsArgs : Args {
     float k1;       // plain, biased: scale * log2 e; capped: scale / softcap
     float c2;       // capped: softcap * log2 e
     float m0;       // capped: the reference
-    float near[4];  // capped: c2 tanh(k1 s) = s * sum near[i] s^2i for |k1 s| <= kTanhNear
+    float near[4];  // capped: c2 tanh(k1 s) = s * sum near[i] s^2i for |k1 s| <= near_max (kTanhNear; wide caps: kTanhSmall)
+    float near_max;
     float *part_o;  // [2 kMaxCtas][D][kRows]: columns of rows
     float *part_ml; // [2 kMaxCtas][kRows][2]
     int4 *merges;   // [kMaxCtas]: (parts, first query row, rows, kv head) of the context begun and cut in that share
@@ -370,7 +371,7 @@ template <int N>
 __device__ __forceinline__ void cap_s(float (&s)[N], uint32_t sp, const RowsArgs &a, float nm, uint64_t nm2) {
     const float top = max_of<true>(s) * fabsf(a.k1);
     cap_near(s, a, nm2);
-    if (__builtin_expect(__any_sync(0xffffffffu, top > kTanhNear), 0)) cap_far(s, sp, a, nm);
+    if (__builtin_expect(__any_sync(0xffffffffu, top > a.near_max), 0)) cap_far(s, sp, a, nm);
 }
 
 // Raw products of N keys at sp, the first `ahead` keys before the row's position -> scores in base 2 plus nm.  beyond: keys
@@ -1319,6 +1320,7 @@ pkv_status run_rows(const Args &args, int head_dim, void *workspace, size_t work
     if (!workspace || workspace_bytes < lay.total || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return PKV_ERR_INVALID;
     RowsArgs a{};
     static_cast<Args &>(a) = args;
+    if (a.s.softcap > kNoCap) a.s.softcap = 0.f;
     a.per_ctx = kRows / a.group;
     a.bshift = a.block_size == 8 ? 3 : a.block_size == 16 ? 4 : 5;
     const int64_t blocks = ((int64_t)a.max_q_len + a.per_ctx - 1) / a.per_ctx;
@@ -1328,11 +1330,13 @@ pkv_status run_rows(const Args &args, int head_dim, void *workspace, size_t work
     if ((int64_t)a.num_seqs * a.num_kv_heads > INT32_MAX / 2 / (blocks * ((a.max_seq_len + kTok - 1) / kTok + 1 + kCharge)))
         return PKV_ERR_UNSUPPORTED;
     const double log2e = 1.4426950408889634;
-    a.k1 = a.s.softcap > 0.f ? (float)((double)a.s.scale / a.s.softcap) : (float)(a.s.scale * log2e);
-    a.c2 = (float)(a.s.softcap * log2e);
+    a.k1 = finite_float(a.s.softcap > 0.f ? (double)a.s.scale / a.s.softcap : a.s.scale * log2e);
+    a.c2 = finite_float(a.s.softcap * log2e);
     a.m0 = 0.25f * a.c2;
     double f = a.s.softcap * log2e * a.k1;
-    for (int i = 0; i < 4; ++i, f *= (double)a.k1 * a.k1) a.near[i] = (float)(kTanh3[i] * f);
+    const bool wide = a.c2 > kWideCap;
+    a.near_max = wide ? kTanhSmall : kTanhNear;
+    for (int i = 0; i < 4; ++i, f *= (double)a.k1 * a.k1) a.near[i] = finite_float((wide ? kTanhSeries : kTanh3)[i] * f);
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     a.part_o = reinterpret_cast<float *>(ws + lay.o);
     a.part_ml = reinterpret_cast<float *>(ws + lay.ml);

@@ -316,6 +316,27 @@ def test_any_finite_scale(kind, scale):
     c.check(run(c))
 
 
+@pytest.mark.parametrize("cap", [60.0, 1e3, 1e6, 3e38])
+@pytest.mark.parametrize("kind", ["f32", "bf16", "rows", "multi"])
+def test_wide_caps_cost_no_accuracy(kind, cap):
+    """Scores far below their cap: the bound is the uncapped one, plus 2^-19 of a score (z >= 1/4: 2^-21 of the cap, at most
+    four times the score; below it the series' 2^-21 and its arithmetic)."""
+    c = Case([77, 300], qlens=[9, 130] if kind == "multi" else None, rows=kind == "rows", softcap=cap, window=90,
+             dtype=torch.float32 if kind == "f32" else torch.bfloat16)
+    got = run(c).double().cpu().numpy()
+    ref, _ = c.reference()
+    c.softcap = 0.0
+    _, tol = c.reference()
+    rep, at = c.Hq // c.Hkv, 0
+    for s, L in enumerate(c.lens):
+        n = int(c.q_starts[s + 1] - c.q_starts[s])
+        q, k = (x.double().abs().numpy() for x in (c.q[at:at + n], c.ks[s]))
+        a = c.scale * max(float((q[:, h] @ k[:, h // rep].T).max()) for h in range(c.Hq))
+        tol[at:at + n] += 4 * 2.0 ** -19 * a * c.vs[s].double().abs().max().item()
+        at += n
+    assert np.all(np.abs(got - ref) <= tol)
+
+
 @pytest.mark.parametrize("kind", ["f32", "bf16", "rows", "multi"])
 def test_negative_and_large_slopes(kind):
     c = Case([200, 1000], qlens=[9, 150] if kind == "multi" else None, rows=kind == "rows", alibi=True,
