@@ -55,7 +55,7 @@ constexpr int kEpiWarp = 4 * kSets, kMmaWarp = 16, kKWarp = 17, kVWarp = 19, kSc
 constexpr int kThreads = 22 * 32;
 constexpr int kDescs = 6;   // piece descriptors in flight
 constexpr int kRecs = 8;    // tile records (more than the K producers can be ahead of the softmax)
-constexpr int kCharge = 2;  // virtual tiles of a context
+constexpr int kCharge = 1;  // virtual tiles of a context (prompts of documents: 1: 170 us, 2: 180, 3: 194)
 constexpr int kMinShare = kCharge + 1;
 constexpr float kJump = 32.f;  // a row's reference moves where a score passes it by more (weights stay below 2^kJump)
 constexpr float kMaxC2 = kWideCap;  // softcap * log2 e up to which capped scores take a fixed reference (cap 50)
@@ -418,19 +418,31 @@ __device__ __forceinline__ void scores(float (&s)[N], uint32_t sp, int ahead, fl
     }
 }
 
+// a += low half, b += high half of a pair of bf16 (mixed adds: 2 % of the call less than widening first).
+__device__ __forceinline__ void add_bf16x2(float &a, float &b, uint32_t v) {
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tadd.f32.bf16 %0, lo, %0;\n\tadd.f32.bf16 %1, hi, %1;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "r"(v));
+}
+
 // Weights 2^s of N keys to P (bf16 pairs) at `to`, the sum of the rounded ones to ls: a row that one key dominates gets its
 // value exactly.
 template <int N>
 __device__ __forceinline__ void weights(const float (&s)[N], uint32_t to, uint64_t (&ls)[2]) {
 #pragma unroll
     for (int i = 0; i < N; i += 16) {
+        float lf[4];
+        f32x2_split(ls[0], lf[0], lf[1]);
+        f32x2_split(ls[1], lf[2], lf[3]);
         uint32_t pk[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             pk[k] = pack_bf16x2(ex2_approx(s[i + 2 * k]), ex2_approx(s[i + 2 * k + 1]));
-            ls[k & 1] = add_f32x2(ls[k & 1], f32x2(bf16x2_lo(pk[k]), bf16x2_hi(pk[k])));
+            add_bf16x2(lf[2 * (k & 1)], lf[2 * (k & 1) + 1], pk[k]);
         }
         st8u(to + i / 2, pk);
+        ls[0] = f32x2(lf[0], lf[1]);
+        ls[1] = f32x2(lf[2], lf[3]);
     }
 }
 
