@@ -22,6 +22,7 @@ is no CPU or PyTorch fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional, Sequence
 
 import numpy as np
@@ -344,6 +345,7 @@ def paged_attention_decode_grouped(out, q, k_cache, v_cache, block_tables, seq_l
 
 
 _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _device_of(t, name: str) -> int:
@@ -354,6 +356,11 @@ def _device_of(t, name: str) -> int:
 
 def _ptr(t, name: str, dtype, dev: int) -> int:
     """Address of a contiguous tensor of that type on device `dev`."""
+    try:
+        if t.get_device() == dev and t.dtype is dtype and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.get_device() != dev:
@@ -362,9 +369,7 @@ def _ptr(t, name: str, dtype, dev: int) -> int:
         raise ValueError(f"{name} is on {t.device}, other tensors of the call on cuda:{dev}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _opt_ptr(t, name: str, dtype, dev: int):
@@ -378,12 +383,17 @@ def _stream_on(stream, dev: int) -> int:
     return _stream(stream)
 
 
+@functools.lru_cache(maxsize=None)
+def _cuda_device(dev: int) -> torch.device:
+    return torch.device("cuda", dev)
+
+
 def _scratch(workspace, need: int, stream, dev: int):
     """(address, bytes) of the caller's workspace, or of one taken here."""
     if workspace is None:
         if need == 0:
             return None, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", dev))
+        workspace = torch.empty(need, dtype=torch.uint8, device=_cuda_device(dev))
         if stream is not None:  # its memory must outlive the work on that stream, not on the current one
             workspace.record_stream(stream if hasattr(stream, "cuda_stream") else
                                     torch.cuda.ExternalStream(int(stream), device=dev))
@@ -395,7 +405,7 @@ def _scratch(workspace, need: int, stream, dev: int):
 
 def _run_on(dev: int, what: str, fn, args) -> None:
     """Call the library with the tensors' device current."""
-    if dev == torch.cuda.current_device():
+    if dev == _current_device():
         st = fn(*args)
     else:
         with torch.cuda.device(dev):
