@@ -414,6 +414,29 @@ def _run_on(dev: int, what: str, fn, args) -> None:
         raise PkvError(st, what)
 
 
+_raw_alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
+_raw_free = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", None)
+
+
+def _run_with_scratch(dev: int, what: str, fn, size_fn, sizes, head, workspace, tail, stream) -> None:
+    """_run_on with a workspace, the caller's or, for this call, one of size_fn(*sizes) bytes: head, its address, its bytes,
+    tail (whose last entry is the stream)."""
+    if workspace is None and _raw_alloc is not None and _raw_free is not None and dev == _current_device():
+        # the allocator's block of the call's stream, without a tensor around it (5 us less)
+        need = size_fn(*sizes)
+        ws = _raw_alloc(need, tail[-1]) if need else None
+        try:
+            st = fn(*head, ws, need, *tail)
+        finally:
+            if ws is not None:
+                _raw_free(ws)  # work on that stream may reuse it, after this call's
+        if st != PKV_OK:
+            raise PkvError(st, what)
+        return
+    ws, n = _scratch(workspace, 0 if workspace is not None else size_fn(*sizes), stream, dev)
+    _run_on(dev, what, fn, (*head, ws, n, *tail))
+
+
 def _fp8_rows_call(what: str, k, v, k_cache, v_cache, k_scales, v_scales, slot_mapping, stream) -> None:
     NB, Hkv, B, D = k_cache.shape
     T = k.shape[0]
@@ -494,16 +517,15 @@ def paged_attention_decode_scored(out, q, k_cache, v_cache, block_tables, seq_le
         raise ValueError("k_new/v_new must be [S, Hkv, D]")
     lib, code, dt, i32 = _lib.load(), _dtype_code(q), q.dtype, torch.int32
     dev = _device_of(q, "q")
-    ws, ws_bytes = _scratch(workspace, 0 if workspace is not None else
-                            lib.paged_attention_decode_scored_workspace_size(S, Hq, D, int(max_seq_len)), stream, dev)
-    _run_on(dev, "paged_attention_decode_scored", lib.paged_attention_decode_scored, (
+    _run_with_scratch(dev, "paged_attention_decode_scored", lib.paged_attention_decode_scored,
+                      lib.paged_attention_decode_scored_workspace_size, (S, Hq, D, int(max_seq_len)), (
         _ptr(out, "out", dt, dev), _ptr(q, "q", dt, dev), _opt_ptr(k_new, "k_new", dt, dev),
         _opt_ptr(v_new, "v_new", dt, dev), _ptr(k_cache, "k_cache", dt, dev), _ptr(v_cache, "v_cache", dt, dev),
         _ptr(block_tables, "block_tables", i32, dev), _ptr(seq_lens, "seq_lens", i32, dev), S, Hq, Hkv, D, B, maxb, NB,
         int(max_seq_len), float(scale), float(softcap), _opt_ptr(alibi_slopes, "alibi_slopes", torch.float32, dev),
         min(int(window), 2 ** 31 - 1),
-        _opt_ptr(prefix_lens, "prefix_lens", i32, dev), _opt_ptr(key_starts, "key_starts", i32, dev), ws, ws_bytes, code,
-        _stream_on(stream, dev)))
+        _opt_ptr(prefix_lens, "prefix_lens", i32, dev), _opt_ptr(key_starts, "key_starts", i32, dev)), workspace,
+        (code, _stream_on(stream, dev)), stream)
     return out
 
 
@@ -521,16 +543,15 @@ def paged_attention_decode_scored_fp8_rows(out, q, k_cache, v_cache, k_scales, v
         raise ValueError("scales must be [NB, Hkv, B]")
     lib, bf, u8, i32 = _lib.load(), torch.bfloat16, torch.uint8, torch.int32
     dev = _device_of(q, "q")
-    ws, ws_bytes = _scratch(workspace, 0 if workspace is not None else
-                            lib.paged_attention_decode_scored_workspace_size(S, Hq, D, int(max_seq_len)), stream, dev)
-    _run_on(dev, "paged_attention_decode_scored_fp8_rows", lib.paged_attention_decode_scored_fp8_rows, (
+    _run_with_scratch(dev, "paged_attention_decode_scored_fp8_rows", lib.paged_attention_decode_scored_fp8_rows,
+                      lib.paged_attention_decode_scored_workspace_size, (S, Hq, D, int(max_seq_len)), (
         _ptr(out, "out", bf, dev), _ptr(q, "q", bf, dev), _ptr(k_cache, "k_cache", u8, dev),
         _ptr(v_cache, "v_cache", u8, dev), _ptr(k_scales, "k_scales", u8, dev), _ptr(v_scales, "v_scales", u8, dev),
         _ptr(block_tables, "block_tables", i32, dev), _ptr(seq_lens, "seq_lens", i32, dev), S, Hq, Hkv, D, B, maxb, NB,
         int(max_seq_len), float(scale), float(softcap), _opt_ptr(alibi_slopes, "alibi_slopes", torch.float32, dev),
         min(int(window), 2 ** 31 - 1),
-        _opt_ptr(prefix_lens, "prefix_lens", i32, dev), _opt_ptr(key_starts, "key_starts", i32, dev), ws, ws_bytes,
-        _stream_on(stream, dev)))
+        _opt_ptr(prefix_lens, "prefix_lens", i32, dev), _opt_ptr(key_starts, "key_starts", i32, dev)), workspace,
+        (_stream_on(stream, dev),), stream)
     return out
 
 
@@ -549,16 +570,15 @@ def paged_attention_multi_token_scored(out, q, k_cache, v_cache, block_tables, s
         raise ValueError("q_starts must be [S + 1]")
     lib, bf, i32 = _lib.load(), torch.bfloat16, torch.int32
     dev = _device_of(q, "q")
-    ws, ws_bytes = _scratch(workspace, 0 if workspace is not None else
-                            lib.paged_attention_multi_token_scored_workspace_size(T, Hq, D, int(max_seq_len)), stream, dev)
-    _run_on(dev, "paged_attention_multi_token_scored", lib.paged_attention_multi_token_scored, (
+    _run_with_scratch(dev, "paged_attention_multi_token_scored", lib.paged_attention_multi_token_scored,
+                      lib.paged_attention_multi_token_scored_workspace_size, (T, Hq, D, int(max_seq_len)), (
         _ptr(out, "out", bf, dev), _ptr(q, "q", bf, dev), _ptr(k_cache, "k_cache", bf, dev),
         _ptr(v_cache, "v_cache", bf, dev), _ptr(block_tables, "block_tables", i32, dev),
         _ptr(seq_lens, "seq_lens", i32, dev), _ptr(q_starts, "q_starts", i32, dev), S, T, Hq, Hkv, D, B, maxb, NB,
         int(max_q_len), int(max_seq_len), float(scale), float(softcap),
         _opt_ptr(alibi_slopes, "alibi_slopes", torch.float32, dev), min(int(window), 2 ** 31 - 1),
-        _opt_ptr(prefix_lens, "prefix_lens", i32, dev), _opt_ptr(key_starts, "key_starts", i32, dev), ws, ws_bytes,
-        _stream_on(stream, dev)))
+        _opt_ptr(prefix_lens, "prefix_lens", i32, dev), _opt_ptr(key_starts, "key_starts", i32, dev)), workspace,
+        (_stream_on(stream, dev),), stream)
     return out
 
 

@@ -410,6 +410,36 @@ def test_captured_and_replayed(kind):
         c.check(out, f"replay {it}")
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16", "rows", "multi"])
+def test_captured_without_a_workspace(kind):
+    """The call's own workspace inside a CUDA graph, beside eager calls and allocations on the stream of the replays."""
+    c = Case([900, 33, 1200], qlens=[60, 3, 9] if kind == "multi" else None, rows=kind == "rows", softcap=15.0, alibi=True,
+             dtype=torch.float32 if kind == "f32" else torch.bfloat16)
+    pools = c.pools()
+    want = run(c, pools)
+    q, out, args = c.q.cuda(), torch.full_like(want, float("nan")), c.device_args()
+    f = (pkv.paged_attention_multi_token_scored if kind == "multi" else
+         pkv.paged_attention_decode_scored_fp8_rows if c.rows else pkv.paged_attention_decode_scored)
+    call = dict(pools, **args, scale=c.scale, max_seq_len=1200,
+                **(dict(q_starts=torch.from_numpy(c.q_starts).cuda(), max_q_len=60) if kind == "multi" else {}))
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        f(out, q, **call)
+        s.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            for _ in range(2):
+                f(out, q, **call)
+        for _ in range(3):
+            out.fill_(float("nan"))
+            junk = torch.randn(1 << 22, device="cuda")
+            g.replay()
+            again = f(torch.empty_like(out), q, **call)
+            junk.mul_(2.0)
+            assert torch.equal(bits(out), bits(want)) and torch.equal(bits(again), bits(want))
+    torch.cuda.synchronize()
+
+
 @pytest.mark.parametrize("kind", ["bf16", "rows", "multi"])
 def test_two_calls_on_two_streams(kind):
     kw = dict(qlens=[150, 90, 7] if kind == "multi" else None, rows=kind == "rows", softcap=20.0)
