@@ -653,8 +653,6 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
     }
-    grid_dependency_wait();
-    grid_launch_dependents();
     if ((smem_u32(smem) & 1023u) != 0u) {  // swizzled tiles need it; never expected
         if (threadIdx.x == 0) flag_error(a.err, PKV_DEVERR_TIMEOUT);
         return;
@@ -695,9 +693,7 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
             if (lane == 31) scratch[warp] = x;
             __syncthreads();
-            int before = scratch[kCarry];
-#pragma unroll 1
-            for (int w = 0; w < warp; ++w) before += scratch[w];
+            const int before = scratch[kCarry] + (int)__reduce_add_sync(0xffffffffu, lane < warp ? (unsigned)scratch[lane] : 0u);
             const int end = before + x;
             start = end - v;
             if (round == 1 && v > 0 && my_s0 >= start && my_s0 < end) {
@@ -712,6 +708,10 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             T = scratch[kCarry];
             shares = Shares(T, gridDim.x);
             __syncthreads();  // every thread has the total before the next round clears it
+            // So far only lengths, starts and prefixes were read, which no kernel of the library writes: this may run under
+            // the previous kernel's tail.  What follows may not.
+            grid_dependency_wait();
+            grid_launch_dependents();
             if (threadIdx.x == 0) a.merges[blockIdx.x] = make_int4(0, 0, 0, 0);
             if (T == 0 || (int)blockIdx.x >= shares.n) return;
             my_s0 = shares.begin(blockIdx.x);
