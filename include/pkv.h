@@ -20,10 +20,10 @@
  *   - Kernels are launched with programmatic dependent launch: a kernel may
  *     start while the previous kernel on the stream finishes if that kernel
  *     triggers its dependents early (griddepcontrol.launch_dependents), and
- *     waits for it before touching its results.  The decode kernels read their
- *     inputs (queries, block tables, lengths) before that wait, so a kernel of
- *     the caller that triggers early must not write those inputs after its
- *     trigger.  Kernels that do not trigger early (the usual case) are waited
+ *     waits for it before touching its results.  The attention kernels read
+ *     inputs (queries, block tables, lengths, query starts, prefix lengths,
+ *     document starts) before that wait, so a kernel of the caller that
+ *     triggers early must not write those inputs after its trigger.  Kernels that do not trigger early (the usual case) are waited
  *     for in full, as without programmatic launch.
  *   - Arguments are checked on the host before any launch; a bad argument
  *     returns PKV_ERR_INVALID (or PKV_ERR_UNSUPPORTED for a valid but
