@@ -185,19 +185,19 @@ __device__ __forceinline__ void load_query(const DecodeArgs &a, int seq, int kvh
 
 // c tanh z, y = 2 z log2 e: c - 2 c / (1 + e^2z), good to 2^-21 of c.
 __device__ __forceinline__ float cap_score(float y, float c2) {
-    float x = c2 - 2.f * c2 * rcp_approx(1.f + ex2_approx(y));
-    if (c2 > kWideCap) {
-        const float z = y * 0.34657359f, u = z * z;
-        constexpr float s1 = (float)kTanhSeries[1], s2 = (float)kTanhSeries[2], s3 = (float)kTanhSeries[3];
-        if (fabsf(z) < kTanhSmall) x = c2 * (z * fmaf(fmaf(fmaf(s3, u, s2), u, s1), u, 1.f));
-    }
-    return x;
+    return c2 - 2.f * c2 * rcp_approx(1.f + ex2_approx(y));
+}
+// The same with the series for small z.
+__device__ __noinline__ float cap_score_wide(float y, float c2) {
+    const float z = y * 0.34657359f, u = z * z;
+    constexpr float s1 = (float)kTanhSeries[1], s2 = (float)kTanhSeries[2], s3 = (float)kTanhSeries[3];
+    return fabsf(z) < kTanhSmall ? c2 * (z * fmaf(fmaf(fmaf(s3, u, s2), u, s1), u, 1.f)) : cap_score(y, c2);
 }
 
 // Raw product -> score in base 2: `f` the head's factor, away = p - t.
 __device__ __forceinline__ float score(float s, float f, float c2, float slope, float away) {
     float x = s * f;
-    if (c2 > 0.f) x = cap_score(x, c2);
+    if (c2 > 0.f) x = c2 > kWideCap ? cap_score_wide(x, c2) : cap_score(x, c2);
     return fmaf(-slope, away, x);
 }
 
@@ -333,7 +333,7 @@ __device__ __forceinline__ void attend_fp8(const DecodeArgs &a, unsigned char *s
                 const float kf = __uint_as_float(i ? (kb & 0xff00u) << 15 : (kb & 0xffu) << 23);
                 const float ve = __uint_as_float(0x4b000000u | (i ? vb >> 8 : vb & 0xffu)) - 8388735.f;  // 2^23 + byte, less 2^23 + 127
                 float s = sc[n][i] * (q.f[0] * kf);
-                if (a.c2 > 0.f) s = cap_score(s, a.c2);
+                if (a.c2 > 0.f) s = a.c2 > kWideCap ? cap_score_wide(s, a.c2) : cap_score(s, a.c2);
                 if (a.s.slopes) s += fmaf(q.slope[0], (float)(8 * n + i), b0);
                 if (!full && !((okh >> (8 * n + 2 * tq + i)) & 1u)) s = -INFINITY;
                 xs[n][i] = s;
