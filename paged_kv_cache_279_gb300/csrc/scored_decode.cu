@@ -21,7 +21,9 @@
 // two, were no faster: 920 instructions a tile against 720.)  A key's scale 2^ke
 // multiplies its scores.  A value's scale 2^ve goes into the weight, w = 2^(x +
 // ve - m + 14) with m the maximum of x + ve, so that w <= 2^14 uses f16's range
-// whatever the scales are; l sums w 2^-ve, and out = o / l as before.
+// whatever the scales are; l sums w 2^-ve, and out = o / l as before.  Scales below
+// 2^-80 (zero rows: 2^-100) count as that in m: an addend of l is then at most 2^94,
+// and no number of keys takes l out of float32's range.
 #include <algorithm>
 #include <atomic>
 #include <climits>
@@ -95,6 +97,13 @@ __device__ __forceinline__ SegTiles load_seg(const DecodeArgs &a, int s) {
     const int raw = a.seq_lens[s];
     const int pre = a.s.prefix_lens ? a.s.prefix_lens[s] : 0, ks = a.s.key_starts ? a.s.key_starts[s] : 0;
     return seg_tiles<TT>(a, s, raw, pre, ks);
+}
+
+constexpr float kLeastExp = -80.f;  // of a value's scale in a row-scaled reference
+
+// l 2^d, d <= 0, also where 2^d is below float32's range (l: up to 2^125, where V rows of the least scale came first).
+__device__ __forceinline__ float lower_sum(float l, float d) {
+    return l * ex2_approx(fmaxf(d, -100.f)) * ex2_approx(fminf(d + 100.f, 0.f));
 }
 
 __device__ __forceinline__ uint32_t range_bits(int a, int b) {  // bits [a, b) of 32, any integers
@@ -339,7 +348,7 @@ __device__ __forceinline__ void attend_fp8(const DecodeArgs &a, unsigned char *s
                 xs[n][i] = s;
                 x[n][i] = s + ve;
                 if (!full && s == -INFINITY) x[n][i] = -INFINITY;  // the scale of a token that is not seen may be anything
-                mx = fmaxf(mx, x[n][i]);
+                mx = fmaxf(mx, s + fmaxf(ve, kLeastExp));
             }
         }
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
@@ -347,7 +356,7 @@ __device__ __forceinline__ void attend_fp8(const DecodeArgs &a, unsigned char *s
         const float top = fmaxf(acc.m[0], mx), ref = top == -INFINITY ? 0.f : top;
         if (__any_sync(0xffffffffu, top != acc.m[0])) {
             const float f = ex2_approx(acc.m[0] - ref);
-            acc.l[0] *= f;
+            acc.l[0] = lower_sum(acc.l[0], acc.m[0] - ref);
             acc.scale(__shfl_sync(0xffffffffu, f, 8 * tq), __shfl_sync(0xffffffffu, f, 8 * tq + 4));
         }
         acc.m[0] = top;
@@ -666,7 +675,7 @@ scored_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
 // One warp per (sequence, query head): the partial states of a segment that was
 // cut, merged in order (part 0 is its first warp's last piece, part j the first
 // piece of warp w0 + j); zero rows where no key is seen.
-template <int D>
+template <int D, bool F8>
 __global__ void __launch_bounds__(128) scored_decode_merge_kernel(const __grid_constant__ DecodeArgs a) {
     // Not earlier: the next call's CTAs would take their places while this kernel's wait beside the attention kernel's last
     // ones, and end up two on some SMs (8 x 16000 tokens FP8: 58 -> 71 us).
@@ -700,7 +709,7 @@ __global__ void __launch_bounds__(128) scored_decode_merge_kernel(const __grid_c
 #pragma unroll
         for (int u = 0; u < U; ++u) mx = fmaxf(mx, x[u].x);
         const float f = M == -INFINITY ? 0.f : ex2_approx(M - mx);
-        L *= f;
+        L = F8 ? lower_sum(L, M - mx) : L * f;
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] *= f;
         M = mx;
@@ -708,7 +717,7 @@ __global__ void __launch_bounds__(128) scored_decode_merge_kernel(const __grid_c
         for (int u = 0; u < U; ++u) {
             const float w = x[u].x == -INFINITY ? 0.f : ex2_approx(x[u].x - M);
             if (j0 + u >= seg.y) continue;
-            L += x[u].y * w;
+            L += F8 ? lower_sum(x[u].y, x[u].x - M) : x[u].y * w;
 #pragma unroll
             for (int e = 0; e < E; ++e) o[e] = w != 0.f ? fmaf(w, v[u][e], o[e]) : o[e];
         }
@@ -772,8 +781,8 @@ pkv_status launch(const DecodeArgs &a, cudaStream_t st) {
         return PKV_ERR_CUDA;
     pkv_status rc = launch_pdl(kern, dim3((unsigned)grid), dim3(kNW * 32), smem, st, mk, mv, a);
     if (rc == PKV_OK)
-        rc = launch_pdl(scored_decode_merge_kernel<D>, dim3((unsigned)(((int64_t)a.num_seqs * a.num_heads + 3) / 4)), dim3(128), 0,
-                        st, a);
+        rc = launch_pdl(scored_decode_merge_kernel<D, F8>, dim3((unsigned)(((int64_t)a.num_seqs * a.num_heads + 3) / 4)), dim3(128),
+                        0, st, a);
     return rc;
 }
 

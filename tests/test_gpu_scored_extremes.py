@@ -1,0 +1,56 @@
+"""Scored attention at the ends of its ranges: V rows of very different sizes, wide caps, extreme scales."""
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_279_gb300 as pkv
+from oracle import fp8_rows
+from scored_cases import Case
+from test_gpu_scored import run
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _no_errors():
+    pkv.read_device_errors(clear=True)
+    yield
+    assert pkv.read_device_errors(clear=True) == 0
+
+
+def _rows_case(n, scores, sizes):
+    """One row-scaled FP8 context of n tokens: q.k is scores[t], V rows are normal times sizes[t]."""
+    c = Case([n], 2, 1, 64, 16, rows=True, scale=1.0)
+    c.q[:] = 0
+    c.q[..., 0] = 1.0
+    k = np.zeros((n, 1, 64), np.float32)
+    k[:, 0, 0] = scores
+    v = (np.random.default_rng(8).standard_normal((n, 1, 64)) * np.asarray(sizes, np.float64)[:, None, None]).astype(np.float32)
+    c.codes = [(fp8_rows.quantise_rows(k), fp8_rows.quantise_rows(v))]
+    c.ks, c.vs = ([torch.from_numpy(fp8_rows.row_values(*p))] for p in c.codes[0])
+    return c
+
+
+@pytest.mark.parametrize("apart", [0.0, -20.75, 20.75])
+@pytest.mark.parametrize("small", [0.0, 2.0 ** -97], ids=["zero", "tiny"])
+def test_rows_long_runs_of_small_values(small, apart):
+    """Half of a long context has V rows of zeros (or of about 2^-97), whose scale is the least there is: the sum of the
+    weights stays finite whatever the order of the halves."""
+    n = 40000
+    first = np.arange(n) < n // 2
+    for head in (first, ~first):
+        c = _rows_case(n, np.where(head, apart, 0.0), np.where(head, small, 1.0))
+        c.check(run(c))
+
+
+@pytest.mark.parametrize("large", [2.0 ** 30, 2.0 ** 60, 2.0 ** 110])
+@pytest.mark.parametrize("n", [60, 300, 5000])
+def test_rows_zeros_beside_large_values(n, large):
+    """Zero rows keep their part of the sum when rows up to 2^200 times the least scale follow or precede them."""
+    first = np.arange(n) < n // 2
+    for head in (first, ~first):
+        c = _rows_case(n, np.zeros(n), np.where(head, 0.0, large))
+        c.check(run(c))
+    # everything tiny: a row of any size keeps its precision
+    c = _rows_case(n, np.linspace(0, 3, n), np.full(n, 2.0 ** -97))
+    c.check(run(c))
