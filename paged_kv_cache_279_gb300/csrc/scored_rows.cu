@@ -338,7 +338,9 @@ __device__ __forceinline__ void no_weights(uint32_t to) {
 // Raw products of N keys (at sp) -> scores in base 2 plus nm: c tanh(z) + nm, z = k1 s.  For |z| small in the whole warp
 // an odd polynomial (the cap's factors folded in on the host) on the FMA pipe, two keys an instruction: the exponential is
 // then the only special function of a score.  Else, in a loop to keep the code short,
-// tanh z = 1 - 2 / (1 + e^2z), good to 2^-21; the scores go back over S.
+// tanh z = 1 - 2 / (1 + e^2z), good to 2^-21; the scores go back over S.  Under a wide cap
+// (WIDE: there may be one) small z take the series there too: what other rows reach must not
+// cost them accuracy.
 template <int N>
 __device__ __forceinline__ void cap_near(float (&s)[N], const RowsArgs &a, uint64_t nm2) {
     const uint64_t q0 = f32x2(a.near[0], a.near[0]), q1 = f32x2(a.near[1], a.near[1]);
@@ -351,27 +353,36 @@ __device__ __forceinline__ void cap_near(float (&s)[N], const RowsArgs &a, uint6
     }
 }
 
-template <int N>
+template <bool WIDE, int N>
 __device__ __forceinline__ void cap_far(float (&s)[N], uint32_t sp, const RowsArgs &a, float nm) {
-    const float z2 = 2.f * 1.44269504f * a.k1;
+    const float z2 = 2.f * 1.44269504f * a.k1, small = WIDE && a.c2 > kWideCap ? kTanhSmall : 0.f;
+    constexpr float s1 = (float)kTanhSeries[1], s2 = (float)kTanhSeries[2], s3 = (float)kTanhSeries[3];
 #pragma unroll 1
     for (int i = 0; i < N / 4; ++i) {
         float x[4];
         ld4(sp + 4 * i, x);
         tc::wait_ld();
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x[k] = (a.c2 + nm) - (2.f * a.c2) * rcp_approx(1.f + ex2_approx(x[k] * z2));
+        for (int k = 0; k < 4; ++k) {
+            const float far = (a.c2 + nm) - (2.f * a.c2) * rcp_approx(1.f + ex2_approx(x[k] * z2));
+            if constexpr (WIDE) {
+                const float z = x[k] * a.k1, u = z * z;
+                x[k] = fabsf(z) < small ? fmaf(a.c2 * z, fmaf(fmaf(fmaf(s3, u, s2), u, s1), u, 1.f), nm) : far;
+            } else {
+                x[k] = far;
+            }
+        }
         st4(sp + 4 * i, x);
     }
     tc::wait_st();
     ld_s(sp, s);
 }
 
-template <int N>
+template <bool WIDE, int N>
 __device__ __forceinline__ void cap_s(float (&s)[N], uint32_t sp, const RowsArgs &a, float nm, uint64_t nm2) {
     const float top = max_of<true>(s) * fabsf(a.k1);
     cap_near(s, a, nm2);
-    if (__builtin_expect(__any_sync(0xffffffffu, top > a.near_max), 0)) cap_far(s, sp, a, nm);
+    if (__builtin_expect(__any_sync(0xffffffffu, top > a.near_max), 0)) cap_far<WIDE>(s, sp, a, nm);
 }
 
 // Raw products of N keys at sp, the first `ahead` keys before the row's position -> scores in base 2 plus nm.  beyond: keys
@@ -382,7 +393,7 @@ __device__ __forceinline__ void scores(float (&s)[N], uint32_t sp, int ahead, fl
     ld_s(sp, s);
     if constexpr (KIND == kCapBias) {
         if (!full) mask_s(s, w, 0.f);  // what is hidden has no say in how the others are capped
-        cap_s(s, sp, a, 0.f, 0ull);
+        cap_s<true>(s, sp, a, 0.f, 0ull);
     }
     const float f = KIND == kCapBias ? 1.f : a.k1;
     const uint64_t f2 = f32x2(f, f), nm2 = f32x2(nm, nm);
@@ -514,7 +525,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t sp, uint32_t op, const Til
 #pragma unroll 1
             for (int c = 0; c < kTok / N; ++c) {
                 ld_s(sp + N * c, x);
-                cap_s(x, sp + N * c, a, nm, nm2);
+                cap_s<false>(x, sp + N * c, a, nm, nm2);
                 weights(x, sp + N / 2 * c, ls);
             }
         } else {
@@ -527,7 +538,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t sp, uint32_t op, const Til
                 }
                 ld_s(sp + N * c, x);
                 mask_s(x, w, 0.f);  // what is hidden has no say in how the others are capped
-                cap_s(x, sp + N * c, a, nm, nm2);
+                cap_s<false>(x, sp + N * c, a, nm, nm2);
                 mask_s(x, w);
                 weights(x, sp + N / 2 * c, ls);
             }

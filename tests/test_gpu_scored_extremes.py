@@ -1,4 +1,6 @@
 """Scored attention at the ends of its ranges: V rows of very different sizes, wide caps, extreme scales."""
+import copy
+
 import numpy as np
 import pytest
 import torch
@@ -54,3 +56,28 @@ def test_rows_zeros_beside_large_values(n, large):
     # everything tiny: a row of any size keeps its precision
     c = _rows_case(n, np.linspace(0, 3, n), np.full(n, 2.0 ** -97))
     c.check(run(c))
+
+
+@pytest.mark.parametrize("cap,hot", [(60.0, 15.0), (1e4, 1500.0), (1e6, 1.5e5), (1e9, 1.5e8)])
+@pytest.mark.parametrize("kind", ["rows", "bf16", "multi", "alibi"])
+def test_a_wide_cap_that_others_reach(kind, cap, hot):
+    """One head's scores reach a wide cap: the other heads' results, far below it, are as good as without it (the bound is
+    the uncapped one, plus 2^-19 of a score)."""
+    c = Case([77, 300], qlens=[9, 130] if kind in ("multi", "alibi") else None, rows=kind == "rows", softcap=cap, window=90,
+             alibi=kind == "alibi")
+    ref, _ = c.reference()
+    plain = copy.copy(c)
+    plain.softcap = 0.0
+    _, tol = plain.reference()
+    rep, at = c.Hq // c.Hkv, 0
+    for s, L in enumerate(c.lens):
+        n = int(c.q_starts[s + 1] - c.q_starts[s])
+        q, k = (x.double().abs().numpy() for x in (c.q[at:at + n], c.ks[s]))
+        a = c.scale * max(float((q[:, h] @ k[:, h // rep].T).max()) for h in range(c.Hq))
+        tol[at:at + n] += 4 * 2.0 ** -19 * a * c.vs[s].double().abs().max().item()
+        at += n
+    c.q = c.q.clone()
+    c.q[:, 1] *= hot
+    got = run(c).double().cpu().numpy()
+    others = [h for h in range(c.Hq) if h != 1]
+    assert np.all(np.abs(got - ref)[:, others] <= tol[:, others])
