@@ -1356,10 +1356,23 @@ pkv_status run_rows(const Args &args, int head_dim, void *workspace, size_t work
     a.k1 = finite_float(a.s.softcap > 0.f ? (double)a.s.scale / a.s.softcap : a.s.scale * log2e);
     a.c2 = finite_float(a.s.softcap * log2e);
     a.m0 = 0.25f * a.c2;
-    double f = a.s.softcap * log2e * a.k1;
-    const bool wide = a.c2 > kWideCap;
-    a.near_max = wide ? kTanhSmall : kTanhNear;
-    for (int i = 0; i < 4; ++i, f *= (double)a.k1 * a.k1) a.near[i] = finite_float((wide ? kTanhSeries : kTanh3)[i] * f);
+    if (a.s.softcap > 0.f) {
+        a.k1 = std::min(std::max(a.k1, -1e38f), 1e38f);  // 2 log2 e k1 stays finite: no score of 0 becomes NaN
+        double f = a.s.softcap * log2e * a.k1;
+        const bool wide = a.c2 > kWideCap;
+        a.near_max = wide ? kTanhSmall : kTanhNear;
+        bool folds = true;  // the cap's factors folded into the coefficients are normal numbers
+        for (int i = 0; i < 4; ++i, f *= (double)a.k1 * a.k1) {
+            const double x = (wide ? kTanhSeries : kTanh3)[i] * f;
+            folds = folds && std::fabs(x) > 1e-37 && std::fabs(x) < 1e37;
+            a.near[i] = (float)(folds ? x : 0.0);
+        }
+        if (!folds) {  // a scale far from the cap's: c2 k1 s where |z| < 2^-12 (off by 2^-25 of it), the others as large ones
+            a.near[0] = finite_float(a.s.softcap * log2e * a.k1);
+            a.near[1] = a.near[2] = a.near[3] = 0.f;
+            a.near_max = a.k1 == 0.f || std::fabs(a.k1) > 1e-22f ? 0x1p-12f : -1.f;  // (-1: s^2 would pass float32's range)
+        }
+    }
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     a.part_o = reinterpret_cast<float *>(ws + lay.o);
     a.part_ml = reinterpret_cast<float *>(ws + lay.ml);

@@ -81,3 +81,13 @@ def test_a_wide_cap_that_others_reach(kind, cap, hot):
     got = run(c).double().cpu().numpy()
     others = [h for h in range(c.Hq) if h != 1]
     assert np.all(np.abs(got - ref)[:, others] <= tol[:, others])
+
+
+@pytest.mark.parametrize("scale", [1e-30, 1e-12, 1e-7, 1e-4, 1e4, 1e7, 1e12, 1e30])
+@pytest.mark.parametrize("cap", [12.0, 200.0])
+@pytest.mark.parametrize("kind", ["f32", "bf16", "rows", "multi"])
+def test_extreme_scales(kind, cap, scale):
+    """Scores of ordinary size made of very large queries and a tiny scale, or the other way round."""
+    c = Case([77, 300], qlens=[9, 130] if kind == "multi" else None, rows=kind == "rows", softcap=cap, scale=scale,
+             qmul=2.0 / scale / 128 ** 0.5, dtype=torch.float32 if kind == "f32" else torch.bfloat16)
+    c.check(run(c))
