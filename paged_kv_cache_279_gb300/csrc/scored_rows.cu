@@ -34,12 +34,22 @@
 // K (a column half each) and 19 of V (one TMA box per block), 20 the scheduler,
 // which walks the share, publishes one descriptor per piece of a context and loads
 // its queries (one box per column half).
+// Infinities and NaN in V: P V multiplies them by the zero weights of rows that do not see
+// their key, and 0 times infinity is NaN.  Nothing guards against that at first.  The epilogue
+// looks at what it reads of O, and a CTA that met an infinity or NaN walks its share a second
+// time, carefully: in tiles that not every row sees whole, the sets take infinities and NaN
+// out of V, and the epilogue adds them to the rows that see their keys.  The look costs 1 of 57 us
+// (64 x 5 queries) and of 177 (prompts of documents); reading every such tile's V for them at once
+// would cost each of them some 100 instructions a thread.  The second walk is code of its own (as a
+// flag in the same code it took 2 to 3 % more).
+//
 // Tensor memory: S at columns 128 (t % 3) (P overwrites its first half as bf16
 // pairs), O at 384.
 // Every wait is bounded; one that gives up flags PKV_DEVERR_TIMEOUT.
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include "pkv_internal.cuh"
 #include "scored.cuh"
@@ -115,7 +125,9 @@ struct Layout {
     static constexpr int bars = recs + kRecs * (int)sizeof(TileRec);
     static constexpr int kBars = 2 * NK + 2 * NV + 3 * kSets + 4 * kSets + 4 + 2 + 4 + 16 + 2 * kDescs + 2;
     static constexpr int misc = bars + kBars * 8;       // TMEM address, scan scratch
-    static constexpr int total = misc + 128;
+    static constexpr int redo = misc + 124;             // an output was infinite or NaN
+    static constexpr int fin_bad = misc + 128;          // [2][4 kSets]: per warp, V entries taken out of a piece's tiles
+    static constexpr int total = fin_bad + 2 * 4 * kSets * 4;
     static_assert(total <= 227 * 1024, "shared memory per CTA");
 };
 
@@ -123,6 +135,10 @@ __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
     return p != 0u;
+}
+
+__device__ __forceinline__ void mbar_inval(uint64_t *bar) {
+    asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 __device__ __forceinline__ void prefetch_l1(const void *p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
@@ -630,6 +646,104 @@ __device__ __forceinline__ void softmax_tile(uint32_t sp, uint32_t op, const Til
 }
 
 // ---------------------------------------------------------------------------
+// Infinities and NaN in V
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ bool odd_lo(uint32_t v) { return (v & 0x7f80u) == 0x7f80u; }
+__device__ __forceinline__ bool odd_hi(uint32_t v) { return (v & 0x7f800000u) == 0x7f800000u; }
+
+// Zeroes the infinities and NaN of the V row at `row` (halves `half` bytes apart); true where there were some.
+template <int H>
+__device__ __noinline__ bool clean_row(uint32_t row, uint32_t half, int lane) {
+    bool any = false;
+#pragma unroll 1
+    for (int i = 0; i < 8 * H; ++i) {
+        const uint32_t at = row + (uint32_t)(i >> 3) * half + (uint32_t)((i + lane) & 7) * 16;
+        const float4 f = lds128(at);
+        uint32_t v[4] = {__float_as_uint(f.x), __float_as_uint(f.y), __float_as_uint(f.z), __float_as_uint(f.w)};
+        bool odd = false;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            odd = odd || odd_lo(v[k]) || odd_hi(v[k]);
+            if (odd_lo(v[k])) v[k] &= 0xffff0000u;
+            if (odd_hi(v[k])) v[k] &= 0xffffu;
+        }
+        if (odd)
+            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+        any = any || odd;
+    }
+    return any;
+}
+
+// Adds the infinities and NaN of V to the O of the rows (of this warp; a lane's sees r) that see their keys, over the tiles
+// of a piece from which the sets took them.  op: O of the warp's rows.  A row none of whose outputs is finite any more is
+// done, which bounds the time where everything is NaN.
+template <int D>
+__device__ __noinline__ void add_odd_values(const RowsArgs &a, const Piece &pc, const KeyRange r, uint32_t op, int lane) {
+    const int32_t *bt = a.block_tables + (int64_t)pc.seq * a.max_blocks;
+    const int B = a.block_size;
+    bool done = false;
+#pragma unroll 1
+    for (int i = pc.i0; i < pc.i0 + pc.ntiles; ++i) {
+        const int t0 = (i < pc.np ? pc.pt0 + i : pc.mt0 + i - pc.np) * kTok;
+        if ((t0 >= pc.flo && t0 + kTok <= pc.fhi) || (t0 >= pc.fks && t0 + kTok <= pc.pre)) continue;  // every row sees it
+#pragma unroll 1
+        for (int c = 0; c < kTok; c += 32) {
+            // a lane a key: its V row, and whether it holds any
+            const int t = t0 + c + lane;
+            const KeyRange cr{pc.ks0, pc.cpre, pc.lo, pc.hi};
+            int64_t row = -1;
+            bool odd = false;
+            if (cr.sees(t)) {
+                const int blk = bt[t >> a.bshift];
+                if (blk >= 0 && blk < a.num_blocks) row = ((int64_t)blk * a.num_kv_heads + pc.kvh) * B + (t & (B - 1));
+            }
+            if (row >= 0) {
+                const uint4 *v = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.v_cache) + row * D);
+#pragma unroll 4
+                for (int k = 0; k < D / 8; ++k) {
+                    const uint4 x = v[k];
+                    odd = odd || odd_lo(x.x) || odd_hi(x.x) || odd_lo(x.y) || odd_hi(x.y) || odd_lo(x.z) || odd_hi(x.z) ||
+                          odd_lo(x.w) || odd_hi(x.w);
+                }
+            }
+#pragma unroll 1
+            for (uint32_t todo = __ballot_sync(0xffffffffu, odd); todo; todo &= todo - 1) {
+                const int k = __ffs(todo) - 1;
+                const bool mine = !done && r.sees(t0 + c + k);
+                if (!__any_sync(0xffffffffu, mine)) continue;
+                const uint32_t *v = reinterpret_cast<const uint32_t *>(static_cast<const __nv_bfloat16 *>(a.v_cache) +
+                                                                       __shfl_sync(0xffffffffu, row, k) * D);
+                bool finite = false;
+#pragma unroll 1
+                for (int d = 0; d < D; d += 16) {
+                    uint32_t x[8];
+                    bool some = false;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        x[j] = v[d / 2 + j];
+                        some = some || odd_lo(x[j]) || odd_hi(x[j]);
+                    }
+                    finite = finite || !some;
+                    if (!some) continue;  // (the same in every lane)
+                    float o[16];
+                    ld16(op + (uint32_t)d, o);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        if (mine && odd_lo(x[j])) o[2 * j] += bf16x2_lo(x[j]);
+                        if (mine && odd_hi(x[j])) o[2 * j + 1] += bf16x2_hi(x[j]);
+                        finite = finite || fabsf(o[2 * j]) < INFINITY || fabsf(o[2 * j + 1]) < INFINITY;
+                    }
+                    st16u(op + (uint32_t)d, reinterpret_cast<const uint32_t(&)[16]>(o));
+                    tc::wait_st();
+                }
+                done = done || !finite;
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
 // The kernel
 // ---------------------------------------------------------------------------
 template <int D, int KIND>
@@ -655,6 +769,7 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     uint64_t *desc_full = started + 16, *desc_empty = desc_full + kDescs, *all_done = desc_empty + kDescs;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::misc);
     int *scratch = reinterpret_cast<int *>(smem + L::misc + 16);  // [22] warp sums, carry, found sequence, its start
+    volatile int *redo = reinterpret_cast<int *>(smem + L::redo), *fin_bad = reinterpret_cast<int *>(smem + L::fin_bad);
     constexpr int kCarry = kThreads / 32, kFound = kCarry + 1, kStart = kCarry + 2;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int Hkv = a.num_kv_heads, G = a.group, B = a.block_size;
@@ -739,493 +854,540 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     for (int i = a.per_ctx * G * 8 + threadIdx.x; i < kRows * 8; i += kThreads)
         for (int t = 0; t < 2 * H; ++t) *reinterpret_cast<uint4 *>(smem + L::q + t * (kRows * 128) + i * 16) = make_uint4(0u, 0u, 0u, 0u);
     fence_proxy_async();
-    if (threadIdx.x == 0) {
-#pragma unroll 1
-        for (int i = 0; i < NK; ++i) {
-            mbar_init(&k_full[i], H);
-            mbar_init(&k_empty[i], 1);
-        }
-#pragma unroll 1
-        for (int i = 0; i < NV; ++i) {
-            mbar_init(&v_full[i], 1);
-            mbar_init(&v_empty[i], 1);
-        }
-#pragma unroll 1
-        for (int i = 0; i < kSets; ++i) {
-            mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 4);
-            mbar_init(&o_done[i], 1);
-        }
-#pragma unroll 1
-        for (int i = 0; i < 4 * kSets; ++i) mbar_init(&m_full[i], 1);
-#pragma unroll 1
-        for (int i = 0; i < 16; ++i) mbar_init(&started[i], 1);
-#pragma unroll 1
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&q_full[i], 1);
-            mbar_init(&q_empty[i], 1);
-            mbar_init(&fin_full[i], 4 * kSets);
-            mbar_init(&fin_empty[i], 4);
-        }
-        mbar_init(o_last, 1);
-        mbar_init(o_free, 4);
-#pragma unroll 1
-        for (int i = 0; i < kDescs; ++i) {
-            mbar_init(&desc_full[i], 1);
-            mbar_init(&desc_empty[i], 4 * kSets + 4 + 2 + H + 1);  // softmax, epilogue, MMA, producers
-        }
-        mbar_init(&all_done[0], 1);
-        mbar_init(&all_done[1], 1);
-        fence_barrier_init();
-    }
     if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                      "r"(kTmemCols)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    tc::fence_before();
-    __syncthreads();
-    tc::fence_after();
-    const uint32_t tmem = *tmem_slot;
-    const uint32_t q_s = smem_u32(smem + L::q), k_s = smem_u32(smem + L::kring), v_s = smem_u32(smem + L::vring);
     bool dead = false;
+    auto walk = [&](auto again) {
+        constexpr bool careful = decltype(again)::value;
+        if (threadIdx.x == 0) {
+            *redo = 0;
+            if (careful)
+#pragma unroll 1
+                for (int i = 0; i < L::kBars; ++i) mbar_inval(&k_full[i]);
+#pragma unroll 1
+            for (int i = 0; i < NK; ++i) {
+                mbar_init(&k_full[i], H);
+                mbar_init(&k_empty[i], 1);
+            }
+#pragma unroll 1
+            for (int i = 0; i < NV; ++i) {
+                mbar_init(&v_full[i], 1);
+                mbar_init(&v_empty[i], 1);
+            }
+#pragma unroll 1
+            for (int i = 0; i < kSets; ++i) {
+                mbar_init(&s_full[i], 1);
+                mbar_init(&p_full[i], 4);
+                mbar_init(&o_done[i], 1);
+            }
+#pragma unroll 1
+            for (int i = 0; i < 4 * kSets; ++i) mbar_init(&m_full[i], 1);
+#pragma unroll 1
+            for (int i = 0; i < 16; ++i) mbar_init(&started[i], 1);
+#pragma unroll 1
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(&q_full[i], 1);
+                mbar_init(&q_empty[i], 1);
+                mbar_init(&fin_full[i], 4 * kSets);
+                mbar_init(&fin_empty[i], 4);
+            }
+            mbar_init(o_last, 1);
+            mbar_init(o_free, 4);
+#pragma unroll 1
+            for (int i = 0; i < kDescs; ++i) {
+                mbar_init(&desc_full[i], 1);
+                mbar_init(&desc_empty[i], 4 * kSets + 4 + 2 + H + 1);  // softmax, epilogue, MMA, producers
+            }
+            mbar_init(&all_done[0], 1);
+            mbar_init(&all_done[1], 1);
+            fence_barrier_init();
+        }
+        tc::fence_before();
+        __syncthreads();
+        tc::fence_after();
+        const uint32_t tmem = *tmem_slot;
+        const uint32_t q_s = smem_u32(smem + L::q), k_s = smem_u32(smem + L::kring), v_s = smem_u32(smem + L::vring);
 
-    if (warp == kSchedWarp) {
-        // ======================= scheduler =======================
-        int s = scratch[kFound];
-        int t = s0;                     // next laid-out tile of the share
-        int seq_start = scratch[kStart];  // laid-out start of sequence s
-        int p = 0;
-        while (t < s1 && !dead) {
-            const Seq x = load_seq(a, s, false);
-            const int fp = first_pos(a, x, s), nb = (x.Q + a.per_ctx - 1) / a.per_ctx;
-            int per_kvh = 0;
+        if (warp == kSchedWarp) {
+            // ======================= scheduler =======================
+            int s = scratch[kFound];
+            int t = s0;                     // next laid-out tile of the share
+            int seq_start = scratch[kStart];  // laid-out start of sequence s
+            int p = 0;
+            while (t < s1 && !dead) {
+                const Seq x = load_seq(a, s, false);
+                const int fp = first_pos(a, x, s), nb = (x.Q + a.per_ctx - 1) / a.per_ctx;
+                int per_kvh = 0;
 #pragma unroll 1
-            for (int b = lane; b < nb; b += 32) per_kvh += laid_out(ctx_tiles(a, x, fp, b).n);
+                for (int b = lane; b < nb; b += 32) per_kvh += laid_out(ctx_tiles(a, x, fp, b).n);
 #pragma unroll
-            for (int sh = 16; sh > 0; sh >>= 1) per_kvh += __shfl_xor_sync(0xffffffffu, per_kvh, sh);
+                for (int sh = 16; sh > 0; sh >>= 1) per_kvh += __shfl_xor_sync(0xffffffffu, per_kvh, sh);
 #pragma unroll
-            for (int kvh = per_kvh > 0 ? (t - seq_start) / per_kvh : Hkv; kvh < Hkv && t < s1 && !dead; ++kvh) {
-                int pos = seq_start + kvh * per_kvh;  // laid-out start of block b0
+                for (int kvh = per_kvh > 0 ? (t - seq_start) / per_kvh : Hkv; kvh < Hkv && t < s1 && !dead; ++kvh) {
+                    int pos = seq_start + kvh * per_kvh;  // laid-out start of block b0
 #pragma unroll 1
-                for (int b0 = 0; b0 < nb && t < s1 && !dead; b0 += 32) {
-                    CtxTiles c{};
-                    if (b0 + lane < nb) c = ctx_tiles(a, x, fp, b0 + lane);
-                    int end = laid_out(c.n);
+                    for (int b0 = 0; b0 < nb && t < s1 && !dead; b0 += 32) {
+                        CtxTiles c{};
+                        if (b0 + lane < nb) c = ctx_tiles(a, x, fp, b0 + lane);
+                        int end = laid_out(c.n);
 #pragma unroll
-                    for (int sh = 1; sh < 32; sh <<= 1) {
-                        const int y = __shfl_up_sync(0xffffffffu, end, sh);
-                        if (lane >= sh) end += y;
-                    }
-                    end += pos;
-                    const int begin = end - laid_out(c.n);
-                    // this lane's context: its real tiles [i0, i1) in the share
-                    const int i0 = max(0, max(s0, begin) - begin - kCharge), i1 = min(s1, end) - begin - kCharge;
-                    const bool mine = c.n > 0 && begin < s1 && end > s0 && i1 > i0;
-#pragma unroll 1
-                    for (uint32_t todo = __ballot_sync(0xffffffffu, mine); todo && !dead; todo &= todo - 1) {
-                        const int d = p % kDescs;
-                        if (lane == 0 && p >= kDescs)
-                            wait_for(&desc_empty[d], (uint32_t)((p / kDescs - 1) & 1), dead);
-                        dead = __shfl_sync(0xffffffffu, dead, 0);
-                        if (lane == __ffs(todo) - 1 && !dead) {
-                            Piece pc;
-                            pc.ntiles = i1 - i0;
-                            pc.i0 = i0;
-                            pc.np = c.np;
-                            pc.pt0 = c.pt0;
-                            pc.mt0 = c.mt0;
-                            pc.seq = s;
-                            pc.kvh = kvh;
-                            const int q0 = (b0 + lane) * a.per_ctx;
-                            pc.row0 = x.q0 + q0;
-                            const int nq = min(x.Q - q0, a.per_ctx);
-                            pc.nq = nq;
-                            pc.nrows = nq * G;
-                            pc.pos0 = fp + q0;
-                            pc.pre = x.pre;
-                            pc.ks0 = c.ks0;
-                            pc.cpre = c.r.pre;
-                            pc.lo = c.r.lo;
-                            pc.hi = c.r.hi;
-                            // what the last row's document or window leaves, up to the first row's position
-                            pc.fks = max(c.ks0, key_start_of(a.s, pc.row0 + nq - 1));
-                            pc.flo = max(pc.fks, a.s.window > 0 ? pc.pos0 + nq - a.s.window : 0);
-                            pc.fhi = pc.pos0 + 1;
-                            const bool begins = begin + kCharge >= s0, ends = end <= s1;
-                            pc.slot = begins && ends ? -1 : 2 * (int)blockIdx.x + (begins ? 1 : 0);
-                            if (begins && !ends)  // the shares that hold the rest
-                                a.merges[blockIdx.x] = make_int4(shares.owner(end - 1) - (int)blockIdx.x + 1, pc.row0,
-                                                                 pc.nrows, kvh);
-                            descs[d] = pc;
-                            mbar_arrive(&desc_full[d]);
-                            // the rows' loads at the piece's start
-                            if (a.s.key_starts)
-#pragma unroll 1
-                                for (int i = 0; i < nq; i += 32) prefetch_l1(a.s.key_starts + pc.row0 + i);
-                            // its queries: per_ctx queries of the KV head's G heads, one box per column half
-                            const int qb = p & 1;
-                            if (p >= 2) wait_for(&q_empty[qb], (uint32_t)((p / 2 - 1) & 1), dead);
-                            if (!dead) {
-                                mbar_arrive_expect_tx(&q_full[qb], (uint32_t)(H * a.per_ctx * G * 128));
-#pragma unroll
-                                for (int h = 0; h < H; ++h)
-                                    tma_load_3d(q_s + (uint32_t)(qb * L::kQTile + h * (kRows * 128)), &tm_q, smem_u32(&q_full[qb]),
-                                                h * 64, kvh * G, pc.row0);
-                            }
+                        for (int sh = 1; sh < 32; sh <<= 1) {
+                            const int y = __shfl_up_sync(0xffffffffu, end, sh);
+                            if (lane >= sh) end += y;
                         }
-                        dead = __any_sync(0xffffffffu, dead);
-                        ++p;
+                        end += pos;
+                        const int begin = end - laid_out(c.n);
+                        // this lane's context: its real tiles [i0, i1) in the share
+                        const int i0 = max(0, max(s0, begin) - begin - kCharge), i1 = min(s1, end) - begin - kCharge;
+                        const bool mine = c.n > 0 && begin < s1 && end > s0 && i1 > i0;
+#pragma unroll 1
+                        for (uint32_t todo = __ballot_sync(0xffffffffu, mine); todo && !dead; todo &= todo - 1) {
+                            const int d = p % kDescs;
+                            if (lane == 0 && p >= kDescs)
+                                wait_for(&desc_empty[d], (uint32_t)((p / kDescs - 1) & 1), dead);
+                            dead = __shfl_sync(0xffffffffu, dead, 0);
+                            if (lane == __ffs(todo) - 1 && !dead) {
+                                Piece pc;
+                                pc.ntiles = i1 - i0;
+                                pc.i0 = i0;
+                                pc.np = c.np;
+                                pc.pt0 = c.pt0;
+                                pc.mt0 = c.mt0;
+                                pc.seq = s;
+                                pc.kvh = kvh;
+                                const int q0 = (b0 + lane) * a.per_ctx;
+                                pc.row0 = x.q0 + q0;
+                                const int nq = min(x.Q - q0, a.per_ctx);
+                                pc.nq = nq;
+                                pc.nrows = nq * G;
+                                pc.pos0 = fp + q0;
+                                pc.pre = x.pre;
+                                pc.ks0 = c.ks0;
+                                pc.cpre = c.r.pre;
+                                pc.lo = c.r.lo;
+                                pc.hi = c.r.hi;
+                                // what the last row's document or window leaves, up to the first row's position
+                                pc.fks = max(c.ks0, key_start_of(a.s, pc.row0 + nq - 1));
+                                pc.flo = max(pc.fks, a.s.window > 0 ? pc.pos0 + nq - a.s.window : 0);
+                                pc.fhi = pc.pos0 + 1;
+                                const bool begins = begin + kCharge >= s0, ends = end <= s1;
+                                pc.slot = begins && ends ? -1 : 2 * (int)blockIdx.x + (begins ? 1 : 0);
+                                if (begins && !ends)  // the shares that hold the rest
+                                    a.merges[blockIdx.x] = make_int4(shares.owner(end - 1) - (int)blockIdx.x + 1, pc.row0,
+                                                                     pc.nrows, kvh);
+                                descs[d] = pc;
+                                mbar_arrive(&desc_full[d]);
+                                // the rows' loads at the piece's start
+                                if (a.s.key_starts)
+#pragma unroll 1
+                                    for (int i = 0; i < nq; i += 32) prefetch_l1(a.s.key_starts + pc.row0 + i);
+                                // its queries: per_ctx queries of the KV head's G heads, one box per column half
+                                const int qb = p & 1;
+                                if (p >= 2) wait_for(&q_empty[qb], (uint32_t)((p / 2 - 1) & 1), dead);
+                                if (!dead) {
+                                    mbar_arrive_expect_tx(&q_full[qb], (uint32_t)(H * a.per_ctx * G * 128));
+#pragma unroll
+                                    for (int h = 0; h < H; ++h)
+                                        tma_load_3d(q_s + (uint32_t)(qb * L::kQTile + h * (kRows * 128)), &tm_q, smem_u32(&q_full[qb]),
+                                                    h * 64, kvh * G, pc.row0);
+                                }
+                            }
+                            dead = __any_sync(0xffffffffu, dead);
+                            ++p;
+                        }
+                        pos = __shfl_sync(0xffffffffu, end, 31);
+                        t = max(t, min(s1, pos));
                     }
-                    pos = __shfl_sync(0xffffffffu, end, 31);
-                    t = max(t, min(s1, pos));
+                }
+                seq_start += per_kvh * Hkv;
+                t = max(t, min(s1, seq_start));
+                ++s;
+                if (s >= a.num_seqs) break;
+            }
+            if (lane == 0 && !dead) {
+                const int d = p % kDescs;
+                if (p >= kDescs) wait_for(&desc_empty[d], (uint32_t)((p / kDescs - 1) & 1), dead);
+                if (!dead) {
+                    descs[d].ntiles = 0;
+                    mbar_arrive(&desc_full[d]);
                 }
             }
-            seq_start += per_kvh * Hkv;
-            t = max(t, min(s1, seq_start));
-            ++s;
-            if (s >= a.num_seqs) break;
-        }
-        if (lane == 0 && !dead) {
-            const int d = p % kDescs;
-            if (p >= kDescs) wait_for(&desc_empty[d], (uint32_t)((p / kDescs - 1) & 1), dead);
-            if (!dead) {
-                descs[d].ntiles = 0;
-                mbar_arrive(&desc_full[d]);
-            }
-        }
-        // queries in flight (only after a timeout) land before the CTA exits
-        if (dead && lane == 0)
+            // queries in flight (only after a timeout) land before the CTA exits
+            if (dead && lane == 0)
 #pragma unroll 1
-            for (int k = max(0, p - 2); k < p; ++k) drain(&q_full[k & 1], (uint32_t)((k >> 1) & 1));
-    } else if (warp == kVWarp || (warp >= kKWarp && warp < kKWarp + H)) {
-        // ======================= producers =======================
-        const bool isk = warp != kVWarp;
-        const int half = warp - kKWarp;  // K: column half
-        const int N = isk ? NK : NV;
-        uint64_t *full = isk ? k_full : v_full, *empty = isk ? k_empty : v_empty;
-        const int bpt = kTok >> a.bshift;  // blocks per tile, at most 16
-        int tau = 0;
+                for (int k = max(0, p - 2); k < p; ++k) drain(&q_full[k & 1], (uint32_t)((k >> 1) & 1));
+        } else if (warp == kVWarp || (warp >= kKWarp && warp < kKWarp + H)) {
+            // ======================= producers =======================
+            const bool isk = warp != kVWarp;
+            const int half = warp - kKWarp;  // K: column half
+            const int N = isk ? NK : NV;
+            uint64_t *full = isk ? k_full : v_full, *empty = isk ? k_empty : v_empty;
+            const int bpt = kTok >> a.bshift;  // blocks per tile, at most 16
+            int tau = 0;
 #pragma unroll 1
-        for (int p = 0; !dead; ++p) {
-            const int d = p % kDescs;
-            if (!wait_for(&desc_full[d], (uint32_t)((p / kDescs) & 1), dead)) break;
-            const Piece &pc = descs[d];
-            const int n = pc.ntiles;
-            if (n == 0) break;
-            const int32_t *bt = a.block_tables + (int64_t)pc.seq * a.max_blocks;
-            const KeyRange r{pc.ks0, pc.cpre, pc.lo, pc.hi};
-            const int kvh = pc.kvh, flo = pc.flo, fhi = pc.fhi, fks = pc.fks, pre = pc.pre;
-            const int i1 = pc.i0 + n, np = pc.np, pt0 = pc.pt0, mt0 = pc.mt0;
-            // the latest keys first: with a bias by distance the largest scores come first, and the rows' reference seldom moves
-            auto first_key = [&](int j) {
-                const int i = i1 - 1 - j;
-                return (i < np ? pt0 + i : mt0 + i - np) * kTok;
-            };
-            // this lane's block of a tile: its id, INT_MIN where no row sees a key of it
-            auto block_id = [&](int j) {
-                if (j >= n || lane >= bpt) return (int)INT_MIN;
-                const int t = first_key(j) + (lane << a.bshift);
-                if (!r.meets(t, t + B)) return (int)INT_MIN;
-                return max((int)bt[t >> a.bshift], INT_MIN + 1);
-            };
-            int next = block_id(0);
+            for (int p = 0; !dead; ++p) {
+                const int d = p % kDescs;
+                if (!wait_for(&desc_full[d], (uint32_t)((p / kDescs) & 1), dead)) break;
+                const Piece &pc = descs[d];
+                const int n = pc.ntiles;
+                if (n == 0) break;
+                const int32_t *bt = a.block_tables + (int64_t)pc.seq * a.max_blocks;
+                const KeyRange r{pc.ks0, pc.cpre, pc.lo, pc.hi};
+                const int kvh = pc.kvh, flo = pc.flo, fhi = pc.fhi, fks = pc.fks, pre = pc.pre;
+                const int i1 = pc.i0 + n, np = pc.np, pt0 = pc.pt0, mt0 = pc.mt0;
+                // the latest keys first: with a bias by distance the largest scores come first, and the rows' reference seldom moves
+                auto first_key = [&](int j) {
+                    const int i = i1 - 1 - j;
+                    return (i < np ? pt0 + i : mt0 + i - np) * kTok;
+                };
+                // this lane's block of a tile: its id, INT_MIN where no row sees a key of it
+                auto block_id = [&](int j) {
+                    if (j >= n || lane >= bpt) return (int)INT_MIN;
+                    const int t = first_key(j) + (lane << a.bshift);
+                    if (!r.meets(t, t + B)) return (int)INT_MIN;
+                    return max((int)bt[t >> a.bshift], INT_MIN + 1);
+                };
+                int next = block_id(0);
 #pragma unroll 1
-            for (int j = 0; j < n; ++j, ++tau) {
-                const int st = tau % N;
-                const int id = next;
-                next = block_id(j + 1);
-                if (tau >= N) wait_for(&empty[st], (uint32_t)((tau / N - 1) & 1), dead);
-                if (__any_sync(0xffffffffu, dead)) {
-                    dead = true;
-                    break;
-                }
-                const bool live = id != INT_MIN, bad = live && (id < 0 || id >= a.num_blocks);
-                const uint32_t nlive = (uint32_t)__popc(__ballot_sync(0xffffffffu, live)), badm = __ballot_sync(0xffffffffu, bad);
-                if (lane == 0) {
-                    if (isk && half == 0) {
-                        const int t0 = first_key(j);
-                        TileRec rec;
-                        rec.t0 = t0;
-                        rec.bad = badm;
-                        rec.whole = badm == 0u && ((t0 >= r.lo && t0 + kTok <= r.hi) || (t0 >= r.first && t0 + kTok <= r.pre));
-                        rec.full = badm == 0u && ((t0 >= flo && t0 + kTok <= fhi) || (t0 >= fks && t0 + kTok <= pre));
-                        recs[tau % kRecs] = rec;
-                        if (badm) flag_error(a.err, PKV_DEVERR_BLOCK_ID);
+                for (int j = 0; j < n; ++j, ++tau) {
+                    const int st = tau % N;
+                    const int id = next;
+                    next = block_id(j + 1);
+                    if (tau >= N) wait_for(&empty[st], (uint32_t)((tau / N - 1) & 1), dead);
+                    if (__any_sync(0xffffffffu, dead)) {
+                        dead = true;
+                        break;
                     }
-                    mbar_arrive_expect_tx(&full[st], nlive * (uint32_t)((isk ? 1 : H) * 128) << a.bshift);
-                }
-                __syncwarp();
-                // an invalid id is read as block 0, its keys masked
-                if (live) {
-                    const int y = (int)(((int64_t)(bad ? 0 : id) * Hkv + kvh) * B);
-                    if (isk)
-                        tma_load_2d(k_s + st * L::kTile + half * (kTok * 128) + ((lane << a.bshift) * 128), &tm_k, smem_u32(&full[st]),
-                                    half * 64, y);
-                    else
-                        tma_load_3d(v_s + st * L::kTile + ((lane << a.bshift) * (H * 128)), &tm_v, smem_u32(&full[st]), 0, y, 0);
-                }
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&desc_empty[d]);
-        }
-        // copies in flight (only after a timeout) land before the CTA exits
-        if (lane == 0 && dead)
-#pragma unroll 1
-            for (int k = max(0, tau - N); k < tau; ++k) drain(&full[k % N], (uint32_t)((k / N) & 1));
-    } else if (warp == kMmaWarp) {
-        // ======================= Q K^T issuer =======================
-        // Both issuers walk as whole warps (uniform registers) and one elected lane issues.
-        constexpr uint32_t idesc = tc::instr_desc(kTok, false);
-        const bool leader = elect_one();
-        const uint64_t qd0 = tc::smem_desc(q_s, 16, 1024), kd0 = tc::smem_desc(k_s, 16, 1024);
-        int st = 0, sb = 0;            // K stage, S buffer
-        uint32_t kph = 0, sph = 1;     // their phases (a buffer's first use waits for nothing)
-        int d = 0;
-        uint32_t dph = 0;
-#pragma unroll 1
-        for (int p = 0;; ++p) {
-            wait_for(&desc_full[d], dph, dead);
-            const int n = dead ? 0 : descs[d].ntiles;
-            if (n == 0) break;
-            wait_for(&q_full[p & 1], (uint32_t)((p >> 1) & 1), dead);
-            const uint64_t qd = qd0 + (uint64_t)((uint32_t)(p & 1) * (uint32_t)(L::kQTile >> 4));
-#pragma unroll 1
-            for (int j = 0; j < n; ++j) {
-                wait_for(&k_full[st], kph, dead);
-                wait_for(&o_done[sb], sph, dead);  // the P V that read the buffer before
-                if (dead) break;
-                tc::fence_after();
-                const uint64_t kd = kd0 + (uint64_t)((uint32_t)st * (uint32_t)(L::kTile >> 4));
-                if (leader) {
-#pragma unroll 1  // (the shorter code leaves more of the instruction cache to the softmax)
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint64_t off = (uint64_t)(((k >> 2) * (kTok * 128) + (k & 3) * 32) >> 4);
-                        tc::mma(tmem + (uint32_t)sb * kTok, qd + off, kd + off, idesc, k > 0 ? 1u : 0u);
-                    }
-                    tc::commit(&s_full[sb]);
-                    tc::commit(&k_empty[st]);
-                    if (j + 1 == n) tc::commit(&q_empty[p & 1]);
-                }
-                __syncwarp();
-                if (++st == NK) st = 0, kph ^= 1u;
-                if (++sb == kSets) sb = 0, sph ^= 1u;
-            }
-            if (lane == 0) mbar_arrive(&desc_empty[d]);
-            if (++d == kDescs) d = 0, dph ^= 1u;
-        }
-        if (leader) tc::commit(&all_done[0]);
-        __syncwarp();
-        drain(&all_done[0], 0u);
-    } else if (warp == kPvWarp) {
-        // ======================= P V issuer =======================
-        constexpr uint32_t idesc = tc::instr_desc(D, true);
-        const uint32_t pv_lbo = (uint32_t)(B * 128), pv_sbo = B >= 16 ? 1024u : (uint32_t)(H * B * 128);
-        const bool leader = elect_one();
-        const uint64_t vd0 = tc::smem_desc(v_s, pv_lbo, pv_sbo);
-        // 16 keys of V further: inside a block of 32 every second step, else a block (B = 8: two)
-        const uint32_t odd = B == 32 ? 16 * 128 >> 4 : (uint32_t)(H * 16 * 128) >> 4, two = (uint32_t)(2 * H * 16 * 128) >> 4;
-        int st = 0, sb = 0;
-        uint32_t vph = 0, sph = 0;
-        int d = 0;
-        uint32_t dph = 0;
-#pragma unroll 1
-        for (int p = 0;; ++p) {
-            wait_for(&desc_full[d], dph, dead);
-            const int n = dead ? 0 : descs[d].ntiles;
-            if (n == 0) break;
-            if (p > 0) wait_for(o_free, (uint32_t)((p - 1) & 1), dead);  // the piece before's O has been read
-#pragma unroll 1
-            for (int j = 0; j < n; ++j) {
-                wait_for(&v_full[st], vph, dead);
-                wait_for(&p_full[sb], sph, dead);
-                if (dead) break;
-                tc::fence_after();
-                const uint64_t vd = vd0 + (uint64_t)((uint32_t)st * (uint32_t)(L::kTile >> 4));
-                if (leader) {
-#pragma unroll 1  // (the shorter code leaves more of the instruction cache to the softmax)
-                    for (int k = 0; k < kTok / 16; ++k)
-                        tc::mma_ts(tmem + kOBase, tmem + (uint32_t)(sb * kTok + 8 * k),
-                                   vd + (uint64_t)((uint32_t)(k >> 1) * two + (uint32_t)(k & 1) * odd), idesc, j > 0 || k > 0 ? 1u : 0u);
-                    tc::commit(&o_done[sb]);
-                    tc::commit(&v_empty[st]);
-                    if (j + 1 == n) tc::commit(o_last);
-                }
-                __syncwarp();
-                if (++st == NV) st = 0, vph ^= 1u;
-                if (++sb == kSets) sb = 0, sph ^= 1u;
-            }
-            if (lane == 0) mbar_arrive(&desc_empty[d]);
-            if (++d == kDescs) d = 0, dph ^= 1u;
-        }
-        // every product has completed before the tensor memory is freed
-        if (leader) tc::commit(&all_done[1]);
-        __syncwarp();
-        drain(&all_done[1], 0u);
-    } else if (warp < kEpiWarp) {
-        // ======================= softmax =======================
-        const int set = warp >> 2, wq = warp & 3;
-        const int rr = wq * 32 + lane;  // TMEM lane and row of the context
-        const int rq = rr / G, rh = rr - rq * G;  // its query and head
-        const uint32_t trow = tmem + ((uint32_t)(wq * 32) << 16);
-        const uint32_t sp = trow + (uint32_t)(set * kTok), op = trow + kOBase;
-        const int prev = set == 0 ? kSets - 1 : set - 1;  // the set of the tile before
-        int tau0 = 0;
-#pragma unroll 1
-        for (int p = 0; !dead; ++p) {
-            const int d = p % kDescs;
-            if (!wait_for(&desc_full[d], (uint32_t)((p / kDescs) & 1), dead)) break;
-            const Piece &pc = descs[d];
-            const int n = pc.ntiles, pre = pc.pre;
-            if (n == 0) break;
-            // warps without rows only pass the barriers; the other rows of a warp with some go by the last query's keys
-            const bool live_warp = wq * 32 < pc.nrows;
-            const int qi = min(rq, pc.nq - 1);
-            RowState st;
-            st.m = KIND == kCap ? a.m0 : -INFINITY;
-            st.l = 0.f;
-            st.p = pc.pos0 + qi;
-            st.r = key_range(max(pc.ks0, key_start_of(a.s, (int64_t)pc.row0 + qi)), pre, a.s.window, st.p, st.p);
-            st.slope2 = 0.f;
-            if constexpr (KIND == kBias || KIND == kCapBias)
-                st.slope2 = a.s.slopes ? a.s.slopes[pc.kvh * G + rh] * 1.44269504f : 0.f;
-            const KeyRange cr{pc.ks0, pc.cpre, pc.lo, pc.hi};
-            bool any = false;
-            int j = set - tau0 % kSets;
-            if (j < 0) j += kSets;
-#pragma unroll 1
-            for (; j < n; j += kSets) {
-                const int tau = tau0 + j, turn = tau / kSets;
-                wait_for(&s_full[set], (uint32_t)(turn & 1), dead);
-                if (dead) break;
-                tc::fence_after();
-                const TileRec rec = recs[tau % kRecs];
-                // the tile before's barriers have come round as often as this one's, one time less for the first set
-                const int bturn = set == 0 ? turn - 1 : turn;
-                Chain ch;
-                ch.mref = mref + rr;
-                ch.start = start_ref + (p & 3) * kRows + rr;
-                ch.started = &started[(p & 3) * 4 + wq];
-                ch.start_parity = (uint32_t)((p >> 2) & 1);
-                ch.begun = any;
-                ch.before = tau > 0 ? &m_full[prev * 4 + wq] : nullptr;
-                ch.mine = &m_full[set * 4 + wq];
-                ch.done = &o_done[prev];
-                ch.parity = (uint32_t)(bturn & 1);
-                ch.first = j == 0;
-                if (live_warp) {
-                    softmax_tile<D, KIND>(sp, op, rec, a, rec.t0 < pre, st, ch, lane, dead);
-                } else if (KIND != kCap) {
-                    if (ch.before) wait_for(ch.before, ch.parity, dead);
-                    __syncwarp();
+                    const bool live = id != INT_MIN, bad = live && (id < 0 || id >= a.num_blocks);
+                    const uint32_t nlive = (uint32_t)__popc(__ballot_sync(0xffffffffu, live)), badm = __ballot_sync(0xffffffffu, bad);
                     if (lane == 0) {
-                        if (ch.first) mbar_arrive(ch.started);
-                        mbar_arrive(ch.mine);
+                        if (isk && half == 0) {
+                            const int t0 = first_key(j);
+                            TileRec rec;
+                            rec.t0 = t0;
+                            rec.bad = badm;
+                            rec.whole = badm == 0u && ((t0 >= r.lo && t0 + kTok <= r.hi) || (t0 >= r.first && t0 + kTok <= r.pre));
+                            rec.full = badm == 0u && ((t0 >= flo && t0 + kTok <= fhi) || (t0 >= fks && t0 + kTok <= pre));
+                            recs[tau % kRecs] = rec;
+                            if (badm) flag_error(a.err, PKV_DEVERR_BLOCK_ID);
+                        }
+                        mbar_arrive_expect_tx(&full[st], nlive * (uint32_t)((isk ? 1 : H) * 128) << a.bshift);
+                    }
+                    __syncwarp();
+                    // an invalid id is read as block 0, its keys masked
+                    if (live) {
+                        const int y = (int)(((int64_t)(bad ? 0 : id) * Hkv + kvh) * B);
+                        if (isk)
+                            tma_load_2d(k_s + st * L::kTile + half * (kTok * 128) + ((lane << a.bshift) * 128), &tm_k, smem_u32(&full[st]),
+                                        half * 64, y);
+                        else
+                            tma_load_3d(v_s + st * L::kTile + ((lane << a.bshift) * (H * 128)), &tm_v, smem_u32(&full[st]), 0, y, 0);
                     }
                 }
-                // V rows of keys that no row sees hold stale values, or none were loaded: zero weights must meet zeros
-                if (!rec.whole) {
-                    // A parity tells a stage's use from the one before it only, and P V is known to be complete up to tile
-                    // tau - kSets: the stage's use before has to be over first (it does not wait for this tile).
-                    const int st_v = tau % NV, used = tau - NV;
-                    if (NV < kSets && used >= 0) wait_for(&o_done[used % kSets], (uint32_t)((used / kSets) & 1), dead);
-                    wait_for(&v_full[st_v], (uint32_t)((tau / NV) & 1), dead);
-                    if (!cr.sees(rec.t0 + rr) || ((rec.bad >> (rr >> a.bshift)) & 1u)) {  // a thread per key
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&desc_empty[d]);
+            }
+            // copies in flight (only after a timeout) land before the CTA exits
+            if (lane == 0 && dead)
+#pragma unroll 1
+                for (int k = max(0, tau - N); k < tau; ++k) drain(&full[k % N], (uint32_t)((k / N) & 1));
+        } else if (warp == kMmaWarp) {
+            // ======================= Q K^T issuer =======================
+            // Both issuers walk as whole warps (uniform registers) and one elected lane issues.
+            constexpr uint32_t idesc = tc::instr_desc(kTok, false);
+            const bool leader = elect_one();
+            const uint64_t qd0 = tc::smem_desc(q_s, 16, 1024), kd0 = tc::smem_desc(k_s, 16, 1024);
+            int st = 0, sb = 0;            // K stage, S buffer
+            uint32_t kph = 0, sph = 1;     // their phases (a buffer's first use waits for nothing)
+            int d = 0, p = 0, tau = 0;
+            uint32_t dph = 0;
+#pragma unroll 1
+            for (;; ++p) {
+                wait_for(&desc_full[d], dph, dead);
+                const int n = dead ? 0 : descs[d].ntiles;
+                if (n == 0) break;
+                tau += n;
+                wait_for(&q_full[p & 1], (uint32_t)((p >> 1) & 1), dead);
+                const uint64_t qd = qd0 + (uint64_t)((uint32_t)(p & 1) * (uint32_t)(L::kQTile >> 4));
+#pragma unroll 1
+                for (int j = 0; j < n; ++j) {
+                    wait_for(&k_full[st], kph, dead);
+                    wait_for(&o_done[sb], sph, dead);  // the P V that read the buffer before
+                    if (dead) break;
+                    tc::fence_after();
+                    const uint64_t kd = kd0 + (uint64_t)((uint32_t)st * (uint32_t)(L::kTile >> 4));
+                    if (leader) {
+#pragma unroll 1  // (the shorter code leaves more of the instruction cache to the softmax)
+                        for (int k = 0; k < D / 16; ++k) {
+                            const uint64_t off = (uint64_t)(((k >> 2) * (kTok * 128) + (k & 3) * 32) >> 4);
+                            tc::mma(tmem + (uint32_t)sb * kTok, qd + off, kd + off, idesc, k > 0 ? 1u : 0u);
+                        }
+                        tc::commit(&s_full[sb]);
+                        tc::commit(&k_empty[st]);
+                        if (j + 1 == n) tc::commit(&q_empty[p & 1]);
+                    }
+                    __syncwarp();
+                    if (++st == NK) st = 0, kph ^= 1u;
+                    if (++sb == kSets) sb = 0, sph ^= 1u;
+                }
+                if (lane == 0) mbar_arrive(&desc_empty[d]);
+                if (++d == kDescs) d = 0, dph ^= 1u;
+            }
+            if (lane == 0) scratch[0] = tau, scratch[1] = p;
+            if (leader) tc::commit(&all_done[0]);
+            __syncwarp();
+            drain(&all_done[0], 0u);
+        } else if (warp == kPvWarp) {
+            // ======================= P V issuer =======================
+            constexpr uint32_t idesc = tc::instr_desc(D, true);
+            const uint32_t pv_lbo = (uint32_t)(B * 128), pv_sbo = B >= 16 ? 1024u : (uint32_t)(H * B * 128);
+            const bool leader = elect_one();
+            const uint64_t vd0 = tc::smem_desc(v_s, pv_lbo, pv_sbo);
+            // 16 keys of V further: inside a block of 32 every second step, else a block (B = 8: two)
+            const uint32_t odd = B == 32 ? 16 * 128 >> 4 : (uint32_t)(H * 16 * 128) >> 4, two = (uint32_t)(2 * H * 16 * 128) >> 4;
+            int st = 0, sb = 0;
+            uint32_t vph = 0, sph = 0;
+            int d = 0;
+            uint32_t dph = 0;
+#pragma unroll 1
+            for (int p = 0;; ++p) {
+                wait_for(&desc_full[d], dph, dead);
+                const int n = dead ? 0 : descs[d].ntiles;
+                if (n == 0) break;
+                if (p > 0) wait_for(o_free, (uint32_t)((p - 1) & 1), dead);  // the piece before's O has been read
+#pragma unroll 1
+                for (int j = 0; j < n; ++j) {
+                    wait_for(&v_full[st], vph, dead);
+                    wait_for(&p_full[sb], sph, dead);
+                    if (dead) break;
+                    tc::fence_after();
+                    const uint64_t vd = vd0 + (uint64_t)((uint32_t)st * (uint32_t)(L::kTile >> 4));
+                    if (leader) {
+#pragma unroll 1  // (the shorter code leaves more of the instruction cache to the softmax)
+                        for (int k = 0; k < kTok / 16; ++k)
+                            tc::mma_ts(tmem + kOBase, tmem + (uint32_t)(sb * kTok + 8 * k),
+                                       vd + (uint64_t)((uint32_t)(k >> 1) * two + (uint32_t)(k & 1) * odd), idesc, j > 0 || k > 0 ? 1u : 0u);
+                        tc::commit(&o_done[sb]);
+                        tc::commit(&v_empty[st]);
+                        if (j + 1 == n) tc::commit(o_last);
+                    }
+                    __syncwarp();
+                    if (++st == NV) st = 0, vph ^= 1u;
+                    if (++sb == kSets) sb = 0, sph ^= 1u;
+                }
+                if (lane == 0) mbar_arrive(&desc_empty[d]);
+                if (++d == kDescs) d = 0, dph ^= 1u;
+            }
+            // every product has completed before the tensor memory is freed
+            if (leader) tc::commit(&all_done[1]);
+            __syncwarp();
+            drain(&all_done[1], 0u);
+        } else if (warp < kEpiWarp) {
+            // ======================= softmax =======================
+            const int set = warp >> 2, wq = warp & 3;
+            const int rr = wq * 32 + lane;  // TMEM lane and row of the context
+            const int rq = rr / G, rh = rr - rq * G;  // its query and head
+            const uint32_t trow = tmem + ((uint32_t)(wq * 32) << 16);
+            const uint32_t sp = trow + (uint32_t)(set * kTok), op = trow + kOBase;
+            const int prev = set == 0 ? kSets - 1 : set - 1;  // the set of the tile before
+            int tau0 = 0;
+#pragma unroll 1
+            for (int p = 0; !dead; ++p) {
+                const int d = p % kDescs;
+                if (!wait_for(&desc_full[d], (uint32_t)((p / kDescs) & 1), dead)) break;
+                const Piece &pc = descs[d];
+                const int n = pc.ntiles, pre = pc.pre;
+                if (n == 0) break;
+                // warps without rows only pass the barriers; the other rows of a warp with some go by the last query's keys
+                const bool live_warp = wq * 32 < pc.nrows;
+                const int qi = min(rq, pc.nq - 1);
+                RowState st;
+                st.m = KIND == kCap ? a.m0 : -INFINITY;
+                st.l = 0.f;
+                st.p = pc.pos0 + qi;
+                st.r = key_range(max(pc.ks0, key_start_of(a.s, (int64_t)pc.row0 + qi)), pre, a.s.window, st.p, st.p);
+                st.slope2 = 0.f;
+                if constexpr (KIND == kBias || KIND == kCapBias)
+                    st.slope2 = a.s.slopes ? a.s.slopes[pc.kvh * G + rh] * 1.44269504f : 0.f;
+                const KeyRange cr{pc.ks0, pc.cpre, pc.lo, pc.hi};
+                bool any = false, taken = false;
+                int j = set - tau0 % kSets;
+                if (j < 0) j += kSets;
+#pragma unroll 1
+                for (; j < n; j += kSets) {
+                    const int tau = tau0 + j, turn = tau / kSets;
+                    wait_for(&s_full[set], (uint32_t)(turn & 1), dead);
+                    if (dead) break;
+                    tc::fence_after();
+                    const TileRec rec = recs[tau % kRecs];
+                    // the tile before's barriers have come round as often as this one's, one time less for the first set
+                    const int bturn = set == 0 ? turn - 1 : turn;
+                    Chain ch;
+                    ch.mref = mref + rr;
+                    ch.start = start_ref + (p & 3) * kRows + rr;
+                    ch.started = &started[(p & 3) * 4 + wq];
+                    ch.start_parity = (uint32_t)((p >> 2) & 1);
+                    ch.begun = any;
+                    ch.before = tau > 0 ? &m_full[prev * 4 + wq] : nullptr;
+                    ch.mine = &m_full[set * 4 + wq];
+                    ch.done = &o_done[prev];
+                    ch.parity = (uint32_t)(bturn & 1);
+                    ch.first = j == 0;
+                    if (live_warp) {
+                        softmax_tile<D, KIND>(sp, op, rec, a, rec.t0 < pre, st, ch, lane, dead);
+                    } else if (KIND != kCap) {
+                        if (ch.before) wait_for(ch.before, ch.parity, dead);
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (ch.first) mbar_arrive(ch.started);
+                            mbar_arrive(ch.mine);
+                        }
+                    }
+                    // V rows of keys that no row sees hold stale values, or none were loaded: zero weights must meet zeros
+                    if (!rec.whole || (careful && !rec.full)) {
+                        // A parity tells a stage's use from the one before it only, and P V is known to be complete up to tile
+                        // tau - kSets: the stage's use before has to be over first (it does not wait for this tile).
+                        const int st_v = tau % NV, used = tau - NV;
+                        if (NV < kSets && used >= 0) wait_for(&o_done[used % kSets], (uint32_t)((used / kSets) & 1), dead);
+                        wait_for(&v_full[st_v], (uint32_t)((tau / NV) & 1), dead);
                         const uint32_t row = v_s + (uint32_t)st_v * L::kTile + (rr >> a.bshift) * (H * 128 << a.bshift) +
                                              (rr & (B - 1)) * 128;
+                        if (!cr.sees(rec.t0 + rr) || ((rec.bad >> (rr >> a.bshift)) & 1u)) {  // a thread per key
 #pragma unroll 4
-                        for (int i = 0; i < 8 * H; ++i)
-                            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(row + (i >> 3) * (128 << a.bshift) +
-                                                                                       ((i + lane) & 7) * 16),
-                                         "r"(0u)
-                                         : "memory");
+                            for (int i = 0; i < 8 * H; ++i)
+                                asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(row + (i >> 3) * (128 << a.bshift) +
+                                                                                           ((i + lane) & 7) * 16),
+                                             "r"(0u)
+                                             : "memory");
+                        } else if (careful && !rec.full) {
+                            taken = clean_row<H>(row, 128 << a.bshift, lane) || taken;
+                        }
+                        fence_proxy_async();
                     }
-                    fence_proxy_async();
+                    any = true;
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_full[set]);
                 }
-                any = true;
+                if (dead) break;
+                tau0 += n;
+                // the piece's reference and sum of this set's tiles, for the epilogue
+                const int f = p & 1;
+                if (p >= 2) wait_for(&fin_empty[f], (uint32_t)((p / 2 - 1) & 1), dead);
+                fin_ml[(f * kSets + set) * kRows + rr] = make_float2(any ? st.m : -INFINITY, st.l);
+                if (careful) taken = __any_sync(0xffffffffu, taken);
+                __syncwarp();
+                if (lane == 0) {
+                    if (careful) fin_bad[f * 4 * kSets + warp] = taken;
+                    mbar_arrive(&fin_full[f]);
+                    mbar_arrive(&desc_empty[d]);
+                }
+            }
+        } else if (warp < kEpiWarp + 4) {
+            // ======================= epilogue =======================
+            const int wq = warp & 3, rr = wq * 32 + lane;
+            const int64_t rel = ((int64_t)(rr / G) * a.num_heads + rr % G) * D;
+            const uint32_t op = tmem + ((uint32_t)(wq * 32) << 16) + kOBase;
+#pragma unroll 1
+            for (int p = 0; !dead; ++p) {
+                const int d = p % kDescs, f = p & 1;
+                if (!wait_for(&desc_full[d], (uint32_t)((p / kDescs) & 1), dead)) break;
+                const Piece &pc = descs[d];
+                if (pc.ntiles == 0) break;
+                const int nrows = pc.nrows, slot = pc.slot;
+                const int64_t orow = ((int64_t)pc.row0 * a.num_heads + pc.kvh * G) * D + rel;
+                wait_for(&fin_full[f], (uint32_t)((p >> 1) & 1), dead);
+                float2 x[kSets];
+#pragma unroll
+                for (int i = 0; i < kSets; ++i) x[i] = fin_ml[(f * kSets + i) * kRows + rr];
+                const bool taken = careful && __any_sync(0xffffffffu, lane < 4 * kSets && fin_bad[f * 4 * kSets + lane] != 0);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&fin_empty[f]);
+                float M = x[0].x, l = 0.f;
+#pragma unroll
+                for (int i = 1; i < kSets; ++i) M = fmaxf(M, x[i].x);
+#pragma unroll
+                for (int i = 0; i < kSets; ++i)  // (a set without a tile: l = 0)
+                    l += x[i].x == -INFINITY || x[i].x == M ? x[i].y : x[i].y * ex2_approx(x[i].x - M);
+                const float inv = l != 0.f ? 1.f / l : 0.f;
+                wait_for(o_last, (uint32_t)(p & 1), dead);
+                if (dead) break;
+                tc::fence_after();
+                const bool live = rr < nrows;
+                if (taken && wq * 32 < nrows) {
+                    const int qi = min(rr / G, pc.nq - 1), pos = pc.pos0 + qi;
+                    add_odd_values<D>(a, pc, key_range(max(pc.ks0, key_start_of(a.s, (int64_t)pc.row0 + qi)), pc.pre, a.s.window, pos, pos),
+                                      op, lane);
+                }
+                // Every row of the product meets every V entry, so any row tells whether a column did: the warps share the columns.
+                uint64_t odd[2] = {0ull, 0ull};  // NaN once an output is infinite or NaN
+                int look = wq * 16;
+                if (wq * 32 < nrows) {
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 16) {
+                        float o[16];
+                        ld16(op + (uint32_t)c, o);
+                        tc::wait_ld();
+                        if (c == look) {
+                            look += (nrows + 31) / 32 * 16;
+#pragma unroll
+                            for (int k = 0; k < 16; k += 2) odd[(k >> 1) & 1] = fma_f32x2(f32x2(o[k], o[k + 1]), 0ull, odd[(k >> 1) & 1]);
+                        }
+                        if (slot < 0) {
+                            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow + c);
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const uint4 v = make_uint4(pack_bf16x2(o[8 * k] * inv, o[8 * k + 1] * inv),
+                                                           pack_bf16x2(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
+                                                           pack_bf16x2(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
+                                                           pack_bf16x2(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+                                if (live) dst[k] = v;
+                            }
+                        } else {
+                            float *dst = a.part_o + ((int64_t)slot * D + c) * kRows + rr;
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) dst[k * kRows] = o[k];
+                        }
+                    }
+                    if (slot >= 0) reinterpret_cast<float2 *>(a.part_ml)[(int64_t)slot * kRows + rr] = make_float2(M, l);
+                }
+                float odd0, odd1;
+                f32x2_split(add_f32x2(odd[0], odd[1]), odd0, odd1);
+                if (live && odd0 + odd1 != 0.f) *redo = 1;
                 tc::fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[set]);
-            }
-            if (dead) break;
-            tau0 += n;
-            // the piece's reference and sum of this set's tiles, for the epilogue
-            const int f = p & 1;
-            if (p >= 2) wait_for(&fin_empty[f], (uint32_t)((p / 2 - 1) & 1), dead);
-            fin_ml[(f * kSets + set) * kRows + rr] = make_float2(any ? st.m : -INFINITY, st.l);
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&fin_full[f]);
-                mbar_arrive(&desc_empty[d]);
+                if (lane == 0) mbar_arrive(o_free);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&desc_empty[d]);
             }
         }
-    } else if (warp < kEpiWarp + 4) {
-        // ======================= epilogue =======================
-        const int wq = warp & 3, rr = wq * 32 + lane;
-        const int64_t rel = ((int64_t)(rr / G) * a.num_heads + rr % G) * D;
-        const uint32_t op = tmem + ((uint32_t)(wq * 32) << 16) + kOBase;
+        tc::fence_before();
+        const bool gave_up = __syncthreads_or(dead);
+        tc::fence_after();
+        return gave_up || careful || *redo == 0;
+    };
+    if (!walk(std::false_type{})) {
+        // The barriers start anew: the issuers' last arrivals that no one has waited for come first.
+        if (threadIdx.x == 0) {
+            const int tau = scratch[0], p = scratch[1];
 #pragma unroll 1
-        for (int p = 0; !dead; ++p) {
-            const int d = p % kDescs, f = p & 1;
-            if (!wait_for(&desc_full[d], (uint32_t)((p / kDescs) & 1), dead)) break;
-            const Piece &pc = descs[d];
-            if (pc.ntiles == 0) break;
-            const int nrows = pc.nrows, slot = pc.slot;
-            const int64_t orow = ((int64_t)pc.row0 * a.num_heads + pc.kvh * G) * D + rel;
-            wait_for(&fin_full[f], (uint32_t)((p >> 1) & 1), dead);
-            float2 x[kSets];
-#pragma unroll
-            for (int i = 0; i < kSets; ++i) x[i] = fin_ml[(f * kSets + i) * kRows + rr];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&fin_empty[f]);
-            float M = x[0].x, l = 0.f;
-#pragma unroll
-            for (int i = 1; i < kSets; ++i) M = fmaxf(M, x[i].x);
-#pragma unroll
-            for (int i = 0; i < kSets; ++i)  // (a set without a tile: l = 0)
-                l += x[i].x == -INFINITY || x[i].x == M ? x[i].y : x[i].y * ex2_approx(x[i].x - M);
-            const float inv = l != 0.f ? 1.f / l : 0.f;
-            wait_for(o_last, (uint32_t)(p & 1), dead);
-            if (dead) break;
-            tc::fence_after();
-            const bool live = rr < nrows;
-            if (wq * 32 < nrows) {
+            for (int k = max(0, tau - NK); k < tau; ++k) wait_for(&k_empty[k % NK], (uint32_t)((k / NK) & 1), dead);
 #pragma unroll 1
-                for (int c = 0; c < D; c += 16) {
-                    float o[16];
-                    ld16(op + (uint32_t)c, o);
-                    tc::wait_ld();
-                    if (slot < 0) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow + c);
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const uint4 v = make_uint4(pack_bf16x2(o[8 * k] * inv, o[8 * k + 1] * inv),
-                                                       pack_bf16x2(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
-                                                       pack_bf16x2(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
-                                                       pack_bf16x2(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
-                            if (live) dst[k] = v;
-                        }
-                    } else {
-                        float *dst = a.part_o + ((int64_t)slot * D + c) * kRows + rr;
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) dst[k * kRows] = o[k];
-                    }
-                }
-                if (slot >= 0) reinterpret_cast<float2 *>(a.part_ml)[(int64_t)slot * kRows + rr] = make_float2(M, l);
-            }
-            tc::fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(o_free);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&desc_empty[d]);
+            for (int k = max(0, tau - NV); k < tau; ++k) wait_for(&v_empty[k % NV], (uint32_t)((k / NV) & 1), dead);
+#pragma unroll 1
+            for (int k = max(0, tau - kSets); k < tau; ++k) wait_for(&o_done[k % kSets], (uint32_t)((k / kSets) & 1), dead);
+#pragma unroll 1
+            for (int k = max(0, p - 2); k < p; ++k) wait_for(&q_empty[k & 1], (uint32_t)((k >> 1) & 1), dead);
         }
+        if (!__syncthreads_or(dead)) walk(std::true_type{});
     }
     if (dead) flag_error(a.err, PKV_DEVERR_TIMEOUT);
-    tc::fence_before();
-    __syncthreads();
     if (warp == kMmaWarp) {
-        tc::fence_after();
+        const uint32_t tmem = *tmem_slot;
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
     }
 }
