@@ -62,7 +62,7 @@ __device__ __forceinline__ KeyRange key_range(int ks, int pre, int window, int p
     KeyRange r;
     r.first = ks;
     r.pre = pre;
-    r.lo = max(ks, window > 0 ? p0 - window + 1 : 0);
+    r.lo = max(ks, window > 0 ? max(p0, 0) - window + 1 : 0);  // (before the context's first token every key is within reach)
     r.hi = p1 + 1;
     if (r.lo >= r.hi) {  // no key at or before p1
         r.lo = ks;

@@ -972,7 +972,7 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                                 pc.hi = c.r.hi;
                                 // what the last row's document or window leaves, up to the first row's position
                                 pc.fks = max(c.ks0, key_start_of(a.s, pc.row0 + nq - 1));
-                                pc.flo = max(pc.fks, a.s.window > 0 ? pc.pos0 + nq - a.s.window : 0);
+                                pc.flo = max(pc.fks, a.s.window > 0 ? max(pc.pos0 + nq, 1) - a.s.window : 0);
                                 pc.fhi = pc.pos0 + 1;
                                 const bool begins = begin + kCharge >= s0, ends = end <= s1;
                                 pc.slot = begins && ends ? -1 : 2 * (int)blockIdx.x + (begins ? 1 : 0);

@@ -102,3 +102,19 @@ def test_many_bad_values_end(value, kw):
     pools = c.pools()
     pools["v_cache"].fill_(value)
     assert not torch.isfinite(run(c, pools)).any()
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 40])
+@pytest.mark.parametrize("kind", ["decode", "multi"])
+def test_the_widest_window_is_none(kind, window):
+    """Also where a call has more queries than the context holds tokens (flagged): those before its first token see
+    nothing, the others what they see without a window."""
+    c = Case([20, 50, 3], qlens=[60, 50, 35] if kind == "multi" else None)
+    pools = c.pools()
+    want = run(c, pools)
+    c.window = window
+    got = run(c, pools)
+    assert torch.equal(bits(got), bits(want))
+    if kind == "multi":
+        assert pkv.read_device_errors(clear=True) == pkv.DEVERR_SEQ_LEN
+        assert torch.all(got[:40] == 0) and torch.all(got[40:60].abs().sum(-1) > 0)
