@@ -118,3 +118,13 @@ def test_the_widest_window_is_none(kind, window):
     if kind == "multi":
         assert pkv.read_device_errors(clear=True) == pkv.DEVERR_SEQ_LEN
         assert torch.all(got[:40] == 0) and torch.all(got[40:60].abs().sum(-1) > 0)
+
+
+@pytest.mark.parametrize("window", [-1, -2 ** 31, -2 ** 32, -2 ** 40])
+def test_negative_windows_are_refused(window):
+    for qlens in (None, [2, 2]):
+        c = Case([40, 40], qlens=qlens, window=0)
+        pools = c.pools()
+        c.window = window
+        with pytest.raises(pkv.PkvError):
+            run(c, pools)
