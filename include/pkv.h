@@ -389,7 +389,12 @@ PKV_EXPORT pkv_status kv_cache_read_fp8_rows(void *k_out, void *v_out, const voi
  * shapes and placement invariance are those of the plain calls; the workspace
  * holds at least ..._scored_workspace_size() bytes, 256-byte aligned (NULL
  * where that is 0), needs no initialisation, and calls that share one must be
- * ordered on the device.
+ * ordered on the device.  With L = min(max_seq_len, max_blocks_per_seq *
+ * block_size), batches of bf16 or FP8 caches whose longest possible contexts
+ * pass 2^30 tiles (num_seqs * num_kv_heads * (L / 16 + 5); several queries:
+ * num_seqs * num_kv_heads * C * (L / 128 + 3) with C = max_q_len / (128 / G) + 1
+ * for G query heads per KV head) are attended in parts, launch after launch; a
+ * single sequence that passes them returns PKV_ERR_UNSUPPORTED.
  *
  * paged_attention_decode_scored -- one query per sequence, p = seq_lens[s] - 1;
  * dtype F32 (float32 arithmetic throughout) or BF16 (float32 accumulation, the

@@ -6,6 +6,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
+#include <climits>
 #include <cmath>
 
 #include "pkv_internal.cuh"
@@ -131,11 +133,37 @@ struct Args {
     unsigned int *err;
 };
 
+// Laid-out tiles are counted in 32-bit integers: a batch that could have more takes a launch for each part of it.
+constexpr int64_t kMaxTiles = INT32_MAX / 2;
+
+// What a context can hold: the caller's limit, or what the block table addresses.
+inline int64_t longest_context(const Args &a) {
+    return std::min<int64_t>(a.max_seq_len, (int64_t)a.max_blocks * a.block_size);
+}
+
+// The call for sequences [s0, s0 + n) of a's.
+inline Args part_of(const Args &a, int head_dim, int s0, int n) {
+    Args p = a;
+    p.num_seqs = n;
+    p.block_tables += (int64_t)s0 * a.max_blocks;
+    p.seq_lens += s0;
+    if (a.s.prefix_lens) p.s.prefix_lens += s0;
+    if (a.q_starts) {  // rows of queries, and their first keys, count over the whole batch
+        p.q_starts += s0;
+    } else {
+        const int64_t at = (int64_t)s0 * a.num_heads * head_dim * 2;  // (bf16)
+        p.out = static_cast<char *>(a.out) + at;
+        p.q = static_cast<const char *>(a.q) + at;
+        p.num_q = n;
+        if (a.s.key_starts) p.s.key_starts += s0;
+    }
+    return p;
+}
+
 // Checks that the calls share; *empty: valid, and nothing to do.
 pkv_status check(const Args &a, int head_dim, int dtype, bool fp8, bool *empty);
 
 // One query per sequence over bf16 or row-scaled FP8 caches (scored_decode.cu).
-constexpr int kMaxDecodeSeqs = 8192;  // more go to the CUDA-core kernel
 size_t decode_workspace(int64_t num_seqs, int num_heads, int head_dim);
 pkv_status run_decode(const Args &a, int head_dim, void *workspace, size_t workspace_bytes, cudaStream_t st);
 

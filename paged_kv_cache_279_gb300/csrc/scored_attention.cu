@@ -2,14 +2,12 @@
 // a tanh or biased by distance and whose keys are limited by a window, a
 // document's start and an always visible prefix (scored.cuh has the rules).
 //   * scored_simt_kernel -- decode, one CTA per (sequence, kv head, 512-token
-//     partition) on CUDA cores, float32 arithmetic with expf and tanhf whatever
-//     the storage; scored_reduce_kernel merges the partitions.  It serves
-//     float32 caches, and batches of more than kMaxDecodeSeqs sequences.
+//     partition) on CUDA cores over float32 caches, float32 arithmetic with expf
+//     and tanhf; scored_reduce_kernel merges the partitions.
 //
-// With x_t the score of a seen key in base 2 and f_t its V row's scale (1 for
-// plain caches), the running state of a row is (M, l, o) with M = max_t x_t,
-// l = sum 2^(x_t - M), o = sum 2^(x_t - M) f_t v_t; states merge by rescaling
-// to the larger M, and the result is o / l (zeros when nothing is seen).
+// With x_t the score of a seen key, the running state of a row is (M, l, o) with
+// M = max_t x_t, l = sum e^(x_t - M), o = sum e^(x_t - M) v_t; states merge by
+// rescaling to the larger M, and the result is o / l (zeros when nothing is seen).
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -21,8 +19,6 @@ namespace pkv {
 namespace scored {
 
 constexpr int kPartition = 512;  // tokens per CTA of the CUDA-core kernel
-
-enum Storage { kF32 = 0, kBf16 = 1, kFp8Rows = 2 };
 
 struct SimtArgs : Args {
     float *part_o;   // [seqs][Hq][parts][D]
@@ -37,52 +33,23 @@ __device__ __forceinline__ int context_len(const Args &a, int seq, bool report) 
     return len;
 }
 
-template <typename T>
-__device__ __forceinline__ void put(T *p, float x);
-template <>
-__device__ __forceinline__ void put<float>(float *p, float x) { *p = x; }
-template <>
-__device__ __forceinline__ void put<__nv_bfloat16>(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
-__device__ __forceinline__ float get(float x) { return x; }
-__device__ __forceinline__ float get(__nv_bfloat16 x) { return __bfloat162float(x); }
-
-// N (2 or 4) consecutive elements of a cache row from element i on, N | i.
-template <int ST, int N>
-__device__ __forceinline__ void load_cached(const void *c, int64_t i, float (&x)[N]) {
-    if constexpr (ST == kF32) {
-        if constexpr (N == 4) {
-            const float4 v = *reinterpret_cast<const float4 *>(static_cast<const float *>(c) + i);
-            x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
-        } else {
-            const float2 v = *reinterpret_cast<const float2 *>(static_cast<const float *>(c) + i);
-            x[0] = v.x, x[1] = v.y;
-        }
-    } else if constexpr (ST == kBf16) {
-        const uint32_t *p = reinterpret_cast<const uint32_t *>(static_cast<const __nv_bfloat16 *>(c) + i);
-        uint32_t v[N / 2];
-        if constexpr (N == 4) {
-            const uint2 w = *reinterpret_cast<const uint2 *>(p);
-            v[0] = w.x, v[1] = w.y;
-        } else {
-            v[0] = *p;
-        }
-#pragma unroll
-        for (int k = 0; k < N / 2; ++k) x[2 * k] = bf16x2_lo(v[k]), x[2 * k + 1] = bf16x2_hi(v[k]);
+// N (2 or 4) consecutive elements of a cache row.
+template <int N>
+__device__ __forceinline__ void load_cached(const float *p, float (&x)[N]) {
+    if constexpr (N == 4) {
+        const float4 v = *reinterpret_cast<const float4 *>(p);
+        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
     } else {
-        const unsigned char *p = static_cast<const unsigned char *>(c) + i;
-        float y[4];
-        e4m3x4_to_float(N == 4 ? *reinterpret_cast<const uint32_t *>(p) : *reinterpret_cast<const uint16_t *>(p), y);
-#pragma unroll
-        for (int k = 0; k < N; ++k) x[k] = y[k];
+        const float2 v = *reinterpret_cast<const float2 *>(p);
+        x[0] = v.x, x[1] = v.y;
     }
 }
 
 // A warp takes eight tokens at once: four lanes share a token's K row (16-byte pieces in turn) for the scores of all heads,
 // and every lane owns D / 32 consecutive entries of the output.  Loads of sixteen rows are in flight; with a token at a
-// time, four float32 sequences of up to 100 tokens took 15 us instead of 6.
-template <int ST, int D>
+// time, four sequences of up to 100 tokens took 15 us instead of 6.
+template <int D>
 __global__ void __launch_bounds__(128) scored_simt_kernel(const SimtArgs a) {
-    using T = typename std::conditional<ST == kF32, float, __nv_bfloat16>::type;
     constexpr int NW = 4, E = D / 32, C = D / 16;  // C: 4-element pieces of a K row per lane
     __shared__ float so[NW][kGMax * D], sm[NW][kGMax], sl[NW][kGMax];
     __shared__ float4 sq[kGMax * D / 4];
@@ -95,8 +62,8 @@ __global__ void __launch_bounds__(128) scored_simt_kernel(const SimtArgs a) {
     const KeyRange kr = key_range(key_start_of(a.s, seq), prefix_of(a.s, seq, len), a.s.window, pos, pos);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, piece = lane & 3;
 
-    const T *qb = static_cast<const T *>(a.q) + ((int64_t)seq * a.num_heads + kvh * G) * D;
-    for (int i = threadIdx.x; i < G * D; i += 128) reinterpret_cast<float *>(sq)[i] = get(qb[i]);
+    const float *qb = static_cast<const float *>(a.q) + ((int64_t)seq * a.num_heads + kvh * G) * D;
+    for (int i = threadIdx.x; i < G * D; i += 128) reinterpret_cast<float *>(sq)[i] = qb[i];
     float o[kGMax][E], m[kGMax], l[kGMax], slope[kGMax];
 #pragma unroll
     for (int g = 0; g < kGMax; ++g) {
@@ -117,20 +84,16 @@ __global__ void __launch_bounds__(128) scored_simt_kernel(const SimtArgs a) {
             if (blk >= 0 && blk < a.num_blocks) row = ((int64_t)blk * a.num_kv_heads + kvh) * B + (t - lb * B);
             else if (piece == 0) flag_error(a.err, PKV_DEVERR_BLOCK_ID);
         }
-        float kf[C][4], vf[8][E], kscale = 1.f, vscale = 1.f;
+        float kf[C][4], vf[8][E];
         if (row >= 0) {
-            if constexpr (ST == kFp8Rows) {
-                kscale = row_scale(a.k_scales[row]);
-                vscale = row_scale(a.v_scales[row]);
-            }
 #pragma unroll
-            for (int c = 0; c < C; ++c) load_cached<ST, 4>(a.k_cache, row * D + 16 * c + 4 * piece, kf[c]);
+            for (int c = 0; c < C; ++c) load_cached(static_cast<const float *>(a.k_cache) + row * D + 16 * c + 4 * piece, kf[c]);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int64_t r = __shfl_sync(0xffffffffu, row, 4 * i);
             if (r >= 0) {
-                load_cached<ST, E>(a.v_cache, r * D + E * lane, vf[i]);
+                load_cached(static_cast<const float *>(a.v_cache) + r * D + E * lane, vf[i]);
             } else {
 #pragma unroll
                 for (int j = 0; j < E; ++j) vf[i][j] = 0.f;
@@ -150,7 +113,7 @@ __global__ void __launch_bounds__(128) scored_simt_kernel(const SimtArgs a) {
             }
             x += __shfl_xor_sync(0xffffffffu, x, 1);
             x += __shfl_xor_sync(0xffffffffu, x, 2);
-            x *= kscale * a.s.scale;
+            x *= a.s.scale;
             if (a.s.softcap > 0.f) x = a.s.softcap * tanhf(x / a.s.softcap);
             x -= slope[g] * away;
             if (row < 0) x = -INFINITY;
@@ -165,11 +128,11 @@ __global__ void __launch_bounds__(128) scored_simt_kernel(const SimtArgs a) {
                 for (int j = 0; j < E; ++j) o[g][j] *= al;
                 m[g] = mn;
             }
-            const float p = row >= 0 ? expf(x - mn) : 0.f, pv = p * vscale;
+            const float p = row >= 0 ? expf(x - mn) : 0.f;
             l[g] += p;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float w = __shfl_sync(0xffffffffu, pv, 4 * i);
+                const float w = __shfl_sync(0xffffffffu, p, 4 * i);
 #pragma unroll
                 for (int j = 0; j < E; ++j) o[g][j] = fmaf(w, vf[i][j], o[g][j]);
             }
@@ -205,7 +168,7 @@ __global__ void __launch_bounds__(128) scored_simt_kernel(const SimtArgs a) {
         }
         const int64_t row = (int64_t)seq * a.num_heads + kvh * G + g;
         if (whole) {
-            put(static_cast<T *>(a.out) + row * D + d, L != 0.f ? O / L : 0.f);
+            static_cast<float *>(a.out)[row * D + d] = L != 0.f ? O / L : 0.f;
         } else {
             const int64_t p = row * a.parts + part;
             a.part_o[p * D + d] = O;
@@ -218,7 +181,7 @@ __global__ void __launch_bounds__(128) scored_simt_kernel(const SimtArgs a) {
 }
 
 // One warp per (sequence, head): the partitions' states, merged in order.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(128) scored_reduce_kernel(const SimtArgs a) {
     constexpr int E = D / 32;
     grid_dependency_wait();
@@ -242,7 +205,7 @@ __global__ void __launch_bounds__(128) scored_reduce_kernel(const SimtArgs a) {
         for (int e = 0; e < E; ++e) o[e] = fmaf(c, po[(int64_t)j * D + 32 * e], o[e]);
     }
 #pragma unroll
-    for (int e = 0; e < E; ++e) put(static_cast<T *>(a.out) + row * D + lane + 32 * e, L != 0.f ? o[e] / L : 0.f);
+    for (int e = 0; e < E; ++e) static_cast<float *>(a.out)[row * D + lane + 32 * e] = L != 0.f ? o[e] / L : 0.f;
 }
 
 static size_t simt_workspace(int64_t seqs, int64_t heads, int64_t D, int64_t max_seq_len) {
@@ -250,9 +213,8 @@ static size_t simt_workspace(int64_t seqs, int64_t heads, int64_t D, int64_t max
     return parts <= 1 ? 0 : round256((size_t)(seqs * heads * parts * D * 4)) + round256((size_t)(seqs * heads * parts * 8));
 }
 
-template <int ST, int D>
+template <int D>
 static pkv_status run_simt(const Args &args, void *workspace, size_t bytes, cudaStream_t st) {
-    using T = typename std::conditional<ST == kF32, float, __nv_bfloat16>::type;
     SimtArgs a{};
     static_cast<Args &>(a) = args;
     a.parts = std::max(1, (a.max_seq_len + kPartition - 1) / kPartition);
@@ -266,10 +228,26 @@ static pkv_status run_simt(const Args &args, void *workspace, size_t bytes, cuda
                                               round256((size_t)a.num_seqs * a.num_heads * a.parts * D * 4));
     }
     const dim3 grid((unsigned)a.num_seqs, (unsigned)a.num_kv_heads, (unsigned)a.parts);
-    pkv_status rc = launch_pdl(scored_simt_kernel<ST, D>, grid, dim3(128), 0, st, a);
+    pkv_status rc = launch_pdl(scored_simt_kernel<D>, grid, dim3(128), 0, st, a);
     if (rc == PKV_OK && a.parts > 1)
-        rc = launch_pdl(scored_reduce_kernel<T, D>, dim3((unsigned)(((int64_t)a.num_seqs * a.num_heads + 3) / 4)), dim3(128), 0, st, a);
+        rc = launch_pdl(scored_reduce_kernel<D>, dim3((unsigned)(((int64_t)a.num_seqs * a.num_heads + 3) / 4)), dim3(128), 0, st, a);
     return rc;
+}
+
+// max_seq_len 0: no context holds a token, and every row is zeros.
+__global__ void __launch_bounds__(256) scored_zero_kernel(const Args a, int64_t chunks) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
+    for (int64_t i = i0; i < chunks; i += step) static_cast<uint4 *>(a.out)[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int64_t s = i0; s < a.num_seqs; s += step) context_len(a, (int)s, true);
+}
+
+// bf16 and row-scaled FP8 caches
+static pkv_status decode_any_length(const Args &a, int head_dim, void *workspace, size_t bytes, cudaStream_t st) {
+    if (a.max_seq_len > 0) return run_decode(a, head_dim, workspace, bytes, st);
+    const int64_t chunks = (int64_t)a.num_seqs * a.num_heads * head_dim / 8;
+    return launch_pdl(scored_zero_kernel, dim3((unsigned)std::min<int64_t>((chunks + 255) / 256, 65536)), dim3(256), 0, st, a, chunks);
 }
 
 pkv_status check(const Args &a, int head_dim, int dtype, bool fp8, bool *empty) {
@@ -309,9 +287,9 @@ using namespace pkv;
 
 PKV_API size_t paged_attention_decode_scored_workspace_size(int num_seqs, int num_heads, int head_dim, int max_seq_len) {
     if (num_seqs <= 0 || num_heads <= 0 || head_dim <= 0 || max_seq_len <= 0) return 0;
-    // whatever the type: the tensor-core kernel's and the CUDA-core kernel's (float32, very many sequences)
+    // whatever the type: the tensor-core kernel's and the CUDA-core kernel's (float32)
     return std::max(scored::simt_workspace(num_seqs, num_heads, head_dim, max_seq_len),
-                    num_seqs <= scored::kMaxDecodeSeqs ? scored::decode_workspace(num_seqs, num_heads, head_dim) : 0);
+                    scored::decode_workspace(num_seqs, num_heads, head_dim));
 }
 
 PKV_API size_t paged_attention_multi_token_scored_workspace_size(int num_q_tokens, int num_heads, int head_dim,
@@ -351,11 +329,9 @@ PKV_API pkv_status paged_attention_decode_scored(void *out, const void *q, const
         if (rc != PKV_OK) return rc;
     }
     if (dtype == PKV_F32)
-        return head_dim == 128 ? scored::run_simt<scored::kF32, 128>(a, workspace, workspace_bytes, st)
-                               : scored::run_simt<scored::kF32, 64>(a, workspace, workspace_bytes, st);
-    if (num_seqs <= scored::kMaxDecodeSeqs && max_seq_len > 0) return scored::run_decode(a, head_dim, workspace, workspace_bytes, st);
-    return head_dim == 128 ? scored::run_simt<scored::kBf16, 128>(a, workspace, workspace_bytes, st)
-                           : scored::run_simt<scored::kBf16, 64>(a, workspace, workspace_bytes, st);
+        return head_dim == 128 ? scored::run_simt<128>(a, workspace, workspace_bytes, st)
+                               : scored::run_simt<64>(a, workspace, workspace_bytes, st);
+    return scored::decode_any_length(a, head_dim, workspace, workspace_bytes, st);
 }
 
 PKV_API pkv_status paged_attention_decode_scored_fp8_rows(
@@ -378,9 +354,7 @@ PKV_API pkv_status paged_attention_decode_scored_fp8_rows(
     if (rc != PKV_OK || empty) return rc;
     a.err = device_error_word();
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (num_seqs <= scored::kMaxDecodeSeqs && max_seq_len > 0) return scored::run_decode(a, head_dim, workspace, workspace_bytes, st);
-    return head_dim == 128 ? scored::run_simt<scored::kFp8Rows, 128>(a, workspace, workspace_bytes, st)
-                           : scored::run_simt<scored::kFp8Rows, 64>(a, workspace, workspace_bytes, st);
+    return scored::decode_any_length(a, head_dim, workspace, workspace_bytes, st);
 }
 
 PKV_API pkv_status paged_attention_multi_token_scored(

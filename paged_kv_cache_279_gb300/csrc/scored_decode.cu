@@ -39,6 +39,7 @@ namespace {
 
 constexpr int kNW = 4, kNS = 2;   // warps per CTA, ring stages per warp
 constexpr int kMaxWarps = 2048;   // partial slots in the workspace: two per warp
+constexpr int kMaxSeqs = 8192;    // of a launch: their tiles' table is in shared memory
 
 template <int D, bool F8>
 struct Tile {
@@ -757,7 +758,7 @@ template <int D, bool F8>
 pkv_status launch(const DecodeArgs &a, cudaStream_t st) {
     static bool done[128] = {};
     auto kern = scored_decode_kernel<D, F8>;
-    if (!ensure_smem(kern, Smem<D, F8>(kMaxDecodeSeqs).total, done)) return PKV_ERR_CUDA;
+    if (!ensure_smem(kern, Smem<D, F8>(kMaxSeqs).total, done)) return PKV_ERR_CUDA;
     const int smem = Smem<D, F8>(a.num_seqs).total;
     // CTAs per SM, asked once per shared-memory size in a row (the devices of a process are alike): (size << 8) | CTAs
     static std::atomic<int64_t> known{0};
@@ -790,7 +791,7 @@ pkv_status launch(const DecodeArgs &a, cudaStream_t st) {
 
 size_t decode_workspace(int64_t num_seqs, int num_heads, int head_dim) {
     // for any grouping: G <= 8 heads a KV head, at most num_heads segments a sequence
-    return WsLayout(num_seqs * num_heads, std::min(num_heads, kGMax), head_dim).total;
+    return WsLayout(std::min<int64_t>(num_seqs, kMaxSeqs) * num_heads, std::min(num_heads, kGMax), head_dim).total;
 }
 
 pkv_status run_decode(const Args &args, int head_dim, void *workspace, size_t workspace_bytes, cudaStream_t st) {
@@ -801,19 +802,26 @@ pkv_status run_decode(const Args &args, int head_dim, void *workspace, size_t wo
     static_cast<Args &>(a) = args;
     if (a.s.softcap > kNoCap) a.s.softcap = 0.f;
     const bool fp8 = a.k_scales != nullptr;
-    // laid-out tiles are counted in 32-bit integers
-    if ((int64_t)a.num_seqs * a.num_kv_heads * ((a.max_seq_len + 15) / 16 + 4) > INT32_MAX / 2) return PKV_ERR_UNSUPPORTED;
+    const int64_t most = std::min<int64_t>(kMaxSeqs, kMaxTiles / (a.num_kv_heads * ((longest_context(a) + 15) / 16 + 4)));
+    if (most < 1) return PKV_ERR_UNSUPPORTED;
     const double log2e = 1.4426950408889634;
     a.c2 = finite_float(a.s.softcap * log2e);
     a.k1 = finite_float(a.s.softcap > 0.f ? 2.0 * a.s.scale / a.s.softcap * log2e : a.s.scale * log2e);
     a.bshift = a.block_size == 8 ? 3 : a.block_size == 16 ? 4 : 5;
-    const WsLayout lay((int64_t)a.num_seqs * a.num_kv_heads, a.group, head_dim);
+    const WsLayout lay(std::min<int64_t>(a.num_seqs, most) * a.num_kv_heads, a.group, head_dim);
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     a.part_o = reinterpret_cast<float *>(ws + lay.o);
     a.part_ml = reinterpret_cast<float *>(ws + lay.ml);
     a.segs = reinterpret_cast<int2 *>(ws + lay.segs);
-    if (fp8) return head_dim == 128 ? launch<128, true>(a, st) : launch<64, true>(a, st);
-    return head_dim == 128 ? launch<128, false>(a, st) : launch<64, false>(a, st);
+    const ScoreArgs score = a.s;
+    pkv_status rc = PKV_OK;
+    for (int64_t s0 = 0; s0 < args.num_seqs && rc == PKV_OK; s0 += most) {  // (a part begins when the one before is through)
+        static_cast<Args &>(a) = part_of(args, head_dim, (int)s0, (int)std::min<int64_t>(most, args.num_seqs - s0));
+        a.s.softcap = score.softcap;
+        if (fp8) rc = head_dim == 128 ? launch<128, true>(a, st) : launch<64, true>(a, st);
+        else rc = head_dim == 128 ? launch<128, false>(a, st) : launch<64, false>(a, st);
+    }
+    return rc;
 }
 
 }  // namespace scored

@@ -1508,12 +1508,12 @@ pkv_status run_rows(const Args &args, int head_dim, void *workspace, size_t work
     if (a.s.softcap > kNoCap) a.s.softcap = 0.f;
     a.per_ctx = kRows / a.group;
     a.bshift = a.block_size == 8 ? 3 : a.block_size == 16 ? 4 : 5;
-    const int64_t blocks = ((int64_t)a.max_q_len + a.per_ctx - 1) / a.per_ctx;
+    const int64_t blocks = ((int64_t)std::min(a.max_q_len, a.num_q) + a.per_ctx - 1) / a.per_ctx;
     a.scan_w = 1;
     while (a.scan_w < 32 && a.scan_w < blocks) a.scan_w *= 2;
-    // laid-out tiles are counted in 32-bit integers
-    if ((int64_t)a.num_seqs * a.num_kv_heads > INT32_MAX / 2 / (blocks * ((a.max_seq_len + kTok - 1) / kTok + 1 + kCharge)))
-        return PKV_ERR_UNSUPPORTED;
+    // (the number of all queries is no bound of a part's contexts: query ranges may overlap)
+    const int64_t most = kMaxTiles / (a.num_kv_heads * blocks * ((longest_context(a) + kTok - 1) / kTok + 1 + kCharge));
+    if (most < 1) return PKV_ERR_UNSUPPORTED;
     const double log2e = 1.4426950408889634;
     a.k1 = finite_float(a.s.softcap > 0.f ? (double)a.s.scale / a.s.softcap : a.s.scale * log2e);
     a.c2 = finite_float(a.s.softcap * log2e);
@@ -1539,7 +1539,14 @@ pkv_status run_rows(const Args &args, int head_dim, void *workspace, size_t work
     a.part_o = reinterpret_cast<float *>(ws + lay.o);
     a.part_ml = reinterpret_cast<float *>(ws + lay.ml);
     a.merges = reinterpret_cast<int4 *>(ws + lay.merges);
-    return head_dim == 128 ? launch_kind<128>(a, st) : launch_kind<64>(a, st);
+    const float softcap = a.s.softcap;
+    pkv_status rc = PKV_OK;
+    for (int64_t s0 = 0; s0 < args.num_seqs && rc == PKV_OK; s0 += most) {  // (a part begins when the one before is through)
+        static_cast<Args &>(a) = part_of(args, head_dim, (int)s0, (int)std::min<int64_t>(most, args.num_seqs - s0));
+        a.s.softcap = softcap;
+        rc = head_dim == 128 ? launch_kind<128>(a, st) : launch_kind<64>(a, st);
+    }
+    return rc;
 }
 
 }  // namespace scored
