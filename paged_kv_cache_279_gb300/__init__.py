@@ -481,7 +481,8 @@ def paged_attention_multi_token_scored_workspace_size(num_q_tokens: int, num_hea
 
 def _int32(x) -> int:
     """A limit as the library's int: beyond its range the largest value, or -1 (refused)."""
-    return max(-1, min(int(x), 2 ** 31 - 1))
+    x = int(x)
+    return x if -1 <= x < 2 ** 31 else 2 ** 31 - 1 if x > 0 else -1
 
 
 def _scored_shapes(out, q, k_cache, v_cache, block_tables, seq_lens, alibi_slopes, prefix_lens, key_starts):
@@ -521,13 +522,13 @@ def paged_attention_decode_scored(out, q, k_cache, v_cache, block_tables, seq_le
     if k_new is not None and (k_new.shape != (S, Hkv, D) or v_new.shape != k_new.shape):
         raise ValueError("k_new/v_new must be [S, Hkv, D]")
     lib, code, dt, i32 = _lib.load(), _dtype_code(q), q.dtype, torch.int32
-    dev = _device_of(q, "q")
+    dev, max_len = _device_of(q, "q"), _int32(max_seq_len)
     _run_with_scratch(dev, "paged_attention_decode_scored", lib.paged_attention_decode_scored,
-                      lib.paged_attention_decode_scored_workspace_size, (S, Hq, D, _int32(max_seq_len)), (
+                      lib.paged_attention_decode_scored_workspace_size, (S, Hq, D, max_len), (
         _ptr(out, "out", dt, dev), _ptr(q, "q", dt, dev), _opt_ptr(k_new, "k_new", dt, dev),
         _opt_ptr(v_new, "v_new", dt, dev), _ptr(k_cache, "k_cache", dt, dev), _ptr(v_cache, "v_cache", dt, dev),
         _ptr(block_tables, "block_tables", i32, dev), _ptr(seq_lens, "seq_lens", i32, dev), S, Hq, Hkv, D, B, maxb, NB,
-        _int32(max_seq_len), float(scale), float(softcap), _opt_ptr(alibi_slopes, "alibi_slopes", torch.float32, dev),
+        max_len, float(scale), float(softcap), _opt_ptr(alibi_slopes, "alibi_slopes", torch.float32, dev),
         _int32(window),
         _opt_ptr(prefix_lens, "prefix_lens", i32, dev), _opt_ptr(key_starts, "key_starts", i32, dev)), workspace,
         (code, _stream_on(stream, dev)), stream)
@@ -547,13 +548,13 @@ def paged_attention_decode_scored_fp8_rows(out, q, k_cache, v_cache, k_scales, v
     if k_scales.shape != (NB, Hkv, B) or v_scales.shape != (NB, Hkv, B):
         raise ValueError("scales must be [NB, Hkv, B]")
     lib, bf, u8, i32 = _lib.load(), torch.bfloat16, torch.uint8, torch.int32
-    dev = _device_of(q, "q")
+    dev, max_len = _device_of(q, "q"), _int32(max_seq_len)
     _run_with_scratch(dev, "paged_attention_decode_scored_fp8_rows", lib.paged_attention_decode_scored_fp8_rows,
-                      lib.paged_attention_decode_scored_workspace_size, (S, Hq, D, _int32(max_seq_len)), (
+                      lib.paged_attention_decode_scored_workspace_size, (S, Hq, D, max_len), (
         _ptr(out, "out", bf, dev), _ptr(q, "q", bf, dev), _ptr(k_cache, "k_cache", u8, dev),
         _ptr(v_cache, "v_cache", u8, dev), _ptr(k_scales, "k_scales", u8, dev), _ptr(v_scales, "v_scales", u8, dev),
         _ptr(block_tables, "block_tables", i32, dev), _ptr(seq_lens, "seq_lens", i32, dev), S, Hq, Hkv, D, B, maxb, NB,
-        _int32(max_seq_len), float(scale), float(softcap), _opt_ptr(alibi_slopes, "alibi_slopes", torch.float32, dev),
+        max_len, float(scale), float(softcap), _opt_ptr(alibi_slopes, "alibi_slopes", torch.float32, dev),
         _int32(window),
         _opt_ptr(prefix_lens, "prefix_lens", i32, dev), _opt_ptr(key_starts, "key_starts", i32, dev)), workspace,
         (_stream_on(stream, dev),), stream)
@@ -574,13 +575,13 @@ def paged_attention_multi_token_scored(out, q, k_cache, v_cache, block_tables, s
     if q_starts.shape != (S + 1,):
         raise ValueError("q_starts must be [S + 1]")
     lib, bf, i32 = _lib.load(), torch.bfloat16, torch.int32
-    dev = _device_of(q, "q")
+    dev, max_len = _device_of(q, "q"), _int32(max_seq_len)
     _run_with_scratch(dev, "paged_attention_multi_token_scored", lib.paged_attention_multi_token_scored,
-                      lib.paged_attention_multi_token_scored_workspace_size, (T, Hq, D, _int32(max_seq_len)), (
+                      lib.paged_attention_multi_token_scored_workspace_size, (T, Hq, D, max_len), (
         _ptr(out, "out", bf, dev), _ptr(q, "q", bf, dev), _ptr(k_cache, "k_cache", bf, dev),
         _ptr(v_cache, "v_cache", bf, dev), _ptr(block_tables, "block_tables", i32, dev),
         _ptr(seq_lens, "seq_lens", i32, dev), _ptr(q_starts, "q_starts", i32, dev), S, T, Hq, Hkv, D, B, maxb, NB,
-        _int32(max_q_len), _int32(max_seq_len), float(scale), float(softcap),
+        _int32(max_q_len), max_len, float(scale), float(softcap),
         _opt_ptr(alibi_slopes, "alibi_slopes", torch.float32, dev), _int32(window),
         _opt_ptr(prefix_lens, "prefix_lens", i32, dev), _opt_ptr(key_starts, "key_starts", i32, dev)), workspace,
         (_stream_on(stream, dev),), stream)
