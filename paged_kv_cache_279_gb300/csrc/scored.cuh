@@ -165,7 +165,8 @@ pkv_status check(const Args &a, int head_dim, int dtype, bool fp8, bool *empty);
 
 // One query per sequence over bf16 or row-scaled FP8 caches (scored_decode.cu).
 size_t decode_workspace(int64_t num_seqs, int num_heads, int head_dim);
-pkv_status run_decode(const Args &a, int head_dim, void *workspace, size_t workspace_bytes, cudaStream_t st);
+bool decode_fits(const Args &a);  // one sequence's longest context can be counted
+pkv_status run_decode(const Args &a, int head_dim, void *workspace, cudaStream_t st);
 
 // Several queries per sequence on the tensor cores (scored_rows.cu).
 size_t rows_workspace(int head_dim);

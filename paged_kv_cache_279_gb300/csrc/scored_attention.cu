@@ -16,6 +16,12 @@
 #include "scored.cuh"
 
 namespace pkv {
+
+pkv_status append_new_tokens(const void *k_new, const void *v_new, void *k_cache, void *v_cache,
+                             const int32_t *block_tables, const int32_t *seq_lens, int num_seqs, int num_kv_heads,
+                             int head_dim, int block_size, int max_blocks_per_seq, int num_blocks, int max_seq_len,
+                             int dtype, cudaStream_t st);
+
 namespace scored {
 
 constexpr int kPartition = 512;  // tokens per CTA of the CUDA-core kernel
@@ -213,16 +219,20 @@ static size_t simt_workspace(int64_t seqs, int64_t heads, int64_t D, int64_t max
     return parts <= 1 ? 0 : round256((size_t)(seqs * heads * parts * D * 4)) + round256((size_t)(seqs * heads * parts * 8));
 }
 
+// What a call of a type needs.
+static size_t decode_need(int64_t seqs, int heads, int head_dim, int max_seq_len, int dtype) {
+    return dtype == PKV_F32 ? simt_workspace(seqs, heads, head_dim, max_seq_len) : decode_workspace(seqs, heads, head_dim);
+}
+
+static int simt_parts(const Args &a) { return std::max(1, (int)(((int64_t)a.max_seq_len + kPartition - 1) / kPartition)); }
+static bool simt_fits(const Args &a) { return a.num_kv_heads <= 65535 && simt_parts(a) <= 65535; }
+
 template <int D>
-static pkv_status run_simt(const Args &args, void *workspace, size_t bytes, cudaStream_t st) {
+static pkv_status run_simt(const Args &args, void *workspace, cudaStream_t st) {
     SimtArgs a{};
     static_cast<Args &>(a) = args;
-    a.parts = std::max(1, (a.max_seq_len + kPartition - 1) / kPartition);
-    if (a.num_kv_heads > 65535 || a.parts > 65535) return PKV_ERR_UNSUPPORTED;
+    a.parts = simt_parts(a);
     if (a.parts > 1) {
-        if (!workspace || bytes < simt_workspace(a.num_seqs, a.num_heads, D, a.max_seq_len) ||
-            (reinterpret_cast<uintptr_t>(workspace) & 255u))
-            return PKV_ERR_INVALID;
         a.part_o = static_cast<float *>(workspace);
         a.part_ml = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) +
                                               round256((size_t)a.num_seqs * a.num_heads * a.parts * D * 4));
@@ -243,9 +253,20 @@ __global__ void __launch_bounds__(256) scored_zero_kernel(const Args a, int64_t 
     for (int64_t s = i0; s < a.num_seqs; s += step) context_len(a, (int)s, true);
 }
 
-// bf16 and row-scaled FP8 caches
-static pkv_status decode_any_length(const Args &a, int head_dim, void *workspace, size_t bytes, cudaStream_t st) {
-    if (a.max_seq_len > 0) return run_decode(a, head_dim, workspace, bytes, st);
+// A valid call, its new tokens stored first: nothing is stored by one that is refused.
+static pkv_status decode(const Args &a, int head_dim, int dtype, const void *k_new, const void *v_new, void *workspace, size_t bytes,
+                         cudaStream_t st) {
+    if (!(dtype == PKV_F32 ? simt_fits(a) : decode_fits(a))) return PKV_ERR_UNSUPPORTED;
+    const size_t need = a.max_seq_len > 0 ? decode_need(a.num_seqs, a.num_heads, head_dim, a.max_seq_len, dtype) : 0;
+    if (need > 0 && (!workspace || bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u))) return PKV_ERR_INVALID;
+    if (k_new) {
+        const pkv_status rc = append_new_tokens(k_new, v_new, const_cast<void *>(a.k_cache), const_cast<void *>(a.v_cache),
+                                                a.block_tables, a.seq_lens, a.num_seqs, a.num_kv_heads, head_dim, a.block_size,
+                                                a.max_blocks, a.num_blocks, a.max_seq_len, dtype, st);
+        if (rc != PKV_OK) return rc;
+    }
+    if (dtype == PKV_F32) return head_dim == 128 ? run_simt<128>(a, workspace, st) : run_simt<64>(a, workspace, st);
+    if (a.max_seq_len > 0) return run_decode(a, head_dim, workspace, st);
     const int64_t chunks = (int64_t)a.num_seqs * a.num_heads * head_dim / 8;
     return launch_pdl(scored_zero_kernel, dim3((unsigned)std::min<int64_t>((chunks + 255) / 256, 65536)), dim3(256), 0, st, a, chunks);
 }
@@ -275,12 +296,6 @@ pkv_status check(const Args &a, int head_dim, int dtype, bool fp8, bool *empty) 
 }
 
 }  // namespace scored
-
-pkv_status append_new_tokens(const void *k_new, const void *v_new, void *k_cache, void *v_cache,
-                             const int32_t *block_tables, const int32_t *seq_lens, int num_seqs, int num_kv_heads,
-                             int head_dim, int block_size, int max_blocks_per_seq, int num_blocks, int max_seq_len,
-                             int dtype, cudaStream_t st);
-
 }  // namespace pkv
 
 using namespace pkv;
@@ -315,23 +330,12 @@ PKV_API pkv_status paged_attention_decode_scored(void *out, const void *q, const
     a.max_q_len = 1;
     a.s = ScoreArgs{scale, softcap, alibi_slopes, window, prefix_lens, key_starts};
     bool empty;
-    pkv_status rc = scored::check(a, head_dim, dtype, false, &empty);
+    const pkv_status rc = scored::check(a, head_dim, dtype, false, &empty);
     if (rc != PKV_OK || empty) return rc;
     if ((k_new == nullptr) != (v_new == nullptr) || !aligned16(k_new) || !aligned16(v_new)) return PKV_ERR_INVALID;
     if (k_new && max_seq_len < 1) return PKV_ERR_INVALID;  // every context holds at least its new token
     a.err = device_error_word();
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (!workspace && paged_attention_decode_scored_workspace_size(num_seqs, num_heads, head_dim, max_seq_len) > 0)
-        return PKV_ERR_INVALID;
-    if (k_new) {
-        rc = append_new_tokens(k_new, v_new, k_cache, v_cache, block_tables, seq_lens, num_seqs, num_kv_heads, head_dim,
-                               block_size, max_blocks_per_seq, num_blocks, max_seq_len, dtype, st);
-        if (rc != PKV_OK) return rc;
-    }
-    if (dtype == PKV_F32)
-        return head_dim == 128 ? scored::run_simt<128>(a, workspace, workspace_bytes, st)
-                               : scored::run_simt<64>(a, workspace, workspace_bytes, st);
-    return scored::decode_any_length(a, head_dim, workspace, workspace_bytes, st);
+    return scored::decode(a, head_dim, dtype, k_new, v_new, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
 }
 
 PKV_API pkv_status paged_attention_decode_scored_fp8_rows(
@@ -353,8 +357,7 @@ PKV_API pkv_status paged_attention_decode_scored_fp8_rows(
     const pkv_status rc = scored::check(a, head_dim, PKV_BF16, true, &empty);
     if (rc != PKV_OK || empty) return rc;
     a.err = device_error_word();
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return scored::decode_any_length(a, head_dim, workspace, workspace_bytes, st);
+    return scored::decode(a, head_dim, PKV_BF16, nullptr, nullptr, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
 }
 
 PKV_API pkv_status paged_attention_multi_token_scored(

@@ -794,16 +794,18 @@ size_t decode_workspace(int64_t num_seqs, int num_heads, int head_dim) {
     return WsLayout(std::min<int64_t>(num_seqs, kMaxSeqs) * num_heads, std::min(num_heads, kGMax), head_dim).total;
 }
 
-pkv_status run_decode(const Args &args, int head_dim, void *workspace, size_t workspace_bytes, cudaStream_t st) {
-    if (!workspace || workspace_bytes < decode_workspace(args.num_seqs, args.num_heads, head_dim) ||
-        (reinterpret_cast<uintptr_t>(workspace) & 255u))
-        return PKV_ERR_INVALID;
+static int64_t seqs_per_launch(const Args &a) {
+    return std::min<int64_t>(kMaxSeqs, kMaxTiles / (a.num_kv_heads * ((longest_context(a) + 15) / 16 + 4)));
+}
+
+bool decode_fits(const Args &a) { return seqs_per_launch(a) >= 1; }
+
+pkv_status run_decode(const Args &args, int head_dim, void *workspace, cudaStream_t st) {
     DecodeArgs a{};
     static_cast<Args &>(a) = args;
     if (a.s.softcap > kNoCap) a.s.softcap = 0.f;
     const bool fp8 = a.k_scales != nullptr;
-    const int64_t most = std::min<int64_t>(kMaxSeqs, kMaxTiles / (a.num_kv_heads * ((longest_context(a) + 15) / 16 + 4)));
-    if (most < 1) return PKV_ERR_UNSUPPORTED;
+    const int64_t most = seqs_per_launch(a);
     const double log2e = 1.4426950408889634;
     a.c2 = finite_float(a.s.softcap * log2e);
     a.k1 = finite_float(a.s.softcap > 0.f ? 2.0 * a.s.scale / a.s.softcap * log2e : a.s.scale * log2e);
