@@ -387,8 +387,9 @@ PKV_EXPORT pkv_status kv_cache_read_fp8_rows(void *k_out, void *v_out, const voi
  * Keys that no query of a call sees are not read (whole tiles of them).
  * scale may be any finite number.  workspace, error bits, zero rows, supported
  * shapes and placement invariance are those of the plain calls; the workspace
- * holds at least ..._scored_workspace_size() bytes, 256-byte aligned (NULL
- * where that is 0), needs no initialisation, and calls that share one must be
+ * holds at least ..._scored_workspace_size() bytes (decode:
+ * ..._workspace_size_for() of its type will do), 256-byte aligned (NULL where
+ * that is 0), needs no initialisation, and calls that share one must be
  * ordered on the device.  With L = min(max_seq_len, max_blocks_per_seq *
  * block_size), batches of bf16 or FP8 caches whose longest possible contexts
  * pass 2^30 tiles (num_seqs * num_kv_heads * (L / 16 + 5); several queries:
@@ -403,6 +404,10 @@ PKV_EXPORT pkv_status kv_cache_read_fp8_rows(void *k_out, void *v_out, const voi
  */
 PKV_EXPORT size_t paged_attention_decode_scored_workspace_size(int num_seqs, int num_heads, int head_dim,
                                                                int max_seq_len);
+/* The same for calls of one type: of q's dtype (BF16 for ..._fp8_rows, whose workspace does not grow with max_seq_len).
+ * Less than the above, which holds for every type. */
+PKV_EXPORT size_t paged_attention_decode_scored_workspace_size_for(int num_seqs, int num_heads, int head_dim,
+                                                                   int max_seq_len, int dtype);
 PKV_EXPORT pkv_status paged_attention_decode_scored(void *out, const void *q, const void *k_new, const void *v_new,
                                                     void *k_cache, void *v_cache, const int32_t *block_tables,
                                                     const int32_t *seq_lens, int num_seqs, int num_heads,

@@ -469,8 +469,16 @@ def kv_cache_read_fp8_rows(k_out, v_out, k_cache, v_cache, k_scales, v_scales, s
     return k_out, v_out
 
 
-def paged_attention_decode_scored_workspace_size(num_seqs: int, num_heads: int, head_dim: int, max_seq_len: int) -> int:
-    return int(_lib.load().paged_attention_decode_scored_workspace_size(num_seqs, num_heads, head_dim, max_seq_len))
+def paged_attention_decode_scored_workspace_size(num_seqs: int, num_heads: int, head_dim: int, max_seq_len: int,
+                                                 dtype: Optional[torch.dtype] = None) -> int:
+    """Bytes of workspace that paged_attention_decode_scored (q of that dtype) or, for bfloat16,
+    paged_attention_decode_scored_fp8_rows needs; without a dtype as much as any of them needs."""
+    lib, size = _lib.load(), (int(num_seqs), int(num_heads), int(head_dim), _int32(max_seq_len))
+    if dtype is None:
+        return int(lib.paged_attention_decode_scored_workspace_size(*size))
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
+    return int(lib.paged_attention_decode_scored_workspace_size_for(*size, PKV_F32 if dtype == torch.float32 else PKV_BF16))
 
 
 def paged_attention_multi_token_scored_workspace_size(num_q_tokens: int, num_heads: int, head_dim: int,
@@ -524,7 +532,7 @@ def paged_attention_decode_scored(out, q, k_cache, v_cache, block_tables, seq_le
     lib, code, dt, i32 = _lib.load(), _dtype_code(q), q.dtype, torch.int32
     dev, max_len = _device_of(q, "q"), _int32(max_seq_len)
     _run_with_scratch(dev, "paged_attention_decode_scored", lib.paged_attention_decode_scored,
-                      lib.paged_attention_decode_scored_workspace_size, (S, Hq, D, max_len), (
+                      lib.paged_attention_decode_scored_workspace_size_for, (S, Hq, D, max_len, code), (
         _ptr(out, "out", dt, dev), _ptr(q, "q", dt, dev), _opt_ptr(k_new, "k_new", dt, dev),
         _opt_ptr(v_new, "v_new", dt, dev), _ptr(k_cache, "k_cache", dt, dev), _ptr(v_cache, "v_cache", dt, dev),
         _ptr(block_tables, "block_tables", i32, dev), _ptr(seq_lens, "seq_lens", i32, dev), S, Hq, Hkv, D, B, maxb, NB,
@@ -550,7 +558,7 @@ def paged_attention_decode_scored_fp8_rows(out, q, k_cache, v_cache, k_scales, v
     lib, bf, u8, i32 = _lib.load(), torch.bfloat16, torch.uint8, torch.int32
     dev, max_len = _device_of(q, "q"), _int32(max_seq_len)
     _run_with_scratch(dev, "paged_attention_decode_scored_fp8_rows", lib.paged_attention_decode_scored_fp8_rows,
-                      lib.paged_attention_decode_scored_workspace_size, (S, Hq, D, max_len), (
+                      lib.paged_attention_decode_scored_workspace_size_for, (S, Hq, D, max_len, PKV_BF16), (
         _ptr(out, "out", bf, dev), _ptr(q, "q", bf, dev), _ptr(k_cache, "k_cache", u8, dev),
         _ptr(v_cache, "v_cache", u8, dev), _ptr(k_scales, "k_scales", u8, dev), _ptr(v_scales, "v_scales", u8, dev),
         _ptr(block_tables, "block_tables", i32, dev), _ptr(seq_lens, "seq_lens", i32, dev), S, Hq, Hkv, D, B, maxb, NB,

@@ -37,6 +37,7 @@ SIGNATURES = {
     "kv_cache_write_fp8_rows": (c_int, [c_void_p] * 7 + [c_int] * 6 + [c_void_p]),
     "kv_cache_read_fp8_rows": (c_int, [c_void_p] * 7 + [c_int] * 6 + [c_void_p]),
     "paged_attention_decode_scored_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int]),
+    "paged_attention_decode_scored_workspace_size_for": (c_size_t, [c_int, c_int, c_int, c_int, c_int]),
     "paged_attention_decode_scored": (c_int, [c_void_p] * 8 + [c_int] * 8 + [c_float, c_float, c_void_p, c_int,
                                               c_void_p, c_void_p, c_void_p, c_size_t, c_int, c_void_p]),
     "paged_attention_decode_scored_fp8_rows": (c_int, [c_void_p] * 8 + [c_int] * 8 +

@@ -303,8 +303,15 @@ using namespace pkv;
 PKV_API size_t paged_attention_decode_scored_workspace_size(int num_seqs, int num_heads, int head_dim, int max_seq_len) {
     if (num_seqs <= 0 || num_heads <= 0 || head_dim <= 0 || max_seq_len <= 0) return 0;
     // whatever the type: the tensor-core kernel's and the CUDA-core kernel's (float32)
-    return std::max(scored::simt_workspace(num_seqs, num_heads, head_dim, max_seq_len),
-                    scored::decode_workspace(num_seqs, num_heads, head_dim));
+    return std::max(scored::decode_need(num_seqs, num_heads, head_dim, max_seq_len, PKV_F32),
+                    scored::decode_need(num_seqs, num_heads, head_dim, max_seq_len, PKV_BF16));
+}
+
+PKV_API size_t paged_attention_decode_scored_workspace_size_for(int num_seqs, int num_heads, int head_dim, int max_seq_len,
+                                                                int dtype) {
+    if (num_seqs <= 0 || num_heads <= 0 || head_dim <= 0 || max_seq_len <= 0) return 0;
+    if (dtype != PKV_F32 && dtype != PKV_BF16) return 0;
+    return scored::decode_need(num_seqs, num_heads, head_dim, max_seq_len, dtype);
 }
 
 PKV_API size_t paged_attention_multi_token_scored_workspace_size(int num_q_tokens, int num_heads, int head_dim,

@@ -119,3 +119,19 @@ def test_parts_of_sequences_store_their_tokens_first():
     c.check(run(c, pools, k_new=torch.stack([k[-1] for k in c.ks]).cuda(), v_new=torch.stack([v[-1] for v in c.vs]).cuda()))
     for n in want:
         assert torch.equal(bits(pools[n]), bits(want[n]))
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "rows"])
+def test_the_workspace_of_a_type_suffices(kind):
+    """Exactly the bytes that the size call gives for the query's type, none for one that needs none."""
+    dt = torch.float32 if kind == "f32" else torch.bfloat16
+    for lens, maxL in (([700, 33, 2000], 131072), ([100, 7], 500)):
+        c = Case(lens, dtype=dt, rows=kind == "rows", softcap=20.0)
+        need = pkv.paged_attention_decode_scored_workspace_size(len(lens), c.Hq, c.D, maxL, dt)
+        ws = torch.randint(0, 256, (need + 256,), dtype=torch.uint8, device="cuda")
+        after = ws[need:].clone()
+        c.check(run(c, workspace=ws[:need] if need else None, max_seq_len=maxL))
+        assert torch.equal(ws[need:], after)
+        if need > 256:
+            with pytest.raises(pkv.PkvError):
+                run(c, workspace=ws[:need - 256], max_seq_len=maxL)
