@@ -610,6 +610,9 @@ scored_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             if (!dead && !wait_tile(&bars[buf], (uint32_t)((k / kNS) & 1))) {
                 if (lane == 0) flag_error(a.err, PKV_DEVERR_TIMEOUT);
                 dead = true;
+                // no copy is issued any more; those in flight land before the CTA's shared memory is another's
+#pragma unroll 1
+                for (int j = k; j < min(ntiles, k + kNS); ++j) wait_tile(&bars[j % kNS], (uint32_t)((j / kNS) & 1));
             }
             Slot t;
             t.mask = __shfl_sync(0xffffffffu, cur.mask, k & 31);
