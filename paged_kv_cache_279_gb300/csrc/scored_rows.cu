@@ -300,81 +300,75 @@ struct RowState {
     float slope2;  // slope * log2 e
 };
 
-// Maximum over N values, four chains of three-input maxima; ABS: of their magnitudes.
-template <bool ABS, int N>
-__device__ __forceinline__ float max_of(const float (&s)[N]) {
+constexpr int kStep = 32;  // keys a step
+
+// Maximum over a step's values, four chains of three-input maxima; ABS: of their magnitudes.
+template <bool ABS>
+__device__ __forceinline__ float max_of(const float (&s)[kStep]) {
     float m[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         m[i] = ABS ? fabsf(s[i]) : s[i];
 #pragma unroll
-        for (int k = i + 4; k + 4 < N; k += 8)
+        for (int k = i + 4; k + 4 < kStep; k += 8)
             m[i] = ABS ? fmax3(m[i], fabsf(s[k]), fabsf(s[k + 4])) : fmax3(m[i], s[k], s[k + 4]);
-        if (N % 8 == 0) m[i] = fmaxf(m[i], ABS ? fabsf(s[N - 4 + i]) : s[N - 4 + i]);
+        m[i] = fmaxf(m[i], ABS ? fabsf(s[kStep - 4 + i]) : s[kStep - 4 + i]);
     }
     return fmaxf(fmax3(m[0], m[1], m[2]), m[3]);
 }
 
-template <int N>
-__device__ __forceinline__ void ld_s(uint32_t taddr, float (&v)[N]) {
-    if constexpr (N == 32) tc::ld32(taddr, v);
-    else ld16(taddr, v);
+__device__ __forceinline__ void ld_s(uint32_t taddr, float (&v)[kStep]) {
+    tc::ld32(taddr, v);
     tc::wait_ld();
 }
 
-// The keys of step c (N keys) of the tile at t0 that the row sees, as bits.
-template <int N>
+// The keys of step c of the tile at t0 that the row sees, as bits.
 __device__ __forceinline__ uint32_t seen_bits(const KeyRange &r, int t0, uint32_t bad, int bshift, int c) {
-    const int t = t0 + N * c;
+    const int t = t0 + kStep * c;
     uint32_t w = bit_range(r.lo - t, r.hi - t);
     if (r.pre > t) w |= bit_range(r.first - t, r.pre - t);
     if (bad) {
 #pragma unroll
-        for (int i = 0; i < N; i += 8)
-            if ((bad >> ((N * c + i) >> bshift)) & 1u) w &= ~(0xffu << i);
+        for (int i = 0; i < kStep; i += 8)
+            if ((bad >> ((kStep * c + i) >> bshift)) & 1u) w &= ~(0xffu << i);
     }
-    return N == 32 ? w : w & 0xffffu;
+    return w;
 }
-template <int N>
-constexpr uint32_t kAllSeen = N == 32 ? 0xffffffffu : (1u << (N & 31)) - 1u;
 
-template <int N>
-__device__ __forceinline__ void mask_s(float (&s)[N], uint32_t w, float hidden = -INFINITY) {
+__device__ __forceinline__ void mask_s(float (&s)[kStep], uint32_t w, float hidden = -INFINITY) {
 #pragma unroll
-    for (int k = 0; k < N; ++k) s[k] = (w >> k) & 1u ? s[k] : hidden;
+    for (int k = 0; k < kStep; ++k) s[k] = (w >> k) & 1u ? s[k] : hidden;
 }
 
-template <int N>
 __device__ __forceinline__ void no_weights(uint32_t to) {
     const uint32_t z[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int i = 0; i < N / 2; i += 8) st8u(to + i, z);
+    for (int i = 0; i < kStep / 2; i += 8) st8u(to + i, z);
 }
 
-// Raw products of N keys (at sp) -> scores in base 2 plus nm: c tanh(z) + nm, z = k1 s.  For |z| small in the whole warp
+// Raw products of kStep keys (at sp) -> scores in base 2 plus nm: c tanh(z) + nm, z = k1 s.  For |z| small in the whole warp
 // an odd polynomial (the cap's factors folded in on the host) on the FMA pipe, two keys an instruction: the exponential is
 // then the only special function of a score.  Else, in a loop to keep the code short,
 // tanh z = 1 - 2 / (1 + e^2z), good to 2^-21; the scores go back over S.  Under a wide cap
 // (WIDE: there may be one) small z take the series there too: what other rows reach must not
 // cost them accuracy.
-template <int N>
-__device__ __forceinline__ void cap_near(float (&s)[N], const RowsArgs &a, uint64_t nm2) {
+__device__ __forceinline__ void cap_near(float (&s)[kStep], const RowsArgs &a, uint64_t nm2) {
     const uint64_t q0 = f32x2(a.near[0], a.near[0]), q1 = f32x2(a.near[1], a.near[1]);
     const uint64_t q2 = f32x2(a.near[2], a.near[2]), q3 = f32x2(a.near[3], a.near[3]);
 #pragma unroll
-    for (int k = 0; k < N; k += 2) {
+    for (int k = 0; k < kStep; k += 2) {
         const uint64_t x = f32x2(s[k], s[k + 1]), u = mul_f32x2(x, x);
         const uint64_t y = fma_f32x2(fma_f32x2(fma_f32x2(q3, u, q2), u, q1), u, q0);
         f32x2_split(fma_f32x2(x, y, nm2), s[k], s[k + 1]);
     }
 }
 
-template <bool WIDE, int N>
-__device__ __forceinline__ void cap_far(float (&s)[N], uint32_t sp, const RowsArgs &a, float nm) {
+template <bool WIDE>
+__device__ __forceinline__ void cap_far(float (&s)[kStep], uint32_t sp, const RowsArgs &a, float nm) {
     const float z2 = 2.f * 1.44269504f * a.k1, small = WIDE && a.c2 > kWideCap ? kTanhSmall : 0.f;
     constexpr float s1 = (float)kTanhSeries[1], s2 = (float)kTanhSeries[2], s3 = (float)kTanhSeries[3];
 #pragma unroll 1
-    for (int i = 0; i < N / 4; ++i) {
+    for (int i = 0; i < kStep / 4; ++i) {
         float x[4];
         ld4(sp + 4 * i, x);
         tc::wait_ld();
@@ -394,17 +388,17 @@ __device__ __forceinline__ void cap_far(float (&s)[N], uint32_t sp, const RowsAr
     ld_s(sp, s);
 }
 
-template <bool WIDE, int N>
-__device__ __forceinline__ void cap_s(float (&s)[N], uint32_t sp, const RowsArgs &a, float nm, uint64_t nm2) {
+template <bool WIDE>
+__device__ __forceinline__ void cap_s(float (&s)[kStep], uint32_t sp, const RowsArgs &a, float nm, uint64_t nm2) {
     const float top = max_of<true>(s) * fabsf(a.k1);
     cap_near(s, a, nm2);
     if (__builtin_expect(__any_sync(0xffffffffu, top > a.near_max), 0)) cap_far<WIDE>(s, sp, a, nm);
 }
 
-// Raw products of N keys at sp, the first `ahead` keys before the row's position -> scores in base 2 plus nm.  beyond: keys
+// Raw products of kStep keys at sp, the first `ahead` keys before the row's position -> scores in base 2 plus nm.  beyond: keys
 // past the position may be seen.
-template <int KIND, int N>
-__device__ __forceinline__ void scores(float (&s)[N], uint32_t sp, int ahead, float slope2, bool beyond, const RowsArgs &a, float nm,
+template <int KIND>
+__device__ __forceinline__ void scores(float (&s)[kStep], uint32_t sp, int ahead, float slope2, bool beyond, const RowsArgs &a, float nm,
                                        bool full, uint32_t w) {
     ld_s(sp, s);
     if constexpr (KIND == kCapBias) {
@@ -415,18 +409,18 @@ __device__ __forceinline__ void scores(float (&s)[N], uint32_t sp, int ahead, fl
     const uint64_t f2 = f32x2(f, f), nm2 = f32x2(nm, nm);
     if constexpr (KIND == kPlain) {
 #pragma unroll
-        for (int k = 0; k < N; k += 2) f32x2_split(fma_f32x2(f32x2(s[k], s[k + 1]), f2, nm2), s[k], s[k + 1]);
+        for (int k = 0; k < kStep; k += 2) f32x2_split(fma_f32x2(f32x2(s[k], s[k + 1]), f2, nm2), s[k], s[k + 1]);
     } else {
         // -slope |ahead - k|, linear unless the position is inside: one FMA for the pair's bias, one for the score
         const float sl = beyond && ahead <= 0 ? -slope2 : slope2, b = fmaf(-sl, (float)ahead, nm);
-        if (__builtin_expect(beyond && __any_sync(0xffffffffu, ahead > 0 && ahead < N - 1), 0)) {
+        if (__builtin_expect(beyond && __any_sync(0xffffffffu, ahead > 0 && ahead < kStep - 1), 0)) {
             if (KIND == kCapBias) {  // capped scores over S
 #pragma unroll
-                for (int i = 0; i < N; i += 4) st4(sp + i, reinterpret_cast<const float(&)[4]>(s[i]));
+                for (int i = 0; i < kStep; i += 4) st4(sp + i, reinterpret_cast<const float(&)[4]>(s[i]));
                 tc::wait_st();
             }
 #pragma unroll 1
-            for (int i = 0; i < N / 4; ++i) {
+            for (int i = 0; i < kStep / 4; ++i) {
                 float x[4];
                 ld4(sp + 4 * i, x);
                 tc::wait_ld();
@@ -440,7 +434,7 @@ __device__ __forceinline__ void scores(float (&s)[N], uint32_t sp, int ahead, fl
         }
         const uint64_t b2 = f32x2(b, b), sl2 = f32x2(sl, sl);
 #pragma unroll
-        for (int k = 0; k < N; k += 2)
+        for (int k = 0; k < kStep; k += 2)
             f32x2_split(fma_f32x2(f32x2(s[k], s[k + 1]), f2, fma_f32x2(sl2, f32x2((float)k, (float)(k + 1)), b2)), s[k], s[k + 1]);
     }
 }
@@ -452,12 +446,11 @@ __device__ __forceinline__ void add_bf16x2(float &a, float &b, uint32_t v) {
         : "r"(v));
 }
 
-// Weights 2^s of N keys to P (bf16 pairs) at `to`, the sum of the rounded ones to ls: a row that one key dominates gets its
+// Weights 2^s of kStep keys to P (bf16 pairs) at `to`, the sum of the rounded ones to ls: a row that one key dominates gets its
 // value exactly.
-template <int N>
-__device__ __forceinline__ void weights(const float (&s)[N], uint32_t to, uint64_t (&ls)[2]) {
+__device__ __forceinline__ void weights(const float (&s)[kStep], uint32_t to, uint64_t (&ls)[2]) {
 #pragma unroll
-    for (int i = 0; i < N; i += 16) {
+    for (int i = 0; i < kStep; i += 16) {
         float lf[4];
         f32x2_split(ls[0], lf[0], lf[1]);
         f32x2_split(ls[1], lf[2], lf[3]);
@@ -531,32 +524,31 @@ __device__ __forceinline__ void softmax_tile(uint32_t sp, uint32_t op, const Til
     const int t0 = rec.t0;
     const bool full = rec.full != 0;
     uint64_t ls[2] = {0ull, 0ull};
-    constexpr int N = 32;  // keys a step
-    float x[N];
+    float x[kStep];
     if constexpr (KIND == kCap) {
         const float nm = -st.m;
         const uint64_t nm2 = f32x2(nm, nm);
         // (a loop for tiles that every row sees whole: the shorter, the faster)
         if (full) {
 #pragma unroll 1
-            for (int c = 0; c < kTok / N; ++c) {
-                ld_s(sp + N * c, x);
-                cap_s<false>(x, sp + N * c, a, nm, nm2);
-                weights(x, sp + N / 2 * c, ls);
+            for (int c = 0; c < kTok / kStep; ++c) {
+                ld_s(sp + kStep * c, x);
+                cap_s<false>(x, sp + kStep * c, a, nm, nm2);
+                weights(x, sp + kStep / 2 * c, ls);
             }
         } else {
 #pragma unroll 1
-            for (int c = 0; c < kTok / N; ++c) {
-                const uint32_t w = seen_bits<N>(st.r, t0, rec.bad, a.bshift, c);
+            for (int c = 0; c < kTok / kStep; ++c) {
+                const uint32_t w = seen_bits(st.r, t0, rec.bad, a.bshift, c);
                 if (!__any_sync(0xffffffffu, w != 0u)) {
-                    no_weights<N>(sp + N / 2 * c);
+                    no_weights(sp + kStep / 2 * c);
                     continue;
                 }
-                ld_s(sp + N * c, x);
+                ld_s(sp + kStep * c, x);
                 mask_s(x, w, 0.f);  // what is hidden has no say in how the others are capped
-                cap_s<false>(x, sp + N * c, a, nm, nm2);
+                cap_s<false>(x, sp + kStep * c, a, nm, nm2);
                 mask_s(x, w);
-                weights(x, sp + N / 2 * c, ls);
+                weights(x, sp + kStep / 2 * c, ls);
             }
         }
     } else {
@@ -577,26 +569,26 @@ __device__ __forceinline__ void softmax_tile(uint32_t sp, uint32_t op, const Til
         };
         float nm = m == -INFINITY ? 0.f : -m, top = m == -INFINITY ? -INFINITY : kJump;
 #pragma unroll 1
-        for (int c = 0; c < kTok / N; ++c) {
-            uint32_t w = kAllSeen<N>;
+        for (int c = 0; c < kTok / kStep; ++c) {
+            uint32_t w = 0xffffffffu;
             if (!full) {
-                w = seen_bits<N>(st.r, t0, rec.bad, a.bshift, c);
+                w = seen_bits(st.r, t0, rec.bad, a.bshift, c);
                 if (!__any_sync(0xffffffffu, w != 0u)) {
-                    no_weights<N>(sp + N / 2 * c);
+                    no_weights(sp + kStep / 2 * c);
                     continue;
                 }
             }
-            scores<KIND>(x, sp + N * c, st.p - t0 - N * c, st.slope2, beyond, a, nm, full, w);
+            scores<KIND>(x, sp + kStep * c, st.p - t0 - kStep * c, st.slope2, beyond, a, nm, full, w);
             if (!full) mask_s(x, w);
             const float mc = max_of<false>(x);
             if (__builtin_expect(__any_sync(0xffffffffu, mc > top), 0)) {
                 const float up = mc > top ? ceilf(mc) : 0.f;  // relative to the reference so far
                 const float f = m == -INFINITY ? 1.f : ex2_approx(-up);  // (no weight so far but 0)
-                if (__any_sync(0xffffffffu, f != 1.f)) rescale_weights(sp, N / 16 * c, f);
+                if (__any_sync(0xffffffffu, f != 1.f)) rescale_weights(sp, kStep / 16 * c, f);
                 ls[0] = mul_f32x2(ls[0], f32x2(f, f));
                 ls[1] = mul_f32x2(ls[1], f32x2(f, f));
 #pragma unroll
-                for (int k = 0; k < N; ++k) x[k] -= up;
+                for (int k = 0; k < kStep; ++k) x[k] -= up;
                 if (mc > top) {
                     m = up - nm;
                     nm = -m;
@@ -604,7 +596,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t sp, uint32_t op, const Til
                 }
                 if (unknown) publish();
             }
-            weights(x, sp + N / 2 * c, ls);
+            weights(x, sp + kStep / 2 * c, ls);
         }
         if (unknown) publish();
         // the tile before's reference
@@ -1490,10 +1482,9 @@ pkv_status launch(const RowsArgs &a, cudaStream_t st) {
 
 template <int D>
 pkv_status launch_kind(const RowsArgs &a, cudaStream_t st) {
-    // a plain score's maximum is found before the scaling, which needs a positive scale
     const bool bias = a.s.slopes != nullptr;
     if (a.s.softcap > 0.f) return bias || a.c2 > kMaxC2 ? launch<D, kCapBias>(a, st) : launch<D, kCap>(a, st);
-    return bias || !(a.s.scale > 0.f) ? launch<D, kBias>(a, st) : launch<D, kPlain>(a, st);
+    return bias ? launch<D, kBias>(a, st) : launch<D, kPlain>(a, st);
 }
 
 }  // namespace

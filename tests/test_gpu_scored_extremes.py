@@ -91,3 +91,12 @@ def test_extreme_scales(kind, cap, scale):
     c = Case([77, 300], qlens=[9, 130] if kind == "multi" else None, rows=kind == "rows", softcap=cap, scale=scale,
              qmul=2.0 / scale / 128 ** 0.5, dtype=torch.float32 if kind == "f32" else torch.bfloat16)
     c.check(run(c))
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.1, 0.3])
+@pytest.mark.parametrize("kind", ["f32", "bf16", "rows", "multi"])
+def test_plain_scores_of_any_scale(kind, scale):
+    """No cap and no bias, scores of either sign."""
+    c = Case([77, 300, 900], qlens=[9, 130, 33] if kind == "multi" else None, rows=kind == "rows", scale=scale, window=250,
+             dtype=torch.float32 if kind == "f32" else torch.bfloat16)
+    c.check(run(c))
