@@ -135,3 +135,11 @@ def test_the_workspace_of_a_type_suffices(kind):
         if need > 256:
             with pytest.raises(pkv.PkvError):
                 run(c, workspace=ws[:need - 256], max_seq_len=maxL)
+
+
+def test_many_queries_that_see_nothing():
+    """Blocks of queries whose documents begin after them: zeros, beside queries that see their own."""
+    c = Case([1000], 8, 2, 128, 16, qlens=[607], starts=[893] * 500 + [900] * 100 + [5000] * 7, softcap=20.0)
+    got = run(c)
+    c.check(got)
+    assert torch.all(got[:507] == 0) and torch.all(got[600:] == 0) and torch.all(got[507:600].abs().sum(-1) > 0)
