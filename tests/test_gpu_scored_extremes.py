@@ -100,3 +100,14 @@ def test_plain_scores_of_any_scale(kind, scale):
     c = Case([77, 300, 900], qlens=[9, 130, 33] if kind == "multi" else None, rows=kind == "rows", scale=scale, window=250,
              dtype=torch.float32 if kind == "f32" else torch.bfloat16)
     c.check(run(c))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("sign,size", [(1.0, 2.0 ** 50), (-1.0, 2.0 ** 50), (1.0, 2.0 ** -30), (-1.0, 2.0 ** -30)])
+def test_multi_values_at_the_ends_of_a_cap(sign, size, D):
+    """Every score at +-50, V large or small: what the fixed reference of capped scores has to hold."""
+    c = Case([900, 40], 4, 1, D, 16, qlens=[140, 40], softcap=50.0, scale=1.0)
+    c.q = c.q.abs() + 8.0
+    c.ks = [(sign * (k.abs() + 8.0)) for k in c.ks]
+    c.vs = [v * size for v in c.vs]
+    c.check(run(c))
