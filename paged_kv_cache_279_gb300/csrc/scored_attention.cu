@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(128) scored_simt_kernel(const SimtArgs a) {
                 for (int j = 0; j < E; ++j) o[g][j] *= al;
                 m[g] = mn;
             }
-            const float p = row >= 0 ? expf(x - mn) : 0.f;
+            const float p = x == -INFINITY ? 0.f : expf(x - mn);  // (a key that is not seen, or one whose score is -infinity)
             l[g] += p;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {

@@ -111,3 +111,27 @@ def test_multi_values_at_the_ends_of_a_cap(sign, size, D):
     c.ks = [(sign * (k.abs() + 8.0)) for k in c.ks]
     c.vs = [v * size for v in c.vs]
     c.check(run(c))
+
+
+@pytest.mark.parametrize("cap", [0.0, 5.0])
+@pytest.mark.parametrize("kind", ["f32", "bf16", "multi"])
+def test_scores_of_minus_infinity(kind, cap):
+    """Keys whose scores are -infinity, whole runs of them at either end: weights of zero, or a cap's lower end."""
+    n = 700
+    c = Case([n, 40], 4, 1, 64, 16, qlens=[60, 5] if kind == "multi" else None, softcap=cap, scale=0.1,
+             dtype=torch.float32 if kind == "f32" else torch.bfloat16)
+    c.q[..., 3] = 1.0
+    low = [np.r_[0:300, 420:430, 600:n - 60], np.r_[0:20]]
+    for k, t in zip(c.ks, low):
+        k[t, :, 3] = -float("inf")
+    pools = c.pools()
+    for k, t in zip(c.ks, low):
+        k[t, :, 3] = -1e30   # the same to 64 bits: exp(-1e29) is 0, tanh(-2e28) is -1
+    ref, _ = c.reference()
+    # the bound of scored_cases with sizes of ordinary scores (scale sum |q||k| below 64) and vmax for sum_t w_t |v_t|
+    vmax = max(v.double().abs().max().item() for v in c.vs)
+    x = (64 + 16) * 2.0 ** -24 * 64 + 2.0 ** -20 + 2.0 ** -18 * cap + 2.0 ** -22 * 64
+    weight = 0.0 if kind == "f32" else 2.0 ** -8
+    tol = 2 * (2 * x + weight + n * 2.0 ** -24) * vmax + torch.finfo(c.dtype).eps / 2 * np.abs(ref) * (1 + 2.0 ** -6)
+    got = run(c, pools).double().cpu().numpy()
+    assert np.all(np.abs(got - ref) <= tol)
