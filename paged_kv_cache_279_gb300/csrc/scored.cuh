@@ -10,6 +10,7 @@
 #include <climits>
 #include <cmath>
 
+#include "mma_sync.cuh"
 #include "pkv_internal.cuh"
 #include "pkv_ptx.cuh"
 
@@ -26,12 +27,7 @@ __device__ __forceinline__ float row_scale(unsigned char b) { return __uint_as_f
 // Four E4M3 codes (bytes 0 .. 3 of c) as floats; exact.
 __device__ __forceinline__ void e4m3x4_to_float(uint32_t c, float *x) {
     uint32_t lo, hi;
-    asm("{\n\t.reg .b16 a, b;\n\t"
-        "mov.b32 {a, b}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(c));
+    e4m3x4_to_f16(c, lo, hi);
     const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
     const float2 q = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
     x[0] = p.x, x[1] = p.y, x[2] = q.x, x[3] = q.y;

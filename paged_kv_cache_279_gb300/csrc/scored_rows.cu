@@ -918,7 +918,7 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 for (int b = lane; b < nb; b += 32) per_kvh += laid_out(ctx_tiles(a, x, fp, b).n);
 #pragma unroll
                 for (int sh = 16; sh > 0; sh >>= 1) per_kvh += __shfl_xor_sync(0xffffffffu, per_kvh, sh);
-#pragma unroll
+#pragma unroll 1
                 for (int kvh = per_kvh > 0 ? (t - seq_start) / per_kvh : Hkv; kvh < Hkv && t < s1 && !dead; ++kvh) {
                     int pos = seq_start + kvh * per_kvh;  // laid-out start of block b0
 #pragma unroll 1
