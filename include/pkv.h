@@ -437,9 +437,10 @@ PKV_EXPORT pkv_status paged_attention_decode_scored_fp8_rows(
  * key_starts must not decrease over a sequence's queries (documents stand in
  * order): where a query's entry is below an earlier one's, it is unspecified
  * which of the keys between the two the sequence's queries see.  With a cap of
- * at most 50 and no slopes, weights are held against a fixed reference: V is to
- * lie within 2^53 (smaller entries than 2^-36 lose precision where every score
- * of a query is near -softcap).
+ * at most 50 and no slopes, weights are held against a fixed reference: V entries
+ * below 2^-36 lose precision where every score of a query is near -softcap.
+ * Infinities and NaN in V reach the queries that see their keys and no others;
+ * a call that meets some takes up to twice its time.
  */
 PKV_EXPORT size_t paged_attention_multi_token_scored_workspace_size(int num_q_tokens, int num_heads, int head_dim,
                                                                     int max_seq_len);

@@ -38,10 +38,12 @@
 // their key, and 0 times infinity is NaN.  Nothing guards against that at first.  The epilogue
 // looks at what it reads of O, and a CTA that met an infinity or NaN walks its share a second
 // time, carefully: in tiles that not every row sees whole, the sets take infinities and NaN
-// out of V, and the epilogue adds them to the rows that see their keys.  The look costs 1 of 57 us
-// (64 x 5 queries) and of 177 (prompts of documents); reading every such tile's V for them at once
-// would cost each of them some 100 instructions a thread.  The second walk is code of its own (as a
-// flag in the same code it took 2 to 3 % more).
+// out of V, and the epilogue adds them to the rows that see their keys.  O may also have passed
+// float32's range by itself (weights up to 2^kJump, under a cap 2^54, on very large V): in the
+// second walk the references follow every score, so weights are at most 1.  The look costs 1 of
+// 57 us (64 x 5 queries) and of 177 (prompts of documents); reading every such tile's V for them at
+// once would cost each of them some 100 instructions a thread.  The second walk is code of its own
+// (as a flag in the same code it took 2 to 3 % more).
 //
 // Tensor memory: S at columns 128 (t % 3) (P overwrites its first half as bf16
 // pairs), O at 384.
@@ -517,8 +519,10 @@ __device__ __forceinline__ void rescale_weights(uint32_t to, int n, float f) {
 // Capped scores without a bias need none of this: they lie within +-c2, and up to
 // kMaxC2 a fixed reference c2 / 4 keeps weights within 2^-(5/4 c2) .. 2^(3/4 c2)
 // (cap 50: 2^-90 .. 2^54), far from the ends of float32's and bf16's range for
-// sums over 2^20 keys of V entries between 2^-36 and 2^53.
-template <int D, int KIND>
+// sums over 2^20 keys of V entries between 2^-36 and 2^53 (larger ones: the second walk).
+//
+// CLOSE: the reference follows every score that passes it (the second walk).
+template <int D, int KIND, bool CLOSE>
 __device__ __forceinline__ void softmax_tile(uint32_t sp, uint32_t op, const TileRec &rec, const RowsArgs &a, bool beyond,
                                              RowState &st, const Chain &ch, int lane, bool &dead) {
     const int t0 = rec.t0;
@@ -552,6 +556,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t sp, uint32_t op, const Til
             }
         }
     } else {
+        constexpr float jump = CLOSE ? 0.f : kJump;
         // what a tile begins with depends on no other's pace, so results do not either
         float m = -INFINITY;
         bool unknown = ch.first;
@@ -567,7 +572,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t sp, uint32_t op, const Til
             if (lane == 0) mbar_arrive(ch.started);
             unknown = false;
         };
-        float nm = m == -INFINITY ? 0.f : -m, top = m == -INFINITY ? -INFINITY : kJump;
+        float nm = m == -INFINITY ? 0.f : -m, top = m == -INFINITY ? -INFINITY : jump;
 #pragma unroll 1
         for (int c = 0; c < kTok / kStep; ++c) {
             uint32_t w = 0xffffffffu;
@@ -592,7 +597,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t sp, uint32_t op, const Til
                 if (mc > top) {
                     m = up - nm;
                     nm = -m;
-                    top = kJump;
+                    top = jump;
                 }
                 if (unknown) publish();
             }
@@ -1180,6 +1185,7 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             drain(&all_done[1], 0u);
         } else if (warp < kEpiWarp) {
             // ======================= softmax =======================
+            constexpr int K = careful && KIND == kCap ? kCapBias : KIND;  // (a moving reference)
             const int set = warp >> 2, wq = warp & 3;
             const int rr = wq * 32 + lane;  // TMEM lane and row of the context
             const int rq = rr / G, rh = rr - rq * G;  // its query and head
@@ -1198,12 +1204,12 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 const bool live_warp = wq * 32 < pc.nrows;
                 const int qi = min(rq, pc.nq - 1);
                 RowState st;
-                st.m = KIND == kCap ? a.m0 : -INFINITY;
+                st.m = K == kCap ? a.m0 : -INFINITY;
                 st.l = 0.f;
                 st.p = pc.pos0 + qi;
                 st.r = key_range(max(pc.ks0, key_start_of(a.s, (int64_t)pc.row0 + qi)), pre, a.s.window, st.p, st.p);
                 st.slope2 = 0.f;
-                if constexpr (KIND == kBias || KIND == kCapBias)
+                if constexpr (K == kBias || K == kCapBias)
                     st.slope2 = a.s.slopes ? a.s.slopes[pc.kvh * G + rh] * 1.44269504f : 0.f;
                 const KeyRange cr{pc.ks0, pc.cpre, pc.lo, pc.hi};
                 bool any = false, taken = false;
@@ -1230,8 +1236,8 @@ scored_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     ch.parity = (uint32_t)(bturn & 1);
                     ch.first = j == 0;
                     if (live_warp) {
-                        softmax_tile<D, KIND>(sp, op, rec, a, rec.t0 < pre, st, ch, lane, dead);
-                    } else if (KIND != kCap) {
+                        softmax_tile<D, K, careful>(sp, op, rec, a, rec.t0 < pre, st, ch, lane, dead);
+                    } else if (K != kCap) {
                         if (ch.before) wait_for(ch.before, ch.parity, dead);
                         __syncwarp();
                         if (lane == 0) {

@@ -103,9 +103,10 @@ def test_plain_scores_of_any_scale(kind, scale):
 
 
 @pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("sign,size", [(1.0, 2.0 ** 50), (-1.0, 2.0 ** 50), (1.0, 2.0 ** -30), (-1.0, 2.0 ** -30)])
+@pytest.mark.parametrize("sign,size", [(1.0, 2.0 ** 50), (-1.0, 2.0 ** 50), (1.0, 2.0 ** -30), (-1.0, 2.0 ** -30), (1.0, 2.0 ** 112),
+                                       (-1.0, 2.0 ** 112)])
 def test_multi_values_at_the_ends_of_a_cap(sign, size, D):
-    """Every score at +-50, V large or small: what the fixed reference of capped scores has to hold."""
+    """Every score at +-50, V large or small: what the fixed reference of capped scores holds, and where it would overflow."""
     c = Case([900, 40], 4, 1, D, 16, qlens=[140, 40], softcap=50.0, scale=1.0)
     c.q = c.q.abs() + 8.0
     c.ks = [(sign * (k.abs() + 8.0)) for k in c.ks]
@@ -135,3 +136,19 @@ def test_scores_of_minus_infinity(kind, cap):
     tol = 2 * (2 * x + weight + n * 2.0 ** -24) * vmax + torch.finfo(c.dtype).eps / 2 * np.abs(ref) * (1 + 2.0 ** -6)
     got = run(c, pools).double().cpu().numpy()
     assert np.all(np.abs(got - ref) <= tol)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("opt", [{}, dict(alibi=True), dict(softcap=50.0), dict(softcap=50.0, alibi=True), dict(softcap=200.0)],
+                         ids=["plain", "alibi", "cap", "cap_alibi", "wide_cap"])
+@pytest.mark.parametrize("kind", ["f32", "bf16", "multi"])
+def test_very_large_values(kind, opt, D):
+    """V of 2^112 under scores that rise along the context by 40: weights relative to the first keys would overflow."""
+    c = Case([900, 300], 4, 1, D, 16, qlens=[140, 33] if kind == "multi" else None,
+             dtype=torch.float32 if kind == "f32" else torch.bfloat16, scale=1.0, **opt)
+    c.q = (0.05 * c.q.float()).to(c.dtype)
+    c.q[..., 0] = 1.0
+    for s, L in enumerate(c.lens):
+        c.ks[s][:, 0, 0] = torch.linspace(-20.0, 20.0, L).to(c.dtype)
+    c.vs = [v * 2.0 ** 112 for v in c.vs]
+    c.check(run(c))
