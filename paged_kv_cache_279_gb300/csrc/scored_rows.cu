@@ -22,8 +22,8 @@
 // pipe, instruction fetches and latency), so three tiles are in flight per SM: three
 // S buffers, three sets of four warps (a thread per row = TMEM lane), tile t with set
 // t % 3, one O.  Two chains of 128 x 128 tiles with an O each left the tensor cores
-// idle between them (8 x 512 queries of 4096: 311 us; this form 255 to 270 us, with
-// the tensor pipe 49 % and the issue slots 54 % busy, at the board's power limit in a
+// idle between them (8 x 512 queries of 4096: 311 us; this form 252 to 274 us, with
+// the tensor pipe 47 % and the issue slots 57 % busy, at the board's power limit in a
 // long run).  What costs most is code size: the loops over a tile are
 // rolled and their rare parts loops of their own; unrolled by two they took 6 to 13 %
 // longer.
