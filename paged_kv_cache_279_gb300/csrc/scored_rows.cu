@@ -1518,7 +1518,7 @@ pkv_status run_rows(const Args &args, int head_dim, void *workspace, size_t work
     a.scan_w = 1;
     while (a.scan_w < 32 && a.scan_w < blocks) a.scan_w *= 2;
     // (the number of all queries is no bound of a part's contexts: query ranges may overlap)
-    const int64_t most = kMaxTiles / (a.num_kv_heads * blocks * ((longest_context(a) + kTok - 1) / kTok + 1 + kCharge));
+    const int64_t most = kMaxTiles / (a.num_kv_heads * ((longest_context(a) + kTok - 1) / kTok + 1 + kCharge)) / blocks;
     if (most < 1) return PKV_ERR_UNSUPPORTED;
     const double log2e = 1.4426950408889634;
     a.k1 = finite_float(a.s.softcap > 0.f ? (double)a.s.scale / a.s.softcap : a.s.scale * log2e);
