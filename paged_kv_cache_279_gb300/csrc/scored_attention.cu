@@ -216,6 +216,7 @@ __global__ void __launch_bounds__(128) scored_reduce_kernel(const SimtArgs a) {
 
 static size_t simt_workspace(int64_t seqs, int64_t heads, int64_t D, int64_t max_seq_len) {
     const int64_t parts = (max_seq_len + kPartition - 1) / kPartition;
+    if ((double)seqs * heads * parts * (D * 4 + 8) > 4e18) return SIZE_MAX;  // (no device holds it: refused)
     return parts <= 1 ? 0 : round256((size_t)(seqs * heads * parts * D * 4)) + round256((size_t)(seqs * heads * parts * 8));
 }
 

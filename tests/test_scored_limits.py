@@ -19,3 +19,13 @@ def test_products_of_maxima(Hkv, maxL):
                                                       maxL, 0.1, 0.0, None, 0, None, None, P, BIG, None) == pkv.PKV_ERR_UNSUPPORTED
     assert lib.paged_attention_decode_scored(P, P, P, P, P, P, P, P, 2 ** 31 - 1, Hkv, Hkv, 128, 8, maxB, 1, maxL, 0.1, 0.0, None, 0,
                                              None, None, P, BIG, 1, None) == pkv.PKV_ERR_UNSUPPORTED
+
+
+def test_a_workspace_past_64_bits():
+    lib = _lib.load()
+    for S in (2 ** 31 - 1, 1 << 30):
+        for L in ((1 << 25) - 512, 3 << 23):
+            for H in (1 << 18, 65535 * 8):
+                assert lib.paged_attention_decode_scored_workspace_size_for(S, H, 128, L, 0) > BIG
+                assert lib.paged_attention_decode_scored(P, P, P, P, P, P, P, P, S, H, H // 8, 128, 8, 1 << 20, 1, L, 0.1, 0.0, None,
+                                                         0, None, None, P, BIG, 0, None) == pkv.PKV_ERR_INVALID
