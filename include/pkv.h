@@ -439,8 +439,9 @@ PKV_EXPORT pkv_status paged_attention_decode_scored_fp8_rows(
  * which of the keys between the two the sequence's queries see.  With a cap of
  * at most 50 and no slopes, weights are held against a fixed reference: V entries
  * below 2^-36 lose precision where every score of a query is near -softcap.
- * Infinities and NaN in V reach the queries that see their keys and no others;
- * a call that meets some takes up to twice its time.
+ * Infinities and NaN in V reach the queries that see their keys and no others; a
+ * call that meets some takes longer (one in the whole cache: 2 to 4 times; one
+ * in each V row: 7 to 60 times).
  */
 PKV_EXPORT size_t paged_attention_multi_token_scored_workspace_size(int num_q_tokens, int num_heads, int head_dim,
                                                                     int max_seq_len);
