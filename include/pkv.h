@@ -453,6 +453,138 @@ PKV_EXPORT pkv_status paged_attention_multi_token_scored(
     const int32_t *prefix_lens, const int32_t *key_starts, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * Rotary positions -- rotary_frequencies, rotary_embed and
+ * kv_cache_write_rotary.
+ *
+ * The pages have no counterpart: they take queries and keys as given.  Models
+ * whose attention knows positions by rotating queries and keys need this in
+ * front of every attention call here, and keys are stored rotated.  A row at
+ * position p has R = rotary_dim rotated entries, from entry `offset` on, in R / 2
+ * pairs; pair i, of frequency f_i radians a position, becomes
+ *     y1 = x1 c - x2 s,  y2 = x2 c + x1 s,  c = a cos(p f_i),  s = a sin(p f_i)
+ * with a = amplitude, computed in float32 and rounded once; the row's other
+ * entries are copied.  Pairs are the entries (i, i + R / 2) of the rotated part,
+ * or (2 i, 2 i + 1) if interleaved.  The angle is exact modulo a turn for every
+ * position of 32 bits (no float32 product of position and frequency).
+ *
+ * rotary_frequencies -- host function: out[i] = base^(-2 i / R), i < R / 2, for
+ * longer contexts than a model was trained on divided by `factor`
+ * (original_len = 0), or by parts: with n_i = original_len f_i / 2 pi turns in the
+ * original length and w = (n_i - low_turns) / (high_turns - low_turns), held in
+ * [0, 1], the frequency becomes f_i (w + (1 - w) / factor).  Any other positive or
+ * negative frequencies may be given to the calls too.
+ *
+ *   out, x         device [num_tokens][num_heads][head_dim], dtype, 16-byte
+ *                  aligned.  out may be x; otherwise they must not overlap.
+ *   positions      device int32 [num_tokens], any value
+ *   frequencies    device float64 [rotary_dim / 2]; infinite, NaN and subnormal
+ *                  ones count as 0
+ *   strides        host int64 [4] or NULL (contiguous): entries from token to
+ *                  token and from head to head, of out and of x, each a multiple
+ *                  of 16 bytes (slices of a fused projection)
+ *   amplitude      finite (the scale of long-context variants, else 1)
+ *   interleaved    0 or 1
+ * Supported: head_dim, rotary_dim and offset multiples of 16, rotary_dim <= 256,
+ * at most 65535 * 16 entries a token.
+ *
+ * kv_cache_write_rotary -- kv_cache_write with the keys rotated on the way, and
+ * the queries too, in one launch.
+ *   q_out, q       device [num_tokens][num_heads][head_dim] or both NULL with
+ *                  num_heads = 0.  q_out may be q.  Every token's queries are
+ *                  rotated, whatever its slot.
+ *   k_new, v_new, k_cache, v_cache, slot_mapping  as for kv_cache_write
+ *   positions, frequencies, offset, amplitude, interleaved  as above
+ *   strides        host int64 [8] or NULL (contiguous): token and head strides of
+ *                  q_out, q, k_new, v_new as above (q's are ignored without q)
+ */
+PKV_EXPORT pkv_status rotary_frequencies(double *out, int rotary_dim, double base, double factor, double original_len,
+                                         double low_turns, double high_turns);
+PKV_EXPORT pkv_status rotary_embed(void *out, const void *x, const int32_t *positions, const double *frequencies,
+                                   int num_tokens, int num_heads, int head_dim, int rotary_dim, int offset,
+                                   const int64_t *strides, float amplitude, int interleaved, int dtype, void *stream);
+PKV_EXPORT pkv_status kv_cache_write_rotary(void *q_out, const void *q, const void *k_new, const void *v_new, void *k_cache,
+                                            void *v_cache, const int64_t *slot_mapping, const int32_t *positions,
+                                            const double *frequencies, int num_tokens, int num_heads, int num_kv_heads,
+                                            int head_dim, int rotary_dim, int offset, int block_size, int num_blocks,
+                                            const int64_t *strides, float amplitude, int interleaved, int dtype,
+                                            void *stream);
+
+/*
+ * Latent attention -- latent_cache_write, paged_latent_attention_decode and
+ * paged_latent_attention_multi_token.
+ *
+ * The pages have no counterpart: models that compress a token's keys and values
+ * into one latent row shared by all heads keep that row in the cache, followed by
+ * a rotated key part of PKV_LATENT_ROPE_DIM entries, also shared.  Attention is
+ * the absorbed form: the projections from the latent to each head's keys and
+ * values are folded into the queries and into what reads the output, so with
+ * c_t = [latent_t | key part_t] the row of token t, V = latent_dim,
+ *     out[h, :] = sum_t softmax_t(scale * q[h, :] . c_t) latent_t
+ * Cache layout: [num_blocks][block_size][latent_dim + PKV_LATENT_ROPE_DIM],
+ * row-major, dtype, base address 16-byte aligned; blocks found through block
+ * tables as for the other caches.  block_copy copies such blocks: give the cache
+ * as K and as V (both copies write the same bytes).
+ * Supported: latent_dim 256 or 512, block_size 8, 16, 32 or 64, 1 to 128 heads,
+ * F32 (float32 arithmetic throughout) or BF16 (float32 accumulation, the softmax
+ * weights rounded to bf16 where the tensor cores take them).
+ *
+ * latent_cache_write -- store the rows of new tokens, their key part rotated.
+ *   latent         device [num_tokens][latent_dim]
+ *   k_rope         device [num_tokens][PKV_LATENT_ROPE_DIM]
+ *   cache          device, layout above, written in place
+ *   q_out, q_rope  device [num_tokens][num_heads][PKV_LATENT_ROPE_DIM] or both NULL
+ *                  with num_heads = 0: the rotary part of the queries, rotated
+ *                  too (q_out: by its strides, the end of each row of the
+ *                  attention's queries)
+ *   slot_mapping   device int64 [num_tokens], as for kv_cache_write
+ *   positions, frequencies, amplitude, interleaved  as for rotary_embed, with
+ *                  rotary_dim = PKV_LATENT_ROPE_DIM
+ *   strides        host int64 [6] or NULL (contiguous): token and head strides of
+ *                  q_out and of q_rope, token strides of latent and of k_rope, in
+ *                  entries, each a multiple of 16 bytes
+ *
+ * paged_latent_attention_decode -- one query a sequence, over its seq_lens[s]
+ * tokens (the new one stored before).
+ *   out            device [num_seqs][num_heads][latent_dim]
+ *   q              device [num_seqs][num_heads][latent_dim + PKV_LATENT_ROPE_DIM]
+ *   block_tables, seq_lens, max_seq_len, scale  as for paged_attention_decode
+ *                  (scale any finite number)
+ * paged_latent_attention_multi_token -- the last Q_s positions of every sequence
+ * (verification of drafted tokens, chunks of a prompt): queries, q_starts and
+ * max_q_len as for paged_attention_multi_token; the query at position p sees the
+ * tokens t <= p.
+ *   workspace      at least paged_latent_attention_workspace_size() bytes
+ *                  (num_q_tokens: num_seqs for decode), 256-byte aligned, NULL
+ *                  where that is 0.  Needs no initialisation; calls that share one
+ *                  must be ordered on the device.
+ * A query that sees no token, or whose scores are all -infinity, gets zeros.  Rows
+ * of out that no query owns are left as they were.  Out-of-range lengths, query
+ * starts and blocks are flagged as in the other calls; the tokens of a bad block
+ * are left out.  Cache rows that a query does not see never reach its output,
+ * whatever they hold.  Results do not depend on which physical blocks hold the
+ * tokens.
+ */
+#define PKV_LATENT_ROPE_DIM 64
+PKV_EXPORT pkv_status latent_cache_write(void *q_out, const void *q_rope, const void *latent, const void *k_rope, void *cache,
+                                         const int64_t *slot_mapping, const int32_t *positions, const double *frequencies,
+                                         int num_tokens, int num_heads, int latent_dim, int block_size, int num_blocks,
+                                         const int64_t *strides, float amplitude, int interleaved, int dtype, void *stream);
+PKV_EXPORT size_t paged_latent_attention_workspace_size(int num_q_tokens, int num_heads, int latent_dim, int max_seq_len,
+                                                        int dtype);
+PKV_EXPORT pkv_status paged_latent_attention_decode(void *out, const void *q, const void *cache, const int32_t *block_tables,
+                                                    const int32_t *seq_lens, int num_seqs, int num_heads, int latent_dim,
+                                                    int block_size, int max_blocks_per_seq, int num_blocks,
+                                                    int max_seq_len, float scale, void *workspace, size_t workspace_bytes,
+                                                    int dtype, void *stream);
+PKV_EXPORT pkv_status paged_latent_attention_multi_token(void *out, const void *q, const void *cache,
+                                                         const int32_t *block_tables, const int32_t *seq_lens,
+                                                         const int32_t *q_starts, int num_seqs, int num_q_tokens,
+                                                         int num_heads, int latent_dim, int block_size,
+                                                         int max_blocks_per_seq, int num_blocks, int max_q_len,
+                                                         int max_seq_len, float scale, void *workspace,
+                                                         size_t workspace_bytes, int dtype, void *stream);
+
+/*
  * block_copy -- copy whole physical blocks, in every layer, for K and V.
  *
  * Source: troisinh page, section "Copy-on-Write cho Beam Search": sequences

@@ -16,6 +16,9 @@ is no CPU or PyTorch fallback.
     kv_cache_write_fp8_rows(...), kv_cache_read_fp8_rows(...)  # E4M3 cache, a scale per row
     paged_attention_decode_scored(...), paged_attention_decode_scored_fp8_rows(...),
     paged_attention_multi_token_scored(...)  # capped or biased scores, windows, documents, prefixes
+    rotary_frequencies(...), rotary_embed(...), kv_cache_write_rotary(...)  # positions by rotation
+    latent_cache_write(...), paged_latent_attention_decode(...),
+    paged_latent_attention_multi_token(...)  # one latent row a token, shared by all heads
     block_copy(k_caches, v_caches, block_pairs)
     BlockAllocator(num_blocks, block_size)   # host allocator: CoW, prefix cache, truncation
 """
@@ -34,6 +37,7 @@ from . import _lib
  PKV_ERR_TOO_LARGE) = range(7)
 NOALLOC_SCRATCH_BYTES = 16 << 20
 PKV_F32, PKV_BF16 = 0, 1
+LATENT_ROPE_DIM = 64
 DEVERR_BLOCK_ID, DEVERR_SEQ_LEN, DEVERR_SLOT, DEVERR_COPY_PAIR, DEVERR_TIMEOUT, DEVERR_PREFIX = (
     1, 2, 4, 8, 16, 32)
 
@@ -45,6 +49,8 @@ __all__ = [
     "kv_cache_write_fp8_rows", "kv_cache_read_fp8_rows", "paged_attention_decode_scored",
     "paged_attention_decode_scored_fp8_rows", "paged_attention_decode_scored_workspace_size",
     "paged_attention_multi_token_scored", "paged_attention_multi_token_scored_workspace_size",
+    "rotary_frequencies", "rotary_embed", "kv_cache_write_rotary", "latent_cache_write",
+    "paged_latent_attention_decode", "paged_latent_attention_multi_token", "paged_latent_attention_workspace_size",
     "paged_attention_grouped_workspace_size", "block_copy", "read_device_errors", "BlockAllocator",
     "library_path",
 ]
@@ -593,6 +599,191 @@ def paged_attention_multi_token_scored(out, q, k_cache, v_cache, block_tables, s
         _opt_ptr(alibi_slopes, "alibi_slopes", torch.float32, dev), _int32(window),
         _opt_ptr(prefix_lens, "prefix_lens", i32, dev), _opt_ptr(key_starts, "key_starts", i32, dev)), workspace,
         (_stream_on(stream, dev),), stream)
+    return out
+
+
+def rotary_frequencies(rotary_dim: int, base: float = 10000.0, factor: float = 1.0, original_len: float = 0.0,
+                       low_turns: float = 1.0, high_turns: float = 32.0, device=None) -> torch.Tensor:
+    """Radians per position of the rotary_dim / 2 pairs, float64: base ** (-2 i / rotary_dim), for longer contexts
+    divided by `factor`; with original_len, by parts: a pair that turns high_turns times or more in that length
+    keeps its frequency, one that turns low_turns times or less has it divided, between them a ramp."""
+    if int(rotary_dim) < 2 or int(rotary_dim) % 2:
+        raise ValueError("rotary_dim must be even and positive")
+    out = torch.empty(int(rotary_dim) // 2, dtype=torch.float64)
+    _check(_lib.load().rotary_frequencies(out.data_ptr(), int(rotary_dim), float(base), float(factor), float(original_len),
+                                          float(low_turns), float(high_turns)), "rotary_frequencies")
+    return out if device is None else out.to(device)
+
+
+def _rows_ptr(t, name: str, dtype, dev: int):
+    """(address, token stride, head stride) of rows [T, H, D] whose entries are contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, other tensors of the call on cuda:{dev}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have 3 dimensions")
+    st, sh, sd = t.stride()
+    if sd != 1 and t.shape[2] > 1:
+        raise ValueError(f"the entries of a row of {name} must be contiguous")
+    # strides of dimensions of one entry say nothing, and are not held against the call
+    return t.data_ptr(), st if t.shape[0] > 1 else 0, sh if t.shape[1] > 1 else 0
+
+
+_strides = {n: ctypes.c_int64 * n for n in (4, 6, 8)}
+
+
+def _frequencies(frequencies, rotary_dim: Optional[int], dev: int):
+    if not isinstance(frequencies, torch.Tensor) or frequencies.dim() != 1:
+        raise ValueError("frequencies must be a vector, one entry per rotated pair")
+    if rotary_dim is not None and frequencies.shape[0] * 2 != rotary_dim:
+        raise ValueError(f"frequencies needs {rotary_dim // 2} entries")
+    return _ptr(frequencies, "frequencies", torch.float64, dev), 2 * frequencies.shape[0]
+
+
+def rotary_embed(out, x, positions, frequencies, amplitude: float = 1.0, interleaved: bool = False, offset: int = 0,
+                 stream=None) -> torch.Tensor:
+    """Rotate rows x [T, H, D] (bf16 or float32) by their positions (int32 [T]) into out, which may be x: the
+    entries from `offset` on, in pairs (i, i + R / 2) or, interleaved, (2 i, 2 i + 1), R = 2 * len(frequencies)
+    (float64, radians per position); pair i turns by position * frequencies[i], scaled by `amplitude`.  Tokens
+    and heads may be strided, in steps of 16 bytes."""
+    T, H, D = x.shape
+    if out.shape != x.shape:
+        raise ValueError("out and x must have the same shape")
+    if positions.shape != (T,):
+        raise ValueError("positions needs one entry per token")
+    lib, dev, dt = _lib.load(), _device_of(x, "x"), x.dtype
+    code = _dtype_code(x)
+    xp, op = _rows_ptr(x, "x", dt, dev), _rows_ptr(out, "out", dt, dev)
+    fp, R = _frequencies(frequencies, None, dev)
+    _run_on(dev, "rotary_embed", lib.rotary_embed, (
+        op[0], xp[0], _ptr(positions, "positions", torch.int32, dev), fp, T, H, D, R, int(offset),
+        _strides[4](op[1], op[2], xp[1], xp[2]), float(amplitude), int(bool(interleaved)), code, _stream_on(stream, dev)))
+    return out
+
+
+def kv_cache_write_rotary(k_new, v_new, k_cache, v_cache, slot_mapping, positions, frequencies, q=None, q_out=None,
+                          amplitude: float = 1.0, interleaved: bool = False, offset: int = 0, stream=None):
+    """kv_cache_write with the keys rotated by their positions on the way (see rotary_embed), and with q [T, Hq, D]
+    the queries too, into q_out (which may be q), in one launch.  k_new, v_new, q and q_out may be strided.
+    Queries are rotated whatever the token's slot.  Returns q_out."""
+    NB, Hkv, B, D = k_cache.shape
+    T = k_new.shape[0]
+    if k_new.shape != (T, Hkv, D) or v_new.shape != k_new.shape or v_cache.shape != k_cache.shape:
+        raise ValueError("shape mismatch between new tokens and caches")
+    if slot_mapping.shape != (T,) or positions.shape != (T,):
+        raise ValueError("slot_mapping and positions need one entry per token")
+    if (q is None) != (q_out is None):
+        raise ValueError("give both q and q_out, or neither")
+    if q is not None and (q.dim() != 3 or q.shape[0] != T or q.shape[2] != D or q_out.shape != q.shape):
+        raise ValueError("q and q_out must be [T, Hq, D]")
+    if q is not None and q.shape[1] == 0:
+        q = q_out = None
+    lib, dev, dt = _lib.load(), _device_of(k_cache, "k_cache"), k_cache.dtype
+    code = _dtype_code(k_cache)
+    kp, vp = _rows_ptr(k_new, "k_new", dt, dev), _rows_ptr(v_new, "v_new", dt, dev)
+    qp = _rows_ptr(q, "q", dt, dev) if q is not None else (None, 0, 0)
+    op = _rows_ptr(q_out, "q_out", dt, dev) if q is not None else (None, 0, 0)
+    fp, R = _frequencies(frequencies, None, dev)
+    _run_on(dev, "kv_cache_write_rotary", lib.kv_cache_write_rotary, (
+        op[0], qp[0], kp[0], vp[0], _ptr(k_cache, "k_cache", dt, dev), _ptr(v_cache, "v_cache", dt, dev),
+        _ptr(slot_mapping, "slot_mapping", torch.int64, dev), _ptr(positions, "positions", torch.int32, dev), fp, T,
+        q.shape[1] if q is not None else 0, Hkv, D, R, int(offset), B, NB,
+        _strides[8](op[1], op[2], qp[1], qp[2], kp[1], kp[2], vp[1], vp[2]), float(amplitude), int(bool(interleaved)), code,
+        _stream_on(stream, dev)))
+    return q_out
+
+
+def latent_cache_write(latent, k_rope, cache, slot_mapping, positions, frequencies, q_rope=None, q_out=None,
+                       amplitude: float = 1.0, interleaved: bool = False, stream=None):
+    """Store one row a token, [latent | k_rope rotated], in cache [NB, B, V + 64] at slot_mapping[t] (int64; negative =
+    skip): latent [T, V], k_rope [T, 64].  With q_rope [T, H, 64] the queries' rotary part is rotated too, into q_out
+    [T, H, 64], say q[..., V:] of the attention's queries.  Rows may be strided, in steps of 16 bytes.  Returns
+    q_out."""
+    NB, B, W = cache.shape
+    T, V = latent.shape
+    if W != V + LATENT_ROPE_DIM or k_rope.shape != (T, LATENT_ROPE_DIM):
+        raise ValueError("cache rows must be [latent | %d], k_rope [T, %d]" % (LATENT_ROPE_DIM, LATENT_ROPE_DIM))
+    if slot_mapping.shape != (T,) or positions.shape != (T,):
+        raise ValueError("slot_mapping and positions need one entry per token")
+    if (q_rope is None) != (q_out is None):
+        raise ValueError("give both q_rope and q_out, or neither")
+    if q_rope is not None and (q_rope.dim() != 3 or q_rope.shape[0] != T or q_rope.shape[2] != LATENT_ROPE_DIM or
+                               q_out.shape != q_rope.shape):
+        raise ValueError("q_rope and q_out must be [T, H, %d]" % LATENT_ROPE_DIM)
+    if q_rope is not None and q_rope.shape[1] == 0:
+        q_rope = q_out = None
+    lib, dev, dt = _lib.load(), _device_of(cache, "cache"), cache.dtype
+    code = _dtype_code(cache)
+    lp, kp = _rows_ptr(latent.unsqueeze(1), "latent", dt, dev), _rows_ptr(k_rope.unsqueeze(1), "k_rope", dt, dev)
+    qp = _rows_ptr(q_rope, "q_rope", dt, dev) if q_rope is not None else (None, 0, 0)
+    op = _rows_ptr(q_out, "q_out", dt, dev) if q_rope is not None else (None, 0, 0)
+    fp, _ = _frequencies(frequencies, LATENT_ROPE_DIM, dev)
+    _run_on(dev, "latent_cache_write", lib.latent_cache_write, (
+        op[0], qp[0], lp[0], kp[0], _ptr(cache, "cache", dt, dev), _ptr(slot_mapping, "slot_mapping", torch.int64, dev),
+        _ptr(positions, "positions", torch.int32, dev), fp, T, q_rope.shape[1] if q_rope is not None else 0, V, B, NB,
+        _strides[6](op[1], op[2], qp[1], qp[2], lp[1], kp[1]), float(amplitude), int(bool(interleaved)), code,
+        _stream_on(stream, dev)))
+    return q_out
+
+
+def paged_latent_attention_workspace_size(num_q_tokens: int, num_heads: int, latent_dim: int, max_seq_len: int,
+                                          dtype: torch.dtype = torch.bfloat16) -> int:
+    """Bytes of workspace of either latent attention call (num_q_tokens: the sequences of a decode)."""
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
+    return int(_lib.load().paged_latent_attention_workspace_size(num_q_tokens, num_heads, latent_dim, _int32(max_seq_len),
+                                                                 PKV_F32 if dtype == torch.float32 else PKV_BF16))
+
+
+def _latent_shapes(out, q, cache, block_tables, seq_lens):
+    """(T, H, V, NB, B, S, maxB) of a latent attention call."""
+    T, H, W = q.shape
+    NB, B, Wc = cache.shape
+    S = seq_lens.shape[0]
+    if Wc != W or W <= LATENT_ROPE_DIM or out.shape != (T, H, W - LATENT_ROPE_DIM):
+        raise ValueError("q must be [T, H, V + %d], cache [NB, B, V + %d], out [T, H, V]" % (LATENT_ROPE_DIM, LATENT_ROPE_DIM))
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or seq_lens.dim() != 1:
+        raise ValueError("block_tables must be [S, maxB] and seq_lens [S]")
+    return T, H, W - LATENT_ROPE_DIM, NB, B, S, block_tables.shape[1]
+
+
+def paged_latent_attention_decode(out, q, cache, block_tables, seq_lens, scale: float, max_seq_len: int,
+                                  workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """out[s, h] = sum_t softmax_t(scale * q[s, h] . c_t) c_t[:V] over the rows c_t = [latent | key part] of
+    sequence s's tokens: q [S, H, V + 64], out [S, H, V] (bf16 or float32), cache [NB, B, V + 64],
+    block_tables int32 [S, maxB], seq_lens int32 [S]."""
+    S, H, V, NB, B, n, maxb = _latent_shapes(out, q, cache, block_tables, seq_lens)
+    if n != S:
+        raise ValueError("one query per sequence")
+    lib, code, dt, i32 = _lib.load(), _dtype_code(q), q.dtype, torch.int32
+    dev, max_len = _device_of(q, "q"), _int32(max_seq_len)
+    _run_with_scratch(dev, "paged_latent_attention_decode", lib.paged_latent_attention_decode,
+                      lib.paged_latent_attention_workspace_size, (S, H, V, max_len, code), (
+        _ptr(out, "out", dt, dev), _ptr(q, "q", dt, dev), _ptr(cache, "cache", dt, dev),
+        _ptr(block_tables, "block_tables", i32, dev), _ptr(seq_lens, "seq_lens", i32, dev), S, H, V, B, maxb, NB, max_len,
+        float(scale)), workspace, (code, _stream_on(stream, dev)), stream)
+    return out
+
+
+def paged_latent_attention_multi_token(out, q, cache, block_tables, seq_lens, q_starts, scale: float, max_q_len: int,
+                                       max_seq_len: int, workspace: Optional[torch.Tensor] = None,
+                                       stream=None) -> torch.Tensor:
+    """paged_latent_attention_decode for each sequence's last Q_s positions, causal: sequence s owns the rows
+    q_starts[s] .. q_starts[s + 1] - 1 of q [T, H, V + 64] and out [T, H, V] (int32 [S + 1])."""
+    T, H, V, NB, B, S, maxb = _latent_shapes(out, q, cache, block_tables, seq_lens)
+    if q_starts.shape != (S + 1,):
+        raise ValueError("q_starts must be [S + 1]")
+    lib, code, dt, i32 = _lib.load(), _dtype_code(q), q.dtype, torch.int32
+    dev, max_len = _device_of(q, "q"), _int32(max_seq_len)
+    _run_with_scratch(dev, "paged_latent_attention_multi_token", lib.paged_latent_attention_multi_token,
+                      lib.paged_latent_attention_workspace_size, (T, H, V, max_len, code), (
+        _ptr(out, "out", dt, dev), _ptr(q, "q", dt, dev), _ptr(cache, "cache", dt, dev),
+        _ptr(block_tables, "block_tables", i32, dev), _ptr(seq_lens, "seq_lens", i32, dev),
+        _ptr(q_starts, "q_starts", i32, dev), S, T, H, V, B, maxb, NB, _int32(max_q_len), max_len, float(scale)), workspace,
+        (code, _stream_on(stream, dev)), stream)
     return out
 
 

@@ -47,6 +47,14 @@ SIGNATURES = {
     "paged_attention_multi_token_scored": (c_int, [c_void_p] * 7 + [c_int] * 10 +
                                            [c_float, c_float, c_void_p, c_int, c_void_p, c_void_p, c_void_p,
                                             c_size_t, c_void_p]),
+    "rotary_frequencies": (c_int, [c_void_p, c_int] + [ctypes.c_double] * 5),
+    "rotary_embed": (c_int, [c_void_p] * 4 + [c_int] * 5 + [c_void_p, c_float, c_int, c_int, c_void_p]),
+    "kv_cache_write_rotary": (c_int, [c_void_p] * 9 + [c_int] * 8 + [c_void_p, c_float, c_int, c_int, c_void_p]),
+    "latent_cache_write": (c_int, [c_void_p] * 8 + [c_int] * 5 + [c_void_p, c_float, c_int, c_int, c_void_p]),
+    "paged_latent_attention_workspace_size": (c_size_t, [c_int] * 5),
+    "paged_latent_attention_decode": (c_int, [c_void_p] * 5 + [c_int] * 7 + [c_float, c_void_p, c_size_t, c_int, c_void_p]),
+    "paged_latent_attention_multi_token": (c_int, [c_void_p] * 6 + [c_int] * 9 +
+                                           [c_float, c_void_p, c_size_t, c_int, c_void_p]),
     "paged_attention_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int, c_int]),
     "paged_attention_decode": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                        c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int,
