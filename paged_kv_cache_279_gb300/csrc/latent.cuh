@@ -53,5 +53,9 @@ __device__ __forceinline__ Seq sequence(const Args &a, int s) {
     return r;
 }
 
+// bf16 on the tensor cores: workspace of a call, and the call, its arguments checked.
+size_t mma_workspace(int64_t T, int H, int V);
+pkv_status run_mma(const Args &a, cudaStream_t st);
+
 }  // namespace latent
 }  // namespace pkv

@@ -7,7 +7,9 @@
 // (the absorbed form: the projections from the latent to a head's keys and values
 // are folded into the query and into what reads the output).
 //
-// latent_simt_kernel: float32, and the smallest calls.  A warp takes kRW heads of
+// bf16 runs on the tensor cores (latent_mma.cu).
+//
+// latent_simt_kernel: float32.  A warp takes kRW heads of
 // one query and every fourth batch of kTok tokens of a run of the context; its
 // lanes hold the heads' queries, the running output and the rows of the batch in
 // registers, split over the row's entries, so each row is read from memory once a
@@ -52,37 +54,14 @@ inline Split split_of(int64_t T, int H, int max_len) {
     return s;
 }
 
-template <typename T>
-struct Load;
-template <>
-struct Load<float> {
-    template <int N>
-    static __device__ __forceinline__ void row(const void *p, float (&x)[N]) {
-        if constexpr (N == 4) {
-            const float4 v = *reinterpret_cast<const float4 *>(p);
-            x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
-        } else {
-            const float2 v = *reinterpret_cast<const float2 *>(p);
-            x[0] = v.x, x[1] = v.y;
-        }
-    }
-};
-template <>
-struct Load<__nv_bfloat16> {
-    template <int N>
-    static __device__ __forceinline__ void row(const void *p, float (&x)[N]) {
-        if constexpr (N == 4) {
-            const uint2 v = *reinterpret_cast<const uint2 *>(p);
-            x[0] = bf16x2_lo(v.x), x[1] = bf16x2_hi(v.x), x[2] = bf16x2_lo(v.y), x[3] = bf16x2_hi(v.y);
-        } else {
-            const uint32_t v = *reinterpret_cast<const uint32_t *>(p);
-            x[0] = bf16x2_lo(v), x[1] = bf16x2_hi(v);
-        }
-    }
-};
-
-__device__ __forceinline__ void store(float *p, float x) { *p = x; }
-__device__ __forceinline__ void store(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void load4(const float *p, float *x) {
+    const float4 v = *reinterpret_cast<const float4 *>(p);
+    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+}
+__device__ __forceinline__ void load2(const float *p, float *x) {
+    const float2 v = *reinterpret_cast<const float2 *>(p);
+    x[0] = v.x, x[1] = v.y;
+}
 
 // Entry e of a lane's share of a row: lanes hold runs of 4 entries, 128 apart.
 __device__ __forceinline__ int entry(int lane, int e) { return (e >> 2) * 128 + 4 * lane + (e & 3); }
@@ -103,7 +82,7 @@ __device__ __forceinline__ int sequence_of(const Args &a, int tok) {
     return lo;
 }
 
-template <typename T, int V>
+template <int V>
 __global__ void __launch_bounds__(kWarps * 32) latent_simt_kernel(const __grid_constant__ Args a, Split sp) {
     constexpr int NV = V / 32;       // entries of the latent part a lane holds
     constexpr int D = V + kRope;
@@ -126,27 +105,22 @@ __global__ void __launch_bounds__(kWarps * 32) latent_simt_kernel(const __grid_c
     if (t0 >= end && part > 0) return;  // parts past the end are not merged either
 
     float q[kRW][NV + 2], o[kRW][NV], m[kRW], l[kRW];
-    const T *qb = (const T *)a.q + ((int64_t)tok * a.H + h0) * D;
+    const float *qb = (const float *)a.q + ((int64_t)tok * a.H + h0) * D;
 #pragma unroll
     for (int r = 0; r < kRW; ++r) {
-        const T *qr = qb + (int64_t)(r < nh ? r : 0) * D;
+        const float *qr = qb + (int64_t)(r < nh ? r : 0) * D;
 #pragma unroll
-        for (int j = 0; j < NV / 4; ++j) {
-            float x[4];
-            Load<T>::row(qr + j * 128 + 4 * lane, x);
+        for (int j = 0; j < NV / 4; ++j) load4(qr + j * 128 + 4 * lane, &q[r][4 * j]);
+        load2(qr + V + 2 * lane, &q[r][NV]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) q[r][4 * j + e] = x[e] * a.scale_log2;
-        }
-        float x[2];
-        Load<T>::row(qr + V + 2 * lane, x);
-        q[r][NV] = x[0] * a.scale_log2, q[r][NV + 1] = x[1] * a.scale_log2;
+        for (int e = 0; e < NV + 2; ++e) q[r][e] *= a.scale_log2;
 #pragma unroll
         for (int e = 0; e < NV; ++e) o[r][e] = 0.f;
         m[r] = -INFINITY;
         l[r] = 0.f;
     }
     const int32_t *table = a.tables + (int64_t)s * a.maxb;
-    const T *cache = (const T *)a.cache;
+    const float *cache = (const float *)a.cache;
     for (int t = t0 + warp * kTok; t < t1; t += kWarps * kTok) {
         float c[kTok][NV + 2];
         bool ok[kTok];
@@ -166,17 +140,10 @@ __global__ void __launch_bounds__(kWarps * 32) latent_simt_kernel(const __grid_c
 #pragma unroll
             for (int e = 0; e < NV + 2; ++e) c[k][e] = 0.f;
             if (ok[k]) {
-                const T *cr = cache + row * D;
+                const float *cr = cache + row * D;
 #pragma unroll
-                for (int j = 0; j < NV / 4; ++j) {
-                    float x[4];
-                    Load<T>::row(cr + j * 128 + 4 * lane, x);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) c[k][4 * j + e] = x[e];
-                }
-                float x[2];
-                Load<T>::row(cr + V + 2 * lane, x);
-                c[k][NV] = x[0], c[k][NV + 1] = x[1];
+                for (int j = 0; j < NV / 4; ++j) load4(cr + j * 128 + 4 * lane, &c[k][4 * j]);
+                load2(cr + V + 2 * lane, &c[k][NV]);
             }
         }
         // 16 sums over the lanes, by halves: after the step over lane bit 4, 3, 2, 1
@@ -260,7 +227,7 @@ __global__ void __launch_bounds__(kWarps * 32) latent_simt_kernel(const __grid_c
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) x += sh_o[w][e] * f[w];
             // a query that sees nothing has sum 0 and gets zeros
-            if (final) store((T *)a.out + orow * V + e, sum == 0.f ? 0.f : x * inv);
+            if (final) ((float *)a.out)[orow * V + e] = sum == 0.f ? 0.f : x * inv;
             else pr[e] = x;
         }
         if (!final && threadIdx.x == 0) pr[V] = top, pr[V + 1] = sum;
@@ -269,7 +236,6 @@ __global__ void __launch_bounds__(kWarps * 32) latent_simt_kernel(const __grid_c
 }
 
 // One CTA a (query, head): the parts of its context, in order.
-template <typename T>
 __global__ void __launch_bounds__(128) latent_join_kernel(const __grid_constant__ Args a, Split sp) {
     grid_dependency_wait();
     const int tok = blockIdx.x / a.H;
@@ -289,7 +255,7 @@ __global__ void __launch_bounds__(128) latent_join_kernel(const __grid_constant_
     for (int e = threadIdx.x; e < a.V; e += 128) {
         float x = 0.f;
         for (int k = 0; k < parts; ++k) x += p[k * partial_floats(a.V) + e] * exp2f(p[k * partial_floats(a.V) + a.V] - ref);
-        store((T *)a.out + (int64_t)blockIdx.x * a.V + e, sum == 0.f ? 0.f : x / sum);
+        ((float *)a.out)[(int64_t)blockIdx.x * a.V + e] = sum == 0.f ? 0.f : x / sum;
     }
 }
 
@@ -299,15 +265,18 @@ size_t simt_workspace(int64_t T, int H, int V) {
     return parts == 1 ? 0 : round256((size_t)T * H * parts * partial_floats(V) * sizeof(float));
 }
 
-template <typename T>
 pkv_status run_simt(const Args &a, cudaStream_t st) {
     const Split sp = split_of(a.T, a.H, a.max_len);
     const int64_t items = (int64_t)a.T * ((a.H + kRW - 1) / kRW);
     const dim3 grid((unsigned)items, (unsigned)sp.parts);
-    const pkv_status rc = a.V == 512 ? launch_pdl(latent_simt_kernel<T, 512>, grid, dim3(kWarps * 32), 0, st, a, sp)
-                                     : launch_pdl(latent_simt_kernel<T, 256>, grid, dim3(kWarps * 32), 0, st, a, sp);
+    const pkv_status rc = a.V == 512 ? launch_pdl(latent_simt_kernel<512>, grid, dim3(kWarps * 32), 0, st, a, sp)
+                                     : launch_pdl(latent_simt_kernel<256>, grid, dim3(kWarps * 32), 0, st, a, sp);
     if (rc != PKV_OK || sp.parts == 1) return rc;
-    return launch_pdl(latent_join_kernel<T>, dim3((unsigned)(a.T * a.H)), dim3(128), 0, st, a, sp);
+    return launch_pdl(latent_join_kernel, dim3((unsigned)(a.T * a.H)), dim3(128), 0, st, a, sp);
+}
+
+size_t workspace(int64_t T, int H, int V, int dtype) {
+    return dtype == PKV_F32 ? simt_workspace(T, H, V) : mma_workspace(T, H, V);
 }
 
 bool known_shape(int H, int V) { return H >= 1 && H <= 128 && (V == 256 || V == 512); }
@@ -329,9 +298,9 @@ pkv_status run(Args &a, float scale, size_t ws_bytes, int dtype, void *stream) {
     a.bshift = a.B == 8 ? 3 : a.B == 16 ? 4 : a.B == 32 ? 5 : 6;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.err = device_error_word();
-    const size_t need = simt_workspace(a.T, a.H, a.V);
+    const size_t need = workspace(a.T, a.H, a.V, dtype);
     if (need && (!a.ws || (reinterpret_cast<uintptr_t>(a.ws) & 255u) || ws_bytes < need)) return PKV_ERR_INVALID;
-    return dtype == PKV_F32 ? run_simt<float>(a, (cudaStream_t)stream) : run_simt<__nv_bfloat16>(a, (cudaStream_t)stream);
+    return dtype == PKV_F32 ? run_simt(a, (cudaStream_t)stream) : run_mma(a, (cudaStream_t)stream);
 }
 
 }  // namespace
@@ -344,7 +313,7 @@ using namespace pkv;
 PKV_API size_t paged_latent_attention_workspace_size(int num_q_tokens, int num_heads, int latent_dim, int max_seq_len, int dtype) {
     if (num_q_tokens < 1 || max_seq_len < 1 || !latent::known_shape(num_heads, latent_dim)) return 0;
     if (dtype != PKV_F32 && dtype != PKV_BF16) return 0;
-    return latent::simt_workspace(num_q_tokens, num_heads, latent_dim);
+    return latent::workspace(num_q_tokens, num_heads, latent_dim, dtype);
 }
 
 PKV_API pkv_status paged_latent_attention_decode(void *out, const void *q, const void *cache, const int32_t *block_tables,
