@@ -615,32 +615,55 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, factor: float = 1
     return out if device is None else out.to(device)
 
 
-def _rows_ptr(t, name: str, dtype, dev: int):
-    """(address, token stride, head stride) of rows [T, H, D] whose entries are contiguous."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, other tensors of the call on cuda:{dev}")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3:
+# The calls below check the shapes and strides of a call once for each combination they meet: the functions
+# under lru_cache see sizes alone, never a tensor, and give what the library's call takes of them.  Types, devices and
+# addresses are looked at in every call.
+_plans = functools.lru_cache(maxsize=4096)
+
+
+def _rows(name: str, shape, stride):
+    """Token and head stride of rows [T, H, D] whose entries are contiguous."""
+    if len(shape) != 3:
         raise ValueError(f"{name} must have 3 dimensions")
-    st, sh, sd = t.stride()
-    if sd != 1 and t.shape[2] > 1:
+    if stride[2] != 1 and shape[2] > 1:
         raise ValueError(f"the entries of a row of {name} must be contiguous")
     # strides of dimensions of one entry say nothing, and are not held against the call
-    return t.data_ptr(), st if t.shape[0] > 1 else 0, sh if t.shape[1] > 1 else 0
+    return stride[0] if shape[0] > 1 else 0, stride[1] if shape[1] > 1 else 0
 
 
-_strides = {n: ctypes.c_int64 * n for n in (4, 6, 8)}
+def _vector(name: str, shape, T: int) -> None:
+    if shape != (T,):
+        raise ValueError(f"{name} needs one entry per token")
 
 
-def _frequencies(frequencies, rotary_dim: Optional[int], dev: int):
-    if not isinstance(frequencies, torch.Tensor) or frequencies.dim() != 1:
+def _pairs(shape, rotary_dim: Optional[int] = None) -> int:
+    if len(shape) != 1:
         raise ValueError("frequencies must be a vector, one entry per rotated pair")
-    if rotary_dim is not None and frequencies.shape[0] * 2 != rotary_dim:
+    if rotary_dim is not None and 2 * shape[0] != rotary_dim:
         raise ValueError(f"frequencies needs {rotary_dim // 2} entries")
-    return _ptr(frequencies, "frequencies", torch.float64, dev), 2 * frequencies.shape[0]
+    return 2 * shape[0]
+
+
+def _row_ptr(t, name: str, dtype, dev: int) -> int:
+    """Address of a tensor of that type on device `dev`, whatever its strides."""
+    try:
+        if t.get_device() == dev and t.dtype is dtype:
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    raise ValueError(f"{name} is on {t.device}, other tensors of the call on cuda:{dev}")
+
+
+@_plans
+def _embed_plan(x, x_stride, out, out_stride, positions, frequencies):
+    if len(x) != 3 or out != x:
+        raise ValueError("x and out must have the same shape [T, H, D]")
+    _vector("positions", positions, x[0])
+    return (*x, _pairs(frequencies)), (ctypes.c_int64 * 4)(*_rows("out", out, out_stride), *_rows("x", x, x_stride))
 
 
 def rotary_embed(out, x, positions, frequencies, amplitude: float = 1.0, interleaved: bool = False, offset: int = 0,
@@ -649,19 +672,32 @@ def rotary_embed(out, x, positions, frequencies, amplitude: float = 1.0, interle
     entries from `offset` on, in pairs (i, i + R / 2) or, interleaved, (2 i, 2 i + 1), R = 2 * len(frequencies)
     (float64, radians per position); pair i turns by position * frequencies[i], scaled by `amplitude`.  Tokens
     and heads may be strided, in steps of 16 bytes."""
-    T, H, D = x.shape
-    if out.shape != x.shape:
-        raise ValueError("out and x must have the same shape")
-    if positions.shape != (T,):
-        raise ValueError("positions needs one entry per token")
-    lib, dev, dt = _lib.load(), _device_of(x, "x"), x.dtype
-    code = _dtype_code(x)
-    xp, op = _rows_ptr(x, "x", dt, dev), _rows_ptr(out, "out", dt, dev)
-    fp, R = _frequencies(frequencies, None, dev)
-    _run_on(dev, "rotary_embed", lib.rotary_embed, (
-        op[0], xp[0], _ptr(positions, "positions", torch.int32, dev), fp, T, H, D, R, int(offset),
-        _strides[4](op[1], op[2], xp[1], xp[2]), float(amplitude), int(bool(interleaved)), code, _stream_on(stream, dev)))
+    size, strides = _embed_plan(x.shape, x.stride(), out.shape, out.stride(), positions.shape, frequencies.shape)
+    dev, dt = _device_of(x, "x"), x.dtype
+    _run_on(dev, "rotary_embed", _lib.load().rotary_embed, (
+        _row_ptr(out, "out", dt, dev), x.data_ptr(), _ptr(positions, "positions", torch.int32, dev),
+        _ptr(frequencies, "frequencies", torch.float64, dev), *size, offset, strides, amplitude, bool(interleaved),
+        _dtype_code(x), _stream_on(stream, dev)))
     return out
+
+
+@_plans
+def _write_plan(k, k_stride, v, v_stride, k_cache, v_cache, slots, positions, frequencies, q, q_stride, out, out_stride):
+    if len(k_cache) != 4 or v_cache != k_cache:
+        raise ValueError("caches must be [NB, Hkv, B, D], and alike")
+    NB, Hkv, B, D = k_cache
+    if len(k) != 3 or k[1:] != (Hkv, D) or v != k:
+        raise ValueError("shape mismatch between new tokens and caches")
+    T, Hq, qs = k[0], 0, (0, 0, 0, 0)
+    _vector("slot_mapping", slots, T)
+    _vector("positions", positions, T)
+    if (q is None) != (out is None):
+        raise ValueError("give both q and q_out, or neither")
+    if q is not None:
+        if len(q) != 3 or q[0] != T or q[2] != D or out != q:
+            raise ValueError("q and q_out must be [T, Hq, D]")
+        Hq, qs = q[1], _rows("q_out", out, out_stride) + _rows("q", q, q_stride)
+    return (T, Hq, Hkv, D, _pairs(frequencies)), (B, NB), (ctypes.c_int64 * 8)(*qs, *_rows("k_new", k, k_stride), *_rows("v_new", v, v_stride))
 
 
 def kv_cache_write_rotary(k_new, v_new, k_cache, v_cache, slot_mapping, positions, frequencies, q=None, q_out=None,
@@ -669,31 +705,41 @@ def kv_cache_write_rotary(k_new, v_new, k_cache, v_cache, slot_mapping, position
     """kv_cache_write with the keys rotated by their positions on the way (see rotary_embed), and with q [T, Hq, D]
     the queries too, into q_out (which may be q), in one launch.  k_new, v_new, q and q_out may be strided.
     Queries are rotated whatever the token's slot.  Returns q_out."""
-    NB, Hkv, B, D = k_cache.shape
-    T = k_new.shape[0]
-    if k_new.shape != (T, Hkv, D) or v_new.shape != k_new.shape or v_cache.shape != k_cache.shape:
-        raise ValueError("shape mismatch between new tokens and caches")
-    if slot_mapping.shape != (T,) or positions.shape != (T,):
-        raise ValueError("slot_mapping and positions need one entry per token")
-    if (q is None) != (q_out is None):
-        raise ValueError("give both q and q_out, or neither")
-    if q is not None and (q.dim() != 3 or q.shape[0] != T or q.shape[2] != D or q_out.shape != q.shape):
-        raise ValueError("q and q_out must be [T, Hq, D]")
-    if q is not None and q.shape[1] == 0:
-        q = q_out = None
-    lib, dev, dt = _lib.load(), _device_of(k_cache, "k_cache"), k_cache.dtype
-    code = _dtype_code(k_cache)
-    kp, vp = _rows_ptr(k_new, "k_new", dt, dev), _rows_ptr(v_new, "v_new", dt, dev)
-    qp = _rows_ptr(q, "q", dt, dev) if q is not None else (None, 0, 0)
-    op = _rows_ptr(q_out, "q_out", dt, dev) if q is not None else (None, 0, 0)
-    fp, R = _frequencies(frequencies, None, dev)
-    _run_on(dev, "kv_cache_write_rotary", lib.kv_cache_write_rotary, (
-        op[0], qp[0], kp[0], vp[0], _ptr(k_cache, "k_cache", dt, dev), _ptr(v_cache, "v_cache", dt, dev),
-        _ptr(slot_mapping, "slot_mapping", torch.int64, dev), _ptr(positions, "positions", torch.int32, dev), fp, T,
-        q.shape[1] if q is not None else 0, Hkv, D, R, int(offset), B, NB,
-        _strides[8](op[1], op[2], qp[1], qp[2], kp[1], kp[2], vp[1], vp[2]), float(amplitude), int(bool(interleaved)), code,
-        _stream_on(stream, dev)))
+    some, out = q is not None, q_out is not None
+    size, blocks, strides = _write_plan(
+        k_new.shape, k_new.stride(), v_new.shape, v_new.stride(), k_cache.shape, v_cache.shape, slot_mapping.shape, positions.shape,
+        frequencies.shape, q.shape if some else None, q.stride() if some else None, q_out.shape if out else None,
+        q_out.stride() if out else None)
+    some = some and size[1] > 0
+    dev, dt = _device_of(k_cache, "k_cache"), k_cache.dtype
+    _run_on(dev, "kv_cache_write_rotary", _lib.load().kv_cache_write_rotary, (
+        _row_ptr(q_out, "q_out", dt, dev) if some else None, _row_ptr(q, "q", dt, dev) if some else None,
+        _row_ptr(k_new, "k_new", dt, dev), _row_ptr(v_new, "v_new", dt, dev), _ptr(k_cache, "k_cache", dt, dev),
+        _ptr(v_cache, "v_cache", dt, dev), _ptr(slot_mapping, "slot_mapping", torch.int64, dev),
+        _ptr(positions, "positions", torch.int32, dev), _ptr(frequencies, "frequencies", torch.float64, dev), *size, offset, *blocks,
+        strides, amplitude, bool(interleaved), _dtype_code(k_cache), _stream_on(stream, dev)))
     return q_out
+
+
+@_plans
+def _latent_write_plan(latent, latent_stride, key, key_stride, cache, slots, positions, frequencies, q, q_stride, out, out_stride):
+    if len(cache) != 3 or len(latent) != 2:
+        raise ValueError("cache must be [NB, B, V + %d], latent [T, V]" % LATENT_ROPE_DIM)
+    (NB, B, W), (T, V) = cache, latent
+    if W != V + LATENT_ROPE_DIM or key != (T, LATENT_ROPE_DIM):
+        raise ValueError("cache rows must be [latent | %d], k_rope [T, %d]" % (LATENT_ROPE_DIM, LATENT_ROPE_DIM))
+    _vector("slot_mapping", slots, T)
+    _vector("positions", positions, T)
+    _pairs(frequencies, LATENT_ROPE_DIM)
+    H, qs = 0, (0, 0, 0, 0)
+    if (q is None) != (out is None):
+        raise ValueError("give both q_rope and q_out, or neither")
+    if q is not None:
+        if len(q) != 3 or q[0] != T or q[2] != LATENT_ROPE_DIM or out != q:
+            raise ValueError("q_rope and q_out must be [T, H, %d]" % LATENT_ROPE_DIM)
+        H, qs = q[1], _rows("q_out", out, out_stride) + _rows("q_rope", q, q_stride)
+    rows = [_rows(n, (x[0], 1, x[1]), (st[0], 0, st[1]))[0] for n, x, st in (("latent", latent, latent_stride), ("k_rope", key, key_stride))]
+    return (T, H, V, B, NB), (ctypes.c_int64 * 6)(*qs, *rows)
 
 
 def latent_cache_write(latent, k_rope, cache, slot_mapping, positions, frequencies, q_rope=None, q_out=None,
@@ -702,29 +748,18 @@ def latent_cache_write(latent, k_rope, cache, slot_mapping, positions, frequenci
     skip): latent [T, V], k_rope [T, 64].  With q_rope [T, H, 64] the queries' rotary part is rotated too, into q_out
     [T, H, 64], say q[..., V:] of the attention's queries.  Rows may be strided, in steps of 16 bytes.  Returns
     q_out."""
-    NB, B, W = cache.shape
-    T, V = latent.shape
-    if W != V + LATENT_ROPE_DIM or k_rope.shape != (T, LATENT_ROPE_DIM):
-        raise ValueError("cache rows must be [latent | %d], k_rope [T, %d]" % (LATENT_ROPE_DIM, LATENT_ROPE_DIM))
-    if slot_mapping.shape != (T,) or positions.shape != (T,):
-        raise ValueError("slot_mapping and positions need one entry per token")
-    if (q_rope is None) != (q_out is None):
-        raise ValueError("give both q_rope and q_out, or neither")
-    if q_rope is not None and (q_rope.dim() != 3 or q_rope.shape[0] != T or q_rope.shape[2] != LATENT_ROPE_DIM or
-                               q_out.shape != q_rope.shape):
-        raise ValueError("q_rope and q_out must be [T, H, %d]" % LATENT_ROPE_DIM)
-    if q_rope is not None and q_rope.shape[1] == 0:
-        q_rope = q_out = None
-    lib, dev, dt = _lib.load(), _device_of(cache, "cache"), cache.dtype
-    code = _dtype_code(cache)
-    lp, kp = _rows_ptr(latent.unsqueeze(1), "latent", dt, dev), _rows_ptr(k_rope.unsqueeze(1), "k_rope", dt, dev)
-    qp = _rows_ptr(q_rope, "q_rope", dt, dev) if q_rope is not None else (None, 0, 0)
-    op = _rows_ptr(q_out, "q_out", dt, dev) if q_rope is not None else (None, 0, 0)
-    fp, _ = _frequencies(frequencies, LATENT_ROPE_DIM, dev)
-    _run_on(dev, "latent_cache_write", lib.latent_cache_write, (
-        op[0], qp[0], lp[0], kp[0], _ptr(cache, "cache", dt, dev), _ptr(slot_mapping, "slot_mapping", torch.int64, dev),
-        _ptr(positions, "positions", torch.int32, dev), fp, T, q_rope.shape[1] if q_rope is not None else 0, V, B, NB,
-        _strides[6](op[1], op[2], qp[1], qp[2], lp[1], kp[1]), float(amplitude), int(bool(interleaved)), code,
+    some, out = q_rope is not None, q_out is not None
+    size, strides = _latent_write_plan(
+        latent.shape, latent.stride(), k_rope.shape, k_rope.stride(), cache.shape, slot_mapping.shape, positions.shape,
+        frequencies.shape, q_rope.shape if some else None, q_rope.stride() if some else None, q_out.shape if out else None,
+        q_out.stride() if out else None)
+    some = some and size[1] > 0
+    dev, dt = _device_of(cache, "cache"), cache.dtype
+    _run_on(dev, "latent_cache_write", _lib.load().latent_cache_write, (
+        _row_ptr(q_out, "q_out", dt, dev) if some else None, _row_ptr(q_rope, "q_rope", dt, dev) if some else None,
+        _row_ptr(latent, "latent", dt, dev), _row_ptr(k_rope, "k_rope", dt, dev), _ptr(cache, "cache", dt, dev),
+        _ptr(slot_mapping, "slot_mapping", torch.int64, dev), _ptr(positions, "positions", torch.int32, dev),
+        _ptr(frequencies, "frequencies", torch.float64, dev), *size, strides, amplitude, bool(interleaved), _dtype_code(cache),
         _stream_on(stream, dev)))
     return q_out
 
@@ -738,16 +773,18 @@ def paged_latent_attention_workspace_size(num_q_tokens: int, num_heads: int, lat
                                                                  PKV_F32 if dtype == torch.float32 else PKV_BF16))
 
 
-def _latent_shapes(out, q, cache, block_tables, seq_lens):
-    """(T, H, V, NB, B, S, maxB) of a latent attention call."""
-    T, H, W = q.shape
-    NB, B, Wc = cache.shape
-    S = seq_lens.shape[0]
-    if Wc != W or W <= LATENT_ROPE_DIM or out.shape != (T, H, W - LATENT_ROPE_DIM):
+@_plans
+def _latent_plan(out, q, cache, tables, lens, starts):
+    """(S, T, H, V, B, maxB, NB); starts None: a decode."""
+    if len(q) != 3 or len(cache) != 3 or cache[2] != q[2] or q[2] <= LATENT_ROPE_DIM or out != (*q[:2], q[2] - LATENT_ROPE_DIM):
         raise ValueError("q must be [T, H, V + %d], cache [NB, B, V + %d], out [T, H, V]" % (LATENT_ROPE_DIM, LATENT_ROPE_DIM))
-    if block_tables.dim() != 2 or block_tables.shape[0] != S or seq_lens.dim() != 1:
+    if len(lens) != 1 or len(tables) != 2 or tables[0] != lens[0]:
         raise ValueError("block_tables must be [S, maxB] and seq_lens [S]")
-    return T, H, W - LATENT_ROPE_DIM, NB, B, S, block_tables.shape[1]
+    if starts is None and lens[0] != q[0]:
+        raise ValueError("one query per sequence")
+    if starts is not None and starts != (lens[0] + 1,):
+        raise ValueError("q_starts must be [S + 1]")
+    return lens[0], q[0], q[1], q[2] - LATENT_ROPE_DIM, cache[1], tables[1], cache[0]
 
 
 def paged_latent_attention_decode(out, q, cache, block_tables, seq_lens, scale: float, max_seq_len: int,
@@ -755,16 +792,14 @@ def paged_latent_attention_decode(out, q, cache, block_tables, seq_lens, scale: 
     """out[s, h] = sum_t softmax_t(scale * q[s, h] . c_t) c_t[:V] over the rows c_t = [latent | key part] of
     sequence s's tokens: q [S, H, V + 64], out [S, H, V] (bf16 or float32), cache [NB, B, V + 64],
     block_tables int32 [S, maxB], seq_lens int32 [S]."""
-    S, H, V, NB, B, n, maxb = _latent_shapes(out, q, cache, block_tables, seq_lens)
-    if n != S:
-        raise ValueError("one query per sequence")
+    S, _, H, V, B, maxb, NB = _latent_plan(out.shape, q.shape, cache.shape, block_tables.shape, seq_lens.shape, None)
     lib, code, dt, i32 = _lib.load(), _dtype_code(q), q.dtype, torch.int32
     dev, max_len = _device_of(q, "q"), _int32(max_seq_len)
     _run_with_scratch(dev, "paged_latent_attention_decode", lib.paged_latent_attention_decode,
                       lib.paged_latent_attention_workspace_size, (S, H, V, max_len, code), (
         _ptr(out, "out", dt, dev), _ptr(q, "q", dt, dev), _ptr(cache, "cache", dt, dev),
         _ptr(block_tables, "block_tables", i32, dev), _ptr(seq_lens, "seq_lens", i32, dev), S, H, V, B, maxb, NB, max_len,
-        float(scale)), workspace, (code, _stream_on(stream, dev)), stream)
+        scale), workspace, (code, _stream_on(stream, dev)), stream)
     return out
 
 
@@ -773,16 +808,14 @@ def paged_latent_attention_multi_token(out, q, cache, block_tables, seq_lens, q_
                                        stream=None) -> torch.Tensor:
     """paged_latent_attention_decode for each sequence's last Q_s positions, causal: sequence s owns the rows
     q_starts[s] .. q_starts[s + 1] - 1 of q [T, H, V + 64] and out [T, H, V] (int32 [S + 1])."""
-    T, H, V, NB, B, S, maxb = _latent_shapes(out, q, cache, block_tables, seq_lens)
-    if q_starts.shape != (S + 1,):
-        raise ValueError("q_starts must be [S + 1]")
+    S, T, H, V, B, maxb, NB = _latent_plan(out.shape, q.shape, cache.shape, block_tables.shape, seq_lens.shape, q_starts.shape)
     lib, code, dt, i32 = _lib.load(), _dtype_code(q), q.dtype, torch.int32
     dev, max_len = _device_of(q, "q"), _int32(max_seq_len)
     _run_with_scratch(dev, "paged_latent_attention_multi_token", lib.paged_latent_attention_multi_token,
                       lib.paged_latent_attention_workspace_size, (T, H, V, max_len, code), (
         _ptr(out, "out", dt, dev), _ptr(q, "q", dt, dev), _ptr(cache, "cache", dt, dev),
         _ptr(block_tables, "block_tables", i32, dev), _ptr(seq_lens, "seq_lens", i32, dev),
-        _ptr(q_starts, "q_starts", i32, dev), S, T, H, V, B, maxb, NB, _int32(max_q_len), max_len, float(scale)), workspace,
+        _ptr(q_starts, "q_starts", i32, dev), S, T, H, V, B, maxb, NB, _int32(max_q_len), max_len, scale), workspace,
         (code, _stream_on(stream, dev)), stream)
     return out
 

@@ -53,9 +53,12 @@ __device__ __forceinline__ Seq sequence(const Args &a, int s) {
     return r;
 }
 
-// bf16 on the tensor cores: workspace of a call, and the call, its arguments checked.
+// bf16 on the tensor cores: workspace of a call, and the call, its arguments checked.  run_mma: row tiles of up to
+// 64 rows; run_pair: of 128.
 size_t mma_workspace(int64_t T, int H, int V);
 pkv_status run_mma(const Args &a, cudaStream_t st);
+size_t pair_workspace(int V);
+pkv_status run_pair(const Args &a, cudaStream_t st);
 
 }  // namespace latent
 }  // namespace pkv

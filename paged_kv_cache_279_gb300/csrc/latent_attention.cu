@@ -30,6 +30,8 @@ constexpr int kRW = 4;     // heads of a warp
 constexpr int kTok = 4;    // tokens of a step
 constexpr int kWarps = 4;  // of a CTA: the same heads, different tokens
 
+constexpr int kPairRows = 64;  // a sequence's query rows above which pairs of CTAs take them (bf16)
+
 // How the tokens of a call are split over CTAs: `parts` runs of `run` tokens.
 struct Split {
     int parts, run;
@@ -259,10 +261,10 @@ __global__ void __launch_bounds__(128) latent_join_kernel(const __grid_constant_
     }
 }
 
-// Does not grow with the longest context: a call may bound that by its block tables.
-size_t simt_workspace(int64_t T, int H, int V) {
+// Grows with the longest context in one step, from nothing: a call may bound that by its block tables.
+size_t simt_workspace(int64_t T, int H, int V, int max_len) {
     const int parts = most_parts(T, H);
-    return parts == 1 ? 0 : round256((size_t)T * H * parts * partial_floats(V) * sizeof(float));
+    return parts == 1 || max_len <= 128 ? 0 : round256((size_t)T * H * parts * partial_floats(V) * sizeof(float));
 }
 
 pkv_status run_simt(const Args &a, cudaStream_t st) {
@@ -275,8 +277,10 @@ pkv_status run_simt(const Args &a, cudaStream_t st) {
     return launch_pdl(latent_join_kernel, dim3((unsigned)(a.T * a.H)), dim3(128), 0, st, a, sp);
 }
 
-size_t workspace(int64_t T, int H, int V, int dtype) {
-    return dtype == PKV_F32 ? simt_workspace(T, H, V) : mma_workspace(T, H, V);
+size_t workspace(int64_t T, int H, int V, int max_len, int dtype) {
+    if (dtype == PKV_F32) return simt_workspace(T, H, V, max_len);
+    const size_t one = mma_workspace(T, H, V), two = T * H > kPairRows ? pair_workspace(V) : 0;
+    return one > two ? one : two;
 }
 
 bool known_shape(int H, int V) { return H >= 1 && H <= 128 && (V == 256 || V == 512); }
@@ -298,9 +302,10 @@ pkv_status run(Args &a, float scale, size_t ws_bytes, int dtype, void *stream) {
     a.bshift = a.B == 8 ? 3 : a.B == 16 ? 4 : a.B == 32 ? 5 : 6;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.err = device_error_word();
-    const size_t need = workspace(a.T, a.H, a.V, dtype);
+    const size_t need = workspace(a.T, a.H, a.V, a.max_len, dtype);
     if (need && (!a.ws || (reinterpret_cast<uintptr_t>(a.ws) & 255u) || ws_bytes < need)) return PKV_ERR_INVALID;
-    return dtype == PKV_F32 ? run_simt(a, (cudaStream_t)stream) : run_mma(a, (cudaStream_t)stream);
+    if (dtype == PKV_F32) return run_simt(a, (cudaStream_t)stream);
+    return (int64_t)(a.q_starts ? a.max_q : 1) * a.H > kPairRows ? run_pair(a, (cudaStream_t)stream) : run_mma(a, (cudaStream_t)stream);
 }
 
 }  // namespace
@@ -313,7 +318,7 @@ using namespace pkv;
 PKV_API size_t paged_latent_attention_workspace_size(int num_q_tokens, int num_heads, int latent_dim, int max_seq_len, int dtype) {
     if (num_q_tokens < 1 || max_seq_len < 1 || !latent::known_shape(num_heads, latent_dim)) return 0;
     if (dtype != PKV_F32 && dtype != PKV_BF16) return 0;
-    return latent::workspace(num_q_tokens, num_heads, latent_dim, dtype);
+    return latent::workspace(num_q_tokens, num_heads, latent_dim, max_seq_len, dtype);
 }
 
 PKV_API pkv_status paged_latent_attention_decode(void *out, const void *q, const void *cache, const int32_t *block_tables,

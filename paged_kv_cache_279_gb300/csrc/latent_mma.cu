@@ -25,93 +25,15 @@
 // context cut by share boundaries leaves partial results that a second kernel joins.
 #include <cmath>
 
-#include "latent.cuh"
-#include "pkv_ptx.cuh"
+#include "latent_tc.cuh"
 
 namespace pkv {
 namespace latent {
 
 namespace {
 
-__device__ __forceinline__ void ld_16x256b(uint32_t taddr, uint32_t (&r)[8]) {
-    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr));
-}
-
-__device__ __forceinline__ void ld_16x256b(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-                 : "r"(taddr));
-}
-
-__device__ __forceinline__ void ld_16x256b(uint32_t taddr, uint32_t (&r)[32]) {
-    asm volatile("tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-                 : "r"(taddr));
-}
-
-__device__ __forceinline__ void ld_32x32b(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-                 : "r"(taddr));
-}
-
-__device__ __forceinline__ void ld_32x32b(uint32_t taddr, uint32_t (&r)[32]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-                 : "r"(taddr));
-}
-
-__device__ __forceinline__ void st_32x32b(uint32_t taddr, const uint32_t (&r)[16]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
-}
-
-__device__ __forceinline__ void st_32x32b(uint32_t taddr, const uint32_t (&r)[32]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]) : "memory");
-}
-
 constexpr int kTok = 64;       // tokens of a tile
 constexpr int kThreads = 224;  // producer warp, a warp that issues each product, four softmax warps
-constexpr int kDescs = 4;
-constexpr int kHead = 2;       // tiles that a context's start and end are worth
-constexpr float kSlack = 8.f;  // log2 of how far a weight may pass 1 before its row's reference moves
-
-// kind::f16 instruction descriptor: bf16 operands, float32 accumulators.
-__host__ __device__ constexpr uint32_t idesc(int m, int n, bool a_mn, bool b_mn) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
-           ((uint32_t)(m >> 4) << 24);
-}
-
-__device__ __forceinline__ bool elect_one() {
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-    return p != 0;
-}
-
-// Maximum of three that is NaN if one of them is.
-__device__ __forceinline__ float max3_nan(float a, float b, float c) {
-    float d;
-    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-
-// Barrier of the softmax warps, alone and with a vote.
-constexpr int kSoftmax = 128;
-__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kSoftmax) : "memory"); }
-__device__ __forceinline__ bool softmax_any(bool x) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"((uint32_t)x), "n"(kSoftmax)
-        : "memory");
-    return r != 0;
-}
-
-__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
-}
 
 __device__ __forceinline__ void stmatrix_x4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
@@ -171,16 +93,6 @@ struct L {
     static_assert(kS + 2 * N <= kCols, "tensor memory");
 };
 
-// One share's part of a context.
-struct Piece {
-    int tiles;     // 0: no more pieces
-    int t0, end;   // first token of the first tile; tokens that some row of the row tile sees
-    int row0, rows;
-    int lim0;      // tokens that row r sees: lim0 + (qh0 + r) / H
-    int qh0;
-    int out;       // 0: the whole context; 1: its first tiles; 2: later ones
-};
-
 struct alignas(8) Misc {
     uint64_t full[2][4], empty[2][4], q_full[2], q_empty[2], s_full[2], s_free[2], p_full, pv_done, o_free, desc_full[kDescs], desc_empty[kDescs], fin[2];
     Piece piece[kDescs];
@@ -190,52 +102,6 @@ struct alignas(8) Misc {
     int dead;
 };
 static_assert(sizeof(Misc) <= 2048, "misc");
-
-// The walk over contexts (sequence, row tile): row tile k of a sequence is rows
-// [k N, k N + N) of its n H query rows.  Its last row's query sees
-//     p0 + 1 + floor(min(k N + N - 1, n H - 1) / H)  tokens, p0 = L - n0 the first query's position,
-// A context counts kHead tiles more than it has, at its start: what its queries' load and the
-// storing of its output take.  Its tiles are, but for the last row tile, floor((k + c) / m) with m = 64 H / N and
-// c = floor((N - 1 + H (p0 + 64)) / N): sums over k have a closed form.
-template <int N>
-struct Walk {
-    int s, k, R;           // sequence, row tile, row tiles of the sequence
-    int L, q0, nH, p0, k0; // k0: first row tile with a query that sees a token
-    bool flagged;
-    __device__ __forceinline__ void open(const Args &a, int seq) {
-        s = seq;
-        const Seq q = sequence(a, seq);
-        flagged = q.flagged;
-        L = q.L, q0 = q.q0, nH = q.n * a.H, p0 = q.L - q.n0;
-        R = (nH + N - 1) / N;
-        const int blind = max(0, min(q.n, -p0));  // queries in front of the context
-        k0 = L == 0 ? R : (int)((int64_t)blind * a.H / N);
-        if (blind == q.n) k0 = R;
-        k = k0;
-    }
-    __device__ __forceinline__ int end(const Args &a, int kk) const {  // tokens row tile kk sees
-        if (!a.q_starts) return L;
-        const int last = min((kk + 1) * N, nH) - 1;
-        return min(L, p0 + 1 + last / a.H);
-    }
-    __device__ __forceinline__ int tiles(const Args &a, int kk) const { return (end(a, kk) + kTok - 1) / kTok; }
-    // tiles, heads included, of row tiles k0 .. kk - 1, kk < R
-    __device__ __forceinline__ int64_t before(const Args &a, int kk) const {
-        if (kk <= k0) return 0;
-        const int64_t m = (int64_t)kTok / N * a.H;  // N divides 64
-        const int64_t c = (N - 1 + (int64_t)a.H * (p0 + kTok)) >> (N == 16 ? 4 : N == 32 ? 5 : 6);  // floor: p0 may be below -64
-        return G(kk + c, m) - G(k0 + c, m) + (int64_t)kHead * (kk - k0);
-    }
-    static __device__ __forceinline__ int64_t G(int64_t x, int64_t m) {  // sum of floor(j / m), j < x
-        const int64_t q = x / m;
-        return m * (q * (q - 1) / 2) + q * (x - q * m);
-    }
-    __device__ __forceinline__ int64_t total(const Args &a) const {
-        if (k0 >= R) return 0;
-        if (!a.q_starts) return (int64_t)R * (tiles(a, 0) + kHead);  // one query: every row tile sees all
-        return before(a, R - 1) + tiles(a, R - 1) + kHead;
-    }
-};
 
 struct Ws {
     int *rec;      // [shares][4]: first row, rows, pieces of the context that begins in a share and is cut
@@ -252,8 +118,6 @@ __device__ __forceinline__ Ws ws_of(const Args &a, int shares, int n, int v) {
     w.rec = (int *)(w.ml + (size_t)shares * 2 * 2 * n);
     return w;
 }
-
-constexpr int kMinShare = 2;  // tiles of a share
 
 template <int V, int N>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -285,83 +149,14 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     grid_dependency_wait();
     grid_launch_dependents();  // the join kernel; it waits for this one before it reads
 
-    // The block tables, read later one entry after another, on their way into L2.
-    if (const int64_t line = (int64_t)cta * kThreads + threadIdx.x; (int64_t)a.S * a.maxb <= 1 << 17 && line * 32 < (int64_t)a.S * a.maxb)
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.tables + line * 32));
-
-    // Where this CTA's share begins: each thread sums the tiles of a run of sequences,
-    // one of them finds the share's first tile in its run.
-    int64_t *scan = reinterpret_cast<int64_t *>(m.red);  // warps' totals; then the first tile's offset, and its row tile
-    Walk<N> &begin = *reinterpret_cast<Walk<N> *>(scan + 10);
-    const int run = (a.S + kThreads - 1) / kThreads;
-    const int sb = min(a.S, (int)threadIdx.x * run), se = min(a.S, sb + run);
-    int64_t mine = 0;
-    Walk<N> w;
-    for (int s = sb; s < se; ++s) {
-        w.open(a, s);
-        mine += w.total(a);
-        if (w.flagged && s % G == cta) flag_error(a.err, PKV_DEVERR_SEQ_LEN);
-    }
-    int64_t incl = mine;
-    for (int d = 1; d < 32; d <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += y;
-    }
-    if (lane == 31) scan[warp] = incl;
-    __syncthreads();
-    int64_t base = 0, total = 0;
-    for (int i = 0; i < kThreads / 32; ++i) {
-        if (i < warp) base += scan[i];
-        total += scan[i];
-    }
-    const int64_t excl = base + incl - mine;
-    int64_t parts = total >= (int64_t)G * kMinShare ? G : (int)total / kMinShare;
-    if (parts < 1) parts = 1;
-    const bool idle = total == 0 || cta >= parts;
-    int64_t first = 0, last = 0;
-    if (!idle && total < (1 << 24)) {  // 32-bit division is a fifth of the time (parts <= 152)
-        first = (uint32_t)cta * (uint32_t)total / (uint32_t)parts;
-        last = (uint32_t)(cta + 1) * (uint32_t)total / (uint32_t)parts;
-    } else if (!idle) {
-        first = (int64_t)cta * total / parts;
-        last = (int64_t)(cta + 1) * total / parts;
-    }
-    if (!idle && first >= excl && first < excl + mine) {
-        int64_t off = first - excl;
-        int s = sb;
-        for (;; ++s) {
-            w.open(a, s);
-            const int64_t t = w.total(a);
-            if (off < t) break;
-            off -= t;
-        }
-        int k;
-        if (!a.q_starts) {
-            k = (int)(off / (w.tiles(a, 0) + kHead));
-            off -= (int64_t)k * (w.tiles(a, 0) + kHead);
-        } else {
-            int lo = w.k0, hi = w.R;  // the last k with before(k) <= off
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (w.before(a, mid) <= off) lo = mid;
-                else hi = mid;
-            }
-            k = lo;
-            off -= w.before(a, k);
-        }
-        w.k = k;
-        begin = w;
-        scan[8] = off;
-    }
+    prefetch_tables(a, (int64_t)cta * kThreads + threadIdx.x);
+    Share<N, kTok> sh = locate<N, kTok>(a, &m.red[0][0], cta, G, kThreads);
     const Ws ws = ws_of(a, G, N, V);
     if (threadIdx.x == 0) ws.rec[4 * cta + 2] = 0;
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
     const uint32_t tmem = m.tmem;
-    const int64_t at_off = scan[8];
-    w = begin;
-    __syncthreads();
 
     bool dead = false;
     auto wait = [&](uint64_t *bar, uint32_t parity) {  // by whole warps
@@ -377,110 +172,75 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         }
     };
 
-    if (idle) {
-    } else if (warp == 0) {
+    if (warp == 0) {
         // ======================= producer =======================
-        int64_t off = at_off;
-        int64_t left = last - first;
         int tile = 0, np = 0, nq = 0, halves = 0;  // tiles, pieces, queries and parts of tiles issued
         for (;;) {
             const int d = np % kDescs;
             wait(&m.desc_empty[d], (uint32_t)(np / kDescs + 1) & 1u);
-            if (left == 0 || dead) {
-                if (lane == 0) {
-                    m.piece[d].tiles = 0;
-                    mbar_arrive(&m.desc_full[d]);
-                }
-                break;
+            Piece pc;
+            int shares;
+            const bool more = !dead && sh.take(a, cta, pc, shares);
+            if (!more) pc.tiles = 0;
+            if (lane == 0) {
+                m.piece[d] = pc;
+                mbar_arrive(&m.desc_full[d]);
+                if (more && shares) ws.rec[4 * cta] = pc.row0, ws.rec[4 * cta + 1] = pc.rows, ws.rec[4 * cta + 2] = shares;
             }
-            // of the context's kHead + nt tiles, `take` from `off` on are this share's
-            const int nt = w.tiles(a, w.k);
-            const int take = (int)min((int64_t)nt + kHead - off, left);
-            const int i0 = max(0, (int)off - kHead), n = max(0, (int)off + take - kHead) - i0;
-            if (n > 0) {
-                Piece pc;
-                pc.tiles = n;
-                pc.t0 = i0 * kTok;
-                pc.end = w.end(a, w.k);
-                pc.qh0 = w.k * N;
-                pc.row0 = w.q0 * a.H + pc.qh0;
-                pc.rows = min(N, w.nH - pc.qh0);
-                pc.lim0 = w.p0 + 1;
-                pc.out = n == nt ? 0 : i0 == 0 ? 1 : 2;
+            __syncwarp();
+            if (!more) break;
+            const int n = pc.tiles;
+            const int32_t *table = a.tables + (int64_t)sh.w.s * a.maxb;
+            // lane l: the cache row of group l & 7 of tile t + (l >> 3); -1: a bad block; -2: no token
+            auto look = [&](int t) {
+                const int tok = pc.t0 + t * kTok + 8 * lane;
+                if (t + (lane >> 3) >= n || tok >= pc.end) return -2;
+                const int blk = __ldg(table + (tok >> a.bshift));
+                return (unsigned)blk < (unsigned)a.NB ? (blk << a.bshift) + (tok & (a.B - 1)) : -1;
+            };
+            auto load_q = [&] {
+                const int qb = np % X::kQBufs;
+                wait(&m.q_empty[qb], (uint32_t)(np / X::kQBufs + 1) & 1u);
+                if (dead) return;
                 if (lane == 0) {
-                    m.piece[d] = pc;
-                    mbar_arrive(&m.desc_full[d]);
-                    if (pc.out == 1) {  // how many shares the rest of the context reaches into
-                        const int64_t stop = last + (nt - n);  // the context's end in the row of all tiles
-                        ws.rec[4 * cta] = pc.row0;
-                        ws.rec[4 * cta + 1] = pc.rows;
-                        ws.rec[4 * cta + 2] = (int)(share_owner(stop - 1, total, parts) - cta) + 1;
-                    }
+                    mbar_arrive_expect_tx(&m.q_full[qb], (uint32_t)X::kQ);
+                    tma_load_3d(smem_u32(smem + X::q) + (uint32_t)(qb * X::kQ), &tm_q, smem_u32(&m.q_full[qb]), 0, pc.row0, 0);
+                }
+                ++nq;
+                __syncwarp();
+            };
+            int row = look(0), next = -2;
+            if (X::kQBufs == 2) load_q();
+            for (int t = 0; t < n && !dead; ++t, ++tile) {
+                if ((t & 3) == 0) {
+                    if (t) row = next;
+                    next = look(t + 4);
+                }
+                const int st = tile % X::kStages;
+                const bool turn = (lane >> 3) == (t & 3);
+                // a group without tokens starts past the tensor's end: zeros
+                const int y = row >= 0 ? row : a.NB << a.bshift;
+                const uint32_t dst = smem_u32(smem + X::ring) + (uint32_t)(st * X::kTile + (lane & 7) * X::kGroup);
+                wait(&m.empty[0][st], (uint32_t)(tile / X::kStages + 1) & 1u);
+                if (dead) break;
+                if (turn && row == -1) flag_error(a.err, PKV_DEVERR_BLOCK_ID);
+                const uint32_t ok = __ballot_sync(0xffffffffu, row >= 0) >> (8 * (t & 3)) & 0xffu;
+                if (lane == 0) {
+                    m.groups[st] = ok;
+                    mbar_arrive_expect_tx(&m.full[0][st], (uint32_t)(kTok * 128 * X::kPart0));
                 }
                 __syncwarp();
-                const int32_t *table = a.tables + (int64_t)w.s * a.maxb;
-                // lane l: the cache row of group l & 7 of tile t + (l >> 3); -1: a bad block; -2: no token
-                auto look = [&](int t) {
-                    const int tok = pc.t0 + t * kTok + 8 * lane;
-                    if (t + (lane >> 3) >= n || tok >= pc.end) return -2;
-                    const int blk = __ldg(table + (tok >> a.bshift));
-                    return (unsigned)blk < (unsigned)a.NB ? (blk << a.bshift) + (tok & (a.B - 1)) : -1;
-                };
-                auto load_q = [&] {
-                    const int qb = np % X::kQBufs;
-                    wait(&m.q_empty[qb], (uint32_t)(np / X::kQBufs + 1) & 1u);
-                    if (dead) return;
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(&m.q_full[qb], (uint32_t)X::kQ);
-                        tma_load_3d(smem_u32(smem + X::q) + (uint32_t)(qb * X::kQ), &tm_q, smem_u32(&m.q_full[qb]), 0, pc.row0, 0);
-                    }
-                    ++nq;
-                    __syncwarp();
-                };
-                int row = look(0), next = -2;
-                if (X::kQBufs == 2) load_q();
-                for (int t = 0; t < n && !dead; ++t, ++tile) {
-                    if ((t & 3) == 0) {
-                        if (t) row = next;
-                        next = look(t + 4);
-                    }
-                    const int st = tile % X::kStages;
-                    const bool turn = (lane >> 3) == (t & 3);
-                    // a group without tokens starts past the tensor's end: zeros
-                    const int y = row >= 0 ? row : a.NB << a.bshift;
-                    const uint32_t dst = smem_u32(smem + X::ring) + (uint32_t)(st * X::kTile + (lane & 7) * X::kGroup);
-                    wait(&m.empty[0][st], (uint32_t)(tile / X::kStages + 1) & 1u);
-                    if (dead) break;
-                    if (turn && row == -1) flag_error(a.err, PKV_DEVERR_BLOCK_ID);
-                    const uint32_t ok = __ballot_sync(0xffffffffu, row >= 0) >> (8 * (t & 3)) & 0xffu;
-                    if (lane == 0) {
-                        m.groups[st] = ok;
-                        mbar_arrive_expect_tx(&m.full[0][st], (uint32_t)(kTok * 128 * X::kPart0));
-                    }
-                    __syncwarp();
-                    if (turn) tma_load_3d(dst, &tm_c0, smem_u32(&m.full[0][st]), 0, y, 0);
-                    ++halves;
-                    wait(&m.empty[1][st], (uint32_t)(tile / X::kStages + 1) & 1u);
-                    if (dead) break;
-                    if (lane == 0) mbar_arrive_expect_tx(&m.full[1][st], (uint32_t)(X::kTile - kTok * 128 * X::kPart0));
-                    __syncwarp();
-                    if (turn) tma_load_3d(dst + X::kPart0 * 1024, &tm_c1, smem_u32(&m.full[1][st]), 0, y, X::kPart0);
-                    ++halves;
-                    if (X::kQBufs == 1 && t == 0) load_q();
-                }
-                ++np;
+                if (turn) tma_load_3d(dst, &tm_c0, smem_u32(&m.full[0][st]), 0, y, 0);
+                ++halves;
+                wait(&m.empty[1][st], (uint32_t)(tile / X::kStages + 1) & 1u);
+                if (dead) break;
+                if (lane == 0) mbar_arrive_expect_tx(&m.full[1][st], (uint32_t)(X::kTile - kTok * 128 * X::kPart0));
+                __syncwarp();
+                if (turn) tma_load_3d(dst + X::kPart0 * 1024, &tm_c1, smem_u32(&m.full[1][st]), 0, y, X::kPart0);
+                ++halves;
+                if (X::kQBufs == 1 && t == 0) load_q();
             }
-            left -= take;
-            off = 0;
-            if (left > 0 && ++w.k >= w.R) {
-                do {
-                    if (w.s + 1 >= a.S) {  // lengths that changed under the call
-                        dead = true;
-                        break;
-                    }
-                    w.open(a, w.s + 1);
-                } while (w.k0 >= w.R);
-            }
+            ++np;
         }
         // no copy outlives the CTA, whoever else gave up
         for (int i = max(0, halves - 2 * X::kStages); i < halves; ++i)
@@ -834,7 +594,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) latent_mma_join_kernel(const 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // queries that see nothing, but for those in a row tile with others
     for (int s = blockIdx.y * gridDim.x + blockIdx.x; s < a.S; s += gridDim.x * gridDim.y) {
-        Walk<N> w;
+        Walk<N, kTok> w;
         w.open(a, s);
         const int64_t vecs = min((int64_t)w.k0 * N, (int64_t)w.nH) * (V / 8);
         uint4 *o = reinterpret_cast<uint4 *>((__nv_bfloat16 *)a.out + (int64_t)w.q0 * a.H * V);
@@ -881,20 +641,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32) latent_mma_join_kernel(const 
 #pragma unroll
         for (int i = 0; i < 2; ++i) sum[j][i] = sum[j][i] == 0.f ? 0.f : 1.f / sum[j][i];
     emit<V, 16>(o, sum, smem_u32(sh) + (uint32_t)(warp * 16 * 32), lane, (__nv_bfloat16 *)a.out + (int64_t)row0 * V + 16 * unit, rows);
-}
-
-// Rows of V + 64 entries as [chunk of 64 entries][row][64]: a box of `box` rows and `deep` chunks.
-bool make_map(CUtensorMap *map, const void *base, int64_t rows, int V, int box, int deep) {
-    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
-    if (!enc) return false;
-    const int chunks = V / 64 + 1;
-    cuuint64_t dims[3] = {64u, (cuuint64_t)rows, (cuuint64_t)chunks};
-    cuuint64_t strides[2] = {(cuuint64_t)(V + kRope) * 2, 128u};
-    cuuint32_t boxd[3] = {64u, (cuuint32_t)box, (cuuint32_t)deep};
-    cuuint32_t estr[3] = {1u, 1u, 1u};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, boxd, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Rows of a row tile: the smallest that holds a sequence's query rows, or 64.

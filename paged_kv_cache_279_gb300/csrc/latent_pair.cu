@@ -1,0 +1,679 @@
+// Latent attention on the 5th-generation tensor cores (bf16), for sequences of more than 64 query
+// rows (several queries, or more than 64 heads): pairs of CTAs on one tile.
+//
+// A row tile is 128 consecutive query rows (a row: one head of one query), 64 a CTA; a tile is 128 tokens.
+//     S = Q C^T    [128 rows x 128 tokens]   Q and S by rows over the two CTAs, C by tokens
+//     O += P L     [128 rows x V entries]    P and O by rows, L by entries
+// with cta_group::2 instructions: each CTA's operands feed both tensor cores, so for a product of 128 x 128
+// (or x 256) an SM reads 64 rows of A and half of B from its shared memory -- half of what the transposed
+// products of 64 rows read for the same work, which is what bounds those.  O of 64 rows takes 256 columns of
+// tensor memory a CTA (V = 512), two S of 64 columns each fit beside it.
+//
+// Each CTA holds a tile's rows twice, in the two forms the products want: 64 tokens by all entries, and all
+// tokens by half of the entries.  Both are read in parts, and a part is loaded anew as soon as the product that read
+// it is done: with V = 512 one tile of each form is all that fits beside Q and P.
+//
+// The leader's (rank 0's) warps issue all products.  What the other CTA has ready it reports to the leader's
+// barriers; what the products have done arrives at both CTAs' barriers.
+//
+// Softmax: a thread has one row and half of the tile's tokens; its pair is 64 threads on.  References, weights,
+// hidden rows, shares and joins as in the transposed kernel.
+#include "latent_tc.cuh"
+
+namespace pkv {
+namespace latent {
+
+namespace {
+
+constexpr int kRows = 128, kTok = 128;
+constexpr int kThreads = 256;  // two producers, a warp for each product (the other CTA's reports loads), four softmax warps
+
+template <int V>
+struct L {
+    static constexpr int kChunks = V / 64 + 1;
+    static constexpr int kPart0 = V / 128;                 // chunks of the first part of the rows by tokens
+    static constexpr int kGroupK = kChunks * 1024;         // bytes of 8 tokens, all entries
+    static constexpr int kGroupV = V / 128 * 1024;         // 8 tokens, half of the latent entries
+    static constexpr int kK = 8 * kGroupK, kV = 16 * kGroupV;
+    static constexpr int kQ = kChunks * 64 * 128;
+    static constexpr int kP = 64 * kTok * 2;
+    static constexpr int q = 0, p = kQ, k = p + kP, v = k + kK, misc = v + kV, total = misc + 2048;
+    static constexpr int kBlocks = V / 256;                // products of 256 entries
+    static constexpr uint32_t kS = kBlocks * 128;          // first column of S
+    static constexpr uint32_t kCols = kS + 128 <= 256 ? 256 : 512;
+    static_assert(total <= 232448 && kS + 128 <= kCols, "memory");
+};
+
+struct alignas(8) Misc {
+    uint64_t k_full[2], k_peer[2], k_empty[2], v_full[2], v_peer[2], v_empty[2], q_full, q_peer, q_empty, s_full[2], s_free[2], p_full, pv_done, o_free;
+    uint64_t meta[4], desc_full[kDescs], desc_empty[kDescs], fin[2], bad_full[2];
+    Piece piece[kDescs];
+    float red[256];
+    uint32_t groups[4];   // valid 8-token groups of a tile
+    uint32_t warp_bad[4][2];
+    uint32_t bad_here[4], bad_there[2][4];
+    uint32_t tmem;
+    int dead;
+};
+static_assert(sizeof(Misc) <= 2048, "misc");
+
+struct Ws {
+    int *rec;
+    float *o;   // [shares][2][2 CTAs][V / 4][128 threads][4]... one thread's entries, four at a time
+    float *ml;  // [shares][2][2 CTAs][2][64]
+};
+inline size_t ws_bytes(int shares, int v) { return (size_t)shares * 16 + (size_t)shares * 2 * kRows * (v + 2) * 4 + 512; }
+__device__ __forceinline__ Ws ws_of(const Args &a, int shares, int v) {
+    Ws w;
+    w.o = (float *)a.ws;
+    w.ml = w.o + (size_t)shares * 2 * kRows * v;
+    w.rec = (int *)(w.ml + (size_t)shares * 2 * 2 * kRows);
+    return w;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// The other CTA's (or the leader's) address of what lies at p here.
+__device__ __forceinline__ uint32_t at_rank(const void *p, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void store_at(uint32_t addr, uint32_t x) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void mma2(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(id), "r"(acc)
+        : "memory");
+}
+// Arrives at `bar` of both CTAs when this thread's products so far are done.
+__device__ __forceinline__ void commit_both(uint64_t *bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+        "h"((unsigned short)3)
+        : "memory");
+}
+
+template <int V>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k0, const __grid_constant__ CUtensorMap tm_k1,
+                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Args a) {
+    using X = L<V>;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    Misc &m = *reinterpret_cast<Misc *>(smem + X::misc);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
+    const uint32_t rank = cluster_rank();
+    const bool lead = rank == 0;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&m.k_full[i], 1), mbar_init(&m.k_peer[i], 1), mbar_init(&m.k_empty[i], 1);
+            mbar_init(&m.v_full[i], 1), mbar_init(&m.v_peer[i], 1), mbar_init(&m.v_empty[i], 1);
+            mbar_init(&m.s_full[i], 1), mbar_init(&m.s_free[i], 8);
+            mbar_init(&m.fin[i], 1), mbar_init(&m.bad_full[i], 1);
+        }
+        mbar_init(&m.q_full, 1), mbar_init(&m.q_peer, 1), mbar_init(&m.q_empty, 1);
+        mbar_init(&m.p_full, 8), mbar_init(&m.pv_done, 1), mbar_init(&m.o_free, 8);
+        for (int i = 0; i < 4; ++i) mbar_init(&m.meta[i], 1);
+        for (int i = 0; i < kDescs; ++i) mbar_init(&m.desc_full[i], 1), mbar_init(&m.desc_empty[i], 7);
+        m.dead = 0;
+        fence_barrier_init();
+    }
+    if (threadIdx.x == 32) prefetch_map(&tm_q), prefetch_map(&tm_k0), prefetch_map(&tm_k1), prefetch_map(&tm_v);
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&m.tmem)), "r"(X::kCols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    grid_dependency_wait();
+    grid_launch_dependents();  // the join kernel; it waits for this one before it reads
+    prefetch_tables(a, (int64_t)blockIdx.x * kThreads + threadIdx.x);
+    Share<kRows, kTok> sh = locate<kRows, kTok>(a, m.red, pair, pairs, kThreads);
+    const Ws ws = ws_of(a, pairs, V);
+    if (lead && threadIdx.x == 0) ws.rec[4 * pair + 2] = 0;
+    tc::fence_before();
+    __syncthreads();
+    cluster_sync();  // both CTAs' barriers are set up
+    tc::fence_after();
+    const uint32_t tmem = m.tmem;
+
+    bool dead = false;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {  // by whole warps
+        bool ok = dead;
+        for (uint32_t i = 0; i < kWaitLimit && !ok; ++i) {
+            ok = try_wait_cluster(bar, parity);
+            if ((i & 255u) == 255u && *(volatile int *)&m.dead) break;
+        }
+        if (__any_sync(0xffffffffu, !ok)) {
+            dead = true;
+            *(volatile int *)&m.dead = 1;
+            flag_error(a.err, PKV_DEVERR_TIMEOUT);
+        }
+    };
+
+    // lane l: the cache row of group l & 15 of tile t + (l >> 4) of a piece; -1: a bad block; -2: no token
+    auto look = [&](const Piece &pc, int t) {
+        const int tok = pc.t0 + t * kTok + 8 * lane;
+        if (t + (lane >> 4) >= pc.tiles || tok >= pc.end) return -2;
+        const int blk = __ldg(a.tables + (int64_t)pc.seq * a.maxb + (tok >> a.bshift));
+        return (unsigned)blk < (unsigned)a.NB ? (blk << a.bshift) + (tok & (a.B - 1)) : -1;
+    };
+    const int none = a.NB << a.bshift;  // where a group without tokens starts: past the tensor's end, zeros
+
+    if (warp == 0) {
+        // ======================= producer of pieces, Q and the rows by tokens =======================
+        int tile = 0, np = 0, nq = 0, nk = 0;  // tiles, pieces, queries and parts issued
+        for (;;) {
+            const int d = np % kDescs;
+            wait(&m.desc_empty[d], (uint32_t)(np / kDescs + 1) & 1u);
+            Piece pc;
+            int shares;
+            const bool more = !dead && sh.take(a, pair, pc, shares);
+            if (!more) pc.tiles = 0;
+            if (lane == 0) {
+                m.piece[d] = pc;
+                mbar_arrive(&m.desc_full[d]);
+                if (lead && more && shares) ws.rec[4 * pair] = pc.row0, ws.rec[4 * pair + 1] = pc.rows, ws.rec[4 * pair + 2] = shares;
+            }
+            __syncwarp();
+            if (!more) break;
+            int row = look(pc, 0), next = -2;
+            wait(&m.q_empty, (uint32_t)(np + 1) & 1u);
+            ++np;
+            if (dead) continue;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&m.q_full, (uint32_t)X::kQ);
+                tma_load_3d(smem_u32(smem + X::q), &tm_q, smem_u32(&m.q_full), 0, pc.row0 + 64 * (int)rank, 0);
+            }
+            ++nq;
+            __syncwarp();
+            for (int t = 0; t < pc.tiles && !dead; ++t, ++tile) {
+                if ((t & 1) == 0) {
+                    if (t) row = next;
+                    next = look(pc, t + 2);
+                }
+                const bool turn = (lane >> 4) == (t & 1);
+                const bool mine = turn && ((lane >> 3) & 1) == (int)rank;  // groups of this CTA's 64 tokens
+                const uint32_t ok = __ballot_sync(0xffffffffu, row >= 0) >> (16 * (t & 1)) & 0xffffu;
+                if (turn && row == -1 && lead) flag_error(a.err, PKV_DEVERR_BLOCK_ID);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    wait(&m.k_empty[h], (uint32_t)(tile + 1) & 1u);
+                    if (dead) break;
+                    if (lane == 0) {
+                        if (h == 0) {
+                            m.groups[tile & 3] = ok;
+                            mbar_arrive(&m.meta[tile & 3]);
+                        }
+                        mbar_arrive_expect_tx(&m.k_full[h], (uint32_t)(64 * 128 * (h ? X::kChunks - X::kPart0 : X::kPart0)));
+                    }
+                    __syncwarp();
+                    if (mine)
+                        tma_load_3d(smem_u32(smem + X::k) + (uint32_t)((lane & 7) * X::kGroupK + h * X::kPart0 * 1024), h ? &tm_k1 : &tm_k0,
+                                    smem_u32(&m.k_full[h]), 0, row >= 0 ? row : none, h * X::kPart0);
+                    ++nk;
+                }
+            }
+        }
+        // no copy outlives the CTA, whoever else gave up
+        for (int i = max(0, nk - 2); i < nk; ++i) mbar_wait_bounded(&m.k_full[i & 1], (uint32_t)(i >> 1) & 1u);
+        if (nq > 0) mbar_wait_bounded(&m.q_full, (uint32_t)(nq - 1) & 1u);
+    } else if (warp == 7) {
+        // ======================= producer of the rows by entries =======================
+        int tile = 0, nv = 0;
+        for (int np = 0;; ++np) {
+            const int d = np % kDescs;
+            wait(&m.desc_full[d], (uint32_t)(np / kDescs) & 1u);
+            if (dead) break;
+            const Piece pc = m.piece[d];
+            if (pc.tiles == 0) break;
+            int row = look(pc, 0), next = -2;
+            for (int t = 0; t < pc.tiles && !dead; ++t, ++tile) {
+                if ((t & 1) == 0) {
+                    if (t) row = next;
+                    next = look(pc, t + 2);
+                }
+                const bool turn = (lane >> 4) == (t & 1);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    wait(&m.v_empty[h], (uint32_t)(tile + 1) & 1u);
+                    if (dead) break;
+                    if (lane == 0) mbar_arrive_expect_tx(&m.v_full[h], (uint32_t)(X::kV / 2));
+                    __syncwarp();
+                    if (turn && ((lane >> 3) & 1) == h)
+                        tma_load_3d(smem_u32(smem + X::v) + (uint32_t)((lane & 15) * X::kGroupV), &tm_v, smem_u32(&m.v_full[h]), 0,
+                                    row >= 0 ? row : none, (int)rank * (V / 128));
+                    ++nv;
+                }
+            }
+            if (dead) break;
+            if (lane == 0) mbar_arrive(&m.desc_empty[d]);
+        }
+        for (int i = max(0, nv - 2); i < nv; ++i) mbar_wait_bounded(&m.v_full[i & 1], (uint32_t)(i >> 1) & 1u);
+    } else if (warp <= 2 && !lead) {
+        // ======================= the other CTA: reports its loads (warp 1: Q, rows by tokens; 2: by entries) =======================
+        uint64_t *full = warp == 1 ? m.k_full : m.v_full;
+        const uint32_t q_peer = at_rank(&m.q_peer, 0), peer = at_rank(warp == 1 ? m.k_peer : m.v_peer, 0);
+        for (int np = 0, tile = 0;; ++np) {
+            const int d = np % kDescs;
+            wait(&m.desc_full[d], (uint32_t)(np / kDescs) & 1u);
+            const int n = dead ? 0 : m.piece[d].tiles;
+            if (n == 0) break;
+            if (warp == 1) {
+                wait(&m.q_full, (uint32_t)np & 1u);
+                if (dead) break;
+                if (lane == 0) arrive_at(q_peer);
+            }
+            for (int t = 0; t < n && !dead; ++t, ++tile)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    wait(&full[h], (uint32_t)tile & 1u);
+                    if (!dead && lane == 0) arrive_at(peer + 8 * h);
+                }
+            if (dead) break;
+            if (lane == 0) mbar_arrive(&m.desc_empty[d]);
+        }
+    } else if (warp == 1) {
+        // ======================= the leader: issuer of S = Q C^T =======================
+        constexpr uint32_t id = idesc(128, kTok, false, false);
+        const bool leader = elect_one();
+        const uint64_t qd = tc::smem_desc(smem_u32(smem + X::q), 16, 1024);
+        const uint64_t kd = tc::smem_desc(smem_u32(smem + X::k), 16, X::kGroupK);
+        for (int np = 0, tile = 0;; ++np) {
+            const int d = np % kDescs;
+            wait(&m.desc_full[d], (uint32_t)(np / kDescs) & 1u);
+            const int n = dead ? 0 : m.piece[d].tiles;
+            if (n == 0) break;
+            wait(&m.q_full, (uint32_t)np & 1u);
+            wait(&m.q_peer, (uint32_t)np & 1u);
+            for (int t = 0; t < n; ++t, ++tile) {
+                const uint32_t s = tmem + X::kS + (uint32_t)((tile & 1) * 64);
+                wait(&m.s_free[tile & 1], (uint32_t)((tile >> 1) + 1) & 1u);
+                wait(&m.k_full[0], (uint32_t)tile & 1u);
+                wait(&m.k_peer[0], (uint32_t)tile & 1u);
+                if (dead) break;
+                tc::fence_after();
+                if (leader) {
+#pragma unroll
+                    for (int c = 0; c < X::kPart0; ++c)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma2(s, qd + (uint64_t)((c * 8192 + k * 32) >> 4), kd + (uint64_t)((c * 1024 + k * 32) >> 4), id, c + k > 0 ? 1u : 0u);
+                    commit_both(&m.k_empty[0]);
+                }
+                __syncwarp();
+                wait(&m.k_full[1], (uint32_t)tile & 1u);
+                wait(&m.k_peer[1], (uint32_t)tile & 1u);
+                if (dead) break;
+                tc::fence_after();
+                if (leader) {
+#pragma unroll
+                    for (int c = X::kPart0; c < X::kChunks; ++c)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma2(s, qd + (uint64_t)((c * 8192 + k * 32) >> 4), kd + (uint64_t)((c * 1024 + k * 32) >> 4), id, 1u);
+                    commit_both(&m.k_empty[1]);
+                    commit_both(&m.s_full[tile & 1]);
+                    if (t + 1 == n) commit_both(&m.q_empty);
+                }
+                __syncwarp();
+            }
+            if (dead) break;
+            if (lane == 0) mbar_arrive(&m.desc_empty[d]);
+        }
+        if (leader) commit_both(&m.fin[0]);
+        __syncwarp();
+    } else if (warp == 2) {
+        // ======================= the leader: issuer of O += P L =======================
+        constexpr uint32_t id = idesc(128, 256, false, true);
+        const bool leader = elect_one();
+        const uint64_t pd = tc::smem_desc(smem_u32(smem + X::p), 16, 1024);
+        const uint64_t vd = tc::smem_desc(smem_u32(smem + X::v), 1024, X::kGroupV);
+        for (int np = 0, tile = 0;; ++np) {
+            const int d = np % kDescs;
+            wait(&m.desc_full[d], (uint32_t)(np / kDescs) & 1u);
+            const int n = dead ? 0 : m.piece[d].tiles;
+            if (n == 0) break;
+            if (np > 0) wait(&m.o_free, (uint32_t)(np - 1) & 1u);
+            for (int t = 0; t < n; ++t, ++tile) {
+                wait(&m.p_full, (uint32_t)tile & 1u);
+                auto half = [&](int h) {  // 4 steps of 16 tokens
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int b = 0; b < X::kBlocks; ++b)
+                            mma2(tmem + (uint32_t)(b * 128), pd + (uint64_t)((h * 8192 + k * 32) >> 4),
+                                 vd + (uint64_t)((b * 2048 + (4 * h + k) * 2 * X::kGroupV) >> 4), id, t == 0 && h + k == 0 ? 0u : 1u);
+                };
+                wait(&m.v_full[0], (uint32_t)tile & 1u);
+                wait(&m.v_peer[0], (uint32_t)tile & 1u);
+                if (dead) break;
+                tc::fence_after();
+                if (leader) {
+                    half(0);
+                    commit_both(&m.v_empty[0]);
+                }
+                __syncwarp();
+                wait(&m.v_full[1], (uint32_t)tile & 1u);
+                wait(&m.v_peer[1], (uint32_t)tile & 1u);
+                if (dead) break;
+                tc::fence_after();
+                if (leader) {
+                    half(1);
+                    commit_both(&m.v_empty[1]);
+                    commit_both(&m.pv_done);
+                }
+                __syncwarp();
+            }
+            if (dead) break;
+            if (lane == 0) mbar_arrive(&m.desc_empty[d]);
+        }
+        if (leader) commit_both(&m.fin[1]);
+        __syncwarp();
+    } else if (warp >= 3 && warp <= 6) {
+        // ======================= softmax and epilogue =======================
+        const int qt = warp & 3;  // quarter of the tensor memory's lanes
+        const int row = (qt & 1) * 32 + lane, half = qt >> 1, me = qt * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(qt * 32) << 16);
+        const float sc = a.scale_log2;
+        unsigned char *p_row = smem + X::p + half * 8192 + row * 128;
+        const uint32_t p_full = at_rank(&m.p_full, 0), o_free = at_rank(&m.o_free, 0);
+        const uint32_t s_free[2] = {at_rank(&m.s_free[0], 0), at_rank(&m.s_free[1], 0)};
+        const uint32_t bad_there = at_rank(&m.bad_there[0][0], rank ^ 1u);
+        const uint32_t bad_full[2] = {at_rank(&m.bad_full[0], rank ^ 1u), at_rank(&m.bad_full[1], rank ^ 1u)};
+        int tile = 0, nbad = 0;
+        bool stop = false;  // the four warps leave together: they share a barrier
+        for (int np = 0;; ++np) {
+            const int d = np % kDescs;
+            wait(&m.desc_full[d], (uint32_t)(np / kDescs) & 1u);
+            if (softmax_any(dead)) break;
+            const Piece pc = m.piece[d];
+            if (pc.tiles == 0) break;
+            float nref = INFINITY, l = 0.f;  // minus the reference: +inf before the first score
+            const int r = 64 * (int)rank + row;
+            const int least = pc.lim0 + pc.qh0 / a.H;                     // tokens that the first row sees
+            const int lim = min(pc.end, pc.lim0 + (pc.qh0 + r) / a.H);    // that this row sees
+            for (int t = 0; t < pc.tiles; ++t, ++tile) {
+                wait(&m.meta[tile & 3], (uint32_t)(tile >> 2) & 1u);
+                wait(&m.s_full[tile & 1], (uint32_t)(tile >> 1) & 1u);
+                tc::fence_after();
+                uint32_t s[64];
+                {
+                    uint32_t (&lo)[32] = *reinterpret_cast<uint32_t (*)[32]>(s), (&hi)[32] = *reinterpret_cast<uint32_t (*)[32]>(s + 32);
+                    ld_32x32b(lanes + X::kS + (uint32_t)((tile & 1) * 64), lo);
+                    ld_32x32b(lanes + X::kS + (uint32_t)((tile & 1) * 64 + 32), hi);
+                }
+                tc::wait_ld();
+                const uint32_t groups = m.groups[tile & 3];
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_at(s_free[tile & 1]);
+                const int tb = pc.t0 + t * kTok;
+                const bool masked = tb + kTok > least || groups != 0xffffu;
+                uint64_t bad = 0;  // tokens of this half whose rows hold an infinity or NaN
+                float top = -INFINITY;
+                if (masked) {
+                    // such a row gives every query such a score: of all rows, in both CTAs, or it is a query's own
+                    uint32_t nf[2] = {0u, 0u};
+#pragma unroll
+                    for (int c = 0; c < 64; ++c)
+                        if ((s[c] & 0x7f800000u) == 0x7f800000u) nf[c >> 5] |= 1u << (c & 31);
+                    if (r >= pc.rows) nf[0] = nf[1] = 0xffffffffu;
+                    nf[0] = __reduce_and_sync(0xffffffffu, nf[0]);
+                    nf[1] = __reduce_and_sync(0xffffffffu, nf[1]);
+                    if (lane == 0) m.warp_bad[qt][0] = nf[0], m.warp_bad[qt][1] = nf[1];
+                    softmax_sync();
+                    if (warp == 3) {
+                        if (lane < 4) {
+                            const uint32_t x = m.warp_bad[lane & 2][lane & 1] & m.warp_bad[(lane & 2) + 1][lane & 1];
+                            m.bad_here[lane] = x;
+                            store_at(bad_there + 16 * (nbad & 1) + 4 * lane, x);
+                        }
+                        __syncwarp();
+                        if (lane == 0) {
+                            asm volatile("fence.acq_rel.cluster;" ::: "memory");
+                            arrive_at(bad_full[nbad & 1]);
+                        }
+                    }
+                    // (two sets: the other CTA may be one such tile ahead, no more)
+                    wait(&m.bad_full[nbad & 1], (uint32_t)(nbad >> 1) & 1u);
+                    softmax_sync();
+                    const uint32_t *here = m.bad_here + 2 * half, *there = m.bad_there[nbad & 1] + 2 * half;
+                    const uint32_t b0 = here[0] & there[0], b1 = here[1] & there[1];
+                    ++nbad;
+                    bad = (uint64_t)b0 | ((uint64_t)b1 << 32);
+                    const uint32_t g8 = (groups >> (8 * half)) & 0xffu;
+                    const int seen = lim - tb - 64 * half;  // tokens of this half that the row sees
+#pragma unroll
+                    for (int c = 0; c < 64; ++c) {
+                        const bool hide = c >= seen || !((g8 >> (c >> 3)) & 1u);
+                        const bool b = (c < 32 ? b0 >> c : b1 >> (c - 32)) & 1u;
+                        s[c] = hide ? __float_as_uint(sc < 0.f ? INFINITY : -INFINITY) : b ? 0x7fffffffu : s[c];
+                    }
+                }
+                // log2 of the weights against the reference (`blank`: against 0 where there is none yet)
+                auto against = [&](uint32_t x, float nr) {
+                    return masked && __uint_as_float(x) == (sc < 0.f ? INFINITY : -INFINITY) ? -INFINITY : fmaf(__uint_as_float(x), sc, nr);
+                };
+#pragma unroll
+                for (int c = 0; c < 64; c += 2) top = max3_nan(top, against(s[c], nref), against(s[c + 1], nref));
+                if (softmax_any(!(top <= kSlack) || dead)) {
+                    if (softmax_any(dead)) {
+                        stop = true;
+                        break;
+                    }
+                    // Some score passed its row's reference by far, or is the row's first: new references for such rows.
+                    // The others keep theirs, so no row's result depends on another's.
+                    const float nr = nref == INFINITY ? 0.f : nref;
+                    float y = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < 64; ++c) y = fmaxf(y, against(s[c], nr));
+                    m.red[me] = y;
+                    softmax_sync();
+                    y = fmaxf(y, m.red[me ^ 64]);
+                    softmax_sync();
+                    float f = 1.f;
+                    if (nref == INFINITY) {
+                        if (y > -INFINITY) nref = -y;
+                    } else if (y > kSlack) {
+                        nref -= y;
+                        f = exp2f(-y);
+                        l *= f;
+                    }
+                    if (t > 0) {
+                        wait(&m.pv_done, (uint32_t)(tile - 1) & 1u);  // O at rest
+                        tc::fence_after();
+                        if (__any_sync(0xffffffffu, f != 1.f)) {
+#pragma unroll 1
+                            for (int b = 0; b < V / 64; ++b) {
+                                uint32_t o[32];
+                                ld_32x32b(lanes + (uint32_t)(b * 32), o);
+                                tc::wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                st_32x32b(lanes + (uint32_t)(b * 32), o);
+                            }
+                            tc::wait_st();
+                        }
+                    }
+                }
+                const float nr = nref == INFINITY ? 0.f : nref;
+                uint32_t w[32];
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    w[c] = pack_bf16x2(ex2_approx(against(s[2 * c], nr)), ex2_approx(against(s[2 * c + 1], nr)));
+                    l += bf16x2_lo(w[c]) + bf16x2_hi(w[c]);
+                }
+                if (tile > 0) wait(&m.pv_done, (uint32_t)(tile - 1) & 1u);  // P is free
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    *reinterpret_cast<uint4 *>(p_row + ((c ^ (row & 7)) << 4)) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+                if (masked) {
+                    wait(&m.v_full[0], (uint32_t)tile & 1u);
+                    wait(&m.v_full[1], (uint32_t)tile & 1u);
+                    // A row that some query does not see must not reach it through 0 * inf: the latent part of bad rows
+                    // and of rows past the last token in sight is zeroed here, those that see a bad one get NaN.
+                    const int tk = 64 * half + (lane & 31) + 32 * (qt & 1);
+                    const int c = (lane & 31) + 32 * (qt & 1);
+                    const bool in = (groups >> (tk >> 3)) & 1u;
+                    if (((bad >> c) & 1u) || (in && tb + tk >= pc.end)) {
+                        unsigned char *g = smem + X::v + (tk >> 3) * X::kGroupV + (tk & 7) * 128;
+                        for (int e = 0; e < V / 128; ++e)
+                            for (int x = 0; x < 8; ++x) *reinterpret_cast<uint4 *>(g + e * 1024 + x * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                }
+                fence_proxy_async();
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_at(p_full);
+            }
+            if (stop) break;
+            softmax_sync();  // red has been read
+            m.red[me] = l;
+            softmax_sync();
+            const float sum = m.red[row] + m.red[row + 64];
+            const size_t slot = (2 * (size_t)pair + (pc.out == 1 ? 1 : 0)) * 2 + rank;
+            if (pc.out && half == 0) ws.ml[slot * 128 + row] = -nref, ws.ml[slot * 128 + 64 + row] = sum;
+            wait(&m.pv_done, (uint32_t)(tile - 1) & 1u);
+            if (softmax_any(dead)) break;
+            tc::fence_after();
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            // entries of column j of block b: half V / 2 + 128 b + j
+            __nv_bfloat16 *out = (__nv_bfloat16 *)a.out + ((int64_t)pc.row0 + r) * V + half * (V / 2);
+            float4 *po = reinterpret_cast<float4 *>(ws.o + slot * 64 * V) + me;
+#pragma unroll 1
+            for (int b = 0; b < V / 64; ++b) {
+                uint32_t o[32];
+                ld_32x32b(lanes + (uint32_t)(b * 32), o);
+                tc::wait_ld();
+                if (pc.out) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        po[(b * 8 + e) * 128] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                                            __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+                } else if (r < pc.rows) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        *reinterpret_cast<uint4 *>(out + b * 32 + e * 8) = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+                }
+            }
+            tc::fence_before();
+            softmax_sync();  // red is read by all before the next piece writes it
+            if (lane == 0) {
+                arrive_at(o_free);
+                mbar_arrive(&m.desc_empty[d]);
+            }
+        }
+    }
+    __syncwarp();
+    if (warp == 1) {  // every product has ended before the memory goes
+        mbar_wait_bounded(&m.fin[0], 0);
+        mbar_wait_bounded(&m.fin[1], 0);
+    }
+    tc::fence_before();
+    __syncthreads();
+    cluster_sync();  // nothing arrives at a CTA that is gone
+    if (warp == 1) {
+        tc::fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(X::kCols) : "memory");
+    }
+}
+
+// Joins the pieces of cut contexts: CTA (c, y) the one that begins in share c, 16 entries of the 64 rows of one
+// CTA (each half's), a thread 16 entries of one row.
+template <int V>
+__global__ void __launch_bounds__(128) latent_pair_join_kernel(const __grid_constant__ Args a, int shares) {
+    grid_dependency_wait();
+    // queries that see nothing, but for those in a row tile with others
+    for (int s = blockIdx.y * gridDim.x + blockIdx.x; s < a.S; s += gridDim.x * gridDim.y) {
+        Walk<kRows, kTok> w;
+        w.open(a, s);
+        const int64_t vecs = min((int64_t)w.k0 * kRows, (int64_t)w.nH) * (V / 8);
+        uint4 *o = reinterpret_cast<uint4 *>((__nv_bfloat16 *)a.out + (int64_t)w.q0 * a.H * V);
+        for (int64_t i = threadIdx.x; i < vecs; i += 128) o[i] = make_uint4(0, 0, 0, 0);
+    }
+    const Ws ws = ws_of(a, shares, V);
+    const int c = blockIdx.x, n = ws.rec[4 * c + 2];
+    if (n == 0) return;
+    const int rank = blockIdx.y & 1, at = blockIdx.y >> 1;
+    const int row = threadIdx.x & 63, half = threadIdx.x >> 6, r = 64 * rank + row;
+    if (r >= ws.rec[4 * c + 1]) return;
+    auto slot_of = [&](int k) { return (size_t)(k ? 2 * (c + k) : 2 * c + 1) * 2 + rank; };
+    float ref = -INFINITY, sum = 0.f, o[16] = {};
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) ref = fmaxf(ref, ws.ml[slot_of(k) * 128 + row]);
+    if (ref == -INFINITY) ref = 0.f;
+#pragma unroll 2
+    for (int k = 0; k < n; ++k) {
+        const size_t slot = slot_of(k);
+        const float f = exp2f(ws.ml[slot * 128 + row] - ref);
+        sum += ws.ml[slot * 128 + 64 + row] * f;
+        const float4 *po = reinterpret_cast<const float4 *>(ws.o + slot * 64 * V) + at * 4 * 128 + threadIdx.x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float4 y = po[e * 128];
+            o[4 * e] += y.x * f, o[4 * e + 1] += y.y * f, o[4 * e + 2] += y.z * f, o[4 * e + 3] += y.w * f;
+        }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    uint32_t w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
+    __nv_bfloat16 *out = (__nv_bfloat16 *)a.out + ((int64_t)ws.rec[4 * c] + r) * V + half * (V / 2) + at * 16;
+    *reinterpret_cast<uint4 *>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4 *>(out + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+template <int V>
+pkv_status launch(const Args &a, cudaStream_t st) {
+    using X = L<V>;
+    static bool done[128];
+    const int pairs = sm_count() / 2;
+    if (pairs == 0 || !ensure_smem(latent_pair_kernel<V>, X::total, done)) return PKV_ERR_CUDA;
+    CUtensorMap tm_q, tm_k0, tm_k1, tm_v;
+    const int64_t rows = (int64_t)a.NB * a.B;
+    if (!make_map(&tm_q, a.q, (int64_t)a.T * a.H, V, 64, X::kChunks) || !make_map(&tm_k0, a.cache, rows, V, 8, X::kPart0) ||
+        !make_map(&tm_k1, a.cache, rows, V, 8, X::kChunks - X::kPart0) || !make_map(&tm_v, a.cache, rows, V, 8, V / 128))
+        return PKV_ERR_CUDA;
+    const pkv_status rc = launch_pdl(latent_pair_kernel<V>, dim3((unsigned)(2 * pairs)), dim3(kThreads), (size_t)X::total, st, tm_q, tm_k0, tm_k1,
+                                     tm_v, a);
+    if (rc != PKV_OK) return rc;
+    return launch_pdl(latent_pair_join_kernel<V>, dim3((unsigned)pairs, V / 16), dim3(128), 0, st, a, pairs);
+}
+
+}  // namespace
+
+size_t pair_workspace(int V) {
+    const int sms = sm_count();
+    return round256(ws_bytes((sms > 0 ? sms : 160) / 2, V));
+}
+
+pkv_status run_pair(const Args &a, cudaStream_t st) { return a.V == 512 ? launch<512>(a, st) : launch<256>(a, st); }
+
+}  // namespace latent
+}  // namespace pkv

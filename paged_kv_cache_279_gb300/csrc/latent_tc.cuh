@@ -1,0 +1,284 @@
+// Shared by the tensor-core kernels of latent attention: tcgen05 pieces, the walk over
+// contexts in equal shares, and the location of a share's first tile.
+#pragma once
+
+#include "latent.cuh"
+#include "pkv_ptx.cuh"
+
+namespace pkv {
+namespace latent {
+
+constexpr int kDescs = 4;      // pieces in flight between the warps of a CTA
+constexpr int kHead = 2;       // tiles that a context's start and end are worth
+constexpr int kMinShare = 2;   // tiles of a share
+constexpr float kSlack = 8.f;  // log2 of how far a weight may pass 1 before its row's reference moves
+
+// kind::f16 instruction descriptor: bf16 operands, float32 accumulators.
+__host__ __device__ constexpr uint32_t idesc(int m, int n, bool a_mn, bool b_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
+           ((uint32_t)(m >> 4) << 24);
+}
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// Maximum of three that is NaN if one of them is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// Barrier of the softmax warps, alone and with a vote.
+constexpr int kSoftmax = 128;
+__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kSoftmax) : "memory"); }
+__device__ __forceinline__ bool softmax_any(bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)x), "n"(kSoftmax)
+        : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
+__device__ __forceinline__ void ld_16x256b(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+
+__device__ __forceinline__ void ld_16x256b(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr));
+}
+
+__device__ __forceinline__ void ld_16x256b(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "r"(taddr));
+}
+
+__device__ __forceinline__ void ld_32x32b(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr));
+}
+
+__device__ __forceinline__ void ld_32x32b(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "r"(taddr));
+}
+
+__device__ __forceinline__ void st_32x32b(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
+}
+
+__device__ __forceinline__ void st_32x32b(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]) : "memory");
+}
+
+// One share's part of a context.
+struct Piece {
+    int tiles;     // 0: no more pieces
+    int t0, end;   // first token of the first tile; tokens that some row of the row tile sees
+    int row0, rows;
+    int lim0;      // tokens that row r sees: lim0 + (qh0 + r) / H
+    int qh0;
+    int seq;
+    int out;       // 0: the whole context; 1: its first tiles; 2: later ones
+};
+
+// The walk over contexts (sequence, row tile): row tile k of a sequence is rows
+// [k N, k N + N) of its n H query rows.  Its last row's query sees
+//     p0 + 1 + floor(min(k N + N - 1, n H - 1) / H)  tokens, p0 = L - n0 the first query's position,
+// A context counts kHead tiles more than it has, at its start: what its queries' load and the
+// storing of its output take.  Its tiles are, but for the last row tile, floor((k + c) / m) with m = TOK H / N and
+// c = floor((N - 1 + H (p0 + TOK)) / N): sums over k have a closed form.
+template <int N, int TOK>
+struct Walk {
+    int s, k, R;           // sequence, row tile, row tiles of the sequence
+    int L, q0, nH, p0, k0; // k0: first row tile with a query that sees a token
+    bool flagged;
+    __device__ __forceinline__ void open(const Args &a, int seq) {
+        s = seq;
+        const Seq q = sequence(a, seq);
+        flagged = q.flagged;
+        L = q.L, q0 = q.q0, nH = q.n * a.H, p0 = q.L - q.n0;
+        R = (nH + N - 1) / N;
+        const int blind = max(0, min(q.n, -p0));  // queries in front of the context
+        k0 = L == 0 ? R : (int)((int64_t)blind * a.H / N);
+        if (blind == q.n) k0 = R;
+        k = k0;
+    }
+    __device__ __forceinline__ int end(const Args &a, int kk) const {  // tokens row tile kk sees
+        if (!a.q_starts) return L;
+        const int last = min((kk + 1) * N, nH) - 1;
+        return min(L, p0 + 1 + last / a.H);
+    }
+    __device__ __forceinline__ int tiles(const Args &a, int kk) const { return (end(a, kk) + TOK - 1) / TOK; }
+    // tiles, heads included, of row tiles k0 .. kk - 1, kk < R
+    __device__ __forceinline__ int64_t before(const Args &a, int kk) const {
+        if (kk <= k0) return 0;
+        const int64_t m = (int64_t)TOK / N * a.H;  // N divides TOK
+        const int64_t c = (N - 1 + (int64_t)a.H * (p0 + TOK)) >> (N == 16 ? 4 : N == 32 ? 5 : N == 64 ? 6 : 7);  // floor: p0 may be below -TOK
+        return G(kk + c, m) - G(k0 + c, m) + (int64_t)kHead * (kk - k0);
+    }
+    static __device__ __forceinline__ int64_t G(int64_t x, int64_t m) {  // sum of floor(j / m), j < x
+        const int64_t q = x / m;
+        return m * (q * (q - 1) / 2) + q * (x - q * m);
+    }
+    __device__ __forceinline__ int64_t total(const Args &a) const {
+        if (k0 >= R) return 0;
+        if (!a.q_starts) return (int64_t)R * (tiles(a, 0) + kHead);  // one query: every row tile sees all
+        return before(a, R - 1) + tiles(a, R - 1) + kHead;
+    }
+};
+
+// A CTA's (or CTA pair's) share of all contexts' tiles laid end to end, heads included: `parts` equal shares at
+// most, this one from tile `off` of context (w.s, w.k) on, `left` tiles.
+template <int N, int TOK>
+struct Share {
+    Walk<N, TOK> w;
+    int64_t off, left, last, total;
+    int parts;
+    bool over;  // the context of w has been handed out
+
+    // The next piece of the share, false if there is none; `shares`: how many shares hold parts of a context that
+    // begins here and does not end here, else 0.
+    __device__ __forceinline__ bool take(const Args &a, int id, Piece &pc, int &shares) {
+        while (left > 0) {
+            if (over) {
+                if (++w.k >= w.R) do {
+                    if (w.s + 1 >= a.S) return false;  // lengths that changed under the call
+                    w.open(a, w.s + 1);
+                } while (w.k0 >= w.R);
+                off = 0;
+            }
+            over = true;
+            // of the context's kHead + nt tiles, `n` from `off` on are this share's
+            const int nt = w.tiles(a, w.k);
+            const int n = (int)min((int64_t)nt + kHead - off, left);
+            const int i0 = max(0, (int)off - kHead), i1 = max(0, (int)off + n - kHead);
+            left -= n;
+            if (i1 == i0) continue;
+            pc.tiles = i1 - i0;
+            pc.t0 = i0 * TOK;
+            pc.end = w.end(a, w.k);
+            pc.qh0 = w.k * N;
+            pc.row0 = w.q0 * a.H + pc.qh0;
+            pc.rows = min(N, w.nH - pc.qh0);
+            pc.lim0 = w.p0 + 1;
+            pc.seq = w.s;
+            pc.out = pc.tiles == nt ? 0 : i0 == 0 ? 1 : 2;
+            // (a context that begins here and is cut ends nt - i1 tiles after the share)
+            shares = pc.out == 1 ? (int)(share_owner(last + (nt - i1) - 1, total, parts) - id) + 1 : 0;
+            return true;
+        }
+        return false;
+    }
+};
+
+// Share `id` of at most `most`: each of the block's `threads` threads sums the tiles of a run of sequences, and
+// the one whose run holds the share's first tile finds it.  By the whole block; `scratch`: 1 KB of shared memory.
+template <int N, int TOK>
+__device__ __forceinline__ Share<N, TOK> locate(const Args &a, float *scratch, int id, int most, int threads) {
+    int64_t *scan = reinterpret_cast<int64_t *>(scratch);  // the warps' totals; then where the share begins
+    Walk<N, TOK> &begin = *reinterpret_cast<Walk<N, TOK> *>(scan + 18);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int run = (a.S + threads - 1) / threads;
+    const int sb = min(a.S, (int)threadIdx.x * run), se = min(a.S, sb + run);
+    int64_t mine = 0;
+    Share<N, TOK> r;
+    Walk<N, TOK> &w = r.w;
+    for (int s = sb; s < se; ++s) {
+        w.open(a, s);
+        mine += w.total(a);
+        if (w.flagged && s % most == id) flag_error(a.err, PKV_DEVERR_SEQ_LEN);
+    }
+    int64_t incl = mine;
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += y;
+    }
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    int64_t base = 0, total = 0;
+    for (int i = 0; i < threads / 32; ++i) {
+        if (i < warp) base += scan[i];
+        total += scan[i];
+    }
+    const int64_t excl = base + incl - mine;
+    int parts = total >= (int64_t)most * kMinShare ? most : (int)total / kMinShare;
+    if (parts < 1) parts = 1;
+    int64_t first = 0, last = 0;
+    if (id < parts && total < (1 << 24)) {  // 32-bit division is a fifth of the time (id < 256)
+        first = (uint32_t)id * (uint32_t)total / (uint32_t)parts;
+        last = (uint32_t)(id + 1) * (uint32_t)total / (uint32_t)parts;
+    } else if (id < parts) {
+        first = (int64_t)id * total / parts;
+        last = (int64_t)(id + 1) * total / parts;
+    }
+    if (first < last && first >= excl && first < excl + mine) {
+        int64_t off = first - excl;
+        for (int s = sb;; ++s) {
+            w.open(a, s);
+            const int64_t t = w.total(a);
+            if (off < t || s + 1 >= se) break;
+            off -= t;
+        }
+        if (!a.q_starts) {
+            const int per = w.tiles(a, 0) + kHead;
+            w.k = (int)off / per;
+            off -= (int64_t)w.k * per;
+        } else {
+            int lo = w.k0, hi = w.R;  // the last k with before(k) <= off
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (w.before(a, mid) <= off) lo = mid;
+                else hi = mid;
+            }
+            w.k = lo;
+            off -= w.before(a, lo);
+        }
+        begin = w;
+        scan[16] = off;
+    }
+    __syncthreads();
+    r.w = begin;
+    r.off = scan[16], r.left = last - first, r.last = last, r.total = total, r.parts = parts, r.over = false;
+    __syncthreads();  // the scratch memory is free
+    return r;
+}
+
+// The block tables, read later one entry after another, on their way into L2.
+__device__ __forceinline__ void prefetch_tables(const Args &a, int64_t line) {
+    if ((int64_t)a.S * a.maxb <= 1 << 17 && line * 32 < (int64_t)a.S * a.maxb)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.tables + line * 32));
+}
+
+// Rows of V + 64 entries as [chunk of 64 entries][row][64]: a box of `box` rows and `deep` chunks.
+inline bool make_map(CUtensorMap *map, const void *base, int64_t rows, int V, int box, int deep) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    const int chunks = V / 64 + 1;
+    cuuint64_t dims[3] = {64u, (cuuint64_t)rows, (cuuint64_t)chunks};
+    cuuint64_t strides[2] = {(cuuint64_t)(V + kRope) * 2, 128u};
+    cuuint32_t boxd[3] = {64u, (cuuint32_t)box, (cuuint32_t)deep};
+    cuuint32_t estr[3] = {1u, 1u, 1u};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, boxd, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace latent
+}  // namespace pkv

@@ -159,6 +159,8 @@ def test_python_refusals():
     with pytest.raises(ValueError):
         pkv.latent_cache_write(torch.zeros(4, 256), x[:, 0, :64], cache, slots, pos, f)
     with pytest.raises(TypeError):
+        pkv.latent_cache_write(torch.zeros(4, 512), x[:, 0, :64], cache, slots, pos, f[:32])
+    with pytest.raises(ValueError):
         pkv.latent_cache_write(torch.zeros(4, 512), x[:, 0, :64], cache, slots, pos, f)
     q, out = torch.zeros(2, 16, 576), torch.zeros(2, 16, 512)
     tables, lens = torch.zeros(2, 1, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
