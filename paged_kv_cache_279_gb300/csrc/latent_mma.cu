@@ -345,7 +345,7 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         for (int np = 0;; ++np) {
             const int d = np % kDescs;
             wait(&m.desc_full[d], (uint32_t)(np / kDescs) & 1u);
-            if (softmax_any(dead)) break;
+            if (softmax_any<128>(dead)) break;
             const Piece pc = m.piece[d];
             if (pc.tiles == 0) break;
             float nref[J][2], l[J][2];  // minus the reference: +inf before the first score
@@ -385,15 +385,15 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                         }
                     // A row of the cache that holds an infinity or NaN gives every query such a score.  It
                     // must not reach, through 0 * inf, the rows that do not see it: its latent part is
-                    // zeroed here, after its scores were taken, and those that see it get NaN.  So are rows
-                    // past the last token in sight, whatever they hold.
+                    // zeroed here, after its scores were taken, and those that see it get NaN.  (So are rows past
+                    // the last token that hold one.)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         nf[h] &= __shfl_xor_sync(0xffffffffu, nf[h], 1);
                         nf[h] &= __shfl_xor_sync(0xffffffffu, nf[h], 2);
                         bad[h] = (nf[h] & 0x7f800000u) == 0x7f800000u;
                         const int tk = tok0 + 8 * h;
-                        if (bad[h] || (in[h] && tb + tk >= pc.end)) {
+                        if (bad[h]) {
                             unsigned char *g = smem + X::ring + st * X::kTile + (tk >> 3) * X::kGroup + (tk & 7) * 128;
                             for (int c = lane & 3; c < V / 64; c += 4)
                                 for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4 *>(g + c * 1024 + e * 16) = make_uint4(0, 0, 0, 0);
@@ -425,8 +425,8 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 };
                 const float top = weigh(INFINITY);
                 if (tile > 0) wait(&m.pv_done, (uint32_t)(tile - 1) & 1u);  // P is free, and O at rest
-                if (softmax_any(!(top <= kSlack) || dead)) {
-                    if (softmax_any(dead)) {
+                if (softmax_any<128>(!(top <= kSlack) || dead)) {
+                    if (softmax_any<128>(dead)) {
                         stop = true;
                         break;
                     }
@@ -443,7 +443,7 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                             y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
                             if (lane < 4) m.red[qt][8 * j + col + i] = y;
                         }
-                    softmax_sync();
+                    softmax_sync<128>();
                     float f[J][2];
 #pragma unroll
                     for (int j = 0; j < J; ++j)
@@ -460,12 +460,12 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                                 l[j][i] *= f[j][i];
                             }
                         }
-                    softmax_sync();
+                    softmax_sync<128>();
                     if (t > 0) {  // O^T has something: scale its columns
                         if (qt == 0 && lane < 4)
 #pragma unroll
                             for (int j = 0; j < J; ++j) m.red[0][8 * j + col] = f[j][0], m.red[0][8 * j + col + 1] = f[j][1];
-                        softmax_sync();
+                        softmax_sync<128>();
                         tc::fence_after();
                         constexpr int W = N < 32 ? 16 : 32;
 #pragma unroll 1
@@ -502,7 +502,7 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 if (lane == 0) mbar_arrive(&m.p_full);
             }
             if (stop) break;
-            softmax_sync();  // red has been read
+            softmax_sync<128>();  // red has been read
             // sums of weights over the tokens; then O^T, row by row
 #pragma unroll
             for (int j = 0; j < J; ++j)
@@ -514,7 +514,7 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     l[j][i] = y + __shfl_xor_sync(0xffffffffu, y, 16);
                     if (lane < 4) m.red[qt][8 * j + col + i] = l[j][i];
                 }
-            softmax_sync();
+            softmax_sync<128>();
             float sum[J][2];
 #pragma unroll
             for (int j = 0; j < J; ++j)
@@ -533,7 +533,7 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                         ws.ml[slot * 2 * N + N + 8 * j + col + i] = sum[j][i];
                     }
             wait(&m.pv_done, (uint32_t)(tile - 1) & 1u);
-            if (softmax_any(dead)) break;
+            if (softmax_any<128>(dead)) break;
             tc::fence_after();
             // O^T, 16 entries at a time; P's memory is free for the transposition
             const uint32_t stage = smem_u32(smem + X::p) + (uint32_t)(qt * N * 32);
@@ -567,7 +567,7 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 put(u + 1, r1);
             }
             tc::fence_before();
-            softmax_sync();  // red is read by all before the next piece writes it
+            softmax_sync<128>();  // red is read by all before the next piece writes it
             if (lane == 0) {
                 mbar_arrive(&m.o_free);
                 mbar_arrive(&m.desc_empty[d]);

@@ -16,7 +16,8 @@
 // The leader's (rank 0's) warps issue all products.  What the other CTA has ready it reports to the leader's
 // barriers; what the products have done arrives at both CTAs' barriers.
 //
-// Softmax: a thread has one row and half of the tile's tokens; its pair is 64 threads on.  References, weights,
+// Softmax: a thread has one row and a quarter of the tile's tokens (eight warps: with four, whose exponentials alone
+// take 512 cycles of each scheduler, a tile took 3300 cycles, not 2200).  References, weights,
 // hidden rows, shares and joins as in the transposed kernel.
 #include "latent_tc.cuh"
 
@@ -26,7 +27,8 @@ namespace latent {
 namespace {
 
 constexpr int kRows = 128, kTok = 128;
-constexpr int kThreads = 256;  // two producers, a warp for each product (the other CTA's reports loads), four softmax warps
+constexpr int kSoftmax = 256;             // threads of the eight softmax warps
+constexpr int kThreads = 128 + kSoftmax;  // two producers, a warp for each product (the other CTA's report loads)
 
 template <int V>
 struct L {
@@ -46,12 +48,11 @@ struct L {
 
 struct alignas(8) Misc {
     uint64_t k_full[2], k_peer[2], k_empty[2], v_full[2], v_peer[2], v_empty[2], q_full, q_peer, q_empty, s_full[2], s_free[2], p_full, pv_done, o_free;
-    uint64_t meta[4], desc_full[kDescs], desc_empty[kDescs], fin[2], bad_full[2];
+    uint64_t meta[4], desc_full[kDescs], desc_empty[kDescs], fin[2];
     Piece piece[kDescs];
-    float red[256];
+    float red[4][64];
     uint32_t groups[4];   // valid 8-token groups of a tile
     uint32_t warp_bad[4][2];
-    uint32_t bad_here[4], bad_there[2][4];
     uint32_t tmem;
     int dead;
 };
@@ -82,22 +83,10 @@ __device__ __forceinline__ uint32_t at_rank(const void *p, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
     return r;
 }
+// (What these arrivals announce is read by the tensor cores, or has been read from tensor memory: the proxy and
+// tcgen05 fences before them order that.  A release at cluster scope would cost a memory barrier, some 1500 cycles.)
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void store_at(uint32_t addr, uint32_t x) {
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
-}
-__device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -132,13 +121,13 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         for (int i = 0; i < 2; ++i) {
             mbar_init(&m.k_full[i], 1), mbar_init(&m.k_peer[i], 1), mbar_init(&m.k_empty[i], 1);
             mbar_init(&m.v_full[i], 1), mbar_init(&m.v_peer[i], 1), mbar_init(&m.v_empty[i], 1);
-            mbar_init(&m.s_full[i], 1), mbar_init(&m.s_free[i], 8);
-            mbar_init(&m.fin[i], 1), mbar_init(&m.bad_full[i], 1);
+            mbar_init(&m.s_full[i], 1), mbar_init(&m.s_free[i], 16);
+            mbar_init(&m.fin[i], 1);
         }
         mbar_init(&m.q_full, 1), mbar_init(&m.q_peer, 1), mbar_init(&m.q_empty, 1);
-        mbar_init(&m.p_full, 8), mbar_init(&m.pv_done, 1), mbar_init(&m.o_free, 8);
+        mbar_init(&m.p_full, 16), mbar_init(&m.pv_done, 1), mbar_init(&m.o_free, 16);
         for (int i = 0; i < 4; ++i) mbar_init(&m.meta[i], 1);
-        for (int i = 0; i < kDescs; ++i) mbar_init(&m.desc_full[i], 1), mbar_init(&m.desc_empty[i], 7);
+        for (int i = 0; i < kDescs; ++i) mbar_init(&m.desc_full[i], 1), mbar_init(&m.desc_empty[i], 11);
         m.dead = 0;
         fence_barrier_init();
     }
@@ -150,7 +139,7 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     grid_dependency_wait();
     grid_launch_dependents();  // the join kernel; it waits for this one before it reads
     prefetch_tables(a, (int64_t)blockIdx.x * kThreads + threadIdx.x);
-    Share<kRows, kTok> sh = locate<kRows, kTok>(a, m.red, pair, pairs, kThreads);
+    Share<kRows, kTok> sh = locate<kRows, kTok>(a, &m.red[0][0], pair, pairs, kThreads);
     const Ws ws = ws_of(a, pairs, V);
     if (lead && threadIdx.x == 0) ws.rec[4 * pair + 2] = 0;
     tc::fence_before();
@@ -163,7 +152,7 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     auto wait = [&](uint64_t *bar, uint32_t parity) {  // by whole warps
         bool ok = dead;
         for (uint32_t i = 0; i < kWaitLimit && !ok; ++i) {
-            ok = try_wait_cluster(bar, parity);
+            ok = mbar_try_wait(bar, parity);
             if ((i & 255u) == 255u && *(volatile int *)&m.dead) break;
         }
         if (__any_sync(0xffffffffu, !ok)) {
@@ -240,7 +229,7 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         // no copy outlives the CTA, whoever else gave up
         for (int i = max(0, nk - 2); i < nk; ++i) mbar_wait_bounded(&m.k_full[i & 1], (uint32_t)(i >> 1) & 1u);
         if (nq > 0) mbar_wait_bounded(&m.q_full, (uint32_t)(nq - 1) & 1u);
-    } else if (warp == 7) {
+    } else if (warp == 3) {
         // ======================= producer of the rows by entries =======================
         int tile = 0, nv = 0;
         for (int np = 0;; ++np) {
@@ -392,26 +381,27 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
         if (leader) commit_both(&m.fin[1]);
         __syncwarp();
-    } else if (warp >= 3 && warp <= 6) {
+    } else if (warp >= 4) {
         // ======================= softmax and epilogue =======================
         const int qt = warp & 3;  // quarter of the tensor memory's lanes
-        const int row = (qt & 1) * 32 + lane, half = qt >> 1, me = qt * 32 + lane;
+        const int row = (qt & 1) * 32 + lane, half = qt >> 1;  // of the CTA's rows; of the tile's tokens, and then
+        const int q2 = warp >> 2 & 1, me = 2 * half + q2;      // of that half's
         const uint32_t lanes = tmem + ((uint32_t)(qt * 32) << 16);
         const float sc = a.scale_log2;
         unsigned char *p_row = smem + X::p + half * 8192 + row * 128;
+        const int p_chunk = 4 * q2;
         const uint32_t p_full = at_rank(&m.p_full, 0), o_free = at_rank(&m.o_free, 0);
         const uint32_t s_free[2] = {at_rank(&m.s_free[0], 0), at_rank(&m.s_free[1], 0)};
-        const uint32_t bad_there = at_rank(&m.bad_there[0][0], rank ^ 1u);
-        const uint32_t bad_full[2] = {at_rank(&m.bad_full[0], rank ^ 1u), at_rank(&m.bad_full[1], rank ^ 1u)};
-        int tile = 0, nbad = 0;
+        int tile = 0;
         bool stop = false;  // the four warps leave together: they share a barrier
         for (int np = 0;; ++np) {
             const int d = np % kDescs;
             wait(&m.desc_full[d], (uint32_t)(np / kDescs) & 1u);
-            if (softmax_any(dead)) break;
+            if (softmax_any<kSoftmax>(dead)) break;
             const Piece pc = m.piece[d];
             if (pc.tiles == 0) break;
-            float nref = INFINITY, l = 0.f;  // minus the reference: +inf before the first score
+            float nref = INFINITY;       // minus the reference: +inf before the first score
+            uint64_t l2 = f32x2(0.f, 0.f);  // sums of the weights of even and odd tokens
             const int r = 64 * (int)rank + row;
             const int least = pc.lim0 + pc.qh0 / a.H;                     // tokens that the first row sees
             const int lim = min(pc.end, pc.lim0 + (pc.qh0 + r) / a.H);    // that this row sees
@@ -419,12 +409,8 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 wait(&m.meta[tile & 3], (uint32_t)(tile >> 2) & 1u);
                 wait(&m.s_full[tile & 1], (uint32_t)(tile >> 1) & 1u);
                 tc::fence_after();
-                uint32_t s[64];
-                {
-                    uint32_t (&lo)[32] = *reinterpret_cast<uint32_t (*)[32]>(s), (&hi)[32] = *reinterpret_cast<uint32_t (*)[32]>(s + 32);
-                    ld_32x32b(lanes + X::kS + (uint32_t)((tile & 1) * 64), lo);
-                    ld_32x32b(lanes + X::kS + (uint32_t)((tile & 1) * 64 + 32), hi);
-                }
+                uint32_t s[32];
+                ld_32x32b(lanes + X::kS + (uint32_t)((tile & 1) * 64 + 32 * q2), s);
                 tc::wait_ld();
                 const uint32_t groups = m.groups[tile & 3];
                 tc::fence_before();
@@ -432,82 +418,65 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (lane == 0) arrive_at(s_free[tile & 1]);
                 const int tb = pc.t0 + t * kTok;
                 const bool masked = tb + kTok > least || groups != 0xffffu;
-                uint64_t bad = 0;  // tokens of this half whose rows hold an infinity or NaN
-                float top = -INFINITY;
+                uint32_t nf = 0u, suspect = 0u;
                 if (masked) {
-                    // such a row gives every query such a score: of all rows, in both CTAs, or it is a query's own
-                    uint32_t nf[2] = {0u, 0u};
+                    // A row of the cache that holds an infinity or NaN gives every query such a score (and may not be the
+                    // only reason for one): the tokens that gave all of this CTA's rows one, a word of 32 tokens a warp.
 #pragma unroll
-                    for (int c = 0; c < 64; ++c)
-                        if ((s[c] & 0x7f800000u) == 0x7f800000u) nf[c >> 5] |= 1u << (c & 31);
-                    if (r >= pc.rows) nf[0] = nf[1] = 0xffffffffu;
-                    nf[0] = __reduce_and_sync(0xffffffffu, nf[0]);
-                    nf[1] = __reduce_and_sync(0xffffffffu, nf[1]);
-                    if (lane == 0) m.warp_bad[qt][0] = nf[0], m.warp_bad[qt][1] = nf[1];
-                    softmax_sync();
-                    if (warp == 3) {
-                        if (lane < 4) {
-                            const uint32_t x = m.warp_bad[lane & 2][lane & 1] & m.warp_bad[(lane & 2) + 1][lane & 1];
-                            m.bad_here[lane] = x;
-                            store_at(bad_there + 16 * (nbad & 1) + 4 * lane, x);
-                        }
-                        __syncwarp();
-                        if (lane == 0) {
-                            asm volatile("fence.acq_rel.cluster;" ::: "memory");
-                            arrive_at(bad_full[nbad & 1]);
-                        }
-                    }
-                    // (two sets: the other CTA may be one such tile ahead, no more)
-                    wait(&m.bad_full[nbad & 1], (uint32_t)(nbad >> 1) & 1u);
-                    softmax_sync();
-                    const uint32_t *here = m.bad_here + 2 * half, *there = m.bad_there[nbad & 1] + 2 * half;
-                    const uint32_t b0 = here[0] & there[0], b1 = here[1] & there[1];
-                    ++nbad;
-                    bad = (uint64_t)b0 | ((uint64_t)b1 << 32);
-                    const uint32_t g8 = (groups >> (8 * half)) & 0xffu;
-                    const int seen = lim - tb - 64 * half;  // tokens of this half that the row sees
+                    for (int c = 0; c < 32; ++c)
+                        if ((s[c] & 0x7f800000u) == 0x7f800000u) nf |= 1u << c;
+                    const uint32_t all = __reduce_and_sync(0xffffffffu, nf);
+                    if (lane == 0) m.warp_bad[qt][q2] = all;
+                    softmax_sync<kSoftmax>();
+                    suspect = m.warp_bad[2 * half][qt & 1] & m.warp_bad[2 * half + 1][qt & 1];  // tokens 64 half + 32 (qt & 1) ..
+                }
+                // log2 of the weights without the reference
+                float x[32];
 #pragma unroll
-                    for (int c = 0; c < 64; ++c) {
-                        const bool hide = c >= seen || !((g8 >> (c >> 3)) & 1u);
-                        const bool b = (c < 32 ? b0 >> c : b1 >> (c - 32)) & 1u;
-                        s[c] = hide ? __float_as_uint(sc < 0.f ? INFINITY : -INFINITY) : b ? 0x7fffffffu : s[c];
+                for (int c = 0; c < 32; c += 2)
+                    f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), f32x2(sc, sc), f32x2(0.f, 0.f)), x[c], x[c + 1]);
+                if (masked) {
+                    const uint32_t g8 = groups >> (8 * half + 4 * q2);
+                    const int seen = lim - tb - 64 * half - 32 * q2;  // of this thread's tokens the row sees so many
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        if ((nf >> c) & 1u) x[c] = __uint_as_float(0x7fffffffu);  // (-infinity too: 0 times an infinity)
+                        if (c >= seen || !((g8 >> (c >> 3)) & 1u)) x[c] = -INFINITY;
                     }
                 }
-                // log2 of the weights against the reference (`blank`: against 0 where there is none yet)
-                auto against = [&](uint32_t x, float nr) {
-                    return masked && __uint_as_float(x) == (sc < 0.f ? INFINITY : -INFINITY) ? -INFINITY : fmaf(__uint_as_float(x), sc, nr);
-                };
+                float top = -INFINITY;
 #pragma unroll
-                for (int c = 0; c < 64; c += 2) top = max3_nan(top, against(s[c], nref), against(s[c + 1], nref));
-                if (softmax_any(!(top <= kSlack) || dead)) {
-                    if (softmax_any(dead)) {
+                for (int c = 0; c < 32; c += 2) top = max3_nan(top, x[c], x[c + 1]);
+                const bool over = nref == INFINITY ? !(top == -INFINITY) : !(top + nref <= kSlack);
+                if (softmax_any<kSoftmax>(over || dead)) {
+                    if (softmax_any<kSoftmax>(dead)) {
                         stop = true;
                         break;
                     }
                     // Some score passed its row's reference by far, or is the row's first: new references for such rows.
                     // The others keep theirs, so no row's result depends on another's.
-                    const float nr = nref == INFINITY ? 0.f : nref;
                     float y = -INFINITY;
 #pragma unroll
-                    for (int c = 0; c < 64; ++c) y = fmaxf(y, against(s[c], nr));
-                    m.red[me] = y;
-                    softmax_sync();
-                    y = fmaxf(y, m.red[me ^ 64]);
-                    softmax_sync();
+                    for (int c = 0; c < 32; ++c) y = fmaxf(y, x[c]);
+                    if (nref != INFINITY) y += nref;
+                    m.red[me][row] = y;
+                    softmax_sync<kSoftmax>();
+                    y = fmaxf(fmaxf(m.red[0][row], m.red[1][row]), fmaxf(m.red[2][row], m.red[3][row]));
+                    softmax_sync<kSoftmax>();
                     float f = 1.f;
                     if (nref == INFINITY) {
                         if (y > -INFINITY) nref = -y;
                     } else if (y > kSlack) {
                         nref -= y;
                         f = exp2f(-y);
-                        l *= f;
+                        l2 = fma_f32x2(l2, f32x2(f, f), f32x2(0.f, 0.f));
                     }
                     if (t > 0) {
                         wait(&m.pv_done, (uint32_t)(tile - 1) & 1u);  // O at rest
                         tc::fence_after();
                         if (__any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll 1
-                            for (int b = 0; b < V / 64; ++b) {
+                            for (int b = q2 * (V / 128); b < (q2 + 1) * (V / 128); ++b) {
                                 uint32_t o[32];
                                 ld_32x32b(lanes + (uint32_t)(b * 32), o);
                                 tc::wait_ld();
@@ -520,29 +489,39 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     }
                 }
                 const float nr = nref == INFINITY ? 0.f : nref;
-                uint32_t w[32];
+                uint32_t w[16];
 #pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    w[c] = pack_bf16x2(ex2_approx(against(s[2 * c], nr)), ex2_approx(against(s[2 * c + 1], nr)));
-                    l += bf16x2_lo(w[c]) + bf16x2_hi(w[c]);
+                for (int c = 0; c < 16; ++c) {
+                    float lo, hi;
+                    f32x2_split(add_f32x2(f32x2(x[2 * c], x[2 * c + 1]), f32x2(nr, nr)), lo, hi);
+                    w[c] = pack_bf16x2(ex2_approx(lo), ex2_approx(hi));
+                    l2 = add_f32x2(l2, f32x2(bf16x2_lo(w[c]), bf16x2_hi(w[c])));
                 }
                 if (tile > 0) wait(&m.pv_done, (uint32_t)(tile - 1) & 1u);  // P is free
 #pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    *reinterpret_cast<uint4 *>(p_row + ((c ^ (row & 7)) << 4)) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-                if (masked) {
+                for (int c = 0; c < 4; ++c)
+                    *reinterpret_cast<uint4 *>(p_row + (((p_chunk + c) ^ (row & 7)) << 4)) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+                if (masked && q2 == 0 && suspect) {
+                    // Such a row must not reach, through 0 * infinity, the queries that do not see it, nor may what lies
+                    // behind the last token: where this CTA's half of its latent part holds one, that is zeroed.
                     wait(&m.v_full[0], (uint32_t)tile & 1u);
                     wait(&m.v_full[1], (uint32_t)tile & 1u);
-                    // A row that some query does not see must not reach it through 0 * inf: the latent part of bad rows
-                    // and of rows past the last token in sight is zeroed here, those that see a bad one get NaN.
-                    const int tk = 64 * half + (lane & 31) + 32 * (qt & 1);
-                    const int c = (lane & 31) + 32 * (qt & 1);
-                    const bool in = (groups >> (tk >> 3)) & 1u;
-                    if (((bad >> c) & 1u) || (in && tb + tk >= pc.end)) {
+                    const int tk = 64 * half + row;  // (as many tokens as rows)
+                    if ((suspect >> lane) & 1u) {
                         unsigned char *g = smem + X::v + (tk >> 3) * X::kGroupV + (tk & 7) * 128;
+                        bool found = false;
                         for (int e = 0; e < V / 128; ++e)
-                            for (int x = 0; x < 8; ++x) *reinterpret_cast<uint4 *>(g + e * 1024 + x * 16) = make_uint4(0, 0, 0, 0);
+                            for (int k = 0; k < 8; ++k) {
+                                const uint4 y = *reinterpret_cast<const uint4 *>(g + e * 1024 + k * 16);
+                                const uint32_t z[4] = {y.x, y.y, y.z, y.w};
+                                for (int i = 0; i < 4; ++i)
+                                    found = found || (z[i] & 0x7f80u) == 0x7f80u || (z[i] & 0x7f800000u) == 0x7f800000u;
+                            }
+                        if (found)
+                            for (int e = 0; e < V / 128; ++e)
+                                for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4 *>(g + e * 1024 + k * 16) = make_uint4(0, 0, 0, 0);
                     }
+                    __syncwarp();
                 }
                 fence_proxy_async();
                 tc::fence_before();
@@ -550,24 +529,23 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (lane == 0) arrive_at(p_full);
             }
             if (stop) break;
-            softmax_sync();  // red has been read
-            m.red[me] = l;
-            softmax_sync();
-            const float sum = m.red[row] + m.red[row + 64];
+            softmax_sync<kSoftmax>();  // red has been read
+            float l_even, l_odd;
+            f32x2_split(l2, l_even, l_odd);
+            m.red[me][row] = l_even + l_odd;
+            softmax_sync<kSoftmax>();
+            const float sum = (m.red[0][row] + m.red[1][row]) + (m.red[2][row] + m.red[3][row]);
             const size_t slot = (2 * (size_t)pair + (pc.out == 1 ? 1 : 0)) * 2 + rank;
-            if (pc.out && half == 0) ws.ml[slot * 128 + row] = -nref, ws.ml[slot * 128 + 64 + row] = sum;
+            if (pc.out && me == 0) ws.ml[slot * 128 + row] = -nref, ws.ml[slot * 128 + 64 + row] = sum;
             wait(&m.pv_done, (uint32_t)(tile - 1) & 1u);
-            if (softmax_any(dead)) break;
+            if (softmax_any<kSoftmax>(dead)) break;
             tc::fence_after();
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
             // entries of column j of block b: half V / 2 + 128 b + j
             __nv_bfloat16 *out = (__nv_bfloat16 *)a.out + ((int64_t)pc.row0 + r) * V + half * (V / 2);
-            float4 *po = reinterpret_cast<float4 *>(ws.o + slot * 64 * V) + me;
-#pragma unroll 1
-            for (int b = 0; b < V / 64; ++b) {
-                uint32_t o[32];
-                ld_32x32b(lanes + (uint32_t)(b * 32), o);
-                tc::wait_ld();
+            const bool sectors = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
+            float4 *po = reinterpret_cast<float4 *>(ws.o + slot * 64 * V) + qt * 32 + lane;
+            auto put = [&](int b, const uint32_t (&o)[32]) {
                 if (pc.out) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
@@ -577,13 +555,32 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     uint32_t w[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+                    if (sectors) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        *reinterpret_cast<uint4 *>(out + b * 32 + e * 8) = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+                        for (int e = 0; e < 16; e += 8)
+                            st_global_32B(out + b * 32 + 2 * e, w[e], w[e + 1], w[e + 2], w[e + 3], w[e + 4], w[e + 5], w[e + 6], w[e + 7]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4)
+                            *reinterpret_cast<uint4 *>(out + b * 32 + 2 * e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
+                    }
                 }
+            };
+            constexpr int kMine = V / 128;  // blocks of 32 columns
+            const uint32_t o_at = lanes + (uint32_t)(q2 * kMine * 32);
+            uint32_t o0[32], o1[32];  // one is loaded while the other is stored
+            ld_32x32b(o_at, o0);
+#pragma unroll 1
+            for (int b = 0; b < kMine; b += 2) {
+                tc::wait_ld();
+                ld_32x32b(o_at + (uint32_t)((b + 1) * 32), o1);
+                put(q2 * kMine + b, o0);
+                tc::wait_ld();
+                if (b + 2 < kMine) ld_32x32b(o_at + (uint32_t)((b + 2) * 32), o0);
+                put(q2 * kMine + b + 1, o1);
             }
             tc::fence_before();
-            softmax_sync();  // red is read by all before the next piece writes it
+            softmax_sync<kSoftmax>();  // red is read by all before the next piece writes it
             if (lane == 0) {
                 arrive_at(o_free);
                 mbar_arrive(&m.desc_empty[d]);

@@ -32,15 +32,18 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
     return d;
 }
 
-// Barrier of the softmax warps, alone and with a vote.
-constexpr int kSoftmax = 128;
-__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kSoftmax) : "memory"); }
+// Barrier of the softmax warps (their THREADS), alone and with a vote.
+template <int THREADS>
+__device__ __forceinline__ void softmax_sync() {
+    asm volatile("barrier.cta.sync 1, %0;" ::"n"(THREADS) : "memory");
+}
+template <int THREADS>
 __device__ __forceinline__ bool softmax_any(bool x) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"((uint32_t)x), "n"(kSoftmax)
+        : "r"((uint32_t)x), "n"(THREADS)
         : "memory");
     return r != 0;
 }
