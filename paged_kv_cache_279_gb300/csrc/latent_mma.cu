@@ -152,7 +152,7 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     prefetch_tables(a, (int64_t)cta * kThreads + threadIdx.x);
     Share<N, kTok> sh = locate<N, kTok>(a, &m.red[0][0], cta, G, kThreads);
     const Ws ws = ws_of(a, G, N, V);
-    if (threadIdx.x == 0) ws.rec[4 * cta + 2] = 0;
+    if (threadIdx.x == 0) leave(ws.rec + 4 * cta, 0, 0, 0);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
@@ -179,13 +179,11 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             const int d = np % kDescs;
             wait(&m.desc_empty[d], (uint32_t)(np / kDescs + 1) & 1u);
             Piece pc;
-            int shares;
-            const bool more = !dead && sh.take(a, cta, pc, shares);
+            const bool more = !dead && sh.take(a, pc);
             if (!more) pc.tiles = 0;
             if (lane == 0) {
                 m.piece[d] = pc;
                 mbar_arrive(&m.desc_full[d]);
-                if (more && shares) ws.rec[4 * cta] = pc.row0, ws.rec[4 * cta + 1] = pc.rows, ws.rec[4 * cta + 2] = shares;
             }
             __syncwarp();
             if (!more) break;
@@ -240,6 +238,7 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 ++halves;
                 if (X::kQBufs == 1 && t == 0) load_q();
             }
+            if (pc.out == 1 && lane == 0) leave(ws.rec + 4 * cta, pc.row0, pc.rows, sh.reach(cta));
             ++np;
         }
         // no copy outlives the CTA, whoever else gave up
@@ -582,65 +581,70 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     }
 }
 
-// Joins the pieces of cut contexts: CTA (c, y) the one that begins in share c, a warp 16 entries of 16
-// rows, in the layout the pieces were stored in.  Small units of work, and the loads of several pieces in
-// flight: a long context has one piece a share.
+// Joins the pieces of cut contexts: CTA (c, y) the one that begins in share c, a warp 16 entries of 16 rows, in the
+// layout the pieces were stored in.  Small units, all at once, and four pieces' loads in flight: what it waits for
+// is L2 (units taken in turn by fewer CTAs, a unit's pieces divided among four warps: 10 us more for 64 contexts).
 constexpr int kJoinWarps = 8;
 
 template <int V, int N>
 __global__ void __launch_bounds__(kJoinWarps * 32) latent_mma_join_kernel(const __grid_constant__ Args a, int shares) {
-    __shared__ __align__(128) unsigned char sh[kJoinWarps * 16 * 32];
+    __shared__ __align__(128) unsigned char stage[kJoinWarps * 16 * 32];
     grid_dependency_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // queries that see nothing, but for those in a row tile with others
-    for (int s = blockIdx.y * gridDim.x + blockIdx.x; s < a.S; s += gridDim.x * gridDim.y) {
-        Walk<N, kTok> w;
-        w.open(a, s);
-        const int64_t vecs = min((int64_t)w.k0 * N, (int64_t)w.nH) * (V / 8);
-        uint4 *o = reinterpret_cast<uint4 *>((__nv_bfloat16 *)a.out + (int64_t)w.q0 * a.H * V);
-        for (int64_t i = threadIdx.x; i < vecs; i += kJoinWarps * 32) o[i] = make_uint4(0, 0, 0, 0);
-    }
+    zero_blind<N, kTok>(a, blockIdx.y * gridDim.x + blockIdx.x, gridDim.x * gridDim.y, kJoinWarps * 32);
     const Ws ws = ws_of(a, shares, N, V);
-    const int c = blockIdx.x, n = ws.rec[4 * c + 2];
-    if (n == 0) return;
+    const int c = blockIdx.x;
+    const int4 rec = *reinterpret_cast<const int4 *>(ws.rec + 4 * c);
     constexpr int kRowUnits = N / 16;
     const int work = blockIdx.y * kJoinWarps + warp, unit = work / kRowUnits, r0 = work % kRowUnits * 16;
-    const int row0 = ws.rec[4 * c] + r0, rows = ws.rec[4 * c + 1] - r0;
-    if (rows <= 0) return;
+    const int n = rec.z, rows = rec.y - r0;
+    if (n == 0 || rows <= 0) return;
     const int col = r0 + 2 * (lane & 3);
-    auto ml_of = [&](int k, int j) { return ws.ml + (size_t)(k ? 2 * (c + k) : 2 * c + 1) * 2 * N + col + 8 * j; };
-    float ref[2][2], sum[2][2] = {}, o[8] = {};
+    float top[4], sum[4] = {}, o[8] = {};  // [2 j + i]: row col + 8 j + i
 #pragma unroll
-    for (int j = 0; j < 2; ++j) ref[j][0] = ref[j][1] = -INFINITY;
-#pragma unroll 4
-    for (int k = 0; k < n; ++k)
+    for (int e = 0; e < 4; ++e) top[e] = -INFINITY;
+    for (int k0 = 0; k0 < n; k0 += 4) {
+        float2 m[4][2], l[4][2];
+        float4 y[4][2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float2 m = *reinterpret_cast<const float2 *>(ml_of(k, j));
-            ref[j][0] = fmaxf(ref[j][0], m.x), ref[j][1] = fmaxf(ref[j][1], m.y);
+        for (int k = 0; k < 4; ++k) {
+            const int kk = min(k0 + k, n - 1);
+            const size_t slot = (size_t)(kk ? 2 * (c + kk) : 2 * c + 1);
+            const float *ml = ws.ml + slot * 2 * N + col;
+            const float4 *po = reinterpret_cast<const float4 *>(ws.o + slot * N * V) + (size_t)(unit * (N / 8) + r0 / 8) * 32 + lane;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                m[k][j] = *reinterpret_cast<const float2 *>(ml + 8 * j);
+                l[k][j] = *reinterpret_cast<const float2 *>(ml + N + 8 * j);
+                y[k][j] = po[j * 32];
+                if (k0 + k >= n) m[k][j] = make_float2(-INFINITY, -INFINITY);
+            }
         }
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) ref[j][i] = ref[j][i] == -INFINITY ? 0.f : ref[j][i];
-#pragma unroll 4
-    for (int k = 0; k < n; ++k) {
-        const float4 *po = reinterpret_cast<const float4 *>(ws.o + (size_t)(k ? 2 * (c + k) : 2 * c + 1) * N * V) +
-                           (size_t)(unit * (N / 8) + r0 / 8) * 32 + lane;
+            for (int i = 0; i < 2; ++i) {
+                const int e = 2 * j + i;
+                auto at = [&](const float2 &v) { return i ? v.y : v.x; };
+                const float now = fmaxf(fmaxf(top[e], at(m[0][j])), fmaxf(fmaxf(at(m[1][j]), at(m[2][j])), at(m[3][j])));
+                const float ref = now == -INFINITY ? 0.f : now, f = exp2f(top[e] - ref);
+                top[e] = now;
+                sum[e] *= f, o[4 * j + i] *= f, o[4 * j + 2 + i] *= f;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float2 m = *reinterpret_cast<const float2 *>(ml_of(k, j)), l = *reinterpret_cast<const float2 *>(ml_of(k, j) + N);
-            const float4 y = po[j * 32];
-            const float f0 = exp2f(m.x - ref[j][0]), f1 = exp2f(m.y - ref[j][1]);
-            sum[j][0] += l.x * f0, sum[j][1] += l.y * f1;
-            o[4 * j] += y.x * f0, o[4 * j + 1] += y.y * f1, o[4 * j + 2] += y.z * f0, o[4 * j + 3] += y.w * f1;
-        }
+                for (int k = 0; k < 4; ++k) {
+                    const float g = exp2f(at(m[k][j]) - ref);
+                    if (k0 + k < n) {
+                        sum[e] += at(l[k][j]) * g;
+                        o[4 * j + i] += (i ? y[k][j].y : y[k][j].x) * g;
+                        o[4 * j + 2 + i] += (i ? y[k][j].w : y[k][j].z) * g;
+                    }
+                }
+            }
     }
+    float inv[2][2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) sum[j][i] = sum[j][i] == 0.f ? 0.f : 1.f / sum[j][i];
-    emit<V, 16>(o, sum, smem_u32(sh) + (uint32_t)(warp * 16 * 32), lane, (__nv_bfloat16 *)a.out + (int64_t)row0 * V + 16 * unit, rows);
+    for (int e = 0; e < 4; ++e) inv[e >> 1][e & 1] = sum[e] == 0.f ? 0.f : 1.f / sum[e];
+    emit<V, 16>(o, inv, smem_u32(stage + warp * 16 * 32), lane, (__nv_bfloat16 *)a.out + (int64_t)(rec.x + r0) * V + 16 * unit, rows);
 }
 
 // Rows of a row tile: the smallest that holds a sequence's query rows, or 64.

@@ -141,7 +141,7 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     prefetch_tables(a, (int64_t)blockIdx.x * kThreads + threadIdx.x);
     Share<kRows, kTok> sh = locate<kRows, kTok>(a, &m.red[0][0], pair, pairs, kThreads);
     const Ws ws = ws_of(a, pairs, V);
-    if (lead && threadIdx.x == 0) ws.rec[4 * pair + 2] = 0;
+    if (lead && threadIdx.x == 0) leave(ws.rec + 4 * pair, 0, 0, 0);
     tc::fence_before();
     __syncthreads();
     cluster_sync();  // both CTAs' barriers are set up
@@ -178,13 +178,11 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const int d = np % kDescs;
             wait(&m.desc_empty[d], (uint32_t)(np / kDescs + 1) & 1u);
             Piece pc;
-            int shares;
-            const bool more = !dead && sh.take(a, pair, pc, shares);
+            const bool more = !dead && sh.take(a, pc);
             if (!more) pc.tiles = 0;
             if (lane == 0) {
                 m.piece[d] = pc;
                 mbar_arrive(&m.desc_full[d]);
-                if (lead && more && shares) ws.rec[4 * pair] = pc.row0, ws.rec[4 * pair + 1] = pc.rows, ws.rec[4 * pair + 2] = shares;
             }
             __syncwarp();
             if (!more) break;
@@ -225,6 +223,7 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     ++nk;
                 }
             }
+            if (lead && pc.out == 1 && lane == 0) leave(ws.rec + 4 * pair, pc.row0, pc.rows, sh.reach(pair));
         }
         // no copy outlives the CTA, whoever else gave up
         for (int i = max(0, nk - 2); i < nk; ++i) mbar_wait_bounded(&m.k_full[i & 1], (uint32_t)(i >> 1) & 1u);
@@ -542,42 +541,64 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             tc::fence_after();
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
             // entries of column j of block b: half V / 2 + 128 b + j
-            __nv_bfloat16 *out = (__nv_bfloat16 *)a.out + ((int64_t)pc.row0 + r) * V + half * (V / 2);
             const bool sectors = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
             float4 *po = reinterpret_cast<float4 *>(ws.o + slot * 64 * V) + qt * 32 + lane;
-            auto put = [&](int b, const uint32_t (&o)[32]) {
-                if (pc.out) {
+            const uint32_t o_at = lanes + (uint32_t)(q2 * (V / 4));
+            if (pc.out) {
+#pragma unroll 1
+                for (int b = 0; b < V / 128; ++b) {
+                    uint32_t o[32];
+                    ld_32x32b(o_at + (uint32_t)(b * 32), o);
+                    tc::wait_ld();
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        po[(b * 8 + e) * 128] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
-                                                            __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
-                } else if (r < pc.rows) {
-                    uint32_t w[16];
+                        po[((q2 * (V / 128) + b) * 8 + e) * 128] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                                                               __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+                }
+            } else {
+                // 64 entries (128 bytes) of a row at a time: four lanes exchange quarters of their rows, so that each
+                // store writes whole 128-byte lines of eight rows (32 rows' sectors: twice the time)
+#pragma unroll 1
+                for (int b = 0; b < V / 256; ++b) {
+                    uint32_t w[4][8];  // quarters of the row, 16 entries each
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-                    if (sectors) {
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t o[32];
+                        ld_32x32b(o_at + (uint32_t)(b * 64 + h * 32), o);
+                        tc::wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 16; e += 8)
-                            st_global_32B(out + b * 32 + 2 * e, w[e], w[e + 1], w[e + 2], w[e + 3], w[e + 4], w[e + 5], w[e + 6], w[e + 7]);
-                    } else {
+                        for (int e = 0; e < 16; ++e)
+                            w[2 * h + (e >> 3)][e & 7] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+                    }
 #pragma unroll
-                        for (int e = 0; e < 16; e += 4)
-                            *reinterpret_cast<uint4 *>(out + b * 32 + 2 * e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
+                    for (int bit = 1; bit <= 2; bit <<= 1) {
+                        const bool up = lane & bit;
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            if (!(x & bit))
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    const uint32_t give = up ? w[x][e] : w[x | bit][e];
+                                    const uint32_t got = __shfl_xor_sync(0xffffffffu, give, bit);
+                                    if (up) w[x][e] = got;
+                                    else w[x | bit][e] = got;
+                                }
+                    }
+                    // now w[x] is quarter lane & 3 of the row of lane (lane & ~3) + x
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int rr = r - (lane & 3) + x;
+                        __nv_bfloat16 *at = (__nv_bfloat16 *)a.out + ((int64_t)pc.row0 + rr) * V + half * (V / 2) + q2 * (V / 4) + b * 64 + 16 * (lane & 3);
+                        if (rr < pc.rows) {
+                            if (sectors) {
+                                st_global_32B(at, w[x][0], w[x][1], w[x][2], w[x][3], w[x][4], w[x][5], w[x][6], w[x][7]);
+                            } else {
+                                *reinterpret_cast<uint4 *>(at) = make_uint4(w[x][0], w[x][1], w[x][2], w[x][3]);
+                                *reinterpret_cast<uint4 *>(at + 8) = make_uint4(w[x][4], w[x][5], w[x][6], w[x][7]);
+                            }
+                        }
                     }
                 }
-            };
-            constexpr int kMine = V / 128;  // blocks of 32 columns
-            const uint32_t o_at = lanes + (uint32_t)(q2 * kMine * 32);
-            uint32_t o0[32], o1[32];  // one is loaded while the other is stored
-            ld_32x32b(o_at, o0);
-#pragma unroll 1
-            for (int b = 0; b < kMine; b += 2) {
-                tc::wait_ld();
-                ld_32x32b(o_at + (uint32_t)((b + 1) * 32), o1);
-                put(q2 * kMine + b, o0);
-                tc::wait_ld();
-                if (b + 2 < kMine) ld_32x32b(o_at + (uint32_t)((b + 2) * 32), o0);
-                put(q2 * kMine + b + 1, o1);
             }
             tc::fence_before();
             softmax_sync<kSoftmax>();  // red is read by all before the next piece writes it
@@ -601,47 +622,52 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     }
 }
 
-// Joins the pieces of cut contexts: CTA (c, y) the one that begins in share c, 16 entries of the 64 rows of one
-// CTA (each half's), a thread 16 entries of one row.
+// Joins the pieces of cut contexts: CTA (c, y) the one that begins in share c, 16 entries (of each half) of the 64 rows
+// of one CTA, a thread 16 entries of one row; the loads of two pieces in flight.
 template <int V>
 __global__ void __launch_bounds__(128) latent_pair_join_kernel(const __grid_constant__ Args a, int shares) {
     grid_dependency_wait();
-    // queries that see nothing, but for those in a row tile with others
-    for (int s = blockIdx.y * gridDim.x + blockIdx.x; s < a.S; s += gridDim.x * gridDim.y) {
-        Walk<kRows, kTok> w;
-        w.open(a, s);
-        const int64_t vecs = min((int64_t)w.k0 * kRows, (int64_t)w.nH) * (V / 8);
-        uint4 *o = reinterpret_cast<uint4 *>((__nv_bfloat16 *)a.out + (int64_t)w.q0 * a.H * V);
-        for (int64_t i = threadIdx.x; i < vecs; i += 128) o[i] = make_uint4(0, 0, 0, 0);
-    }
+    zero_blind<kRows, kTok>(a, blockIdx.y * gridDim.x + blockIdx.x, gridDim.x * gridDim.y, 128);
     const Ws ws = ws_of(a, shares, V);
-    const int c = blockIdx.x, n = ws.rec[4 * c + 2];
-    if (n == 0) return;
-    const int rank = blockIdx.y & 1, at = blockIdx.y >> 1;
+    const int c = blockIdx.x, rank = blockIdx.y & 1, at = blockIdx.y >> 1;
     const int row = threadIdx.x & 63, half = threadIdx.x >> 6, r = 64 * rank + row;
-    if (r >= ws.rec[4 * c + 1]) return;
-    auto slot_of = [&](int k) { return (size_t)(k ? 2 * (c + k) : 2 * c + 1) * 2 + rank; };
-    float ref = -INFINITY, sum = 0.f, o[16] = {};
-#pragma unroll 4
-    for (int k = 0; k < n; ++k) ref = fmaxf(ref, ws.ml[slot_of(k) * 128 + row]);
-    if (ref == -INFINITY) ref = 0.f;
-#pragma unroll 2
-    for (int k = 0; k < n; ++k) {
-        const size_t slot = slot_of(k);
-        const float f = exp2f(ws.ml[slot * 128 + row] - ref);
-        sum += ws.ml[slot * 128 + 64 + row] * f;
-        const float4 *po = reinterpret_cast<const float4 *>(ws.o + slot * 64 * V) + at * 4 * 128 + threadIdx.x;
+    const int4 rec = *reinterpret_cast<const int4 *>(ws.rec + 4 * c);
+    const int n = rec.z;
+    if (n == 0 || r >= rec.y) return;
+    float top = -INFINITY, sum = 0.f, o[16] = {};
+    for (int k0 = 0; k0 < n; k0 += 2) {
+        float m[2], l[2];
+        float4 y[2][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float4 y = po[e * 128];
-            o[4 * e] += y.x * f, o[4 * e + 1] += y.y * f, o[4 * e + 2] += y.z * f, o[4 * e + 3] += y.w * f;
+        for (int k = 0; k < 2; ++k) {
+            const int kk = min(k0 + k, n - 1);
+            const size_t slot = (size_t)(kk ? 2 * (c + kk) : 2 * c + 1) * 2 + rank;
+            m[k] = k0 + k < n ? ws.ml[slot * 128 + row] : -INFINITY;
+            l[k] = ws.ml[slot * 128 + 64 + row];
+            const float4 *po = reinterpret_cast<const float4 *>(ws.o + slot * 64 * V) + at * 4 * 128 + threadIdx.x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[k][e] = po[e * 128];
         }
+        const float now = fmaxf(top, fmaxf(m[0], m[1])), ref = now == -INFINITY ? 0.f : now, f = exp2f(top - ref);
+        top = now;
+        sum *= f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[e] *= f;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (k0 + k < n) {
+                const float g = exp2f(m[k] - ref);
+                sum += l[k] * g;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    o[4 * e] += y[k][e].x * g, o[4 * e + 1] += y[k][e].y * g, o[4 * e + 2] += y[k][e].z * g, o[4 * e + 3] += y[k][e].w * g;
+            }
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     uint32_t w[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) w[e] = pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
-    __nv_bfloat16 *out = (__nv_bfloat16 *)a.out + ((int64_t)ws.rec[4 * c] + r) * V + half * (V / 2) + at * 16;
+    __nv_bfloat16 *out = (__nv_bfloat16 *)a.out + ((int64_t)rec.x + r) * V + half * (V / 2) + at * 16;
     *reinterpret_cast<uint4 *>(out) = make_uint4(w[0], w[1], w[2], w[3]);
     *reinterpret_cast<uint4 *>(out + 8) = make_uint4(w[4], w[5], w[6], w[7]);
 }

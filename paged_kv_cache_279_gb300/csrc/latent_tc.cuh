@@ -156,9 +156,10 @@ struct Share {
     int parts;
     bool over;  // the context of w has been handed out
 
-    // The next piece of the share, false if there is none; `shares`: how many shares hold parts of a context that
-    // begins here and does not end here, else 0.
-    __device__ __forceinline__ bool take(const Args &a, int id, Piece &pc, int &shares) {
+    int after;  // tiles of the last piece's context behind it
+
+    // The next piece of the share, false if there is none.
+    __device__ __forceinline__ bool take(const Args &a, Piece &pc) {
         while (left > 0) {
             if (over) {
                 if (++w.k >= w.R) do {
@@ -183,12 +184,14 @@ struct Share {
             pc.lim0 = w.p0 + 1;
             pc.seq = w.s;
             pc.out = pc.tiles == nt ? 0 : i0 == 0 ? 1 : 2;
-            // (a context that begins here and is cut ends nt - i1 tiles after the share)
-            shares = pc.out == 1 ? (int)(share_owner(last + (nt - i1) - 1, total, parts) - id) + 1 : 0;
+            after = nt - i1;
             return true;
         }
         return false;
     }
+    // How many shares, from this one (`id`) on, hold parts of the context that begins here and is cut, once the last
+    // piece is taken: it ends `after` tiles behind the share.
+    __device__ __forceinline__ int reach(int id) const { return (int)(share_owner(last + after - 1, total, parts) - id) + 1; }
 };
 
 // Share `id` of at most `most`: each of the block's `threads` threads sums the tiles of a run of sequences, and
@@ -261,6 +264,24 @@ __device__ __forceinline__ Share<N, TOK> locate(const Args &a, float *scratch, i
     r.off = scan[16], r.left = last - first, r.last = last, r.total = total, r.parts = parts, r.over = false;
     __syncthreads();  // the scratch memory is free
     return r;
+}
+
+// What a share leaves for the join of the context that begins in it and is cut: first row, rows, and the number of
+// shares (pieces); 0 pieces: none.
+__device__ __forceinline__ void leave(int *rec, int row0, int rows, int pieces) {
+    *reinterpret_cast<int4 *>(rec) = make_int4(row0, rows, pieces, 0);
+}
+
+// Zeros for the queries that see nothing, but for those in a row tile with others; sequence after sequence.
+template <int N, int TOK>
+__device__ __forceinline__ void zero_blind(const Args &a, int first, int step, int threads) {
+    for (int s = first; s < a.S; s += step) {
+        Walk<N, TOK> w;
+        w.open(a, s);
+        const int64_t vecs = min((int64_t)w.k0 * N, (int64_t)w.nH) * (a.V / 8);
+        uint4 *o = reinterpret_cast<uint4 *>((unsigned char *)a.out + (int64_t)w.q0 * a.H * a.V * 2);
+        for (int64_t i = threadIdx.x; i < vecs; i += threads) o[i] = make_uint4(0, 0, 0, 0);
+    }
 }
 
 // The block tables, read later one entry after another, on their way into L2.
