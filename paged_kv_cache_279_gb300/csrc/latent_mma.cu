@@ -77,7 +77,7 @@ struct L {
     static constexpr int kChunks = V / 64 + 1;
     static constexpr int kGroup = kChunks * 1024;  // bytes of 8 tokens
     static constexpr int kTile = kTok / 8 * kGroup;
-    static constexpr int kPart0 = V / 128;         // chunks of the tile's first part; the second has the rest
+    static constexpr int kPart0 = V / 64 - 2;      // chunks of the tile's first part; the second, awaited last, has three
     static constexpr int kQ = kChunks * N * 128;
     static constexpr int kQBufs = N <= 32 ? 2 : 1;  // the next piece's queries are loaded under this one's, where they fit
     static constexpr int kP = kTok * 128;
@@ -104,7 +104,7 @@ struct alignas(8) Misc {
 static_assert(sizeof(Misc) <= 2048, "misc");
 
 struct Ws {
-    int *rec;      // [shares][4]: first row, rows, pieces of the context that begins in a share and is cut
+    int *rec;      // [shares][4]: what the context that begins in a share left for the join; or one for each context
     float *o;      // [shares][2][N][V]
     float *ml;     // [shares][2][2][N]: reference (base 2), sum of weights
 };
@@ -122,7 +122,7 @@ __device__ __forceinline__ Ws ws_of(const Args &a, int shares, int n, int v) {
 template <int V, int N>
 __global__ void __launch_bounds__(kThreads, 1)
 latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_c0,
-                  const __grid_constant__ CUtensorMap tm_c1, const __grid_constant__ Args a) {
+                  const __grid_constant__ CUtensorMap tm_c1, const __grid_constant__ Args a, int by_context) {
     using X = L<V, N>;
     extern __shared__ __align__(1024) unsigned char smem[];
     Misc &m = *reinterpret_cast<Misc *>(smem + X::misc);
@@ -149,10 +149,10 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     grid_dependency_wait();
     grid_launch_dependents();  // the join kernel; it waits for this one before it reads
 
-    prefetch_tables(a, (int64_t)cta * kThreads + threadIdx.x);
+    prefetch_tables(a, (int64_t)threadIdx.x * G + cta);
     Share<N, kTok> sh = locate<N, kTok>(a, &m.red[0][0], cta, G, kThreads);
     const Ws ws = ws_of(a, G, N, V);
-    if (threadIdx.x == 0) leave(ws.rec + 4 * cta, 0, 0, 0);
+    if (threadIdx.x == 0 && !by_context) leave(ws.rec + 4 * cta, 0, 0, 0, 0);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
@@ -238,7 +238,10 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 ++halves;
                 if (X::kQBufs == 1 && t == 0) load_q();
             }
-            if (pc.out == 1 && lane == 0) leave(ws.rec + 4 * cta, pc.row0, pc.rows, sh.reach(cta));
+            if (lane == 0) {
+                if (by_context && pc.out != 2) leave(ws.rec + 4 * (pc.seq * sh.w.R + sh.w.k), pc.row0, pc.rows, pc.out ? sh.reach(cta) : 0, cta);
+                else if (pc.out == 1) leave(ws.rec + 4 * cta, pc.row0, pc.rows, sh.reach(cta), cta);
+            }
             ++np;
         }
         // no copy outlives the CTA, whoever else gave up
@@ -581,33 +584,40 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     }
 }
 
-// Joins the pieces of cut contexts: CTA (c, y) the one that begins in share c, a warp 16 entries of 16 rows, in the
-// layout the pieces were stored in.  Small units, all at once, and four pieces' loads in flight: what it waits for
-// is L2 (units taken in turn by fewer CTAs, a unit's pieces divided among four warps: 10 us more for 64 contexts).
+// Joins the pieces of cut contexts: CTA (c, y) that of one context (or of the one that begins in share c), SPLIT warps
+// 16 entries of 16 rows, in the layout the pieces were stored in.  What it waits for is L2, 1 to 1.5 us for each batch of
+// loads.  So the pieces of a context of many (a few long contexts) are divided among four warps (8 contexts of 19 pieces:
+// 5 us less), and a batch is two pieces: with four, the registers keep this kernel's CTAs off the SMs until the first
+// kernel's have gone (1 to 3 us more).
 constexpr int kJoinWarps = 8;
 
-template <int V, int N>
-__global__ void __launch_bounds__(kJoinWarps * 32) latent_mma_join_kernel(const __grid_constant__ Args a, int shares) {
-    __shared__ __align__(128) unsigned char stage[kJoinWarps * 16 * 32];
+template <int V, int N, int SPLIT>
+__global__ void __launch_bounds__(kJoinWarps * 32) latent_mma_join_kernel(const __grid_constant__ Args a, int shares, int by_context) {
+    __shared__ __align__(128) unsigned char stage[kJoinWarps / SPLIT][16 * 32];
+    __shared__ float part[SPLIT > 1 ? kJoinWarps : 1][16][32];
     grid_dependency_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    zero_blind<N, kTok>(a, blockIdx.y * gridDim.x + blockIdx.x, gridDim.x * gridDim.y, kJoinWarps * 32);
     const Ws ws = ws_of(a, shares, N, V);
-    const int c = blockIdx.x;
-    const int4 rec = *reinterpret_cast<const int4 *>(ws.rec + 4 * c);
+    int4 rec = *reinterpret_cast<const int4 *>(ws.rec + 4 * blockIdx.x);
+    zero_blind<N, kTok>(a, blockIdx.y * gridDim.x + blockIdx.x, gridDim.x * gridDim.y, kJoinWarps * 32);
+    if (by_context) {  // contexts without tokens leave nothing
+        Walk<N, kTok> w;
+        w.open(a, blockIdx.x / ((a.H + N - 1) / N));
+        if (w.k0 >= w.R) return;
+    }
     constexpr int kRowUnits = N / 16;
-    const int work = blockIdx.y * kJoinWarps + warp, unit = work / kRowUnits, r0 = work % kRowUnits * 16;
-    const int n = rec.z, rows = rec.y - r0;
-    if (n == 0 || rows <= 0) return;
+    const int g = warp % SPLIT, work = blockIdx.y * (kJoinWarps / SPLIT) + warp / SPLIT, unit = work / kRowUnits, r0 = work % kRowUnits * 16;
+    const int n = rec.z, rows = rec.y - r0, c = rec.w;
+    if (n == 0) return;
     const int col = r0 + 2 * (lane & 3);
     float top[4], sum[4] = {}, o[8] = {};  // [2 j + i]: row col + 8 j + i
 #pragma unroll
     for (int e = 0; e < 4; ++e) top[e] = -INFINITY;
-    for (int k0 = 0; k0 < n; k0 += 4) {
-        float2 m[4][2], l[4][2];
-        float4 y[4][2];
+    for (int k0 = 2 * g; k0 < n && rows > 0; k0 += 2 * SPLIT) {
+        float2 m[2][2], l[2][2];
+        float4 y[2][2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 2; ++k) {
             const int kk = min(k0 + k, n - 1);
             const size_t slot = (size_t)(kk ? 2 * (c + kk) : 2 * c + 1);
             const float *ml = ws.ml + slot * 2 * N + col;
@@ -626,25 +636,51 @@ __global__ void __launch_bounds__(kJoinWarps * 32) latent_mma_join_kernel(const 
             for (int i = 0; i < 2; ++i) {
                 const int e = 2 * j + i;
                 auto at = [&](const float2 &v) { return i ? v.y : v.x; };
-                const float now = fmaxf(fmaxf(top[e], at(m[0][j])), fmaxf(fmaxf(at(m[1][j]), at(m[2][j])), at(m[3][j])));
+                const float now = fmaxf(top[e], fmaxf(at(m[0][j]), at(m[1][j])));
                 const float ref = now == -INFINITY ? 0.f : now, f = exp2f(top[e] - ref);
                 top[e] = now;
                 sum[e] *= f, o[4 * j + i] *= f, o[4 * j + 2 + i] *= f;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float g = exp2f(at(m[k][j]) - ref);
+                for (int k = 0; k < 2; ++k) {
+                    const float g2 = exp2f(at(m[k][j]) - ref);
                     if (k0 + k < n) {
-                        sum[e] += at(l[k][j]) * g;
-                        o[4 * j + i] += (i ? y[k][j].y : y[k][j].x) * g;
-                        o[4 * j + 2 + i] += (i ? y[k][j].w : y[k][j].z) * g;
+                        sum[e] += at(l[k][j]) * g2;
+                        o[4 * j + i] += (i ? y[k][j].y : y[k][j].x) * g2;
+                        o[4 * j + 2 + i] += (i ? y[k][j].w : y[k][j].z) * g2;
                     }
                 }
             }
     }
+    if constexpr (SPLIT > 1) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) part[warp][e][lane] = o[e];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) part[warp][8 + e][lane] = top[e], part[warp][12 + e][lane] = sum[e];
+        __syncthreads();
+        if (g) return;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int at = 4 * (e >> 1) + (e & 1);
+            float now = top[e], f[SPLIT];
+#pragma unroll
+            for (int k = 1; k < SPLIT; ++k) now = fmaxf(now, part[warp + k][8 + e][lane]);
+            if (now == -INFINITY) now = 0.f;
+#pragma unroll
+            for (int k = 0; k < SPLIT; ++k) f[k] = exp2f((k ? part[warp + k][8 + e][lane] : top[e]) - now);
+            sum[e] *= f[0], o[at] *= f[0], o[at + 2] *= f[0];
+#pragma unroll
+            for (int k = 1; k < SPLIT; ++k) {
+                sum[e] += part[warp + k][12 + e][lane] * f[k];
+                o[at] += part[warp + k][at][lane] * f[k];
+                o[at + 2] += part[warp + k][at + 2][lane] * f[k];
+            }
+        }
+    }
+    if (rows <= 0) return;
     float inv[2][2];
 #pragma unroll
     for (int e = 0; e < 4; ++e) inv[e >> 1][e & 1] = sum[e] == 0.f ? 0.f : 1.f / sum[e];
-    emit<V, 16>(o, inv, smem_u32(stage + warp * 16 * 32), lane, (__nv_bfloat16 *)a.out + (int64_t)(rec.x + r0) * V + 16 * unit, rows);
+    emit<V, 16>(o, inv, smem_u32(stage[warp / SPLIT]), lane, (__nv_bfloat16 *)a.out + (int64_t)(rec.x + r0) * V + 16 * unit, rows);
 }
 
 // Rows of a row tile: the smallest that holds a sequence's query rows, or 64.
@@ -661,9 +697,18 @@ pkv_status launch(const Args &a, cudaStream_t st) {
     if (!make_map(&tm_q, a.q, (int64_t)a.T * a.H, V, N, X::kChunks) || !make_map(&tm_c0, a.cache, rows, V, 8, X::kPart0) ||
         !make_map(&tm_c1, a.cache, rows, V, 8, X::kChunks - X::kPart0))
         return PKV_ERR_CUDA;
-    const pkv_status rc = launch_pdl(latent_mma_kernel<V, N>, dim3((unsigned)sms), dim3(kThreads), (size_t)X::total, st, tm_q, tm_c0, tm_c1, a);
+    // A decode of no more contexts than shares: the join's CTAs go by contexts, fewer than the shares.
+    const int64_t contexts = (int64_t)a.S * ((a.H + N - 1) / N);
+    const int by_context = !a.q_starts && contexts <= sms;
+    const pkv_status rc = launch_pdl(latent_mma_kernel<V, N>, dim3((unsigned)sms), dim3(kThreads), (size_t)X::total, st, tm_q, tm_c0, tm_c1, a,
+                                     by_context);
     if (rc != PKV_OK) return rc;
-    return launch_pdl(latent_mma_join_kernel<V, N>, dim3((unsigned)sms, (unsigned)(V * N / 256 / kJoinWarps)), dim3(kJoinWarps * 32), 0, st, a, sms);
+    constexpr unsigned kUnits = V * N / 256;
+    const unsigned cuts = by_context ? (unsigned)contexts : (unsigned)sms;
+    // (pieces of a context: about shares / contexts)
+    if (by_context && contexts * 4 < sms)
+        return launch_pdl(latent_mma_join_kernel<V, N, 4>, dim3(cuts, kUnits * 4 / kJoinWarps), dim3(kJoinWarps * 32), 0, st, a, sms, by_context);
+    return launch_pdl(latent_mma_join_kernel<V, N, 1>, dim3(cuts, kUnits / kJoinWarps), dim3(kJoinWarps * 32), 0, st, a, sms, by_context);
 }
 
 }  // namespace

@@ -138,10 +138,10 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     }
     grid_dependency_wait();
     grid_launch_dependents();  // the join kernel; it waits for this one before it reads
-    prefetch_tables(a, (int64_t)blockIdx.x * kThreads + threadIdx.x);
+    prefetch_tables(a, (int64_t)threadIdx.x * gridDim.x + blockIdx.x);
     Share<kRows, kTok> sh = locate<kRows, kTok>(a, &m.red[0][0], pair, pairs, kThreads);
     const Ws ws = ws_of(a, pairs, V);
-    if (lead && threadIdx.x == 0) leave(ws.rec + 4 * pair, 0, 0, 0);
+    if (lead && threadIdx.x == 0) leave(ws.rec + 4 * pair, 0, 0, 0, 0);
     tc::fence_before();
     __syncthreads();
     cluster_sync();  // both CTAs' barriers are set up
@@ -223,7 +223,7 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     ++nk;
                 }
             }
-            if (lead && pc.out == 1 && lane == 0) leave(ws.rec + 4 * pair, pc.row0, pc.rows, sh.reach(pair));
+            if (lead && pc.out == 1 && lane == 0) leave(ws.rec + 4 * pair, pc.row0, pc.rows, sh.reach(pair), pair);
         }
         // no copy outlives the CTA, whoever else gave up
         for (int i = max(0, nk - 2); i < nk; ++i) mbar_wait_bounded(&m.k_full[i & 1], (uint32_t)(i >> 1) & 1u);

@@ -266,10 +266,10 @@ __device__ __forceinline__ Share<N, TOK> locate(const Args &a, float *scratch, i
     return r;
 }
 
-// What a share leaves for the join of the context that begins in it and is cut: first row, rows, and the number of
-// shares (pieces); 0 pieces: none.
-__device__ __forceinline__ void leave(int *rec, int row0, int rows, int pieces) {
-    *reinterpret_cast<int4 *>(rec) = make_int4(row0, rows, pieces, 0);
+// What is left for the join of a context that is cut: first row, rows, pieces (one in each of as many shares), and the
+// first piece's share; 0 pieces: nothing to join.
+__device__ __forceinline__ void leave(int *rec, int row0, int rows, int pieces, int share) {
+    *reinterpret_cast<int4 *>(rec) = make_int4(row0, rows, pieces, share);
 }
 
 // Zeros for the queries that see nothing, but for those in a row tile with others; sequence after sequence.
@@ -284,7 +284,8 @@ __device__ __forceinline__ void zero_blind(const Args &a, int first, int step, i
     }
 }
 
-// The block tables, read later one entry after another, on their way into L2.
+// The block tables, read later one entry after another, on their way into L2; line after line over the CTAs, so that
+// each SM has the tables' pages at hand.
 __device__ __forceinline__ void prefetch_tables(const Args &a, int64_t line) {
     if ((int64_t)a.S * a.maxb <= 1 << 17 && line * 32 < (int64_t)a.S * a.maxb)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(a.tables + line * 32));
