@@ -21,6 +21,7 @@ struct Args {
     unsigned char *ws;
     unsigned int *err;
     int S, T, H, V, B, bshift, maxb, NB, max_q, max_len;
+    int rows;                // most query rows of a sequence, at most T * H
     float scale_log2;        // scale * log2(e)
 };
 

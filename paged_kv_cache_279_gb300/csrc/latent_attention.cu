@@ -267,6 +267,17 @@ size_t simt_workspace(int64_t T, int H, int V, int max_len) {
     return parts == 1 || max_len <= 128 ? 0 : round256((size_t)T * H * parts * partial_floats(V) * sizeof(float));
 }
 
+// Zeros for every query, and the flags of bad lengths and starts: nothing is in sight.
+__global__ void __launch_bounds__(256) latent_zero_kernel(const __grid_constant__ Args a) {
+    grid_dependency_wait();
+    for (int s = blockIdx.x; s < a.S; s += gridDim.x) {
+        const Seq q = sequence(a, s);
+        if (q.flagged && threadIdx.x == 0) flag_error(a.err, PKV_DEVERR_SEQ_LEN);
+        uint4 *o = reinterpret_cast<uint4 *>((__nv_bfloat16 *)a.out + (int64_t)q.q0 * a.H * a.V);
+        for (int64_t i = threadIdx.x; i < (int64_t)q.n * a.H * a.V / 8; i += 256) o[i] = make_uint4(0, 0, 0, 0);
+    }
+}
+
 pkv_status run_simt(const Args &a, cudaStream_t st) {
     const Split sp = split_of(a.T, a.H, a.max_len);
     const int64_t items = (int64_t)a.T * ((a.H + kRW - 1) / kRW);
@@ -278,6 +289,7 @@ pkv_status run_simt(const Args &a, cudaStream_t st) {
 }
 
 size_t workspace(int64_t T, int H, int V, int max_len, int dtype) {
+    if (max_len < 1) return 0;
     if (dtype == PKV_F32) return simt_workspace(T, H, V, max_len);
     const size_t one = mma_workspace(T, H, V), two = T * H > kPairRows ? pair_workspace(V) : 0;
     return one > two ? one : two;
@@ -293,19 +305,25 @@ pkv_status run(Args &a, float scale, size_t ws_bytes, int dtype, void *stream) {
     if (!known_shape(a.H, a.V)) return PKV_ERR_UNSUPPORTED;
     if (a.B != 8 && a.B != 16 && a.B != 32 && a.B != 64) return PKV_ERR_UNSUPPORTED;
     if (a.S == 0 || a.T == 0) return PKV_OK;
-    if ((int64_t)a.maxb * a.B > 0x7fffffffll) return PKV_ERR_INVALID;          // positions past 31 bits
-    if ((int64_t)a.NB * a.B > 0x7fffffffll) return PKV_ERR_UNSUPPORTED;        // cache rows past 31 bits
-    if ((int64_t)a.T * a.H > 0x7fffffffll) return PKV_ERR_UNSUPPORTED;         // query rows past 31 bits
+    // positions, cache rows and query rows of 31 bits, with room for a tile past the last
+    if ((int64_t)a.maxb * a.B > 0x7ffff000ll) return PKV_ERR_INVALID;
+    if ((int64_t)a.NB * a.B > 0x7fffffffll) return PKV_ERR_UNSUPPORTED;
+    if ((int64_t)a.T * a.H > 0x7ffff000ll) return PKV_ERR_UNSUPPORTED;
     if (!a.out || !a.q || !a.cache || !a.tables || !a.lens) return PKV_ERR_INVALID;
     if (!aligned16(a.out) || !aligned16(a.q) || !aligned16(a.cache)) return PKV_ERR_INVALID;
     a.max_len = (int)((int64_t)a.max_len < (int64_t)a.maxb * a.B ? a.max_len : (int64_t)a.maxb * a.B);
+    a.rows = (a.q_starts ? (a.max_q < a.T ? a.max_q : a.T) : 1) * a.H;
     a.bshift = a.B == 8 ? 3 : a.B == 16 ? 4 : a.B == 32 ? 5 : 6;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.err = device_error_word();
     const size_t need = workspace(a.T, a.H, a.V, a.max_len, dtype);
     if (need && (!a.ws || (reinterpret_cast<uintptr_t>(a.ws) & 255u) || ws_bytes < need)) return PKV_ERR_INVALID;
     if (dtype == PKV_F32) return run_simt(a, (cudaStream_t)stream);
-    return (int64_t)(a.q_starts ? a.max_q : 1) * a.H > kPairRows ? run_pair(a, (cudaStream_t)stream) : run_mma(a, (cudaStream_t)stream);
+    if (a.max_len == 0) {  // contexts without a token
+        const unsigned grid = a.S < 1024 ? (unsigned)a.S : 1024u;
+        return launch_pdl(latent_zero_kernel, dim3(grid), dim3(256), 0, (cudaStream_t)stream, a);
+    }
+    return a.rows > kPairRows ? run_pair(a, (cudaStream_t)stream) : run_mma(a, (cudaStream_t)stream);
 }
 
 }  // namespace

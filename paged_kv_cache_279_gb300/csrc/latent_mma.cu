@@ -600,15 +600,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32) latent_mma_join_kernel(const 
     const Ws ws = ws_of(a, shares, N, V);
     int4 rec = *reinterpret_cast<const int4 *>(ws.rec + 4 * blockIdx.x);
     zero_blind<N, kTok>(a, blockIdx.y * gridDim.x + blockIdx.x, gridDim.x * gridDim.y, kJoinWarps * 32);
-    if (by_context) {  // contexts without tokens leave nothing
+    if (by_context) {
         Walk<N, kTok> w;
-        w.open(a, blockIdx.x / ((a.H + N - 1) / N));
-        if (w.k0 >= w.R) return;
+        const int R = (a.H + N - 1) / N, s = blockIdx.x / R, k = blockIdx.x - s * R;
+        w.open(a, s);
+        if (w.k0 >= w.R) return;  // a context without tokens leaves nothing
+        rec.x = s * a.H + k * N, rec.y = min(N, a.H - k * N);
     }
     constexpr int kRowUnits = N / 16;
     const int g = warp % SPLIT, work = blockIdx.y * (kJoinWarps / SPLIT) + warp / SPLIT, unit = work / kRowUnits, r0 = work % kRowUnits * 16;
     const int n = rec.z, rows = rec.y - r0, c = rec.w;
-    if (n == 0) return;
+    if (n <= 0 || c < 0 || c > shares - n) return;  // (after a wait that ran out a record may not have been left)
     const int col = r0 + 2 * (lane & 3);
     float top[4], sum[4] = {}, o[8] = {};  // [2 j + i]: row col + 8 j + i
 #pragma unroll
@@ -719,8 +721,7 @@ size_t mma_workspace(int64_t T, int H, int V) {
 }
 
 pkv_status run_mma(const Args &a, cudaStream_t st) {
-    const int64_t rows = (int64_t)(a.q_starts ? a.max_q : 1) * a.H;
-    switch (rows_of(rows)) {
+    switch (rows_of(a.rows)) {
         case 16: return a.V == 512 ? launch<512, 16>(a, st) : launch<256, 16>(a, st);
         case 32: return a.V == 512 ? launch<512, 32>(a, st) : launch<256, 32>(a, st);
         default: return a.V == 512 ? launch<512, 64>(a, st) : launch<256, 64>(a, st);

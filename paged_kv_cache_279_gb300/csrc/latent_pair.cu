@@ -108,7 +108,7 @@ __device__ __forceinline__ void commit_both(uint64_t *bar) {
 template <int V>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k0, const __grid_constant__ CUtensorMap tm_k1,
-                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Args a) {
+                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Args a, int by_context) {
     using X = L<V>;
     extern __shared__ __align__(1024) unsigned char smem[];
     Misc &m = *reinterpret_cast<Misc *>(smem + X::misc);
@@ -141,7 +141,7 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     prefetch_tables(a, (int64_t)threadIdx.x * gridDim.x + blockIdx.x);
     Share<kRows, kTok> sh = locate<kRows, kTok>(a, &m.red[0][0], pair, pairs, kThreads);
     const Ws ws = ws_of(a, pairs, V);
-    if (lead && threadIdx.x == 0) leave(ws.rec + 4 * pair, 0, 0, 0, 0);
+    if (lead && threadIdx.x == 0 && !by_context) leave(ws.rec + 4 * pair, 0, 0, 0, 0);
     tc::fence_before();
     __syncthreads();
     cluster_sync();  // both CTAs' barriers are set up
@@ -223,7 +223,10 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     ++nk;
                 }
             }
-            if (lead && pc.out == 1 && lane == 0) leave(ws.rec + 4 * pair, pc.row0, pc.rows, sh.reach(pair), pair);
+            if (lead && lane == 0) {
+                if (by_context && pc.out != 2) leave(ws.rec + 4 * pc.seq, pc.row0, pc.rows, pc.out ? sh.reach(pair) : 0, pair);
+                else if (pc.out == 1) leave(ws.rec + 4 * pair, pc.row0, pc.rows, sh.reach(pair), pair);
+            }
         }
         // no copy outlives the CTA, whoever else gave up
         for (int i = max(0, nk - 2); i < nk; ++i) mbar_wait_bounded(&m.k_full[i & 1], (uint32_t)(i >> 1) & 1u);
@@ -622,20 +625,29 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     }
 }
 
-// Joins the pieces of cut contexts: CTA (c, y) the one that begins in share c, 16 entries (of each half) of the 64 rows
-// of one CTA, a thread 16 entries of one row; the loads of two pieces in flight.
-template <int V>
-__global__ void __launch_bounds__(128) latent_pair_join_kernel(const __grid_constant__ Args a, int shares) {
+// Joins the pieces of cut contexts: CTA (c, y) that of one context (or of the one that begins in share c), 16 entries (of
+// each half) of the 64 rows of one CTA, a thread 16 entries of one row, SPLIT threads its pieces (a few long contexts have
+// many).
+template <int V, int SPLIT>
+__global__ void __launch_bounds__(128 * SPLIT) latent_pair_join_kernel(const __grid_constant__ Args a, int shares, int by_context) {
+    __shared__ float part[SPLIT > 1 ? SPLIT - 1 : 1][18][128];
     grid_dependency_wait();
-    zero_blind<kRows, kTok>(a, blockIdx.y * gridDim.x + blockIdx.x, gridDim.x * gridDim.y, 128);
     const Ws ws = ws_of(a, shares, V);
-    const int c = blockIdx.x, rank = blockIdx.y & 1, at = blockIdx.y >> 1;
-    const int row = threadIdx.x & 63, half = threadIdx.x >> 6, r = 64 * rank + row;
-    const int4 rec = *reinterpret_cast<const int4 *>(ws.rec + 4 * c);
-    const int n = rec.z;
-    if (n == 0 || r >= rec.y) return;
+    int4 rec = *reinterpret_cast<const int4 *>(ws.rec + 4 * blockIdx.x);
+    zero_blind<kRows, kTok>(a, blockIdx.y * gridDim.x + blockIdx.x, gridDim.x * gridDim.y, 128 * SPLIT);
+    if (by_context) {  // (one row tile a sequence: at most 128 heads)
+        Walk<kRows, kTok> w;
+        w.open(a, blockIdx.x);
+        if (w.k0 >= w.R) return;  // a context without tokens leaves nothing
+        rec.x = blockIdx.x * a.H, rec.y = a.H;
+    }
+    const int rank = blockIdx.y & 1, at = blockIdx.y >> 1, g = threadIdx.x >> 7, me = threadIdx.x & 127;
+    const int row = me & 63, half = me >> 6, r = 64 * rank + row;
+    const int n = rec.z, c = rec.w;
+    // (after a wait that ran out a record may not have been left)
+    if (n <= 0 || c < 0 || c > shares - n || 64 * rank >= rec.y) return;
     float top = -INFINITY, sum = 0.f, o[16] = {};
-    for (int k0 = 0; k0 < n; k0 += 2) {
+    for (int k0 = 2 * g; k0 < n; k0 += 2 * SPLIT) {
         float m[2], l[2];
         float4 y[2][4];
 #pragma unroll
@@ -644,7 +656,7 @@ __global__ void __launch_bounds__(128) latent_pair_join_kernel(const __grid_cons
             const size_t slot = (size_t)(kk ? 2 * (c + kk) : 2 * c + 1) * 2 + rank;
             m[k] = k0 + k < n ? ws.ml[slot * 128 + row] : -INFINITY;
             l[k] = ws.ml[slot * 128 + 64 + row];
-            const float4 *po = reinterpret_cast<const float4 *>(ws.o + slot * 64 * V) + at * 4 * 128 + threadIdx.x;
+            const float4 *po = reinterpret_cast<const float4 *>(ws.o + slot * 64 * V) + at * 4 * 128 + me;
 #pragma unroll
             for (int e = 0; e < 4; ++e) y[k][e] = po[e * 128];
         }
@@ -656,13 +668,38 @@ __global__ void __launch_bounds__(128) latent_pair_join_kernel(const __grid_cons
 #pragma unroll
         for (int k = 0; k < 2; ++k)
             if (k0 + k < n) {
-                const float g = exp2f(m[k] - ref);
-                sum += l[k] * g;
+                const float f2 = exp2f(m[k] - ref);
+                sum += l[k] * f2;
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    o[4 * e] += y[k][e].x * g, o[4 * e + 1] += y[k][e].y * g, o[4 * e + 2] += y[k][e].z * g, o[4 * e + 3] += y[k][e].w * g;
+                    o[4 * e] += y[k][e].x * f2, o[4 * e + 1] += y[k][e].y * f2, o[4 * e + 2] += y[k][e].z * f2, o[4 * e + 3] += y[k][e].w * f2;
             }
     }
+    if constexpr (SPLIT > 1) {
+        if (g) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) part[g - 1][e][me] = o[e];
+            part[g - 1][16][me] = top, part[g - 1][17][me] = sum;
+        }
+        __syncthreads();
+        if (g) return;
+        float now = top, f[SPLIT];
+#pragma unroll
+        for (int k = 1; k < SPLIT; ++k) now = fmaxf(now, part[k - 1][16][me]);
+        if (now == -INFINITY) now = 0.f;
+#pragma unroll
+        for (int k = 0; k < SPLIT; ++k) f[k] = exp2f((k ? part[k - 1][16][me] : top) - now);
+        sum *= f[0];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[e] *= f[0];
+#pragma unroll
+        for (int k = 1; k < SPLIT; ++k) {
+            sum += part[k - 1][17][me] * f[k];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] += part[k - 1][e][me] * f[k];
+        }
+    }
+    if (r >= rec.y) return;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     uint32_t w[8];
 #pragma unroll
@@ -683,10 +720,14 @@ pkv_status launch(const Args &a, cudaStream_t st) {
     if (!make_map(&tm_q, a.q, (int64_t)a.T * a.H, V, 64, X::kChunks) || !make_map(&tm_k0, a.cache, rows, V, 8, X::kPart0) ||
         !make_map(&tm_k1, a.cache, rows, V, 8, X::kChunks - X::kPart0) || !make_map(&tm_v, a.cache, rows, V, 8, V / 128))
         return PKV_ERR_CUDA;
+    // A decode of no more contexts than shares: the join's CTAs go by contexts.
+    const int by_context = !a.q_starts && a.S <= pairs;
     const pkv_status rc = launch_pdl(latent_pair_kernel<V>, dim3((unsigned)(2 * pairs)), dim3(kThreads), (size_t)X::total, st, tm_q, tm_k0, tm_k1,
-                                     tm_v, a);
+                                     tm_v, a, by_context);
     if (rc != PKV_OK) return rc;
-    return launch_pdl(latent_pair_join_kernel<V>, dim3((unsigned)pairs, V / 16), dim3(128), 0, st, a, pairs);
+    const dim3 grid(by_context ? (unsigned)a.S : (unsigned)pairs, V / 16);
+    if (by_context && a.S * 4 < pairs) return launch_pdl(latent_pair_join_kernel<V, 4>, grid, dim3(512), 0, st, a, pairs, by_context);
+    return launch_pdl(latent_pair_join_kernel<V, 1>, grid, dim3(128), 0, st, a, pairs, by_context);
 }
 
 }  // namespace

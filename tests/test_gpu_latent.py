@@ -52,6 +52,54 @@ def test_limits_above_the_contexts():
     lc.check(lc.run(c, max_len=10 ** 9, max_q=10 ** 9), c)
 
 
+def test_a_loose_limit_on_the_queries_of_few_rows():
+    """Fewer than 64 query rows in all, whatever max_q_len says: the workspace is sized by what there is."""
+    for nq, H in (([3], 16), ([2, 1], 1), ([2, 2], 16), ([1], 32)):
+        c = lc.make([400, 90][:len(nq)], H, queries=nq)
+        n = pkv.paged_latent_attention_workspace_size(sum(nq), H, 512, 400)
+        ws = torch.full((n + 4096,), 77, dtype=torch.uint8, device="cuda")
+        lc.check(lc.run(c, max_q=10 ** 9, workspace=ws[:n]), c)
+        assert torch.all(ws[n:] == 77)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("queries", [None, [2, 3]])
+def test_no_tokens_at_all(dtype, queries):
+    c = lc.make([8, 8], 5, 256, 8, dtype, queries=queries)
+    c["lens"] = [0, 0]
+    out = torch.full((c["q"].shape[0] + 1, 5, 256), 7.0, dtype=dtype, device="cuda")
+    args = [out[:-1], c["q"].cuda(), c["cache"].cuda(), torch.from_numpy(c["tables"]).cuda(), torch.zeros(2, dtype=torch.int32).cuda()]
+    for max_len in (0, 8):
+        out.fill_(7.0)
+        if queries is None:
+            pkv.paged_latent_attention_decode(*args, 0.1, max_len)
+        else:
+            pkv.paged_latent_attention_multi_token(*args, torch.from_numpy(c["starts"]).cuda(), 0.1, 3, max_len)
+        assert torch.all(out[:-1] == 0) and torch.all(out[-1] == 7.0)
+    # queries without tokens to stand at are flagged, as are lengths above max_seq_len
+    assert pkv.read_device_errors(clear=True) == (pkv.DEVERR_SEQ_LEN if queries else 0)
+
+
+@pytest.mark.parametrize("V,H", [(512, 4), (256, 20), (512, 100)])
+def test_many_sequences(V, H):
+    r = np.random.default_rng(0)
+    lens = [int(x) for x in r.integers(1, 200, 400)]
+    lens[7] = lens[333] = 0
+    c = lc.make(lens, H, V, 16, seed=2)
+    lc.check(lc.run(c), c)
+    lens = [int(x) for x in r.integers(1, 100, 250)]
+    c = lc.make(lens, H, V, 32, queries=[int(min(L, x)) for L, x in zip(lens, r.integers(0, 6, 250))], seed=2)
+    lc.check(lc.run(c), c)
+
+
+@pytest.mark.parametrize("V,H,L", [(512, 128, 5000), (256, 128, 3000), (256, 64, 5000), (512, 33, 4000), (256, 8, 7000)])
+def test_one_long_context(V, H, L):
+    c = lc.make([L], H, V, 64, seed=5)
+    lc.check(lc.run(c), c)
+    c = lc.make([L, 30], H, V, 16, queries=[5, 2], seed=6)
+    lc.check(lc.run(c), c)
+
+
 def test_empty_contexts_and_rows_of_no_query():
     c = lc.make([0, 30, 0], 5)
     out = lc.run(c)
@@ -213,6 +261,43 @@ def test_streams_workspaces_and_graphs():
     graphs[0].replay()
     d = dict(c, lens=[2999, 9, 499], rows=[x[:-1] for x in c["rows"]])
     lc.check(outs[0], d)
+
+
+def test_pairs_on_streams_in_graphs_and_beside_each_other():
+    """Calls of more than 64 query rows: a captured one replayed with other lengths, two on two streams at once."""
+    c = lc.make([900, 40, 333], 16, queries=[40, 9, 100])
+    want = lc.run(c)
+    cache, q = c["cache"].cuda(), c["q"].cuda()
+    tables, lens = torch.from_numpy(c["tables"]).cuda(), torch.tensor(c["lens"], dtype=torch.int32).cuda()
+    starts = torch.from_numpy(c["starts"]).cuda()
+    outs = [torch.zeros_like(want) for _ in range(3)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for o, st in zip(outs, streams):
+            pkv.paged_latent_attention_multi_token(o, q, cache, tables, lens, starts, lc.SCALE, 100, 900, stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs[:2])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        pkv.paged_latent_attention_multi_token(outs[2], q, cache, tables, lens, starts, lc.SCALE, 100, 900)
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[2], want)
+    lens -= 1
+    g.replay()
+    lc.check(outs[2], dict(c, lens=[x - 1 for x in c["lens"]], rows=[x[:-1] for x in c["rows"]]))
+
+
+def test_an_output_16_bytes_off_a_sector():
+    for queries in (None, [20, 9]):
+        c = lc.make([300, 77], 16, queries=queries)
+        want = lc.run(c)
+        flat = torch.full((want.numel() + 24,), 7.0, dtype=BF, device="cuda")
+        out = flat[8:8 + want.numel()].view(want.shape)
+        assert torch.equal(lc.run(c, out=out), want)
+        assert torch.all(flat[:8] == 7.0) and torch.all(flat[8 + want.numel():] == 7.0)
 
 
 @pytest.mark.parametrize("V,H", [(512, 16), (256, 40)])
