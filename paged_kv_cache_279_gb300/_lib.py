@@ -117,6 +117,8 @@ def load():
     """The loaded libpkv.so.  Raises if it has not been built: there is no
     fallback implementation."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = library_path()

@@ -137,7 +137,8 @@ struct Walk {
         return G(kk + c, m) - G(k0 + c, m) + (int64_t)kHead * (kk - k0);
     }
     static __device__ __forceinline__ int64_t G(int64_t x, int64_t m) {  // sum of floor(j / m), j < x
-        const int64_t q = x / m;
+        // (32-bit division is a fifth of the time)
+        const int64_t q = (uint64_t)x < (1ull << 32) && m < (1ll << 31) ? (int64_t)((uint32_t)x / (uint32_t)m) : x / m;
         return m * (q * (q - 1) / 2) + q * (x - q * m);
     }
     __device__ __forceinline__ int64_t total(const Args &a) const {
@@ -195,7 +196,8 @@ struct Share {
 };
 
 // Share `id` of at most `most`: each of the block's `threads` threads sums the tiles of a run of sequences, and
-// the one whose run holds the share's first tile finds it.  By the whole block; `scratch`: 1 KB of shared memory.
+// the one whose run holds the share's first tile finds it.  By the whole block; `scratch`: 1 KB of shared memory,
+// free after the block's next barrier.
 template <int N, int TOK>
 __device__ __forceinline__ Share<N, TOK> locate(const Args &a, float *scratch, int id, int most, int threads) {
     int64_t *scan = reinterpret_cast<int64_t *>(scratch);  // the warps' totals; then where the share begins
@@ -236,7 +238,7 @@ __device__ __forceinline__ Share<N, TOK> locate(const Args &a, float *scratch, i
     }
     if (first < last && first >= excl && first < excl + mine) {
         int64_t off = first - excl;
-        for (int s = sb;; ++s) {
+        for (int s = sb; run > 1; ++s) {
             w.open(a, s);
             const int64_t t = w.total(a);
             if (off < t || s + 1 >= se) break;
@@ -244,8 +246,7 @@ __device__ __forceinline__ Share<N, TOK> locate(const Args &a, float *scratch, i
         }
         if (!a.q_starts) {
             const int per = w.tiles(a, 0) + kHead;
-            w.k = (int)off / per;
-            off -= (int64_t)w.k * per;
+            for (w.k = 0; off >= per; ++w.k) off -= per;  // (a few row tiles)
         } else {
             int lo = w.k0, hi = w.R;  // the last k with before(k) <= off
             while (hi - lo > 1) {
@@ -262,7 +263,6 @@ __device__ __forceinline__ Share<N, TOK> locate(const Args &a, float *scratch, i
     __syncthreads();
     r.w = begin;
     r.off = scan[16], r.left = last - first, r.last = last, r.total = total, r.parts = parts, r.over = false;
-    __syncthreads();  // the scratch memory is free
     return r;
 }
 
