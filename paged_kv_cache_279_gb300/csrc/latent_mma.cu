@@ -97,6 +97,7 @@ struct alignas(8) Misc {
     uint64_t full[2][4], empty[2][4], q_full[2], q_empty[2], s_full[2], s_free[2], p_full, pv_done, o_free, desc_full[kDescs], desc_empty[kDescs], fin[2];
     Piece piece[kDescs];
     float red[4][64];
+    int lim[64];         // tokens that a row of the piece sees
     uint32_t groups[4];  // valid 8-token groups of a stage's tile
     uint32_t tmem;
     int dead;
@@ -160,16 +161,7 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 
     bool dead = false;
     auto wait = [&](uint64_t *bar, uint32_t parity) {  // by whole warps
-        bool ok = dead;
-        for (uint32_t i = 0; i < kWaitLimit && !ok; ++i) {
-            ok = mbar_try_wait(bar, parity);
-            if ((i & 255u) == 255u && *(volatile int *)&m.dead) break;
-        }
-        if (__any_sync(0xffffffffu, !ok)) {
-            dead = true;
-            *(volatile int *)&m.dead = 1;
-            flag_error(a.err, PKV_DEVERR_TIMEOUT);
-        }
+        if (!dead && !__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) dead = wait_on(bar, parity, &m.dead, a.err);
     };
 
     if (warp == 0) {
@@ -265,9 +257,9 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 const int st = tile % X::kStages;
                 wait(&m.s_free[tile & 1], (uint32_t)((tile >> 1) + 1) & 1u);
                 const uint64_t c0 = cd + (uint64_t)(st * (X::kTile >> 4)), q0 = qd + (uint64_t)(qb * (X::kQ >> 4));
-                auto part = [&](auto lo, auto hi) {
-#pragma unroll
-                    for (int c = lo(); c < hi(); ++c)
+                auto part = [&](int lo, int hi) {
+#pragma unroll 1
+                    for (int c = lo; c < hi; ++c)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             tc::mma(tmem + X::kS + (uint32_t)((tile & 1) * N), c0 + (uint64_t)((c * 1024 + k * 32) >> 4),
@@ -276,12 +268,12 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 wait(&m.full[0][st], (uint32_t)(tile / X::kStages) & 1u);
                 if (dead) break;
                 tc::fence_after();
-                if (leader) part([] { return 0; }, [] { return X::kPart0; });
+                if (leader) part(0, X::kPart0);
                 __syncwarp();
                 wait(&m.full[1][st], (uint32_t)(tile / X::kStages) & 1u);
                 if (dead) break;
                 if (leader) {
-                    part([] { return X::kPart0; }, [] { return X::kChunks; });
+                    part(X::kPart0, X::kChunks);
                     tc::commit(&m.s_full[tile & 1]);
                     if (t + 1 == n) tc::commit(&m.q_empty[qb]);
                 }
@@ -314,7 +306,7 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 tc::fence_after();
                 if (leader) {
                     const uint64_t l0 = ld + (uint64_t)(st * (X::kTile >> 4));
-#pragma unroll
+#pragma unroll 1
                     for (int b = 0; b < X::kBlocks; ++b) {
 #pragma unroll
                         for (int k = 0; k < kTok / 16; ++k)
@@ -353,7 +345,9 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             float nref[J][2], l[J][2];  // minus the reference: +inf before the first score
 #pragma unroll
             for (int j = 0; j < J; ++j) nref[j][0] = nref[j][1] = INFINITY, l[j][0] = l[j][1] = 0.f;
-            const int least = pc.lim0 + pc.qh0 / a.H;  // tokens that the first row sees
+            if (threadIdx.x - 96 < N) m.lim[threadIdx.x - 96] = min(pc.end, pc.lim0 + (pc.qh0 + (int)threadIdx.x - 96) / a.H);
+            softmax_sync<128>();
+            const int least = m.lim[0];  // tokens that the first row sees
             for (int t = 0; t < pc.tiles; ++t, ++tile) {
                 const int st = tile % X::kStages;
                 wait(&m.s_full[tile & 1], (uint32_t)(tile >> 1) & 1u);
@@ -378,7 +372,7 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             const int c = 8 * j + col + i;
-                            const int lim = min(pc.end, pc.lim0 + (pc.qh0 + c) / a.H);
+                            const int lim = m.lim[c];
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
                                 if (c < pc.rows) nf[h] &= r[4 * j + 2 * h + i];
@@ -402,10 +396,12 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                         }
                     }
                 }
-                float x[4 * J];
-                // log2 of the weights against the references (`blank`: against 0 where there is none yet);
-                // the largest, or NaN
-                auto weigh = [&](float blank) {
+                // x: log2 of the weights against the references.  Once, if no score passes its row's reference by far; else
+                // against 0 where there is none yet, for new references, and a third time.  (A rolled loop: this code is
+                // fetched for every tile.)
+                float x[4 * J], blank = INFINITY;
+#pragma unroll 1
+                for (int pass = 0;; ++pass) {
                     float top = -INFINITY;
 #pragma unroll
                     for (int j = 0; j < J; ++j)
@@ -414,27 +410,28 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                             const float nr = nref[j][i] == INFINITY ? blank : nref[j][i];
                             x[4 * j + i] = fmaf(__uint_as_float(r[4 * j + i]), sc, nr);
                             x[4 * j + 2 + i] = fmaf(__uint_as_float(r[4 * j + 2 + i]), sc, nr);
-                            if (masked) {
-#pragma unroll
-                                for (int h = 0; h < 2; ++h)
-                                    x[4 * j + 2 * h + i] = (hide[h] >> (2 * j + i)) & 1u ? -INFINITY
-                                                           : bad[h]                      ? __uint_as_float(0x7fffffffu)
-                                                                                         : x[4 * j + 2 * h + i];
-                            }
-                            top = max3_nan(top, x[4 * j + i], x[4 * j + 2 + i]);
                         }
-                    return top;
-                };
-                const float top = weigh(INFINITY);
-                if (tile > 0) wait(&m.pv_done, (uint32_t)(tile - 1) & 1u);  // P is free, and O at rest
-                if (softmax_any<128>(!(top <= kSlack) || dead)) {
-                    if (softmax_any<128>(dead)) {
-                        stop = true;
-                        break;
+                    if (masked)
+#pragma unroll
+                        for (int e = 0; e < 4 * J; ++e) {
+                            const int h = (e >> 1) & 1;
+                            x[e] = (hide[h] >> (2 * (e >> 2) + (e & 1))) & 1u ? -INFINITY : bad[h] ? __uint_as_float(0x7fffffffu) : x[e];
+                        }
+#pragma unroll
+                    for (int e = 0; e < 4 * J; e += 2) top = max3_nan(top, x[e], x[e + 1]);
+                    if (pass == 2) break;
+                    if (pass == 0) {
+                        if (tile > 0) wait(&m.pv_done, (uint32_t)(tile - 1) & 1u);  // P is free, and O at rest
+                        if (!softmax_any<128>(!(top <= kSlack) || dead)) break;
+                        if (softmax_any<128>(dead)) {
+                            stop = true;
+                            break;
+                        }
+                        blank = 0.f;
+                        continue;
                     }
-                    // Some score passed its row's reference by far, or is the row's first: new references
-                    // for such rows.  The others keep theirs, so no row's result depends on another's.
-                    weigh(0.f);
+                    // New references for the rows that need one.  The others keep theirs, so no row's result depends on
+                    // another's.
 #pragma unroll
                     for (int j = 0; j < J; ++j)
 #pragma unroll
@@ -458,7 +455,7 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                                 if (y > -INFINITY) nref[j][i] = -y;
                             } else if (y > kSlack) {
                                 nref[j][i] -= y;
-                                f[j][i] = exp2f(-y);
+                                f[j][i] = ex2_approx(-y);
                                 l[j][i] *= f[j][i];
                             }
                         }
@@ -482,8 +479,8 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                         }
                         tc::wait_st();
                     }
-                    weigh(0.f);
                 }
+                if (stop) break;
                 uint32_t w2[2 * J];  // [2 j + h]: columns col, col + 1 of block j, token h
 #pragma unroll
                 for (int j = 0; j < J; ++j)
@@ -542,7 +539,7 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 #pragma unroll
             for (int j = 0; j < J; ++j)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) sum[j][i] = sum[j][i] == 0.f ? 0.f : 1.f / sum[j][i];
+                for (int i = 0; i < 2; ++i) sum[j][i] = sum[j][i] == 0.f ? 0.f : __fdividef(1.f, sum[j][i]);
             auto fetch = [&](int u, uint32_t (&r)[4 * J]) { ld_16x256b(lanes + ((uint32_t)(u & 1) << 20) + (uint32_t)((u >> 1) * N), r); };
             auto put = [&](int u, const uint32_t (&r)[4 * J]) {
                 const int unit = ((u >> 1) * 4 + qt) * 2 + (u & 1);  // entries 16 unit ..
@@ -560,13 +557,12 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             uint32_t r0[4 * J], r1[4 * J];  // one is loaded while the other is stored
             fetch(0, r0);
 #pragma unroll 1
-            for (int u = 0; u < 2 * X::kBlocks; u += 2) {
+            for (int u = 0; u < 2 * X::kBlocks; ++u) {
                 tc::wait_ld();
-                fetch(u + 1, r1);
-                put(u, r0);
-                tc::wait_ld();
-                if (u + 2 < 2 * X::kBlocks) fetch(u + 2, r0);
-                put(u + 1, r1);
+#pragma unroll
+                for (int e = 0; e < 4 * J; ++e) r1[e] = r0[e];
+                if (u + 1 < 2 * X::kBlocks) fetch(u + 1, r0);
+                put(u, r1);
             }
             tc::fence_before();
             softmax_sync<128>();  // red is read by all before the next piece writes it

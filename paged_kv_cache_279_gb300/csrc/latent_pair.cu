@@ -150,16 +150,7 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 
     bool dead = false;
     auto wait = [&](uint64_t *bar, uint32_t parity) {  // by whole warps
-        bool ok = dead;
-        for (uint32_t i = 0; i < kWaitLimit && !ok; ++i) {
-            ok = mbar_try_wait(bar, parity);
-            if ((i & 255u) == 255u && *(volatile int *)&m.dead) break;
-        }
-        if (__any_sync(0xffffffffu, !ok)) {
-            dead = true;
-            *(volatile int *)&m.dead = 1;
-            flag_error(a.err, PKV_DEVERR_TIMEOUT);
-        }
+        if (!dead && !__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) dead = wait_on(bar, parity, &m.dead, a.err);
     };
 
     // lane l: the cache row of group l & 15 of tile t + (l >> 4) of a piece; -1: a bad block; -2: no token
@@ -307,7 +298,7 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (dead) break;
                 tc::fence_after();
                 if (leader) {
-#pragma unroll
+#pragma unroll 1  // (rolled: the instruction cache holds what the softmax needs)
                     for (int c = 0; c < X::kPart0; ++c)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
@@ -320,7 +311,7 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (dead) break;
                 tc::fence_after();
                 if (leader) {
-#pragma unroll
+#pragma unroll 1
                     for (int c = X::kPart0; c < X::kChunks; ++c)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
@@ -351,7 +342,7 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             for (int t = 0; t < n; ++t, ++tile) {
                 wait(&m.p_full, (uint32_t)tile & 1u);
                 auto half = [&](int h) {  // 4 steps of 16 tokens
-#pragma unroll
+#pragma unroll 1
                     for (int k = 0; k < 4; ++k)
 #pragma unroll
                         for (int b = 0; b < X::kBlocks; ++b)
@@ -470,7 +461,7 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         if (y > -INFINITY) nref = -y;
                     } else if (y > kSlack) {
                         nref -= y;
-                        f = exp2f(-y);
+                        f = ex2_approx(-y);
                         l2 = fma_f32x2(l2, f32x2(f, f), f32x2(0.f, 0.f));
                     }
                     if (t > 0) {
@@ -542,7 +533,7 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             wait(&m.pv_done, (uint32_t)(tile - 1) & 1u);
             if (softmax_any<kSoftmax>(dead)) break;
             tc::fence_after();
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const float inv = sum == 0.f ? 0.f : __fdividef(1.f, sum);
             // entries of column j of block b: half V / 2 + 128 b + j
             const bool sectors = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
             float4 *po = reinterpret_cast<float4 *>(ws.o + slot * 64 * V) + qt * 32 + lane;

@@ -25,6 +25,20 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
+// A bounded wait by a whole warp, the part that is seldom reached (out of line: the kernels' speed is their
+// instruction cache's); true: it gave up, or some other warp of the CTA had.
+static __device__ __noinline__ bool wait_on(uint64_t *bar, uint32_t parity, int *dead, unsigned int *err) {
+    bool ok = false;
+    for (uint32_t i = 0; i < kWaitLimit && !ok; ++i) {
+        ok = mbar_try_wait(bar, parity);
+        if ((i & 255u) == 255u && *(volatile int *)dead) break;
+    }
+    if (!__any_sync(0xffffffffu, !ok)) return false;
+    *(volatile int *)dead = 1;
+    flag_error(err, PKV_DEVERR_TIMEOUT);
+    return true;
+}
+
 // Maximum of three that is NaN if one of them is.
 __device__ __forceinline__ float max3_nan(float a, float b, float c) {
     float d;
