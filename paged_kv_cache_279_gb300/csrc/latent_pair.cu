@@ -108,7 +108,7 @@ __device__ __forceinline__ void commit_both(uint64_t *bar) {
 template <int V>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k0, const __grid_constant__ CUtensorMap tm_k1,
-                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Args a, int by_context) {
+                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o, const __grid_constant__ Args a, int by_context) {
     using X = L<V>;
     extern __shared__ __align__(1024) unsigned char smem[];
     Misc &m = *reinterpret_cast<Misc *>(smem + X::misc);
@@ -131,7 +131,7 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         m.dead = 0;
         fence_barrier_init();
     }
-    if (threadIdx.x == 32) prefetch_map(&tm_q), prefetch_map(&tm_k0), prefetch_map(&tm_k1), prefetch_map(&tm_v);
+    if (threadIdx.x == 32) prefetch_map(&tm_q), prefetch_map(&tm_k0), prefetch_map(&tm_k1), prefetch_map(&tm_v), prefetch_map(&tm_o);
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&m.tmem)), "r"(X::kCols) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
@@ -414,14 +414,20 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 uint32_t nf = 0u, suspect = 0u;
                 if (masked) {
                     // A row of the cache that holds an infinity or NaN gives every query such a score (and may not be the
-                    // only reason for one): the tokens that gave all of this CTA's rows one, a word of 32 tokens a warp.
+                    // only reason for one): seldom there, looked for in earnest only if some score is one.
+                    float most = 0.f;
 #pragma unroll
-                    for (int c = 0; c < 32; ++c)
-                        if ((s[c] & 0x7f800000u) == 0x7f800000u) nf |= 1u << c;
-                    const uint32_t all = __reduce_and_sync(0xffffffffu, nf);
-                    if (lane == 0) m.warp_bad[qt][q2] = all;
-                    softmax_sync<kSoftmax>();
-                    suspect = m.warp_bad[2 * half][qt & 1] & m.warp_bad[2 * half + 1][qt & 1];  // tokens 64 half + 32 (qt & 1) ..
+                    for (int c = 0; c < 32; c += 2) most = max3_nan(most, fabsf(__uint_as_float(s[c])), fabsf(__uint_as_float(s[c + 1])));
+                    if (softmax_any<kSoftmax>(!(most < INFINITY))) {
+                        // the tokens that gave all of this CTA's rows one, a word of 32 tokens a warp
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            if ((s[c] & 0x7f800000u) == 0x7f800000u) nf |= 1u << c;
+                        const uint32_t all = __reduce_and_sync(0xffffffffu, nf);
+                        if (lane == 0) m.warp_bad[qt][q2] = all;
+                        softmax_sync<kSoftmax>();
+                        suspect = m.warp_bad[2 * half][qt & 1] & m.warp_bad[2 * half + 1][qt & 1];  // tokens 64 half + 32 (qt & 1) ..
+                    }
                 }
                 // log2 of the weights without the reference
                 float x[32];
@@ -429,12 +435,14 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 for (int c = 0; c < 32; c += 2)
                     f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), f32x2(sc, sc), f32x2(0.f, 0.f)), x[c], x[c + 1]);
                 if (masked) {
-                    const uint32_t g8 = groups >> (8 * half + 4 * q2);
+                    const uint32_t g4 = groups >> (8 * half + 4 * q2);
                     const int seen = lim - tb - 64 * half - 32 * q2;  // of this thread's tokens the row sees so many
+                    uint32_t hide = seen <= 0 ? 0xffffffffu : seen >= 32 ? 0u : 0xffffffffu << seen;
+                    hide |= (g4 & 1u ? 0u : 0xffu) | (g4 & 2u ? 0u : 0xff00u) | (g4 & 4u ? 0u : 0xff0000u) | (g4 & 8u ? 0u : 0xff000000u);
 #pragma unroll
                     for (int c = 0; c < 32; ++c) {
                         if ((nf >> c) & 1u) x[c] = __uint_as_float(0x7fffffffu);  // (-infinity too: 0 times an infinity)
-                        if (c >= seen || !((g8 >> (c >> 3)) & 1u)) x[c] = -INFINITY;
+                        if ((hide >> c) & 1u) x[c] = -INFINITY;
                     }
                 }
                 float top = -INFINITY;
@@ -535,7 +543,6 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             tc::fence_after();
             const float inv = sum == 0.f ? 0.f : __fdividef(1.f, sum);
             // entries of column j of block b: half V / 2 + 128 b + j
-            const bool sectors = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
             float4 *po = reinterpret_cast<float4 *>(ws.o + slot * 64 * V) + qt * 32 + lane;
             const uint32_t o_at = lanes + (uint32_t)(q2 * (V / 4));
             if (pc.out) {
@@ -550,49 +557,50 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                                                                                __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
                 }
             } else {
-                // 64 entries (128 bytes) of a row at a time: four lanes exchange quarters of their rows, so that each
-                // store writes whole 128-byte lines of eight rows (32 rows' sectors: twice the time)
+                // 32 rows of 32 entries at a time through this warp's 2 KB of P's memory (free by now), and out by a
+                // bulk copy, or, where not all of the rows are the piece's, by hand: stores straight from the registers
+                // would write 32 rows' sectors each, at twice the time.
+                unsigned char *stage = smem + X::p + (warp - 4) * 2048;
+                const int r0 = r - lane, x0 = half * (V / 2) + q2 * (V / 4);
+                uint32_t o[32];
+                ld_32x32b(o_at, o);
 #pragma unroll 1
-                for (int b = 0; b < V / 256; ++b) {
-                    uint32_t w[4][8];  // quarters of the row, 16 entries each
+                for (int b = 0; b < V / 128; ++b) {
+                    tc::wait_ld();
+                    uint32_t w[16];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t o[32];
-                        ld_32x32b(o_at + (uint32_t)(b * 64 + h * 32), o);
-                        tc::wait_ld();
+                    for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+                    if (b + 1 < V / 128) ld_32x32b(o_at + (uint32_t)((b + 1) * 32), o);
+                    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the copy before has read it
+                    __syncwarp();
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            w[2 * h + (e >> 3)][e & 7] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-                    }
-#pragma unroll
-                    for (int bit = 1; bit <= 2; bit <<= 1) {
-                        const bool up = lane & bit;
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            if (!(x & bit))
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) {
-                                    const uint32_t give = up ? w[x][e] : w[x | bit][e];
-                                    const uint32_t got = __shfl_xor_sync(0xffffffffu, give, bit);
-                                    if (up) w[x][e] = got;
-                                    else w[x | bit][e] = got;
-                                }
-                    }
-                    // now w[x] is quarter lane & 3 of the row of lane (lane & ~3) + x
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const int rr = r - (lane & 3) + x;
-                        __nv_bfloat16 *at = (__nv_bfloat16 *)a.out + ((int64_t)pc.row0 + rr) * V + half * (V / 2) + q2 * (V / 4) + b * 64 + 16 * (lane & 3);
-                        if (rr < pc.rows) {
-                            if (sectors) {
-                                st_global_32B(at, w[x][0], w[x][1], w[x][2], w[x][3], w[x][4], w[x][5], w[x][6], w[x][7]);
-                            } else {
-                                *reinterpret_cast<uint4 *>(at) = make_uint4(w[x][0], w[x][1], w[x][2], w[x][3]);
-                                *reinterpret_cast<uint4 *>(at + 8) = make_uint4(w[x][4], w[x][5], w[x][6], w[x][7]);
-                            }
+                    for (int e = 0; e < 4; ++e)  // (64-byte swizzle)
+                        *reinterpret_cast<uint4 *>(stage + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4)) =
+                            make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+                    if (r0 + 32 <= pc.rows) {
+                        fence_proxy_async();
+                        __syncwarp();
+                        if (lane == 0) {
+                            asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                                             reinterpret_cast<uint64_t>(&tm_o)),
+                                         "r"(smem_u32(stage)), "r"(x0 + b * 32), "r"(pc.row0 + r0)
+                                         : "memory");
+                            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                         }
+                    } else {
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int rr = 8 * i + (lane >> 2), e = lane & 3;
+                            const uint4 y = *reinterpret_cast<const uint4 *>(stage + rr * 64 + ((e ^ ((rr >> 1) & 3)) << 4));
+                            if (r0 + rr < pc.rows)
+                                *reinterpret_cast<uint4 *>((__nv_bfloat16 *)a.out + ((int64_t)pc.row0 + r0 + rr) * V + x0 + b * 32 + 8 * e) = y;
+                        }
+                        __syncwarp();
                     }
                 }
+                if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                __syncwarp();
             }
             tc::fence_before();
             softmax_sync<kSoftmax>();  // red is read by all before the next piece writes it
@@ -602,6 +610,7 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
         }
     }
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // the output copies that this thread issued
     __syncwarp();
     if (warp == 1) {  // every product has ended before the memory goes
         mbar_wait_bounded(&m.fin[0], 0);
@@ -700,21 +709,33 @@ __global__ void __launch_bounds__(128 * SPLIT) latent_pair_join_kernel(const __g
     *reinterpret_cast<uint4 *>(out + 8) = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
+// The output's rows: boxes of 32 rows of 32 entries.
+bool make_out_map(CUtensorMap *map, void *out, int64_t rows, int V) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)V, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)V * 2};
+    cuuint32_t box[2] = {32u, 32u}, estr[2] = {1u, 1u};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, out, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int V>
 pkv_status launch(const Args &a, cudaStream_t st) {
     using X = L<V>;
     static bool done[128];
     const int pairs = sm_count() / 2;
     if (pairs == 0 || !ensure_smem(latent_pair_kernel<V>, X::total, done)) return PKV_ERR_CUDA;
-    CUtensorMap tm_q, tm_k0, tm_k1, tm_v;
+    CUtensorMap tm_q, tm_k0, tm_k1, tm_v, tm_o;
     const int64_t rows = (int64_t)a.NB * a.B;
     if (!make_map(&tm_q, a.q, (int64_t)a.T * a.H, V, 64, X::kChunks) || !make_map(&tm_k0, a.cache, rows, V, 8, X::kPart0) ||
-        !make_map(&tm_k1, a.cache, rows, V, 8, X::kChunks - X::kPart0) || !make_map(&tm_v, a.cache, rows, V, 8, V / 128))
+        !make_map(&tm_k1, a.cache, rows, V, 8, X::kChunks - X::kPart0) || !make_map(&tm_v, a.cache, rows, V, 8, V / 128) ||
+        !make_out_map(&tm_o, a.out, (int64_t)a.T * a.H, V))
         return PKV_ERR_CUDA;
     // A decode of no more contexts than shares: the join's CTAs go by contexts.
     const int by_context = !a.q_starts && a.S <= pairs;
     const pkv_status rc = launch_pdl(latent_pair_kernel<V>, dim3((unsigned)(2 * pairs)), dim3(kThreads), (size_t)X::total, st, tm_q, tm_k0, tm_k1,
-                                     tm_v, a, by_context);
+                                     tm_v, tm_o, a, by_context);
     if (rc != PKV_OK) return rc;
     const dim3 grid(by_context ? (unsigned)a.S : (unsigned)pairs, V / 16);
     if (by_context && a.S * 4 < pairs) return launch_pdl(latent_pair_join_kernel<V, 4>, grid, dim3(512), 0, st, a, pairs, by_context);
