@@ -22,6 +22,7 @@ struct Args {
     unsigned int *err;
     int S, T, H, V, B, bshift, maxb, NB, max_q, max_len;
     int rows;                // most query rows of a sequence, at most T * H
+    int whole;               // > 0: no context is cut, share id is row tile id % whole of sequence id / whole
     float scale_log2;        // scale * log2(e)
 };
 

@@ -10,7 +10,7 @@
 // bf16 runs on the tensor cores (latent_mma.cu).
 //
 // latent_simt_kernel: float32.  A warp takes kRW heads of
-// one query and every fourth batch of kTok tokens of a run of the context; its
+// one query and every eighth batch of kTok tokens of a run of the context; its
 // lanes hold the heads' queries, the running output and the rows of the batch in
 // registers, split over the row's entries, so each row is read from memory once a
 // warp in 16-byte loads and used for kRW heads.  The kRW * kTok sums over the lanes
@@ -28,7 +28,7 @@ namespace {
 
 constexpr int kRW = 4;     // heads of a warp
 constexpr int kTok = 4;    // tokens of a step
-constexpr int kWarps = 4;  // of a CTA: the same heads, different tokens
+constexpr int kWarps = 8;  // of a CTA: the same heads, different tokens
 
 constexpr int kPairRows = 64;  // a sequence's query rows above which pairs of CTAs take them (bf16)
 
@@ -36,11 +36,10 @@ constexpr int kPairRows = 64;  // a sequence's query rows above which pairs of C
 struct Split {
     int parts, run;
 };
-// Parts that fill the GPU with about four CTAs an SM; with fewer queries and heads
-// than that alone, more.
+// Parts that fill the GPU with one CTA an SM (what their registers allow).
 inline int most_parts(int64_t T, int H) {
     const int64_t items = T * ((H + kRW - 1) / kRW);
-    const int64_t want = items < 1 ? 1 : (608 + items - 1) / items;
+    const int64_t want = items < 1 ? 1 : (152 + items - 1) / items;
     return (int)(want > 64 ? 64 : want);
 }
 inline Split split_of(int64_t T, int H, int max_len) {

@@ -153,7 +153,7 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     prefetch_tables(a, (int64_t)threadIdx.x * G + cta);
     Share<N, kTok> sh = locate<N, kTok>(a, &m.red[0][0], cta, G, kThreads);
     const Ws ws = ws_of(a, G, N, V);
-    if (threadIdx.x == 0 && !by_context) leave(ws.rec + 4 * cta, 0, 0, 0, 0);
+    if (threadIdx.x == 0 && !by_context && !a.whole) leave(ws.rec + 4 * cta, 0, 0, 0, 0);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
@@ -231,7 +231,8 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 if (X::kQBufs == 1 && t == 0) load_q();
             }
             if (lane == 0) {
-                if (by_context && pc.out != 2) leave(ws.rec + 4 * (pc.seq * sh.w.R + sh.w.k), pc.row0, pc.rows, pc.out ? sh.reach(cta) : 0, cta);
+                if (a.whole) {
+                } else if (by_context && pc.out != 2) leave(ws.rec + 4 * (pc.seq * sh.w.R + sh.w.k), pc.row0, pc.rows, pc.out ? sh.reach(cta) : 0, cta);
                 else if (pc.out == 1) leave(ws.rec + 4 * cta, pc.row0, pc.rows, sh.reach(cta), cta);
             }
             ++np;
@@ -685,7 +686,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) latent_mma_join_kernel(const 
 int rows_of(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
 template <int V, int N>
-pkv_status launch(const Args &a, cudaStream_t st) {
+pkv_status launch(Args a, cudaStream_t st) {
     static bool done[128];
     const int sms = sm_count();
     if (sms == 0 || !ensure_smem(latent_mma_kernel<V, N>, L<V, N>::total, done)) return PKV_ERR_CUDA;
@@ -698,9 +699,11 @@ pkv_status launch(const Args &a, cudaStream_t st) {
     // A decode of no more contexts than shares: the join's CTAs go by contexts, fewer than the shares.
     const int64_t contexts = (int64_t)a.S * ((a.H + N - 1) / N);
     const int by_context = !a.q_starts && contexts <= sms;
-    const pkv_status rc = launch_pdl(latent_mma_kernel<V, N>, dim3((unsigned)sms), dim3(kThreads), (size_t)X::total, st, tm_q, tm_c0, tm_c1, a,
+    a.whole = whole_contexts(a, N, kTok, sms);
+    const unsigned grid = a.whole ? (unsigned)(a.S * a.whole) : (unsigned)sms;
+    const pkv_status rc = launch_pdl(latent_mma_kernel<V, N>, dim3(grid), dim3(kThreads), (size_t)X::total, st, tm_q, tm_c0, tm_c1, a,
                                      by_context);
-    if (rc != PKV_OK) return rc;
+    if (rc != PKV_OK || a.whole) return rc;
     constexpr unsigned kUnits = V * N / 256;
     const unsigned cuts = by_context ? (unsigned)contexts : (unsigned)sms;
     // (pieces of a context: about shares / contexts)

@@ -141,7 +141,7 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     prefetch_tables(a, (int64_t)threadIdx.x * gridDim.x + blockIdx.x);
     Share<kRows, kTok> sh = locate<kRows, kTok>(a, &m.red[0][0], pair, pairs, kThreads);
     const Ws ws = ws_of(a, pairs, V);
-    if (lead && threadIdx.x == 0 && !by_context) leave(ws.rec + 4 * pair, 0, 0, 0, 0);
+    if (lead && threadIdx.x == 0 && !by_context && !a.whole) leave(ws.rec + 4 * pair, 0, 0, 0, 0);
     tc::fence_before();
     __syncthreads();
     cluster_sync();  // both CTAs' barriers are set up
@@ -215,7 +215,8 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
             }
             if (lead && lane == 0) {
-                if (by_context && pc.out != 2) leave(ws.rec + 4 * pc.seq, pc.row0, pc.rows, pc.out ? sh.reach(pair) : 0, pair);
+                if (a.whole) {
+                } else if (by_context && pc.out != 2) leave(ws.rec + 4 * pc.seq, pc.row0, pc.rows, pc.out ? sh.reach(pair) : 0, pair);
                 else if (pc.out == 1) leave(ws.rec + 4 * pair, pc.row0, pc.rows, sh.reach(pair), pair);
             }
         }
@@ -721,7 +722,7 @@ bool make_out_map(CUtensorMap *map, void *out, int64_t rows, int V) {
 }
 
 template <int V>
-pkv_status launch(const Args &a, cudaStream_t st) {
+pkv_status launch(Args a, cudaStream_t st) {
     using X = L<V>;
     static bool done[128];
     const int pairs = sm_count() / 2;
@@ -734,9 +735,11 @@ pkv_status launch(const Args &a, cudaStream_t st) {
         return PKV_ERR_CUDA;
     // A decode of no more contexts than shares: the join's CTAs go by contexts.
     const int by_context = !a.q_starts && a.S <= pairs;
-    const pkv_status rc = launch_pdl(latent_pair_kernel<V>, dim3((unsigned)(2 * pairs)), dim3(kThreads), (size_t)X::total, st, tm_q, tm_k0, tm_k1,
+    a.whole = whole_contexts(a, kRows, kTok, pairs);
+    const unsigned ctas = 2 * (a.whole ? (unsigned)(a.S * a.whole) : (unsigned)pairs);
+    const pkv_status rc = launch_pdl(latent_pair_kernel<V>, dim3(ctas), dim3(kThreads), (size_t)X::total, st, tm_q, tm_k0, tm_k1,
                                      tm_v, tm_o, a, by_context);
-    if (rc != PKV_OK) return rc;
+    if (rc != PKV_OK || a.whole) return rc;
     const dim3 grid(by_context ? (unsigned)a.S : (unsigned)pairs, V / 16);
     if (by_context && a.S * 4 < pairs) return launch_pdl(latent_pair_join_kernel<V, 4>, grid, dim3(512), 0, st, a, pairs, by_context);
     return launch_pdl(latent_pair_join_kernel<V, 1>, grid, dim3(128), 0, st, a, pairs, by_context);

@@ -209,6 +209,14 @@ struct Share {
     __device__ __forceinline__ int reach(int id) const { return (int)(share_owner(last + after - 1, total, parts) - id) + 1; }
 };
 
+// Zeros for a sequence's queries that see nothing, but for those in a row tile with others; by a block of `threads`.
+template <int N, int TOK>
+__device__ __forceinline__ void zero_blind(const Args &a, const Walk<N, TOK> &w, int threads) {
+    const int64_t vecs = min((int64_t)w.k0 * N, (int64_t)w.nH) * (a.V / 8);
+    uint4 *o = reinterpret_cast<uint4 *>((unsigned char *)a.out + (int64_t)w.q0 * a.H * a.V * 2);
+    for (int64_t i = threadIdx.x; i < vecs; i += threads) o[i] = make_uint4(0, 0, 0, 0);
+}
+
 // Share `id` of at most `most`: each of the block's `threads` threads sums the tiles of a run of sequences, and
 // the one whose run holds the share's first tile finds it.  By the whole block; `scratch`: 1 KB of shared memory,
 // free after the block's next barrier.
@@ -222,6 +230,20 @@ __device__ __forceinline__ Share<N, TOK> locate(const Args &a, float *scratch, i
     int64_t mine = 0;
     Share<N, TOK> r;
     Walk<N, TOK> &w = r.w;
+    if (a.whole) {
+        const int s = id / a.whole, k = id - s * a.whole;
+        r.off = r.left = r.last = r.total = r.parts = 0;
+        r.over = false;
+        if (s >= a.S) return r;
+        w.open(a, s);
+        if (k == 0) {
+            if (w.flagged && threadIdx.x == 0) flag_error(a.err, PKV_DEVERR_SEQ_LEN);
+            zero_blind(a, w, threads);
+        }
+        w.k = k;
+        if (k >= w.k0 && k < w.R) r.left = w.tiles(a, k) + kHead;
+        return r;
+    }
     for (int s = sb; s < se; ++s) {
         w.open(a, s);
         mine += w.total(a);
@@ -286,15 +308,13 @@ __device__ __forceinline__ void leave(int *rec, int row0, int rows, int pieces, 
     *reinterpret_cast<int4 *>(rec) = make_int4(row0, rows, pieces, share);
 }
 
-// Zeros for the queries that see nothing, but for those in a row tile with others; sequence after sequence.
+// The same, sequence after sequence.
 template <int N, int TOK>
 __device__ __forceinline__ void zero_blind(const Args &a, int first, int step, int threads) {
     for (int s = first; s < a.S; s += step) {
         Walk<N, TOK> w;
         w.open(a, s);
-        const int64_t vecs = min((int64_t)w.k0 * N, (int64_t)w.nH) * (a.V / 8);
-        uint4 *o = reinterpret_cast<uint4 *>((unsigned char *)a.out + (int64_t)w.q0 * a.H * a.V * 2);
-        for (int64_t i = threadIdx.x; i < vecs; i += threads) o[i] = make_uint4(0, 0, 0, 0);
+        zero_blind(a, w, threads);
     }
 }
 
@@ -303,6 +323,20 @@ __device__ __forceinline__ void zero_blind(const Args &a, int first, int step, i
 __device__ __forceinline__ void prefetch_tables(const Args &a, int64_t line) {
     if ((int64_t)a.S * a.maxb <= 1 << 17 && line * 32 < (int64_t)a.S * a.maxb)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(a.tables + line * 32));
+}
+
+// Whether every context of a call gets a share of its own, uncut, and nothing is left to join by a second kernel: there
+// are shares enough, and the longest context there may be has few tiles -- 4, and up to 10 the more of the shares are
+// in use (lengths differ: the limit is for contexts that are half of it on average).  Uncut against cut, in us, 32 heads:
+// 4 sequences of 64 / 256 / 384 / 512 tokens 7.1 / 10.1 / 12.6 / 15.0 against 9.6 / 11.7 / 11.9 / 12.0; 64 sequences of
+// 64 / 256 / 512 / 1024: 7.4 / 10.3 / 18.0 / 29.8 against 9.8 / 15.0 / 21.5 / 28.0; in pairs of CTAs (128 heads), 64
+// sequences of 256 / 512 / 1024: 12.1 / 17.8 / 26.1 against 21.2 / 25.9 / 37.6.
+// Returns the row tiles to count a sequence for, or 0.
+inline int whole_contexts(const Args &a, int n, int tok, int shares) {
+    const int64_t tiles = (int64_t)a.rows / n + (a.rows % n != 0), most = (int64_t)a.maxb * a.B;
+    const int64_t len = a.max_len < most ? a.max_len : most, contexts = a.S * tiles;
+    if (contexts > shares) return 0;
+    return len <= (4 + 6 * contexts / shares) * tok ? (int)tiles : 0;
 }
 
 // Rows of V + 64 entries as [chunk of 64 entries][row][64]: a box of `box` rows and `deep` chunks.
