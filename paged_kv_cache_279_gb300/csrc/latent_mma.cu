@@ -14,7 +14,7 @@
 // size from 8 on, eight boxes a tile, and both products see 128-byte swizzled
 // operands (C by rows, L^T by columns) whose 8-token groups are one stride apart.
 //
-// Softmax: four warps, a thread holds two tokens of every fourth pair of columns.
+// Softmax: four warps, or two sets of four; a thread holds two tokens of every fourth pair of columns.
 // Maxima over tokens would be shuffles over lanes, so the reference of a row moves
 // only when a score passes it by 2^kSlack: usually in the first tile alone.  Sums of
 // weights stay in the threads, per token, until the end of the piece.  Weights are
@@ -33,7 +33,6 @@ namespace latent {
 namespace {
 
 constexpr int kTok = 64;       // tokens of a tile
-constexpr int kThreads = 224;  // producer warp, a warp that issues each product, four softmax warps
 
 __device__ __forceinline__ void stmatrix_x4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
@@ -81,11 +80,14 @@ struct L {
     static constexpr int kQ = kChunks * N * 128;
     static constexpr int kQBufs = N <= 32 ? 2 : 1;  // the next piece's queries are loaded under this one's, where they fit
     static constexpr int kP = kTok * 128;
-    static constexpr int kMisc = 4096;
+    // softmax warps: four for each 32 rows of 64 (a tile of 64 rows keeps four busy for 1000 cycles), else four
+    static constexpr int kSets = N == 64 ? 2 : 1, kCols1 = N / kSets, kSoftmax = 128 * kSets;
+    static constexpr int kThreads = 96 + kSoftmax;  // and a producer, and a warp that issues each product
+    static constexpr int kMisc = 3072;
     static constexpr int kMax = 232448;  // shared memory of a CTA
-    static constexpr int kStages = (kMax - kMisc + 2048 - kQBufs * kQ - kP) / kTile < 4 ? (kMax - kMisc + 2048 - kQBufs * kQ - kP) / kTile : 4;
+    static constexpr int kStages = (kMax - kMisc - kQBufs * kQ - kP) / kTile < 4 ? (kMax - kMisc - kQBufs * kQ - kP) / kTile : 4;
     static constexpr int q = 0, p = kQBufs * kQ, ring = p + kP, misc = ring + kStages * kTile;
-    static constexpr int total = misc + 2048;
+    static constexpr int total = misc + kMisc;
     static constexpr int kBlocks = V / 128;              // of O^T
     static constexpr uint32_t kS = kBlocks * N;          // first column of S^T
     static constexpr uint32_t kCols = kS + 2 * N <= 128 ? 128 : kS + 2 * N <= 256 ? 256 : 512;
@@ -98,11 +100,12 @@ struct alignas(8) Misc {
     Piece piece[kDescs];
     float red[4][64];
     int lim[64];         // tokens that a row of the piece sees
+    uint32_t nf[2][64];  // by each set's rows: exponents of a token's scores, all of them together
     uint32_t groups[4];  // valid 8-token groups of a stage's tile
     uint32_t tmem;
     int dead;
 };
-static_assert(sizeof(Misc) <= 2048, "misc");
+static_assert(sizeof(Misc) <= 3072, "misc");
 
 struct Ws {
     int *rec;      // [shares][4]: what the context that begins in a share left for the join; or one for each context
@@ -121,7 +124,7 @@ __device__ __forceinline__ Ws ws_of(const Args &a, int shares, int n, int v) {
 }
 
 template <int V, int N>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(L<V, N>::kThreads, 1)
 latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_c0,
                   const __grid_constant__ CUtensorMap tm_c1, const __grid_constant__ Args a, int by_context) {
     using X = L<V, N>;
@@ -134,9 +137,9 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         for (int i = 0; i < 8; ++i) mbar_init(&m.full[i >> 2][i & 3], 1), mbar_init(&m.empty[i >> 2][i & 3], 1);
         for (int i = 0; i < 2; ++i) mbar_init(&m.q_full[i], 1), mbar_init(&m.q_empty[i], 1);
         mbar_init(&m.s_full[0], 1), mbar_init(&m.s_full[1], 1);
-        mbar_init(&m.s_free[0], 4), mbar_init(&m.s_free[1], 4);
-        mbar_init(&m.p_full, 4), mbar_init(&m.pv_done, 1), mbar_init(&m.o_free, 4), mbar_init(&m.fin[0], 1), mbar_init(&m.fin[1], 1);
-        for (int i = 0; i < kDescs; ++i) mbar_init(&m.desc_full[i], 1), mbar_init(&m.desc_empty[i], 6);
+        mbar_init(&m.s_free[0], 4 * X::kSets), mbar_init(&m.s_free[1], 4 * X::kSets);
+        mbar_init(&m.p_full, 4 * X::kSets), mbar_init(&m.pv_done, 1), mbar_init(&m.o_free, 4 * X::kSets), mbar_init(&m.fin[0], 1), mbar_init(&m.fin[1], 1);
+        for (int i = 0; i < kDescs; ++i) mbar_init(&m.desc_full[i], 1), mbar_init(&m.desc_empty[i], 2 + 4 * X::kSets);
         m.dead = 0;
         fence_barrier_init();
     }
@@ -151,7 +154,7 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     grid_launch_dependents();  // the join kernel; it waits for this one before it reads
 
     prefetch_tables(a, (int64_t)threadIdx.x * G + cta);
-    Share<N, kTok> sh = locate<N, kTok>(a, &m.red[0][0], cta, G, kThreads);
+    Share<N, kTok> sh = locate<N, kTok>(a, &m.red[0][0], cta, G, X::kThreads);
     const Ws ws = ws_of(a, G, N, V);
     if (threadIdx.x == 0 && !by_context && !a.whole) leave(ws.rec + 4 * cta, 0, 0, 0, 0);
     tc::fence_before();
@@ -330,24 +333,25 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         // ======================= softmax and epilogue =======================
         const int qt = warp & 3;  // quarter of the tensor memory's lanes
         const uint32_t lanes = tmem + ((uint32_t)(qt * 32) << 16);
-        constexpr int J = N / 8;
+        constexpr int NL = X::kCols1, J = NL / 8;
+        const int set = (warp - 3) >> 2;  // which of the rows
         const float sc = a.scale_log2;
-        const int col = 2 * (lane & 3), tok0 = qt * 16 + (lane >> 2);  // first column, first token (the other: 8 on)
+        const int col = set * NL + 2 * (lane & 3), tok0 = qt * 16 + (lane >> 2);  // first column, first token (the other: 8 on)
         // stmatrix: lane gives the address of row (lane & 7) of matrix lane >> 3: tokens 0-7, 8-15 of column block j, then j + 1
         const uint32_t p_s = smem_u32(smem + X::p) + (uint32_t)((qt * 2 + ((lane >> 3) & 1)) * 1024 + (lane & 7) * 128);
         int tile = 0;
-        bool stop = false;  // the four warps leave together: they share a barrier
+        bool stop = false;  // the softmax warps leave together: they share a barrier
         for (int np = 0;; ++np) {
             const int d = np % kDescs;
             wait(&m.desc_full[d], (uint32_t)(np / kDescs) & 1u);
-            if (softmax_any<128>(dead)) break;
+            if (softmax_any<X::kSoftmax>(dead)) break;
             const Piece pc = m.piece[d];
             if (pc.tiles == 0) break;
             float nref[J][2], l[J][2];  // minus the reference: +inf before the first score
 #pragma unroll
             for (int j = 0; j < J; ++j) nref[j][0] = nref[j][1] = INFINITY, l[j][0] = l[j][1] = 0.f;
             if (threadIdx.x - 96 < N) m.lim[threadIdx.x - 96] = min(pc.end, pc.lim0 + (pc.qh0 + (int)threadIdx.x - 96) / a.H);
-            softmax_sync<128>();
+            softmax_sync<X::kSoftmax>();
             const int least = m.lim[0];  // tokens that the first row sees
             for (int t = 0; t < pc.tiles; ++t, ++tile) {
                 const int st = tile % X::kStages;
@@ -355,7 +359,7 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 wait(&m.full[0][st], (uint32_t)(tile / X::kStages) & 1u);  // (complete: orders the read of groups)
                 tc::fence_after();
                 uint32_t r[4 * J];
-                ld_16x256b(lanes + X::kS + (uint32_t)((tile & 1) * N), r);
+                ld_16x256b(lanes + X::kS + (uint32_t)((tile & 1) * N + set * NL), r);
                 tc::wait_ld();
                 tc::fence_before();
                 __syncwarp();
@@ -388,9 +392,17 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     for (int h = 0; h < 2; ++h) {
                         nf[h] &= __shfl_xor_sync(0xffffffffu, nf[h], 1);
                         nf[h] &= __shfl_xor_sync(0xffffffffu, nf[h], 2);
+                    }
+                    if constexpr (X::kSets == 2) {
+                        if ((lane & 3) == 0) m.nf[set][tok0] = nf[0], m.nf[set][tok0 + 8] = nf[1];
+                        softmax_sync<X::kSoftmax>();
+                        nf[0] &= m.nf[set ^ 1][tok0], nf[1] &= m.nf[set ^ 1][tok0 + 8];
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
                         bad[h] = (nf[h] & 0x7f800000u) == 0x7f800000u;
                         const int tk = tok0 + 8 * h;
-                        if (bad[h]) {
+                        if (bad[h] && set == 0) {
                             unsigned char *g = smem + X::ring + st * X::kTile + (tk >> 3) * X::kGroup + (tk & 7) * 128;
                             for (int c = lane & 3; c < V / 64; c += 4)
                                 for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4 *>(g + c * 1024 + e * 16) = make_uint4(0, 0, 0, 0);
@@ -423,8 +435,8 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     if (pass == 2) break;
                     if (pass == 0) {
                         if (tile > 0) wait(&m.pv_done, (uint32_t)(tile - 1) & 1u);  // P is free, and O at rest
-                        if (!softmax_any<128>(!(top <= kSlack) || dead)) break;
-                        if (softmax_any<128>(dead)) {
+                        if (!softmax_any<X::kSoftmax>(!(top <= kSlack) || dead)) break;
+                        if (softmax_any<X::kSoftmax>(dead)) {
                             stop = true;
                             break;
                         }
@@ -443,7 +455,7 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                             y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
                             if (lane < 4) m.red[qt][8 * j + col + i] = y;
                         }
-                    softmax_sync<128>();
+                    softmax_sync<X::kSoftmax>();
                     float f[J][2];
 #pragma unroll
                     for (int j = 0; j < J; ++j)
@@ -460,23 +472,22 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                                 l[j][i] *= f[j][i];
                             }
                         }
-                    softmax_sync<128>();
+                    softmax_sync<X::kSoftmax>();
                     if (t > 0) {  // O^T has something: scale its columns
                         if (qt == 0 && lane < 4)
 #pragma unroll
                             for (int j = 0; j < J; ++j) m.red[0][8 * j + col] = f[j][0], m.red[0][8 * j + col + 1] = f[j][1];
-                        softmax_sync<128>();
+                        softmax_sync<X::kSoftmax>();
                         tc::fence_after();
-                        constexpr int W = N < 32 ? 16 : 32;
 #pragma unroll 1
-                        for (int b = 0; b < X::kBlocks * N / W; ++b) {
-                            uint32_t o[W];
-                            ld_32x32b(lanes + (uint32_t)(b * W), o);
+                        for (int b = 0; b < X::kBlocks; ++b) {
+                            uint32_t o[NL];
+                            const uint32_t at = lanes + (uint32_t)(b * N + set * NL);
+                            ld_32x32b(at, o);
                             tc::wait_ld();
-                            const int c0 = b * W % N;
 #pragma unroll
-                            for (int e = 0; e < W; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * m.red[0][c0 + e]);
-                            st_32x32b(lanes + (uint32_t)(b * W), o);
+                            for (int e = 0; e < NL; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * m.red[0][set * NL + e]);
+                            st_32x32b(at, o);
                         }
                         tc::wait_st();
                     }
@@ -494,7 +505,7 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     }
 #pragma unroll
                 for (int j = 0; j < J; j += 2)
-                    stmatrix_x4(p_s + (uint32_t)(((j + (lane >> 4)) ^ (lane & 7)) << 4), w2[2 * j], w2[2 * j + 1], w2[2 * j + 2],
+                    stmatrix_x4(p_s + (uint32_t)(((set * J + j + (lane >> 4)) ^ (lane & 7)) << 4), w2[2 * j], w2[2 * j + 1], w2[2 * j + 2],
                                 w2[2 * j + 3]);
                 fence_proxy_async();
                 tc::fence_before();
@@ -502,7 +513,7 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 if (lane == 0) mbar_arrive(&m.p_full);
             }
             if (stop) break;
-            softmax_sync<128>();  // red has been read
+            softmax_sync<X::kSoftmax>();  // red has been read
             // sums of weights over the tokens; then O^T, row by row
 #pragma unroll
             for (int j = 0; j < J; ++j)
@@ -514,7 +525,7 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     l[j][i] = y + __shfl_xor_sync(0xffffffffu, y, 16);
                     if (lane < 4) m.red[qt][8 * j + col + i] = l[j][i];
                 }
-            softmax_sync<128>();
+            softmax_sync<X::kSoftmax>();
             float sum[J][2];
 #pragma unroll
             for (int j = 0; j < J; ++j)
@@ -533,26 +544,26 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                         ws.ml[slot * 2 * N + N + 8 * j + col + i] = sum[j][i];
                     }
             wait(&m.pv_done, (uint32_t)(tile - 1) & 1u);
-            if (softmax_any<128>(dead)) break;
+            if (softmax_any<X::kSoftmax>(dead)) break;
             tc::fence_after();
             // O^T, 16 entries at a time; P's memory is free for the transposition
-            const uint32_t stage = smem_u32(smem + X::p) + (uint32_t)(qt * N * 32);
+            const uint32_t stage = smem_u32(smem + X::p) + (uint32_t)((set * 4 + qt) * NL * 32);
 #pragma unroll
             for (int j = 0; j < J; ++j)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) sum[j][i] = sum[j][i] == 0.f ? 0.f : __fdividef(1.f, sum[j][i]);
-            auto fetch = [&](int u, uint32_t (&r)[4 * J]) { ld_16x256b(lanes + ((uint32_t)(u & 1) << 20) + (uint32_t)((u >> 1) * N), r); };
+            auto fetch = [&](int u, uint32_t (&r)[4 * J]) { ld_16x256b(lanes + ((uint32_t)(u & 1) << 20) + (uint32_t)((u >> 1) * N + set * NL), r); };
             auto put = [&](int u, const uint32_t (&r)[4 * J]) {
                 const int unit = ((u >> 1) * 4 + qt) * 2 + (u & 1);  // entries 16 unit ..
                 if (pc.out) {
-                    uint4 *po = reinterpret_cast<uint4 *>(ws.o + slot * N * V) + (size_t)unit * J * 32 + lane;
+                    uint4 *po = reinterpret_cast<uint4 *>(ws.o + slot * N * V) + (size_t)(unit * (N / 8) + set * J) * 32 + lane;
 #pragma unroll
                     for (int j = 0; j < J; ++j) po[j * 32] = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
                 } else {
                     float o[4 * J];
 #pragma unroll
                     for (int e = 0; e < 4 * J; ++e) o[e] = __uint_as_float(r[e]);
-                    emit<V, N>(o, sum, stage, lane, (__nv_bfloat16 *)a.out + (int64_t)pc.row0 * V + 16 * unit, pc.rows);
+                    emit<V, NL>(o, sum, stage, lane, (__nv_bfloat16 *)a.out + (int64_t)(pc.row0 + set * NL) * V + 16 * unit, pc.rows - set * NL);
                 }
             };
             uint32_t r0[4 * J], r1[4 * J];  // one is loaded while the other is stored
@@ -566,7 +577,7 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 put(u, r1);
             }
             tc::fence_before();
-            softmax_sync<128>();  // red is read by all before the next piece writes it
+            softmax_sync<X::kSoftmax>();  // red is read by all before the next piece writes it
             if (lane == 0) {
                 mbar_arrive(&m.o_free);
                 mbar_arrive(&m.desc_empty[d]);
@@ -701,7 +712,7 @@ pkv_status launch(Args a, cudaStream_t st) {
     const int by_context = !a.q_starts && contexts <= sms;
     a.whole = whole_contexts(a, N, kTok, sms);
     const unsigned grid = a.whole ? (unsigned)(a.S * a.whole) : (unsigned)sms;
-    const pkv_status rc = launch_pdl(latent_mma_kernel<V, N>, dim3(grid), dim3(kThreads), (size_t)X::total, st, tm_q, tm_c0, tm_c1, a,
+    const pkv_status rc = launch_pdl(latent_mma_kernel<V, N>, dim3(grid), dim3(X::kThreads), (size_t)X::total, st, tm_q, tm_c0, tm_c1, a,
                                      by_context);
     if (rc != PKV_OK || a.whole) return rc;
     constexpr unsigned kUnits = V * N / 256;
