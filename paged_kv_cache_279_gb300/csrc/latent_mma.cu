@@ -23,6 +23,12 @@
 //
 // All contexts' tiles are laid end to end and cut into equal shares, one a CTA.  A
 // context cut by share boundaries leaves partial results that a second kernel joins.
+//
+// What bounds it: DRAM while tiles stream (5 TB/s of 6.7), before that a chain of loads
+// (lengths, block table, first tile: 3.8 us), after it the join (5 us).  64 contexts of 64
+// to 2048 tokens, 32 heads: 29.0 us for 73 MB; 8 of 16000, 64 heads: 46.6 us for 149 MB.
+// A tile takes 36 + 16 products, 1452 cycles at 16 rows, 1920 at 64 (operand bytes out of
+// shared memory); 3200 is its share of DRAM.
 #include <cmath>
 
 #include "latent_tc.cuh"

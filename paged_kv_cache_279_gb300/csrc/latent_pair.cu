@@ -16,6 +16,9 @@
 // The leader's (rank 0's) warps issue all products.  What the other CTA has ready it reports to the leader's
 // barriers; what the products have done arrives at both CTAs' barriers.
 //
+// Measured: 8 x 512 queries of 4096, 32 heads: 703 us (80 % of the measured bf16 rate), a tile 2300 to 2800 cycles where
+// its products are 2176; the transposed kernel took 1272.  4 prompts of 3200 to 4000 tokens, 16 heads: 566 us.
+//
 // Softmax: a thread has one row and a quarter of the tile's tokens (eight warps: with four, whose exponentials alone
 // take 512 cycles of each scheduler, a tile took 3300 cycles, not 2200).  References, weights,
 // hidden rows, shares and joins as in the transposed kernel.
