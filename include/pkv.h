@@ -475,7 +475,8 @@ PKV_EXPORT pkv_status paged_attention_multi_token_scored(
  * negative frequencies may be given to the calls too.
  *
  *   out, x         device [num_tokens][num_heads][head_dim], dtype, 16-byte
- *                  aligned.  out may be x; otherwise they must not overlap.
+ *                  aligned.  out may be x, with x's strides; otherwise they must
+ *                  not overlap.
  *   positions      device int32 [num_tokens], any value
  *   frequencies    device float64 [rotary_dim / 2]; infinite, NaN and subnormal
  *                  ones count as 0
@@ -548,7 +549,7 @@ PKV_EXPORT pkv_status kv_cache_write_rotary(void *q_out, const void *q, const vo
  *   out            device [num_seqs][num_heads][latent_dim]
  *   q              device [num_seqs][num_heads][latent_dim + PKV_LATENT_ROPE_DIM]
  *   block_tables, seq_lens, max_seq_len, scale  as for paged_attention_decode
- *                  (scale any finite number)
+ *                  (scale any finite number of at most 2^127 in size)
  * paged_latent_attention_multi_token -- the last Q_s positions of every sequence
  * (verification of drafted tokens, chunks of a prompt): queries, q_starts and
  * max_q_len as for paged_attention_multi_token; the query at position p sees the
@@ -560,7 +561,10 @@ PKV_EXPORT pkv_status kv_cache_write_rotary(void *q_out, const void *q, const vo
  * A query that sees no token, or whose scores are all -infinity, gets zeros.  Rows
  * of out that no query owns are left as they were.  Out-of-range lengths, query
  * starts and blocks are flagged as in the other calls; the tokens of a bad block
- * are left out.  Cache rows that a query does not see never reach its output,
+ * are left out, and where query starts decrease it is unspecified which sequence's
+ * results the rows in question hold.  BF16: weights may pass 1 by up to 2^8 before
+ * they are scaled back, so latent entries above 2^119 may overflow, and infinities
+ * and NaN in a row may make NaN of any entry of the queries that see it.  Cache rows that a query does not see never reach its output,
  * whatever they hold.  Results do not depend on which physical blocks hold the
  * tokens.
  */

@@ -301,7 +301,8 @@ bool known_shape(int H, int V) { return H >= 1 && H <= 128 && (V == 256 || V == 
 pkv_status run(Args &a, float scale, size_t ws_bytes, int dtype, void *stream) {
     if (a.S < 0 || a.T < 0 || a.H < 1 || a.V < 1 || a.B < 1 || a.maxb < 1 || a.NB < 1 || a.max_len < 0 || a.max_q < 1)
         return PKV_ERR_INVALID;
-    if (!std::isfinite(scale)) return PKV_ERR_INVALID;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    if (!std::isfinite(a.scale_log2)) return PKV_ERR_INVALID;
     if (dtype != PKV_F32 && dtype != PKV_BF16) return PKV_ERR_UNSUPPORTED;
     if (!known_shape(a.H, a.V)) return PKV_ERR_UNSUPPORTED;
     if (a.B != 8 && a.B != 16 && a.B != 32 && a.B != 64) return PKV_ERR_UNSUPPORTED;
@@ -315,7 +316,6 @@ pkv_status run(Args &a, float scale, size_t ws_bytes, int dtype, void *stream) {
     a.max_len = (int)((int64_t)a.max_len < (int64_t)a.maxb * a.B ? a.max_len : (int64_t)a.maxb * a.B);
     a.rows = (a.q_starts ? (a.max_q < a.T ? a.max_q : a.T) : 1) * a.H;
     a.bshift = a.B == 8 ? 3 : a.B == 16 ? 4 : a.B == 32 ? 5 : 6;
-    a.scale_log2 = scale * 1.4426950408889634f;
     a.err = device_error_word();
     const size_t need = workspace(a.T, a.H, a.V, a.max_len, dtype);
     if (need && (!a.ws || (reinterpret_cast<uintptr_t>(a.ws) & 255u) || ws_bytes < need)) return PKV_ERR_INVALID;

@@ -36,6 +36,24 @@ def test_multi_token(dtype, lens, nq, H, V, B):
     lc.check(lc.run(c), c)
 
 
+FAR = 10 ** 6  # a limit above the contexts: they are cut into shares and joined, however short
+
+
+@pytest.mark.parametrize("lens,H,V,B", [([1, 17, 33, 100], 4, 512, 16), ([64], 16, 512, 64), ([65, 63, 128], 3, 256, 32), ([0, 129, 0, 1, 700], 33, 512, 16),
+                                        ([40] * 9, 65, 256, 16), ([300, 2, 0], 128, 512, 8), ([130] * 170, 10, 256, 8)])
+def test_decode_cut(lens, H, V, B):
+    c = lc.make(lens, H, V, B)
+    lc.check(lc.run(c, max_len=FAR), c)
+
+
+@pytest.mark.parametrize("lens,nq,H,V,B", [([7], [7], 4, 512, 16), ([100, 33, 1], [5, 1, 1], 4, 512, 16), ([200], [130], 3, 256, 8),
+                                           ([64, 65], [64, 65], 1, 512, 64), ([300, 40], [9, 40], 33, 256, 32), ([90, 500], [64, 3], 128, 512, 16),
+                                           ([20, 30, 40], [0, 5, 0], 16, 512, 16), ([33] * 120, [1, 2, 0, 4] * 30, 16, 512, 16)])
+def test_multi_token_cut(lens, nq, H, V, B):
+    c = lc.make(lens, H, V, B, queries=nq)
+    lc.check(lc.run(c, max_len=FAR), c)
+
+
 def test_long_context_is_split_and_joined():
     for dtype, H in ((BF, 16), (F32, 2), (BF, 2)):
         c = lc.make([9000, 10], H, 512, 16, dtype, seed=3)
@@ -114,39 +132,42 @@ def test_empty_contexts_and_rows_of_no_query():
     lc.check(out[:6], c)
 
 
-def test_more_queries_than_tokens():
-    c = lc.make([3, 40], 4, queries=[3, 4])
-    # two more queries in front of the first sequence's: they see nothing
-    c["q"] = torch.cat([c["q"][:2], c["q"]])
-    c["starts"] = np.array([0, 5, 9], dtype=np.int32)
-    c["nq"] = [5, 4]
-    out = lc.run(c)
+@pytest.mark.parametrize("L,more,H", [(3, 2, 4), (3, 40, 4), (60, 70, 16), (700, 100, 5), (0, 50, 16), (0, 3, 2)])
+@pytest.mark.parametrize("max_len", [None, FAR])
+def test_more_queries_than_tokens(L, more, H, max_len):
+    c = lc.make([L, 40], H, queries=[L, 4])
+    # more queries in front of the first sequence's: they see nothing
+    r = torch.from_numpy(np.random.default_rng(8).standard_normal((more, H, 576)).astype(np.float32)).to(BF)
+    c["q"] = torch.cat([r, c["q"]])
+    c["starts"] = np.array([0, L + more, L + more + 4], dtype=np.int32)
+    c["nq"] = [L + more, 4]
+    out = lc.run(c, max_len=max_len)
     assert pkv.read_device_errors(clear=True) == pkv.DEVERR_SEQ_LEN
-    assert torch.all(out[:2] == 0)
+    assert torch.all(out[:more] == 0)
     lc.check(out, c)
 
 
-@pytest.mark.parametrize("queries", [None, [5, 3]])
-@pytest.mark.parametrize("dtype", [BF, F32])
-def test_what_is_not_seen_does_not_matter(dtype, queries):
+@pytest.mark.parametrize("queries", [None, [5, 3], [50, 70]])
+@pytest.mark.parametrize("dtype,max_len", [(BF, None), (F32, None), (BF, FAR)])
+def test_what_is_not_seen_does_not_matter(dtype, max_len, queries):
     """Other slots of the pool hold NaN, infinities, the largest and the lowest numbers: the same bits."""
     c = lc.make([77, 130], 6, 512, 16, dtype, queries, fill=0.0)
-    want = lc.run(c)
+    want = lc.run(c, max_len=max_len)
     for fill in (float("nan"), float("inf"), -float("inf"), torch.finfo(dtype).max, torch.finfo(dtype).min):
         d = lc.make([77, 130], 6, 512, 16, dtype, queries, fill=fill)
-        assert torch.equal(lc.run(d), want)
+        assert torch.equal(lc.run(d, max_len=max_len), want)
 
 
-@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dtype,max_len", [(BF, None), (F32, None), (BF, FAR)])
 @pytest.mark.parametrize("H", [1, 16, 40])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
-def test_a_bad_row_reaches_only_the_queries_that_see_it(dtype, H, bad):
+def test_a_bad_row_reaches_only_the_queries_that_see_it(dtype, max_len, H, bad):
     c = lc.make([70, 150, 20], H, 512, 16, dtype, queries=[10, 80, 20])
-    want = lc.run(c)
+    want = lc.run(c, max_len=max_len)
     pos, s = 110, 1  # token 110 of sequence 1, whose queries stand at 70 .. 149
     cache = c["cache"].clone()
     cache[int(c["tables"][s][pos // 16]), pos % 16, 33] = bad
-    got = lc.run(c, cache=cache.cuda())
+    got = lc.run(c, cache=cache.cuda(), max_len=max_len)
     first = c["starts"][s] + (pos - 70)
     keep = torch.ones(110, dtype=torch.bool)
     keep[first:c["starts"][s + 1]] = False
@@ -155,12 +176,13 @@ def test_a_bad_row_reaches_only_the_queries_that_see_it(dtype, H, bad):
     assert torch.all(~torch.isfinite(seen[..., 33]))
 
 
-def test_a_bad_query_stays_by_itself():
-    for queries in (None, [20, 30]):
+@pytest.mark.parametrize("max_len", [None, FAR])
+def test_a_bad_query_stays_by_itself(max_len):
+    for queries in (None, [20, 30], [2, 2]):
         c = lc.make([70, 150], 16, queries=queries)
-        want = lc.run(c)
+        want = lc.run(c, max_len=max_len)
         c["q"][1, 3] = float("nan")
-        got = lc.run(c)
+        got = lc.run(c, max_len=max_len)
         assert torch.all(torch.isnan(got[1, 3]))
         got[1, 3] = want[1, 3]
         assert torch.equal(got, want)
@@ -172,6 +194,7 @@ def test_scores_of_any_size(dtype, size):
     for queries in (None, [40, 3]):
         c = lc.make([150, 600], 9, 512, 16, dtype, queries, size=size)
         lc.check(lc.run(c), c)
+        lc.check(lc.run(c, max_len=FAR), c)
         lc.check(lc.run(c, scale=-0.1), c, scale=-0.1)
         lc.check(lc.run(c, scale=0.0), c, scale=0.0)
 

@@ -109,7 +109,7 @@ def test_attention_calls(call):
     assert call(P, maxL=-1) == bad and call(P, B=0) == bad and call(P, V=0) == bad
     assert call(P, H=129) == no and call(P, V=384) == no and call(P, V=1024) == no and call(P, B=12) == no
     assert call(P, dt=2) == no
-    for x in (NAN, INF):
+    for x in (NAN, INF, 3e38, -3e38):
         assert call(P, scale=x) == bad
     assert call(P, maxB=1 << 28) == bad                        # positions past 31 bits
     assert call(P, NB=1 << 28) == no                           # cache rows past 31 bits
