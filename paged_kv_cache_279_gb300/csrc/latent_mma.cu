@@ -710,8 +710,8 @@ pkv_status launch(Args a, cudaStream_t st) {
     using X = L<V, N>;
     CUtensorMap tm_q, tm_c0, tm_c1;
     const int64_t rows = (int64_t)a.NB * a.B;
-    if (!make_map(&tm_q, a.q, (int64_t)a.T * a.H, V, N, X::kChunks) || !make_map(&tm_c0, a.cache, rows, V, 8, X::kPart0) ||
-        !make_map(&tm_c1, a.cache, rows, V, 8, X::kChunks - X::kPart0))
+    if (!make_rows_map(&tm_q, a.q, (int64_t)a.T * a.H, V, N, X::kChunks) || !make_rows_map(&tm_c0, a.cache, rows, V, 8, X::kPart0) ||
+        !make_rows_map(&tm_c1, a.cache, rows, V, 8, X::kChunks - X::kPart0))
         return PKV_ERR_CUDA;
     // A decode of no more contexts than shares: the join's CTAs go by contexts, fewer than the shares.
     const int64_t contexts = (int64_t)a.S * ((a.H + N - 1) / N);

@@ -715,13 +715,7 @@ __global__ void __launch_bounds__(128 * SPLIT) latent_pair_join_kernel(const __g
 
 // The output's rows: boxes of 32 rows of 32 entries.
 bool make_out_map(CUtensorMap *map, void *out, int64_t rows, int V) {
-    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
-    if (!enc) return false;
-    cuuint64_t dims[2] = {(cuuint64_t)V, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)V * 2};
-    cuuint32_t box[2] = {32u, 32u}, estr[2] = {1u, 1u};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, out, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return make_map(map, out, MapShape{2, CU_TENSOR_MAP_SWIZZLE_64B, {(uint64_t)V, (uint64_t)rows, 0u}, {(uint64_t)V * 2, 0u}, {32u, 32u, 0u}});
 }
 
 template <int V>
@@ -732,8 +726,8 @@ pkv_status launch(Args a, cudaStream_t st) {
     if (pairs == 0 || !ensure_smem(latent_pair_kernel<V>, X::total, done)) return PKV_ERR_CUDA;
     CUtensorMap tm_q, tm_k0, tm_k1, tm_v, tm_o;
     const int64_t rows = (int64_t)a.NB * a.B;
-    if (!make_map(&tm_q, a.q, (int64_t)a.T * a.H, V, 64, X::kChunks) || !make_map(&tm_k0, a.cache, rows, V, 8, X::kPart0) ||
-        !make_map(&tm_k1, a.cache, rows, V, 8, X::kChunks - X::kPart0) || !make_map(&tm_v, a.cache, rows, V, 8, V / 128) ||
+    if (!make_rows_map(&tm_q, a.q, (int64_t)a.T * a.H, V, 64, X::kChunks) || !make_rows_map(&tm_k0, a.cache, rows, V, 8, X::kPart0) ||
+        !make_rows_map(&tm_k1, a.cache, rows, V, 8, X::kChunks - X::kPart0) || !make_rows_map(&tm_v, a.cache, rows, V, 8, V / 128) ||
         !make_out_map(&tm_o, a.out, (int64_t)a.T * a.H, V))
         return PKV_ERR_CUDA;
     // A decode of no more contexts than shares: the join's CTAs go by contexts.

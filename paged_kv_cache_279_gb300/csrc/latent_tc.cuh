@@ -341,18 +341,57 @@ inline int whole_contexts(const Args &a, int n, int tok, int shares) {
     return len <= (4 + 6 * contexts / shares) * tok ? (int)tiles : 0;
 }
 
-// Rows of V + 64 entries as [chunk of 64 entries][row][64]: a box of `box` rows and `deep` chunks.
-inline bool make_map(CUtensorMap *map, const void *base, int64_t rows, int V, int box, int deep) {
+// A tensor map takes the driver half a microsecond to encode; a call has three to six, of the same shapes in every step of
+// a serving loop.  The last few of a thread are kept by their shapes, and given this call's address.
+struct MapShape {
+    int dims, swizzle;
+    uint64_t size[3], stride[2];
+    uint32_t box[3];
+};
+inline bool make_map(CUtensorMap *map, void *base, const MapShape &sh) {
+    struct Kept {
+        MapShape shape;
+        CUtensorMap map;
+    };
+    constexpr unsigned kKept = 16;
+    static thread_local Kept kept[kKept];
+    static thread_local unsigned used = 0;
+    static const PFN_cuTensorMapReplaceAddress_v12000 replace = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapReplaceAddress", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+                        q == cudaDriverEntryPointSuccess;
+        return ok ? reinterpret_cast<PFN_cuTensorMapReplaceAddress_v12000>(p) : nullptr;
+    }();
+    if (replace)
+        for (unsigned i = 0; i < kKept && i < used; ++i) {
+            const MapShape &k = kept[i].shape;
+            if (k.dims == sh.dims && k.swizzle == sh.swizzle && k.size[0] == sh.size[0] && k.size[1] == sh.size[1] && k.size[2] == sh.size[2] &&
+                k.stride[0] == sh.stride[0] && k.stride[1] == sh.stride[1] && k.box[0] == sh.box[0] && k.box[1] == sh.box[1] &&
+                k.box[2] == sh.box[2]) {
+                *map = kept[i].map;
+                return replace(map, base) == CUDA_SUCCESS;
+            }
+        }
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (!enc) return false;
-    const int chunks = V / 64 + 1;
-    cuuint64_t dims[3] = {64u, (cuuint64_t)rows, (cuuint64_t)chunks};
-    cuuint64_t strides[2] = {(cuuint64_t)(V + kRope) * 2, 128u};
-    cuuint32_t boxd[3] = {64u, (cuuint32_t)box, (cuuint32_t)deep};
-    cuuint32_t estr[3] = {1u, 1u, 1u};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, boxd, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint64_t size[3] = {sh.size[0], sh.size[1], sh.size[2]}, stride[2] = {sh.stride[0], sh.stride[1]};
+    const cuuint32_t step[3] = {1u, 1u, 1u};
+    if (enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)sh.dims, base, size, stride, sh.box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            (CUtensorMapSwizzle)sh.swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return false;
+    Kept &k = kept[used++ % kKept];
+    if (used >= 2 * kKept) used -= kKept;
+    k.shape = sh;
+    k.map = *map;
+    return true;
+}
+
+// Rows of V + 64 entries as [chunk of 64 entries][row][64]: a box of `box` rows and `deep` chunks.
+inline bool make_rows_map(CUtensorMap *map, const void *base, int64_t rows, int V, int box, int deep) {
+    return make_map(map, const_cast<void *>(base),
+                    MapShape{3, CU_TENSOR_MAP_SWIZZLE_128B, {64u, (uint64_t)rows, (uint64_t)(V / 64 + 1)}, {(uint64_t)(V + kRope) * 2, 128u},
+                             {64u, (uint32_t)box, (uint32_t)deep}});
 }
 
 }  // namespace latent
