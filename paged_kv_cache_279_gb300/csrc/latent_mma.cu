@@ -87,7 +87,7 @@ struct L {
     static constexpr int kQBufs = N <= 32 ? 2 : 1;  // the next piece's queries are loaded under this one's, where they fit
     static constexpr int kP = kTok * 128;
     // softmax warps: four for each 32 rows of 64 (a tile of 64 rows keeps four busy for 1000 cycles), else four
-    static constexpr int kSets = N == 64 ? 2 : 1, kCols1 = N / kSets, kSoftmax = 128 * kSets;
+    static constexpr int kSets = N >= 32 ? 2 : 1, kCols1 = N / kSets, kSoftmax = 128 * kSets;
     static constexpr int kThreads = 96 + kSoftmax;  // and a producer, and a warp that issues each product
     static constexpr int kMisc = 3072;
     static constexpr int kMax = 232448;  // shared memory of a CTA
