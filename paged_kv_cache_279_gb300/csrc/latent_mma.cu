@@ -178,7 +178,7 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         int tile = 0, np = 0, nq = 0, halves = 0;  // tiles, pieces, queries and parts of tiles issued
         for (;;) {
             const int d = np % kDescs;
-            if (np >= kDescs) wait(&m.desc_empty[d], (uint32_t)(np / kDescs + 1) & 1u);
+            wait(&m.desc_empty[d], (uint32_t)(np / kDescs + 1) & 1u);
             Piece pc;
             const bool more = !dead && sh.take(a, pc);
             if (!more) pc.tiles = 0;
@@ -199,7 +199,7 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             };
             auto load_q = [&] {
                 const int qb = np % X::kQBufs;
-                if (np >= X::kQBufs) wait(&m.q_empty[qb], (uint32_t)(np / X::kQBufs + 1) & 1u);
+                wait(&m.q_empty[qb], (uint32_t)(np / X::kQBufs + 1) & 1u);
                 if (dead) return;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(&m.q_full[qb], (uint32_t)X::kQ);
@@ -220,7 +220,7 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 // a group without tokens starts past the tensor's end: zeros
                 const int y = row >= 0 ? row : a.NB << a.bshift;
                 const uint32_t dst = smem_u32(smem + X::ring) + (uint32_t)(st * X::kTile + (lane & 7) * X::kGroup);
-                if (tile >= X::kStages) wait(&m.empty[0][st], (uint32_t)(tile / X::kStages + 1) & 1u);
+                wait(&m.empty[0][st], (uint32_t)(tile / X::kStages + 1) & 1u);
                 if (dead) break;
                 if (turn && row == -1) flag_error(a.err, PKV_DEVERR_BLOCK_ID);
                 const uint32_t ok = __ballot_sync(0xffffffffu, row >= 0) >> (8 * (t & 3)) & 0xffu;
@@ -231,7 +231,7 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 __syncwarp();
                 if (turn) tma_load_3d(dst, &tm_c0, smem_u32(&m.full[0][st]), 0, y, 0);
                 ++halves;
-                if (tile >= X::kStages) wait(&m.empty[1][st], (uint32_t)(tile / X::kStages + 1) & 1u);
+                wait(&m.empty[1][st], (uint32_t)(tile / X::kStages + 1) & 1u);
                 if (dead) break;
                 if (lane == 0) mbar_arrive_expect_tx(&m.full[1][st], (uint32_t)(X::kTile - kTok * 128 * X::kPart0));
                 __syncwarp();
