@@ -140,7 +140,8 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     grid_dependency_wait();
-    grid_launch_dependents();  // the join kernel; it waits for this one before it reads
+    // the join kernel, which waits for this one before it reads (no other: attention kernels read queries before they wait)
+    if (!a.whole) grid_launch_dependents();
     prefetch_tables(a, (int64_t)threadIdx.x * gridDim.x + blockIdx.x);
     Share<kRows, kTok> sh = locate<kRows, kTok>(a, &m.red[0][0], pair, pairs, kThreads);
     const Ws ws = ws_of(a, pairs, V);

@@ -313,6 +313,29 @@ def test_pairs_on_streams_in_graphs_and_beside_each_other():
     lc.check(outs[2], dict(c, lens=[x - 1 for x in c["lens"]], rows=[x[:-1] for x in c["rows"]]))
 
 
+@pytest.mark.parametrize("dtype,NB", [(BF, 480000), (F32, 250000)])
+@pytest.mark.parametrize("queries,H", [(None, 16), ([70, 3], 16)])
+def test_a_pool_past_32_bits(dtype, NB, queries, H):
+    """Blocks whose entries lie past 2^31 (float32) and 2^32 (bf16) entries of the pool: the results of a small pool, bit for bit."""
+    c = lc.make([90, 130], H, dtype=dtype, queries=queries)
+    want = lc.run(c)
+    cache = torch.empty((NB, 16, 576), dtype=dtype, device="cuda")
+    n = c["cache"].shape[0]
+    cache[NB - n:] = c["cache"].cuda()
+    cache[:n] = float("nan")  # where an offset cut to 32 bits might lead
+    assert torch.equal(lc.run(dict(c, tables=c["tables"] + (NB - n)), cache=cache), want)
+    # and rows written there
+    src = c["rows"][1].cuda()
+    f, at = pkv.rotary_frequencies(64, device="cuda"), torch.zeros(130, dtype=torch.int32, device="cuda")
+    slots = torch.from_numpy(c["tables"][1].astype(np.int64)).cuda()[torch.arange(130, device="cuda") // 16] + (NB - n)
+    slots = slots * 16 + torch.arange(130, device="cuda") % 16
+    held = cache[NB - n:].clone()
+    cache[NB - n:] = float("nan")
+    pkv.latent_cache_write(src[:, :512], src[:, 512:], cache, slots, at, f)  # positions 0: rows as they are
+    assert torch.equal(cache.view(-1, 576)[slots], src)
+    assert torch.equal(held.view(-1, 576)[slots - (NB - n) * 16], src)
+
+
 def test_an_output_16_bytes_off_a_sector():
     for queries in (None, [20, 9]):
         c = lc.make([300, 77], 16, queries=queries)

@@ -143,6 +143,19 @@ def test_latent_write(dtype, T, H, V, B):
         assert torch.all(q[..., :V] == 3.0)
 
 
+def test_a_cache_past_32_bits():
+    NB, Hkv, B, D, T = 140000, 8, 16, 128, 40  # 2.3e9 entries each
+    kv = _rows((T, 2 * Hkv, D), BF, 5).cuda()
+    ps, f = torch.arange(T, dtype=torch.int32, device="cuda"), pkv.rotary_frequencies(D, device="cuda")
+    kc, vc = (torch.empty((NB, Hkv, B, D), dtype=BF, device="cuda") for _ in range(2))
+    kc[-4:], vc[-4:] = 7.0, 7.0
+    small = [torch.full((4, Hkv, B, D), 7.0, dtype=BF, device="cuda") for _ in range(2)]
+    at = torch.randperm(4 * B, device="cuda")[:T]
+    pkv.kv_cache_write_rotary(kv[:, :Hkv], kv[:, Hkv:], *small, at, ps, f)
+    pkv.kv_cache_write_rotary(kv[:, :Hkv], kv[:, Hkv:], kc, vc, at + (NB - 4) * B, ps, f)
+    assert torch.equal(kc[-4:], small[0]) and torch.equal(vc[-4:], small[1])
+
+
 def test_bad_slots_are_flagged_and_skipped():
     T, Hkv, B, NB = 6, 2, 16, 2
     k = _rows((T, Hkv, 64), BF, 1).cuda()
