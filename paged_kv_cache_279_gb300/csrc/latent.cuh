@@ -23,6 +23,7 @@ struct Args {
     int S, T, H, V, B, bshift, maxb, NB, max_q, max_len;
     int rows;                // most query rows of a sequence, at most T * H
     int whole;               // > 0: no context is cut, share id is row tile id % whole of sequence id / whole
+    int once;                // the cache's rows are the first to leave L2
     float scale_log2;        // scale * log2(e)
 };
 

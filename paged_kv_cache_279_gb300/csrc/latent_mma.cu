@@ -176,6 +176,7 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 
     if (warp == 0) {
         // ======================= producer =======================
+        const uint64_t policy = row_policy(a);
         int tile = 0, np = 0, nq = 0, halves = 0;  // tiles, pieces, queries and parts of tiles issued
         for (;;) {
             const int d = np % kDescs;
@@ -230,13 +231,13 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     mbar_arrive_expect_tx(&m.full[0][st], (uint32_t)(kTok * 128 * X::kPart0));
                 }
                 __syncwarp();
-                if (turn) tma_load_3d(dst, &tm_c0, smem_u32(&m.full[0][st]), 0, y, 0);
+                if (turn) tma_load_3d_hint(dst, &tm_c0, smem_u32(&m.full[0][st]), 0, y, 0, policy);
                 ++halves;
                 wait(&m.empty[1][st], (uint32_t)(tile / X::kStages + 1) & 1u);
                 if (dead) break;
                 if (lane == 0) mbar_arrive_expect_tx(&m.full[1][st], (uint32_t)(X::kTile - kTok * 128 * X::kPart0));
                 __syncwarp();
-                if (turn) tma_load_3d(dst + X::kPart0 * 1024, &tm_c1, smem_u32(&m.full[1][st]), 0, y, X::kPart0);
+                if (turn) tma_load_3d_hint(dst + X::kPart0 * 1024, &tm_c1, smem_u32(&m.full[1][st]), 0, y, X::kPart0, policy);
                 ++halves;
                 if (X::kQBufs == 1 && t == 0) load_q();
             }
@@ -718,6 +719,7 @@ pkv_status launch(Args a, cudaStream_t st) {
     const int64_t contexts = (int64_t)a.S * ((a.H + N - 1) / N);
     const int by_context = !a.q_starts && contexts <= sms;
     a.whole = whole_contexts(a, N, kTok, sms);
+    a.once = read_once(a, N);
     const unsigned grid = a.whole ? (unsigned)(a.S * a.whole) : (unsigned)sms;
     const pkv_status rc = launch_pdl(latent_mma_kernel<V, N>, dim3(grid), dim3(X::kThreads), (size_t)X::total, st, tm_q, tm_c0, tm_c1, a,
                                      by_context);

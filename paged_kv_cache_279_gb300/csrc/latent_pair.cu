@@ -168,6 +168,7 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 
     if (warp == 0) {
         // ======================= producer of pieces, Q and the rows by tokens =======================
+        const uint64_t policy = row_policy(a);
         int tile = 0, np = 0, nq = 0, nk = 0;  // tiles, pieces, queries and parts issued
         for (;;) {
             const int d = np % kDescs;
@@ -213,8 +214,8 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     }
                     __syncwarp();
                     if (mine)
-                        tma_load_3d(smem_u32(smem + X::k) + (uint32_t)((lane & 7) * X::kGroupK + h * X::kPart0 * 1024), h ? &tm_k1 : &tm_k0,
-                                    smem_u32(&m.k_full[h]), 0, row >= 0 ? row : none, h * X::kPart0);
+                        tma_load_3d_hint(smem_u32(smem + X::k) + (uint32_t)((lane & 7) * X::kGroupK + h * X::kPart0 * 1024), h ? &tm_k1 : &tm_k0,
+                                    smem_u32(&m.k_full[h]), 0, row >= 0 ? row : none, h * X::kPart0, policy);
                     ++nk;
                 }
             }
@@ -229,6 +230,7 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         if (nq > 0) mbar_wait_bounded(&m.q_full, (uint32_t)(nq - 1) & 1u);
     } else if (warp == 3) {
         // ======================= producer of the rows by entries =======================
+        const uint64_t policy = row_policy(a);
         int tile = 0, nv = 0;
         for (int np = 0;; ++np) {
             const int d = np % kDescs;
@@ -250,8 +252,8 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     if (lane == 0) mbar_arrive_expect_tx(&m.v_full[h], (uint32_t)(X::kV / 2));
                     __syncwarp();
                     if (turn && ((lane >> 3) & 1) == h)
-                        tma_load_3d(smem_u32(smem + X::v) + (uint32_t)((lane & 15) * X::kGroupV), &tm_v, smem_u32(&m.v_full[h]), 0,
-                                    row >= 0 ? row : none, (int)rank * (V / 128));
+                        tma_load_3d_hint(smem_u32(smem + X::v) + (uint32_t)((lane & 15) * X::kGroupV), &tm_v, smem_u32(&m.v_full[h]), 0,
+                                    row >= 0 ? row : none, (int)rank * (V / 128), policy);
                     ++nv;
                 }
             }
@@ -734,6 +736,7 @@ pkv_status launch(Args a, cudaStream_t st) {
     // A decode of no more contexts than shares: the join's CTAs go by contexts.
     const int by_context = !a.q_starts && a.S <= pairs;
     a.whole = whole_contexts(a, kRows, kTok, pairs);
+    a.once = read_once(a, kRows);
     const unsigned ctas = 2 * (a.whole ? (unsigned)(a.S * a.whole) : (unsigned)pairs);
     const pkv_status rc = launch_pdl(latent_pair_kernel<V>, dim3(ctas), dim3(kThreads), (size_t)X::total, st, tm_q, tm_k0, tm_k1,
                                      tm_v, tm_o, a, by_context);
