@@ -243,7 +243,7 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             }
             if (lane == 0) {
                 if (a.whole) {
-                } else if (by_context && pc.out != 2) leave(ws.rec + 4 * (pc.seq * sh.w.R + sh.w.k), pc.row0, pc.rows, pc.out ? sh.reach(cta) : 0, cta);
+                } else if (by_context && pc.out != 2) leave(ws.rec + 4 * pc.seq, pc.row0, pc.rows, pc.out ? sh.reach(cta) : 0, cta);
                 else if (pc.out == 1) leave(ws.rec + 4 * cta, pc.row0, pc.rows, sh.reach(cta), cta);
             }
             ++np;
@@ -347,6 +347,7 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         const int col = set * NL + 2 * (lane & 3), tok0 = qt * 16 + (lane >> 2);  // first column, first token (the other: 8 on)
         // stmatrix: lane gives the address of row (lane & 7) of matrix lane >> 3: tokens 0-7, 8-15 of column block j, then j + 1
         const uint32_t p_s = smem_u32(smem + X::p) + (uint32_t)((qt * 2 + ((lane >> 3) & 1)) * 1024 + (lane & 7) * 128);
+        if (sh.blind) zero_blind<N, kTok>(a, cta, G, threadIdx.x - 96, X::kSoftmax, by_context ? ws.rec : nullptr);
         int tile = 0;
         bool stop = false;  // the softmax warps leave together: they share a barrier
         for (int np = 0;; ++np) {
@@ -615,18 +616,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) latent_mma_join_kernel(const 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Ws ws = ws_of(a, shares, N, V);
     int4 rec = *reinterpret_cast<const int4 *>(ws.rec + 4 * blockIdx.x);
-    zero_blind<N, kTok>(a, blockIdx.y * gridDim.x + blockIdx.x, gridDim.x * gridDim.y, kJoinWarps * 32);
-    if (by_context) {
-        Walk<N, kTok> w;
-        const int R = (a.H + N - 1) / N, s = blockIdx.x / R, k = blockIdx.x - s * R;
-        w.open(a, s);
-        if (w.k0 >= w.R) return;  // a context without tokens leaves nothing
-        rec.x = s * a.H + k * N, rec.y = min(N, a.H - k * N);
-    }
+    if (by_context) rec.x = blockIdx.x * a.H, rec.y = a.H;  // (whatever a wait that ran out kept from being left)
     constexpr int kRowUnits = N / 16;
     const int g = warp % SPLIT, work = blockIdx.y * (kJoinWarps / SPLIT) + warp / SPLIT, unit = work / kRowUnits, r0 = work % kRowUnits * 16;
     const int n = rec.z, rows = rec.y - r0, c = rec.w;
-    if (n <= 0 || c < 0 || c > shares - n) return;  // (after a wait that ran out a record may not have been left)
+    if (n <= 0 || c < 0 || c > shares - n) return;
     const int col = r0 + 2 * (lane & 3);
     float top[4], sum[4] = {}, o[8] = {};  // [2 j + i]: row col + 8 j + i
 #pragma unroll
@@ -716,8 +710,7 @@ pkv_status launch(Args a, cudaStream_t st) {
         !make_rows_map(&tm_c1, a.cache, rows, V, 8, X::kChunks - X::kPart0))
         return PKV_ERR_CUDA;
     // A decode of no more contexts than shares: the join's CTAs go by contexts, fewer than the shares.
-    const int64_t contexts = (int64_t)a.S * ((a.H + N - 1) / N);
-    const int by_context = !a.q_starts && contexts <= sms;
+    const int by_context = !a.q_starts && a.S <= sms;
     a.whole = whole_contexts(a, N, kTok, sms);
     a.once = read_once(a, N);
     const unsigned grid = a.whole ? (unsigned)(a.S * a.whole) : (unsigned)sms;
@@ -725,9 +718,9 @@ pkv_status launch(Args a, cudaStream_t st) {
                                      by_context);
     if (rc != PKV_OK || a.whole) return rc;
     constexpr unsigned kUnits = V * N / 256;
-    const unsigned cuts = by_context ? (unsigned)contexts : (unsigned)sms;
+    const unsigned cuts = by_context ? (unsigned)a.S : (unsigned)sms;
     // (pieces of a context: about shares / contexts)
-    if (by_context && contexts * 4 < sms)
+    if (by_context && a.S * 4 < sms)
         return launch_pdl(latent_mma_join_kernel<V, N, 4>, dim3(cuts, kUnits * 4 / kJoinWarps), dim3(kJoinWarps * 32), 0, st, a, sms, by_context);
     return launch_pdl(latent_mma_join_kernel<V, N, 1>, dim3(cuts, kUnits / kJoinWarps), dim3(kJoinWarps * 32), 0, st, a, sms, by_context);
 }

@@ -392,6 +392,7 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const int p_chunk = 4 * q2;
         const uint32_t p_full = at_rank(&m.p_full, 0), o_free = at_rank(&m.o_free, 0);
         const uint32_t s_free[2] = {at_rank(&m.s_free[0], 0), at_rank(&m.s_free[1], 0)};
+        if (sh.blind && lead) zero_blind<kRows, kTok>(a, pair, pairs, threadIdx.x - 128, kSoftmax, by_context ? ws.rec : nullptr);
         int tile = 0;
         bool stop = false;  // the four warps leave together: they share a barrier
         for (int np = 0;; ++np) {
@@ -641,17 +642,10 @@ __global__ void __launch_bounds__(128 * SPLIT) latent_pair_join_kernel(const __g
     grid_dependency_wait();
     const Ws ws = ws_of(a, shares, V);
     int4 rec = *reinterpret_cast<const int4 *>(ws.rec + 4 * blockIdx.x);
-    zero_blind<kRows, kTok>(a, blockIdx.y * gridDim.x + blockIdx.x, gridDim.x * gridDim.y, 128 * SPLIT);
-    if (by_context) {  // (one row tile a sequence: at most 128 heads)
-        Walk<kRows, kTok> w;
-        w.open(a, blockIdx.x);
-        if (w.k0 >= w.R) return;  // a context without tokens leaves nothing
-        rec.x = blockIdx.x * a.H, rec.y = a.H;
-    }
+    if (by_context) rec.x = blockIdx.x * a.H, rec.y = a.H;  // (whatever a wait that ran out kept from being left)
     const int rank = blockIdx.y & 1, at = blockIdx.y >> 1, g = threadIdx.x >> 7, me = threadIdx.x & 127;
     const int row = me & 63, half = me >> 6, r = 64 * rank + row;
     const int n = rec.z, c = rec.w;
-    // (after a wait that ran out a record may not have been left)
     if (n <= 0 || c < 0 || c > shares - n || 64 * rank >= rec.y) return;
     float top = -INFINITY, sum = 0.f, o[16] = {};
     for (int k0 = 2 * g; k0 < n; k0 += 2 * SPLIT) {

@@ -183,7 +183,8 @@ struct Share {
     Walk<N, TOK> w;
     int64_t off, left, last, total;
     int parts;
-    bool over;  // the context of w has been handed out
+    bool over;   // the context of w has been handed out
+    bool blind;  // some sequence s with s mod `most` = id has queries that see nothing
 
     int after;  // tiles of the last piece's context behind it
 
@@ -223,12 +224,12 @@ struct Share {
     __device__ __forceinline__ int reach(int id) const { return (int)(share_owner(last + after - 1, total, parts) - id) + 1; }
 };
 
-// Zeros for a sequence's queries that see nothing, but for those in a row tile with others; by a block of `threads`.
+// Zeros for a sequence's queries that see nothing, but for those in a row tile with others; by thread `me` of `threads`.
 template <int N, int TOK>
-__device__ __forceinline__ void zero_blind(const Args &a, const Walk<N, TOK> &w, int threads) {
+__device__ __forceinline__ void zero_blind(const Args &a, const Walk<N, TOK> &w, int me, int threads) {
     const int64_t vecs = min((int64_t)w.k0 * N, (int64_t)w.nH) * (a.V / 8);
     uint4 *o = reinterpret_cast<uint4 *>((unsigned char *)a.out + (int64_t)w.q0 * a.H * a.V * 2);
-    for (int64_t i = threadIdx.x; i < vecs; i += threads) o[i] = make_uint4(0, 0, 0, 0);
+    for (int64_t i = me; i < vecs; i += threads) o[i] = make_uint4(0, 0, 0, 0);
 }
 
 // Share `id` of at most `most`: each of the block's `threads` threads sums the tiles of a run of sequences, and
@@ -242,17 +243,18 @@ __device__ __forceinline__ Share<N, TOK> locate(const Args &a, float *scratch, i
     const int run = (a.S + threads - 1) / threads;
     const int sb = min(a.S, (int)threadIdx.x * run), se = min(a.S, sb + run);
     int64_t mine = 0;
+    bool blind = false;
     Share<N, TOK> r;
     Walk<N, TOK> &w = r.w;
     if (a.whole) {
         const int s = id / a.whole, k = id - s * a.whole;
         r.off = r.left = r.last = r.total = r.parts = 0;
-        r.over = false;
+        r.over = r.blind = false;
         if (s >= a.S) return r;
         w.open(a, s);
         if (k == 0) {
             if (w.flagged && threadIdx.x == 0) flag_error(a.err, PKV_DEVERR_SEQ_LEN);
-            zero_blind(a, w, threads);
+            zero_blind(a, w, threadIdx.x, threads);
         }
         w.k = k;
         if (k >= w.k0 && k < w.R) r.left = w.tiles(a, k) + kHead;
@@ -261,7 +263,10 @@ __device__ __forceinline__ Share<N, TOK> locate(const Args &a, float *scratch, i
     for (int s = sb; s < se; ++s) {
         w.open(a, s);
         mine += w.total(a);
-        if (w.flagged && s % most == id) flag_error(a.err, PKV_DEVERR_SEQ_LEN);
+        if ((w.flagged || w.k0 > 0) && s % most == id) {
+            if (w.flagged) flag_error(a.err, PKV_DEVERR_SEQ_LEN);
+            blind |= w.k0 > 0;
+        }
     }
     int64_t incl = mine;
     for (int d = 1; d < 32; d <<= 1) {
@@ -269,7 +274,7 @@ __device__ __forceinline__ Share<N, TOK> locate(const Args &a, float *scratch, i
         if (lane >= d) incl += y;
     }
     if (lane == 31) scan[warp] = incl;
-    __syncthreads();
+    r.blind = __syncthreads_or(blind);
     int64_t base = 0, total = 0;
     for (int i = 0; i < threads / 32; ++i) {
         if (i < warp) base += scan[i];
@@ -325,13 +330,15 @@ __device__ __forceinline__ void leave(int *rec, int row0, int rows, int pieces, 
     *reinterpret_cast<int4 *>(rec) = make_int4(row0, rows, pieces, share);
 }
 
-// The same, sequence after sequence.
+// The same for sequences first, first + step, ...; and, where `rec` has a record for each context, those of sequences without
+// tokens: nothing to join.
 template <int N, int TOK>
-__device__ __forceinline__ void zero_blind(const Args &a, int first, int step, int threads) {
+__device__ __forceinline__ void zero_blind(const Args &a, int first, int step, int me, int threads, int *rec) {
     for (int s = first; s < a.S; s += step) {
         Walk<N, TOK> w;
         w.open(a, s);
-        zero_blind(a, w, threads);
+        zero_blind(a, w, me, threads);
+        if (rec && me == 0 && w.k0 >= w.R) leave(rec + 4 * s, 0, 0, 0, 0);
     }
 }
 
