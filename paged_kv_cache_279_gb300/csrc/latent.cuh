@@ -23,6 +23,8 @@ struct Args {
     int S, T, H, V, B, bshift, maxb, NB, max_q, max_len;
     int rows;                // most query rows of a sequence, at most T * H
     int whole;               // > 0: no context is cut, share id is row tile id % whole of sequence id / whole
+    uint32_t hmul;           // x / H = x * hmul >> hshift for x < 2^31
+    int hshift;
     int once;                // the cache's rows are the first to leave L2
     float scale_log2;        // scale * log2(e)
 };
@@ -55,6 +57,9 @@ __device__ __forceinline__ Seq sequence(const Args &a, int s) {
     if (r.n != r.n0 || r.n0 > r.L) r.flagged = true;
     return r;
 }
+
+// x / H, 0 <= x < 2^31: with l = ceil(log2 H), hmul = floor(2^(31 + l) / H) + 1 passes 2^(31 + l) / H by at most 2^l / H.
+__device__ __forceinline__ int by_heads(const Args &a, int x) { return (int)((uint64_t)(uint32_t)x * a.hmul >> a.hshift); }
 
 // bf16 on the tensor cores: workspace of a call, and the call, its arguments checked.  run_mma: row tiles of up to
 // 64 rows; run_pair: of 128.

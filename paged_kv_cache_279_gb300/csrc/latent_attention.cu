@@ -316,6 +316,10 @@ pkv_status run(Args &a, float scale, size_t ws_bytes, int dtype, void *stream) {
     a.max_len = (int)((int64_t)a.max_len < (int64_t)a.maxb * a.B ? a.max_len : (int64_t)a.maxb * a.B);
     a.rows = (a.q_starts ? (a.max_q < a.T ? a.max_q : a.T) : 1) * a.H;
     a.bshift = a.B == 8 ? 3 : a.B == 16 ? 4 : a.B == 32 ? 5 : 6;
+    int l = 0;
+    while (1 << l < a.H) ++l;
+    a.hshift = 31 + l;
+    a.hmul = (uint32_t)(((1ull << a.hshift) / (unsigned)a.H) + 1);
     a.err = device_error_word();
     const size_t need = workspace(a.T, a.H, a.V, a.max_len, dtype);
     if (need && (!a.ws || (reinterpret_cast<uintptr_t>(a.ws) & 255u) || ws_bytes < need)) return PKV_ERR_INVALID;

@@ -359,7 +359,7 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             float nref[J][2], l[J][2];  // minus the reference: +inf before the first score
 #pragma unroll
             for (int j = 0; j < J; ++j) nref[j][0] = nref[j][1] = INFINITY, l[j][0] = l[j][1] = 0.f;
-            if (threadIdx.x - 96 < N) m.lim[threadIdx.x - 96] = min(pc.end, pc.lim0 + (pc.qh0 + (int)threadIdx.x - 96) / a.H);
+            if (threadIdx.x - 96 < N) m.lim[threadIdx.x - 96] = min(pc.end, pc.lim0 + by_heads(a, pc.qh0 + (int)threadIdx.x - 96));
             softmax_sync<X::kSoftmax>();
             const int least = m.lim[0];  // tokens that the first row sees
             for (int t = 0; t < pc.tiles; ++t, ++tile) {

@@ -91,9 +91,8 @@ __device__ __forceinline__ uint32_t at_rank(const void *p, uint32_t rank) {
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void mma2(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
@@ -139,6 +138,8 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&m.tmem)), "r"(X::kCols) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
+    __syncwarp();
+    cluster_arrive();  // both CTAs' barriers are set up (awaited below)
     grid_dependency_wait();
     // the join kernel, which waits for this one before it reads (no other: attention kernels read queries before they wait)
     if (!a.whole) grid_launch_dependents();
@@ -148,7 +149,7 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     if (lead && threadIdx.x == 0 && !by_context && !a.whole) leave(ws.rec + 4 * pair, 0, 0, 0, 0);
     tc::fence_before();
     __syncthreads();
-    cluster_sync();  // both CTAs' barriers are set up
+    cluster_wait();
     tc::fence_after();
     const uint32_t tmem = m.tmem;
 
@@ -404,8 +405,8 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             float nref = INFINITY;       // minus the reference: +inf before the first score
             uint64_t l2 = f32x2(0.f, 0.f);  // sums of the weights of even and odd tokens
             const int r = 64 * (int)rank + row;
-            const int least = pc.lim0 + pc.qh0 / a.H;                     // tokens that the first row sees
-            const int lim = min(pc.end, pc.lim0 + (pc.qh0 + r) / a.H);    // that this row sees
+            const int least = pc.lim0 + by_heads(a, pc.qh0);                     // tokens that the first row sees
+            const int lim = min(pc.end, pc.lim0 + by_heads(a, pc.qh0 + r));    // that this row sees
             for (int t = 0; t < pc.tiles; ++t, ++tile) {
                 wait(&m.meta[tile & 3], (uint32_t)(tile >> 2) & 1u);
                 wait(&m.s_full[tile & 1], (uint32_t)(tile >> 1) & 1u);
@@ -626,7 +627,8 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     }
     tc::fence_before();
     __syncthreads();
-    cluster_sync();  // nothing arrives at a CTA that is gone
+    cluster_arrive();
+    cluster_wait();  // nothing arrives at a CTA that is gone
     if (warp == 1) {
         tc::fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(X::kCols) : "memory");

@@ -154,19 +154,19 @@ struct Walk {
     __device__ __forceinline__ int end(const Args &a, int kk) const {  // tokens row tile kk sees
         if (!a.q_starts) return L;
         const int last = min((kk + 1) * N, nH) - 1;
-        return min(L, p0 + 1 + last / a.H);
+        return min(L, p0 + 1 + by_heads(a, last));
     }
     __device__ __forceinline__ int tiles(const Args &a, int kk) const { return (end(a, kk) + TOK - 1) / TOK; }
     // tiles, heads included, of row tiles k0 .. kk - 1, kk < R
     __device__ __forceinline__ int64_t before(const Args &a, int kk) const {
         if (kk <= k0) return 0;
-        const int64_t m = (int64_t)TOK / N * a.H;  // N divides TOK
+        constexpr int kPer = TOK / N;  // (N divides TOK)
         const int64_t c = (N - 1 + (int64_t)a.H * (p0 + TOK)) >> (N == 16 ? 4 : N == 32 ? 5 : N == 64 ? 6 : 7);  // floor: p0 may be below -TOK
-        return G(kk + c, m) - G(k0 + c, m) + (int64_t)kHead * (kk - k0);
+        return G(a, kk + c, kPer) - G(a, k0 + c, kPer) + (int64_t)kHead * (kk - k0);
     }
-    static __device__ __forceinline__ int64_t G(int64_t x, int64_t m) {  // sum of floor(j / m), j < x
-        // (32-bit division is a fifth of the time)
-        const int64_t q = (uint64_t)x < (1ull << 32) && m < (1ll << 31) ? (int64_t)((uint32_t)x / (uint32_t)m) : x / m;
+    static __device__ __forceinline__ int64_t G(const Args &a, int64_t x, int per) {  // sum of floor(j / m), j < x, m = per H
+        const int64_t y = x / per, m = (int64_t)per * a.H;
+        const int64_t q = (uint64_t)y < (1ull << 31) ? by_heads(a, (int)y) : y / a.H;
         return m * (q * (q - 1) / 2) + q * (x - q * m);
     }
     __device__ __forceinline__ int64_t total(const Args &a) const {
