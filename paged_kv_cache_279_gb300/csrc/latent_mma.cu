@@ -24,9 +24,12 @@
 // All contexts' tiles are laid end to end and cut into equal shares, one a CTA.  A
 // context cut by share boundaries leaves partial results that a second kernel joins.
 //
-// What bounds it: DRAM while tiles stream (5 TB/s of 6.7), before that a chain of loads
-// (lengths, block table, first tile: 3.8 us), after it the join (5 us).  64 contexts of 64
-// to 2048 tokens, 32 heads: 29.0 us for 73 MB; 8 of 16000, 64 heads: 46.6 us for 149 MB.
+// What bounds it: DRAM while tiles stream (what 32000 tokens more a context cost, 8 contexts: 6.7 TB/s at 16 and 32 rows,
+// 6.3 at 64, of 6.7), before that a chain of loads (lengths, block table, first tile: 3.2 us until it is asked for), after
+// it the join (1.2 us between the kernels, 4 in it).  64 contexts of 64 to 2048 tokens, 32 heads: 26.5 us for 73 MB; 8 of
+// 16000, 64 heads: 42.5 us for 149 MB.  Joined in this kernel, by CTAs that wait for one another's pieces, one context of
+// 16000 took 20.0 us, not 22.7, but these 26.7 and 43.7 (from a host's stream of calls 1 to 2 us more: such a launch is a
+// cooperative one).
 // A tile takes 36 + 16 products, 1452 cycles at 16 rows, 1920 at 64 (operand bytes out of
 // shared memory); 3200 is its share of DRAM.
 #include <cmath>

@@ -314,7 +314,7 @@ def test_pairs_on_streams_in_graphs_and_beside_each_other():
 
 
 @pytest.mark.parametrize("dtype,NB", [(BF, 480000), (F32, 250000)])
-@pytest.mark.parametrize("queries,H", [(None, 16), ([70, 3], 16)])
+@pytest.mark.parametrize("queries,H", [(None, 16), (None, 100), ([70, 3], 16)])
 def test_a_pool_past_32_bits(dtype, NB, queries, H):
     """Blocks whose entries lie past 2^31 (float32) and 2^32 (bf16) entries of the pool: the results of a small pool, bit for bit."""
     c = lc.make([90, 130], H, dtype=dtype, queries=queries)
