@@ -619,6 +619,12 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, factor: float = 1
 # under lru_cache see sizes alone, never a tensor, and give what the library's call takes of them.  Types, devices and
 # addresses are looked at in every call.
 _plans = functools.lru_cache(maxsize=4096)
+_codes = {torch.float32: PKV_F32, torch.bfloat16: PKV_BF16}
+
+
+def _code(t) -> int:
+    code = _codes.get(t.dtype)
+    return _dtype_code(t) if code is None else code
 
 
 def _rows(name: str, shape, stride):
@@ -677,7 +683,7 @@ def rotary_embed(out, x, positions, frequencies, amplitude: float = 1.0, interle
     _run_on(dev, "rotary_embed", _lib.load().rotary_embed, (
         _row_ptr(out, "out", dt, dev), x.data_ptr(), _ptr(positions, "positions", torch.int32, dev),
         _ptr(frequencies, "frequencies", torch.float64, dev), *size, offset, strides, amplitude, bool(interleaved),
-        _dtype_code(x), _stream_on(stream, dev)))
+        _code(x), _stream_on(stream, dev)))
     return out
 
 
@@ -717,7 +723,7 @@ def kv_cache_write_rotary(k_new, v_new, k_cache, v_cache, slot_mapping, position
         _row_ptr(k_new, "k_new", dt, dev), _row_ptr(v_new, "v_new", dt, dev), _ptr(k_cache, "k_cache", dt, dev),
         _ptr(v_cache, "v_cache", dt, dev), _ptr(slot_mapping, "slot_mapping", torch.int64, dev),
         _ptr(positions, "positions", torch.int32, dev), _ptr(frequencies, "frequencies", torch.float64, dev), *size, offset, *blocks,
-        strides, amplitude, bool(interleaved), _dtype_code(k_cache), _stream_on(stream, dev)))
+        strides, amplitude, bool(interleaved), _code(k_cache), _stream_on(stream, dev)))
     return q_out
 
 
@@ -759,7 +765,7 @@ def latent_cache_write(latent, k_rope, cache, slot_mapping, positions, frequenci
         _row_ptr(q_out, "q_out", dt, dev) if some else None, _row_ptr(q_rope, "q_rope", dt, dev) if some else None,
         _row_ptr(latent, "latent", dt, dev), _row_ptr(k_rope, "k_rope", dt, dev), _ptr(cache, "cache", dt, dev),
         _ptr(slot_mapping, "slot_mapping", torch.int64, dev), _ptr(positions, "positions", torch.int32, dev),
-        _ptr(frequencies, "frequencies", torch.float64, dev), *size, strides, amplitude, bool(interleaved), _dtype_code(cache),
+        _ptr(frequencies, "frequencies", torch.float64, dev), *size, strides, amplitude, bool(interleaved), _code(cache),
         _stream_on(stream, dev)))
     return q_out
 
@@ -787,16 +793,22 @@ def _latent_plan(out, q, cache, tables, lens, starts):
     return lens[0], q[0], q[1], q[2] - LATENT_ROPE_DIM, cache[1], tables[1], cache[0]
 
 
+@_plans
+def _latent_workspace(dev: int, T: int, H: int, V: int, max_len: int, code: int) -> int:
+    with torch.cuda.device(dev):
+        return _lib.load().paged_latent_attention_workspace_size(T, H, V, max_len, code)
+
+
 def paged_latent_attention_decode(out, q, cache, block_tables, seq_lens, scale: float, max_seq_len: int,
                                   workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """out[s, h] = sum_t softmax_t(scale * q[s, h] . c_t) c_t[:V] over the rows c_t = [latent | key part] of
     sequence s's tokens: q [S, H, V + 64], out [S, H, V] (bf16 or float32), cache [NB, B, V + 64],
     block_tables int32 [S, maxB], seq_lens int32 [S]."""
     S, _, H, V, B, maxb, NB = _latent_plan(out.shape, q.shape, cache.shape, block_tables.shape, seq_lens.shape, None)
-    lib, code, dt, i32 = _lib.load(), _dtype_code(q), q.dtype, torch.int32
+    lib, code, dt, i32 = _lib.load(), _code(q), q.dtype, torch.int32
     dev, max_len = _device_of(q, "q"), _int32(max_seq_len)
     _run_with_scratch(dev, "paged_latent_attention_decode", lib.paged_latent_attention_decode,
-                      lib.paged_latent_attention_workspace_size, (S, H, V, max_len, code), (
+                      _latent_workspace, (dev, S, H, V, max_len, code), (
         _ptr(out, "out", dt, dev), _ptr(q, "q", dt, dev), _ptr(cache, "cache", dt, dev),
         _ptr(block_tables, "block_tables", i32, dev), _ptr(seq_lens, "seq_lens", i32, dev), S, H, V, B, maxb, NB, max_len,
         scale), workspace, (code, _stream_on(stream, dev)), stream)
@@ -809,10 +821,10 @@ def paged_latent_attention_multi_token(out, q, cache, block_tables, seq_lens, q_
     """paged_latent_attention_decode for each sequence's last Q_s positions, causal: sequence s owns the rows
     q_starts[s] .. q_starts[s + 1] - 1 of q [T, H, V + 64] and out [T, H, V] (int32 [S + 1])."""
     S, T, H, V, B, maxb, NB = _latent_plan(out.shape, q.shape, cache.shape, block_tables.shape, seq_lens.shape, q_starts.shape)
-    lib, code, dt, i32 = _lib.load(), _dtype_code(q), q.dtype, torch.int32
+    lib, code, dt, i32 = _lib.load(), _code(q), q.dtype, torch.int32
     dev, max_len = _device_of(q, "q"), _int32(max_seq_len)
     _run_with_scratch(dev, "paged_latent_attention_multi_token", lib.paged_latent_attention_multi_token,
-                      lib.paged_latent_attention_workspace_size, (T, H, V, max_len, code), (
+                      _latent_workspace, (dev, T, H, V, max_len, code), (
         _ptr(out, "out", dt, dev), _ptr(q, "q", dt, dev), _ptr(cache, "cache", dt, dev),
         _ptr(block_tables, "block_tables", i32, dev), _ptr(seq_lens, "seq_lens", i32, dev),
         _ptr(q_starts, "q_starts", i32, dev), S, T, H, V, B, maxb, NB, _int32(max_q_len), max_len, scale), workspace,
