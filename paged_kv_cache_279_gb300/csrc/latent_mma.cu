@@ -41,8 +41,6 @@ namespace latent {
 
 namespace {
 
-constexpr int kTok = 64;       // tokens of a tile
-
 __device__ __forceinline__ void stmatrix_x4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
@@ -83,20 +81,24 @@ __device__ __forceinline__ void emit(const float (&o)[N / 2], const float (&inv)
 template <int V, int N>
 struct L {
     static constexpr int kChunks = V / 64 + 1;
+    // Tokens of a tile: 64, or 48 where three stages of those fit and two of 64.  (A product's 64 rows then reach into what
+    // lies behind the tile, for scores that no one looks at.)
+    static constexpr int kTok = V == 512 && N <= 32 ? 48 : 64, kAll = (1 << kTok / 8) - 1;
     static constexpr int kGroup = kChunks * 1024;  // bytes of 8 tokens
     static constexpr int kTile = kTok / 8 * kGroup;
     static constexpr int kPart0 = V / 64 - 2;      // chunks of the tile's first part; the second, awaited last, has three
     static constexpr int kQ = kChunks * N * 128;
-    static constexpr int kQBufs = N <= 32 ? 2 : 1;  // the next piece's queries are loaded under this one's, where they fit
-    static constexpr int kP = kTok * 128;
+    static constexpr int kQBufs = N <= 16 || (V == 256 && N == 32) ? 2 : 1;  // the next piece's queries are loaded under this one's, where they fit
+    static constexpr int kP = 64 * 128;
     // softmax warps: four for each 32 rows of 64 (a tile of 64 rows keeps four busy for 1000 cycles), else four
     static constexpr int kSets = N >= 32 ? 2 : 1, kCols1 = N / kSets, kSoftmax = 128 * kSets;
     static constexpr int kThreads = 96 + kSoftmax;  // and a producer, and a warp that issues each product
     static constexpr int kMisc = 3072;
     static constexpr int kMax = 232448;  // shared memory of a CTA
     static constexpr int kStages = (kMax - kMisc - kQBufs * kQ - kP) / kTile < 4 ? (kMax - kMisc - kQBufs * kQ - kP) / kTile : 4;
-    static constexpr int q = 0, p = kQBufs * kQ, ring = p + kP, misc = ring + kStages * kTile;
+    static constexpr int ring = 0, q = kStages * kTile, p = q + kQBufs * kQ, misc = p + kP;
     static constexpr int total = misc + kMisc;
+    static_assert((8 - kTok / 8) * kGroup <= kQBufs * kQ, "the last stage's product ends in Q");
     static constexpr int kBlocks = V / 128;              // of O^T
     static constexpr uint32_t kS = kBlocks * N;          // first column of S^T
     static constexpr uint32_t kCols = kS + 2 * N <= 128 ? 128 : kS + 2 * N <= 256 ? 256 : 512;
@@ -164,7 +166,7 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     if (!a.whole) grid_launch_dependents();
 
     prefetch_tables(a, (int64_t)threadIdx.x * G + cta);
-    Share<N, kTok> sh = locate<N, kTok>(a, &m.red[0][0], cta, G, X::kThreads);
+    Share<N, X::kTok> sh = locate<N, X::kTok>(a, &m.red[0][0], cta, G, X::kThreads);
     const Ws ws = ws_of(a, G, N, V);
     if (threadIdx.x == 0 && !by_context && !a.whole) leave(ws.rec + 4 * cta, 0, 0, 0, 0);
     tc::fence_before();
@@ -197,8 +199,8 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             const int32_t *table = a.tables + (int64_t)sh.w.s * a.maxb;
             // lane l: the cache row of group l & 7 of tile t + (l >> 3); -1: a bad block; -2: no token
             auto look = [&](int t) {
-                const int tok = pc.t0 + t * kTok + 8 * lane;
-                if (t + (lane >> 3) >= n || tok >= pc.end) return -2;
+                const int tok = pc.t0 + (t + (lane >> 3)) * X::kTok + 8 * (lane & 7);
+                if (t + (lane >> 3) >= n || tok >= pc.end || (lane & 7) >= X::kTok / 8) return -2;
                 const int blk = __ldg(table + (tok >> a.bshift));
                 return (unsigned)blk < (unsigned)a.NB ? (blk << a.bshift) + (tok & (a.B - 1)) : -1;
             };
@@ -221,7 +223,7 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     next = look(t + 4);
                 }
                 const int st = tile % X::kStages;
-                const bool turn = (lane >> 3) == (t & 3);
+                const bool turn = (lane >> 3) == (t & 3) && (lane & 7) < X::kTok / 8;
                 // a group without tokens starts past the tensor's end: zeros
                 const int y = row >= 0 ? row : a.NB << a.bshift;
                 const uint32_t dst = smem_u32(smem + X::ring) + (uint32_t)(st * X::kTile + (lane & 7) * X::kGroup);
@@ -231,14 +233,14 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 const uint32_t ok = __ballot_sync(0xffffffffu, row >= 0) >> (8 * (t & 3)) & 0xffu;
                 if (lane == 0) {
                     m.groups[st] = ok;
-                    mbar_arrive_expect_tx(&m.full[0][st], (uint32_t)(kTok * 128 * X::kPart0));
+                    mbar_arrive_expect_tx(&m.full[0][st], (uint32_t)(X::kTok * 128 * X::kPart0));
                 }
                 __syncwarp();
                 if (turn) tma_load_3d_hint(dst, &tm_c0, smem_u32(&m.full[0][st]), 0, y, 0, policy);
                 ++halves;
                 wait(&m.empty[1][st], (uint32_t)(tile / X::kStages + 1) & 1u);
                 if (dead) break;
-                if (lane == 0) mbar_arrive_expect_tx(&m.full[1][st], (uint32_t)(X::kTile - kTok * 128 * X::kPart0));
+                if (lane == 0) mbar_arrive_expect_tx(&m.full[1][st], (uint32_t)(X::kTile - X::kTok * 128 * X::kPart0));
                 __syncwarp();
                 if (turn) tma_load_3d_hint(dst + X::kPart0 * 1024, &tm_c1, smem_u32(&m.full[1][st]), 0, y, X::kPart0, policy);
                 ++halves;
@@ -324,7 +326,7 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 #pragma unroll 1
                     for (int b = 0; b < X::kBlocks; ++b) {
 #pragma unroll
-                        for (int k = 0; k < kTok / 16; ++k)
+                        for (int k = 0; k < X::kTok / 16; ++k)
                             tc::mma(tmem + (uint32_t)(b * N), l0 + (uint64_t)((b * 2048 + k * 2 * X::kGroup) >> 4),
                                     pd + (uint64_t)((k * 2048) >> 4), id, t == 0 && k == 0 ? 0u : 1u);
                         if (2 * b + 2 == X::kPart0) tc::commit(&m.empty[0][st]);
@@ -347,10 +349,11 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         constexpr int NL = X::kCols1, J = NL / 8;
         const int set = (warp - 3) >> 2;  // which of the rows
         const float sc = a.scale_log2;
+        const uint32_t idle = qt * 16 >= X::kTok ? ~0u : 0u;  // this warp's tokens are none of the tile's
         const int col = set * NL + 2 * (lane & 3), tok0 = qt * 16 + (lane >> 2);  // first column, first token (the other: 8 on)
         // stmatrix: lane gives the address of row (lane & 7) of matrix lane >> 3: tokens 0-7, 8-15 of column block j, then j + 1
         const uint32_t p_s = smem_u32(smem + X::p) + (uint32_t)((qt * 2 + ((lane >> 3) & 1)) * 1024 + (lane & 7) * 128);
-        if (sh.blind) zero_blind<N, kTok>(a, cta, G, threadIdx.x - 96, X::kSoftmax, by_context ? ws.rec : nullptr);
+        if (sh.blind) zero_blind<N, X::kTok>(a, cta, G, threadIdx.x - 96, X::kSoftmax, by_context ? ws.rec : nullptr);
         int tile = 0;
         bool stop = false;  // the softmax warps leave together: they share a barrier
         for (int np = 0;; ++np) {
@@ -376,11 +379,11 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 tc::fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&m.s_free[tile & 1]);
-                const int tb = pc.t0 + t * kTok;
+                const int tb = pc.t0 + t * X::kTok;
                 const uint32_t groups = m.groups[st];
-                const bool masked = tb + kTok > least || groups != 0xffu;
+                const bool masked = tb + X::kTok > least || groups != X::kAll;
                 bool bad[2] = {false, false};
-                uint32_t hide[2] = {0u, 0u};  // bit 2 j + i: not seen by column 8 j + col + i
+                uint32_t hide[2] = {idle, idle};  // bit 2 j + i: not seen by column 8 j + col + i
                 if (masked) {
                     const bool in[2] = {((groups >> (2 * qt)) & 1u) != 0, ((groups >> (2 * qt + 1)) & 1u) != 0};
                     uint32_t nf[2] = {0x7f800000u, 0x7f800000u};
@@ -412,7 +415,7 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        bad[h] = (nf[h] & 0x7f800000u) == 0x7f800000u;
+                        bad[h] = !idle && (nf[h] & 0x7f800000u) == 0x7f800000u;
                         const int tk = tok0 + 8 * h;
                         if (bad[h] && set == 0) {
                             unsigned char *g = smem + X::ring + st * X::kTile + (tk >> 3) * X::kGroup + (tk & 7) * 128;
@@ -436,7 +439,7 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                             x[4 * j + i] = fmaf(__uint_as_float(r[4 * j + i]), sc, nr);
                             x[4 * j + 2 + i] = fmaf(__uint_as_float(r[4 * j + 2 + i]), sc, nr);
                         }
-                    if (masked)
+                    if (masked || idle)
 #pragma unroll
                         for (int e = 0; e < 4 * J; ++e) {
                             const int h = (e >> 1) & 1;
@@ -713,7 +716,7 @@ pkv_status launch(Args a, cudaStream_t st) {
         return PKV_ERR_CUDA;
     // A decode of no more contexts than shares: the join's CTAs go by contexts, fewer than the shares.
     const int by_context = !a.q_starts && a.S <= sms;
-    a.whole = whole_contexts(a, N, kTok, sms);
+    a.whole = whole_contexts(a, N, 64, sms);
     a.once = read_once(a, N);
     const unsigned grid = a.whole ? (unsigned)(a.S * a.whole) : (unsigned)sms;
     const pkv_status rc = launch_pdl(latent_mma_kernel<V, N>, dim3(grid), dim3(X::kThreads), (size_t)X::total, st, tm_q, tm_c0, tm_c1, a,
