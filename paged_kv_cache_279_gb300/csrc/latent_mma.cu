@@ -216,7 +216,7 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 __syncwarp();
             };
             int row = look(0), next = -2;
-            if (X::kQBufs == 2) load_q();
+            if (X::kQBufs == 2 || np == 0) load_q();
             for (int t = 0; t < n && !dead; ++t, ++tile) {
                 if ((t & 3) == 0) {
                     if (t) row = next;
@@ -244,7 +244,7 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 __syncwarp();
                 if (turn) tma_load_3d_hint(dst + X::kPart0 * 1024, &tm_c1, smem_u32(&m.full[1][st]), 0, y, X::kPart0, policy);
                 ++halves;
-                if (X::kQBufs == 1 && t == 0) load_q();
+                if (X::kQBufs == 1 && np > 0 && t == 0) load_q();
             }
             if (lane == 0) {
                 if (a.whole) {
