@@ -2,7 +2,7 @@
 //
 // A row tile is up to N (16, 32 or 64) consecutive query rows of one sequence, a
 // row being one head of one query; a decode step's heads, or the heads of a few
-// drafted tokens, are one.  It is attended against tiles of 64 tokens, transposed:
+// drafted tokens, are one.  It is attended against tiles of 48 or 64 tokens, transposed:
 //     S^T = C Q^T   [64 tokens x N rows]        (C: the tile's cache rows, 9 or 5 chunks of 64 entries)
 //     O^T += L^T P^T [V entries x N rows]       (L: the latent part of C, P = exp2(S scale - ref))
 // so the tile itself is the wide operand of both products, read once into shared
@@ -11,7 +11,7 @@
 // rows alone would fill it.
 //
 // The cache rows of 8 tokens are one TMA box [chunk][8 rows][128 bytes]: any block
-// size from 8 on, eight boxes a tile, and both products see 128-byte swizzled
+// size from 8 on, six or eight boxes a tile, and both products see 128-byte swizzled
 // operands (C by rows, L^T by columns) whose 8-token groups are one stride apart.
 //
 // Softmax: four warps, or two sets of four; a thread holds two tokens of every fourth pair of columns.
@@ -26,11 +26,11 @@
 //
 // What bounds it: DRAM while tiles stream (what 32000 tokens more a context cost, 8 contexts: 6.7 TB/s at 16 and 32 rows,
 // 6.3 at 64, of 6.7), before that a chain of loads (lengths, block table, first tile: 3.2 us until it is asked for), after
-// it the join (1.2 us between the kernels, 4 in it).  64 contexts of 64 to 2048 tokens, 32 heads: 26.5 us for 73 MB; 8 of
-// 16000, 64 heads: 42.5 us for 149 MB.  Joined in this kernel, by CTAs that wait for one another's pieces, one context of
-// 16000 took 20.0 us, not 22.7, but these 26.7 and 43.7 (from a host's stream of calls 1 to 2 us more: such a launch is a
-// cooperative one).
-// A tile takes 36 + 16 products, 1452 cycles at 16 rows, 1920 at 64 (operand bytes out of
+// it the join (1.2 us between the kernels, 4 in it).  64 contexts of 64 to 2048 tokens, 32 heads: 24.8 us for 73 MB; 8 of
+// 16000, 64 heads: 42.2 us for 149 MB.  Joined in this kernel, by CTAs that wait for one another's pieces (two stages, as
+// below), one context of 16000 took 20.0 us, not 22.7, but these 26.7 and 43.7, not 26.5 and 42.5, and 1 to 2 us more from a
+// host's stream of calls: such a launch is a cooperative one.
+// A tile of 64 takes 36 + 16 products, 1452 cycles at 16 rows, 1920 at 64 (operand bytes out of
 // shared memory); 3200 is its share of DRAM.
 #include <cmath>
 
@@ -81,8 +81,11 @@ __device__ __forceinline__ void emit(const float (&o)[N / 2], const float (&inv)
 template <int V, int N>
 struct L {
     static constexpr int kChunks = V / 64 + 1;
-    // Tokens of a tile: 64, or 48 where three stages of those fit and two of 64.  (A product's 64 rows then reach into what
-    // lies behind the tile, for scores that no one looks at.)
+    // Tokens of a tile: 64, or 48 where three stages of those fit and two of 64: a stage is loaded anew when its tile's last
+    // product is done, and with two nothing is under way for half of that time.  64 contexts of 64 to 2048, 32 heads, 26.5 ->
+    // 24.8 us, 140, 16 heads, 38.9 -> 35.9, one of 16000 22.6 -> 18.9; 4 of 64, 32 heads, 7.1 -> 7.6; five stages of 32
+    // tokens: 26.0, 37.9, 25.4.  (A product's 64 rows then reach into what lies behind the tile, for scores that no one
+    // looks at.)
     static constexpr int kTok = V == 512 && N <= 32 ? 48 : 64, kAll = (1 << kTok / 8) - 1;
     static constexpr int kGroup = kChunks * 1024;  // bytes of 8 tokens
     static constexpr int kTile = kTok / 8 * kGroup;

@@ -282,7 +282,7 @@ __device__ __forceinline__ Share<N, TOK> locate(const Args &a, float *scratch, i
     }
     const int64_t excl = base + incl - mine;
     // The least share grows with the root of a context's tiles: what a context's pieces cost to join grows with their
-    // number (16000 tokens alone: 25.8 us with shares of 2 tiles, 21.1 with 4; two of 600 to 1500: 11.6 and 14.6).
+    // number (16000 tokens alone: 23.0 us with shares of 2 tiles, 18.7 with 4; two of 600 to 1500: 10.8 and 11.6).
     const int least = max(2, (int)sqrtf((float)total / (16.f * (float)a.S)));
     int parts = total >= (int64_t)most * least ? most : (int)total / least;
     if (parts < 1) parts = 1;
@@ -352,9 +352,9 @@ __device__ __forceinline__ void prefetch_tables(const Args &a, int64_t line) {
 // Whether every context of a call gets a share of its own, uncut, and nothing is left to join by a second kernel: there
 // are shares enough, and the longest context there may be has few tiles -- 4, and up to 10 the more of the shares are
 // in use (lengths differ: the limit is for contexts that are half of it on average).  Uncut against cut, in us, 32 heads:
-// 4 sequences of 64 / 256 / 384 / 512 tokens 7.1 / 10.1 / 12.6 / 15.0 against 9.6 / 11.7 / 11.9 / 12.0; 64 sequences of
-// 64 / 256 / 512 / 1024: 7.4 / 10.3 / 18.0 / 29.8 against 9.8 / 15.0 / 21.5 / 28.0; in pairs of CTAs (128 heads), 64
-// sequences of 256 / 512 / 1024: 12.1 / 17.8 / 26.1 against 21.2 / 25.9 / 37.6.
+// 4 sequences of 64 / 256 / 384 / 512 tokens 7.6 / 11.1 / 12.6 / 15.3 against 9.6 / 11.2 / 11.2 / 11.1; 64 sequences of
+// 64 / 256 / 512 / 1024: 7.9 / 12.1 / 17.5 / 27.6 against 10.1 / 15.4 / 19.0 / 25.0; in pairs of CTAs (128 heads), 64
+// sequences of 256 / 512 / 1024: 11.8 / 16.6 / 24.7 against 20.4 / 23.6 / 33.8.
 // Returns the row tiles to count a sequence for, or 0.
 inline int whole_contexts(const Args &a, int n, int tok, int shares) {
     const int64_t tiles = (int64_t)a.rows / n + (a.rows % n != 0), most = (int64_t)a.maxb * a.B;
@@ -365,8 +365,8 @@ inline int whole_contexts(const Args &a, int n, int tok, int shares) {
 
 // Whether a call's cache rows are the first to leave L2: each is read by one row tile, and the pool, one layer's, is a
 // quarter of L2 or more, so that no row is found there at the next step.  Block tables, queries, partial results and the
-// kernels' code then stay: 64 contexts of 64 to 2048 tokens, 32 heads, 28.5 -> 27.0 us, 128 heads 34.6 -> 33.2; 8 of 16000,
-// 64 heads, 46.3 -> 42.9.  Where it is not done: a pool of 18 MB read again and again, 22.8 us against 24.4; 8 x 512 queries
+// kernels' code then stay: 64 contexts of 64 to 2048 tokens, 32 heads, 26.2 -> 24.9 us, 128 heads 33.9 -> 32.7; 8 of 16000,
+// 64 heads, 45.0 -> 42.2.  Where it is not done: a pool of 18 MB read again and again, 18.8 us against 20.0; 8 x 512 queries
 // of 4096, whose rows are read by 128 row tiles, 674 against 894.
 inline bool read_once(const Args &a, int n) {
     return a.rows <= n && (int64_t)a.NB * a.B * (a.V + kRope) * 2 >= 32 << 20;
