@@ -96,7 +96,7 @@ struct L {
     // softmax warps: four for each 32 rows of 64 (a tile of 64 rows keeps four busy for 1000 cycles), else four
     static constexpr int kSets = N >= 32 ? 2 : 1, kCols1 = N / kSets, kSoftmax = 128 * kSets;
     static constexpr int kThreads = 96 + kSoftmax;  // and a producer, and a warp that issues each product
-    static constexpr int kMisc = 3072;
+    static constexpr int kMisc = 3 * 1024;
     static constexpr int kMax = 232448;  // shared memory of a CTA
     static constexpr int kStages = (kMax - kMisc - kQBufs * kQ - kP) / kTile < 4 ? (kMax - kMisc - kQBufs * kQ - kP) / kTile : 4;
     static constexpr int ring = 0, q = kStages * kTile, p = q + kQBufs * kQ, misc = p + kP;
@@ -119,7 +119,7 @@ struct alignas(8) Misc {
     uint32_t tmem;
     int dead;
 };
-static_assert(sizeof(Misc) <= 3072, "misc");
+static_assert(sizeof(Misc) <= 3 * 1024, "misc");
 
 struct Ws {
     int *rec;      // [shares][4]: what the context that begins in a share left for the join; or one for each context
