@@ -27,7 +27,7 @@
 // What bounds it: DRAM while tiles stream (what 32000 tokens more a context cost, 8 contexts: 6.7 TB/s at 16 and 32 rows,
 // 6.3 at 64, of 6.7), before that a chain of loads (lengths, block table, first tile: 3.2 us until it is asked for), after
 // it the join (1.2 us between the kernels, 4 in it).  64 contexts of 64 to 2048 tokens, 32 heads: 24.8 us for 73 MB; 8 of
-// 16000, 64 heads: 42.2 us for 149 MB.  Joined in this kernel, by CTAs that wait for one another's pieces (two stages, as
+// 16000, 64 heads: 41.2 us for 149 MB.  Joined in this kernel, by CTAs that wait for one another's pieces (two stages, as
 // below), one context of 16000 took 20.0 us, not 22.7, but these 26.7 and 43.7, not 26.5 and 42.5, and 1 to 2 us more from a
 // host's stream of calls: such a launch is a cooperative one.
 // A tile of 64 takes 36 + 16 products, 1452 cycles at 16 rows, 1920 at 64 (operand bytes out of
@@ -248,6 +248,12 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 if (turn) tma_load_3d_hint(dst + X::kPart0 * 1024, &tm_c1, smem_u32(&m.full[1][st]), 0, y, X::kPart0, policy);
                 ++halves;
                 if (X::kQBufs == 1 && np > 0 && t == 0) load_q();
+                // The tile that this stage takes next, into L2 (64 rows: 8 x 16000 42.5 -> 41.2 us; with three stages no gain,
+                // and 36.0 -> 38.9 for 140 contexts of 16 heads).
+                if constexpr (X::kStages == 2) {
+                    const int ahead = (t & 3) < 2 ? row : next;
+                    if ((lane >> 3) == ((t + 2) & 3) && ahead >= 0) prefetch_rows<V>(a, ahead, policy);
+                }
             }
             if (lane == 0) {
                 if (a.whole) {

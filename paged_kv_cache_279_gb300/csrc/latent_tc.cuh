@@ -118,6 +118,16 @@ __device__ __forceinline__ void tma_load_3d_hint(uint32_t dst, const CUtensorMap
         : "memory");
 }
 
+// 8 rows of the cache from `row` on, on their way into L2.
+template <int V>
+__device__ __forceinline__ void prefetch_rows(const Args &a, int row, uint64_t policy) {
+    constexpr int kRow = (V + kRope) * 2;
+    asm volatile("cp.async.bulk.prefetch.L2.global.L2::cache_hint [%0], %1, %2;" ::"l"(
+                     __cvta_generic_to_global((const unsigned char *)a.cache + (int64_t)row * kRow)),
+                 "r"(8 * kRow), "l"(policy)
+                 : "memory");
+}
+
 // One share's part of a context.
 struct Piece {
     int tiles;     // 0: no more pieces
