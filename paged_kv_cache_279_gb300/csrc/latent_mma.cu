@@ -252,7 +252,7 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 // and 36.0 -> 38.9 for 140 contexts of 16 heads).
                 if constexpr (X::kStages == 2) {
                     const int ahead = (t & 3) < 2 ? row : next;
-                    if ((lane >> 3) == ((t + 2) & 3) && ahead >= 0) prefetch_rows<V>(a, ahead, policy);
+                    if ((lane >> 3) == ((t + 2) & 3) && ahead >= 0) prefetch_rows<V>(a, ahead);
                 }
             }
             if (lane == 0) {

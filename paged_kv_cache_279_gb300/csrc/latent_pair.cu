@@ -169,7 +169,6 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 
     if (warp == 0) {
         // ======================= producer of pieces, Q and the rows by tokens =======================
-        const uint64_t policy = row_policy(a);
         int tile = 0, np = 0, nq = 0, nk = 0;  // tiles, pieces, queries and parts issued
         for (;;) {
             const int d = np % kDescs;
@@ -215,16 +214,18 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     }
                     __syncwarp();
                     if (mine)
-                        tma_load_3d_hint(smem_u32(smem + X::k) + (uint32_t)((lane & 7) * X::kGroupK + h * X::kPart0 * 1024), h ? &tm_k1 : &tm_k0,
-                                    smem_u32(&m.k_full[h]), 0, row >= 0 ? row : none, h * X::kPart0, policy);
+                        tma_load_3d(smem_u32(smem + X::k) + (uint32_t)((lane & 7) * X::kGroupK + h * X::kPart0 * 1024), h ? &tm_k1 : &tm_k0,
+                                    smem_u32(&m.k_full[h]), 0, row >= 0 ? row : none, h * X::kPart0);
                     ++nk;
                 }
-                // The next tile's rows, of whose load nothing is under way yet, into L2, where two to eight row tiles read
-                // them: 64 x 5 queries, 32 heads, 48.4 -> 46.2 us, 4 x 8 queries of 128 heads 40.2 -> 39.8.  (One: 32.7
-                // -> 34.0.  More, and they are mostly there: 8 x 64 queries of 32 heads 111 -> 116.)
+                // The next tile's rows, of whose load nothing is under way yet, into L2, where up to eight row tiles read
+                // them: 64 x 5 queries, 32 heads, 48.4 -> 46.2 us, 64 x 4 35.6 -> 34.8, 4 x 8 queries of 128 heads 40.2 ->
+                // 39.8.  (More, and they are mostly there: 8 x 64 queries of 32 heads 111 -> 116.  And where rows are the
+                // first to leave, it is the load by entries, the later one, that says so: the other, and a decode of 128
+                // heads takes 33.9 us, not 32.4.)
                 const int ahead = (t & 1) == 0 ? row : next;
-                if (a.rows > kRows && a.rows <= 8 * kRows && (lane >> 4) == ((t + 1) & 1) && ((lane >> 3) & 1) == (int)rank && ahead >= 0)
-                    prefetch_rows<V>(a, ahead, policy);
+                if (a.rows <= 8 * kRows && (lane >> 4) == ((t + 1) & 1) && ((lane >> 3) & 1) == (int)rank && ahead >= 0)
+                    prefetch_rows<V>(a, ahead);
             }
             if (lead && lane == 0) {
                 if (a.whole) {

@@ -120,11 +120,11 @@ __device__ __forceinline__ void tma_load_3d_hint(uint32_t dst, const CUtensorMap
 
 // 8 rows of the cache from `row` on, on their way into L2.
 template <int V>
-__device__ __forceinline__ void prefetch_rows(const Args &a, int row, uint64_t policy) {
+__device__ __forceinline__ void prefetch_rows(const Args &a, int row) {
     constexpr int kRow = (V + kRope) * 2;
-    asm volatile("cp.async.bulk.prefetch.L2.global.L2::cache_hint [%0], %1, %2;" ::"l"(
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
                      __cvta_generic_to_global((const unsigned char *)a.cache + (int64_t)row * kRow)),
-                 "r"(8 * kRow), "l"(policy)
+                 "r"(8 * kRow)
                  : "memory");
 }
 
