@@ -408,10 +408,11 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                                 if (!in[h] || tb + tok0 + 8 * h >= lim) hide[h] |= 1u << (2 * j + i);
                             }
                         }
-                    // A row of the cache that holds an infinity or NaN gives every query such a score.  It
-                    // must not reach, through 0 * inf, the rows that do not see it: its latent part is
+                    // A row of the cache whose latent part holds an infinity or NaN gives every query a score that is no
+                    // number.  It must not reach, through 0 * inf, the rows that do not see it: its latent part is
                     // zeroed here, after its scores were taken, and those that see it get NaN.  (So are rows past
-                    // the last token that hold one.)
+                    // the last token that hold one.)  Scores alone do not tell: finite entries whose products pass
+                    // float32's range give every query one too, so the latent part itself is looked at.
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         nf[h] &= __shfl_xor_sync(0xffffffffu, nf[h], 1);
@@ -422,15 +423,28 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                         softmax_sync<X::kSoftmax>();
                         nf[0] &= m.nf[set ^ 1][tok0], nf[1] &= m.nf[set ^ 1][tok0 + 8];
                     }
+                    const bool suspect[2] = {!idle && (nf[0] & 0x7f800000u) == 0x7f800000u, !idle && (nf[1] & 0x7f800000u) == 0x7f800000u};
+                    if (__any_sync(0xffffffffu, suspect[0] || suspect[1])) {  // (alike in the two sets' warps of these tokens)
+                        wait(&m.full[1][st], (uint32_t)(tile / X::kStages) & 1u);  // (complete: orders the reads of the tile)
+                        auto latent = [&](int h, int c, int e) {  // 16 bytes of token h's latent part
+                            const int tk = tok0 + 8 * h;
+                            return reinterpret_cast<uint4 *>(smem + X::ring + st * X::kTile + (tk >> 3) * X::kGroup + (tk & 7) * 128 + c * 1024 + e * 16);
+                        };
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        bad[h] = !idle && (nf[h] & 0x7f800000u) == 0x7f800000u;
-                        const int tk = tok0 + 8 * h;
-                        if (bad[h] && set == 0) {
-                            unsigned char *g = smem + X::ring + st * X::kTile + (tk >> 3) * X::kGroup + (tk & 7) * 128;
-                            for (int c = lane & 3; c < V / 64; c += 4)
-                                for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4 *>(g + c * 1024 + e * 16) = make_uint4(0, 0, 0, 0);
+                        for (int h = 0; h < 2; ++h) {
+                            if (suspect[h])
+                                for (int c = lane & 3; c < V / 64; c += 4)
+                                    for (int e = 0; e < 8; ++e) bad[h] |= not_finite(*latent(h, c, e));
+                            bad[h] |= __shfl_xor_sync(0xffffffffu, (int)bad[h], 1) != 0;
+                            bad[h] |= __shfl_xor_sync(0xffffffffu, (int)bad[h], 2) != 0;
                         }
+                        // both sets have looked before one of them zeroes
+                        if constexpr (X::kSets == 2) asm volatile("barrier.cta.sync %0, 64;" ::"r"(2 + qt) : "memory");
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            if (bad[h] && set == 0)
+                                for (int c = lane & 3; c < V / 64; c += 4)
+                                    for (int e = 0; e < 8; ++e) *latent(h, c, e) = make_uint4(0, 0, 0, 0);
                     }
                 }
                 // x: log2 of the weights against the references.  Once, if no score passes its row's reference by far; else

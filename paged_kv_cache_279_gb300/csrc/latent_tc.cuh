@@ -45,6 +45,15 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
     return d;
 }
 
+// Whether one of eight bf16 entries is an infinity or NaN.
+__device__ __forceinline__ bool not_finite(const uint4 &y) {
+    const uint32_t z[4] = {y.x, y.y, y.z, y.w};
+    bool found = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) found |= (z[i] & 0x7f80u) == 0x7f80u || (z[i] & 0x7f800000u) == 0x7f800000u;
+    return found;
+}
+
 // Barrier of the softmax warps (their THREADS), alone and with a vote.
 template <int THREADS>
 __device__ __forceinline__ void softmax_sync() {

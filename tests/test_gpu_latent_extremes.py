@@ -1,0 +1,126 @@
+"""GPU: latent attention where scores pass float32's range."""
+import numpy as np
+import pytest
+import torch
+
+import latent_cases as lc
+import latent_more as lm
+import paged_kv_cache_279_gb300 as pkv
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(autouse=True)
+def _clear_errors():
+    pkv.read_device_errors(clear=True)
+    yield
+    assert pkv.read_device_errors(clear=True) == 0
+
+
+def _tokens(which, L):
+    t = np.zeros(L, dtype=bool)
+    if which == "last":
+        t[-1] = True
+    elif which == "early":
+        t[5] = True
+    elif which == "several":
+        t[np.random.default_rng(L).permutation(L)[:L // 3]] = True
+    elif which == "tail":
+        t[L - L % 48 - 1:] = True
+    elif which == "all":
+        t[:] = True
+    return t
+
+
+def _overflow(which, heads, H, V, dtype, queries, at, sign=-1.0, lens=(150, 77), power=64):
+    """A case of finite numbers, some products 2^(2 power + 1) in size: (case, dead tokens a sequence)."""
+    c = lc.make(list(lens), H, V, 16, dtype, queries, seed=3, fill=0.0)
+    e = V + 5 if at == "key" else 9
+    some = np.ones(H, dtype=bool) if heads == "all" else np.arange(H) % 2 == 1
+    c["q"][:, :, e] = torch.from_numpy(np.where(some, 2.0 ** power, 0.0)).to(dtype)
+    dead = []
+    for x in c["rows"]:
+        t = _tokens(which, x.shape[0])
+        x[:, e] = torch.from_numpy(np.where(t, sign * 2.0 ** (power + 1), 0.0)).to(dtype)
+        dead.append(some[:, None] & t[None])
+    return lm.store(c), dead
+
+
+# up to 64 rows of a sequence
+FEW = [(1, None, 512, BF), (16, None, 512, BF), (33, None, 256, BF), (64, None, 512, BF), (1, [3, 2], 512, BF), (4, [9, 5], 512, BF),
+       (16, [4, 2], 256, BF)]
+
+
+def _hidden_by_overflow(which, heads, H, queries, V, dtype, at, sign, table, power=64):
+    c, dead = _overflow(which, heads, H, V, dtype, queries, at, sign, power=power)
+    if table:
+        c = lm.wide(c, table)
+    scale = lc.SCALE if sign < 0 else -lc.SCALE
+    got = lc.run(c, scale=scale, max_len=10 ** 6)
+    lm.check(got, lm.expected(c, dead, scale))
+    if which == "all":  # every score of these heads is -infinity
+        assert torch.all(got[:, dead[0][:, 0]] == 0)
+
+
+WHERE = [("last", "all", "key", -1.0), ("early", "all", "key", -1.0), ("several", "some", "key", -1.0),
+         ("several", "all", "latent", -1.0), ("tail", "some", "latent", 1.0),
+         ("tail", "all", "key", -1.0), ("all", "all", "key", 1.0), ("all", "some", "key", -1.0)]
+
+
+@pytest.mark.parametrize("table", [0, 8192])
+@pytest.mark.parametrize("which,heads,at,sign", WHERE)
+@pytest.mark.parametrize("H,queries,V,dtype", FEW)
+def test_scores_below_all_numbers(H, queries, V, dtype, which, heads, at, sign, table):
+    """Products of finite entries that pass 3.4e38: scores of -infinity, weights of 0, wherever the tokens lie."""
+    _hidden_by_overflow(which, heads, H, queries, V, dtype, at, sign, table)
+
+
+@pytest.mark.parametrize("which,heads,at,sign", WHERE)
+@pytest.mark.parametrize("H,queries,V", [(5, None, 512), (3, [9, 5], 256)])
+def test_float32_scores_below_all_numbers(H, queries, V, which, heads, at, sign):
+    """The same in float32, which scales queries before the products: 2^133 times 0.104 (scale and log2 e) passes its range,
+    2^129 times that does not."""
+    _hidden_by_overflow(which, heads, H, queries, V, F32, at, sign, 0, power=66)
+
+
+@pytest.mark.parametrize("dtype,H,queries", [(BF, 16, None), (F32, 5, None), (BF, 4, [9, 5])])
+def test_an_infinite_query_whose_scores_are_all_minus_infinity(dtype, H, queries):
+    c = lc.make([150, 77], H, 512, 16, dtype, queries, fill=0.0)
+    for x in c["rows"]:
+        x[:, 520] = -1.0
+    want = lc.run(lm.store(c))
+    c["q"][:, 2, 520] = float("inf")
+    got = lc.run(c)
+    assert torch.all(got[:, 2] == 0)
+    keep = torch.arange(H) != 2
+    assert torch.equal(got[:, keep], want[:, keep])
+
+
+def _bad_row_beside(H, queries, at, bad, table):
+    """Token 60 holds something that is no number, 57 and 70 have scores of -infinity: who does not see 60 is not touched by it."""
+    c, dead = _overflow("none", "all", H, 512, BF, queries, "key", lens=(90, 77))
+    e = 512 + 5
+    for t in (57, 70):
+        c["rows"][0][t, e] = -2.0 ** 65
+        dead[0][:, t] = True
+    c = lm.store(lm.wide(c, table) if table else c)
+    want = lc.run(c, max_len=10 ** 6)
+    lm.check(want, lm.expected(c, dead))
+    cache = c["cache"].clone()
+    cache[int(c["tables"][0][60 // 16]), 60 % 16, at] = bad
+    got = lc.run(c, cache=cache.cuda(), max_len=10 ** 6)
+    n = c["nq"][0]
+    sees = torch.zeros(want.shape[0], dtype=torch.bool)
+    sees[max(0, 60 - (90 - n)):n] = True
+    assert torch.equal(got[~sees.cuda()], want[~sees.cuda()])
+    if at < 512 or bad != bad:
+        assert torch.all(~torch.isfinite(got[sees.cuda()][..., min(at, 511)]))
+
+
+@pytest.mark.parametrize("at", [33, 512 + 40])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("table", [0, 8192])
+@pytest.mark.parametrize("H,queries", [(1, [40, 9]), (2, [32, 3]), (16, [4, 4]), (16, None)])
+def test_a_row_that_is_no_number_beside_such_scores(H, queries, at, bad, table):
+    _bad_row_beside(H, queries, at, bad, table)
