@@ -55,7 +55,7 @@ struct alignas(8) Misc {
     Piece piece[kDescs];
     float red[4][64];
     uint32_t groups[4];   // valid 8-token groups of a tile
-    uint32_t warp_bad[4][2];
+    uint32_t warp_bad[4][2], row_bad[2][2];  // by 32 tokens: scores that are no numbers; latent parts
     uint32_t tmem;
     int dead;
 };
@@ -105,6 +105,21 @@ __device__ __forceinline__ void commit_both(uint64_t *bar) {
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
         "h"((unsigned short)3)
         : "memory");
+}
+
+// Whether the latent part of token `tok` of a sequence holds an infinity or NaN, as it lies in the cache.  (Out of line, as
+// it is seldom asked: inlined, 8 x 512 queries of 4096 took 714 us, not 710.)
+template <int V>
+__device__ __noinline__ bool latent_not_finite(const Args &a, int seq, int tok) {
+    const int blk = __ldg(a.tables + (int64_t)seq * a.maxb + (tok >> a.bshift));
+    bool found = false;
+    if ((unsigned)blk < (unsigned)a.NB) {
+        const int64_t row = ((int64_t)blk << a.bshift) + (tok & (a.B - 1));
+        const uint4 *y = reinterpret_cast<const uint4 *>((const unsigned char *)a.cache + row * (V + kRope) * 2);
+#pragma unroll 1
+        for (int e = 0; e < V / 8; ++e) found |= not_finite(y[e]);
+    }
+    return found;
 }
 
 template <int V>
@@ -427,22 +442,32 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (lane == 0) arrive_at(s_free[tile & 1]);
                 const int tb = pc.t0 + t * kTok;
                 const bool masked = tb + kTok > least || groups != 0xffffu;
-                uint32_t nf = 0u, suspect = 0u;
+                uint32_t bad = 0u, wipe = 0u;  // rows that hold an infinity or NaN: among this thread's tokens; among those it zeroes
                 if (masked) {
-                    // A row of the cache that holds an infinity or NaN gives every query such a score (and may not be the
-                    // only reason for one): seldom there, looked for in earnest only if some score is one.
+                    // A row of the cache whose latent part holds an infinity or NaN gives every query a score that is no
+                    // number.  Finite entries whose products pass float32's range may do so too, and there a score of
+                    // -infinity is a weight of 0: so the rows themselves decide, looked at only if some score is none.
                     float most = 0.f;
 #pragma unroll
                     for (int c = 0; c < 32; c += 2) most = max3_nan(most, fabsf(__uint_as_float(s[c])), fabsf(__uint_as_float(s[c + 1])));
                     if (softmax_any<kSoftmax>(!(most < INFINITY))) {
                         // the tokens that gave all of this CTA's rows one, a word of 32 tokens a warp
+                        uint32_t nf = 0u;
 #pragma unroll
                         for (int c = 0; c < 32; ++c)
                             if ((s[c] & 0x7f800000u) == 0x7f800000u) nf |= 1u << c;
                         const uint32_t all = __reduce_and_sync(0xffffffffu, nf);
                         if (lane == 0) m.warp_bad[qt][q2] = all;
                         softmax_sync<kSoftmax>();
-                        suspect = m.warp_bad[2 * half][qt & 1] & m.warp_bad[2 * half + 1][qt & 1];  // tokens 64 half + 32 (qt & 1) ..
+                        if (q2 == 0) {  // four warps, tokens 64 half + 32 (qt & 1) .., one a lane; this CTA has half of a row alone
+                            const uint32_t suspect = m.warp_bad[2 * half][qt & 1] & m.warp_bad[2 * half + 1][qt & 1];
+                            const int at = 64 * half + 32 * (qt & 1) + lane;
+                            const bool found = (suspect >> lane) & (groups >> (at >> 3)) & 1u ? latent_not_finite<V>(a, pc.seq, tb + at) : false;
+                            wipe = __ballot_sync(0xffffffffu, found);
+                            if (lane == 0) m.row_bad[half][qt & 1] = wipe;
+                        }
+                        softmax_sync<kSoftmax>();
+                        bad = m.row_bad[half][q2];
                     }
                 }
                 // log2 of the weights without the reference
@@ -457,7 +482,7 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     hide |= (g4 & 1u ? 0u : 0xffu) | (g4 & 2u ? 0u : 0xff00u) | (g4 & 4u ? 0u : 0xff0000u) | (g4 & 8u ? 0u : 0xff000000u);
 #pragma unroll
                     for (int c = 0; c < 32; ++c) {
-                        if ((nf >> c) & 1u) x[c] = __uint_as_float(0x7fffffffu);  // (-infinity too: 0 times an infinity)
+                        if ((bad >> c) & 1u) x[c] = __uint_as_float(0x7fffffffu);  // (-infinity too: 0 times an infinity)
                         if ((hide >> c) & 1u) x[c] = -INFINITY;
                     }
                 }
@@ -518,25 +543,18 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
                     *reinterpret_cast<uint4 *>(p_row + (((p_chunk + c) ^ (row & 7)) << 4)) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-                if (masked && q2 == 0 && suspect) {
+                if (wipe) {
                     // Such a row must not reach, through 0 * infinity, the queries that do not see it, nor may what lies
-                    // behind the last token: where this CTA's half of its latent part holds one, that is zeroed.
+                    // behind the last token: this CTA's half of its latent part is zeroed.
                     wait(&m.v_full[0], (uint32_t)tile & 1u);
                     wait(&m.v_full[1], (uint32_t)tile & 1u);
                     const int tk = 64 * half + row;  // (as many tokens as rows)
-                    if ((suspect >> lane) & 1u) {
+                    if ((wipe >> lane) & 1u) {
                         unsigned char *g = smem + X::v + (tk >> 3) * X::kGroupV + (tk & 7) * 128;
-                        bool found = false;
+#pragma unroll 1
                         for (int e = 0; e < V / 128; ++e)
-                            for (int k = 0; k < 8; ++k) {
-                                const uint4 y = *reinterpret_cast<const uint4 *>(g + e * 1024 + k * 16);
-                                const uint32_t z[4] = {y.x, y.y, y.z, y.w};
-                                for (int i = 0; i < 4; ++i)
-                                    found = found || (z[i] & 0x7f80u) == 0x7f80u || (z[i] & 0x7f800000u) == 0x7f800000u;
-                            }
-                        if (found)
-                            for (int e = 0; e < V / 128; ++e)
-                                for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4 *>(g + e * 1024 + k * 16) = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+                            for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4 *>(g + e * 1024 + k * 16) = make_uint4(0, 0, 0, 0);
                     }
                     __syncwarp();
                 }

@@ -50,6 +50,7 @@ def _overflow(which, heads, H, V, dtype, queries, at, sign=-1.0, lens=(150, 77),
 # up to 64 rows of a sequence
 FEW = [(1, None, 512, BF), (16, None, 512, BF), (33, None, 256, BF), (64, None, 512, BF), (1, [3, 2], 512, BF), (4, [9, 5], 512, BF),
        (16, [4, 2], 256, BF)]
+MANY = [(128, None, 512, BF), (100, None, 256, BF), (16, [40, 9], 512, BF), (6, [70, 30], 256, BF), (1, [140, 70], 512, BF)]
 
 
 def _hidden_by_overflow(which, heads, H, queries, V, dtype, at, sign, table, power=64):
@@ -73,6 +74,14 @@ WHERE = [("last", "all", "key", -1.0), ("early", "all", "key", -1.0), ("several"
 @pytest.mark.parametrize("H,queries,V,dtype", FEW)
 def test_scores_below_all_numbers(H, queries, V, dtype, which, heads, at, sign, table):
     """Products of finite entries that pass 3.4e38: scores of -infinity, weights of 0, wherever the tokens lie."""
+    _hidden_by_overflow(which, heads, H, queries, V, dtype, at, sign, table)
+
+
+@pytest.mark.parametrize("table", [0, 8192])
+@pytest.mark.parametrize("which,heads,at,sign", WHERE)
+@pytest.mark.parametrize("H,queries,V,dtype", MANY)
+def test_scores_below_all_numbers_on_pairs(H, queries, V, dtype, which, heads, at, sign, table):
+    """The same for more than 64 query rows a sequence."""
     _hidden_by_overflow(which, heads, H, queries, V, dtype, at, sign, table)
 
 
@@ -124,3 +133,24 @@ def _bad_row_beside(H, queries, at, bad, table):
 @pytest.mark.parametrize("H,queries", [(1, [40, 9]), (2, [32, 3]), (16, [4, 4]), (16, None)])
 def test_a_row_that_is_no_number_beside_such_scores(H, queries, at, bad, table):
     _bad_row_beside(H, queries, at, bad, table)
+
+
+@pytest.mark.parametrize("at", [33, 300, 512 + 40])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("table", [0, 8192])
+@pytest.mark.parametrize("H,queries", [(2, [50, 9]), (16, [40, 9]), (128, None), (70, [3, 2])])
+def test_a_row_that_is_no_number_beside_such_scores_on_pairs(H, queries, at, bad, table):
+    _bad_row_beside(H, queries, at, bad, table)
+
+
+def test_an_infinite_query_on_pairs_whose_scores_are_all_minus_infinity():
+    for H, queries in ((100, None), (5, [30, 20])):
+        c = lc.make([150, 77], H, 512, 16, BF, queries, fill=0.0)
+        for x in c["rows"]:
+            x[:, 520] = -1.0
+        want = lc.run(lm.store(c))
+        c["q"][:, 2, 520] = float("inf")
+        got = lc.run(c)
+        assert torch.all(got[:, 2] == 0)
+        keep = torch.arange(H) != 2
+        assert torch.equal(got[:, keep], want[:, keep])
