@@ -37,7 +37,7 @@ struct Seq {
     int L, q0, n, n0;
     bool flagged;
 };
-__device__ __forceinline__ Seq sequence(const Args &a, int s) {
+__host__ __device__ __forceinline__ Seq sequence(const Args &a, int s) {
     Seq r;
     const int len = a.lens[s];
     const int cap = (int)min((int64_t)a.max_len, (int64_t)a.maxb * a.B);
@@ -59,7 +59,7 @@ __device__ __forceinline__ Seq sequence(const Args &a, int s) {
 }
 
 // x / H, 0 <= x < 2^31: with l = ceil(log2 H), hmul = floor(2^(31 + l) / H) + 1 passes 2^(31 + l) / H by at most 2^l / H.
-__device__ __forceinline__ int by_heads(const Args &a, int x) { return (int)((uint64_t)(uint32_t)x * a.hmul >> a.hshift); }
+__host__ __device__ __forceinline__ int by_heads(const Args &a, int x) { return (int)((uint64_t)(uint32_t)x * a.hmul >> a.hshift); }
 
 // bf16 on the tensor cores: workspace of a call, and the call, its arguments checked.  run_mma: row tiles of up to
 // 64 rows; run_pair: of 128.

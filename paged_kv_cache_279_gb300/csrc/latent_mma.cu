@@ -169,7 +169,7 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     if (!a.whole) grid_launch_dependents();
 
     prefetch_tables(a, (int64_t)threadIdx.x * G + cta);
-    Share<N, X::kTok> sh = locate<N, X::kTok>(a, &m.red[0][0], cta, G, X::kThreads);
+    Share<N, X::kTok, true> sh = locate<N, X::kTok, true>(a, &m.red[0][0], cta, G, X::kThreads);
     const Ws ws = ws_of(a, G, N, V);
     if (threadIdx.x == 0 && !by_context && !a.whole) leave(ws.rec + 4 * cta, 0, 0, 0, 0);
     tc::fence_before();
@@ -362,7 +362,7 @@ latent_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         const int col = set * NL + 2 * (lane & 3), tok0 = qt * 16 + (lane >> 2);  // first column, first token (the other: 8 on)
         // stmatrix: lane gives the address of row (lane & 7) of matrix lane >> 3: tokens 0-7, 8-15 of column block j, then j + 1
         const uint32_t p_s = smem_u32(smem + X::p) + (uint32_t)((qt * 2 + ((lane >> 3) & 1)) * 1024 + (lane & 7) * 128);
-        if (sh.blind) zero_blind<N, X::kTok>(a, cta, G, threadIdx.x - 96, X::kSoftmax, by_context ? ws.rec : nullptr);
+        if (sh.blind) zero_blind<N, X::kTok, true>(a, cta, G, threadIdx.x - 96, X::kSoftmax, by_context ? ws.rec : nullptr);
         int tile = 0;
         bool stop = false;  // the softmax warps leave together: they share a barrier
         for (int np = 0;; ++np) {

@@ -159,7 +159,7 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     // the join kernel, which waits for this one before it reads (no other: attention kernels read queries before they wait)
     if (!a.whole) grid_launch_dependents();
     prefetch_tables(a, (int64_t)threadIdx.x * gridDim.x + blockIdx.x);
-    Share<kRows, kTok> sh = locate<kRows, kTok>(a, &m.red[0][0], pair, pairs, kThreads);
+    Share<kRows, kTok, false> sh = locate<kRows, kTok, false>(a, &m.red[0][0], pair, pairs, kThreads);
     const Ws ws = ws_of(a, pairs, V);
     if (lead && threadIdx.x == 0 && !by_context && !a.whole) leave(ws.rec + 4 * pair, 0, 0, 0, 0);
     tc::fence_before();
@@ -415,7 +415,7 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const int p_chunk = 4 * q2;
         const uint32_t p_full = at_rank(&m.p_full, 0), o_free = at_rank(&m.o_free, 0);
         const uint32_t s_free[2] = {at_rank(&m.s_free[0], 0), at_rank(&m.s_free[1], 0)};
-        if (sh.blind && lead) zero_blind<kRows, kTok>(a, pair, pairs, threadIdx.x - 128, kSoftmax, by_context ? ws.rec : nullptr);
+        if (sh.blind && lead) zero_blind<kRows, kTok, false>(a, pair, pairs, threadIdx.x - 128, kSoftmax, by_context ? ws.rec : nullptr);
         int tile = 0;
         bool stop = false;  // the four warps leave together: they share a barrier
         for (int np = 0;; ++np) {

@@ -153,13 +153,14 @@ struct Piece {
 //     p0 + 1 + floor(min(k N + N - 1, n H - 1) / H)  tokens, p0 = L - n0 the first query's position,
 // A context counts kHead tiles more than it has, at its start: what its queries' load and the
 // storing of its output take.  Its tiles are, but for the last row tile, floor((k + c) / m) with m = TOK H / N and
-// c = floor((N - 1 + H (p0 + TOK)) / N): sums over k have a closed form.
-template <int N, int TOK>
+// c = floor((N - 1 + H (p0 + TOK)) / N): where N divides TOK, sums over k have a closed form.
+// ONE: a sequence's rows are one row tile at most (N rows hold any, as the transposed kernel's do); N need not divide TOK.
+template <int N, int TOK, bool ONE>
 struct Walk {
     int s, k, R;           // sequence, row tile, row tiles of the sequence
     int L, q0, nH, p0, k0; // k0: first row tile with a query that sees a token
     bool flagged;
-    __device__ __forceinline__ void open(const Args &a, int seq) {
+    __host__ __device__ __forceinline__ void open(const Args &a, int seq) {
         s = seq;
         const Seq q = sequence(a, seq);
         flagged = q.flagged;
@@ -170,36 +171,50 @@ struct Walk {
         if (blind == q.n) k0 = R;
         k = k0;
     }
-    __device__ __forceinline__ int end(const Args &a, int kk) const {  // tokens row tile kk sees
+    __host__ __device__ __forceinline__ int end(const Args &a, int kk) const {  // tokens row tile kk sees
         if (!a.q_starts) return L;
         const int last = min((kk + 1) * N, nH) - 1;
         return min(L, p0 + 1 + by_heads(a, last));
     }
-    __device__ __forceinline__ int tiles(const Args &a, int kk) const { return (end(a, kk) + TOK - 1) / TOK; }
+    __host__ __device__ __forceinline__ int tiles(const Args &a, int kk) const { return (end(a, kk) + TOK - 1) / TOK; }
     // tiles, heads included, of row tiles k0 .. kk - 1, kk < R
-    __device__ __forceinline__ int64_t before(const Args &a, int kk) const {
+    __host__ __device__ __forceinline__ int64_t before(const Args &a, int kk) const {
+        static_assert(!ONE && TOK % N == 0 && (N & (N - 1)) == 0, "the closed form");
         if (kk <= k0) return 0;
-        constexpr int kPer = TOK / N;  // (N divides TOK)
-        const int64_t c = (N - 1 + (int64_t)a.H * (p0 + TOK)) >> (N == 16 ? 4 : N == 32 ? 5 : N == 64 ? 6 : 7);  // floor: p0 may be below -TOK
+        constexpr int kPer = TOK / N;
+        const int64_t x = N - 1 + (int64_t)a.H * (p0 + TOK), c = (x - (x & (N - 1))) / N;  // floor: p0 may be below -TOK
         return G(a, kk + c, kPer) - G(a, k0 + c, kPer) + (int64_t)kHead * (kk - k0);
     }
-    static __device__ __forceinline__ int64_t G(const Args &a, int64_t x, int per) {  // sum of floor(j / m), j < x, m = per H
+    static __host__ __device__ __forceinline__ int64_t G(const Args &a, int64_t x, int per) {  // sum of floor(j / m), j < x, m = per H
         const int64_t y = x / per, m = (int64_t)per * a.H;
         const int64_t q = (uint64_t)y < (1ull << 31) ? by_heads(a, (int)y) : y / a.H;
         return m * (q * (q - 1) / 2) + q * (x - q * m);
     }
-    __device__ __forceinline__ int64_t total(const Args &a) const {
+    __host__ __device__ __forceinline__ int64_t total(const Args &a) const {
         if (k0 >= R) return 0;
-        if (!a.q_starts) return (int64_t)R * (tiles(a, 0) + kHead);  // one query: every row tile sees all
-        return before(a, R - 1) + tiles(a, R - 1) + kHead;
+        if constexpr (ONE) return tiles(a, 0) + kHead;
+        else return before(a, R - 1) + tiles(a, R - 1) + kHead;
+    }
+    // The row tile that tile `off` of the sequence, heads included, falls in; off then counts from its start.
+    __host__ __device__ __forceinline__ void find(const Args &a, int64_t &off) {
+        k = k0;
+        if constexpr (!ONE) {
+            int hi = R;  // the last k with before(k) <= off
+            while (hi - k > 1) {
+                const int mid = (k + hi) >> 1;
+                if (before(a, mid) <= off) k = mid;
+                else hi = mid;
+            }
+            off -= before(a, k);
+        }
     }
 };
 
 // A CTA's (or CTA pair's) share of all contexts' tiles laid end to end, heads included: `parts` equal shares at
 // most, this one from tile `off` of context (w.s, w.k) on, `left` tiles.
-template <int N, int TOK>
+template <int N, int TOK, bool ONE>
 struct Share {
-    Walk<N, TOK> w;
+    Walk<N, TOK, ONE> w;
     int64_t off, left, last, total;
     int parts;
     bool over;   // the context of w has been handed out
@@ -244,8 +259,8 @@ struct Share {
 };
 
 // Zeros for a sequence's queries that see nothing, but for those in a row tile with others; by thread `me` of `threads`.
-template <int N, int TOK>
-__device__ __forceinline__ void zero_blind(const Args &a, const Walk<N, TOK> &w, int me, int threads) {
+template <int N, int TOK, bool ONE>
+__device__ __forceinline__ void zero_blind(const Args &a, const Walk<N, TOK, ONE> &w, int me, int threads) {
     const int64_t vecs = min((int64_t)w.k0 * N, (int64_t)w.nH) * (a.V / 8);
     uint4 *o = reinterpret_cast<uint4 *>((unsigned char *)a.out + (int64_t)w.q0 * a.H * a.V * 2);
     for (int64_t i = me; i < vecs; i += threads) o[i] = make_uint4(0, 0, 0, 0);
@@ -254,17 +269,17 @@ __device__ __forceinline__ void zero_blind(const Args &a, const Walk<N, TOK> &w,
 // Share `id` of at most `most`: each of the block's `threads` threads sums the tiles of a run of sequences, and
 // the one whose run holds the share's first tile finds it.  By the whole block; `scratch`: 1 KB of shared memory,
 // free after the block's next barrier.
-template <int N, int TOK>
-__device__ __forceinline__ Share<N, TOK> locate(const Args &a, float *scratch, int id, int most, int threads) {
+template <int N, int TOK, bool ONE>
+__device__ __forceinline__ Share<N, TOK, ONE> locate(const Args &a, float *scratch, int id, int most, int threads) {
     int64_t *scan = reinterpret_cast<int64_t *>(scratch);  // the warps' totals; then where the share begins
-    Walk<N, TOK> &begin = *reinterpret_cast<Walk<N, TOK> *>(scan + 18);
+    Walk<N, TOK, ONE> &begin = *reinterpret_cast<Walk<N, TOK, ONE> *>(scan + 18);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int run = (a.S + threads - 1) / threads;
     const int sb = min(a.S, (int)threadIdx.x * run), se = min(a.S, sb + run);
     int64_t mine = 0;
     bool blind = false;
-    Share<N, TOK> r;
-    Walk<N, TOK> &w = r.w;
+    Share<N, TOK, ONE> r;
+    Walk<N, TOK, ONE> &w = r.w;
     if (a.whole) {
         const int s = id / a.whole, k = id - s * a.whole;
         r.off = r.left = r.last = r.total = r.parts = 0;
@@ -321,19 +336,7 @@ __device__ __forceinline__ Share<N, TOK> locate(const Args &a, float *scratch, i
             if (off < t || s + 1 >= se) break;
             off -= t;
         }
-        if (!a.q_starts) {
-            const int per = w.tiles(a, 0) + kHead;
-            for (w.k = 0; off >= per; ++w.k) off -= per;  // (a few row tiles)
-        } else {
-            int lo = w.k0, hi = w.R;  // the last k with before(k) <= off
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (w.before(a, mid) <= off) lo = mid;
-                else hi = mid;
-            }
-            w.k = lo;
-            off -= w.before(a, lo);
-        }
+        w.find(a, off);
         begin = w;
         scan[16] = off;
     }
@@ -351,10 +354,10 @@ __device__ __forceinline__ void leave(int *rec, int row0, int rows, int pieces, 
 
 // The same for sequences first, first + step, ...; and, where `rec` has a record for each context, those of sequences without
 // tokens: nothing to join.
-template <int N, int TOK>
+template <int N, int TOK, bool ONE>
 __device__ __forceinline__ void zero_blind(const Args &a, int first, int step, int me, int threads, int *rec) {
     for (int s = first; s < a.S; s += step) {
-        Walk<N, TOK> w;
+        Walk<N, TOK, ONE> w;
         w.open(a, s);
         zero_blind(a, w, me, threads);
         if (rec && me == 0 && w.k0 >= w.R) leave(rec + 4 * s, 0, 0, 0, 0);
