@@ -307,10 +307,11 @@ pkv_status run(Args &a, float scale, size_t ws_bytes, int dtype, void *stream) {
     if (!known_shape(a.H, a.V)) return PKV_ERR_UNSUPPORTED;
     if (a.B != 8 && a.B != 16 && a.B != 32 && a.B != 64) return PKV_ERR_UNSUPPORTED;
     if (a.S == 0 || a.T == 0) return PKV_OK;
-    // positions, cache rows and query rows of 31 bits, with room for a tile past the last
+    // positions, cache rows, query rows and sequences of 31 bits, with room for a tile (or the sequences of a block's threads)
+    // past the last
     if ((int64_t)a.maxb * a.B > 0x7ffff000ll) return PKV_ERR_INVALID;
     if ((int64_t)a.NB * a.B > 0x7fffffffll) return PKV_ERR_UNSUPPORTED;
-    if ((int64_t)a.T * a.H > 0x7ffff000ll) return PKV_ERR_UNSUPPORTED;
+    if ((int64_t)a.T * a.H > 0x7ffff000ll || a.S > 0x7ffff000) return PKV_ERR_UNSUPPORTED;
     if (!a.out || !a.q || !a.cache || !a.tables || !a.lens) return PKV_ERR_INVALID;
     if (!aligned16(a.out) || !aligned16(a.q) || !aligned16(a.cache)) return PKV_ERR_INVALID;
     a.max_len = (int)((int64_t)a.max_len < (int64_t)a.maxb * a.B ? a.max_len : (int64_t)a.maxb * a.B);
