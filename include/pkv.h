@@ -475,14 +475,15 @@ PKV_EXPORT pkv_status paged_attention_multi_token_scored(
  * negative frequencies may be given to the calls too.
  *
  *   out, x         device [num_tokens][num_heads][head_dim], dtype, 16-byte
- *                  aligned.  out may be x, with x's strides; otherwise they must
- *                  not overlap.
+ *                  aligned.  out may be x, with x's strides (with others the
+ *                  call is refused); otherwise they must not overlap.
  *   positions      device int32 [num_tokens], any value
  *   frequencies    device float64 [rotary_dim / 2]; infinite, NaN and subnormal
  *                  ones count as 0
  *   strides        host int64 [4] or NULL (contiguous): entries from token to
  *                  token and from head to head, of out and of x, each a multiple
- *                  of 16 bytes (slices of a fused projection)
+ *                  of 16 bytes (slices of a fused projection), of either sign, in
+ *                  any order; rows of out that overlap are refused
  *   amplitude      finite (the scale of long-context variants, else 1)
  *   interleaved    0 or 1
  * Supported: head_dim, rotary_dim and offset multiples of 16, rotary_dim <= 256,

@@ -272,13 +272,36 @@ pkv_status check_rotation(int num_tokens, int dim, int rotary_dim, int offset, f
 
 constexpr int kMaxUnits = 65535;  // of one token's rows
 
-// Strides in entries: whole 16-byte vectors, and no two rows written to one place.
+// Strides in entries: whole 16-byte vectors.
 bool strides_ok(const int64_t *s, int n, int64_t elt) {
     for (int i = 0; i < n; ++i)
         if (s[i] > (int64_t)1 << 56 || s[i] < -((int64_t)1 << 56) || (s[i] * elt) & 15) return false;
     return true;
 }
-bool writes_apart(const int64_t *s, int tokens, int heads) { return (tokens < 2 || s[0] != 0) && (heads < 2 || s[1] != 0); }
+
+// Whether rows of `dim` entries, token and head strides s, lie apart: no i < tokens and j < heads but (0, 0) with
+// |i s[0] +- j s[1]| < dim.
+bool rows_apart(const int64_t *s, int tokens, int heads, int dim) {
+    uint64_t st = (uint64_t)(s[0] < 0 ? -s[0] : s[0]), sh = (uint64_t)(s[1] < 0 ? -s[1] : s[1]), n = (uint64_t)tokens, d = (uint64_t)dim;
+    if (heads < 2) return tokens < 2 || st >= d;
+    if (sh < d) return false;
+    if (tokens < 2) return true;
+    if (st < d) return false;
+    // one kind of steps within the other's, as in all usual layouts
+    if (st >= sh ? (st - d) / sh >= (uint64_t)(heads - 1) : (sh - d) / st >= n - 1) return true;
+    for (int j = 1; j < heads; ++j) {
+        const unsigned __int128 x = (unsigned __int128)sh * (unsigned)j, i = x / st;
+        const uint64_t r = (uint64_t)(x % st);
+        if ((i < n && r < d) || (i + 1 < n && st - r < d)) return false;
+    }
+    return true;
+}
+
+// Rows written (s[0], s[1]) and read (s[2], s[3]): written rows lie apart, and are the rows read where out is x.
+bool rows_ok(const void *out, const void *x, const int64_t *s, int tokens, int heads, int dim) {
+    if (out == x && ((tokens > 1 && s[0] != s[2]) || (heads > 1 && s[1] != s[3]))) return false;
+    return rows_apart(s, tokens, heads, dim);
+}
 
 }  // namespace
 
@@ -318,7 +341,7 @@ PKV_API pkv_status rotary_embed(void *out, const void *x, const int32_t *positio
     const int64_t elt = dtype == PKV_F32 ? 4 : 2;
     const int64_t dense[4] = {(int64_t)num_heads * head_dim, head_dim, (int64_t)num_heads * head_dim, head_dim};
     const int64_t *s = strides ? strides : dense;
-    if (!strides_ok(s, 4, elt) || !writes_apart(s, num_tokens, num_heads)) return PKV_ERR_INVALID;
+    if (!strides_ok(s, 4, elt) || !rows_ok(out, x, s, num_tokens, num_heads, head_dim)) return PKV_ERR_INVALID;
     RotArgs a{};
     a.positions = positions;
     a.freqs = frequencies;
@@ -351,7 +374,7 @@ PKV_API pkv_status kv_cache_write_rotary(void *q_out, const void *q, const void 
     const int64_t elt = dtype == PKV_F32 ? 4 : 2, D = head_dim, qd = num_heads * D, kd = num_kv_heads * D;
     const int64_t dense[8] = {qd, D, qd, D, kd, D, kd, D};
     const int64_t *s = strides ? strides : dense;
-    if (num_heads && (!strides_ok(s, 4, elt) || !writes_apart(s, num_tokens, num_heads))) return PKV_ERR_INVALID;
+    if (num_heads && (!strides_ok(s, 4, elt) || !rows_ok(q_out, q, s, num_tokens, num_heads, head_dim))) return PKV_ERR_INVALID;
     if (!strides_ok(s + 4, 4, elt)) return PKV_ERR_INVALID;
     RotArgs a{};
     a.slots = slot_mapping;
@@ -386,7 +409,7 @@ PKV_API pkv_status latent_cache_write(void *q_out, const void *q_rope, const voi
     const int64_t elt = dtype == PKV_F32 ? 4 : 2, row = latent_dim + kRope, qd = (int64_t)num_heads * kRope;
     const int64_t dense[6] = {qd, kRope, qd, kRope, latent_dim, kRope};
     const int64_t *s = strides ? strides : dense;
-    if (num_heads && (!strides_ok(s, 4, elt) || !writes_apart(s, num_tokens, num_heads))) return PKV_ERR_INVALID;
+    if (num_heads && (!strides_ok(s, 4, elt) || !rows_ok(q_out, q_rope, s, num_tokens, num_heads, kRope))) return PKV_ERR_INVALID;
     if (!strides_ok(s + 4, 2, elt)) return PKV_ERR_INVALID;
     RotArgs a{};
     a.slots = slot_mapping;
