@@ -325,6 +325,7 @@ PKV_API pkv_status rotary_frequencies(double *out, int rotary_dim, double base, 
             w = w < 0.0 ? 0.0 : w > 1.0 ? 1.0 : w;
         }
         out[i] = f * (w + (1.0 - w) / factor);
+        if (!std::isfinite(out[i])) return PKV_ERR_INVALID;  // (the calls would take it for 0)
     }
     return PKV_OK;
 }

@@ -62,3 +62,13 @@ def test_written_rows_that_overlap(call):
 def test_in_place_with_other_strides(call):
     for st in ((512, 64, 256, 64), (256, 64, 512, 64), (1024, 128, 1024, 64), (64, 320, 256, 64)):
         assert call(X, X, st, 5, 4, 64) == pkv.PKV_ERR_INVALID
+
+
+def test_frequencies_past_float64():
+    """Rotation takes an infinite or NaN frequency for 0: none is handed out."""
+    f, out = _lib.load().rotary_frequencies, (ctypes.c_double * 4)()
+    assert f(out, 8, 1e-300, 1e-60, 0.0, 1.0, 32.0) == pkv.PKV_OK and out[3] == pytest.approx(1e285, rel=1e-9)
+    assert f(out, 8, 1e-300, 1e-100, 0.0, 1.0, 32.0) == pkv.PKV_ERR_INVALID              # infinite
+    assert f(out, 8, 1e-300, 4.0, 1e200, -1e308, 1e308) == pkv.PKV_ERR_INVALID           # infinity over infinity
+    with pytest.raises(pkv.PkvError):
+        pkv.rotary_frequencies(8, base=1e-300, factor=1e-100)
