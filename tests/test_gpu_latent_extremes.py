@@ -1,4 +1,4 @@
-"""GPU: latent attention where scores pass float32's range."""
+"""GPU: latent attention where scores pass float32's range, or are very large."""
 import numpy as np
 import pytest
 import torch
@@ -154,3 +154,43 @@ def test_an_infinite_query_on_pairs_whose_scores_are_all_minus_infinity():
         assert torch.all(got[:, 2] == 0)
         keep = torch.arange(H) != 2
         assert torch.equal(got[:, keep], want[:, keep])
+
+
+def _sparse(H, V, dtype, queries, top, order, seed=7, lens=(150, 600)):
+    """Integers times a power of two, 24 entries of a query not zero: products and their sums are exact in float32 (up to the
+    scale), scores up to about ``top``."""
+    c = lc.make(list(lens), H, V, 16, dtype, queries, seed=seed, fill=0.0)
+    r = np.random.default_rng(seed)
+    T = c["q"].shape[0]
+    q = np.zeros((T, H, V + 64))
+    for t in range(T):
+        for h in range(H):
+            q[t, h, r.permutation(V + 64)[:24]] = r.integers(1, 9, 24) * r.choice([-1, 1], 24)
+    c["q"] = torch.from_numpy(q).to(dtype)
+    for x in c["rows"]:
+        y = r.integers(-8, 9, tuple(x.shape)).astype(np.float64)
+        if order:  # scores that rise or fall along the context
+            y *= 2.0 ** np.round(np.linspace(-3, 3, x.shape[0]) * order)[:, None]
+        x.copy_(torch.from_numpy(y).to(dtype))
+    biggest = max(np.abs(c["q"].double().numpy() @ x.double().numpy().T).max() for x in c["rows"])
+    return lm.store(c), top / biggest
+
+
+def _large_scores(H, V, dtype, queries, top, order, table):
+    c, scale = _sparse(H, V, dtype, queries, top, order)
+    scale = float(np.float32(scale))
+    if table:
+        c = lm.wide(c, table)
+    for sc in (scale, -scale):
+        want, tol = lm.expected(c, lm.none_dead(c), sc, terms=24, moves=2 + 600 // 48)
+        live = np.abs(want) > 1e-30
+        assert np.mean(np.abs(want[live]) > 4 * tol[live]) > 0.9  # (zeros, or signs turned, would not do)
+        lm.check(lc.run(c, scale=sc, max_len=10 ** 6), (want, tol))
+
+
+@pytest.mark.parametrize("table", [0, 8192])
+@pytest.mark.parametrize("top,order", [(30.0, 0), (1000.0, 0), (1000.0, 1), (1000.0, -1)])
+@pytest.mark.parametrize("H,V,dtype,queries", [(9, 512, BF, None), (64, 256, BF, None), (128, 512, BF, None), (4, 512, BF, [9, 3]), (5, 256, BF, [40, 3]),
+                                               (5, 512, F32, None), (3, 256, F32, [9, 3])])
+def test_large_scores(H, V, dtype, queries, top, order, table):
+    _large_scores(H, V, dtype, queries, top, order, table)
