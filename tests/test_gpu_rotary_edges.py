@@ -1,4 +1,4 @@
-"""GPU: rotary positions at the edges: every stride that keeps rows apart."""
+"""GPU: rotary positions at the edges: every stride that keeps rows apart, attention over what was written."""
 import ctypes
 
 import numpy as np
@@ -56,3 +56,38 @@ def test_rows_apart_in_any_order(T, H):
             assert call(p, p, ps.data_ptr(), f.data_ptr(), T, H, D, D, 0, st, 1.0, 0, pkv.PKV_BF16, stream) == pkv.PKV_OK
             assert torch.equal(flat, clean)
     assert met > 100
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,D,B", [(50, 8, 2, 64, 16), (77, 4, 4, 128, 32)])
+def test_attention_over_rows_that_were_rotated_and_written(T, Hq, Hkv, D, B):
+    """kv_cache_write_rotary stores what rotary_embed and kv_cache_write do, bit for bit; the attention calls read it, queries
+    and all: within the errors of their own arithmetic on the stored numbers (scores of D products and exponentials in
+    float32, weights and the output rounded to bf16)."""
+    from oracle.multi_token import multi_token_attention
+    qkv = _rows((T, Hq + 2 * Hkv, D), BF, 8).cuda()
+    f, at = pkv.rotary_frequencies(D, device="cuda"), torch.arange(T, device="cuda")
+    tables = torch.tensor([[5, 2, 7, 0]], dtype=torch.int32, device="cuda")
+    slots = tables[0].long()[at // B] * B + at % B
+    kc, vc, kc2, vc2 = (torch.full((8, Hkv, B, D), float("nan"), dtype=BF, device="cuda") for _ in range(4))
+    q, q2 = (torch.empty((T, Hq, D), dtype=BF, device="cuda") for _ in range(2))
+    k, v = qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
+    pkv.kv_cache_write_rotary(k, v, kc, vc, slots, at.int(), f, q=qkv[:, :Hq], q_out=q)
+    rot = torch.empty((T, Hkv, D), dtype=BF, device="cuda")
+    pkv.rotary_embed(rot, k, at.int(), f)
+    pkv.rotary_embed(q2, qkv[:, :Hq], at.int(), f)
+    pkv.kv_cache_write(rot, v.contiguous(), kc2, vc2, slots)
+    bits = lambda x: x.view(torch.int16)  # noqa: E731  (NaN in unused slots)
+    assert torch.equal(q, q2) and torch.equal(bits(kc), bits(kc2)) and torch.equal(bits(vc), bits(vc2))
+    lens = torch.tensor([T], dtype=torch.int32, device="cuda")
+    out, one = torch.empty_like(q), torch.empty((1, Hq, D), dtype=BF, device="cuda")
+    pkv.paged_attention_multi_token(out, q, kc, vc, tables, lens, torch.tensor([0, T], dtype=torch.int32, device="cuda"), 0.125, T, T)
+    pkv.paged_attention_decode(one, q[-1:].contiguous(), kc, vc, tables, lens, 0.125, T)
+    qd, kd, vd = (x.double().cpu().numpy() for x in (q, rot, v))
+    ref, = multi_token_attention([qd], [kd], [vd], 0.125)
+    spread, = multi_token_attention([qd], [kd], [np.abs(vd)], 0.125)
+    g = Hq // Hkv
+    reach = 0.125 * max((np.abs(qd[:, h]) @ np.abs(kd[:, h // g]).T).max() for h in range(Hq))
+    rel = 2 * (reach * (D + 4) * 2.0 ** -24 + 2.0 ** -21 + (T + 2) * 2.0 ** -24) + 2 * 2.0 ** -8
+    tol = rel * spread + 2.0 ** -8 * np.abs(ref)
+    assert np.all(np.abs(out.double().cpu().numpy() - ref) <= tol)
+    assert np.all(np.abs(one.double().cpu().numpy()[0] - ref[-1]) <= tol[-1])
