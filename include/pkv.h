@@ -464,8 +464,9 @@ PKV_EXPORT pkv_status paged_attention_multi_token_scored(
  *     y1 = x1 c - x2 s,  y2 = x2 c + x1 s,  c = a cos(p f_i),  s = a sin(p f_i)
  * with a = amplitude, computed in float32 and rounded once; the row's other
  * entries are copied.  Pairs are the entries (i, i + R / 2) of the rotated part,
- * or (2 i, 2 i + 1) if interleaved.  The angle is exact modulo a turn for every
- * position of 32 bits (no float32 product of position and frequency).
+ * or (2 i, 2 i + 1) if interleaved.  The angle is off by at most
+ * |p| (2^-64 + |f_i| 2^-72) turns, for every position of 32 bits (no float32
+ * product of position and frequency).
  *
  * rotary_frequencies -- host function: out[i] = base^(-2 i / R), i < R / 2, for
  * longer contexts than a model was trained on divided by `factor`
@@ -563,11 +564,15 @@ PKV_EXPORT pkv_status kv_cache_write_rotary(void *q_out, const void *q, const vo
  * of out that no query owns are left as they were.  Out-of-range lengths, query
  * starts and blocks are flagged as in the other calls; the tokens of a bad block
  * are left out, and where query starts decrease it is unspecified which sequence's
- * results the rows in question hold.  BF16: weights may pass 1 by up to 2^8 before
- * they are scaled back, so latent entries above 2^119 may overflow, and infinities
- * and NaN in a row may make NaN of any entry of the queries that see it.  Cache rows that a query does not see never reach its output,
- * whatever they hold.  Results do not depend on which physical blocks hold the
- * tokens.
+ * results the rows in question hold.
+ * Large numbers: a score is -infinity or +infinity where (scale * q) . c (F32) or
+ * q . c or scale times it (BF16) passes float32's range; the first is a weight of
+ * 0, the second makes the query's output NaN.  Sums are scaled back at the end, of
+ * weights of at most 1 (F32) or 2^8 (BF16): latent entries may overflow above
+ * 2^128 (F32) or 2^120 (BF16) divided by the tokens a query sees.  Infinities and
+ * NaN in a row may make NaN of any entry of the queries that see it (BF16).
+ * Cache rows that a query does not see never reach its output, whatever they hold.
+ * Results do not depend on which physical blocks hold the tokens.
  */
 #define PKV_LATENT_ROPE_DIM 64
 PKV_EXPORT pkv_status latent_cache_write(void *q_out, const void *q_rope, const void *latent, const void *k_rope, void *cache,

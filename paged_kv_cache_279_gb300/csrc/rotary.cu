@@ -9,7 +9,8 @@
 // Angles.  In float32 the product p f_i of a far position is off by up to
 // 2^-25 of itself, 0.03 radians at a million.  Here it is held in turns as a
 // 64-bit binary fraction: f_i / 2 pi = G 2^-64 once, then p G modulo 2^64 is the
-// angle modulo one turn, exact but for G's last place (p 2^-64 turns), in one
+// angle modulo one turn, off by p times G's error (its last place, and f_i 2^-72 of
+// the constant's 64 bits: p (2^-64 + f_i 2^-72) turns at most), in one
 // integer multiplication, with no 64-bit floating point and no table of
 // positions.  Its signed value converts to float32 half turns with a relative
 // error of 2^-24, and sincospif needs no range reduction there.
@@ -67,7 +68,7 @@ __device__ __forceinline__ uint32_t div16(uint32_t n, uint32_t d, uint32_t magic
 
 // f / 2 pi modulo 1 in 64 binary places, truncated: f = m 2^(e - 52) with a
 // 53-bit m, and 2^66 / 2 pi = 11743562013128004905.985, so
-// f / 2 pi 2^64 = (m 11743562013128004906) 2^(e - 54).  Zero, subnormal, infinite and NaN
+// f / 2 pi 2^64 = (m 11743562013128004906) 2^(e - 54), too large by 2^-69.4 of itself.  Zero, subnormal, infinite and NaN
 // frequencies give 0.
 __device__ __forceinline__ uint64_t turns64(double f) {
     const uint64_t b = (uint64_t)__double_as_longlong(f);

@@ -1,4 +1,4 @@
-"""GPU: latent attention where scores pass float32's range, or are very large."""
+"""GPU: latent attention where scores pass float32's range, or scores or latent entries are very large."""
 import numpy as np
 import pytest
 import torch
@@ -194,3 +194,20 @@ def _large_scores(H, V, dtype, queries, top, order, table):
                                                (5, 512, F32, None), (3, 256, F32, [9, 3])])
 def test_large_scores(H, V, dtype, queries, top, order, table):
     _large_scores(H, V, dtype, queries, top, order, table)
+
+
+@pytest.mark.parametrize("rise", [0.0, 5.4, 100.0])
+@pytest.mark.parametrize("H,dtype,queries", [(9, BF, None), (64, BF, None), (100, BF, None), (5, BF, [40, 3]), (5, F32, None)])
+def test_the_largest_latent_entries(H, dtype, queries, rise):
+    """Just below 2^120 over the tokens in bf16, 2^128 over them in float32: the sums stay finite, also where scores rise along
+    the context, by almost 2^8 in weight before the reference moves, or by far more."""
+    c = lc.make([255, 100], H, 512, 16, dtype, queries, fill=0.0)
+    c["q"][..., :512] = 0.0  # (the latent entries are part of the keys)
+    c["q"][..., 512:] *= 0.1
+    c["q"][..., 575] = 1.0
+    for x in c["rows"]:
+        x[:, :512] = (torch.sign(x[:, :512].float()) * (2.0 ** 112 if dtype == BF else 2.0 ** 120)).to(dtype)
+        x[:, :7] = x[:, :7].abs()  # entries whose sums do not cancel
+        x[:, 575] = torch.linspace(0.0, rise / lc.SCALE, x.shape[0]).to(dtype)
+    lc.check(lc.run(lm.store(c)), c)
+    lc.check(lc.run(lm.wide(c), max_len=10 ** 6), c)

@@ -1,4 +1,4 @@
-"""GPU: rotary positions at the edges: every stride that keeps rows apart, attention over what was written."""
+"""GPU: rotary positions at the edges: every stride that keeps rows apart, attention over what was written, large frequencies."""
 import ctypes
 
 import numpy as np
@@ -6,10 +6,11 @@ import pytest
 import torch
 
 import paged_kv_cache_279_gb300 as pkv
+from oracle import rotary
 from paged_kv_cache_279_gb300 import _lib
 
 pytestmark = pytest.mark.gpu
-BF = torch.bfloat16
+BF, F32 = torch.bfloat16, torch.float32
 
 
 @pytest.fixture(autouse=True)
@@ -91,3 +92,19 @@ def test_attention_over_rows_that_were_rotated_and_written(T, Hq, Hkv, D, B):
     tol = rel * spread + 2.0 ** -8 * np.abs(ref)
     assert np.all(np.abs(out.double().cpu().numpy() - ref) <= tol)
     assert np.all(np.abs(one.double().cpu().numpy()[0] - ref[-1]) <= tol[-1])
+
+
+def test_large_frequencies():
+    """Angles within |p| (2^-64 + |f| 2^-72) turns, then the roundings of float32 (2^-21 of the pair)."""
+    pos = np.array([1, -1, 1000, -77777, 10 ** 6, 2 ** 31 - 1, -2 ** 31], dtype=np.int64)
+    f = np.array([1e3, 1e6, 2.0 ** 30 + 0.1, 1e9, -1e10, 1e11, 1e12, 3e5])
+    x = _rows((len(pos), 3, 16), F32, 5)
+    out = torch.empty_like(x, device="cuda")
+    pkv.rotary_embed(out, x.cuda(), torch.from_numpy(pos).int().cuda(), torch.from_numpy(f).cuda())
+    x64 = x.double().numpy()
+    want = rotary.rotate(x64, pos, f, far=True)
+    angle = 2 * np.pi * np.abs(pos)[:, None] * (2.0 ** -64 + np.abs(f) * 2.0 ** -72)
+    pair = np.abs(x64[..., :8]) + np.abs(x64[..., 8:])
+    tol = np.concatenate([(2.0 ** -21 + angle)[:, None] * pair] * 2, -1)
+    assert np.all(np.abs(out.double().cpu().numpy() - want) <= tol)
+    assert np.median(tol / (np.abs(want) + 1e-30)) < 1e-5  # (most of these angles are as good as exact)
