@@ -148,3 +148,15 @@ def test_cut_calls_repeat_themselves_in_graphs_too(queries, H):
     lens -= 1
     graphs[1].replay()
     lc.check(outs[1], dict(c, lens=[x - 1 for x in c["lens"]], rows=[x[:-1] for x in c["rows"]]))
+
+
+@pytest.mark.parametrize("dtype,H,n", [(F32, 3, 4), (BF, 16, 4), (BF, 16, 40), (BF, 100, 5)])
+@pytest.mark.parametrize("table", [0, 8192])
+def test_a_batch_without_queries(dtype, H, n, table):
+    """No sequence owns a row: nothing is written; empty sequences around one that does, and empty contexts among them."""
+    c = lc.make([100, 64, 50], H, 512, 16, dtype, queries=[0, n, 0])
+    c = lm.wide(c, table) if table else c
+    got = lc.run(dict(c, starts=np.zeros(4, dtype=np.int32)), max_len=10 ** 6)
+    assert torch.all(got == 7.0)
+    got = lc.run(dict(c, lens=[0, 64, 0]), max_len=10 ** 6)
+    lc.check(got, c)

@@ -33,9 +33,9 @@ def _tokens(which, L):
     return t
 
 
-def _overflow(which, heads, H, V, dtype, queries, at, sign=-1.0, lens=(150, 77), power=64):
+def _overflow(which, heads, H, V, dtype, queries, at, sign=-1.0, lens=(150, 77), power=64, B=16):
     """A case of finite numbers, some products 2^(2 power + 1) in size: (case, dead tokens a sequence)."""
-    c = lc.make(list(lens), H, V, 16, dtype, queries, seed=3, fill=0.0)
+    c = lc.make(list(lens), H, V, B, dtype, queries, seed=3, fill=0.0)
     e = V + 5 if at == "key" else 9
     some = np.ones(H, dtype=bool) if heads == "all" else np.arange(H) % 2 == 1
     c["q"][:, :, e] = torch.from_numpy(np.where(some, 2.0 ** power, 0.0)).to(dtype)
@@ -106,10 +106,10 @@ def test_an_infinite_query_whose_scores_are_all_minus_infinity(dtype, H, queries
     assert torch.equal(got[:, keep], want[:, keep])
 
 
-def _bad_row_beside(H, queries, at, bad, table):
+def _bad_row_beside(H, queries, at, bad, table, V=512, B=16):
     """Token 60 holds something that is no number, 57 and 70 have scores of -infinity: who does not see 60 is not touched by it."""
-    c, dead = _overflow("none", "all", H, 512, BF, queries, "key", lens=(90, 77))
-    e = 512 + 5
+    c, dead = _overflow("none", "all", H, V, BF, queries, "key", lens=(90, 77), B=B)
+    e = V + 5
     for t in (57, 70):
         c["rows"][0][t, e] = -2.0 ** 65
         dead[0][:, t] = True
@@ -117,14 +117,14 @@ def _bad_row_beside(H, queries, at, bad, table):
     want = lc.run(c, max_len=10 ** 6)
     lm.check(want, lm.expected(c, dead))
     cache = c["cache"].clone()
-    cache[int(c["tables"][0][60 // 16]), 60 % 16, at] = bad
+    cache[int(c["tables"][0][60 // B]), 60 % B, at] = bad
     got = lc.run(c, cache=cache.cuda(), max_len=10 ** 6)
     n = c["nq"][0]
     sees = torch.zeros(want.shape[0], dtype=torch.bool)
     sees[max(0, 60 - (90 - n)):n] = True
     assert torch.equal(got[~sees.cuda()], want[~sees.cuda()])
-    if at < 512 or bad != bad:
-        assert torch.all(~torch.isfinite(got[sees.cuda()][..., min(at, 511)]))
+    if at < V or bad != bad:
+        assert torch.all(~torch.isfinite(got[sees.cuda()][..., min(at, V - 1)]))
 
 
 @pytest.mark.parametrize("at", [33, 512 + 40])
@@ -141,6 +141,14 @@ def test_a_row_that_is_no_number_beside_such_scores(H, queries, at, bad, table):
 @pytest.mark.parametrize("H,queries", [(2, [50, 9]), (16, [40, 9]), (128, None), (70, [3, 2])])
 def test_a_row_that_is_no_number_beside_such_scores_on_pairs(H, queries, at, bad, table):
     _bad_row_beside(H, queries, at, bad, table)
+
+
+@pytest.mark.parametrize("at", [0, 130, 255])
+@pytest.mark.parametrize("bad", [float("nan"), -float("inf")])
+@pytest.mark.parametrize("table", [0, 8192])
+@pytest.mark.parametrize("H,queries,B", [(64, None, 8), (2, [25, 9], 64), (5, [3, 2], 32), (2, [50, 9], 8), (100, None, 64)])
+def test_a_row_that_is_no_number_in_256_entries(H, queries, B, at, bad, table):
+    _bad_row_beside(H, queries, at, bad, table, V=256, B=B)
 
 
 def test_an_infinite_query_on_pairs_whose_scores_are_all_minus_infinity():

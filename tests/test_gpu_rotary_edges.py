@@ -108,3 +108,21 @@ def test_large_frequencies():
     tol = np.concatenate([(2.0 ** -21 + angle)[:, None] * pair] * 2, -1)
     assert np.all(np.abs(out.double().cpu().numpy() - want) <= tol)
     assert np.median(tol / (np.abs(want) + 1e-30)) < 1e-5  # (most of these angles are as good as exact)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_rows_read_more_than_once(dtype):
+    """One row for all heads or all tokens (steps of 0 where rows are read), and slots of no token."""
+    T, H, D, B = 7, 5, 64, 16
+    f, ps = pkv.rotary_frequencies(D, device="cuda"), torch.arange(T, dtype=torch.int32, device="cuda") * 9
+    for x in (_rows((T, 1, D), dtype, 1).cuda().expand(T, H, D), _rows((1, H, D), dtype, 2).cuda().expand(T, H, D)):
+        want, out = torch.empty((T, H, D), dtype=dtype, device="cuda"), torch.empty((T, H, D), dtype=dtype, device="cuda")
+        pkv.rotary_embed(want, x.contiguous(), ps, f)
+        assert torch.equal(pkv.rotary_embed(out, x, ps, f), want)
+        kc, vc = torch.full((2, H, B, D), 7.0, dtype=dtype, device="cuda"), torch.full((2, H, B, D), 7.0, dtype=dtype, device="cuda")
+        slots = torch.tensor([3, -1, 17, 0, 31, -5, 16], device="cuda")
+        pkv.kv_cache_write_rotary(x, x, kc, vc, slots, ps, f)
+        for t, s in enumerate(slots.tolist()):
+            if s >= 0:
+                assert torch.equal(kc[s // B, :, s % B], want[t]) and torch.equal(vc[s // B, :, s % B], x[t])
+        assert int((kc == 7.0).all(-1).sum()) == H * (2 * B - 5)
