@@ -560,6 +560,11 @@ PKV_EXPORT pkv_status kv_cache_write_rotary(void *q_out, const void *q, const vo
  *                  (num_q_tokens: num_seqs for decode), 256-byte aligned, NULL
  *                  where that is 0.  Needs no initialisation; calls that share one
  *                  must be ordered on the device.
+ * Limits that are near what the call holds make it faster: BF16 calls of more than
+ * 64 query rows a sequence (num_heads, times max_q_len) go to a kernel of 128 rows,
+ * all sequences alike, and contexts are attended in one piece only where max_seq_len
+ * and the block table's width allow few tokens.  F32 reads a context once for every
+ * four heads of every query: meant for decode and few queries.
  * A query that sees no token, or whose scores are all -infinity, gets zeros.  Rows
  * of out that no query owns are left as they were.  Out-of-range lengths, query
  * starts and blocks are flagged as in the other calls; the tokens of a bad block

@@ -674,10 +674,10 @@ def _embed_plan(x, x_stride, out, out_stride, positions, frequencies):
 
 def rotary_embed(out, x, positions, frequencies, amplitude: float = 1.0, interleaved: bool = False, offset: int = 0,
                  stream=None) -> torch.Tensor:
-    """Rotate rows x [T, H, D] (bf16 or float32) by their positions (int32 [T]) into out, which may be x: the
+    """Rotate rows x [T, H, D] (bf16 or float32) by their positions (int32 [T]) into out, which may be x itself: the
     entries from `offset` on, in pairs (i, i + R / 2) or, interleaved, (2 i, 2 i + 1), R = 2 * len(frequencies)
     (float64, radians per position); pair i turns by position * frequencies[i], scaled by `amplitude`.  Tokens
-    and heads may be strided, in steps of 16 bytes."""
+    and heads may be strided, in steps of 16 bytes; rows of out must not overlap."""
     size, strides = _embed_plan(x.shape, x.stride(), out.shape, out.stride(), positions.shape, frequencies.shape)
     dev, dt = _device_of(x, "x"), x.dtype
     _run_on(dev, "rotary_embed", _lib.load().rotary_embed, (

@@ -14,7 +14,8 @@
 // lanes hold the heads' queries, the running output and the rows of the batch in
 // registers, split over the row's entries, so each row is read from memory once a
 // warp in 16-byte loads and used for kRW heads.  The kRW * kTok sums over the lanes
-// are formed by exchanging halves (16 shuffles for 16 sums, not 80).  Bound by
+// are formed by exchanging halves (16 shuffles for 16 sums, not 80).  Nothing is shared
+// between queries: each reads its context once for every kRW heads.  Bound by
 // float32 arithmetic: (2 V + 64) FMAs a head and token.  4 sequences of up to 100
 // tokens, 4 heads: 8.7 us, of which four dependent loads (length, block, row, and the
 // query's) are half.

@@ -26,8 +26,9 @@
 //
 // What bounds it: DRAM while tiles stream (what 32000 tokens more a context cost, 8 contexts: 6.7 TB/s at 16 and 32 rows,
 // 6.3 at 64, of 6.7), before that a chain of loads (lengths, block table, first tile: 3.2 us until it is asked for), after
-// it the join (1.2 us between the kernels, 4 in it).  64 contexts of 64 to 2048 tokens, 32 heads: 24.8 us for 73 MB; 8 of
-// 16000, 64 heads: 41.2 us for 149 MB.  Joined in this kernel, by CTAs that wait for one another's pieces (two stages, as
+// it the join (1.2 us between the kernels, 4 in it), and shares that are equal in tiles but end up to 8 us apart.  64 contexts
+// of 64 to 2048 tokens, 32 heads: 24.9 us for 73 MB (all times here from CUDA graphs of many calls); 8 of 16000, 64 heads:
+// 41.2 us for 149 MB.  Joined in this kernel, by CTAs that wait for one another's pieces (two stages, as
 // below), one context of 16000 took 20.0 us, not 22.7, but these 26.7 and 43.7, not 26.5 and 42.5, and 1 to 2 us more from a
 // host's stream of calls: such a launch is a cooperative one.
 // A tile of 64 takes 36 + 16 products, 1452 cycles at 16 rows, 1920 at 64 (operand bytes out of
@@ -83,7 +84,8 @@ struct L {
     static constexpr int kChunks = V / 64 + 1;
     // Tokens of a tile: 64, or 48 where three stages of those fit and two of 64: a stage is loaded anew when its tile's last
     // product is done, and with two nothing is under way for half of that time.  64 contexts of 64 to 2048, 32 heads, 26.5 ->
-    // 24.8 us, 140, 16 heads, 38.9 -> 35.9, one of 16000 22.6 -> 18.9; 4 of 64, 32 heads, 7.1 -> 7.6; five stages of 32
+    // 24.8 us, 140, 16 heads, 38.9 -> 35.9, one of 16000 22.6 -> 18.9; some with few tiles to a share got slower: 4 of
+    // 64, 32 heads, 7.1 -> 7.6, 16 of 1024, 16 heads, 11.5 -> 12.4, 20 x 4 queries of 8 heads 18.8 -> 19.4.  Five stages of 32
     // tokens: 26.0, 37.9, 25.4.  (A product's 64 rows then reach into what lies behind the tile, for scores that no one
     // looks at.)
     static constexpr int kTok = V == 512 && N <= 32 ? 48 : 64, kAll = (1 << kTok / 8) - 1;

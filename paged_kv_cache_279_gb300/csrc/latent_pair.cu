@@ -16,8 +16,10 @@
 // The leader's (rank 0's) warps issue all products.  What the other CTA has ready it reports to the leader's
 // barriers; what the products have done arrives at both CTAs' barriers.
 //
-// Measured: 8 x 512 queries of 4096, 32 heads: 703 us (80 % of the measured bf16 rate), a tile 2300 to 2800 cycles where
-// its products are 2176; the transposed kernel took 1272.  4 prompts of 3200 to 4000 tokens, 16 heads: 566 us.
+// Measured, calls from a host in a row (from CUDA graphs): 8 x 512 queries of 4096, 32 heads, 708 us (679), 79 % (83 %) of the
+// measured bf16 rate, a tile 2300 to 2800 cycles where its products are 2176; the transposed kernel took 1272.  4 prompts of
+// 3200 to 4000 tokens, 16 heads: 576 us (556).  A decode of 64 contexts of 64 to 2048 tokens, 128 heads: 34.2 us from graphs, 2.6
+// times its floor: its tiles come from DRAM, twice (both forms) through the one stage there is, as for 64 x 5 queries (45.7).
 //
 // Softmax: a thread has one row and a quarter of the tile's tokens (eight warps: with four, whose exponentials alone
 // take 512 cycles of each scheduler, a tile took 3300 cycles, not 2200).  References, weights,

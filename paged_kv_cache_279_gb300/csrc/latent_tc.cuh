@@ -372,11 +372,13 @@ __device__ __forceinline__ void prefetch_tables(const Args &a, int64_t line) {
 }
 
 // Whether every context of a call gets a share of its own, uncut, and nothing is left to join by a second kernel: there
-// are shares enough, and the longest context there may be has few tiles -- 4, and up to 10 the more of the shares are
-// in use (lengths differ: the limit is for contexts that are half of it on average).  Uncut against cut, in us, 32 heads:
-// 4 sequences of 64 / 256 / 384 / 512 tokens 7.6 / 11.1 / 12.6 / 15.3 against 9.6 / 11.2 / 11.2 / 11.1; 64 sequences of
-// 64 / 256 / 512 / 1024: 7.9 / 12.1 / 17.5 / 27.6 against 10.1 / 15.4 / 19.0 / 25.0; in pairs of CTAs (128 heads), 64
-// sequences of 256 / 512 / 1024: 11.8 / 16.6 / 24.7 against 20.4 / 23.6 / 33.8.
+// are shares enough, and the longest context there may be has few tiles (of `tok` tokens: 64, also where the kernel's are 48,
+// or 128 in pairs of CTAs) -- 4, and up to 10 the more of the shares are
+// in use (lengths differ: the limit is for contexts that are half of it on average).  Uncut against cut, in us from graphs, 32
+// heads: 4 sequences of 64 / 128 / 256 tokens 7.8 / 8.6 / 11.2 against 9.7 / 11.0 / 11.2, and (uncut by hand) 384 / 512 tokens
+// 12.6 / 15.3 against 11.2 / 11.1; 64 sequences of 64 / 256 / 384: 7.9 / 12.0 / 14.3 against 10.1 / 15.3 / 18.2, by hand 512 /
+// 1024: 17.5 / 27.6 against 19.0 / 25.0; in pairs (128 heads), 64 sequences of 256 / 512 / 768: 11.7 / 17.2 / 21.3 against 20.7 /
+// 25.3 / 30.0.  The longest context is what the call's max_seq_len and the block table's width allow.
 // Returns the row tiles to count a sequence for, or 0.
 inline int whole_contexts(const Args &a, int n, int tok, int shares) {
     const int64_t tiles = (int64_t)a.rows / n + (a.rows % n != 0), most = (int64_t)a.maxb * a.B;
@@ -389,7 +391,7 @@ inline int whole_contexts(const Args &a, int n, int tok, int shares) {
 // quarter of L2 or more, so that no row is found there at the next step.  Block tables, queries, partial results and the
 // kernels' code then stay: 64 contexts of 64 to 2048 tokens, 32 heads, 26.2 -> 24.9 us, 128 heads 33.9 -> 32.7; 8 of 16000,
 // 64 heads, 45.0 -> 42.2.  Where it is not done: a pool of 18 MB read again and again, 18.8 us against 20.0; 8 x 512 queries
-// of 4096, whose rows are read by 128 row tiles, 674 against 894.
+// of 4096, whose rows are read by 128 row tiles, 674 against 894 (all from graphs).
 inline bool read_once(const Args &a, int n) {
     return a.rows <= n && (int64_t)a.NB * a.B * (a.V + kRope) * 2 >= 32 << 20;
 }

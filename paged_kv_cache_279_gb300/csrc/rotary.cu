@@ -22,8 +22,8 @@
 // long inputs, for short ones the launch and one chain of dependent loads
 // (position, angle).  So each CTA computes the sines and cosines of its tokens
 // once, one pair a thread, into shared memory, for all heads, while the loads of
-// the threads' first entries are in flight.  Measured: 64 tokens of 32 to 48 heads 2 us; 16384 tokens of 32 heads of 128
-// bf16 46.5 us (5.8 TB/s, 87 % of a plain copy), 16001 of 32 + 8 + 8 heads into a cache 64.6 us (6.1 TB/s).  A second unit in
+// the threads' first entries are in flight.  Measured, from CUDA graphs: 64 tokens of 32 to 48 heads 2 us; 16384 tokens of 32
+// heads of 128 bf16 46.4 us (5.8 TB/s, 87 % of a plain copy), 16001 of 32 + 8 + 8 heads into a cache 64.5 us (6.1 TB/s).  A second unit in
 // flight a thread (70 instead of 40 registers) takes 6 to 18 % longer, 32 registers by spilling 7 % longer.
 #include <cmath>
 
